@@ -1,0 +1,412 @@
+// Beam selection over beams and vocabulary under an automaton, and the reordering of the beams'
+// states.
+//
+// A cell (beam k, token v) has the value scores[k] + logp[k, v].  Its key is the value's
+// order-preserving bit pattern above the complement of its flat index k V + v: keys are distinct,
+// larger is better and ties go to the lowest index, so the result does not depend on the order in
+// which cells are met.  Selection is one pass over logp.  A block walks batches of 8192 cells of
+// one beam, 32 per thread in registers, and keeps the `top` best keys met so far in shared
+// memory; the smallest of them is the threshold that nearly every later cell fails.  Where more
+// than `top` threads hold a cell above the threshold, the top-th largest of the threads' maxima
+// is a better one (at least `top` cells reach it), which bounds a batch's candidates by 32 top.
+// A second launch merges the blocks' lists of a sequence the same way and looks up the states.
+#include "fa_lm.cuh"
+
+namespace {
+
+constexpr int NT = 256;
+constexpr int PER = 32;            // cells of a batch per thread
+constexpr int BATCH = NT * PER;
+typedef unsigned long long key_t64;
+
+__device__ __forceinline__ key_t64 cell_key(float v, uint32_t flat) {
+    const uint32_t u = __float_as_uint(v + 0.0f);   // -0 becomes 0
+    const uint32_t ord = (u >> 31) ? ~u : (u | 0x80000000u);
+    return ((key_t64)ord << 32) | (0xffffffffu - flat);
+}
+__device__ __forceinline__ float key_value(key_t64 k) {
+    const uint32_t ord = (uint32_t)(k >> 32);
+    return __uint_as_float((ord >> 31) ? (ord & 0x7fffffffu) : ~ord);
+}
+
+// The `top` best keys met so far: list[0 .. count), all distinct; threshold = the smallest of
+// them once there are `top`, else 0 (below every cell's key).
+struct BestShared {
+    key_t64 maxima[NT];
+    key_t64 threshold;
+    int count;
+};
+
+// Offer every thread's n keys get(0 .. n) (0 = no cell).  Called by all threads of the block;
+// list has room for top + n * top keys, and work for as many.
+template <class F>
+__device__ __forceinline__ void offer(BestShared &sh, key_t64 *list, key_t64 *work, int top, int n, key_t64 best, F get) {
+    const int tid = threadIdx.x;
+    key_t64 thr = sh.threshold;
+    const int above = __syncthreads_count(best > thr);
+    if (!above) return;
+    if (above > top) {
+        sh.maxima[tid] = best;
+        __syncthreads();
+        int rank = 0;
+        for (int i = 0; i < NT; ++i) rank += sh.maxima[i] > best;
+        if (rank == top - 1 && best > thr) sh.threshold = best - 1;   // the top-th maximum itself still passes
+        __syncthreads();
+        thr = sh.threshold;
+    }
+    if (best > thr)
+        for (int i = 0; i < n; ++i) {
+            const key_t64 k = get(i);
+            if (k > thr) list[atomicAdd(&sh.count, 1)] = k;
+        }
+    __syncthreads();
+    const int m = sh.count;
+    if (m >= top) {
+        // keep the best `top` in order; the last of them is the threshold
+        for (int i = tid; i < m; i += NT) {
+            const key_t64 k = list[i];
+            int rank = 0;
+            for (int j = 0; j < m; ++j) rank += list[j] > k;
+            if (rank < top) work[rank] = k;
+        }
+        __syncthreads();
+        for (int i = tid; i < top; i += NT) list[i] = work[i];
+        if (tid == 0) { sh.count = top; sh.threshold = work[top - 1]; }
+        __syncthreads();
+    }
+}
+
+struct SelectArgs {
+    int N, K, V, top, S, words, nb;      // nb blocks per sequence
+    const void *logp;
+    int64_t ln, lk;
+    const float *scores;
+    const int32_t *states;
+    const int16_t *next;
+    const uint32_t *live;
+    key_t64 *keys;                       // [N, nb, top]
+    float *out_score;
+    int32_t *out_parent, *out_token, *out_state;
+};
+
+// the live bits of W consecutive tokens from v0 on (v0 may be negative or near the row's end)
+template <int W>
+__device__ __forceinline__ uint32_t live_bits(const uint32_t *row, int words, int v0) {
+    const int w = v0 >> 5, sh = v0 & 31;
+    const uint32_t lo = w >= 0 && w < words ? __ldg(row + w) : 0u;
+    uint32_t bits = lo >> sh;
+    if (sh + W > 32 && w + 1 < words) bits |= __ldg(row + w + 1) << (32 - sh);
+    return bits;
+}
+
+__device__ void store_cell(const SelectArgs &a, int n, int i, key_t64 k) {
+    const int64_t at = (int64_t)n * a.top + i;
+    if (!k) {
+        a.out_score[at] = -INFINITY;
+        a.out_parent[at] = a.out_token[at] = -1;
+        if (a.out_state) a.out_state[at] = -1;
+        return;
+    }
+    const uint32_t flat = 0xffffffffu - (uint32_t)k;
+    const int parent = (int)(flat / (uint32_t)a.V), token = (int)(flat % (uint32_t)a.V);
+    a.out_score[at] = key_value(k);
+    a.out_parent[at] = parent;
+    a.out_token[at] = token;
+    if (a.out_state) a.out_state[at] = a.next[(int64_t)a.states[(int64_t)n * a.K + parent] * a.V + token];
+}
+
+// write the block's best keys: to the outputs when it is the sequence's only block
+__device__ void finish(const SelectArgs &a, BestShared &sh, key_t64 *list, key_t64 *work, int n, bool last) {
+    const int tid = threadIdx.x, m = sh.count;
+    if (last) {
+        for (int i = tid; i < a.top; i += NT) work[i] = 0;
+        __syncthreads();
+        for (int i = tid; i < m; i += NT) {
+            int rank = 0;
+            for (int j = 0; j < m; ++j) rank += list[j] > list[i];
+            work[rank] = list[i];
+        }
+        __syncthreads();
+        for (int i = tid; i < a.top; i += NT) store_cell(a, n, i, work[i]);
+    } else {
+        key_t64 *out = a.keys + ((int64_t)n * a.nb + blockIdx.x) * a.top;
+        for (int i = tid; i < a.top; i += NT) out[i] = i < m ? list[i] : 0;
+    }
+}
+
+template <class T>
+__global__ void __launch_bounds__(NT) k_beam_scan(SelectArgs a) {
+    extern __shared__ key_t64 dyn[];
+    __shared__ BestShared sh;
+    constexpr int VEC = fa_vec<T>::N, NV = PER / VEC;
+    key_t64 *list = dyn, *work = dyn + (size_t)(PER + 1) * a.top;
+    const int tid = threadIdx.x, n = blockIdx.y;
+    if (tid == 0) { sh.threshold = 0; sh.count = 0; }
+    __syncthreads();
+    const int per_beam = (a.V + VEC - 1 + BATCH - 1) / BATCH;   // a misaligned row starts up to VEC - 1 cells early
+    for (int bt = blockIdx.x; bt < a.K * per_beam; bt += gridDim.x) {
+        const int k = bt / per_beam, first = (bt % per_beam) * BATCH;
+        const float score = a.scores[(int64_t)n * a.K + k];
+        const int state = a.S ? a.states[(int64_t)n * a.K + k] : 0;
+        if (!(score > -INFINITY) || (a.S && (unsigned)state >= (unsigned)a.S)) continue;   // a dead beam
+        const T *row = (const T *)a.logp + n * a.ln + k * a.lk;
+        const int mis = (int)(((uintptr_t)row & 15) / sizeof(T));   // vector i holds cells i VEC - mis ...
+        const uint32_t *lrow = a.S ? a.live + (int64_t)state * a.words : nullptr;
+        uint4 raw[NV];
+        uint32_t bits[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v0 = first + (i * NT + tid) * VEC - mis;
+            constexpr uint32_t all = VEC == 32 ? 0xffffffffu : (1u << VEC) - 1;
+            uint32_t m = v0 < a.V && v0 > -VEC ? all : 0u;
+            if (m && lrow) m &= live_bits<VEC>(lrow, a.words, v0);
+            if (m && v0 < 0) m &= all << -v0;
+            if (m && v0 + VEC > a.V) m &= all >> (v0 + VEC - a.V);
+            bits[i] = m;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v0 = first + (i * NT + tid) * VEC - mis;
+            raw[i] = make_uint4(0, 0, 0, 0);
+            if (!bits[i]) continue;
+            if (v0 >= 0 && v0 + VEC <= a.V) {
+                raw[i] = __ldg(reinterpret_cast<const uint4 *>(row + v0));
+            } else {
+                float f[VEC];
+                for (int e = 0; e < VEC; ++e) f[e] = (bits[i] >> e & 1) ? fa_to_f32(row[v0 + e]) : 0.0f;
+                raw[i] = fa_pack(f, T());
+            }
+        }
+        float top_value = -INFINITY;
+        key_t64 best = 0;
+        auto cell = [&](int i, int e, float x) -> key_t64 {
+            const float v = score + x;
+            if (!(bits[i] >> e & 1) || !(v > -INFINITY)) return 0;
+            return cell_key(v, (uint32_t)(k * a.V + first + (i * NT + tid) * VEC - mis + e));
+        };
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float f[VEC];
+            fa_unpack(raw[i], f, T());
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                if ((bits[i] >> e & 1) && score + f[e] > top_value) {   // a thread's cells come in ascending order
+                    top_value = score + f[e];
+                    best = cell(i, e, f[e]);
+                }
+        }
+        offer(sh, list, work, a.top, PER, best, [&](int q) -> key_t64 {
+            const int i = q / VEC, e = q % VEC;
+            uint4 r = raw[0];
+            uint32_t m = bits[0];
+#pragma unroll
+            for (int j = 1; j < NV; ++j)
+                if (i == j) { r = raw[j]; m = bits[j]; }
+            float f[VEC];
+            fa_unpack(r, f, T());
+            float x = f[0];
+#pragma unroll
+            for (int j = 1; j < VEC; ++j)
+                if (e == j) x = f[j];
+            const float v = score + x;
+            if (!(m >> e & 1) || !(v > -INFINITY)) return 0;
+            return cell_key(v, (uint32_t)(k * a.V + first + (i * NT + tid) * VEC - mis + e));
+        });
+    }
+    finish(a, sh, list, work, n, gridDim.x == 1);
+}
+
+// merge a sequence's lists
+__global__ void __launch_bounds__(NT) k_beam_merge(SelectArgs a) {
+    extern __shared__ key_t64 dyn[];
+    __shared__ BestShared sh;
+    key_t64 *list = dyn, *work = dyn + 5 * (size_t)a.top;
+    const int tid = threadIdx.x, n = blockIdx.x;
+    if (tid == 0) { sh.threshold = 0; sh.count = 0; }
+    __syncthreads();
+    const key_t64 *keys = a.keys + (int64_t)n * a.nb * a.top;
+    const int total = a.nb * a.top;
+    for (int first = 0; first < total; first += 4 * NT) {
+        key_t64 k[4], best = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int at = first + i * NT + tid;
+            k[i] = at < total ? keys[at] : 0;
+            best = max(best, k[i]);
+        }
+        offer(sh, list, work, a.top, 4, best, [&](int q) { return q == 0 ? k[0] : q == 1 ? k[1] : q == 2 ? k[2] : k[3]; });
+    }
+    finish(a, sh, list, work, n, true);
+}
+
+__global__ void __launch_bounds__(NT) k_beam_reorder(int K, int top, int64_t words, const int32_t *__restrict__ src,
+                                                     const int32_t *__restrict__ parent,
+                                                     const int32_t *__restrict__ token, int64_t at, int32_t *dst) {
+    const int64_t r = blockIdx.x, n = r / top;
+    const int p = parent[r];
+    const bool found = (unsigned)p < (unsigned)K;
+    const int32_t *from = src + (n * K + (found ? p : 0)) * words;
+    int32_t *to = dst + r * words;
+    for (int64_t w = (int64_t)blockIdx.y * NT + threadIdx.x; w < words; w += (int64_t)gridDim.y * NT)
+        to[w] = token && w == at ? token[r] : found ? from[w] : -1;
+}
+
+// ----------------------------------------------------------------------------- tables
+
+__global__ void __launch_bounds__(NT) k_table_clear(int64_t n, int16_t *next) {
+    for (int64_t i = (int64_t)blockIdx.x * NT + threadIdx.x; i < n; i += (int64_t)gridDim.x * NT) next[i] = -1;
+}
+
+// which states reach an accepting one, as bits: backwards over the edges until nothing changes
+// (at most S times); one block
+__global__ void __launch_bounds__(1024) k_table_reach(int S, int E, const int32_t *accept_mask, const int32_t *src,
+                                                      const int32_t *dst, uint32_t *reach) {
+    __shared__ uint32_t got[FA_MAX_STATES / 32];
+    const int words = (S + 31) / 32, tid = threadIdx.x;
+    for (int w = tid; w < words; w += 1024) got[w] = 0;
+    __syncthreads();
+    for (int s = tid; s < S; s += 1024)
+        if (accept_mask[s]) atomicOr(&got[s / 32], 1u << (s % 32));
+    __syncthreads();
+    for (int round = 0; round < S; ++round) {
+        int changed = 0;
+        for (int e = tid; e < E; e += 1024) {
+            const int s = src[e], d = dst[e];
+            if ((got[d / 32] >> (d % 32) & 1) && !(got[s / 32] >> (s % 32) & 1)) {
+                atomicOr(&got[s / 32], 1u << (s % 32));
+                changed = 1;
+            }
+        }
+        if (!__syncthreads_or(changed)) break;
+    }
+    for (int w = tid; w < words; w += 1024) reach[w] = got[w];
+}
+
+// a block per edge: its tokens lead to its destination, if that can still be accepted
+__global__ void __launch_bounds__(NT) k_table_fill(int E, int V, const int64_t *lab_off, const int32_t *lab_tok,
+                                                   const int32_t *src, const int32_t *dst, const uint32_t *reach,
+                                                   int16_t *next) {
+    for (int e = blockIdx.x; e < E; e += gridDim.x) {
+        const int s = src[e], d = dst[e];
+        if (!(reach[d / 32] >> (d % 32) & 1)) continue;
+        for (int64_t i = lab_off[e] + threadIdx.x; i < lab_off[e + 1]; i += NT) next[(int64_t)s * V + lab_tok[i]] = (int16_t)d;
+    }
+}
+
+// one warp per word
+__global__ void __launch_bounds__(NT) k_table_bits(int64_t n_words, int words, int V, const int16_t *next, uint32_t *live) {
+    const int lane = threadIdx.x & 31;
+    for (int64_t w = (int64_t)blockIdx.x * (NT / 32) + threadIdx.x / 32; w < n_words; w += (int64_t)gridDim.x * (NT / 32)) {
+        const int64_t s = w / words;
+        const int v = (int)(w % words) * 32 + lane;
+        const uint32_t bits = __ballot_sync(0xffffffffu, v < V && next[s * V + v] >= 0);
+        if (lane == 0) live[w] = bits;
+    }
+}
+
+// blocks per sequence: four per SM over all sequences, one batch each at least
+int select_blocks(int N, int K, int V) {
+    const int64_t batches = (int64_t)K * ((V + 7 + BATCH - 1) / BATCH);
+    const int64_t want = std::max<int64_t>(1, (152 * 4 + N - 1) / N);
+    return (int)std::min(batches, want);
+}
+
+fa_status select_sizes(const char *fn, int32_t N, int32_t K, int32_t V, int32_t top) {
+    if (N < 0 || N > 65535 || K < 1 || V < 1 || (int64_t)K * V >= 2147483648LL) return fa_refuse(fn, "N, K or V out of range");
+    if (top < 1 || top > FA_MAX_BEAM_TOP) return fa_refuse(fn, "top must be in [1, FA_MAX_BEAM_TOP]");
+    return FA_OK;
+}
+
+}  // namespace
+
+extern "C" fa_status fa_beam_select_workspace_bytes(int32_t N, int32_t K, int32_t V, int32_t top, size_t *bytes) {
+    const char *fn = "fa_beam_select_workspace_bytes";
+    if (!bytes) return fa_refuse(fn, "NULL argument");
+    fa_status st = select_sizes(fn, N, K, V, top);
+    if (st != FA_OK) return st;
+    *bytes = (size_t)N * select_blocks(std::max(N, 1), K, V) * top * sizeof(key_t64);
+    return FA_OK;
+}
+
+extern "C" fa_status fa_beam_select(int32_t dtype, int32_t N, int32_t K, int32_t V, int32_t top, const void *logp,
+                                    int64_t logp_seq_stride, int64_t logp_beam_stride, const float *scores,
+                                    const int32_t *states, int32_t S, const int16_t *next, const uint32_t *live,
+                                    float *out_score, int32_t *out_parent, int32_t *out_token, int32_t *out_state,
+                                    void *workspace, size_t ws_bytes, fa_stream stream) {
+    const char *fn = "fa_beam_select";
+    if (!fa_dtype_ok(dtype)) return fa_refuse(fn, "unknown dtype");
+    fa_status st = select_sizes(fn, N, K, V, top);
+    if (st != FA_OK) return st;
+    if (S < 0 || S > FA_MAX_STATES) return fa_refuse(fn, "S out of [0, FA_MAX_STATES]");
+    const bool aut = S > 0;
+    if (aut != (states != nullptr) || aut != (next != nullptr) || aut != (live != nullptr) || aut != (out_state != nullptr))
+        return fa_refuse(fn, "states, next, live and out_state go together with S > 0");
+    if (N == 0) return FA_OK;
+    if (!logp || !scores || !out_score || !out_parent || !out_token) return fa_refuse(fn, "NULL buffer");
+    if ((uintptr_t)logp % fa_dtype_bytes(dtype)) return fa_refuse(fn, "logp is not aligned to its type");
+    SelectArgs a;
+    a.N = N; a.K = K; a.V = V; a.top = top; a.S = S; a.words = (V + 31) / 32;
+    a.nb = select_blocks(N, K, V);
+    const size_t need = (size_t)N * a.nb * top * sizeof(key_t64);
+    if (ws_bytes < need || (need && !workspace))
+        return fa_refuse(fn, ("workspace needs " + std::to_string(need) + " bytes").c_str(), FA_ERR_WORKSPACE_TOO_SMALL);
+    if ((uintptr_t)workspace & 255) return fa_refuse(fn, "workspace not 256-byte aligned");
+    a.logp = logp; a.ln = logp_seq_stride; a.lk = logp_beam_stride;
+    a.scores = scores; a.states = states; a.next = next; a.live = live;
+    a.keys = (key_t64 *)workspace;
+    a.out_score = out_score; a.out_parent = out_parent; a.out_token = out_token; a.out_state = out_state;
+    cudaStream_t s = (cudaStream_t)stream;
+    const size_t smem = (size_t)(PER + 1) * top * 8 + (size_t)top * 8;
+    auto go = [&](auto tag) {
+        using T = decltype(tag);
+        if (smem > 40 * 1024) {
+            cudaError_t e = cudaFuncSetAttribute(k_beam_scan<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e != cudaSuccess) return e;
+        }
+        k_beam_scan<T><<<dim3((unsigned)a.nb, (unsigned)N), NT, smem, s>>>(a);
+        return cudaSuccess;
+    };
+    const cudaError_t e = dtype == FA_DTYPE_F32 ? go(0.0f) : dtype == FA_DTYPE_F16 ? go(__half()) : go(__nv_bfloat16());
+    if (e != cudaSuccess) return fa_refuse(fn, cudaGetErrorString(e), FA_ERR_CUDA);
+    if ((st = fa_launch_check("beam scan")) != FA_OK || a.nb == 1) return st;
+    k_beam_merge<<<(unsigned)N, NT, (size_t)6 * top * 8, s>>>(a);
+    return fa_launch_check("beam merge");
+}
+
+extern "C" fa_status fa_beam_reorder(int32_t N, int32_t K, int32_t top, int64_t words, const int32_t *src,
+                                     const int32_t *parent, const int32_t *token, int64_t at, int32_t *dst,
+                                     fa_stream stream) {
+    const char *fn = "fa_beam_reorder";
+    if (N < 0 || K < 0 || top < 0 || words < 0 || (int64_t)N * top > 2147483647) return fa_refuse(fn, "sizes out of range");
+    if (token && (at < 0 || at >= words)) return fa_refuse(fn, "at must be in [0, words)");
+    if ((int64_t)N * top == 0 || words == 0) return FA_OK;
+    if ((K > 0 && !src) || !parent || !dst) return fa_refuse(fn, "NULL buffer");
+    const unsigned gy = (unsigned)std::min<int64_t>((words + NT * 4 - 1) / (NT * 4), 1024);
+    k_beam_reorder<<<dim3((unsigned)(N * top), gy), NT, 0, (cudaStream_t)stream>>>(K, top, words, src, parent, token, at, dst);
+    return fa_launch_check("beam reorder");
+}
+
+extern "C" fa_status fa_beam_tables(const fa_automaton *aut, int16_t *next, uint32_t *live, fa_stream stream) {
+    const char *fn = "fa_beam_tables";
+    if (!aut) return fa_refuse(fn, "NULL automaton");
+    if (!aut->is_dfa) return fa_refuse(fn, "the automaton is not deterministic", FA_ERR_UNSUPPORTED);
+    if (!next || !live) return fa_refuse(fn, "NULL buffer");
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return fa_refuse(fn, cudaGetErrorString(e), FA_ERR_CUDA);
+    if (dev != aut->device) return fa_refuse(fn, "current device differs from the automaton's device");
+    cudaStream_t s = (cudaStream_t)stream;
+    const int S = aut->S, V = aut->V, E = aut->E, words = (V + 31) / 32;
+    k_table_clear<<<152 * 8, NT, 0, s>>>((int64_t)S * V, next);
+    fa_status st = fa_launch_check("beam tables");
+    if (st != FA_OK) return st;
+    // live is free until the last kernel: its first words hold the reachable states meanwhile
+    k_table_reach<<<1, 1024, 0, s>>>(S, E, aut->accept_mask, aut->edge_src, aut->edge_dst, live);
+    if ((st = fa_launch_check("beam tables")) != FA_OK) return st;
+    if (E > 0) {
+        k_table_fill<<<(unsigned)std::min(E, 152 * 64), NT, 0, s>>>(E, V, aut->lab_off, aut->lab_tok, aut->edge_src, aut->edge_dst, live, next);
+        if ((st = fa_launch_check("beam tables")) != FA_OK) return st;
+    }
+    k_table_bits<<<152 * 16, NT, 0, s>>>((int64_t)S * words, words, V, next, live);
+    return fa_launch_check("beam tables");
+}

@@ -78,6 +78,8 @@ struct fa_automaton {
 };
 
 void fa_set_error(const std::string &msg);
+// counts a kernel launch and turns its error into a status (fa_step.cu)
+fa_status fa_launch_check(const char *what);
 
 // ----------------------------------------------------------------------------- device side
 

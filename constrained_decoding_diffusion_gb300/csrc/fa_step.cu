@@ -2756,6 +2756,8 @@ fa_status step_impl(const fa_automaton *aut, int32_t B, int32_t L, const float *
 }
 }  // namespace
 
+fa_status fa_launch_check(const char *what) { return launch_check(what); }
+
 extern "C" fa_status fa_profile_enable(int32_t enable) {
     if (enable && !g_stage.created) {
         for (int i = 0; i <= FA_N_STAGES; ++i) {

@@ -33,7 +33,10 @@ EXPORTS = ("fa_compile", "fa_destroy", "fa_query", "fa_export_csr", "fa_step_wor
            "fa_token_marginals", "fa_map_step", "fa_constrained_step_host",
            "fa_apply_commits", "fa_constrained_step_noalloc", "fa_debug_inject_wait_timeouts",
            "fa_profile_enable", "fa_profile_read",
-           "fa_launch_count", "fa_last_error")
+           "fa_launch_count", "fa_last_error",
+           "fa_rope", "fa_cache_write", "fa_cache_read", "fa_cache_keep", "fa_tree_mask",
+           "fa_tree_attention_workspace_bytes", "fa_tree_attention", "fa_beam_tables",
+           "fa_beam_select_workspace_bytes", "fa_beam_select", "fa_beam_reorder")
 N_STAGES = 4
 STAGES = ("reweight", "upsweep", "topdown", "leaf_commit")
 
@@ -93,6 +96,22 @@ def load(path: str = LIB_PATH):
     lib.fa_profile_read.restype = st
     lib.fa_launch_count.argtypes = [P]
     lib.fa_launch_count.restype = st
+    f32 = ctypes.c_float
+    # the model-side operators (bound in lm.py)
+    lib.fa_rope.argtypes = [i32, i64, i32, i32, i32, i32, i32, P, i64, i64, P, P, f32, P, i64, i64, P]
+    lib.fa_cache_write.argtypes = [P, i32, i32, i32, P, i64, i64, i64, P, i64, i64, i64, P, i32, P, P, P, P, i32, i32,
+                                   f32, P]
+    lib.fa_cache_read.argtypes = [P, i32, i32, i32, P, i32, P, P, P, P]
+    lib.fa_cache_keep.argtypes = [P, i32, i32, P, i32, P, P, P]
+    lib.fa_tree_mask.argtypes = [i32, i32, P, P, P, P]
+    lib.fa_tree_attention_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, ctypes.POINTER(sz)]
+    lib.fa_tree_attention.argtypes = [P, i32, i32, i32, i32, P, i64, i64, i64, P, i32, P, P, P, f32, P, P, P, sz, P]
+    lib.fa_beam_tables.argtypes = [P, P, P, P]
+    lib.fa_beam_select_workspace_bytes.argtypes = [i32, i32, i32, i32, ctypes.POINTER(sz)]
+    lib.fa_beam_select.argtypes = [i32, i32, i32, i32, i32, P, i64, i64, P, P, i32, P, P, P, P, P, P, P, sz, P]
+    lib.fa_beam_reorder.argtypes = [i32, i32, i32, i64, P, P, P, i64, P, P]
+    for name in EXPORTS[EXPORTS.index("fa_rope"):]:
+        getattr(lib, name).restype = st
     lib.fa_last_error.argtypes = []
     lib.fa_last_error.restype = ctypes.c_char_p
     _lib = lib

@@ -356,6 +356,198 @@ fa_status fa_constrained_step_noalloc(const fa_automaton *aut, int32_t B, int32_
                                       fa_stream stream);
 
 /*
+ * ---------------------------------------------------------------------------------------
+ * The model's side of a decoding step: rotary positions, a paged key/value cache, attention
+ * of drafted tokens over it, and beam selection under an automaton.
+ *
+ * A program that drafts a block with the automaton needs these next to the constrained step:
+ * beams over the block's distributions give a tree of drafted tokens, one attention pass of
+ * the tree over the cached prefix scores them, and the accepted path stays in the cache.
+ * With every drafted token seeing every other one, the same pass is a block-wise denoiser's
+ * attention of the block being decoded over the prefix.  The operators are the common ones
+ * of transformer decoding and have no counterpart on the pages.
+ *
+ * All arrays are DEVICE memory.  Strides are in elements, the innermost dimension is
+ * contiguous.  Lengths, page tables and masks are read on the device, so a decoding loop
+ * needs no host synchronisation.  A page number outside [0, n_pages) is not followed: its
+ * slots are not written, read back as zeros and are not attended to.
+ */
+enum { FA_DTYPE_F32 = 0, FA_DTYPE_F16 = 1, FA_DTYPE_BF16 = 2 };
+
+/*
+ * fa_rope -- rotary positions: the first rot_dim elements of every head are rotated pair by
+ * pair, the others copied.  With t = positions[n] and pair i holding (x0, x1),
+ *     y0 = mscale (x0 cos a - x1 sin a),  y1 = mscale (x0 sin a + x1 cos a),
+ *     a = 2 pi * frac(t * phase[i] / 2^64).
+ * inverse = 1 rotates by -a with the same mscale: the gradient of the forward call.
+ *
+ *   dtype        FA_DTYPE_* of x and out
+ *   x, out       [n_tokens, n_heads, head_dim] with token and head strides; out may be x
+ *                with the same strides, and may not overlap it otherwise
+ *   rot_dim      even, 0 <= rot_dim <= head_dim <= 1024
+ *   interleaved  1: pair i = elements (2i, 2i + 1); 0: pair i = (i, i + rot_dim / 2)
+ *   positions    [n_tokens] int32 (negative positions rotate backwards)
+ *   phase        [rot_dim / 2] turns per position as a 64-bit fraction of a turn: the angle is
+ *                reduced exactly at any position, and any scaling for long contexts
+ *                (interpolated positions, a stretched base, a blend by wavelength) is a
+ *                choice of phase and mscale
+ * Sums and products in fp32, rounded once.  Errors: FA_ERR_INVALID_ARG, FA_ERR_CUDA.
+ */
+fa_status fa_rope(int32_t dtype, int64_t n_tokens, int32_t n_heads, int32_t head_dim, int32_t rot_dim,
+                  int32_t interleaved, int32_t inverse, const void *x, int64_t x_token_stride,
+                  int64_t x_head_stride, const int32_t *positions, const uint64_t *phase, float mscale, void *out,
+                  int64_t out_token_stride, int64_t out_head_stride, fa_stream stream);
+
+/* A paged key/value cache, owned by the caller.  Sequence b's slot t lies in page
+ * page_table[b * max_pages + t / page_size], place t % page_size. */
+enum {
+    FA_CACHE_F16 = 1,
+    FA_CACHE_BF16 = 2,
+    FA_CACHE_E4M3 = 3 /* 8-bit codes (4 exponent, 3 mantissa bits) with one scale per slot and head */
+};
+typedef struct {
+    void *k, *v;               /* [n_pages, kv_heads, page_size, head_dim], contiguous, 16-byte aligned */
+    float *k_scale, *v_scale;  /* [n_pages, kv_heads, page_size] for FA_CACHE_E4M3, else NULL */
+    int32_t format;            /* FA_CACHE_* */
+    int32_t n_pages;
+    int32_t page_size;         /* a power of two in [1, 1024] */
+    int32_t kv_heads;
+    int32_t head_dim;          /* a multiple of 16 in [16, 256] */
+} fa_kv_cache;
+
+/*
+ * fa_cache_write -- rotate new keys, quantise keys and values and store them in their pages.
+ *
+ * Token j < count[b] of sequence b goes to slot start[b] + j; others are ignored.  FA_CACHE_E4M3
+ * stores, per slot and head, scale = max|x| / 448 and the codes of x / scale rounded to nearest
+ * even (an all-zero row: scale 0); a row that holds a NaN or an infinity gets a NaN scale, so
+ * it reads back as NaN.  The 16-bit formats store x rounded once.
+ *
+ *   dtype           FA_DTYPE_* of k and v
+ *   k, v            [B, T, kv_heads, head_dim] with batch, token and head strides
+ *   page_table      [B, max_pages] int32; slots past max_pages * page_size are ignored
+ *   start, count    [B] int32; count may be NULL (all T tokens)
+ *   positions       [B, T] int32 and phase [rot_dim / 2] as for fa_rope rotate the keys;
+ *                   both NULL stores the keys as they are
+ * Two tokens of one call must not share a slot.  Errors: FA_ERR_INVALID_ARG, FA_ERR_CUDA.
+ */
+fa_status fa_cache_write(const fa_kv_cache *cache, int32_t dtype, int32_t B, int32_t T, const void *k,
+                         int64_t k_batch_stride, int64_t k_token_stride, int64_t k_head_stride, const void *v,
+                         int64_t v_batch_stride, int64_t v_token_stride, int64_t v_head_stride,
+                         const int32_t *page_table, int32_t max_pages, const int32_t *start, const int32_t *count,
+                         const int32_t *positions, const uint64_t *phase, int32_t rot_dim, int32_t interleaved,
+                         float mscale, fa_stream stream);
+
+/*
+ * fa_cache_read -- slots [0, min(length[b], N)) of every sequence back as dense arrays
+ * k_out, v_out [B, N, kv_heads, head_dim] (contiguous, dtype FA_DTYPE_*, 16-byte aligned);
+ * code * scale in fp32, rounded once; the rows past length[b] are set to zero.
+ * Errors: FA_ERR_INVALID_ARG, FA_ERR_CUDA.
+ */
+fa_status fa_cache_read(const fa_kv_cache *cache, int32_t dtype, int32_t B, int32_t N, const int32_t *page_table,
+                        int32_t max_pages, const int32_t *length, void *k_out, void *v_out, fa_stream stream);
+
+/*
+ * fa_cache_keep -- after a draft: move the accepted path's slots together.  For every sequence,
+ * slot length[b] + path[b, i] is copied to slot length[b] + i for i = 0, 1, ... until the
+ * first path[b, i] < 0 or P.  path[b, .] must ascend (a node's ancestors come before it),
+ * so path[b, i] >= i; an entry that does not ascend ends the path.  Codes and scales move as they are.
+ *   path  [B, P] int32.   Errors: FA_ERR_INVALID_ARG, FA_ERR_CUDA.
+ */
+fa_status fa_cache_keep(const fa_kv_cache *cache, int32_t B, int32_t P, const int32_t *page_table, int32_t max_pages,
+                        const int32_t *length, const int32_t *path, fa_stream stream);
+
+/*
+ * fa_tree_mask -- the mask and the depths of a draft tree.  parents[b, j] < j is the drafted
+ * token that j follows, or negative for one that follows the prefix (a parent >= j counts
+ * as negative).  Token j sees its ancestors and itself: bit i % 64 of
+ * mask[b, j, i / 64]; depth[b, j] is its number of ancestors (its position past the prefix).
+ *   parents  [B, T] int32, mask [B, T, ceil(T / 64)] uint64 out, depth [B, T] int32 out or NULL;
+ *   T <= FA_MAX_DRAFT.    Errors: FA_ERR_INVALID_ARG, FA_ERR_CUDA.
+ */
+#define FA_MAX_DRAFT 1024
+fa_status fa_tree_mask(int32_t B, int32_t T, const int32_t *parents, uint64_t *mask, int32_t *depth,
+                       fa_stream stream);
+
+/*
+ * fa_tree_attention -- attention of drafted tokens over a paged cache that already holds
+ * their keys and values (slots length[b] .. length[b] + T - 1):
+ *     out[b, i, h] = sum_t softmax_t(scale * q[b, i, h] . k[b, t, h / group]) v[b, t, h / group]
+ * over the slots t < length[b] and the drafted slots length[b] + j with bit j of mask[b, i] set.
+ * Query heads [g * group, (g + 1) * group) share key/value head g, group = q_heads / kv_heads.
+ *
+ *   dtype        FA_DTYPE_F16 or FA_DTYPE_BF16 of q and out; a 16-bit cache has the same type
+ *   q            [B, T, q_heads, head_dim] with batch, token and head strides that are
+ *                multiples of 8, 16-byte aligned; head_dim <= 128
+ *   length       [B] int32: slots before the draft (0 is fine)
+ *   count        [B] int32 or NULL: how many of the T drafted tokens are in use; the rows
+ *                of the others come out empty and their slots are not attended to
+ *   mask         [B, T, ceil(T / 64)] uint64 (bit j % 64 of word j / 64), or NULL: every
+ *                drafted token sees all drafted tokens (a block being denoised)
+ *   out          [B, T, q_heads, head_dim] contiguous, 16-byte aligned
+ *   lse          [B, T, q_heads] fp32 or NULL: ln sum_t exp(scale * q . k)
+ *   workspace    fa_tree_attention_workspace_bytes() bytes, 256-byte aligned; contents are
+ *                overwritten; concurrent calls need separate workspaces
+ * A row that sees nothing gives out = 0 and lse = -inf.  What a row does not see has no part in its result,
+ * whatever it holds (NaN and infinities included).  Scores, softmax statistics and sums are
+ * fp32; the softmax weights are rounded to 16 bits for the product with the values.
+ * T <= FA_MAX_DRAFT, B <= 65535.
+ * Errors: FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED (types, head_dim), FA_ERR_WORKSPACE_TOO_SMALL,
+ * FA_ERR_CUDA.
+ */
+fa_status fa_tree_attention_workspace_bytes(int32_t B, int32_t T, int32_t q_heads, int32_t kv_heads,
+                                            int32_t head_dim, size_t *bytes);
+fa_status fa_tree_attention(const fa_kv_cache *cache, int32_t dtype, int32_t B, int32_t T, int32_t q_heads,
+                            const void *q, int64_t q_batch_stride, int64_t q_token_stride, int64_t q_head_stride,
+                            const int32_t *page_table, int32_t max_pages, const int32_t *length,
+                            const int32_t *count, const uint64_t *mask, float scale, void *out, float *lse,
+                            void *workspace, size_t ws_bytes, fa_stream stream);
+
+/*
+ * fa_beam_tables -- the tables that beam selection reads, from a compiled DFA:
+ * next[s, v] int16 [S, V] is the state after token v in state s, or -1 when there is none or no
+ * accepting state can be reached from it; live [S, ceil(V / 32)] uint32 has bit v % 32 of
+ * word v / 32 set where next[s, v] >= 0.
+ * Errors: FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED (an NFA), FA_ERR_CUDA.
+ */
+fa_status fa_beam_tables(const fa_automaton *aut, int16_t *next, uint32_t *live, fa_stream stream);
+
+/*
+ * fa_beam_select -- one step of beam search: of all (beam k, token v) of sequence n with
+ * value scores[n, k] + logp[n, k, v] (one fp32 addition), the `top` largest, descending, ties to
+ * the lowest k * V + v.  Under an automaton only tokens with a live bit in the beam's state take
+ * part.  Values of -inf and NaN never do.
+ *
+ *   dtype      FA_DTYPE_* of logp
+ *   logp       [N, K, V] with sequence and beam strides
+ *   scores     [N, K] fp32; a beam with -inf or NaN is dead
+ *   states     [N, K] int32 with next and live as from fa_beam_tables, S states; a state outside
+ *              [0, S) is dead.  All three NULL (S = 0): no automaton
+ *   top        in [1, FA_MAX_BEAM_TOP]
+ *   out_score  [N, top] fp32, out_parent, out_token [N, top] int32, out_state [N, top] int32
+ *              (NULL without an automaton): past the last selectable cell -inf and -1
+ *   workspace  fa_beam_select_workspace_bytes() bytes, 256-byte aligned
+ * K * V < 2^31.  Errors: FA_ERR_INVALID_ARG, FA_ERR_WORKSPACE_TOO_SMALL, FA_ERR_CUDA.
+ */
+#define FA_MAX_BEAM_TOP 256
+fa_status fa_beam_select_workspace_bytes(int32_t N, int32_t K, int32_t V, int32_t top, size_t *bytes);
+fa_status fa_beam_select(int32_t dtype, int32_t N, int32_t K, int32_t V, int32_t top, const void *logp,
+                         int64_t logp_seq_stride, int64_t logp_beam_stride, const float *scores,
+                         const int32_t *states, int32_t S, const int16_t *next, const uint32_t *live,
+                         float *out_score, int32_t *out_parent, int32_t *out_token, int32_t *out_state,
+                         void *workspace, size_t ws_bytes, fa_stream stream);
+
+/*
+ * fa_beam_reorder -- the beams' states follow the selection: row k of dst [N, top, words] is row
+ * parent[n, k] of src [N, K, words] (int32 words: token histories, page tables, anything),
+ * and -1 in every word where parent[n, k] is outside [0, K).  With token, word `at` of the row
+ * becomes token[n, k] (a history gets its new token).  dst must not overlap src.
+ * Errors: FA_ERR_INVALID_ARG, FA_ERR_CUDA.
+ */
+fa_status fa_beam_reorder(int32_t N, int32_t K, int32_t top, int64_t words, const int32_t *src,
+                          const int32_t *parent, const int32_t *token, int64_t at, int32_t *dst, fa_stream stream);
+
+/*
  * fa_debug_inject_wait_timeouts -- failure-injection hook for tests (no counterpart on the
  * pages).  The next n_launches launches of the tensor-core span product (|S| >= 128) make
  * their MMA-issuing thread wait, with a short limit (about half a millisecond), on a
