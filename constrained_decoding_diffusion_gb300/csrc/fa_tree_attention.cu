@@ -1,13 +1,149 @@
-// Attention of drafted tokens over a paged cache.
+// Attention of drafted tokens over a paged cache, on the 5th-generation tensor cores.
+//
+// The mathematics.  A row is one query (drafted token i, query head) of a sequence and a
+// key/value head; it sees the slots before the draft and the drafted slots its mask allows.  With
+// x_t = log2(e) scale q . k_t, out = sum_t 2^(x_t) v_t / sum_t 2^(x_t), computed in one pass
+// over the slots: every weight is taken relative to a reference B of the row, p_t = 2^(x_t - B),
+// with l = sum p_t and O = sum p_t v_t; when a tile's largest x_t exceeds the reference's by more
+// than 6 (a factor of 64), B moves and O and l are scaled by 2^(B_old - B_new).  out = O / l
+// and lse = (B + log2 l) ln 2 for any B, and parts over disjoint slots join by their lse.
+//
+// An 8-bit cache (codes times one scale per slot and head): the key's scale multiplies the
+// score, the value's the weight, so the codes themselves go to the tensor cores, as fp16 (exact).
+// q is scaled per row by a power of two into the middle of the fp16 range (exact) and the factor
+// goes to the exponent; B also follows the largest value scale a row sees, so that p_t times
+// the value's scale stays in fp16's range with 28 bits below the largest.
+//
+// The layout.  All query heads of one key/value head and all drafted tokens are rows of one
+// problem, so a cached tile is read once for up to 256 rows: two tiles of 128 rows are two
+// streams (a warpgroup each, its own scores and accumulator in tensor memory) over the same key
+// and value tiles.  With up to 128 rows the two streams take alternate key/value tiles of the
+// same rows instead, and their results are joined at the end: either way the tensor cores work on
+// one stream while the other one's softmax runs.  The work is the list of all tiles of 128
+// slots of all (sequence, head, row block) units; one block per SM takes an equal run of it,
+// whatever the lengths, which are read on the device.  A unit that is cut by the runs leaves
+// partial results, joined by a second small kernel in a fixed order.
+//
+// Roles (16 warps): warps 0-7 the two softmax warpgroups (a thread per row), warps 8-14 load and
+// convert (16-byte asynchronous copies into 128-byte-swizzled tiles), warp 15 issues the MMAs:
+// S = Q K^T (both from shared memory), P overwrites S in tensor memory as the 16-bit left operand
+// of O += P V, with V read from the same layout as K but as the MN-major operand.
+//
+// Every wait is bounded (about a second).  A wait that runs out marks the block's status; the
+// joining kernel then sets the rows the block had a part in to NaN.
 #include "fa_lm.cuh"
 
 namespace {
 
-constexpr int NW = 4;
+constexpr int TS = 128;                      // slots of a tile, rows of a stream
+constexpr int NLOAD = 7 * 32, NTHR = 16 * 32;
+constexpr int MAX_CTAS = 152;
+constexpr long long kSpinCycles = 2000000000LL;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kGrow = 6.0f;                // how far a score may exceed the reference (log2)
+
+__device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// bounded wait; once a wait of the block has failed, every other one returns at once
+__device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volatile int *fail) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*fail) return false;
+        if (clock64() - t0 > kSpinCycles) { *fail = 1; return false; }
+    }
+    return true;
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void bar_sync(int id, int n) { __syncwarp(); asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// shared-memory matrix descriptor: 128-byte swizzle (8 rows x 128 bytes atoms), descriptor version 1
+__device__ __forceinline__ uint64_t umma_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)((lbo & 0x3FFFFu) >> 4) << 16 |
+           (uint64_t)((sbo & 0x3FFFFu) >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void umma_commit(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+        "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]),
+        "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]),
+        "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 struct AttendArgs {
     fa_cache_view c;
-    int format, T, heads, group, words;
+    int B, T, heads, group, words, rows, blocks;   // rows of a unit's problem, row blocks of 256
     const void *q;
     int64_t qb, qt, qh;
     const int32_t *length, *count;
@@ -15,81 +151,814 @@ struct AttendArgs {
     float scale;
     void *out;
     float *lse;
+    float *part_o, *part_lse;                      // [MAX_CTAS, 2, 256, DP], [MAX_CTAS, 2, 256]
+    int *status;                                   // [MAX_CTAS]
 };
 
-__device__ __forceinline__ float cached(const void *p, const float *scale, int format, int64_t row, int D, int d) {
-    const int64_t at = row * D + d;
-    if (format == FA_CACHE_F16) return __half2float(((const __half *)p)[at]);
-    if (format == FA_CACHE_BF16) return __bfloat162float(((const __nv_bfloat16 *)p)[at]);
-    const uint32_t h = fa_e4m3x2_to_half2(((const uint8_t *)p)[at]);
-    return __half2float(__ushort_as_half((unsigned short)(h & 0xffff))) * scale[row];
+// ----------------------------------------------------------------------------- the work list
+
+// sequence b's slots: before the draft, drafted, and the end of what can be read
+__device__ __forceinline__ void extent(const AttendArgs &a, int b, int64_t &n, int &use, int64_t &end) {
+    n = max(__ldg(a.length + b), 0);
+    use = a.count ? min(max(__ldg(a.count + b), 0), a.T) : a.T;
+    end = min(n + use, (int64_t)a.c.max_pages << a.c.page_shift);
+}
+__device__ __forceinline__ int tiles_of(const AttendArgs &a, int b) {
+    int64_t n, end;
+    int use;
+    extent(a, b, n, use, end);
+    return (int)max((int64_t)1, (end + TS - 1) / TS);   // an empty sequence's rows are written by one masked tile
 }
 
-// One block per (sequence, drafted token, query head): every warp walks every fourth slot with
-// its own running maximum and sum (lane l holds elements l, l + 32, ...), then the warps' parts
-// are joined.
-template <class T>
-__global__ void __launch_bounds__(32 * NW) k_attend(AttendArgs a) {
-    __shared__ float sm[NW], sl[NW], so[NW][128];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = a.c.head_dim;
-    const int64_t r = blockIdx.x;
-    const int h = (int)(r % a.heads);
-    const int64_t bt = r / a.heads;
-    const int b = (int)(bt / a.T), t = (int)(bt % a.T), kv = h / a.group;
-    const int64_t n = max(a.length[b], 0);
-    const int use = a.count ? min(max(a.count[b], 0), a.T) : a.T;
-    const T *q = (const T *)a.q + b * a.qb + t * a.qt + h * a.qh;
-    float qf[4], o[4] = {0, 0, 0, 0}, m = -INFINITY, l = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) qf[i] = lane + 32 * i < D ? fa_to_f32(q[lane + 32 * i]) * a.scale : 0.0f;
-    const int64_t end = t < use ? n + use : 0;
-    for (int64_t s = warp; s < end; s += NW) {
-        if (s >= n && a.mask) {
-            const int j = (int)(s - n);
-            if (!(a.mask[bt * a.words + j / 64] >> (j % 64) & 1)) continue;
-        }
-        const int64_t row = a.c.row(b, s, kv);
-        if (row < 0) continue;
-        float x = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (lane + 32 * i < D) x += qf[i] * cached(a.c.k, a.c.k_scale, a.format, row, D, lane + 32 * i);
-        x = fa_warp_sum(x);
-        const float m2 = fmaxf(m, x), w = expf(m - m2), p = expf(x - m2);
-        l = l * w + p;
-        m = m2;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (lane + 32 * i < D) o[i] = o[i] * w + p * cached(a.c.v, a.c.v_scale, a.format, row, D, lane + 32 * i);
+constexpr int RUNS = 64;
+struct Work {
+    int64_t cum[RUNS + 1];   // tiles of one (head, row block) before each of 64 runs of sequences
+};
+__device__ __forceinline__ int run_length(const AttendArgs &a) { return (a.B + RUNS - 1) / RUNS; }
+
+// all threads of the block, 64 at least
+__device__ __forceinline__ void plan(const AttendArgs &a, Work &w) {
+    const int tid = threadIdx.x, per = run_length(a);
+    if (tid < RUNS) {
+        int64_t s = 0;
+        for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) s += tiles_of(a, b);
+        w.cum[tid] = s;
     }
-    if (lane == 0) { sm[warp] = m; sl[warp] = l; }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) so[warp][lane + 32 * i] = o[i];
     __syncthreads();
-    float mm = -INFINITY, ll = 0.0f;
-    for (int w = 0; w < NW; ++w) mm = fmaxf(mm, sm[w]);
-    float f[NW];
-    for (int w = 0; w < NW; ++w) {
-        f[w] = sm[w] == -INFINITY ? 0.0f : expf(sm[w] - mm);
-        ll += f[w] * sl[w];
+    if (tid < 32) {
+        const int64_t s0 = w.cum[2 * tid], s = s0 + w.cum[2 * tid + 1];
+        int64_t before = s;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t up = __shfl_up_sync(0xffffffffu, before, o);
+            if (tid >= o) before += up;
+        }
+        w.cum[2 * tid] = before - s;
+        w.cum[2 * tid + 1] = before - s + s0;
+        if (tid == 31) w.cum[RUNS] = before;
     }
-    const int d = threadIdx.x;
-    if (d < D) {
-        float y = 0.0f;
-        for (int w = 0; w < NW; ++w)
-            if (f[w] > 0.0f) y += f[w] * so[w][d];
-        ((T *)a.out)[r * D + d] = fa_from_f32<T>(ll > 0.0f ? y / ll : mm == -INFINITY ? 0.0f : y / ll);
-    }
-    if (d == 0 && a.lse) a.lse[r] = mm == -INFINITY ? -INFINITY : mm + logf(ll);
+    __syncthreads();
 }
 
-// two partial results of up to 256 rows for each of 152 blocks
-size_t workspace_bytes(int head_dim) { return (size_t)152 * 2 * 256 * ((head_dim <= 64 ? 64 : 128) + 2) * sizeof(float); }
+struct Segment {
+    int b, head, block;       // the unit
+    int nt, t0, n;            // its tiles, the first of this segment, how many
+    int rows;                 // rows of the row block (up to 256)
+    bool two;                 // two row tiles over the same key/value tiles
+    int64_t slots;            // before the draft
+    int use;
+    int64_t end;
+};
+
+struct Walk {
+    int64_t g, g1, base;
+    int b, units;
+    __device__ __forceinline__ Walk(const AttendArgs &a, const Work &w, int cta, int ctas) {
+        units = a.c.kv_heads * a.blocks;
+        const int64_t total = w.cum[RUNS] * units;
+        ctas = (int)min(total, (int64_t)ctas);      // no run is empty
+        g = g1 = 0;
+        if (cta >= ctas) return;
+        g = total * cta / ctas;
+        g1 = total * (cta + 1) / ctas;
+        int lo = 0, hi = RUNS;                      // the last run that starts at or before g
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (w.cum[mid] * units <= g) lo = mid; else hi = mid;
+        }
+        b = lo * run_length(a);
+        base = w.cum[lo] * units;
+        while (true) {
+            const int64_t next = base + (int64_t)tiles_of(a, b) * units;
+            if (g < next) break;
+            base = next;
+            ++b;
+        }
+    }
+    __device__ __forceinline__ bool next(const AttendArgs &a, Segment &s) {
+        if (g >= g1) return false;
+        extent(a, b, s.slots, s.use, s.end);
+        s.b = b;
+        s.nt = (int)max((int64_t)1, (s.end + TS - 1) / TS);
+        const int64_t off = g - base;
+        const int u = (int)(off / s.nt);
+        s.t0 = (int)(off - (int64_t)u * s.nt);
+        s.head = u / a.blocks;
+        s.block = u % a.blocks;
+        s.n = (int)min((int64_t)(s.nt - s.t0), g1 - g);
+        s.rows = min(a.rows - 256 * s.block, 256);
+        s.two = s.rows > TS;
+        g += s.n;
+        if (g >= base + (int64_t)s.nt * units) { base += (int64_t)s.nt * units; ++b; }
+        return true;
+    }
+};
+
+// The order in which a segment's key and value tiles are consumed: with two row tiles K0 V0 K1 V1
+// ...; with alternating streams K0 K1 V0 K2 V1 ... (the next tile's scores are started before the
+// previous tile's weights are ready).
+__device__ __forceinline__ void item_of(const Segment &s, int i, int &tile, bool &value) {
+    if (s.two || s.n == 1) { tile = i >> 1; value = i & 1; return; }
+    if (i < 2) { tile = i; value = false; return; }
+    const int j = (i - 2) >> 1;
+    value = !(i & 1) || j + 2 >= s.n;
+    tile = !(i & 1) ? j : j + 2 < s.n ? j + 2 : s.n - 1;
+}
+
+// ----------------------------------------------------------------------------- the kernel
+
+template <int DP> constexpr int LAG = DP == 64 ? 6 : 3;            // 16-bit tiles in flight before one is handed on
+
+template <int DP, bool E4M3>
+struct Shape {
+    static constexpr int TILE = TS * DP * 2;                       // a 16-bit tile in shared memory
+    static constexpr int NS = E4M3 ? (DP == 64 ? 4 : 3) : (DP == 64 ? 10 : 5);   // tiles in the ring
+    static constexpr int RAW = TS * DP, NR = E4M3 ? (DP == 64 ? 8 : 4) : 0;      // raw 8-bit tiles in flight
+    static constexpr int Q = 0, RING = 2 * TILE, RAWS = RING + NS * TILE, MISC = RAWS + NR * RAW;
+};
+
+struct Misc {
+    uint64_t full[10], empty[10], s_full[2], p_full[2], pv_done[2], q_full[2], done;
+    uint32_t tmem;
+    int fail;
+    int odd[8];                       // segment & 7: a drafted value is not finite
+    uint32_t held[2][4];              // per stream: which slots of its tile have a page
+};
+struct Scales { float k[2][TS], v[2][TS]; };   // per stream, of its tile
+
+template <int DP, bool E4M3> constexpr size_t smem_bytes() {
+    return Shape<DP, E4M3>::MISC + sizeof(Misc) + sizeof(Work) + (E4M3 ? sizeof(Scales) : 0);
+}
+
+// where chunk c (16 bytes = 8 elements) of row r lies in a 128-byte-swizzled tile: halves of 64
+// columns, rows of 128 bytes, the eight chunks of a row permuted by the row's low bits
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+    return (uint32_t)((c >> 3) * (TS * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+// zero the elements of eight 16-bit floats that are not finite; true if there was one
+template <class M> __device__ __forceinline__ bool zero_odd(uint4 &x) {
+    constexpr uint32_t em = sizeof(M) == 2 && std::is_same<M, __half>::value ? 0x7c00u : 0x7f80u;
+    uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if ((w[i] & em) == em) { w[i] &= 0xffff0000u; odd = true; }
+        if ((w[i] >> 16 & em) == em) { w[i] &= 0x0000ffffu; odd = true; }
+    }
+    x = make_uint4(w[0], w[1], w[2], w[3]);
+    return odd;
+}
+
+// which of the 32 slots from `first` on drafted token i of sequence b sees
+__device__ __forceinline__ uint32_t seen_bits(const AttendArgs &a, const Segment &s, int i, int64_t first) {
+    const int64_t d0 = first - s.slots;
+    if (d0 <= -32) return 0xffffffffu;
+    const int from = d0 < 0 ? 0 : (int)min(d0, (int64_t)s.use);
+    uint32_t v = 0xffffffffu;
+    if (a.mask && from < s.use) {
+        const uint64_t *m = a.mask + ((int64_t)s.b * a.T + i) * a.words;
+        const int w = from >> 6, sh = from & 63;
+        uint64_t x = __ldg(m + w) >> sh;
+        if (sh > 32 && w + 1 < a.words) x |= __ldg(m + w + 1) << (64 - sh);
+        v = (uint32_t)x;
+    }
+    const int left = s.use - from;
+    if (left < 32) v &= left > 0 ? (1u << left) - 1 : 0u;
+    if (d0 < 0) v = v << (int)-d0 | ((1u << (int)-d0) - 1);
+    return v;
+}
+
+// M: the tensor cores' 16-bit type; T: q's and out's
+template <int DP, bool E4M3, class T, class M>
+__global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
+    using S = Shape<DP, E4M3>;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    constexpr size_t MISC = S::MISC + (E4M3 ? sizeof(Scales) : 0);
+    static_assert(S::MISC % 16 == 0 && MISC % 8 == 0 && sizeof(Misc) % 8 == 0, "alignment of the parts");
+    Scales &sc = *reinterpret_cast<Scales *>(smem + S::MISC);       // first: read in 16-byte pieces
+    Misc &sh = *reinterpret_cast<Misc *>(smem + MISC);
+    Work &work = *reinterpret_cast<Work *>(smem + MISC + sizeof(Misc));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    constexpr bool F16 = std::is_same<M, __half>::value;
+    constexpr float OFF = F16 ? 4.0f : 0.0f;          // fp16 weights reach 2^10 above and 2^-28 below a row's largest
+    const int D = a.c.head_dim;
+    volatile int *fail = &sh.fail;
+    if (smem_u32(smem) & 1023) {           // the swizzled tiles need it
+        if (tid == 0) a.status[blockIdx.x] = 1;
+        return;
+    }
+
+    plan(a, work);
+    if (tid == 0) {
+        for (int i = 0; i < S::NS; ++i) { mbar_init(&sh.full[i], NLOAD); mbar_init(&sh.empty[i], 1); }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.p_full[i], TS);
+            mbar_init(&sh.pv_done[i], 1);
+            mbar_init(&sh.q_full[i], TS);
+        }
+        mbar_init(&sh.done, 1);
+        sh.fail = 0;
+        for (int i = 0; i < 8; ++i) sh.odd[i] = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 15) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    Walk walk(a, work, blockIdx.x, gridDim.x);
+    Segment s;
+
+    if (warp == 15) {
+        if (lane == 0) {
+            // ---- the MMAs
+            constexpr uint32_t fmt = F16 ? 0u : 1u;
+            constexpr uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(TS >> 4) << 24);
+            constexpr uint32_t idesc_s = idesc | ((uint32_t)(TS >> 3) << 17);                 // S: N = 128 slots
+            constexpr uint32_t idesc_o = idesc | ((uint32_t)(DP >> 3) << 17) | (1u << 16);    // O: N = DP, V is MN-major
+            int it = 0, nq[2] = {0, 0}, np[2] = {0, 0};
+            const uint32_t q0 = smem_u32(smem + S::Q), ring = smem_u32(smem + S::RING);
+            auto next_tile = [&]() -> int {
+                const int slot = it % S::NS;
+                if (!mbar_wait(&sh.full[slot], (uint32_t)(it / S::NS) & 1, fail)) return -1;
+                ++it;
+                return slot;
+            };
+            auto scores = [&](int st, int slot) {
+                const uint32_t qa = q0 + st * S::TILE, ka = ring + slot * S::TILE;
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k) {
+                    const uint32_t off = (k >> 2) * (TS * 128) + (k & 3) * 32;
+                    umma_ss(tmem + st * TS, umma_desc(qa + off, 16, 1024), umma_desc(ka + off, 16, 1024), idesc_s, k > 0);
+                }
+                umma_commit(&sh.s_full[st]);
+            };
+            auto values = [&](int st, int slot, bool first) {
+                const uint32_t va = ring + slot * S::TILE;
+#pragma unroll
+                for (int k = 0; k < TS / 16; ++k)
+                    umma_ts(tmem + 256 + st * DP, tmem + st * TS + k * 8, umma_desc(va + k * 2048, TS * 128, 1024), idesc_o,
+                            !first || k > 0);
+                umma_commit(&sh.pv_done[st]);
+            };
+            auto wait_p = [&](int st) {
+                const bool ok = mbar_wait(&sh.p_full[st], (uint32_t)np[st] & 1, fail);
+                ++np[st];
+                tc_fence_after();
+                return ok;
+            };
+            while (!*fail && walk.next(a, s)) {
+                const int streams = s.two || s.n > 1 ? 2 : 1;
+                bool ok = true;
+                for (int st = 0; st < streams; ++st) ok &= mbar_wait(&sh.q_full[st], (uint32_t)nq[st]++ & 1, fail);
+                if (!ok) break;
+                tc_fence_after();
+                int slot;
+                if (s.two) {
+                    if ((slot = next_tile()) < 0) break;
+                    scores(0, slot);
+                    scores(1, slot);
+                    umma_commit(&sh.empty[slot]);
+                    for (int j = 0; j < s.n && ok; ++j) {
+                        const int vs = next_tile();
+                        if (vs < 0 || !wait_p(0)) { ok = false; break; }
+                        values(0, vs, j == 0);
+                        int ks = -1;
+                        if (j + 1 < s.n) {
+                            if ((ks = next_tile()) < 0) { ok = false; break; }
+                            scores(0, ks);
+                        }
+                        if (!wait_p(1)) { ok = false; break; }
+                        values(1, vs, j == 0);
+                        umma_commit(&sh.empty[vs]);
+                        if (ks >= 0) {
+                            scores(1, ks);
+                            umma_commit(&sh.empty[ks]);
+                        }
+                    }
+                } else {
+                    for (int j = 0; j < streams && ok; ++j) {
+                        if ((slot = next_tile()) < 0) { ok = false; break; }
+                        scores(j, slot);
+                        umma_commit(&sh.empty[slot]);
+                    }
+                    for (int j = 0; j < s.n && ok; ++j) {
+                        const int st = j & 1;
+                        if ((slot = next_tile()) < 0 || !wait_p(st)) { ok = false; break; }
+                        values(st, slot, j < 2);
+                        umma_commit(&sh.empty[slot]);
+                        if (j + 2 < s.n) {
+                            if ((slot = next_tile()) < 0) { ok = false; break; }
+                            scores(st, slot);
+                            umma_commit(&sh.empty[slot]);
+                        }
+                    }
+                }
+                if (!ok) break;
+            }
+            umma_commit(&sh.done);   // completes once every MMA issued above has
+        }
+    } else if (warp >= 8) {
+        // ---- loading
+        const int lt = tid - 256;
+        const uint32_t ring = smem_u32(smem + S::RING);
+        constexpr int CPR = DP / 8;                                 // 16-byte chunks of a 16-bit row
+        int it = 0, seg = 0;
+        auto wait_empty = [&](int i) {
+            return i < S::NS || mbar_wait(&sh.empty[i % S::NS], (uint32_t)(i / S::NS - 1) & 1, fail);
+        };
+        if constexpr (!E4M3) {
+            bool ok = true;
+            while (ok && walk.next(a, s)) {
+                for (int i = 0; i < 2 * s.n; ++i, ++it) {
+                    int tile;
+                    bool value;
+                    item_of(s, i, tile, value);
+                    if (!(ok = wait_empty(it))) break;
+                    const int64_t first = (int64_t)(s.t0 + tile) * TS;
+                    const T *src = (const T *)(value ? a.c.v : a.c.k);
+                    const uint32_t dst = ring + (it % S::NS) * S::TILE;
+                    const bool draft = value && first + TS > s.slots;   // drafted values may be hidden from some rows
+#pragma unroll
+                    for (int q = 0; q < (TS * CPR + NLOAD - 1) / NLOAD; ++q) {
+                        const int x = lt + q * NLOAD;
+                        if (x >= TS * CPR) break;
+                        const int r = x / CPR, c = x % CPR;
+                        const int64_t row = first + r < s.end ? a.c.row(s.b, first + r, s.head) : -1;
+                        const bool there = row >= 0 && c * 8 < D;
+                        const T *p = src + (there ? row * D + c * 8 : 0);
+                        if (!draft) {
+                            cp_async16(dst + chunk_at(r, c), p, there);
+                        } else {
+                            uint4 v = there ? __ldg(reinterpret_cast<const uint4 *>(p)) : make_uint4(0, 0, 0, 0);
+                            if (first + r >= s.slots && zero_odd<M>(v)) sh.odd[seg & 7] = 1;
+                            *reinterpret_cast<uint4 *>(smem + S::RING + (it % S::NS) * S::TILE + chunk_at(r, c)) = v;
+                        }
+                    }
+                    cp_commit();
+                    if (it >= LAG<DP>) {
+                        cp_wait<LAG<DP>>();
+                        proxy_fence();
+                        mbar_arrive(&sh.full[(it - LAG<DP>) % S::NS]);
+                    }
+                }
+                ++seg;
+            }
+            cp_wait<0>();
+            proxy_fence();
+            if (ok)
+                for (int i = max(it - LAG<DP>, 0); i < it; ++i) mbar_arrive(&sh.full[i % S::NS]);
+        } else {
+            // raw codes arrive NR - 1 tiles ahead, each thread converting the chunks it copied
+            Walk ahead = walk;
+            Segment sa;
+            sa.n = 0;
+            int ia = 0, issued = 0;
+            const uint32_t raws = smem_u32(smem + S::RAWS);
+            constexpr int RPR = DP / 16, ITER = (TS * RPR + NLOAD - 1) / NLOAD;   // 16-byte chunks of a row of codes
+            auto issue = [&]() {
+                if (ia == 2 * sa.n) {
+                    ia = 0;
+                    if (!ahead.next(a, sa)) { sa.n = 0; cp_commit(); return; }
+                }
+                int tile;
+                bool value;
+                item_of(sa, ia++, tile, value);
+                const int64_t first = (int64_t)(sa.t0 + tile) * TS;
+                const uint8_t *src = (const uint8_t *)(value ? a.c.v : a.c.k);
+                const uint32_t dst = raws + (issued % S::NR) * S::RAW;
+#pragma unroll
+                for (int q = 0; q < ITER; ++q) {
+                    const int x = lt + q * NLOAD;
+                    if (x >= TS * RPR) break;
+                    const int r = x / RPR, c = x % RPR;
+                    const int64_t row = first + r < sa.end ? a.c.row(sa.b, first + r, sa.head) : -1;
+                    const bool there = row >= 0 && c * 16 < D;
+                    cp_async16(dst + x * 16, src + (there ? row * D + c * 16 : 0), there);
+                }
+                cp_commit();
+                ++issued;
+            };
+            for (int i = 0; i < S::NR - 1; ++i) issue();
+            bool ok = true;
+            while (ok && walk.next(a, s)) {
+                for (int i = 0; i < 2 * s.n; ++i, ++it) {
+                    int tile;
+                    bool value;
+                    item_of(s, i, tile, value);
+                    issue();
+                    cp_wait<S::NR - 1>();
+                    if (!(ok = wait_empty(it))) break;
+                    const int64_t first = (int64_t)(s.t0 + tile) * TS;
+                    const bool draft = value && first + TS > s.slots;
+                    const unsigned char *raw = smem + S::RAWS + (it % S::NR) * S::RAW;
+                    unsigned char *dst = smem + S::RING + (it % S::NS) * S::TILE;
+#pragma unroll
+                    for (int q = 0; q < ITER; ++q) {
+                        const int x = lt + q * NLOAD;
+                        if (x >= TS * RPR) break;
+                        const int r = x / RPR, c = x % RPR;
+                        const uint4 w = *reinterpret_cast<const uint4 *>(raw + x * 16);
+                        uint4 lo = make_uint4(fa_e4m3x2_to_half2(w.x), fa_e4m3x2_to_half2(w.x >> 16),
+                                              fa_e4m3x2_to_half2(w.y), fa_e4m3x2_to_half2(w.y >> 16));
+                        uint4 hi = make_uint4(fa_e4m3x2_to_half2(w.z), fa_e4m3x2_to_half2(w.z >> 16),
+                                              fa_e4m3x2_to_half2(w.w), fa_e4m3x2_to_half2(w.w >> 16));
+                        if (draft && first + r >= s.slots) {
+                            const bool o1 = zero_odd<M>(lo), o2 = zero_odd<M>(hi);
+                            if (o1 || o2) sh.odd[seg & 7] = 1;
+                        }
+                        *reinterpret_cast<uint4 *>(dst + chunk_at(r, 2 * c)) = lo;
+                        *reinterpret_cast<uint4 *>(dst + chunk_at(r, 2 * c + 1)) = hi;
+                    }
+                    proxy_fence();
+                    mbar_arrive(&sh.full[it % S::NS]);
+                }
+                ++seg;
+            }
+            cp_wait<0>();
+        }
+    } else {
+        // ---- softmax: stream st, row r of its tile
+        const int st = warp >> 2, r = tid & 127;
+        const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t ts = tmem + lane_base + st * TS, to = tmem + lane_base + 256 + st * DP;
+        int ns = 0, npv = 0, seg = 0;
+        float *given = reinterpret_cast<float *>(smem + S::Q + S::TILE);   // stream 1's statistics, where its Q was
+        while (walk.next(a, s)) {
+            const int step = s.two ? 1 : 2, begin = s.two ? 0 : st, mine = s.two ? s.n : (s.n + 1 - st) / 2;
+            const int sg = seg++;
+            if (mine <= 0) continue;                       // a single tile: stream 1 has none
+            const int row = (s.two ? st * TS : 0) + r;     // of the row block
+            const bool live = row < s.rows;
+            const bool warp_live = row - lane < s.rows;    // the same for the whole warp
+            const int rr = 256 * s.block + row, ti = live ? rr / a.group : 0;
+            const int hq = s.head * a.group + (live ? rr - ti * a.group : 0);
+            const bool used = live && ti < s.use;
+            float c = a.scale * kLog2e;
+            {
+                // the row of Q into the stream's tile
+                const T *q = (const T *)a.q + s.b * a.qb + ti * a.qt + hq * a.qh;
+                unsigned char *dst = smem + S::Q + st * S::TILE;
+                float pow = 1.0f;
+                if (E4M3) {
+                    float top = 0.0f;
+                    if (live)
+                        for (int ch = 0; ch < D / 8; ++ch) {
+                            float f[8];
+                            fa_unpack(__ldg(reinterpret_cast<const uint4 *>(q) + ch), f, T());
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
+                        }
+                    // the largest element to [2^8, 2^9)
+                    const int e = top > 0.0f && top < INFINITY ? max(min(fa_exponent(top) - 8, 120), -120) : 0;
+                    pow = fa_pow2(-e);
+                    c *= fa_pow2(e);
+                }
+#pragma unroll 4
+                for (int ch = 0; ch < DP / 8; ++ch) {
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (live && ch < D / 8) {
+                        v = __ldg(reinterpret_cast<const uint4 *>(q) + ch);
+                        if (E4M3) {
+                            float f[8];
+                            fa_unpack(v, f, T());
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) f[e] *= pow;
+                            v = fa_pack(f, M());
+                        }
+                    }
+                    *reinterpret_cast<uint4 *>(dst + chunk_at(r, ch)) = v;
+                }
+                proxy_fence();
+                mbar_arrive(&sh.q_full[st]);
+            }
+            float m = -INFINITY, l = 0.0f, bias = 0.0f;
+            int ev = -120;
+            // slot r of each tile: whether it is held and its scales, one tile ahead
+            float ks = 0.0f, vs = 0.0f;
+            bool there = false;
+            auto fetch = [&](int tile) {
+                const int64_t slot = (int64_t)(s.t0 + tile) * TS + r;
+                const int64_t at = slot < s.end ? a.c.row(s.b, slot, s.head) : -1;
+                there = at >= 0;
+                if (E4M3) {
+                    ks = there ? __ldg(a.c.k_scale + at) : 0.0f;
+                    vs = there ? __ldg(a.c.v_scale + at) : 0.0f;
+                }
+            };
+            fetch(begin);
+            for (int q = 0; q < mine; ++q) {
+                const int tile = begin + q * step;
+                const int64_t first = (int64_t)(s.t0 + tile) * TS;
+                const uint32_t got = __ballot_sync(0xffffffffu, there);
+                if (q > 0) bar_sync(1 + st, TS);          // the previous tile's have been read
+                if (lane == 0) sh.held[st][warp & 3] = got;
+                if (E4M3) { sc.k[st][r] = ks; sc.v[st][r] = vs; }
+                if (q + 1 < mine) fetch(tile + step);
+                bar_sync(1 + st, TS);
+                uint32_t held[4];
+                bool whole = first + TS <= s.slots;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    held[w] = sh.held[st][w];
+                    whole &= held[w] == 0xffffffffu;
+                }
+                mbar_wait(&sh.s_full[st], (uint32_t)ns++ & 1, fail);
+                __syncwarp();
+                tc_fence_after();
+                if (warp_live) {
+                    uint32_t see[4];
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) see[w] = whole ? 0xffffffffu : used ? held[w] & seen_bits(a, s, ti, first + 32 * w) : 0u;
+                    float mx = -INFINITY, vmx = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        float x[32];
+                        tmem_ld32(ts + 32 * w, x);
+                        if (E4M3) {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                const float4 f = *reinterpret_cast<const float4 *>(&sc.k[st][32 * w + e]);
+                                const float4 g = *reinterpret_cast<const float4 *>(&sc.v[st][32 * w + e]);
+                                x[e] *= f.x; x[e + 1] *= f.y; x[e + 2] *= f.z; x[e + 3] *= f.w;
+                                if (whole) {
+                                    vmx = fmaxf(vmx, fmaxf(fmaxf(g.x, g.y), fmaxf(g.z, g.w)));
+                                } else {
+                                    if (see[w] >> e & 1) vmx = fmaxf(vmx, g.x);
+                                    if (see[w] >> (e + 1) & 1) vmx = fmaxf(vmx, g.y);
+                                    if (see[w] >> (e + 2) & 1) vmx = fmaxf(vmx, g.z);
+                                    if (see[w] >> (e + 3) & 1) vmx = fmaxf(vmx, g.w);
+                                }
+                            }
+                        }
+                        if (whole) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) mx = fmaxf(mx, x[e]);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) mx = fmaxf(mx, (see[w] >> e & 1) ? x[e] : -INFINITY);
+                        }
+                    }
+                    const int e2 = E4M3 ? max(ev, min(max(fa_exponent(vmx) + 1, -120), 120)) : 0;
+                    const bool move = mx > -INFINITY && ((mx - m) * c > kGrow || e2 > ev || m == -INFINITY);
+                    if (__any_sync(0xffffffffu, move)) {
+                        float f = 1.0f;
+                        if (move) {
+                            const bool had = m > -INFINITY;
+                            m = fmaxf(m, mx);
+                            if (E4M3) ev = e2;
+                            const float b2 = m * c + (E4M3 ? (float)ev : 0.0f) - OFF;
+                            f = had ? ex2(bias - b2) : 0.0f;
+                            bias = b2;
+                            l *= f;
+                        }
+                        if (q > 0) {
+                            // the previous tile's values have been added
+                            mbar_wait(&sh.pv_done[st], (uint32_t)(npv - 1) & 1, fail);
+                            __syncwarp();
+                            tc_fence_after();
+#pragma unroll
+                            for (int w = 0; w < DP / 32; ++w) {
+                                float o[32];
+                                tmem_ld32(to + 32 * w, o);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] *= f;
+                                tmem_st32(to + 32 * w, o);
+                            }
+                        }
+                    }
+                    float sum[4] = {0, 0, 0, 0};
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        float x[32];
+                        uint32_t p[16];
+                        tmem_ld32(ts + 32 * w, x);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            float4 f = make_float4(1, 1, 1, 1), g = f;
+                            if (E4M3) {
+                                f = *reinterpret_cast<const float4 *>(&sc.k[st][32 * w + e]);
+                                g = *reinterpret_cast<const float4 *>(&sc.v[st][32 * w + e]);
+                                x[e] *= f.x; x[e + 1] *= f.y; x[e + 2] *= f.z; x[e + 3] *= f.w;
+                            }
+                            float y[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                y[j] = ex2(fmaf(x[e + j], c, -bias));
+                                if (!whole && !(see[w] >> (e + j) & 1)) y[j] = 0.0f;
+                                sum[j] += y[j];
+                            }
+                            if (E4M3) {
+                                y[0] *= g.x; y[1] *= g.y; y[2] *= g.z; y[3] *= g.w;
+                                if (!whole) {
+#pragma unroll
+                                    for (int j = 0; j < 4; ++j)
+                                        if (!(see[w] >> (e + j) & 1)) y[j] = 0.0f;   // whatever the scale is
+                                }
+                            }
+                            p[e / 2] = fa_pack2(y[0], y[1], M());
+                            p[e / 2 + 1] = fa_pack2(y[2], y[3], M());
+                        }
+                        tmem_st16(ts + 16 * w, p);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tmem_st_wait();
+                }
+                tc_fence_before();
+                mbar_arrive(&sh.p_full[st]);
+                ++npv;
+            }
+            // ---- the segment's result
+            mbar_wait(&sh.pv_done[st], (uint32_t)(npv - 1) & 1, fail);
+            __syncwarp();
+            tc_fence_after();
+            const bool join = !s.two && s.n > 1;
+            float f0 = 1.0f, f1 = 0.0f;
+            if (join) {
+                if (st == 1) { given[r] = bias; given[TS + r] = l; tc_fence_before(); }
+                bar_sync(3, 2 * TS);
+                tc_fence_after();
+                if (st == 0) {
+                    const float b1 = given[r], l1 = given[TS + r];
+                    const bool h0 = !(l == 0.0f), h1 = !(l1 == 0.0f);   // a stream that saw something (or NaN)
+                    const float top = h0 && h1 ? fmaxf(bias, b1) : h1 ? b1 : bias;
+                    f0 = h0 ? ex2(bias - top) : 0.0f;
+                    f1 = h1 ? ex2(b1 - top) : 0.0f;
+                    l = l * f0 + l1 * f1;
+                    bias = top;
+                }
+            }
+            if (st == 0 || s.two) {
+                const bool partial = s.n < s.nt;
+                const bool odd = sh.odd[sg & 7] != 0;
+                // the block's first segment uses its first partial slot, its last the second
+                const int64_t prow = ((int64_t)blockIdx.x * 2 + (sg == 0 ? 0 : 1)) * 256 + row;
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                const int64_t orow = ((int64_t)s.b * a.T + ti) * a.heads + hq;
+                if (warp_live) {
+#pragma unroll
+                    for (int w = 0; w < DP / 32; ++w) {
+                        float o[32];
+                        __syncwarp();
+                        tmem_ld32(to + 32 * w, o);
+                        if (join) {
+                            float o1[32];
+                            tmem_ld32(to + DP + 32 * w, o1);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = o[e] * f0 + o1[e] * f1;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = used && l != 0.0f ? o[e] * inv : 0.0f;
+                        if (odd && used) {
+                            // drafted values that are not finite were left out of the product
+                            for (int j = 0; j < s.use; ++j) {
+                                const int64_t slot = s.slots + j;
+                                if (slot < (int64_t)s.t0 * TS || slot >= (int64_t)(s.t0 + s.n) * TS || slot >= s.end) continue;
+                                if (!(seen_bits(a, s, ti, slot) & 1)) continue;
+                                const int64_t at = a.c.row(s.b, slot, s.head);
+                                if (at < 0) continue;
+                                for (int e = 0; e < 32 && 32 * w + e < D; ++e) {
+                                    const int64_t x = at * D + 32 * w + e;
+                                    float y;
+                                    if (E4M3) y = (((const uint8_t *)a.c.v)[x] & 0x7f) == 0x7f ? NAN : 0.0f;
+                                    else y = fa_to_f32(((const T *)a.c.v)[x]);
+                                    if (!isfinite(y)) {
+#pragma unroll
+                                        for (int k = 0; k < 32; ++k)
+                                            if (k == e) o[k] += y;
+                                    }
+                                }
+                            }
+                        }
+                        if (live) {
+                            if (partial) {
+                                float4 *dst = reinterpret_cast<float4 *>(a.part_o + prow * DP + 32 * w);
+#pragma unroll
+                                for (int e = 0; e < 32; e += 4) dst[e / 4] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                            } else {
+                                T *dst = (T *)a.out + orow * D + 32 * w;
+#pragma unroll
+                                for (int e = 0; e < 32; e += 8) {
+                                    const float f[8] = {o[e], o[e + 1], o[e + 2], o[e + 3], o[e + 4], o[e + 5], o[e + 6], o[e + 7]};
+                                    if (32 * w + e < D) *reinterpret_cast<uint4 *>(dst + e) = fa_pack(f, T());
+                                }
+                            }
+                        }
+                    }
+                }
+                if (live) {
+                    const float lse = used && l != 0.0f ? bias + log2f(l) : -INFINITY;
+                    if (partial) a.part_lse[prow] = lse;
+                    else if (a.lse) a.lse[orow] = lse * kLn2;
+                }
+            }
+            tc_fence_before();
+            // stream 1 may go on: its accumulator has been read, and so has the segment's flag
+            if (join || s.two) bar_sync(3, 2 * TS);
+            else bar_sync(1 + st, TS);
+            if (tid == 0) sh.odd[sg & 7] = 0;
+        }
+    }
+    __syncwarp();
+    // the MMAs issued have completed before tensor memory is released
+    mbar_wait(&sh.done, 0, fail);
+    tc_fence_after();
+    __syncthreads();
+    if (tid == 0) a.status[blockIdx.x] = sh.fail;
+    if (warp == 15) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// Joins the parts of units that were cut, in the order of their slots.  Block (unit, 32 rows); a
+// warp per row, lanes across the columns.
+template <int DP, class T>
+__global__ void __launch_bounds__(256) k_attend_join(AttendArgs a, int ctas) {
+    __shared__ Work work;
+    __shared__ int64_t before;
+    plan(a, work);
+    const int units = a.c.kv_heads * a.blocks;
+    const int64_t id = blockIdx.x;
+    const int b = (int)(id / units), u = (int)(id % units);
+    if (threadIdx.x == 0) {
+        const int per = run_length(a);
+        int64_t g = work.cum[b / per];
+        for (int i = b / per * per; i < b; ++i) g += tiles_of(a, i);
+        before = g;
+    }
+    __syncthreads();
+    const int nt = tiles_of(a, b);
+    const int64_t total = work.cum[RUNS] * units, g0 = before * units + (int64_t)u * nt, g1 = g0 + nt - 1;
+    ctas = (int)min(total, (int64_t)ctas);
+    const int c0 = (int)(((g0 + 1) * ctas - 1) / total), c1 = (int)(((g1 + 1) * ctas - 1) / total);
+    const int lane = threadIdx.x & 31, head = u / a.blocks, block = u % a.blocks;
+    const int rows = min(a.rows - 256 * block, 256), D = a.c.head_dim;
+    bool failed = false;
+    for (int c = c0; c <= c1; ++c) failed |= a.status[c] != 0;
+    if (c0 == c1 && !failed) return;
+    const int slot0 = total * c0 / ctas == g0 ? 0 : 1;
+    for (int row = blockIdx.y * 32 + (threadIdx.x >> 5); row < min(rows, (int)blockIdx.y * 32 + 32); row += 8) {
+        float top = -INFINITY, l = 0.0f, o[DP / 32];
+#pragma unroll
+        for (int i = 0; i < DP / 32; ++i) o[i] = 0.0f;
+        for (int c = c0; c <= c1; ++c) {
+            const float x = a.part_lse[((int64_t)c * 2 + (c == c0 ? slot0 : 0)) * 256 + row];
+            if (!(x <= top)) top = x;          // NaN stays
+        }
+        if (c0 != c1)
+            for (int c = c0; c <= c1; ++c) {
+                const int64_t at = ((int64_t)c * 2 + (c == c0 ? slot0 : 0)) * 256 + row;
+                const float x = a.part_lse[at];
+                if (x == -INFINITY) continue;
+                const float f = ex2(x - top);
+                l += f;
+#pragma unroll
+                for (int i = 0; i < DP / 32; ++i) o[i] += f * a.part_o[at * DP + lane * (DP / 32) + i];
+            }
+        const int rr = 256 * block + row, ti = rr / a.group;
+        const int64_t orow = ((int64_t)b * a.T + ti) * a.heads + head * a.group + rr % a.group;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+        for (int i = 0; i < DP / 32; ++i) {
+            const int d = lane * (DP / 32) + i;
+            if (d < D) ((T *)a.out)[orow * D + d] = fa_from_f32<T>(failed ? NAN : o[i] * inv);
+        }
+        if (lane == 0 && a.lse) a.lse[orow] = failed ? NAN : l == 0.0f ? -INFINITY : (top + log2f(l)) * kLn2;
+    }
+}
+
+// two partial results of up to 256 rows and a status for each block
+size_t workspace_bytes(int head_dim) {
+    const size_t dp = head_dim <= 64 ? 64 : 128;
+    return (size_t)MAX_CTAS * 2 * 256 * (dp + 1) * sizeof(float) + MAX_CTAS * sizeof(int);
+}
+
+template <int DP, bool E4M3, class T, class M>
+fa_status launch(const AttendArgs &a, cudaStream_t s) {
+    constexpr size_t smem = smem_bytes<DP, E4M3>();
+    static_assert(smem <= 232448, "shared memory of a block");
+    int dev = 0, n_sm = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(k_attend<DP, E4M3, T, M>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return fa_refuse("fa_tree_attention", cudaGetErrorString(e), FA_ERR_CUDA);
+    const int ctas = std::min(n_sm, MAX_CTAS);
+    k_attend<DP, E4M3, T, M><<<ctas, NTHR, smem, s>>>(a);
+    fa_status st = fa_launch_check("tree attention");
+    if (st != FA_OK) return st;
+    const int64_t units = (int64_t)a.B * a.c.kv_heads * a.blocks;
+    k_attend_join<DP, T><<<dim3((unsigned)units, (unsigned)((std::min(a.rows, 256) + 31) / 32)), 256, 0, s>>>(a, ctas);
+    return fa_launch_check("tree attention join");
+}
 
 fa_status sizes(const char *fn, int32_t B, int32_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
     if (B < 0 || B > 65535 || T < 0 || T > FA_MAX_DRAFT) return fa_refuse(fn, "B or T out of range");
     if (kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads) return fa_refuse(fn, "q_heads must be a multiple of kv_heads");
-    if ((int64_t)B * T * q_heads > 2147483647) return fa_refuse(fn, "B * T * q_heads out of range");
+    if ((int64_t)B * std::max(T, 1) * q_heads > 2147483647) return fa_refuse(fn, "B * T * q_heads out of range");
     if (head_dim < 16 || head_dim % 16) return fa_refuse(fn, "head_dim must be a multiple of 16");
     if (head_dim > 128) return fa_refuse(fn, "head_dim above 128", FA_ERR_UNSUPPORTED);
     return FA_OK;
@@ -120,19 +989,33 @@ extern "C" fa_status fa_tree_attention(const fa_kv_cache *cache, int32_t dtype, 
     if (dtype != FA_DTYPE_F16 && dtype != FA_DTYPE_BF16) return fa_refuse(fn, "q must be fp16 or bf16", FA_ERR_UNSUPPORTED);
     if (cache->format != FA_CACHE_E4M3 && cache->format != dtype)
         return fa_refuse(fn, "a 16-bit cache must have the type of q", FA_ERR_UNSUPPORTED);
+    if (!(scale > 0.0f && scale < INFINITY)) return fa_refuse(fn, "scale must be positive and finite");
+    if (((int64_t)max_pages << a.c.page_shift) > 2147483647LL - 4096) return fa_refuse(fn, "max_pages * page_size out of range");
     if (B == 0 || T == 0) return FA_OK;
     if (!q || !out || !length) return fa_refuse(fn, "NULL buffer");
-    if (((uintptr_t)q | (uintptr_t)out) & 15 || (q_batch_stride | q_token_stride | q_head_stride) & 7)
+    if ((((uintptr_t)q | (uintptr_t)out) & 15) || ((q_batch_stride | q_token_stride | q_head_stride) & 7))
         return fa_refuse(fn, "q and out must be 16-byte aligned, with strides that are multiples of 8");
     const size_t need = workspace_bytes(cache->head_dim);
     if (ws_bytes < need || !workspace)
         return fa_refuse(fn, ("workspace needs " + std::to_string(need) + " bytes").c_str(), FA_ERR_WORKSPACE_TOO_SMALL);
     if ((uintptr_t)workspace & 255) return fa_refuse(fn, "workspace not 256-byte aligned");
-    a.format = cache->format; a.T = T; a.heads = q_heads; a.group = q_heads / cache->kv_heads; a.words = (T + 63) / 64;
+    a.B = B; a.T = T; a.heads = q_heads; a.group = q_heads / cache->kv_heads; a.words = (T + 63) / 64;
+    if ((int64_t)T * a.group > 1 << 24) return fa_refuse(fn, "T * group out of range");
+    a.rows = T * a.group;
+    a.blocks = (a.rows + 255) / 256;
+    if ((int64_t)B * cache->kv_heads * a.blocks > 2147483647) return fa_refuse(fn, "B * kv_heads out of range");
     a.q = q; a.qb = q_batch_stride; a.qt = q_token_stride; a.qh = q_head_stride;
     a.length = length; a.count = count; a.mask = mask; a.scale = scale; a.out = out; a.lse = lse;
-    const unsigned grid = (unsigned)((int64_t)B * T * q_heads);
-    if (dtype == FA_DTYPE_F16) k_attend<__half><<<grid, 32 * NW, 0, (cudaStream_t)stream>>>(a);
-    else k_attend<__nv_bfloat16><<<grid, 32 * NW, 0, (cudaStream_t)stream>>>(a);
-    return fa_launch_check("tree attention");
+    const size_t dp = cache->head_dim <= 64 ? 64 : 128;
+    a.part_o = (float *)workspace;
+    a.part_lse = a.part_o + (size_t)MAX_CTAS * 2 * 256 * dp;
+    a.status = (int *)(a.part_lse + (size_t)MAX_CTAS * 2 * 256);
+    cudaStream_t s = (cudaStream_t)stream;
+    const bool f16 = dtype == FA_DTYPE_F16;
+    if (cache->format == FA_CACHE_E4M3) {
+        if (dp == 64) return f16 ? launch<64, true, __half, __half>(a, s) : launch<64, true, __nv_bfloat16, __half>(a, s);
+        return f16 ? launch<128, true, __half, __half>(a, s) : launch<128, true, __nv_bfloat16, __half>(a, s);
+    }
+    if (dp == 64) return f16 ? launch<64, false, __half, __half>(a, s) : launch<64, false, __nv_bfloat16, __nv_bfloat16>(a, s);
+    return f16 ? launch<128, false, __half, __half>(a, s) : launch<128, false, __nv_bfloat16, __nv_bfloat16>(a, s);
 }
