@@ -24,8 +24,8 @@
 // whatever the lengths, which are read on the device.  A unit that is cut by the runs leaves
 // partial results, joined by a second small kernel in a fixed order.
 //
-// Roles (16 warps): warps 0-7 the two softmax warpgroups (a thread per row), warps 8-14 load and
-// convert (16-byte asynchronous copies into 128-byte-swizzled tiles), warp 15 issues the MMAs:
+// Roles (17 warps): warps 0-7 the two softmax warpgroups (a thread per row), warps 8-15 load and
+// convert (16-byte asynchronous copies into 128-byte-swizzled tiles), warp 16 issues the MMAs:
 // S = Q K^T (both from shared memory), P overwrites S in tensor memory as the 16-bit left operand
 // of O += P V, with V read from the same layout as K but as the MN-major operand.
 //
@@ -36,7 +36,7 @@
 namespace {
 
 constexpr int TS = 128;                      // slots of a tile, rows of a stream
-constexpr int NLOAD = 7 * 32, NTHR = 16 * 32;
+constexpr int NLOAD = 8 * 32, NTHR = 17 * 32;
 constexpr int MAX_CTAS = 152;
 constexpr long long kSpinCycles = 2000000000LL;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -135,6 +135,28 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
         : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// two fp32 operations at a time
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t r, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -282,7 +304,8 @@ struct Misc {
     uint32_t tmem;
     int fail;
     int odd[8];                       // segment & 7: a drafted value is not finite
-    uint32_t held[2][4];              // per stream: which slots of its tile have a page
+    uint32_t held[2][4];              // per stream: which slots of its tile have a page,
+    float vtop[2][4];                 // and the largest value scale of 32 of them
 };
 struct Scales { float k[2][TS], v[2][TS]; };   // per stream, of its tile
 
@@ -309,6 +332,21 @@ template <class M> __device__ __forceinline__ bool zero_odd(uint4 &x) {
     x = make_uint4(w[0], w[1], w[2], w[3]);
     return odd;
 }
+
+// Where a sequence's slots lie for one head: element offsets of rows, or -1 where no page holds
+// the slot.  The slot is below Segment::end, so its page number is in the table.
+struct Rows {
+    const int32_t *pages;
+    uint32_t n_pages, heads, head, shift, D;
+    __device__ __forceinline__ Rows(const AttendArgs &a, const Segment &s)
+        : pages(a.c.page_table + (int64_t)s.b * a.c.max_pages), n_pages(a.c.n_pages), heads(a.c.kv_heads), head(s.head),
+          shift(a.c.page_shift), D(a.c.head_dim) {}
+    __device__ __forceinline__ int64_t row(uint32_t slot) const {
+        const uint32_t page = (uint32_t)__ldg(pages + (slot >> shift));
+        if (page >= n_pages) return -1;
+        return ((int64_t)(page * heads + head) << shift) + (slot & ((1u << shift) - 1));
+    }
+};
 
 // which of the 32 slots from `first` on drafted token i of sequence b sees
 __device__ __forceinline__ uint32_t seen_bits(const AttendArgs &a, const Segment &s, int i, int64_t first) {
@@ -363,7 +401,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
         for (int i = 0; i < 8; ++i) sh.odd[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 15) {
+    if (warp == 16) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -374,7 +412,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
     Walk walk(a, work, blockIdx.x, gridDim.x);
     Segment s;
 
-    if (warp == 15) {
+    if (warp == 16) {
         if (lane == 0) {
             // ---- the MMAs
             constexpr uint32_t fmt = F16 ? 0u : 1u;
@@ -467,37 +505,48 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
         // ---- loading
         const int lt = tid - 256;
         const uint32_t ring = smem_u32(smem + S::RING);
-        constexpr int CPR = DP / 8;                                 // 16-byte chunks of a 16-bit row
         int it = 0, seg = 0;
         auto wait_empty = [&](int i) {
             return i < S::NS || mbar_wait(&sh.empty[i % S::NS], (uint32_t)(i / S::NS - 1) & 1, fail);
         };
         if constexpr (!E4M3) {
+            // a thread copies one 16-byte chunk of every STEP-th row
+            constexpr int CPR = DP / 8, STEP = NLOAD / CPR, ITER = TS / STEP;
+            const int c = lt % CPR, r0 = lt / CPR;
+            const uint32_t to = chunk_at(r0, c);
+            const bool column = c * 8 < D;
             bool ok = true;
             while (ok && walk.next(a, s)) {
+                const Rows rows(a, s);
                 for (int i = 0; i < 2 * s.n; ++i, ++it) {
                     int tile;
                     bool value;
                     item_of(s, i, tile, value);
-                    if (!(ok = wait_empty(it))) break;
-                    const int64_t first = (int64_t)(s.t0 + tile) * TS;
-                    const T *src = (const T *)(value ? a.c.v : a.c.k);
-                    const uint32_t dst = ring + (it % S::NS) * S::TILE;
-                    const bool draft = value && first + TS > s.slots;   // drafted values may be hidden from some rows
+                    const uint32_t first = (uint32_t)(s.t0 + tile) * TS + r0, end = (uint32_t)s.end;
+                    const T *src = (const T *)(value ? a.c.v : a.c.k) + c * 8;
+                    const bool draft = value && (int64_t)(s.t0 + tile + 1) * TS > s.slots;   // may be hidden from some rows
+                    int64_t row[ITER];
 #pragma unroll
-                    for (int q = 0; q < (TS * CPR + NLOAD - 1) / NLOAD; ++q) {
-                        const int x = lt + q * NLOAD;
-                        if (x >= TS * CPR) break;
-                        const int r = x / CPR, c = x % CPR;
-                        const int64_t row = first + r < s.end ? a.c.row(s.b, first + r, s.head) : -1;
-                        const bool there = row >= 0 && c * 8 < D;
-                        const T *p = src + (there ? row * D + c * 8 : 0);
-                        if (!draft) {
-                            cp_async16(dst + chunk_at(r, c), p, there);
-                        } else {
-                            uint4 v = there ? __ldg(reinterpret_cast<const uint4 *>(p)) : make_uint4(0, 0, 0, 0);
-                            if (first + r >= s.slots && zero_odd<M>(v)) sh.odd[seg & 7] = 1;
-                            *reinterpret_cast<uint4 *>(smem + S::RING + (it % S::NS) * S::TILE + chunk_at(r, c)) = v;
+                    for (int q = 0; q < ITER; ++q) row[q] = first + q * STEP < end && column ? rows.row(first + q * STEP) : -1;
+                    if (!(ok = wait_empty(it))) break;
+                    if (!draft) {
+                        const uint32_t dst = ring + (it % S::NS) * S::TILE + to;
+#pragma unroll
+                        for (int q = 0; q < ITER; ++q)
+                            cp_async16(dst + q * STEP * 128, src + (row[q] < 0 ? 0 : row[q] * D), row[q] >= 0);
+                    } else {
+                        unsigned char *dst = smem + S::RING + (it % S::NS) * S::TILE + to;
+#pragma unroll
+                        for (int h = 0; h < ITER; h += 4) {
+                            uint4 v[4];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                v[q] = row[h + q] >= 0 ? __ldg(reinterpret_cast<const uint4 *>(src + row[h + q] * D)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                if (first + (h + q) * STEP >= s.slots && zero_odd<M>(v[q])) sh.odd[seg & 7] = 1;
+                                *reinterpret_cast<uint4 *>(dst + (h + q) * STEP * 128) = v[q];
+                            }
                         }
                     }
                     cp_commit();
@@ -514,13 +563,17 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
             if (ok)
                 for (int i = max(it - LAG<DP>, 0); i < it; ++i) mbar_arrive(&sh.full[i % S::NS]);
         } else {
-            // raw codes arrive NR - 1 tiles ahead, each thread converting the chunks it copied
+            // raw codes arrive NR - 1 tiles ahead, each thread converting the chunks it copied: one
+            // 16-byte chunk of every STEP-th row
+            constexpr int RPR = DP / 16, STEP = NLOAD / RPR, ITER = TS / STEP;
+            const int c = lt % RPR, r0 = lt / RPR;
+            const uint32_t to0 = chunk_at(r0, 2 * c), to1 = chunk_at(r0, 2 * c + 1);
+            const bool column = c * 16 < D;
             Walk ahead = walk;
             Segment sa;
             sa.n = 0;
             int ia = 0, issued = 0;
-            const uint32_t raws = smem_u32(smem + S::RAWS);
-            constexpr int RPR = DP / 16, ITER = (TS * RPR + NLOAD - 1) / NLOAD;   // 16-byte chunks of a row of codes
+            const uint32_t raws = smem_u32(smem + S::RAWS) + lt * 16;
             auto issue = [&]() {
                 if (ia == 2 * sa.n) {
                     ia = 0;
@@ -529,18 +582,16 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
                 int tile;
                 bool value;
                 item_of(sa, ia++, tile, value);
-                const int64_t first = (int64_t)(sa.t0 + tile) * TS;
-                const uint8_t *src = (const uint8_t *)(value ? a.c.v : a.c.k);
+                const Rows rows(a, sa);
+                const uint32_t first = (uint32_t)(sa.t0 + tile) * TS + r0, end = (uint32_t)sa.end;
+                const uint8_t *src = (const uint8_t *)(value ? a.c.v : a.c.k) + c * 16;
                 const uint32_t dst = raws + (issued % S::NR) * S::RAW;
+                int64_t row[ITER];
 #pragma unroll
-                for (int q = 0; q < ITER; ++q) {
-                    const int x = lt + q * NLOAD;
-                    if (x >= TS * RPR) break;
-                    const int r = x / RPR, c = x % RPR;
-                    const int64_t row = first + r < sa.end ? a.c.row(sa.b, first + r, sa.head) : -1;
-                    const bool there = row >= 0 && c * 16 < D;
-                    cp_async16(dst + x * 16, src + (there ? row * D + c * 16 : 0), there);
-                }
+                for (int q = 0; q < ITER; ++q) row[q] = first + q * STEP < end && column ? rows.row(first + q * STEP) : -1;
+#pragma unroll
+                for (int q = 0; q < ITER; ++q)
+                    cp_async16(dst + q * NLOAD * 16, src + (row[q] < 0 ? 0 : row[q] * D), row[q] >= 0);
                 cp_commit();
                 ++issued;
             };
@@ -554,26 +605,23 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
                     issue();
                     cp_wait<S::NR - 1>();
                     if (!(ok = wait_empty(it))) break;
-                    const int64_t first = (int64_t)(s.t0 + tile) * TS;
-                    const bool draft = value && first + TS > s.slots;
-                    const unsigned char *raw = smem + S::RAWS + (it % S::NR) * S::RAW;
+                    const uint32_t first = (uint32_t)(s.t0 + tile) * TS + r0;
+                    const bool draft = value && (int64_t)(s.t0 + tile + 1) * TS > s.slots;
+                    const unsigned char *raw = smem + S::RAWS + (it % S::NR) * S::RAW + lt * 16;
                     unsigned char *dst = smem + S::RING + (it % S::NS) * S::TILE;
 #pragma unroll
                     for (int q = 0; q < ITER; ++q) {
-                        const int x = lt + q * NLOAD;
-                        if (x >= TS * RPR) break;
-                        const int r = x / RPR, c = x % RPR;
-                        const uint4 w = *reinterpret_cast<const uint4 *>(raw + x * 16);
+                        const uint4 w = *reinterpret_cast<const uint4 *>(raw + q * NLOAD * 16);
                         uint4 lo = make_uint4(fa_e4m3x2_to_half2(w.x), fa_e4m3x2_to_half2(w.x >> 16),
                                               fa_e4m3x2_to_half2(w.y), fa_e4m3x2_to_half2(w.y >> 16));
                         uint4 hi = make_uint4(fa_e4m3x2_to_half2(w.z), fa_e4m3x2_to_half2(w.z >> 16),
                                               fa_e4m3x2_to_half2(w.w), fa_e4m3x2_to_half2(w.w >> 16));
-                        if (draft && first + r >= s.slots) {
+                        if (draft && first + q * STEP >= s.slots) {
                             const bool o1 = zero_odd<M>(lo), o2 = zero_odd<M>(hi);
                             if (o1 || o2) sh.odd[seg & 7] = 1;
                         }
-                        *reinterpret_cast<uint4 *>(dst + chunk_at(r, 2 * c)) = lo;
-                        *reinterpret_cast<uint4 *>(dst + chunk_at(r, 2 * c + 1)) = hi;
+                        *reinterpret_cast<uint4 *>(dst + to0 + q * STEP * 128) = lo;
+                        *reinterpret_cast<uint4 *>(dst + to1 + q * STEP * 128) = hi;
                     }
                     proxy_fence();
                     mbar_arrive(&sh.full[it % S::NS]);
@@ -642,9 +690,10 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
             // slot r of each tile: whether it is held and its scales, one tile ahead
             float ks = 0.0f, vs = 0.0f;
             bool there = false;
+            const Rows rows(a, s);
             auto fetch = [&](int tile) {
-                const int64_t slot = (int64_t)(s.t0 + tile) * TS + r;
-                const int64_t at = slot < s.end ? a.c.row(s.b, slot, s.head) : -1;
+                const uint32_t slot = (uint32_t)(s.t0 + tile) * TS + r;
+                const int64_t at = slot < (uint32_t)s.end ? rows.row(slot) : -1;
                 there = at >= 0;
                 if (E4M3) {
                     ks = there ? __ldg(a.c.k_scale + at) : 0.0f;
@@ -656,52 +705,68 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
                 const int tile = begin + q * step;
                 const int64_t first = (int64_t)(s.t0 + tile) * TS;
                 const uint32_t got = __ballot_sync(0xffffffffu, there);
+                float vt = vs;
+                if (E4M3)
+#pragma unroll
+                    for (int o = 16; o; o >>= 1) vt = fmaxf(vt, __shfl_xor_sync(0xffffffffu, vt, o));
                 if (q > 0) bar_sync(1 + st, TS);          // the previous tile's have been read
-                if (lane == 0) sh.held[st][warp & 3] = got;
+                if (lane == 0) {
+                    sh.held[st][warp & 3] = got;
+                    if (E4M3) sh.vtop[st][warp & 3] = vt;
+                }
                 if (E4M3) { sc.k[st][r] = ks; sc.v[st][r] = vs; }
                 if (q + 1 < mine) fetch(tile + step);
                 bar_sync(1 + st, TS);
-                uint32_t held[4];
                 bool whole = first + TS <= s.slots;
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    held[w] = sh.held[st][w];
-                    whole &= held[w] == 0xffffffffu;
-                }
+                for (int w = 0; w < 4; ++w) whole &= sh.held[st][w] == 0xffffffffu;
                 mbar_wait(&sh.s_full[st], (uint32_t)ns++ & 1, fail);
                 __syncwarp();
                 tc_fence_after();
                 if (warp_live) {
-                    uint32_t see[4];
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) see[w] = whole ? 0xffffffffu : used ? held[w] & seen_bits(a, s, ti, first + 32 * w) : 0u;
+                    // the largest score (before the scale), and the largest value scale, that the row sees
                     float mx = -INFINITY, vmx = 0.0f;
+                    uint32_t see[4];
+                    if (whole) {
+                        if (E4M3)
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        float x[32];
-                        tmem_ld32(ts + 32 * w, x);
-                        if (E4M3) {
+                            for (int w = 0; w < 4; ++w) vmx = fmaxf(vmx, sh.vtop[st][w]);
+#pragma unroll 1
+                        for (int w = 0; w < 4; ++w) {
+                            float x[32];
+                            tmem_ld32(ts + 32 * w, x);
+                            if (E4M3)
 #pragma unroll
-                            for (int e = 0; e < 32; e += 4) {
-                                const float4 f = *reinterpret_cast<const float4 *>(&sc.k[st][32 * w + e]);
-                                const float4 g = *reinterpret_cast<const float4 *>(&sc.v[st][32 * w + e]);
-                                x[e] *= f.x; x[e + 1] *= f.y; x[e + 2] *= f.z; x[e + 3] *= f.w;
-                                if (whole) {
-                                    vmx = fmaxf(vmx, fmaxf(fmaxf(g.x, g.y), fmaxf(g.z, g.w)));
-                                } else {
-                                    if (see[w] >> e & 1) vmx = fmaxf(vmx, g.x);
-                                    if (see[w] >> (e + 1) & 1) vmx = fmaxf(vmx, g.y);
-                                    if (see[w] >> (e + 2) & 1) vmx = fmaxf(vmx, g.z);
-                                    if (see[w] >> (e + 3) & 1) vmx = fmaxf(vmx, g.w);
+                                for (int e = 0; e < 32; e += 4) {
+                                    const float4 f = *reinterpret_cast<const float4 *>(&sc.k[st][32 * w + e]);
+                                    unpair(mul2(pair(x[e], x[e + 1]), pair(f.x, f.y)), x[e], x[e + 1]);
+                                    unpair(mul2(pair(x[e + 2], x[e + 3]), pair(f.z, f.w)), x[e + 2], x[e + 3]);
                                 }
-                            }
+                            float top[4] = {mx, x[0], x[1], x[2]};
+#pragma unroll
+                            for (int e = 3; e < 27; e += 8)
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) top[j] = fmaxf(fmaxf(top[j], x[e + 2 * j]), x[e + 2 * j + 1]);
+                            top[0] = fmaxf(fmaxf(top[0], x[27]), x[28]);
+                            top[1] = fmaxf(fmaxf(top[1], x[29]), x[30]);
+                            mx = fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), x[31]);
                         }
-                        if (whole) {
+                    } else {
+#pragma unroll 1
+                        for (int w = 0; w < 4; ++w) {
+                            float x[32];
+                            const uint32_t z = used ? sh.held[st][w] & seen_bits(a, s, ti, first + 32 * w) : 0u;
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) mx = fmaxf(mx, x[e]);
-                        } else {
+                            for (int j = 0; j < 4; ++j)
+                                if (j == w) see[j] = z;
+                            __syncwarp();
+                            tmem_ld32(ts + 32 * w, x);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) mx = fmaxf(mx, (see[w] >> e & 1) ? x[e] : -INFINITY);
+                            for (int e = 0; e < 32; ++e)
+                                if (z >> e & 1) {
+                                    mx = fmaxf(mx, E4M3 ? x[e] * sc.k[st][32 * w + e] : x[e]);
+                                    if (E4M3) vmx = fmaxf(vmx, sc.v[st][32 * w + e]);
+                                }
                         }
                     }
                     const int e2 = E4M3 ? max(ev, min(max(fa_exponent(vmx) + 1, -120), 120)) : 0;
@@ -722,7 +787,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
                             mbar_wait(&sh.pv_done[st], (uint32_t)(npv - 1) & 1, fail);
                             __syncwarp();
                             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                             for (int w = 0; w < DP / 32; ++w) {
                                 float o[32];
                                 tmem_ld32(to + 32 * w, o);
@@ -732,41 +797,67 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
                             }
                         }
                     }
-                    float sum[4] = {0, 0, 0, 0};
-#pragma unroll
+                    const uint64_t cc = pair(c, c), nb = pair(-bias, -bias);
+                    uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll 1
                     for (int w = 0; w < 4; ++w) {
                         float x[32];
                         uint32_t p[16];
                         tmem_ld32(ts + 32 * w, x);
+                        uint32_t z = 0xffffffffu;
+                        if (!whole) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            float4 f = make_float4(1, 1, 1, 1), g = f;
-                            if (E4M3) {
-                                f = *reinterpret_cast<const float4 *>(&sc.k[st][32 * w + e]);
-                                g = *reinterpret_cast<const float4 *>(&sc.v[st][32 * w + e]);
-                                x[e] *= f.x; x[e + 1] *= f.y; x[e + 2] *= f.z; x[e + 3] *= f.w;
-                            }
-                            float y[4];
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                y[j] = ex2(fmaf(x[e + j], c, -bias));
-                                if (!whole && !(see[w] >> (e + j) & 1)) y[j] = 0.0f;
-                                sum[j] += y[j];
-                            }
-                            if (E4M3) {
-                                y[0] *= g.x; y[1] *= g.y; y[2] *= g.z; y[3] *= g.w;
-                                if (!whole) {
-#pragma unroll
-                                    for (int j = 0; j < 4; ++j)
-                                        if (!(see[w] >> (e + j) & 1)) y[j] = 0.0f;   // whatever the scale is
-                                }
-                            }
-                            p[e / 2] = fa_pack2(y[0], y[1], M());
-                            p[e / 2 + 1] = fa_pack2(y[2], y[3], M());
+                            for (int j = 0; j < 4; ++j)
+                                if (j == w) z = see[j];
                         }
+                        if (z == 0xffffffffu) {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                uint64_t a0 = pair(x[e], x[e + 1]), a1 = pair(x[e + 2], x[e + 3]);
+                                if (E4M3) {
+                                    const float4 f = *reinterpret_cast<const float4 *>(&sc.k[st][32 * w + e]);
+                                    a0 = mul2(a0, pair(f.x, f.y));
+                                    a1 = mul2(a1, pair(f.z, f.w));
+                                }
+                                float y[4];
+                                unpair(fma2(a0, cc, nb), y[0], y[1]);
+                                unpair(fma2(a1, cc, nb), y[2], y[3]);
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) y[j] = ex2(y[j]);
+                                a0 = pair(y[0], y[1]);
+                                a1 = pair(y[2], y[3]);
+                                sum0 = add2(sum0, a0);
+                                sum1 = add2(sum1, a1);
+                                if (E4M3) {
+                                    const float4 g = *reinterpret_cast<const float4 *>(&sc.v[st][32 * w + e]);
+                                    unpair(mul2(a0, pair(g.x, g.y)), y[0], y[1]);
+                                    unpair(mul2(a1, pair(g.z, g.w)), y[2], y[3]);
+                                }
+                                p[e / 2] = fa_pack2(y[0], y[1], M());
+                                p[e / 2 + 1] = fa_pack2(y[2], y[3], M());
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2) {
+                                float y[2];
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) {
+                                    const bool on = z >> (e + j) & 1;
+                                    const float t = E4M3 ? x[e + j] * sc.k[st][32 * w + e + j] : x[e + j];
+                                    y[j] = on ? ex2(fmaf(t, c, -bias)) : 0.0f;
+                                    l += y[j];
+                                    if (E4M3) y[j] = on ? y[j] * sc.v[st][32 * w + e + j] : 0.0f;   // whatever the scale is
+                                }
+                                p[e / 2] = fa_pack2(y[0], y[1], M());
+                            }
+                        }
+                        __syncwarp();
                         tmem_st16(ts + 16 * w, p);
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    float t0, t1, t2, t3;
+                    unpair(sum0, t0, t1);
+                    unpair(sum1, t2, t3);
+                    l += (t0 + t1) + (t2 + t3);
                     tmem_st_wait();
                 }
                 tc_fence_before();
@@ -801,7 +892,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;
                 const int64_t orow = ((int64_t)s.b * a.T + ti) * a.heads + hq;
                 if (warp_live) {
-#pragma unroll
+#pragma unroll 1
                     for (int w = 0; w < DP / 32; ++w) {
                         float o[32];
                         __syncwarp();
@@ -820,7 +911,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
                                 const int64_t slot = s.slots + j;
                                 if (slot < (int64_t)s.t0 * TS || slot >= (int64_t)(s.t0 + s.n) * TS || slot >= s.end) continue;
                                 if (!(seen_bits(a, s, ti, slot) & 1)) continue;
-                                const int64_t at = a.c.row(s.b, slot, s.head);
+                                const int64_t at = rows.row((uint32_t)slot);
                                 if (at < 0) continue;
                                 for (int e = 0; e < 32 && 32 * w + e < D; ++e) {
                                     const int64_t x = at * D + 32 * w + e;
@@ -870,7 +961,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
     tc_fence_after();
     __syncthreads();
     if (tid == 0) a.status[blockIdx.x] = sh.fail;
-    if (warp == 15) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    if (warp == 16) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
 // Joins the parts of units that were cut, in the order of their slots.  Block (unit, 32 rows); a
@@ -991,6 +1082,7 @@ extern "C" fa_status fa_tree_attention(const fa_kv_cache *cache, int32_t dtype, 
         return fa_refuse(fn, "a 16-bit cache must have the type of q", FA_ERR_UNSUPPORTED);
     if (!(scale > 0.0f && scale < INFINITY)) return fa_refuse(fn, "scale must be positive and finite");
     if (((int64_t)max_pages << a.c.page_shift) > 2147483647LL - 4096) return fa_refuse(fn, "max_pages * page_size out of range");
+    if ((int64_t)cache->n_pages * cache->kv_heads > 2147483647LL) return fa_refuse(fn, "n_pages * kv_heads out of range");
     if (B == 0 || T == 0) return FA_OK;
     if (!q || !out || !length) return fa_refuse(fn, "NULL buffer");
     if ((((uintptr_t)q | (uintptr_t)out) & 15) || ((q_batch_stride | q_token_stride | q_head_stride) & 7))
