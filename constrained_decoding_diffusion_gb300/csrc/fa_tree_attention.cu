@@ -24,8 +24,9 @@
 // whatever the lengths, which are read on the device.  A unit that is cut by the runs leaves
 // partial results, joined by a second small kernel in a fixed order.
 //
-// Roles (17 warps): warps 0-7 the two softmax warpgroups (a thread per row), warps 8-15 load and
-// convert (16-byte asynchronous copies into 128-byte-swizzled tiles), warp 16 issues the MMAs:
+// Roles (20 warps): warps 0-7 the two softmax warpgroups (a thread per row), warps 8-15 load and
+// convert (16-byte asynchronous copies into 128-byte-swizzled tiles), warp 16 issues the MMAs
+// (17-19 only complete its warpgroup, whose registers go to the softmax):
 // S = Q K^T (both from shared memory), P overwrites S in tensor memory as the 16-bit left operand
 // of O += P V, with V read from the same layout as K but as the MN-major operand.
 //
@@ -36,7 +37,10 @@
 namespace {
 
 constexpr int TS = 128;                      // slots of a tile, rows of a stream
-constexpr int NLOAD = 8 * 32, NTHR = 17 * 32;
+constexpr int NLOAD = 8 * 32, NTHR = 20 * 32;
+// registers a thread of each role, of the 96 the block is launched with: 256 * 144 + 256 * 64 +
+// 128 * 64 = 640 * 96
+constexpr int REGS_SOFTMAX = 144, REGS_LOAD = 64, REGS_MMA = 64;
 constexpr int MAX_CTAS = 152;
 constexpr long long kSpinCycles = 2000000000LL;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -80,10 +84,10 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool t
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// shared-memory matrix descriptor: 128-byte swizzle (8 rows x 128 bytes atoms), descriptor version 1
-__device__ __forceinline__ uint64_t umma_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)((lbo & 0x3FFFFu) >> 4) << 16 |
-           (uint64_t)((sbo & 0x3FFFFu) >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+// shared-memory matrix descriptor: 128-byte swizzle (8 rows x 128 bytes atoms, 1024 bytes apart),
+// descriptor version 1; stepping the start address by n bytes adds n / 16 to the low word
+__device__ __forceinline__ uint64_t umma_desc(uint32_t addr, uint32_t lbo) {
+    return (uint64_t)((addr >> 4) | (lbo >> 4) << 16) | (uint64_t)(1024u >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 __device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
@@ -101,20 +105,29 @@ __device__ __forceinline__ void umma_commit(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                  : "memory");
 }
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
-    uint32_t r[32];
+// the load alone; nothing of v may be used before tmem_wait(v)
+__device__ __forceinline__ void tmem_ld32_start(uint32_t taddr, float (&r)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
         "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+          "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+          "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
         : "r"(taddr)
         : "memory");
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+// waits for the thread's loads; v passes through so that its uses stay behind the wait
+__device__ __forceinline__ void tmem_wait(float (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]), "+f"(r[8]),
+                   "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]), "+f"(r[16]),
+                   "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]), "+f"(r[24]),
+                   "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]), "+f"(r[30]), "+f"(r[31])::"memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+    tmem_ld32_start(taddr, v);
+    tmem_wait(v);
 }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
     asm volatile(
@@ -179,22 +192,23 @@ struct AttendArgs {
 
 // ----------------------------------------------------------------------------- the work list
 
-// sequence b's slots: before the draft, drafted, and the end of what can be read
-__device__ __forceinline__ void extent(const AttendArgs &a, int b, int64_t &n, int &use, int64_t &end) {
-    n = max(__ldg(a.length + b), 0);
+// sequence b's slots: before the draft (up to the table's end), drafted, and the end of what can be
+// read.  The host has checked that slots and the number of tiles of all units stay below 2^31.
+__device__ __forceinline__ void extent(const AttendArgs &a, int b, int &n, int &use, int &end) {
+    const int cap = a.c.max_pages << a.c.page_shift;
+    n = min(max(__ldg(a.length + b), 0), cap);
     use = a.count ? min(max(__ldg(a.count + b), 0), a.T) : a.T;
-    end = min(n + use, (int64_t)a.c.max_pages << a.c.page_shift);
+    end = min(n + use, cap);
 }
 __device__ __forceinline__ int tiles_of(const AttendArgs &a, int b) {
-    int64_t n, end;
-    int use;
+    int n, use, end;
     extent(a, b, n, use, end);
-    return (int)max((int64_t)1, (end + TS - 1) / TS);   // an empty sequence's rows are written by one masked tile
+    return max(1, (end + TS - 1) / TS);   // an empty sequence's rows are written by one masked tile
 }
 
 constexpr int RUNS = 64;
 struct Work {
-    int64_t cum[RUNS + 1];   // tiles of one (head, row block) before each of 64 runs of sequences
+    int cum[RUNS + 2];   // tiles of one (head, row block) before each of 64 runs of sequences
 };
 __device__ __forceinline__ int run_length(const AttendArgs &a) { return (a.B + RUNS - 1) / RUNS; }
 
@@ -202,17 +216,17 @@ __device__ __forceinline__ int run_length(const AttendArgs &a) { return (a.B + R
 __device__ __forceinline__ void plan(const AttendArgs &a, Work &w) {
     const int tid = threadIdx.x, per = run_length(a);
     if (tid < RUNS) {
-        int64_t s = 0;
+        int s = 0;
         for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) s += tiles_of(a, b);
         w.cum[tid] = s;
     }
     __syncthreads();
     if (tid < 32) {
-        const int64_t s0 = w.cum[2 * tid], s = s0 + w.cum[2 * tid + 1];
-        int64_t before = s;
+        const int s0 = w.cum[2 * tid], s = s0 + w.cum[2 * tid + 1];
+        int before = s;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t up = __shfl_up_sync(0xffffffffu, before, o);
+            const int up = __shfl_up_sync(0xffffffffu, before, o);
             if (tid >= o) before += up;
         }
         w.cum[2 * tid] = before - s;
@@ -222,27 +236,27 @@ __device__ __forceinline__ void plan(const AttendArgs &a, Work &w) {
     __syncthreads();
 }
 
+// the first tile of block c's run, of `total` tiles over `ctas` blocks
+__device__ __forceinline__ int run_start(int total, int c, int ctas) { return (int)((int64_t)total * c / ctas); }
+
 struct Segment {
     int b, head, block;       // the unit
     int nt, t0, n;            // its tiles, the first of this segment, how many
     int rows;                 // rows of the row block (up to 256)
-    bool two;                 // two row tiles over the same key/value tiles
-    int64_t slots;            // before the draft
-    int use;
-    int64_t end;
+    int slots, use, end;      // before the draft, drafted, the end of what can be read
+    // two row tiles over the same key/value tiles, or one over alternate ones
+    __device__ __forceinline__ bool two() const { return rows > TS; }
 };
 
 struct Walk {
-    int64_t g, g1, base;
-    int b, units;
+    int g, g1, base, b;
     __device__ __forceinline__ Walk(const AttendArgs &a, const Work &w, int cta, int ctas) {
-        units = a.c.kv_heads * a.blocks;
-        const int64_t total = w.cum[RUNS] * units;
-        ctas = (int)min(total, (int64_t)ctas);      // no run is empty
-        g = g1 = 0;
+        const int units = a.c.kv_heads * a.blocks, total = w.cum[RUNS] * units;
+        ctas = min(total, ctas);                    // no run is empty
+        g = g1 = base = b = 0;
         if (cta >= ctas) return;
-        g = total * cta / ctas;
-        g1 = total * (cta + 1) / ctas;
+        g = run_start(total, cta, ctas);
+        g1 = run_start(total, cta + 1, ctas);
         int lo = 0, hi = RUNS;                      // the last run that starts at or before g
         while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
@@ -251,7 +265,7 @@ struct Walk {
         b = lo * run_length(a);
         base = w.cum[lo] * units;
         while (true) {
-            const int64_t next = base + (int64_t)tiles_of(a, b) * units;
+            const int next = base + tiles_of(a, b) * units;
             if (g < next) break;
             base = next;
             ++b;
@@ -261,17 +275,15 @@ struct Walk {
         if (g >= g1) return false;
         extent(a, b, s.slots, s.use, s.end);
         s.b = b;
-        s.nt = (int)max((int64_t)1, (s.end + TS - 1) / TS);
-        const int64_t off = g - base;
-        const int u = (int)(off / s.nt);
-        s.t0 = (int)(off - (int64_t)u * s.nt);
+        s.nt = max(1, (s.end + TS - 1) / TS);
+        const int off = g - base, u = off / s.nt;
+        s.t0 = off - u * s.nt;
         s.head = u / a.blocks;
-        s.block = u % a.blocks;
-        s.n = (int)min((int64_t)(s.nt - s.t0), g1 - g);
+        s.block = u - s.head * a.blocks;
+        s.n = min(s.nt - s.t0, g1 - g);
         s.rows = min(a.rows - 256 * s.block, 256);
-        s.two = s.rows > TS;
         g += s.n;
-        if (g >= base + (int64_t)s.nt * units) { base += (int64_t)s.nt * units; ++b; }
+        if (g - base >= s.nt * a.c.kv_heads * a.blocks) { base = g; ++b; }
         return true;
     }
 };
@@ -280,7 +292,7 @@ struct Walk {
 // ...; with alternating streams K0 K1 V0 K2 V1 ... (the next tile's scores are started before the
 // previous tile's weights are ready).
 __device__ __forceinline__ void item_of(const Segment &s, int i, int &tile, bool &value) {
-    if (s.two || s.n == 1) { tile = i >> 1; value = i & 1; return; }
+    if (s.two() || s.n == 1) { tile = i >> 1; value = i & 1; return; }
     if (i < 2) { tile = i; value = false; return; }
     const int j = (i - 2) >> 1;
     value = !(i & 1) || j + 2 >= s.n;
@@ -333,26 +345,65 @@ template <class M> __device__ __forceinline__ bool zero_odd(uint4 &x) {
     return odd;
 }
 
-// Where a sequence's slots lie for one head: element offsets of rows, or -1 where no page holds
-// the slot.  The slot is below Segment::end, so its page number is in the table.
+// Where a sequence's slots lie for one head.  The slot is below Segment::end, so its page number is
+// in the table.
 struct Rows {
     const int32_t *pages;
-    uint32_t n_pages, heads, head, shift, D;
+    uint32_t n_pages, heads, head, shift;
+    __device__ __forceinline__ Rows() {}
     __device__ __forceinline__ Rows(const AttendArgs &a, const Segment &s)
         : pages(a.c.page_table + (int64_t)s.b * a.c.max_pages), n_pages(a.c.n_pages), heads(a.c.kv_heads), head(s.head),
-          shift(a.c.page_shift), D(a.c.head_dim) {}
-    __device__ __forceinline__ int64_t row(uint32_t slot) const {
-        const uint32_t page = (uint32_t)__ldg(pages + (slot >> shift));
+          shift(a.c.page_shift) {}
+    __device__ __forceinline__ uint32_t page(uint32_t slot) const { return (uint32_t)__ldg(pages + (slot >> shift)); }
+    // the row of a slot in a page, or -1 when there is no such page
+    __device__ __forceinline__ int64_t row(uint32_t page, uint32_t slot) const {
         if (page >= n_pages) return -1;
         return ((int64_t)(page * heads + head) << shift) + (slot & ((1u << shift) - 1));
     }
+    __device__ __forceinline__ int64_t row(uint32_t slot) const { return row(page(slot), slot); }
 };
 
-// which of the 32 slots from `first` on drafted token i of sequence b sees
-__device__ __forceinline__ uint32_t seen_bits(const AttendArgs &a, const Segment &s, int i, int64_t first) {
-    const int64_t d0 = first - s.slots;
+// The key and value tiles of a block's work in the order of their consumption.
+struct Feed {
+    Walk walk;
+    Segment s;
+    int i, seg, tile;
+    bool value;
+    __device__ __forceinline__ Feed(const Walk &w) : walk(w), i(0), seg(-1) { s.n = 0; }
+    __device__ __forceinline__ bool next(const AttendArgs &a) {
+        if (i == 2 * s.n) {
+            i = 0;
+            if (!walk.next(a, s)) { s.n = 0; return false; }
+            ++seg;
+        }
+        item_of(s, i++, tile, value);
+        return true;
+    }
+    __device__ __forceinline__ uint32_t first() const { return (uint32_t)(s.t0 + tile) * TS; }
+    // drafted values may be hidden from some rows
+    __device__ __forceinline__ bool draft() const { return value && (s.t0 + tile + 1) * TS > s.slots; }
+};
+
+// A loading thread's share of a tile: one 16-byte chunk of every STEP-th row.  The page numbers of
+// the next tile are fetched while the current one is issued.
+template <int STEP>
+struct Share {
+    static constexpr int ITER = TS / STEP;
+    uint32_t page[ITER];
+    Rows rows;
+    __device__ __forceinline__ void look(const AttendArgs &a, const Feed &f, uint32_t r0, bool column) {
+        rows = Rows(a, f.s);
+        const uint32_t first = f.first() + r0, end = (uint32_t)f.s.end;
+#pragma unroll
+        for (int q = 0; q < ITER; ++q) page[q] = column && first + q * STEP < end ? rows.page(first + q * STEP) : 0xffffffffu;
+    }
+};
+
+// which of the 32 slots from `first` on drafted token i// which of the 32 slots from `first` on drafted token i of sequence b sees
+__device__ __forceinline__ uint32_t seen_bits(const AttendArgs &a, const Segment &s, int i, int first) {
+    const int d0 = first - s.slots;
     if (d0 <= -32) return 0xffffffffu;
-    const int from = d0 < 0 ? 0 : (int)min(d0, (int64_t)s.use);
+    const int from = min(max(d0, 0), s.use);
     uint32_t v = 0xffffffffu;
     if (a.mask && from < s.use) {
         const uint64_t *m = a.mask + ((int64_t)s.b * a.T + i) * a.words;
@@ -363,7 +414,7 @@ __device__ __forceinline__ uint32_t seen_bits(const AttendArgs &a, const Segment
     }
     const int left = s.use - from;
     if (left < 32) v &= left > 0 ? (1u << left) - 1 : 0u;
-    if (d0 < 0) v = v << (int)-d0 | ((1u << (int)-d0) - 1);
+    if (d0 < 0) v = v << -d0 | ((1u << -d0) - 1);
     return v;
 }
 
@@ -412,8 +463,9 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
     Walk walk(a, work, blockIdx.x, gridDim.x);
     Segment s;
 
-    if (warp == 16) {
-        if (lane == 0) {
+    if (warp >= 16) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_MMA));
+        if (warp == 16 && lane == 0) {
             // ---- the MMAs
             constexpr uint32_t fmt = F16 ? 0u : 1u;
             constexpr uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(TS >> 4) << 24);
@@ -428,20 +480,20 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
                 return slot;
             };
             auto scores = [&](int st, int slot) {
-                const uint32_t qa = q0 + st * S::TILE, ka = ring + slot * S::TILE;
+                const uint64_t qd = umma_desc(q0 + st * S::TILE, 16), kd = umma_desc(ring + slot * S::TILE, 16);
+                const uint32_t d = tmem + st * TS;
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k) {
-                    const uint32_t off = (k >> 2) * (TS * 128) + (k & 3) * 32;
-                    umma_ss(tmem + st * TS, umma_desc(qa + off, 16, 1024), umma_desc(ka + off, 16, 1024), idesc_s, k > 0);
+                    const uint32_t off = ((k >> 2) * (TS * 128) + (k & 3) * 32) / 16;
+                    umma_ss(d, qd + off, kd + off, idesc_s, k > 0);
                 }
                 umma_commit(&sh.s_full[st]);
             };
             auto values = [&](int st, int slot, bool first) {
-                const uint32_t va = ring + slot * S::TILE;
+                const uint64_t vd = umma_desc(ring + slot * S::TILE, TS * 128);
+                const uint32_t d = tmem + 256 + st * DP, p = tmem + st * TS;
 #pragma unroll
-                for (int k = 0; k < TS / 16; ++k)
-                    umma_ts(tmem + 256 + st * DP, tmem + st * TS + k * 8, umma_desc(va + k * 2048, TS * 128, 1024), idesc_o,
-                            !first || k > 0);
+                for (int k = 0; k < TS / 16; ++k) umma_ts(d, p + k * 8, vd + k * (2048 / 16), idesc_o, !first || k > 0);
                 umma_commit(&sh.pv_done[st]);
             };
             auto wait_p = [&](int st) {
@@ -451,13 +503,13 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
                 return ok;
             };
             while (!*fail && walk.next(a, s)) {
-                const int streams = s.two || s.n > 1 ? 2 : 1;
+                const int streams = s.two() || s.n > 1 ? 2 : 1;
                 bool ok = true;
                 for (int st = 0; st < streams; ++st) ok &= mbar_wait(&sh.q_full[st], (uint32_t)nq[st]++ & 1, fail);
                 if (!ok) break;
                 tc_fence_after();
                 int slot;
-                if (s.two) {
+                if (s.two()) {
                     if ((slot = next_tile()) < 0) break;
                     scores(0, slot);
                     scores(1, slot);
@@ -503,145 +555,126 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
         }
     } else if (warp >= 8) {
         // ---- loading
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_LOAD));
         const int lt = tid - 256;
         const uint32_t ring = smem_u32(smem + S::RING);
-        int it = 0, seg = 0;
+        int it = 0;
         auto wait_empty = [&](int i) {
             return i < S::NS || mbar_wait(&sh.empty[i % S::NS], (uint32_t)(i / S::NS - 1) & 1, fail);
         };
+        Feed f(walk);
         if constexpr (!E4M3) {
-            // a thread copies one 16-byte chunk of every STEP-th row
-            constexpr int CPR = DP / 8, STEP = NLOAD / CPR, ITER = TS / STEP;
+            constexpr int CPR = DP / 8, STEP = NLOAD / CPR;
             const int c = lt % CPR, r0 = lt / CPR;
             const uint32_t to = chunk_at(r0, c);
             const bool column = c * 8 < D;
-            bool ok = true;
-            while (ok && walk.next(a, s)) {
-                const Rows rows(a, s);
-                for (int i = 0; i < 2 * s.n; ++i, ++it) {
-                    int tile;
-                    bool value;
-                    item_of(s, i, tile, value);
-                    const uint32_t first = (uint32_t)(s.t0 + tile) * TS + r0, end = (uint32_t)s.end;
-                    const T *src = (const T *)(value ? a.c.v : a.c.k) + c * 8;
-                    const bool draft = value && (int64_t)(s.t0 + tile + 1) * TS > s.slots;   // may be hidden from some rows
-                    int64_t row[ITER];
+            Share<STEP> x;
+            bool more = f.next(a);
+            if (more) x.look(a, f, r0, column);
+            for (; more; ++it) {
+                const uint32_t first = f.first() + r0;
+                const T *src = (const T *)(f.value ? a.c.v : a.c.k) + c * 8;
+                if (!wait_empty(it)) break;
+                if (!f.draft()) {
+                    const uint32_t dst = ring + (it % S::NS) * S::TILE + to;
 #pragma unroll
-                    for (int q = 0; q < ITER; ++q) row[q] = first + q * STEP < end && column ? rows.row(first + q * STEP) : -1;
-                    if (!(ok = wait_empty(it))) break;
-                    if (!draft) {
-                        const uint32_t dst = ring + (it % S::NS) * S::TILE + to;
-#pragma unroll
-                        for (int q = 0; q < ITER; ++q)
-                            cp_async16(dst + q * STEP * 128, src + (row[q] < 0 ? 0 : row[q] * D), row[q] >= 0);
-                    } else {
-                        unsigned char *dst = smem + S::RING + (it % S::NS) * S::TILE + to;
-#pragma unroll
-                        for (int h = 0; h < ITER; h += 4) {
-                            uint4 v[4];
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                v[q] = row[h + q] >= 0 ? __ldg(reinterpret_cast<const uint4 *>(src + row[h + q] * D)) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                if (first + (h + q) * STEP >= s.slots && zero_odd<M>(v[q])) sh.odd[seg & 7] = 1;
-                                *reinterpret_cast<uint4 *>(dst + (h + q) * STEP * 128) = v[q];
-                            }
-                        }
+                    for (int q = 0; q < x.ITER; ++q) {
+                        const int64_t row = x.rows.row(x.page[q], first + q * STEP);
+                        cp_async16(dst + q * STEP * 128, src + (row < 0 ? 0 : row * D), row >= 0);
                     }
-                    cp_commit();
-                    if (it >= LAG<DP>) {
-                        cp_wait<LAG<DP>>();
-                        proxy_fence();
-                        mbar_arrive(&sh.full[(it - LAG<DP>) % S::NS]);
+                } else {
+                    unsigned char *dst = smem + S::RING + (it % S::NS) * S::TILE + to;
+#pragma unroll
+                    for (int q = 0; q < x.ITER; ++q) {
+                        const int64_t row = x.rows.row(x.page[q], first + q * STEP);
+                        uint4 v = make_uint4(0, 0, 0, 0);
+                        if (row >= 0) v = __ldg(reinterpret_cast<const uint4 *>(src + row * D));
+                        if (first + q * STEP >= (uint32_t)f.s.slots && zero_odd<M>(v)) sh.odd[f.seg & 7] = 1;
+                        *reinterpret_cast<uint4 *>(dst + q * STEP * 128) = v;
                     }
                 }
-                ++seg;
+                cp_commit();
+                more = f.next(a);
+                if (more) x.look(a, f, r0, column);
+                if (it >= LAG<DP>) {
+                    cp_wait<LAG<DP>>();
+                    proxy_fence();
+                    mbar_arrive(&sh.full[(it - LAG<DP>) % S::NS]);
+                }
             }
             cp_wait<0>();
             proxy_fence();
-            if (ok)
+            if (!more)
                 for (int i = max(it - LAG<DP>, 0); i < it; ++i) mbar_arrive(&sh.full[i % S::NS]);
         } else {
-            // raw codes arrive NR - 1 tiles ahead, each thread converting the chunks it copied: one
-            // 16-byte chunk of every STEP-th row
-            constexpr int RPR = DP / 16, STEP = NLOAD / RPR, ITER = TS / STEP;
+            // raw codes arrive NR - 1 tiles ahead, each thread converting the chunks it copied
+            constexpr int RPR = DP / 16, STEP = NLOAD / RPR;
             const int c = lt % RPR, r0 = lt / RPR;
             const uint32_t to0 = chunk_at(r0, 2 * c), to1 = chunk_at(r0, 2 * c + 1);
             const bool column = c * 16 < D;
-            Walk ahead = walk;
-            Segment sa;
-            sa.n = 0;
-            int ia = 0, issued = 0;
+            Feed ahead(walk);
+            Share<STEP> x;
+            int issued = 0;
             const uint32_t raws = smem_u32(smem + S::RAWS) + lt * 16;
+            bool more = ahead.next(a);
+            if (more) x.look(a, ahead, r0, column);
             auto issue = [&]() {
-                if (ia == 2 * sa.n) {
-                    ia = 0;
-                    if (!ahead.next(a, sa)) { sa.n = 0; cp_commit(); return; }
+                if (more) {
+                    const uint32_t first = ahead.first() + r0;
+                    const uint8_t *src = (const uint8_t *)(ahead.value ? a.c.v : a.c.k) + c * 16;
+                    const uint32_t dst = raws + (issued % S::NR) * S::RAW;
+#pragma unroll
+                    for (int q = 0; q < x.ITER; ++q) {
+                        const int64_t row = x.rows.row(x.page[q], first + q * STEP);
+                        cp_async16(dst + q * NLOAD * 16, src + (row < 0 ? 0 : row * D), row >= 0);
+                    }
+                    ++issued;
+                    more = ahead.next(a);
+                    if (more) x.look(a, ahead, r0, column);
                 }
-                int tile;
-                bool value;
-                item_of(sa, ia++, tile, value);
-                const Rows rows(a, sa);
-                const uint32_t first = (uint32_t)(sa.t0 + tile) * TS + r0, end = (uint32_t)sa.end;
-                const uint8_t *src = (const uint8_t *)(value ? a.c.v : a.c.k) + c * 16;
-                const uint32_t dst = raws + (issued % S::NR) * S::RAW;
-                int64_t row[ITER];
-#pragma unroll
-                for (int q = 0; q < ITER; ++q) row[q] = first + q * STEP < end && column ? rows.row(first + q * STEP) : -1;
-#pragma unroll
-                for (int q = 0; q < ITER; ++q)
-                    cp_async16(dst + q * NLOAD * 16, src + (row[q] < 0 ? 0 : row[q] * D), row[q] >= 0);
                 cp_commit();
-                ++issued;
             };
             for (int i = 0; i < S::NR - 1; ++i) issue();
-            bool ok = true;
-            while (ok && walk.next(a, s)) {
-                for (int i = 0; i < 2 * s.n; ++i, ++it) {
-                    int tile;
-                    bool value;
-                    item_of(s, i, tile, value);
-                    issue();
-                    cp_wait<S::NR - 1>();
-                    if (!(ok = wait_empty(it))) break;
-                    const uint32_t first = (uint32_t)(s.t0 + tile) * TS + r0;
-                    const bool draft = value && (int64_t)(s.t0 + tile + 1) * TS > s.slots;
-                    const unsigned char *raw = smem + S::RAWS + (it % S::NR) * S::RAW + lt * 16;
-                    unsigned char *dst = smem + S::RING + (it % S::NS) * S::TILE;
+            for (; f.next(a); ++it) {
+                issue();
+                cp_wait<S::NR - 1>();
+                if (!wait_empty(it)) break;
+                const uint32_t first = f.first() + r0;
+                const bool draft = f.draft();
+                const unsigned char *raw = smem + S::RAWS + (it % S::NR) * S::RAW + lt * 16;
+                unsigned char *dst = smem + S::RING + (it % S::NS) * S::TILE;
 #pragma unroll
-                    for (int q = 0; q < ITER; ++q) {
-                        const uint4 w = *reinterpret_cast<const uint4 *>(raw + q * NLOAD * 16);
-                        uint4 lo = make_uint4(fa_e4m3x2_to_half2(w.x), fa_e4m3x2_to_half2(w.x >> 16),
-                                              fa_e4m3x2_to_half2(w.y), fa_e4m3x2_to_half2(w.y >> 16));
-                        uint4 hi = make_uint4(fa_e4m3x2_to_half2(w.z), fa_e4m3x2_to_half2(w.z >> 16),
-                                              fa_e4m3x2_to_half2(w.w), fa_e4m3x2_to_half2(w.w >> 16));
-                        if (draft && first + q * STEP >= s.slots) {
-                            const bool o1 = zero_odd<M>(lo), o2 = zero_odd<M>(hi);
-                            if (o1 || o2) sh.odd[seg & 7] = 1;
-                        }
-                        *reinterpret_cast<uint4 *>(dst + to0 + q * STEP * 128) = lo;
-                        *reinterpret_cast<uint4 *>(dst + to1 + q * STEP * 128) = hi;
+                for (int q = 0; q < x.ITER; ++q) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(raw + q * NLOAD * 16);
+                    uint4 lo = make_uint4(fa_e4m3x2_to_half2(w.x), fa_e4m3x2_to_half2(w.x >> 16),
+                                          fa_e4m3x2_to_half2(w.y), fa_e4m3x2_to_half2(w.y >> 16));
+                    uint4 hi = make_uint4(fa_e4m3x2_to_half2(w.z), fa_e4m3x2_to_half2(w.z >> 16),
+                                          fa_e4m3x2_to_half2(w.w), fa_e4m3x2_to_half2(w.w >> 16));
+                    if (draft && first + q * STEP >= (uint32_t)f.s.slots) {
+                        const bool o1 = zero_odd<M>(lo), o2 = zero_odd<M>(hi);
+                        if (o1 || o2) sh.odd[f.seg & 7] = 1;
                     }
-                    proxy_fence();
-                    mbar_arrive(&sh.full[it % S::NS]);
+                    *reinterpret_cast<uint4 *>(dst + to0 + q * STEP * 128) = lo;
+                    *reinterpret_cast<uint4 *>(dst + to1 + q * STEP * 128) = hi;
                 }
-                ++seg;
+                proxy_fence();
+                mbar_arrive(&sh.full[it % S::NS]);
             }
             cp_wait<0>();
         }
     } else {
         // ---- softmax: stream st, row r of its tile
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
         const int st = warp >> 2, r = tid & 127;
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t ts = tmem + lane_base + st * TS, to = tmem + lane_base + 256 + st * DP;
         int ns = 0, npv = 0, seg = 0;
         float *given = reinterpret_cast<float *>(smem + S::Q + S::TILE);   // stream 1's statistics, where its Q was
         while (walk.next(a, s)) {
-            const int step = s.two ? 1 : 2, begin = s.two ? 0 : st, mine = s.two ? s.n : (s.n + 1 - st) / 2;
+            const int step = s.two() ? 1 : 2, begin = s.two() ? 0 : st, mine = s.two() ? s.n : (s.n + 1 - st) / 2;
             const int sg = seg++;
             if (mine <= 0) continue;                       // a single tile: stream 1 has none
-            const int row = (s.two ? st * TS : 0) + r;     // of the row block
+            const int row = (s.two() ? st * TS : 0) + r;     // of the row block
             const bool live = row < s.rows;
             const bool warp_live = row - lane < s.rows;    // the same for the whole warp
             const int rr = 256 * s.block + row, ti = live ? rr / a.group : 0;
@@ -649,39 +682,39 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
             const bool used = live && ti < s.use;
             float c = a.scale * kLog2e;
             {
-                // the row of Q into the stream's tile
-                const T *q = (const T *)a.q + s.b * a.qb + ti * a.qt + hq * a.qh;
+                // the stream's tile of Q: DP / 8 lanes to a row of 16-byte chunks
+                constexpr int LPR = DP / 8, RPI = 32 / LPR;       // lanes per row, rows per step
                 unsigned char *dst = smem + S::Q + st * S::TILE;
-                float pow = 1.0f;
-                if (E4M3) {
-                    float top = 0.0f;
-                    if (live)
-                        for (int ch = 0; ch < D / 8; ++ch) {
-                            float f[8];
-                            fa_unpack(__ldg(reinterpret_cast<const uint4 *>(q) + ch), f, T());
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
-                        }
-                    // the largest element to [2^8, 2^9)
-                    const int e = top > 0.0f && top < INFINITY ? max(min(fa_exponent(top) - 8, 120), -120) : 0;
-                    pow = fa_pow2(-e);
-                    c *= fa_pow2(e);
-                }
+                const int ch = lane % LPR, sub = lane / LPR, w0 = 32 * (warp & 3);
+                int mine_e = 0;
 #pragma unroll 4
-                for (int ch = 0; ch < DP / 8; ++ch) {
+                for (int i = 0; i < LPR; ++i) {
+                    const int tr = w0 + i * RPI + sub, brow = (s.two() ? st * TS : 0) + tr;
                     uint4 v = make_uint4(0, 0, 0, 0);
-                    if (live && ch < D / 8) {
-                        v = __ldg(reinterpret_cast<const uint4 *>(q) + ch);
-                        if (E4M3) {
-                            float f[8];
-                            fa_unpack(v, f, T());
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) f[e] *= pow;
-                            v = fa_pack(f, M());
-                        }
+                    if (brow < s.rows && ch < D / 8) {
+                        const int pr = 256 * s.block + brow, t = pr / a.group;
+                        v = __ldg(reinterpret_cast<const uint4 *>((const T *)a.q + s.b * a.qb + t * a.qt +
+                                                                  (int64_t)(s.head * a.group + pr - t * a.group) * a.qh) + ch);
                     }
-                    *reinterpret_cast<uint4 *>(dst + chunk_at(r, ch)) = v;
+                    if (E4M3) {
+                        float f[8], top = 0.0f;
+                        fa_unpack(v, f, T());
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
+#pragma unroll
+                        for (int o = LPR / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        // the largest element of the row to [2^8, 2^9)
+                        const int e = top > 0.0f && top < INFINITY ? max(min(fa_exponent(top) - 8, 120), -120) : 0;
+                        const float pow = fa_pow2(-e);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) f[j] *= pow;
+                        v = fa_pack(f, M());
+                        const int from = __shfl_sync(0xffffffffu, e, (lane % RPI) * LPR);
+                        if (lane / RPI == i) mine_e = from;        // this thread's own row
+                    }
+                    *reinterpret_cast<uint4 *>(dst + chunk_at(tr, ch)) = v;
                 }
+                if (E4M3) c *= fa_pow2(mine_e);
                 proxy_fence();
                 mbar_arrive(&sh.q_full[st]);
             }
@@ -703,7 +736,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
             fetch(begin);
             for (int q = 0; q < mine; ++q) {
                 const int tile = begin + q * step;
-                const int64_t first = (int64_t)(s.t0 + tile) * TS;
+                const int first = (s.t0 + tile) * TS;
                 const uint32_t got = __ballot_sync(0xffffffffu, there);
                 float vt = vs;
                 if (E4M3)
@@ -732,24 +765,28 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
 #pragma unroll
                             for (int w = 0; w < 4; ++w) vmx = fmaxf(vmx, sh.vtop[st][w]);
 #pragma unroll 1
-                        for (int w = 0; w < 4; ++w) {
-                            float x[32];
-                            tmem_ld32(ts + 32 * w, x);
-                            if (E4M3)
+                        for (int w = 0; w < 4; w += 2) {
+                            float x[2][32];
+                            tmem_ld32_start(ts + 32 * w, x[0]);
+                            tmem_ld32_start(ts + 32 * w + 32, x[1]);
+                            tmem_wait(x[0]);
+                            tmem_wait(x[1]);
+                            float top[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
 #pragma unroll
                                 for (int e = 0; e < 32; e += 4) {
-                                    const float4 f = *reinterpret_cast<const float4 *>(&sc.k[st][32 * w + e]);
-                                    unpair(mul2(pair(x[e], x[e + 1]), pair(f.x, f.y)), x[e], x[e + 1]);
-                                    unpair(mul2(pair(x[e + 2], x[e + 3]), pair(f.z, f.w)), x[e + 2], x[e + 3]);
+                                    float (&y)[32] = x[h];
+                                    if (E4M3) {
+                                        const float4 f = *reinterpret_cast<const float4 *>(&sc.k[st][32 * (w + h) + e]);
+                                        unpair(mul2(pair(y[e], y[e + 1]), pair(f.x, f.y)), y[e], y[e + 1]);
+                                        unpair(mul2(pair(y[e + 2], y[e + 3]), pair(f.z, f.w)), y[e + 2], y[e + 3]);
+                                    }
+                                    const int j = (e >> 2) & 1;
+                                    top[2 * j] = fmaxf(fmaxf(top[2 * j], y[e]), y[e + 1]);
+                                    top[2 * j + 1] = fmaxf(fmaxf(top[2 * j + 1], y[e + 2]), y[e + 3]);
                                 }
-                            float top[4] = {mx, x[0], x[1], x[2]};
-#pragma unroll
-                            for (int e = 3; e < 27; e += 8)
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) top[j] = fmaxf(fmaxf(top[j], x[e + 2 * j]), x[e + 2 * j + 1]);
-                            top[0] = fmaxf(fmaxf(top[0], x[27]), x[28]);
-                            top[1] = fmaxf(fmaxf(top[1], x[29]), x[30]);
-                            mx = fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), x[31]);
+                            mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                         }
                     } else {
 #pragma unroll 1
@@ -799,11 +836,13 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
                     }
                     const uint64_t cc = pair(c, c), nb = pair(-bias, -bias);
                     uint64_t sum0 = 0, sum1 = 0;
-#pragma unroll 1
-                    for (int w = 0; w < 4; ++w) {
-                        float x[32];
+                    float buf[2][32];
+                    tmem_ld32_start(ts, buf[0]);
+                    // chunk w of the scores (in x) to weights, with the next chunk on its way to nx
+                    auto weigh = [&](int w, float (&x)[32], float (&nx)[32]) {
                         uint32_t p[16];
-                        tmem_ld32(ts + 32 * w, x);
+                        tmem_wait(x);
+                        if (w < 3) tmem_ld32_start(ts + 32 * w + 32, nx);
                         uint32_t z = 0xffffffffu;
                         if (!whole) {
 #pragma unroll
@@ -853,6 +892,11 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
                         }
                         __syncwarp();
                         tmem_st16(ts + 16 * w, p);
+                    };
+#pragma unroll 1
+                    for (int w = 0; w < 4; w += 2) {
+                        weigh(w, buf[0], buf[1]);
+                        weigh(w + 1, buf[1], buf[0]);
                     }
                     float t0, t1, t2, t3;
                     unpair(sum0, t0, t1);
@@ -868,7 +912,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
             mbar_wait(&sh.pv_done[st], (uint32_t)(npv - 1) & 1, fail);
             __syncwarp();
             tc_fence_after();
-            const bool join = !s.two && s.n > 1;
+            const bool join = !s.two() && s.n > 1;
             float f0 = 1.0f, f1 = 0.0f;
             if (join) {
                 if (st == 1) { given[r] = bias; given[TS + r] = l; tc_fence_before(); }
@@ -884,7 +928,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
                     bias = top;
                 }
             }
-            if (st == 0 || s.two) {
+            if (st == 0 || s.two()) {
                 const bool partial = s.n < s.nt;
                 const bool odd = sh.odd[sg & 7] != 0;
                 // the block's first segment uses its first partial slot, its last the second
@@ -908,8 +952,8 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
                         if (odd && used) {
                             // drafted values that are not finite were left out of the product
                             for (int j = 0; j < s.use; ++j) {
-                                const int64_t slot = s.slots + j;
-                                if (slot < (int64_t)s.t0 * TS || slot >= (int64_t)(s.t0 + s.n) * TS || slot >= s.end) continue;
+                                const int slot = s.slots + j;
+                                if (slot < s.t0 * TS || slot >= (s.t0 + s.n) * TS || slot >= s.end) continue;
                                 if (!(seen_bits(a, s, ti, slot) & 1)) continue;
                                 const int64_t at = rows.row((uint32_t)slot);
                                 if (at < 0) continue;
@@ -950,7 +994,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
             }
             tc_fence_before();
             // stream 1 may go on: its accumulator has been read, and so has the segment's flag
-            if (join || s.two) bar_sync(3, 2 * TS);
+            if (join || s.two()) bar_sync(3, 2 * TS);
             else bar_sync(1 + st, TS);
             if (tid == 0) sh.odd[sg & 7] = 0;
         }
@@ -969,28 +1013,27 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
 template <int DP, class T>
 __global__ void __launch_bounds__(256) k_attend_join(AttendArgs a, int ctas) {
     __shared__ Work work;
-    __shared__ int64_t before;
+    __shared__ int before;
     plan(a, work);
     const int units = a.c.kv_heads * a.blocks;
-    const int64_t id = blockIdx.x;
-    const int b = (int)(id / units), u = (int)(id % units);
+    const int b = (int)(blockIdx.x / units), u = (int)(blockIdx.x % units);
     if (threadIdx.x == 0) {
         const int per = run_length(a);
-        int64_t g = work.cum[b / per];
+        int g = work.cum[b / per];
         for (int i = b / per * per; i < b; ++i) g += tiles_of(a, i);
         before = g;
     }
     __syncthreads();
-    const int nt = tiles_of(a, b);
-    const int64_t total = work.cum[RUNS] * units, g0 = before * units + (int64_t)u * nt, g1 = g0 + nt - 1;
-    ctas = (int)min(total, (int64_t)ctas);
-    const int c0 = (int)(((g0 + 1) * ctas - 1) / total), c1 = (int)(((g1 + 1) * ctas - 1) / total);
+    const int nt = tiles_of(a, b), total = work.cum[RUNS] * units, g0 = before * units + u * nt, g1 = g0 + nt - 1;
+    ctas = min(total, ctas);
+    // the blocks whose runs hold the unit's first and last tile
+    const int c0 = (int)((((int64_t)g0 + 1) * ctas - 1) / total), c1 = (int)((((int64_t)g1 + 1) * ctas - 1) / total);
     const int lane = threadIdx.x & 31, head = u / a.blocks, block = u % a.blocks;
     const int rows = min(a.rows - 256 * block, 256), D = a.c.head_dim;
     bool failed = false;
     for (int c = c0; c <= c1; ++c) failed |= a.status[c] != 0;
     if (c0 == c1 && !failed) return;
-    const int slot0 = total * c0 / ctas == g0 ? 0 : 1;
+    const int slot0 = run_start(total, c0, ctas) == g0 ? 0 : 1;
     for (int row = blockIdx.y * 32 + (threadIdx.x >> 5); row < min(rows, (int)blockIdx.y * 32 + 32); row += 8) {
         float top = -INFINITY, l = 0.0f, o[DP / 32];
 #pragma unroll
@@ -1081,7 +1124,8 @@ extern "C" fa_status fa_tree_attention(const fa_kv_cache *cache, int32_t dtype, 
     if (cache->format != FA_CACHE_E4M3 && cache->format != dtype)
         return fa_refuse(fn, "a 16-bit cache must have the type of q", FA_ERR_UNSUPPORTED);
     if (!(scale > 0.0f && scale < INFINITY)) return fa_refuse(fn, "scale must be positive and finite");
-    if (((int64_t)max_pages << a.c.page_shift) > 2147483647LL - 4096) return fa_refuse(fn, "max_pages * page_size out of range");
+    const int64_t slots = (int64_t)max_pages << a.c.page_shift;
+    if (slots > 2147483647LL - 4096) return fa_refuse(fn, "max_pages * page_size out of range");
     if ((int64_t)cache->n_pages * cache->kv_heads > 2147483647LL) return fa_refuse(fn, "n_pages * kv_heads out of range");
     if (B == 0 || T == 0) return FA_OK;
     if (!q || !out || !length) return fa_refuse(fn, "NULL buffer");
@@ -1095,7 +1139,8 @@ extern "C" fa_status fa_tree_attention(const fa_kv_cache *cache, int32_t dtype, 
     if ((int64_t)T * a.group > 1 << 24) return fa_refuse(fn, "T * group out of range");
     a.rows = T * a.group;
     a.blocks = (a.rows + 255) / 256;
-    if ((int64_t)B * cache->kv_heads * a.blocks > 2147483647) return fa_refuse(fn, "B * kv_heads out of range");
+    if ((int64_t)B * cache->kv_heads * a.blocks * ((slots + TS - 1) / TS + 1) > 2147483647)
+        return fa_refuse(fn, "B * kv_heads * row blocks * tiles of 128 slots out of range");
     a.q = q; a.qb = q_batch_stride; a.qt = q_token_stride; a.qh = q_head_stride;
     a.length = length; a.count = count; a.mask = mask; a.scale = scale; a.out = out; a.lse = lse;
     const size_t dp = cache->head_dim <= 64 ? 64 : 128;
