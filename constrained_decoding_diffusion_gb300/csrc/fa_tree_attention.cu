@@ -44,6 +44,7 @@ constexpr int REGS_SOFTMAX = 144, REGS_LOAD = 64, REGS_MMA = 64;
 constexpr int MAX_CTAS = 152;
 constexpr long long kSpinCycles = 2000000000LL;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kUnitCost = 3;                 // what starting a unit costs, in tiles
 constexpr float kGrow = 6.0f;                // how far a score may exceed the reference (log2)
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -72,6 +73,19 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volati
 }
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint64_t *bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                 "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+// one arrival for the warp, after what its lanes did before
+__device__ __forceinline__ void warp_arrive(uint64_t *bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -128,6 +142,15 @@ __device__ __forceinline__ void tmem_wait(float (&r)[32]) {
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
     tmem_ld32_start(taddr, v);
     tmem_wait(v);
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+        : "r"(taddr)
+        : "memory");
 }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
     asm volatile(
@@ -205,10 +228,13 @@ __device__ __forceinline__ int tiles_of(const AttendArgs &a, int b) {
     extent(a, b, n, use, end);
     return max(1, (end + TS - 1) / TS);   // an empty sequence's rows are written by one masked tile
 }
+// A unit's share of the work list: its tiles, then kUnitCost places that stand for its start (its
+// queries, its masked tile, its result) and hold no tile.
+__device__ __forceinline__ int places_of(const AttendArgs &a, int b) { return tiles_of(a, b) + kUnitCost; }
 
 constexpr int RUNS = 64;
 struct Work {
-    int cum[RUNS + 2];   // tiles of one (head, row block) before each of 64 runs of sequences
+    int cum[RUNS + 2];   // places of one (head, row block) before each of 64 runs of sequences
 };
 __device__ __forceinline__ int run_length(const AttendArgs &a) { return (a.B + RUNS - 1) / RUNS; }
 
@@ -217,7 +243,7 @@ __device__ __forceinline__ void plan(const AttendArgs &a, Work &w) {
     const int tid = threadIdx.x, per = run_length(a);
     if (tid < RUNS) {
         int s = 0;
-        for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) s += tiles_of(a, b);
+        for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) s += places_of(a, b);
         w.cum[tid] = s;
     }
     __syncthreads();
@@ -236,7 +262,7 @@ __device__ __forceinline__ void plan(const AttendArgs &a, Work &w) {
     __syncthreads();
 }
 
-// the first tile of block c's run, of `total` tiles over `ctas` blocks
+// the first place of block c's run, of `total` places over `ctas` blocks
 __device__ __forceinline__ int run_start(int total, int c, int ctas) { return (int)((int64_t)total * c / ctas); }
 
 struct Segment {
@@ -265,26 +291,28 @@ struct Walk {
         b = lo * run_length(a);
         base = w.cum[lo] * units;
         while (true) {
-            const int next = base + tiles_of(a, b) * units;
+            const int next = base + places_of(a, b) * units;
             if (g < next) break;
             base = next;
             ++b;
         }
     }
     __device__ __forceinline__ bool next(const AttendArgs &a, Segment &s) {
-        if (g >= g1) return false;
-        extent(a, b, s.slots, s.use, s.end);
-        s.b = b;
-        s.nt = max(1, (s.end + TS - 1) / TS);
-        const int off = g - base, u = off / s.nt;
-        s.t0 = off - u * s.nt;
-        s.head = u / a.blocks;
-        s.block = u - s.head * a.blocks;
-        s.n = min(s.nt - s.t0, g1 - g);
-        s.rows = min(a.rows - 256 * s.block, 256);
-        g += s.n;
-        if (g - base >= s.nt * a.c.kv_heads * a.blocks) { base = g; ++b; }
-        return true;
+        while (g < g1) {
+            extent(a, b, s.slots, s.use, s.end);
+            s.b = b;
+            s.nt = max(1, (s.end + TS - 1) / TS);
+            const int places = s.nt + kUnitCost, off = g - base, u = off / places;
+            s.t0 = off - u * places;
+            s.head = u / a.blocks;
+            s.block = u - s.head * a.blocks;
+            s.n = min(s.nt - s.t0, g1 - g);
+            s.rows = min(a.rows - 256 * s.block, 256);
+            g += min(places - s.t0, g1 - g);
+            if (g - base >= places * a.c.kv_heads * a.blocks) { base = g; ++b; }
+            if (s.n > 0) return true;               // the run may begin behind a unit's last tile
+        }
+        return false;
     }
 };
 
@@ -313,6 +341,8 @@ struct Shape {
 
 struct Misc {
     uint64_t full[10], empty[10], s_full[2], p_full[2], pv_done[2], q_full[2], done;
+    uint64_t raw_full[8], raw_empty[8];
+    uint32_t raw_rows[8][4];          // which rows of a raw tile were copied
     uint32_t tmem;
     int fail;
     int odd[8];                       // segment & 7: a drafted value is not finite
@@ -418,6 +448,28 @@ __device__ __forceinline__ uint32_t seen_bits(const AttendArgs &a, const Segment
     return v;
 }
 
+// Drafted values that are not finite are left out of the products (a row that does not see them must
+// not meet them); here they join the rows that do: N columns from col on of drafted token t's result.
+template <bool E4M3, class T, int N>
+__device__ __forceinline__ void add_odd(const AttendArgs &a, const Segment &s, const Rows &rows, int t, int col, float (&o)[N]) {
+#pragma unroll 1
+    for (int j = 0; j < s.use; ++j) {
+        const int slot = s.slots + j;
+        if (slot < s.t0 * TS || slot >= (s.t0 + s.n) * TS || slot >= s.end || !(seen_bits(a, s, t, slot) & 1)) continue;
+        const int64_t at = rows.row((uint32_t)slot);
+        if (at < 0) continue;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            if (col + e >= a.c.head_dim) break;
+            const int64_t x = at * a.c.head_dim + col + e;
+            float y;
+            if (E4M3) y = (((const uint8_t *)a.c.v)[x] & 0x7f) == 0x7f || !(fabsf(a.c.v_scale[at]) < INFINITY) ? NAN : 0.0f;
+            else y = fa_to_f32(((const T *)a.c.v)[x]);
+            if (!isfinite(y)) o[e] += y;
+        }
+    }
+}
+
 // M: the tensor cores' 16-bit type; T: q's and out's
 template <int DP, bool E4M3, class T, class M>
 __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
@@ -440,12 +492,13 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
 
     plan(a, work);
     if (tid == 0) {
-        for (int i = 0; i < S::NS; ++i) { mbar_init(&sh.full[i], NLOAD); mbar_init(&sh.empty[i], 1); }
+        for (int i = 0; i < S::NS; ++i) { mbar_init(&sh.full[i], NLOAD / 32); mbar_init(&sh.empty[i], 1); }
+        for (int i = 0; i < S::NR; ++i) { mbar_init(&sh.raw_full[i], 1); mbar_init(&sh.raw_empty[i], NLOAD / 32); }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s_full[i], 1);
-            mbar_init(&sh.p_full[i], TS);
+            mbar_init(&sh.p_full[i], 4);
             mbar_init(&sh.pv_done[i], 1);
-            mbar_init(&sh.q_full[i], TS);
+            mbar_init(&sh.q_full[i], 4);
         }
         mbar_init(&sh.done, 1);
         sh.fail = 0;
@@ -553,6 +606,60 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
             }
             umma_commit(&sh.done);   // completes once every MMA issued above has
         }
+        if constexpr (E4M3) {
+        if (warp == 17) {
+            // ---- raw codes: one bulk copy for the slots of a tile that share a page
+            Feed f(walk);
+            Rows rows;
+            uint32_t page[4];
+            auto look = [&]() {
+                rows = Rows(a, f.s);
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const uint32_t slot = f.first() + 32 * w + lane;
+                    page[w] = slot < (uint32_t)f.s.end ? rows.page(slot) : 0xffffffffu;
+                }
+            };
+            const uint32_t in_page = (1u << a.c.page_shift) - 1;
+            bool more = f.next(a);
+            if (more) look();
+            int it = 0;
+            for (; more; ++it) {
+                const int slot = it % S::NR;
+                if (it >= S::NR && !mbar_wait(&sh.raw_empty[slot], (uint32_t)(it / S::NR - 1) & 1, fail)) break;
+                __syncwarp();
+                uint32_t there[4], n = 0;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    there[w] = __ballot_sync(0xffffffffu, page[w] < rows.n_pages);
+                    n += __popc(there[w]);
+                }
+                if (lane == 0) {
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) sh.raw_rows[slot][w] = there[w];
+                    mbar_expect(&sh.raw_full[slot], n * D);
+                }
+                __syncwarp();
+                const uint8_t *src = (const uint8_t *)(f.value ? a.c.v : a.c.k);
+                const uint32_t dst = smem_u32(smem + S::RAWS) + slot * S::RAW;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const uint32_t r = 32 * w + lane, at = f.first() + r;
+                    if (page[w] < rows.n_pages && ((at & in_page) == 0 || r == 0)) {
+                        const uint32_t len = min(min(in_page + 1 - (at & in_page), TS - r), (uint32_t)f.s.end - at);
+                        bulk_copy(dst + r * D, src + rows.row(page[w], at) * D, len * D, &sh.raw_full[slot]);
+                    }
+                }
+                more = f.next(a);
+                if (more) look();
+            }
+            // no copy may land after the block has gone
+            for (int i = max(it - S::NR, 0); i < it; ++i) {
+                const long long t0 = clock64();
+                while (!mbar_try_wait(&sh.raw_full[i % S::NR], (uint32_t)(i / S::NR) & 1) && clock64() - t0 < kSpinCycles) {}
+            }
+        }
+        }
     } else if (warp >= 8) {
         // ---- loading
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_LOAD));
@@ -599,57 +706,40 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
                 if (it >= LAG<DP>) {
                     cp_wait<LAG<DP>>();
                     proxy_fence();
-                    mbar_arrive(&sh.full[(it - LAG<DP>) % S::NS]);
+                    warp_arrive(&sh.full[(it - LAG<DP>) % S::NS]);
                 }
             }
             cp_wait<0>();
             proxy_fence();
             if (!more)
-                for (int i = max(it - LAG<DP>, 0); i < it; ++i) mbar_arrive(&sh.full[i % S::NS]);
+                for (int i = max(it - LAG<DP>, 0); i < it; ++i) warp_arrive(&sh.full[i % S::NS]);
         } else {
-            // raw codes arrive NR - 1 tiles ahead, each thread converting the chunks it copied
-            constexpr int RPR = DP / 16, STEP = NLOAD / RPR;
+            // a thread converts one 16-byte chunk of every STEP-th row
+            constexpr int RPR = DP / 16, STEP = NLOAD / RPR, ITER = TS / STEP;
             const int c = lt % RPR, r0 = lt / RPR;
             const uint32_t to0 = chunk_at(r0, 2 * c), to1 = chunk_at(r0, 2 * c + 1);
             const bool column = c * 16 < D;
-            Feed ahead(walk);
-            Share<STEP> x;
-            int issued = 0;
-            const uint32_t raws = smem_u32(smem + S::RAWS) + lt * 16;
-            bool more = ahead.next(a);
-            if (more) x.look(a, ahead, r0, column);
-            auto issue = [&]() {
-                if (more) {
-                    const uint32_t first = ahead.first() + r0;
-                    const uint8_t *src = (const uint8_t *)(ahead.value ? a.c.v : a.c.k) + c * 16;
-                    const uint32_t dst = raws + (issued % S::NR) * S::RAW;
-#pragma unroll
-                    for (int q = 0; q < x.ITER; ++q) {
-                        const int64_t row = x.rows.row(x.page[q], first + q * STEP);
-                        cp_async16(dst + q * NLOAD * 16, src + (row < 0 ? 0 : row * D), row >= 0);
-                    }
-                    ++issued;
-                    more = ahead.next(a);
-                    if (more) x.look(a, ahead, r0, column);
-                }
-                cp_commit();
-            };
-            for (int i = 0; i < S::NR - 1; ++i) issue();
             for (; f.next(a); ++it) {
-                issue();
-                cp_wait<S::NR - 1>();
+                const int from = it % S::NR;
+                if (!mbar_wait(&sh.raw_full[from], (uint32_t)(it / S::NR) & 1, fail)) break;
+                const unsigned char *raw = smem + S::RAWS + from * S::RAW + (r0 * D + c * 16);
+                uint4 w[ITER];
+#pragma unroll
+                for (int q = 0; q < ITER; ++q) {
+                    const int r = r0 + q * STEP;
+                    const bool there = column && (sh.raw_rows[from][r >> 5] >> (r & 31) & 1);
+                    w[q] = there ? *reinterpret_cast<const uint4 *>(raw + q * STEP * D) : make_uint4(0, 0, 0, 0);
+                }
                 if (!wait_empty(it)) break;
                 const uint32_t first = f.first() + r0;
                 const bool draft = f.draft();
-                const unsigned char *raw = smem + S::RAWS + (it % S::NR) * S::RAW + lt * 16;
                 unsigned char *dst = smem + S::RING + (it % S::NS) * S::TILE;
 #pragma unroll
-                for (int q = 0; q < x.ITER; ++q) {
-                    const uint4 w = *reinterpret_cast<const uint4 *>(raw + q * NLOAD * 16);
-                    uint4 lo = make_uint4(fa_e4m3x2_to_half2(w.x), fa_e4m3x2_to_half2(w.x >> 16),
-                                          fa_e4m3x2_to_half2(w.y), fa_e4m3x2_to_half2(w.y >> 16));
-                    uint4 hi = make_uint4(fa_e4m3x2_to_half2(w.z), fa_e4m3x2_to_half2(w.z >> 16),
-                                          fa_e4m3x2_to_half2(w.w), fa_e4m3x2_to_half2(w.w >> 16));
+                for (int q = 0; q < ITER; ++q) {
+                    uint4 lo = make_uint4(fa_e4m3x2_to_half2(w[q].x), fa_e4m3x2_to_half2(w[q].x >> 16),
+                                          fa_e4m3x2_to_half2(w[q].y), fa_e4m3x2_to_half2(w[q].y >> 16));
+                    uint4 hi = make_uint4(fa_e4m3x2_to_half2(w[q].z), fa_e4m3x2_to_half2(w[q].z >> 16),
+                                          fa_e4m3x2_to_half2(w[q].w), fa_e4m3x2_to_half2(w[q].w >> 16));
                     if (draft && first + q * STEP >= (uint32_t)f.s.slots) {
                         const bool o1 = zero_odd<M>(lo), o2 = zero_odd<M>(hi);
                         if (o1 || o2) sh.odd[f.seg & 7] = 1;
@@ -657,10 +747,10 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
                     *reinterpret_cast<uint4 *>(dst + to0 + q * STEP * 128) = lo;
                     *reinterpret_cast<uint4 *>(dst + to1 + q * STEP * 128) = hi;
                 }
+                warp_arrive(&sh.raw_empty[from]);
                 proxy_fence();
-                mbar_arrive(&sh.full[it % S::NS]);
+                warp_arrive(&sh.full[it % S::NS]);
             }
-            cp_wait<0>();
         }
     } else {
         // ---- softmax: stream st, row r of its tile
@@ -674,28 +764,32 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
             const int step = s.two() ? 1 : 2, begin = s.two() ? 0 : st, mine = s.two() ? s.n : (s.n + 1 - st) / 2;
             const int sg = seg++;
             if (mine <= 0) continue;                       // a single tile: stream 1 has none
-            const int row = (s.two() ? st * TS : 0) + r;     // of the row block
+            // Up to 64 (32) rows lie two (four) times in the 128 lanes: copy `copy` weighs its part of
+            // a tile's columns and gives the others no weight, and the copies are joined at the end.
+            const int copies = s.rows <= 32 ? 4 : s.rows <= 64 ? 2 : 1, pad = TS / copies;
+            const int copy = r / pad, w_begin = copy * (4 / copies), w_end = w_begin + 4 / copies;
+            const int row = (s.two() ? st * TS : 0) + r - copy * pad;   // of the row block
             const bool live = row < s.rows;
             const bool warp_live = row - lane < s.rows;    // the same for the whole warp
             const int rr = 256 * s.block + row, ti = live ? rr / a.group : 0;
             const int hq = s.head * a.group + (live ? rr - ti * a.group : 0);
             const bool used = live && ti < s.use;
             float c = a.scale * kLog2e;
-            {
-                // the stream's tile of Q: DP / 8 lanes to a row of 16-byte chunks
+            if (warp_live) {
+                // the warp's rows of Q into the stream's tile: DP / 8 lanes to a row of 16-byte chunks
                 constexpr int LPR = DP / 8, RPI = 32 / LPR;       // lanes per row, rows per step
                 unsigned char *dst = smem + S::Q + st * S::TILE;
                 const int ch = lane % LPR, sub = lane / LPR, w0 = 32 * (warp & 3);
+                const long long mine_at = s.b * a.qb + ti * a.qt + hq * a.qh;
+                const int rows_here = min(s.rows - (row - lane), 32);
                 int mine_e = 0;
 #pragma unroll 4
                 for (int i = 0; i < LPR; ++i) {
-                    const int tr = w0 + i * RPI + sub, brow = (s.two() ? st * TS : 0) + tr;
+                    if (i * RPI >= rows_here) break;
+                    const int of = i * RPI + sub;
+                    const long long at = __shfl_sync(0xffffffffu, mine_at, of);
                     uint4 v = make_uint4(0, 0, 0, 0);
-                    if (brow < s.rows && ch < D / 8) {
-                        const int pr = 256 * s.block + brow, t = pr / a.group;
-                        v = __ldg(reinterpret_cast<const uint4 *>((const T *)a.q + s.b * a.qb + t * a.qt +
-                                                                  (int64_t)(s.head * a.group + pr - t * a.group) * a.qh) + ch);
-                    }
+                    if (of < rows_here && ch < D / 8) v = __ldg(reinterpret_cast<const uint4 *>((const T *)a.q + at) + ch);
                     if (E4M3) {
                         float f[8], top = 0.0f;
                         fa_unpack(v, f, T());
@@ -705,19 +799,19 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
                         for (int o = LPR / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
                         // the largest element of the row to [2^8, 2^9)
                         const int e = top > 0.0f && top < INFINITY ? max(min(fa_exponent(top) - 8, 120), -120) : 0;
-                        const float pow = fa_pow2(-e);
+                        const float pow = __int_as_float((127 - e) << 23);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) f[j] *= pow;
                         v = fa_pack(f, M());
                         const int from = __shfl_sync(0xffffffffu, e, (lane % RPI) * LPR);
                         if (lane / RPI == i) mine_e = from;        // this thread's own row
                     }
-                    *reinterpret_cast<uint4 *>(dst + chunk_at(tr, ch)) = v;
+                    *reinterpret_cast<uint4 *>(dst + chunk_at(w0 + of, ch)) = v;
                 }
-                if (E4M3) c *= fa_pow2(mine_e);
+                if (E4M3) c *= __int_as_float((127 + mine_e) << 23);
                 proxy_fence();
-                mbar_arrive(&sh.q_full[st]);
             }
+            warp_arrive(&sh.q_full[st]);
             float m = -INFINITY, l = 0.0f, bias = 0.0f;
             int ev = -120;
             // slot r of each tile: whether it is held and its scales, one tile ahead
@@ -747,7 +841,11 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
                     sh.held[st][warp & 3] = got;
                     if (E4M3) sh.vtop[st][warp & 3] = vt;
                 }
-                if (E4M3) { sc.k[st][r] = ks; sc.v[st][r] = vs; }
+                if (E4M3) {
+                    if (first + r >= s.slots && !(fabsf(vs) < INFINITY)) { vs = 0.0f; sh.odd[sg & 7] = 1; }
+                    sc.k[st][r] = ks;
+                    sc.v[st][r] = vs;
+                }
                 if (q + 1 < mine) fetch(tile + step);
                 bar_sync(1 + st, TS);
                 bool whole = first + TS <= s.slots;
@@ -759,52 +857,52 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
                 if (warp_live) {
                     // the largest score (before the scale), and the largest value scale, that the row sees
                     float mx = -INFINITY, vmx = 0.0f;
-                    uint32_t see[4];
-                    if (whole) {
+                    uint32_t see[4] = {0, 0, 0, 0};
+                    float buf[2][32];
+                    // chunk w of 32 scores, times the keys' scales, hidden ones to -inf
+                    auto finish_chunk = [&](int w, float (&x)[32], uint32_t z) {
                         if (E4M3)
 #pragma unroll
-                            for (int w = 0; w < 4; ++w) vmx = fmaxf(vmx, sh.vtop[st][w]);
+                            for (int e = 0; e < 32; e += 4) {
+                                const float4 f = *reinterpret_cast<const float4 *>(&sc.k[st][32 * w + e]);
+                                unpair(mul2(pair(x[e], x[e + 1]), pair(f.x, f.y)), x[e], x[e + 1]);
+                                unpair(mul2(pair(x[e + 2], x[e + 3]), pair(f.z, f.w)), x[e + 2], x[e + 3]);
+                            }
+                        if (z != 0xffffffffu)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) x[e] = (z >> e & 1) ? x[e] : -INFINITY;
+                    };
+                    auto seen = [&](int w) {
+                        uint32_t z = see[0];
+#pragma unroll
+                        for (int j = 1; j < 4; ++j) z = j == w ? see[j] : z;
+                        return z;
+                    };
 #pragma unroll 1
-                        for (int w = 0; w < 4; w += 2) {
-                            float x[2][32];
-                            tmem_ld32_start(ts + 32 * w, x[0]);
-                            tmem_ld32_start(ts + 32 * w + 32, x[1]);
-                            tmem_wait(x[0]);
-                            tmem_wait(x[1]);
-                            float top[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
+                    for (int w = w_begin; w < w_end; ++w) {
+                        float (&x)[32] = buf[0];
+                        tmem_ld32_start(ts + 32 * w, x);
+                        uint32_t z = 0xffffffffu;
+                        if (!whole) z = used ? sh.held[st][w] & seen_bits(a, s, ti, first + 32 * w) : 0u;
 #pragma unroll
-                            for (int h = 0; h < 2; ++h)
+                        for (int j = 0; j < 4; ++j) see[j] = j == w ? z : see[j];
+                        if (E4M3) {
+                            if (whole) {
+                                vmx = fmaxf(vmx, sh.vtop[st][w]);
+                            } else {
 #pragma unroll
-                                for (int e = 0; e < 32; e += 4) {
-                                    float (&y)[32] = x[h];
-                                    if (E4M3) {
-                                        const float4 f = *reinterpret_cast<const float4 *>(&sc.k[st][32 * (w + h) + e]);
-                                        unpair(mul2(pair(y[e], y[e + 1]), pair(f.x, f.y)), y[e], y[e + 1]);
-                                        unpair(mul2(pair(y[e + 2], y[e + 3]), pair(f.z, f.w)), y[e + 2], y[e + 3]);
-                                    }
-                                    const int j = (e >> 2) & 1;
-                                    top[2 * j] = fmaxf(fmaxf(top[2 * j], y[e]), y[e + 1]);
-                                    top[2 * j + 1] = fmaxf(fmaxf(top[2 * j + 1], y[e + 2]), y[e + 3]);
-                                }
-                            mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                                for (int e = 0; e < 32; ++e) vmx = (z >> e & 1) ? fmaxf(vmx, sc.v[st][32 * w + e]) : vmx;
+                            }
                         }
-                    } else {
-#pragma unroll 1
-                        for (int w = 0; w < 4; ++w) {
-                            float x[32];
-                            const uint32_t z = used ? sh.held[st][w] & seen_bits(a, s, ti, first + 32 * w) : 0u;
+                        __syncwarp();
+                        tmem_wait(x);
+                        finish_chunk(w, x, z);
+                        float top[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                if (j == w) see[j] = z;
-                            __syncwarp();
-                            tmem_ld32(ts + 32 * w, x);
+                        for (int e = 0; e < 32; e += 8)
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (z >> e & 1) {
-                                    mx = fmaxf(mx, E4M3 ? x[e] * sc.k[st][32 * w + e] : x[e]);
-                                    if (E4M3) vmx = fmaxf(vmx, sc.v[st][32 * w + e]);
-                                }
-                        }
+                            for (int j = 0; j < 4; ++j) top[j] = fmaxf(fmaxf(top[j], x[e + 2 * j]), x[e + 2 * j + 1]);
+                        mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                     }
                     const int e2 = E4M3 ? max(ev, min(max(fa_exponent(vmx) + 1, -120), 120)) : 0;
                     const bool move = mx > -INFINITY && ((mx - m) * c > kGrow || e2 > ev || m == -INFINITY);
@@ -836,67 +934,49 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
                     }
                     const uint64_t cc = pair(c, c), nb = pair(-bias, -bias);
                     uint64_t sum0 = 0, sum1 = 0;
-                    float buf[2][32];
-                    tmem_ld32_start(ts, buf[0]);
                     // chunk w of the scores (in x) to weights, with the next chunk on its way to nx
-                    auto weigh = [&](int w, float (&x)[32], float (&nx)[32]) {
+                    auto weigh = [&](int w, float (&x)[32], float (&nx)[32], bool loaded) {
                         uint32_t p[16];
-                        tmem_wait(x);
-                        if (w < 3) tmem_ld32_start(ts + 32 * w + 32, nx);
-                        uint32_t z = 0xffffffffu;
-                        if (!whole) {
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                if (j == w) z = see[j];
+                        if (!loaded) {
+                            tmem_wait(x);
+                            if (w + 1 < w_end) tmem_ld32_start(ts + 32 * w + 32, nx);
+                            finish_chunk(w, x, seen(w));
                         }
-                        if (z == 0xffffffffu) {
 #pragma unroll
-                            for (int e = 0; e < 32; e += 4) {
-                                uint64_t a0 = pair(x[e], x[e + 1]), a1 = pair(x[e + 2], x[e + 3]);
-                                if (E4M3) {
-                                    const float4 f = *reinterpret_cast<const float4 *>(&sc.k[st][32 * w + e]);
-                                    a0 = mul2(a0, pair(f.x, f.y));
-                                    a1 = mul2(a1, pair(f.z, f.w));
-                                }
-                                float y[4];
-                                unpair(fma2(a0, cc, nb), y[0], y[1]);
-                                unpair(fma2(a1, cc, nb), y[2], y[3]);
+                        for (int e = 0; e < 32; e += 4) {
+                            float y[4];
+                            unpair(fma2(pair(x[e], x[e + 1]), cc, nb), y[0], y[1]);
+                            unpair(fma2(pair(x[e + 2], x[e + 3]), cc, nb), y[2], y[3]);
 #pragma unroll
-                                for (int j = 0; j < 4; ++j) y[j] = ex2(y[j]);
-                                a0 = pair(y[0], y[1]);
-                                a1 = pair(y[2], y[3]);
-                                sum0 = add2(sum0, a0);
-                                sum1 = add2(sum1, a1);
-                                if (E4M3) {
-                                    const float4 g = *reinterpret_cast<const float4 *>(&sc.v[st][32 * w + e]);
-                                    unpair(mul2(a0, pair(g.x, g.y)), y[0], y[1]);
-                                    unpair(mul2(a1, pair(g.z, g.w)), y[2], y[3]);
-                                }
-                                p[e / 2] = fa_pack2(y[0], y[1], M());
-                                p[e / 2 + 1] = fa_pack2(y[2], y[3], M());
+                            for (int j = 0; j < 4; ++j) y[j] = ex2(y[j]);
+                            const uint64_t a0 = pair(y[0], y[1]), a1 = pair(y[2], y[3]);
+                            sum0 = add2(sum0, a0);
+                            sum1 = add2(sum1, a1);
+                            if (E4M3) {
+                                const float4 g = *reinterpret_cast<const float4 *>(&sc.v[st][32 * w + e]);
+                                unpair(mul2(a0, pair(g.x, g.y)), y[0], y[1]);
+                                unpair(mul2(a1, pair(g.z, g.w)), y[2], y[3]);
                             }
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 32; e += 2) {
-                                float y[2];
-#pragma unroll
-                                for (int j = 0; j < 2; ++j) {
-                                    const bool on = z >> (e + j) & 1;
-                                    const float t = E4M3 ? x[e + j] * sc.k[st][32 * w + e + j] : x[e + j];
-                                    y[j] = on ? ex2(fmaf(t, c, -bias)) : 0.0f;
-                                    l += y[j];
-                                    if (E4M3) y[j] = on ? y[j] * sc.v[st][32 * w + e + j] : 0.0f;   // whatever the scale is
-                                }
-                                p[e / 2] = fa_pack2(y[0], y[1], M());
-                            }
+                            p[e / 2] = fa_pack2(y[0], y[1], M());
+                            p[e / 2 + 1] = fa_pack2(y[2], y[3], M());
                         }
-                        __syncwarp();
                         tmem_st16(ts + 16 * w, p);
                     };
+                    if (copies == 4) {
+                        weigh(w_begin, buf[0], buf[1], true);       // the one chunk is still in registers
+                    } else {
+                        tmem_ld32_start(ts + 32 * w_begin, buf[0]);
 #pragma unroll 1
-                    for (int w = 0; w < 4; w += 2) {
-                        weigh(w, buf[0], buf[1]);
-                        weigh(w + 1, buf[1], buf[0]);
+                        for (int w = w_begin; w < w_end; w += 2) {
+                            weigh(w, buf[0], buf[1], false);
+                            weigh(w + 1, buf[1], buf[0], false);
+                        }
+                    }
+                    if (copies > 1) {
+                        const uint32_t none[16] = {};
+#pragma unroll 1
+                        for (int w = 0; w < 4; ++w)
+                            if (w < w_begin || w >= w_end) tmem_st16(ts + 16 * w, none);
                     }
                     float t0, t1, t2, t3;
                     unpair(sum0, t0, t1);
@@ -905,14 +985,87 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
                     tmem_st_wait();
                 }
                 tc_fence_before();
-                mbar_arrive(&sh.p_full[st]);
+                warp_arrive(&sh.p_full[st]);
                 ++npv;
             }
             // ---- the segment's result
             mbar_wait(&sh.pv_done[st], (uint32_t)(npv - 1) & 1, fail);
             __syncwarp();
             tc_fence_after();
-            const bool join = !s.two() && s.n > 1;
+            const bool pair_up = !s.two() && s.n > 1, join = pair_up && copies == 1, partial = s.n < s.nt;
+            // of the block's partial results, slot 1 is a unit's first part, slot 0 a later one
+            const int64_t prow0 = ((int64_t)blockIdx.x * 2 + (s.t0 == 0 ? 1 : 0)) * 256;
+            if (copies > 1) {
+                // join the copies (of both streams) through shared memory, a quarter of the columns
+                // at a time: stream 0's queries become the sums, what follows them the statistics
+                constexpr int EC = DP / 4, EG = EC / 4;            // columns, 16-byte groups of them
+                const int streams = pair_up ? 2 : 1, threads = streams * TS, me = st * TS + r;
+                float *acc = reinterpret_cast<float *>(smem + S::Q);
+                float *stats = acc + threads * EC;
+                auto sync = [&]() { bar_sync(pair_up ? 3 : 1, threads); };
+                sync();                                            // all products with the queries are done
+                stats[me] = bias;
+                stats[threads + me] = l;
+                sync();
+                const int parts = copies * streams;
+                float top = -INFINITY, sum = 0.0f;
+                for (int i = 0; i < parts; ++i) {
+                    const int at = row + i * pad;
+                    if (!(stats[threads + at] == 0.0f)) top = fmaxf(top, stats[at]);
+                }
+                for (int i = 0; i < parts; ++i) {
+                    const int at = row + i * pad;
+                    const float li = stats[threads + at];
+                    if (!(li == 0.0f)) sum += li * ex2(stats[at] - top);
+                }
+                const float f = l == 0.0f || !used ? 0.0f : ex2(bias - top) / sum;
+                const bool odd = sh.odd[sg & 7] != 0;
+#pragma unroll 1
+                for (int w = 0; w < 4; ++w) {
+                    if (warp_live) {
+                        float o[EC];
+                        if constexpr (EC == 32) tmem_ld32(to + EC * w, o);
+                        else tmem_ld16(to + EC * w, o);
+#pragma unroll
+                        for (int g = 0; g < EG; ++g)
+                            *reinterpret_cast<float4 *>(acc + me * EC + ((g ^ (me & (EG - 1))) << 2)) =
+                                f == 0.0f ? make_float4(0, 0, 0, 0)
+                                          : make_float4(o[4 * g] * f, o[4 * g + 1] * f, o[4 * g + 2] * f, o[4 * g + 3] * f);
+                    }
+                    sync();
+                    for (int x = me; x < s.rows * EG; x += threads) {
+                        const int q = x / EG, g = x % EG, col = EC * w + 4 * g;
+                        float4 y = make_float4(0, 0, 0, 0);
+                        for (int i = 0; i < parts; ++i) {
+                            const int at = q + i * pad;
+                            const float4 z = *reinterpret_cast<const float4 *>(acc + at * EC + ((g ^ (at & (EG - 1))) << 2));
+                            y.x += z.x; y.y += z.y; y.z += z.z; y.w += z.w;
+                        }
+                        const int qr = 256 * s.block + q, t = qr / a.group;
+                        if (odd && t < s.use) {
+                            float o[4] = {y.x, y.y, y.z, y.w};
+                            add_odd<E4M3, T, 4>(a, s, rows, t, col, o);
+                            y = make_float4(o[0], o[1], o[2], o[3]);
+                        }
+                        if (partial) {
+                            *reinterpret_cast<float4 *>(a.part_o + (prow0 + q) * DP + col) = y;
+                        } else if (col < D) {
+                            T *dst = (T *)a.out + (((int64_t)s.b * a.T + t) * a.heads + s.head * a.group + qr - t * a.group) * D + col;
+                            *reinterpret_cast<uint2 *>(dst) = make_uint2(fa_pack2(y.x, y.y, T()), fa_pack2(y.z, y.w, T()));
+                        }
+                    }
+                    sync();
+                }
+                if (st == 0 && copy == 0 && live) {
+                    const float lse = used && sum != 0.0f ? top + log2f(sum) : -INFINITY;
+                    if (partial) a.part_lse[prow0 + row] = lse;
+                    else if (a.lse) a.lse[((int64_t)s.b * a.T + ti) * a.heads + hq] = lse * kLn2;
+                }
+                tc_fence_before();
+                sync();
+                if (tid == 0) sh.odd[sg & 7] = 0;
+                continue;
+            }
             float f0 = 1.0f, f1 = 0.0f;
             if (join) {
                 if (st == 1) { given[r] = bias; given[TS + r] = l; tc_fence_before(); }
@@ -929,10 +1082,8 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
                 }
             }
             if (st == 0 || s.two()) {
-                const bool partial = s.n < s.nt;
                 const bool odd = sh.odd[sg & 7] != 0;
-                // the block's first segment uses its first partial slot, its last the second
-                const int64_t prow = ((int64_t)blockIdx.x * 2 + (sg == 0 ? 0 : 1)) * 256 + row;
+                const int64_t prow = prow0 + row;
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;
                 const int64_t orow = ((int64_t)s.b * a.T + ti) * a.heads + hq;
                 if (warp_live) {
@@ -949,27 +1100,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
                         }
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] = used && l != 0.0f ? o[e] * inv : 0.0f;
-                        if (odd && used) {
-                            // drafted values that are not finite were left out of the product
-                            for (int j = 0; j < s.use; ++j) {
-                                const int slot = s.slots + j;
-                                if (slot < s.t0 * TS || slot >= (s.t0 + s.n) * TS || slot >= s.end) continue;
-                                if (!(seen_bits(a, s, ti, slot) & 1)) continue;
-                                const int64_t at = rows.row((uint32_t)slot);
-                                if (at < 0) continue;
-                                for (int e = 0; e < 32 && 32 * w + e < D; ++e) {
-                                    const int64_t x = at * D + 32 * w + e;
-                                    float y;
-                                    if (E4M3) y = (((const uint8_t *)a.c.v)[x] & 0x7f) == 0x7f ? NAN : 0.0f;
-                                    else y = fa_to_f32(((const T *)a.c.v)[x]);
-                                    if (!isfinite(y)) {
-#pragma unroll
-                                        for (int k = 0; k < 32; ++k)
-                                            if (k == e) o[k] += y;
-                                    }
-                                }
-                            }
-                        }
+                        if (odd && used) add_odd<E4M3, T, 32>(a, s, rows, ti, 32 * w, o);
                         if (live) {
                             if (partial) {
                                 float4 *dst = reinterpret_cast<float4 *>(a.part_o + prow * DP + 32 * w);
@@ -1020,11 +1151,11 @@ __global__ void __launch_bounds__(256) k_attend_join(AttendArgs a, int ctas) {
     if (threadIdx.x == 0) {
         const int per = run_length(a);
         int g = work.cum[b / per];
-        for (int i = b / per * per; i < b; ++i) g += tiles_of(a, i);
+        for (int i = b / per * per; i < b; ++i) g += places_of(a, i);
         before = g;
     }
     __syncthreads();
-    const int nt = tiles_of(a, b), total = work.cum[RUNS] * units, g0 = before * units + u * nt, g1 = g0 + nt - 1;
+    const int nt = tiles_of(a, b), total = work.cum[RUNS] * units, g0 = before * units + u * (nt + kUnitCost), g1 = g0 + nt - 1;
     ctas = min(total, ctas);
     // the blocks whose runs hold the unit's first and last tile
     const int c0 = (int)((((int64_t)g0 + 1) * ctas - 1) / total), c1 = (int)((((int64_t)g1 + 1) * ctas - 1) / total);
@@ -1033,18 +1164,17 @@ __global__ void __launch_bounds__(256) k_attend_join(AttendArgs a, int ctas) {
     bool failed = false;
     for (int c = c0; c <= c1; ++c) failed |= a.status[c] != 0;
     if (c0 == c1 && !failed) return;
-    const int slot0 = run_start(total, c0, ctas) == g0 ? 0 : 1;
     for (int row = blockIdx.y * 32 + (threadIdx.x >> 5); row < min(rows, (int)blockIdx.y * 32 + 32); row += 8) {
         float top = -INFINITY, l = 0.0f, o[DP / 32];
 #pragma unroll
         for (int i = 0; i < DP / 32; ++i) o[i] = 0.0f;
         for (int c = c0; c <= c1; ++c) {
-            const float x = a.part_lse[((int64_t)c * 2 + (c == c0 ? slot0 : 0)) * 256 + row];
+            const float x = a.part_lse[((int64_t)c * 2 + (c == c0 ? 1 : 0)) * 256 + row];
             if (!(x <= top)) top = x;          // NaN stays
         }
         if (c0 != c1)
             for (int c = c0; c <= c1; ++c) {
-                const int64_t at = ((int64_t)c * 2 + (c == c0 ? slot0 : 0)) * 256 + row;
+                const int64_t at = ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * 256 + row;
                 const float x = a.part_lse[at];
                 if (x == -INFINITY) continue;
                 const float f = ex2(x - top);
@@ -1139,7 +1269,7 @@ extern "C" fa_status fa_tree_attention(const fa_kv_cache *cache, int32_t dtype, 
     if ((int64_t)T * a.group > 1 << 24) return fa_refuse(fn, "T * group out of range");
     a.rows = T * a.group;
     a.blocks = (a.rows + 255) / 256;
-    if ((int64_t)B * cache->kv_heads * a.blocks * ((slots + TS - 1) / TS + 1) > 2147483647)
+    if ((int64_t)B * cache->kv_heads * a.blocks * ((slots + TS - 1) / TS + 1 + kUnitCost) > 2147483647)
         return fa_refuse(fn, "B * kv_heads * row blocks * tiles of 128 slots out of range");
     a.q = q; a.qb = q_batch_stride; a.qt = q_token_stride; a.qh = q_head_stride;
     a.length = length; a.count = count; a.mask = mask; a.scale = scale; a.out = out; a.lse = lse;
