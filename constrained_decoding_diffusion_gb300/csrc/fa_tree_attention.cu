@@ -38,9 +38,9 @@ namespace {
 
 constexpr int TS = 128;                      // slots of a tile, rows of a stream
 constexpr int NLOAD = 8 * 32, NTHR = 20 * 32;
-// registers a thread of each role, of the 96 the block is launched with: 256 * 144 + 256 * 64 +
-// 128 * 64 = 640 * 96
-constexpr int REGS_SOFTMAX = 144, REGS_LOAD = 64, REGS_MMA = 64;
+// registers a thread of each role, of the 96 the block is launched with: 256 softmax + 256 load +
+// 128 MMA threads use 640 * 96 either way (the smallest that spill nothing)
+template <bool E4M3> struct Regs { static constexpr int SOFTMAX = E4M3 ? 128 : 112, LOAD = E4M3 ? 72 : 88, MMA = 80; };
 constexpr int MAX_CTAS = 152;
 constexpr long long kSpinCycles = 2000000000LL;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -119,29 +119,17 @@ __device__ __forceinline__ void umma_commit(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                  : "memory");
 }
-// the load alone; nothing of v may be used before tmem_wait(v)
-__device__ __forceinline__ void tmem_ld32_start(uint32_t taddr, float (&r)[32]) {
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&r)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+        "tcgen05.wait::ld.sync.aligned;"
         : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
           "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
           "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
           "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
         : "r"(taddr)
         : "memory");
-}
-// waits for the thread's loads; v passes through so that its uses stay behind the wait
-__device__ __forceinline__ void tmem_wait(float (&r)[32]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]), "+f"(r[8]),
-                   "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]), "+f"(r[16]),
-                   "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]), "+f"(r[24]),
-                   "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]), "+f"(r[30]), "+f"(r[31])::"memory");
-}
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
-    tmem_ld32_start(taddr, v);
-    tmem_wait(v);
 }
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
     asm volatile(
@@ -171,28 +159,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
         : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// two fp32 operations at a time
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpair(uint64_t r, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -517,7 +483,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
     Segment s;
 
     if (warp >= 16) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_MMA));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<E4M3>::MMA));
         if (warp == 16 && lane == 0) {
             // ---- the MMAs
             constexpr uint32_t fmt = F16 ? 0u : 1u;
@@ -662,7 +628,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
         }
     } else if (warp >= 8) {
         // ---- loading
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_LOAD));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<E4M3>::LOAD));
         const int lt = tid - 256;
         const uint32_t ring = smem_u32(smem + S::RING);
         int it = 0;
@@ -754,7 +720,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
         }
     } else {
         // ---- softmax: stream st, row r of its tile
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<E4M3>::SOFTMAX));
         const int st = warp >> 2, r = tid & 127;
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t ts = tmem + lane_base + st * TS, to = tmem + lane_base + 256 + st * DP;
@@ -814,20 +780,25 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
             warp_arrive(&sh.q_full[st]);
             float m = -INFINITY, l = 0.0f, bias = 0.0f;
             int ev = -120;
-            // slot r of each tile: whether it is held and its scales, one tile ahead
+            // slot r of each tile: whether it is held and its scales are fetched one tile ahead, the
+            // number of its page two tiles ahead
             float ks = 0.0f, vs = 0.0f;
             bool there = false;
             const Rows rows(a, s);
-            auto fetch = [&](int tile) {
+            auto page_of = [&](int tile) {
                 const uint32_t slot = (uint32_t)(s.t0 + tile) * TS + r;
-                const int64_t at = slot < (uint32_t)s.end ? rows.row(slot) : -1;
+                return tile < s.n && slot < (uint32_t)s.end ? rows.page(slot) : 0xffffffffu;
+            };
+            auto fetch = [&](int tile, uint32_t page) {
+                const int64_t at = rows.row(page, (uint32_t)(s.t0 + tile) * TS + r);
                 there = at >= 0;
                 if (E4M3) {
                     ks = there ? __ldg(a.c.k_scale + at) : 0.0f;
                     vs = there ? __ldg(a.c.v_scale + at) : 0.0f;
                 }
             };
-            fetch(begin);
+            uint32_t next_page = page_of(begin + step);
+            fetch(begin, page_of(begin));
             for (int q = 0; q < mine; ++q) {
                 const int tile = begin + q * step;
                 const int first = (s.t0 + tile) * TS;
@@ -846,7 +817,10 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
                     sc.k[st][r] = ks;
                     sc.v[st][r] = vs;
                 }
-                if (q + 1 < mine) fetch(tile + step);
+                if (q + 1 < mine) {
+                    fetch(tile + step, next_page);
+                    next_page = page_of(tile + 2 * step);
+                }
                 bar_sync(1 + st, TS);
                 bool whole = first + TS <= s.slots;
 #pragma unroll
@@ -854,49 +828,41 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
                 mbar_wait(&sh.s_full[st], (uint32_t)ns++ & 1, fail);
                 __syncwarp();
                 tc_fence_after();
-                if (warp_live) {
-                    // the largest score (before the scale), and the largest value scale, that the row sees
-                    float mx = -INFINITY, vmx = 0.0f;
-                    uint32_t see[4] = {0, 0, 0, 0};
-                    float buf[2][32];
+                // The tile's scores to weights.  WHOLE: every row sees every slot; the code of the
+                // other tiles is kept apart so that the common one stays short.
+                auto weigh = [&](auto whole_tag) {
+                    constexpr bool WHOLE = decltype(whole_tag)::value;
+                    float x[32];
+                    // which of chunk w's slots the row sees
+                    auto seen = [&](int w) {
+                        return WHOLE ? 0xffffffffu : used ? sh.held[st][w] & seen_bits(a, s, ti, first + 32 * w) : 0u;
+                    };
                     // chunk w of 32 scores, times the keys' scales, hidden ones to -inf
-                    auto finish_chunk = [&](int w, float (&x)[32], uint32_t z) {
+                    auto load_chunk = [&](int w, uint32_t z) {
+                        if (!WHOLE) __syncwarp();
+                        tmem_ld32(ts + 32 * w, x);
                         if (E4M3)
 #pragma unroll
                             for (int e = 0; e < 32; e += 4) {
                                 const float4 f = *reinterpret_cast<const float4 *>(&sc.k[st][32 * w + e]);
-                                unpair(mul2(pair(x[e], x[e + 1]), pair(f.x, f.y)), x[e], x[e + 1]);
-                                unpair(mul2(pair(x[e + 2], x[e + 3]), pair(f.z, f.w)), x[e + 2], x[e + 3]);
+                                x[e] *= f.x; x[e + 1] *= f.y; x[e + 2] *= f.z; x[e + 3] *= f.w;
                             }
-                        if (z != 0xffffffffu)
+                        if (!WHOLE)
 #pragma unroll
                             for (int e = 0; e < 32; ++e) x[e] = (z >> e & 1) ? x[e] : -INFINITY;
                     };
-                    auto seen = [&](int w) {
-                        uint32_t z = see[0];
-#pragma unroll
-                        for (int j = 1; j < 4; ++j) z = j == w ? see[j] : z;
-                        return z;
-                    };
+                    // the largest score (before the scale), and the largest value scale, that the row sees
+                    float mx = -INFINITY, vmx = 0.0f;
 #pragma unroll 1
                     for (int w = w_begin; w < w_end; ++w) {
-                        float (&x)[32] = buf[0];
-                        tmem_ld32_start(ts + 32 * w, x);
-                        uint32_t z = 0xffffffffu;
-                        if (!whole) z = used ? sh.held[st][w] & seen_bits(a, s, ti, first + 32 * w) : 0u;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) see[j] = j == w ? z : see[j];
+                        const uint32_t z = seen(w);
                         if (E4M3) {
-                            if (whole) {
-                                vmx = fmaxf(vmx, sh.vtop[st][w]);
-                            } else {
+                            if (WHOLE) vmx = fmaxf(vmx, sh.vtop[st][w]);
+                            else
 #pragma unroll
                                 for (int e = 0; e < 32; ++e) vmx = (z >> e & 1) ? fmaxf(vmx, sc.v[st][32 * w + e]) : vmx;
-                            }
                         }
-                        __syncwarp();
-                        tmem_wait(x);
-                        finish_chunk(w, x, z);
+                        load_chunk(w, z);
                         float top[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                         for (int e = 0; e < 32; e += 8)
@@ -904,14 +870,14 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
                             for (int j = 0; j < 4; ++j) top[j] = fmaxf(fmaxf(top[j], x[e + 2 * j]), x[e + 2 * j + 1]);
                         mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                     }
-                    const int e2 = E4M3 ? max(ev, min(max(fa_exponent(vmx) + 1, -120), 120)) : 0;
-                    const bool move = mx > -INFINITY && ((mx - m) * c > kGrow || e2 > ev || m == -INFINITY);
+                    const int e2 = E4M3 ? max(ev, min(max(fa_exponent(vmx) + 1, -120), 120)) : ev;
+                    const bool move = live && mx > -INFINITY && ((mx - m) * c > kGrow || e2 > ev || m == -INFINITY);
                     if (__any_sync(0xffffffffu, move)) {
                         float f = 1.0f;
                         if (move) {
                             const bool had = m > -INFINITY;
                             m = fmaxf(m, mx);
-                            if (E4M3) ev = e2;
+                            ev = e2;
                             const float b2 = m * c + (E4M3 ? (float)ev : 0.0f) - OFF;
                             f = had ? ex2(bias - b2) : 0.0f;
                             bias = b2;
@@ -932,45 +898,27 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
                             }
                         }
                     }
-                    const uint64_t cc = pair(c, c), nb = pair(-bias, -bias);
-                    uint64_t sum0 = 0, sum1 = 0;
-                    // chunk w of the scores (in x) to weights, with the next chunk on its way to nx
-                    auto weigh = [&](int w, float (&x)[32], float (&nx)[32], bool loaded) {
+                    float sum[4] = {0, 0, 0, 0};
+#pragma unroll 1
+                    for (int w = w_begin; w < w_end; ++w) {
                         uint32_t p[16];
-                        if (!loaded) {
-                            tmem_wait(x);
-                            if (w + 1 < w_end) tmem_ld32_start(ts + 32 * w + 32, nx);
-                            finish_chunk(w, x, seen(w));
-                        }
+                        if (copies < 4) load_chunk(w, seen(w));   // else the one chunk is still there
 #pragma unroll
                         for (int e = 0; e < 32; e += 4) {
                             float y[4];
-                            unpair(fma2(pair(x[e], x[e + 1]), cc, nb), y[0], y[1]);
-                            unpair(fma2(pair(x[e + 2], x[e + 3]), cc, nb), y[2], y[3]);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) y[j] = ex2(y[j]);
-                            const uint64_t a0 = pair(y[0], y[1]), a1 = pair(y[2], y[3]);
-                            sum0 = add2(sum0, a0);
-                            sum1 = add2(sum1, a1);
+                            for (int j = 0; j < 4; ++j) {
+                                y[j] = ex2(fmaf(x[e + j], c, -bias));
+                                sum[j] += y[j];
+                            }
                             if (E4M3) {
                                 const float4 g = *reinterpret_cast<const float4 *>(&sc.v[st][32 * w + e]);
-                                unpair(mul2(a0, pair(g.x, g.y)), y[0], y[1]);
-                                unpair(mul2(a1, pair(g.z, g.w)), y[2], y[3]);
+                                y[0] *= g.x; y[1] *= g.y; y[2] *= g.z; y[3] *= g.w;
                             }
                             p[e / 2] = fa_pack2(y[0], y[1], M());
                             p[e / 2 + 1] = fa_pack2(y[2], y[3], M());
                         }
                         tmem_st16(ts + 16 * w, p);
-                    };
-                    if (copies == 4) {
-                        weigh(w_begin, buf[0], buf[1], true);       // the one chunk is still in registers
-                    } else {
-                        tmem_ld32_start(ts + 32 * w_begin, buf[0]);
-#pragma unroll 1
-                        for (int w = w_begin; w < w_end; w += 2) {
-                            weigh(w, buf[0], buf[1], false);
-                            weigh(w + 1, buf[1], buf[0], false);
-                        }
                     }
                     if (copies > 1) {
                         const uint32_t none[16] = {};
@@ -978,11 +926,12 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
                         for (int w = 0; w < 4; ++w)
                             if (w < w_begin || w >= w_end) tmem_st16(ts + 16 * w, none);
                     }
-                    float t0, t1, t2, t3;
-                    unpair(sum0, t0, t1);
-                    unpair(sum1, t2, t3);
-                    l += (t0 + t1) + (t2 + t3);
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                     tmem_st_wait();
+                };
+                if (warp_live) {
+                    if (whole) weigh(std::true_type());
+                    else weigh(std::false_type());
                 }
                 tc_fence_before();
                 warp_arrive(&sh.p_full[st]);
