@@ -40,7 +40,7 @@ constexpr int TS = 128;                      // slots of a tile, rows of a strea
 constexpr int NLOAD = 8 * 32, NTHR = 20 * 32;
 // registers a thread of each role, of the 96 the block is launched with: 256 softmax + 256 load +
 // 128 MMA threads use 640 * 96 either way (the smallest that spill nothing)
-template <bool E4M3> struct Regs { static constexpr int SOFTMAX = E4M3 ? 128 : 112, LOAD = E4M3 ? 72 : 88, MMA = 80; };
+template <bool E4M3> struct Regs { static constexpr int SOFTMAX = E4M3 ? 128 : 112, LOAD = E4M3 ? 72 : 80, MMA = E4M3 ? 80 : 96; };
 constexpr int MAX_CTAS = 152;
 constexpr long long kSpinCycles = 2000000000LL;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -312,8 +312,8 @@ struct Misc {
     uint32_t tmem;
     int fail;
     int odd[8];                       // segment & 7: a drafted value is not finite
-    uint32_t held[2][4];              // per stream: which slots of its tile have a page,
-    float vtop[2][4];                 // and the largest value scale of 32 of them
+    int hole[16];                     // key tile & 15: a slot of the tile has no page or lies past the end
+    float vtop[2][4];                 // per stream: the largest value scale of 32 slots
 };
 struct Scales { float k[2][TS], v[2][TS]; };   // per stream, of its tile
 
@@ -340,6 +340,15 @@ template <class M> __device__ __forceinline__ bool zero_odd(uint4 &x) {
     x = make_uint4(w[0], w[1], w[2], w[3]);
     return odd;
 }
+
+// A position in a ring of N barriers: the slot and how often the ring has been round.
+template <int N> struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void operator++() {
+        if (++slot == N) { slot = 0; phase ^= 1; }
+    }
+};
 
 // Where a sequence's slots lie for one head.  The slot is below Segment::end, so its page number is
 // in the table.
@@ -381,18 +390,30 @@ struct Feed {
 };
 
 // A loading thread's share of a tile: one 16-byte chunk of every STEP-th row.  The page numbers of
-// the next tile are fetched while the current one is issued.
+// the next tile are fetched while the current one is issued.  A page's rows of one head are
+// contiguous, and the place of a tile's row in its page depends on the tile only when a page is
+// longer than a tile.
 template <int STEP>
 struct Share {
     static constexpr int ITER = TS / STEP;
     uint32_t page[ITER];
-    Rows rows;
-    __device__ __forceinline__ void look(const AttendArgs &a, const Feed &f, uint32_t r0, bool column) {
-        rows = Rows(a, f.s);
+    uint32_t n_pages, in_page, page_bytes, row_bytes, r0;
+    __device__ __forceinline__ Share(const AttendArgs &a, int r0_, int row_bytes_)
+        : n_pages(a.c.n_pages), in_page((1u << a.c.page_shift) - 1), row_bytes(row_bytes_), r0(r0_) {
+        page_bytes = (uint32_t)row_bytes << a.c.page_shift;
+    }
+    __device__ __forceinline__ void look(const AttendArgs &a, const Feed &f) {
+        const int32_t *pages = a.c.page_table + (int64_t)f.s.b * a.c.max_pages;
         const uint32_t first = f.first() + r0, end = (uint32_t)f.s.end;
 #pragma unroll
-        for (int q = 0; q < ITER; ++q) page[q] = column && first + q * STEP < end ? rows.page(first + q * STEP) : 0xffffffffu;
+        for (int q = 0; q < ITER; ++q)
+            page[q] = first + q * STEP < end ? (uint32_t)__ldg(pages + ((first + q * STEP) >> a.c.page_shift)) : 0xffffffffu;
     }
+    // the bytes of the q-th row, from the head's bytes in page 0
+    __device__ __forceinline__ const unsigned char *at(const unsigned char *base, uint64_t stride, uint32_t first, int q) const {
+        return base + (page[q] < n_pages ? page[q] : 0) * stride + ((first + q * STEP) & in_page) * row_bytes;
+    }
+    __device__ __forceinline__ bool held(int q) const { return page[q] < n_pages; }
 };
 
 // which of the 32 slots from `first` on drafted token i// which of the 32 slots from `first` on drafted token i of sequence b sees
@@ -469,6 +490,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
         mbar_init(&sh.done, 1);
         sh.fail = 0;
         for (int i = 0; i < 8; ++i) sh.odd[i] = 0;
+        for (int i = 0; i < 16; ++i) sh.hole[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 16) {
@@ -490,12 +512,13 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
             constexpr uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(TS >> 4) << 24);
             constexpr uint32_t idesc_s = idesc | ((uint32_t)(TS >> 3) << 17);                 // S: N = 128 slots
             constexpr uint32_t idesc_o = idesc | ((uint32_t)(DP >> 3) << 17) | (1u << 16);    // O: N = DP, V is MN-major
-            int it = 0, nq[2] = {0, 0}, np[2] = {0, 0};
+            Ring<S::NS> get;
+            int nq[2] = {0, 0}, np[2] = {0, 0};
             const uint32_t q0 = smem_u32(smem + S::Q), ring = smem_u32(smem + S::RING);
             auto next_tile = [&]() -> int {
-                const int slot = it % S::NS;
-                if (!mbar_wait(&sh.full[slot], (uint32_t)(it / S::NS) & 1, fail)) return -1;
-                ++it;
+                const int slot = get.slot;
+                if (!mbar_wait(&sh.full[slot], get.phase, fail)) return -1;
+                ++get;
                 return slot;
             };
             auto scores = [&](int st, int slot) {
@@ -570,7 +593,11 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
                 }
                 if (!ok) break;
             }
-            umma_commit(&sh.done);   // completes once every MMA issued above has
+            // every MMA issued has completed before tensor memory is released
+            umma_commit(&sh.done);
+            const long long t0 = clock64();
+            while (!mbar_try_wait(&sh.done, 0))
+                if (clock64() - t0 > kSpinCycles) { *fail = 1; break; }
         }
         if constexpr (E4M3) {
         if (warp == 17) {
@@ -589,10 +616,11 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
             const uint32_t in_page = (1u << a.c.page_shift) - 1;
             bool more = f.next(a);
             if (more) look();
-            int it = 0;
+            int it = 0, keys = 0;
+            Ring<S::NR> put;
             for (; more; ++it) {
-                const int slot = it % S::NR;
-                if (it >= S::NR && !mbar_wait(&sh.raw_empty[slot], (uint32_t)(it / S::NR - 1) & 1, fail)) break;
+                const int slot = put.slot;
+                if (it >= S::NR && !mbar_wait(&sh.raw_empty[slot], put.phase ^ 1, fail)) break;
                 __syncwarp();
                 uint32_t there[4], n = 0;
 #pragma unroll
@@ -603,9 +631,11 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
                 if (lane == 0) {
 #pragma unroll
                     for (int w = 0; w < 4; ++w) sh.raw_rows[slot][w] = there[w];
+                    if (!f.value) sh.hole[keys & 15] = n < TS;
                     mbar_expect(&sh.raw_full[slot], n * D);
                 }
                 __syncwarp();
+                keys += !f.value;
                 const uint8_t *src = (const uint8_t *)(f.value ? a.c.v : a.c.k);
                 const uint32_t dst = smem_u32(smem + S::RAWS) + slot * S::RAW;
 #pragma unroll
@@ -616,6 +646,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
                         bulk_copy(dst + r * D, src + rows.row(page[w], at) * D, len * D, &sh.raw_full[slot]);
                     }
                 }
+                ++put;
                 more = f.next(a);
                 if (more) look();
             }
@@ -631,9 +662,12 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<E4M3>::LOAD));
         const int lt = tid - 256;
         const uint32_t ring = smem_u32(smem + S::RING);
-        int it = 0;
-        auto wait_empty = [&](int i) {
-            return i < S::NS || mbar_wait(&sh.empty[i % S::NS], (uint32_t)(i / S::NS - 1) & 1, fail);
+        Ring<S::NS> put;                         // the tile to fill: free at first, then when it has been used
+        bool again = false;
+        auto wait_empty = [&]() { return !again || mbar_wait(&sh.empty[put.slot], put.phase ^ 1, fail); };
+        auto advance = [&]() {
+            ++put;
+            again |= put.slot == 0;
         };
         Feed f(walk);
         if constexpr (!E4M3) {
@@ -641,81 +675,93 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
             const int c = lt % CPR, r0 = lt / CPR;
             const uint32_t to = chunk_at(r0, c);
             const bool column = c * 8 < D;
-            Share<STEP> x;
+            Share<STEP> x(a, r0, D * 2);
+            const uint64_t stride = (uint64_t)x.page_bytes * a.c.kv_heads;
             bool more = f.next(a);
-            if (more) x.look(a, f, r0, column);
+            if (more) x.look(a, f);
+            Ring<S::NS> told;                    // the tile to hand on
+            int it = 0, keys = 0;
             for (; more; ++it) {
                 const uint32_t first = f.first() + r0;
-                const T *src = (const T *)(f.value ? a.c.v : a.c.k) + c * 8;
-                if (!wait_empty(it)) break;
+                const unsigned char *src = (const unsigned char *)(f.value ? a.c.v : a.c.k) + (uint64_t)f.s.head * x.page_bytes + c * 16;
+                if (!wait_empty()) break;
+                if (!f.value) {
+                    bool hole = false;
+#pragma unroll
+                    for (int q = 0; q < x.ITER; ++q) hole |= !x.held(q);
+                    if (hole) sh.hole[keys & 15] = 1;
+                    if (lt == 0) sh.hole[(keys + 8) & 15] = 0;   // at most NS tiles are under way
+                    ++keys;
+                }
                 if (!f.draft()) {
-                    const uint32_t dst = ring + (it % S::NS) * S::TILE + to;
+                    const uint32_t dst = ring + put.slot * S::TILE + to;
 #pragma unroll
-                    for (int q = 0; q < x.ITER; ++q) {
-                        const int64_t row = x.rows.row(x.page[q], first + q * STEP);
-                        cp_async16(dst + q * STEP * 128, src + (row < 0 ? 0 : row * D), row >= 0);
-                    }
+                    for (int q = 0; q < x.ITER; ++q)
+                        cp_async16(dst + q * STEP * 128, x.at(src, stride, first, q), x.held(q) && column);
                 } else {
-                    unsigned char *dst = smem + S::RING + (it % S::NS) * S::TILE + to;
+                    unsigned char *dst = smem + S::RING + put.slot * S::TILE + to;
 #pragma unroll
                     for (int q = 0; q < x.ITER; ++q) {
-                        const int64_t row = x.rows.row(x.page[q], first + q * STEP);
                         uint4 v = make_uint4(0, 0, 0, 0);
-                        if (row >= 0) v = __ldg(reinterpret_cast<const uint4 *>(src + row * D));
+                        if (x.held(q) && column) v = __ldg(reinterpret_cast<const uint4 *>(x.at(src, stride, first, q)));
                         if (first + q * STEP >= (uint32_t)f.s.slots && zero_odd<M>(v)) sh.odd[f.seg & 7] = 1;
                         *reinterpret_cast<uint4 *>(dst + q * STEP * 128) = v;
                     }
                 }
                 cp_commit();
+                advance();
                 more = f.next(a);
-                if (more) x.look(a, f, r0, column);
+                if (more) x.look(a, f);
                 if (it >= LAG<DP>) {
                     cp_wait<LAG<DP>>();
                     proxy_fence();
-                    warp_arrive(&sh.full[(it - LAG<DP>) % S::NS]);
+                    warp_arrive(&sh.full[told.slot]);
+                    ++told;
                 }
             }
             cp_wait<0>();
             proxy_fence();
             if (!more)
-                for (int i = max(it - LAG<DP>, 0); i < it; ++i) warp_arrive(&sh.full[i % S::NS]);
+                for (int i = min(it, LAG<DP>); i > 0; --i) { warp_arrive(&sh.full[told.slot]); ++told; }
         } else {
             // a thread converts one 16-byte chunk of every STEP-th row
             constexpr int RPR = DP / 16, STEP = NLOAD / RPR, ITER = TS / STEP;
             const int c = lt % RPR, r0 = lt / RPR;
             const uint32_t to0 = chunk_at(r0, 2 * c), to1 = chunk_at(r0, 2 * c + 1);
             const bool column = c * 16 < D;
-            for (; f.next(a); ++it) {
-                const int from = it % S::NR;
-                if (!mbar_wait(&sh.raw_full[from], (uint32_t)(it / S::NR) & 1, fail)) break;
-                const unsigned char *raw = smem + S::RAWS + from * S::RAW + (r0 * D + c * 16);
+            Ring<S::NR> from;
+            while (f.next(a)) {
+                if (!mbar_wait(&sh.raw_full[from.slot], from.phase, fail)) break;
+                const unsigned char *raw = smem + S::RAWS + from.slot * S::RAW + (r0 * D + c * 16);
                 uint4 w[ITER];
 #pragma unroll
                 for (int q = 0; q < ITER; ++q) {
                     const int r = r0 + q * STEP;
-                    const bool there = column && (sh.raw_rows[from][r >> 5] >> (r & 31) & 1);
+                    const bool there = column && (sh.raw_rows[from.slot][r >> 5] >> (r & 31) & 1);
                     w[q] = there ? *reinterpret_cast<const uint4 *>(raw + q * STEP * D) : make_uint4(0, 0, 0, 0);
                 }
-                if (!wait_empty(it)) break;
-                const uint32_t first = f.first() + r0;
-                const bool draft = f.draft();
-                unsigned char *dst = smem + S::RING + (it % S::NS) * S::TILE;
+                if (!wait_empty()) break;
+                unsigned char *dst = smem + S::RING + put.slot * S::TILE;
+                // drafted values that are not finite are left out
+                const uint32_t odd_from = f.draft() ? (uint32_t)f.s.slots - f.first() : 0xffffffffu;
 #pragma unroll
                 for (int q = 0; q < ITER; ++q) {
                     uint4 lo = make_uint4(fa_e4m3x2_to_half2(w[q].x), fa_e4m3x2_to_half2(w[q].x >> 16),
                                           fa_e4m3x2_to_half2(w[q].y), fa_e4m3x2_to_half2(w[q].y >> 16));
                     uint4 hi = make_uint4(fa_e4m3x2_to_half2(w[q].z), fa_e4m3x2_to_half2(w[q].z >> 16),
                                           fa_e4m3x2_to_half2(w[q].w), fa_e4m3x2_to_half2(w[q].w >> 16));
-                    if (draft && first + q * STEP >= (uint32_t)f.s.slots) {
+                    if (odd_from != 0xffffffffu && r0 + q * STEP >= (int)odd_from) {
                         const bool o1 = zero_odd<M>(lo), o2 = zero_odd<M>(hi);
                         if (o1 || o2) sh.odd[f.seg & 7] = 1;
                     }
                     *reinterpret_cast<uint4 *>(dst + to0 + q * STEP * 128) = lo;
                     *reinterpret_cast<uint4 *>(dst + to1 + q * STEP * 128) = hi;
                 }
-                warp_arrive(&sh.raw_empty[from]);
+                warp_arrive(&sh.raw_empty[from.slot]);
                 proxy_fence();
-                warp_arrive(&sh.full[it % S::NS]);
+                warp_arrive(&sh.full[put.slot]);
+                ++from;
+                advance();
             }
         }
     } else {
@@ -724,11 +770,13 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
         const int st = warp >> 2, r = tid & 127;
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t ts = tmem + lane_base + st * TS, to = tmem + lane_base + 256 + st * DP;
-        int ns = 0, npv = 0, seg = 0;
+        int ns = 0, npv = 0, seg = 0, keys = 0;   // keys: key tiles of both streams before the segment's
         float *given = reinterpret_cast<float *>(smem + S::Q + S::TILE);   // stream 1's statistics, where its Q was
         while (walk.next(a, s)) {
             const int step = s.two() ? 1 : 2, begin = s.two() ? 0 : st, mine = s.two() ? s.n : (s.n + 1 - st) / 2;
             const int sg = seg++;
+            const int keys_before = keys;
+            keys += s.n;
             if (mine <= 0) continue;                       // a single tile: stream 1 has none
             // Up to 64 (32) rows lie two (four) times in the 128 lanes: copy `copy` weighs its part of
             // a tile's columns and gives the others no weight, and the copies are joined at the end.
@@ -780,10 +828,8 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
             warp_arrive(&sh.q_full[st]);
             float m = -INFINITY, l = 0.0f, bias = 0.0f;
             int ev = -120;
-            // slot r of each tile: whether it is held and its scales are fetched one tile ahead, the
-            // number of its page two tiles ahead
+            // the scales of slot r of each tile are fetched one tile ahead, its page's number two
             float ks = 0.0f, vs = 0.0f;
-            bool there = false;
             const Rows rows(a, s);
             auto page_of = [&](int tile) {
                 const uint32_t slot = (uint32_t)(s.t0 + tile) * TS + r;
@@ -791,43 +837,41 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
             };
             auto fetch = [&](int tile, uint32_t page) {
                 const int64_t at = rows.row(page, (uint32_t)(s.t0 + tile) * TS + r);
-                there = at >= 0;
-                if (E4M3) {
-                    ks = there ? __ldg(a.c.k_scale + at) : 0.0f;
-                    vs = there ? __ldg(a.c.v_scale + at) : 0.0f;
-                }
+                ks = at >= 0 ? __ldg(a.c.k_scale + at) : 0.0f;
+                vs = at >= 0 ? __ldg(a.c.v_scale + at) : 0.0f;
             };
-            uint32_t next_page = page_of(begin + step);
-            fetch(begin, page_of(begin));
+            uint32_t next_page = 0;
+            if (E4M3) {
+                next_page = page_of(begin + step);
+                fetch(begin, page_of(begin));
+            }
+            // with four copies a warp weighs the very slots whose scales it fetches
+            auto scales_sync = [&]() {
+                if (copies == 4) __syncwarp();
+                else bar_sync(1 + st, TS);
+            };
             for (int q = 0; q < mine; ++q) {
                 const int tile = begin + q * step;
                 const int first = (s.t0 + tile) * TS;
-                const uint32_t got = __ballot_sync(0xffffffffu, there);
-                float vt = vs;
-                if (E4M3)
+                if (E4M3) {
+                    float vt = vs;
 #pragma unroll
                     for (int o = 16; o; o >>= 1) vt = fmaxf(vt, __shfl_xor_sync(0xffffffffu, vt, o));
-                if (q > 0) bar_sync(1 + st, TS);          // the previous tile's have been read
-                if (lane == 0) {
-                    sh.held[st][warp & 3] = got;
-                    if (E4M3) sh.vtop[st][warp & 3] = vt;
-                }
-                if (E4M3) {
+                    if (q > 0) scales_sync();             // the previous tile's have been read
+                    if (lane == 0) sh.vtop[st][warp & 3] = vt;
                     if (first + r >= s.slots && !(fabsf(vs) < INFINITY)) { vs = 0.0f; sh.odd[sg & 7] = 1; }
                     sc.k[st][r] = ks;
                     sc.v[st][r] = vs;
+                    if (q + 1 < mine) {
+                        fetch(tile + step, next_page);
+                        next_page = page_of(tile + 2 * step);
+                    }
+                    scales_sync();
                 }
-                if (q + 1 < mine) {
-                    fetch(tile + step, next_page);
-                    next_page = page_of(tile + 2 * step);
-                }
-                bar_sync(1 + st, TS);
-                bool whole = first + TS <= s.slots;
-#pragma unroll
-                for (int w = 0; w < 4; ++w) whole &= sh.held[st][w] == 0xffffffffu;
                 mbar_wait(&sh.s_full[st], (uint32_t)ns++ & 1, fail);
                 __syncwarp();
                 tc_fence_after();
+                const bool whole = first + TS <= s.slots && !sh.hole[(keys_before + tile) & 15];
                 // The tile's scores to weights.  WHOLE: every row sees every slot; the code of the
                 // other tiles is kept apart so that the common one stays short.
                 auto weigh = [&](auto whole_tag) {
@@ -835,7 +879,10 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
                     float x[32];
                     // which of chunk w's slots the row sees
                     auto seen = [&](int w) {
-                        return WHOLE ? 0xffffffffu : used ? sh.held[st][w] & seen_bits(a, s, ti, first + 32 * w) : 0u;
+                        if (WHOLE) return 0xffffffffu;
+                        const uint32_t slot = first + 32 * w + lane;
+                        const uint32_t held = __ballot_sync(0xffffffffu, slot < (uint32_t)s.end && rows.page(slot) < rows.n_pages);
+                        return used ? held & seen_bits(a, s, ti, first + 32 * w) : 0u;
                     };
                     // chunk w of 32 scores, times the keys' scales, hidden ones to -inf
                     auto load_chunk = [&](int w, uint32_t z) {
@@ -1080,10 +1127,9 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
         }
     }
     __syncwarp();
-    // the MMAs issued have completed before tensor memory is released
-    mbar_wait(&sh.done, 0, fail);
-    tc_fence_after();
+    tc_fence_before();
     __syncthreads();
+    tc_fence_after();
     if (tid == 0) a.status[blockIdx.x] = sh.fail;
     if (warp == 16) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
