@@ -32,6 +32,8 @@
 //
 // Every wait is bounded (about a second).  A wait that runs out marks the block's status; the
 // joining kernel then sets the rows the block had a part in to NaN.
+#include <cuda.h>
+
 #include "fa_lm.cuh"
 
 namespace {
@@ -81,6 +83,13 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
                  "r"(bytes), "r"(smem_u32(bar))
                  : "memory");
+}
+// a box of a two-dimensional tensor map, x = element, y = row; outside the tensor zeros arrive
+__device__ __forceinline__ void tensor_copy(uint32_t dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+        : "memory");
 }
 // one arrival for the warp, after what its lanes did before
 __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
@@ -177,6 +186,7 @@ struct AttendArgs {
     float *lse;
     float *part_o, *part_lse;                      // [MAX_CTAS, 2, 256, DP], [MAX_CTAS, 2, 256]
     int *status;                                   // [MAX_CTAS]
+    int box_rows;                                  // rows of a tensor-map box, 0 = no tensor maps
 };
 
 // ----------------------------------------------------------------------------- the work list
@@ -295,8 +305,6 @@ __device__ __forceinline__ void item_of(const Segment &s, int i, int &tile, bool
 
 // ----------------------------------------------------------------------------- the kernel
 
-template <int DP> constexpr int LAG = DP == 64 ? 6 : 3;            // 16-bit tiles in flight before one is handed on
-
 template <int DP, bool E4M3>
 struct Shape {
     static constexpr int TILE = TS * DP * 2;                       // a 16-bit tile in shared memory
@@ -308,6 +316,7 @@ struct Shape {
 struct Misc {
     uint64_t full[10], empty[10], s_full[2], p_full[2], pv_done[2], q_full[2], done;
     uint64_t raw_full[8], raw_empty[8];
+    uint64_t by_hand[16];             // tile by hand & 15: its place in the ring is free
     uint32_t raw_rows[8][4];          // which rows of a raw tile were copied
     uint32_t tmem;
     int fail;
@@ -387,6 +396,11 @@ struct Feed {
     __device__ __forceinline__ uint32_t first() const { return (uint32_t)(s.t0 + tile) * TS; }
     // drafted values may be hidden from some rows
     __device__ __forceinline__ bool draft() const { return value && (s.t0 + tile + 1) * TS > s.slots; }
+    // a 16-bit tile that the loading warps bring themselves: a page may end in it, or its values need
+    // a look; all others come by tensor copies
+    __device__ __forceinline__ bool by_hand(const AttendArgs &a) const {
+        return !a.box_rows || (s.t0 + tile + 1) * TS > s.end || draft();
+    }
 };
 
 // A loading thread's share of a tile: one 16-byte chunk of every STEP-th row.  The page numbers of
@@ -459,7 +473,8 @@ __device__ __forceinline__ void add_odd(const AttendArgs &a, const Segment &s, c
 
 // M: the tensor cores' 16-bit type; T: q's and out's
 template <int DP, bool E4M3, class T, class M>
-__global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
+__global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a, const __grid_constant__ CUtensorMap map_k,
+                                                    const __grid_constant__ CUtensorMap map_v) {
     using S = Shape<DP, E4M3>;
     extern __shared__ __align__(1024) unsigned char smem[];
     constexpr size_t MISC = S::MISC + (E4M3 ? sizeof(Scales) : 0);
@@ -477,7 +492,6 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
         return;
     }
 
-    plan(a, work);
     if (tid == 0) {
         for (int i = 0; i < S::NS; ++i) { mbar_init(&sh.full[i], NLOAD / 32); mbar_init(&sh.empty[i], 1); }
         for (int i = 0; i < S::NR; ++i) { mbar_init(&sh.raw_full[i], 1); mbar_init(&sh.raw_empty[i], NLOAD / 32); }
@@ -487,6 +501,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
             mbar_init(&sh.pv_done[i], 1);
             mbar_init(&sh.q_full[i], 4);
         }
+        for (int i = 0; i < 16; ++i) mbar_init(&sh.by_hand[i], 1);
         mbar_init(&sh.done, 1);
         sh.fail = 0;
         for (int i = 0; i < 8; ++i) sh.odd[i] = 0;
@@ -496,9 +511,9 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
     if (warp == 16) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        tc_fence_before();
     }
-    tc_fence_before();
-    __syncthreads();
+    plan(a, work);
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
     Walk walk(a, work, blockIdx.x, gridDim.x);
@@ -656,6 +671,62 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
                 while (!mbar_try_wait(&sh.raw_full[i % S::NR], (uint32_t)(i / S::NR) & 1) && clock64() - t0 < kSpinCycles) {}
             }
         }
+        } else if (warp == 17 && a.box_rows) {
+            // ---- 16-bit tiles by tensor copies: a lane per box of (a page's rows) x 64 columns
+            Feed f(walk);
+            const int boxes = TS / a.box_rows, mine = lane % boxes, half = lane / boxes;
+            const bool copies_box = half < DP / 64;
+            const uint32_t in_page = (1u << a.c.page_shift) - 1;
+            uint32_t page = 0;
+            auto look = [&]() {
+                if (!f.by_hand(a) && copies_box)
+                    page = (uint32_t)__ldg(a.c.page_table + (int64_t)f.s.b * a.c.max_pages +
+                                           ((f.first() + mine * a.box_rows) >> a.c.page_shift));
+            };
+            bool more = f.next(a), again = false;
+            if (more) look();
+            int keys = 0, hand = 0;
+            Ring<S::NS> put;
+            uint32_t copied = 0, copied_phase = 0;   // bit i: slot i's last tile came by copies, and its phase
+            for (; more;) {
+                if (again && !mbar_wait(&sh.empty[put.slot], put.phase ^ 1, fail)) break;
+                __syncwarp();
+                if (!f.by_hand(a)) {
+                    const bool held = !copies_box || page < (uint32_t)a.c.n_pages;
+                    const bool hole = __any_sync(0xffffffffu, !held);
+                    if (lane == 0) {
+                        if (!f.value) sh.hole[keys & 15] = hole;
+                        mbar_expect(&sh.full[put.slot], S::TILE);
+                    }
+                    __syncwarp();
+                    if (lane > 0 && lane < NLOAD / 32) mbar_arrive(&sh.full[put.slot]);
+                    if (copies_box) {
+                        const uint32_t first = f.first() + mine * a.box_rows;
+                        const int y = held ? (int)(((page * a.c.kv_heads + f.s.head) << a.c.page_shift) + (first & in_page))
+                                           : a.c.n_pages * a.c.kv_heads << a.c.page_shift;   // past the end: zeros
+                        tensor_copy(smem_u32(smem + S::RING) + put.slot * S::TILE + half * (TS * 128) + mine * a.box_rows * 128,
+                                    f.value ? &map_v : &map_k, half * 64, y, &sh.full[put.slot]);
+                    }
+                    copied |= 1u << put.slot;
+                    copied_phase = (copied_phase & ~(1u << put.slot)) | put.phase << put.slot;
+                } else {
+                    // at most NS tiles are under way, so the loading warps are never 16 behind
+                    if (lane == 0) mbar_arrive(&sh.by_hand[hand & 15]);
+                    ++hand;
+                    copied &= ~(1u << put.slot);   // the place is free: its last copy has landed
+                }
+                keys += !f.value;
+                ++put;
+                again |= put.slot == 0;
+                more = f.next(a);
+                if (more) look();
+            }
+            // no copy may land after the block has gone
+            for (int i = 0; i < S::NS; ++i)
+                if (copied >> i & 1) {
+                    const long long t0 = clock64();
+                    while (!mbar_try_wait(&sh.full[i], copied_phase >> i & 1) && clock64() - t0 < kSpinCycles) {}
+                }
         }
     } else if (warp >= 8) {
         // ---- loading
@@ -671,58 +742,59 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
         };
         Feed f(walk);
         if constexpr (!E4M3) {
+            int keys = 0, hand = 0;
             constexpr int CPR = DP / 8, STEP = NLOAD / CPR;
             const int c = lt % CPR, r0 = lt / CPR;
             const uint32_t to = chunk_at(r0, c);
             const bool column = c * 8 < D;
             Share<STEP> x(a, r0, D * 2);
             const uint64_t stride = (uint64_t)x.page_bytes * a.c.kv_heads;
-            bool more = f.next(a);
-            if (more) x.look(a, f);
-            Ring<S::NS> told;                    // the tile to hand on
-            int it = 0, keys = 0;
-            for (; more; ++it) {
+            while (f.next(a)) {
+                if (!f.by_hand(a)) {
+                    keys += !f.value;
+                    advance();
+                    continue;
+                }
+                x.look(a, f);
                 const uint32_t first = f.first() + r0;
                 const unsigned char *src = (const unsigned char *)(f.value ? a.c.v : a.c.k) + (uint64_t)f.s.head * x.page_bytes + c * 16;
-                if (!wait_empty()) break;
+                // with tensor copies their warp says when a place is free: only it follows every round of
+                // the ring
+                if (!(a.box_rows ? mbar_wait(&sh.by_hand[hand & 15], (uint32_t)hand >> 4 & 1, fail) : wait_empty())) break;
+                ++hand;
                 if (!f.value) {
                     bool hole = false;
 #pragma unroll
                     for (int q = 0; q < x.ITER; ++q) hole |= !x.held(q);
                     if (hole) sh.hole[keys & 15] = 1;
-                    if (lt == 0) sh.hole[(keys + 8) & 15] = 0;   // at most NS tiles are under way
-                    ++keys;
                 }
+                if (!a.box_rows && lt == 0 && !f.value) sh.hole[(keys + 8) & 15] = 0;   // at most NS tiles are under way
+                keys += !f.value;
                 if (!f.draft()) {
                     const uint32_t dst = ring + put.slot * S::TILE + to;
 #pragma unroll
                     for (int q = 0; q < x.ITER; ++q)
                         cp_async16(dst + q * STEP * 128, x.at(src, stride, first, q), x.held(q) && column);
+                    cp_commit();
+                    cp_wait<0>();
                 } else {
                     unsigned char *dst = smem + S::RING + put.slot * S::TILE + to;
+                    uint4 v[x.ITER];
 #pragma unroll
                     for (int q = 0; q < x.ITER; ++q) {
-                        uint4 v = make_uint4(0, 0, 0, 0);
-                        if (x.held(q) && column) v = __ldg(reinterpret_cast<const uint4 *>(x.at(src, stride, first, q)));
-                        if (first + q * STEP >= (uint32_t)f.s.slots && zero_odd<M>(v)) sh.odd[f.seg & 7] = 1;
-                        *reinterpret_cast<uint4 *>(dst + q * STEP * 128) = v;
+                        v[q] = make_uint4(0, 0, 0, 0);
+                        if (x.held(q) && column) v[q] = __ldg(reinterpret_cast<const uint4 *>(x.at(src, stride, first, q)));
+                    }
+#pragma unroll
+                    for (int q = 0; q < x.ITER; ++q) {
+                        if (first + q * STEP >= (uint32_t)f.s.slots && zero_odd<M>(v[q])) sh.odd[f.seg & 7] = 1;
+                        *reinterpret_cast<uint4 *>(dst + q * STEP * 128) = v[q];
                     }
                 }
-                cp_commit();
+                proxy_fence();
+                warp_arrive(&sh.full[put.slot]);
                 advance();
-                more = f.next(a);
-                if (more) x.look(a, f);
-                if (it >= LAG<DP>) {
-                    cp_wait<LAG<DP>>();
-                    proxy_fence();
-                    warp_arrive(&sh.full[told.slot]);
-                    ++told;
-                }
             }
-            cp_wait<0>();
-            proxy_fence();
-            if (!more)
-                for (int i = min(it, LAG<DP>); i > 0; --i) { warp_arrive(&sh.full[told.slot]); ++told; }
         } else {
             // a thread converts one 16-byte chunk of every STEP-th row
             constexpr int RPR = DP / 16, STEP = NLOAD / RPR, ITER = TS / STEP;
@@ -797,30 +869,37 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
                 const long long mine_at = s.b * a.qb + ti * a.qt + hq * a.qh;
                 const int rows_here = min(s.rows - (row - lane), 32);
                 int mine_e = 0;
-#pragma unroll 4
-                for (int i = 0; i < LPR; ++i) {
-                    if (i * RPI >= rows_here) break;
-                    const int of = i * RPI + sub;
-                    const long long at = __shfl_sync(0xffffffffu, mine_at, of);
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (of < rows_here && ch < D / 8) v = __ldg(reinterpret_cast<const uint4 *>((const T *)a.q + at) + ch);
-                    if (E4M3) {
-                        float f[8], top = 0.0f;
-                        fa_unpack(v, f, T());
+#pragma unroll 1
+                for (int i0 = 0; i0 < LPR && i0 * RPI < rows_here; i0 += 8) {
+                    uint4 v[8];                            // eight steps' loads under way together
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
-#pragma unroll
-                        for (int o = LPR / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                        // the largest element of the row to [2^8, 2^9)
-                        const int e = top > 0.0f && top < INFINITY ? max(min(fa_exponent(top) - 8, 120), -120) : 0;
-                        const float pow = __int_as_float((127 - e) << 23);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) f[j] *= pow;
-                        v = fa_pack(f, M());
-                        const int from = __shfl_sync(0xffffffffu, e, (lane % RPI) * LPR);
-                        if (lane / RPI == i) mine_e = from;        // this thread's own row
+                    for (int i = 0; i < 8; ++i) {
+                        const int of = (i0 + i) * RPI + sub;
+                        const long long at = __shfl_sync(0xffffffffu, mine_at, of & 31);
+                        v[i] = make_uint4(0, 0, 0, 0);
+                        if (of < rows_here && ch < D / 8) v[i] = __ldg(reinterpret_cast<const uint4 *>((const T *)a.q + at) + ch);
                     }
-                    *reinterpret_cast<uint4 *>(dst + chunk_at(w0 + of, ch)) = v;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (E4M3) {
+                            float f[8], top = 0.0f;
+                            fa_unpack(v[i], f, T());
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
+#pragma unroll
+                            for (int o = LPR / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                            // the largest element of the row to [2^8, 2^9)
+                            const int e = top > 0.0f && top < INFINITY ? max(min(fa_exponent(top) - 8, 120), -120) : 0;
+                            const float pow = __int_as_float((127 - e) << 23);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) f[j] *= pow;
+                            v[i] = fa_pack(f, M());
+                            const int from = __shfl_sync(0xffffffffu, e, (lane % RPI) * LPR);
+                            if (lane / RPI == i0 + i) mine_e = from;        // this thread's own row
+                        }
+                        *reinterpret_cast<uint4 *>(dst + chunk_at(w0 + (i0 + i) * RPI + sub, ch)) = v[i];
+                        if ((i0 + i + 1) * RPI >= rows_here) break;
+                    }
                 }
                 if (E4M3) c *= __int_as_float((127 + mine_e) << 23);
                 proxy_fence();
@@ -992,18 +1071,18 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
             // of the block's partial results, slot 1 is a unit's first part, slot 0 a later one
             const int64_t prow0 = ((int64_t)blockIdx.x * 2 + (s.t0 == 0 ? 1 : 0)) * 256;
             if (copies > 1) {
-                // join the copies (of both streams) through shared memory, a quarter of the columns
-                // at a time: stream 0's queries become the sums, what follows them the statistics
-                constexpr int EC = DP / 4, EG = EC / 4;            // columns, 16-byte groups of them
-                const int streams = pair_up ? 2 : 1, threads = streams * TS, me = st * TS + r;
-                float *acc = reinterpret_cast<float *>(smem + S::Q);
-                float *stats = acc + threads * EC;
+                // join the copies (of both streams) through shared memory, where the queries were
+                const int streams = pair_up ? 2 : 1, threads = streams * TS, me = st * TS + r, parts = copies * streams;
+                float *stats = reinterpret_cast<float *>(smem + S::Q);             // 2 threads floats, then the sums
+                float *acc = stats + 512;
+                // columns at a time: all of them when the rows are few
+                const int room = S::TILE * streams / 4 - 512;
+                const int cols = parts * s.rows * DP <= room ? DP : parts * s.rows * (DP / 2) <= room ? DP / 2 : DP / 4;
                 auto sync = [&]() { bar_sync(pair_up ? 3 : 1, threads); };
                 sync();                                            // all products with the queries are done
                 stats[me] = bias;
                 stats[threads + me] = l;
                 sync();
-                const int parts = copies * streams;
                 float top = -INFINITY, sum = 0.0f;
                 for (int i = 0; i < parts; ++i) {
                     const int at = row + i * pad;
@@ -1016,25 +1095,29 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
                 }
                 const float f = l == 0.0f || !used ? 0.0f : ex2(bias - top) / sum;
                 const bool odd = sh.odd[sg & 7] != 0;
+                const int groups = cols / 4, part = st * copies + copy;
 #pragma unroll 1
-                for (int w = 0; w < 4; ++w) {
+                for (int col0 = 0; col0 < DP; col0 += cols) {
                     if (warp_live) {
-                        float o[EC];
-                        if constexpr (EC == 32) tmem_ld32(to + EC * w, o);
-                        else tmem_ld16(to + EC * w, o);
+#pragma unroll 1
+                        for (int w = 0; w < cols; w += 16) {
+                            float o[16];
+                            __syncwarp();
+                            tmem_ld16(to + col0 + w, o);
+                            if (live)
 #pragma unroll
-                        for (int g = 0; g < EG; ++g)
-                            *reinterpret_cast<float4 *>(acc + me * EC + ((g ^ (me & (EG - 1))) << 2)) =
-                                f == 0.0f ? make_float4(0, 0, 0, 0)
-                                          : make_float4(o[4 * g] * f, o[4 * g + 1] * f, o[4 * g + 2] * f, o[4 * g + 3] * f);
+                                for (int g = 0; g < 4; ++g)
+                                    *reinterpret_cast<float4 *>(acc + (part * s.rows + row) * cols + (((w / 4 + g) ^ (row & 3)) << 2)) =
+                                        f == 0.0f ? make_float4(0, 0, 0, 0)
+                                                  : make_float4(o[4 * g] * f, o[4 * g + 1] * f, o[4 * g + 2] * f, o[4 * g + 3] * f);
+                        }
                     }
                     sync();
-                    for (int x = me; x < s.rows * EG; x += threads) {
-                        const int q = x / EG, g = x % EG, col = EC * w + 4 * g;
+                    for (int x = me; x < s.rows * groups; x += threads) {
+                        const int q = x / groups, g = x - q * groups, col = col0 + 4 * g;
                         float4 y = make_float4(0, 0, 0, 0);
                         for (int i = 0; i < parts; ++i) {
-                            const int at = q + i * pad;
-                            const float4 z = *reinterpret_cast<const float4 *>(acc + at * EC + ((g ^ (at & (EG - 1))) << 2));
+                            const float4 z = *reinterpret_cast<const float4 *>(acc + (i * s.rows + q) * cols + ((g ^ (q & 3)) << 2));
                             y.x += z.x; y.y += z.y; y.z += z.z; y.w += z.w;
                         }
                         const int qr = 256 * s.block + q, t = qr / a.group;
@@ -1050,7 +1133,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
                             *reinterpret_cast<uint2 *>(dst) = make_uint2(fa_pack2(y.x, y.y, T()), fa_pack2(y.z, y.w, T()));
                         }
                     }
-                    sync();
+                    if (col0 + cols < DP) sync();
                 }
                 if (st == 0 && copy == 0 && live) {
                     const float lse = used && sum != 0.0f ? top + log2f(sum) : -INFINITY;
@@ -1079,38 +1162,56 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a) {
             }
             if (st == 0 || s.two()) {
                 const bool odd = sh.odd[sg & 7] != 0;
-                const int64_t prow = prow0 + row;
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                const int64_t orow = ((int64_t)s.b * a.T + ti) * a.heads + hq;
+                const int64_t orow = ((int64_t)s.b * a.T + ti) * a.heads + hq, prow = prow0 + row;
                 if (warp_live) {
+                    // Rows leave through shared memory (the stream's queries are done with), so that a
+                    // row's stores are contiguous: the 16-bit result whole, fp32 parts in two halves.
+                    constexpr int LPR = DP / 8, RPI = 32 / LPR;
+                    unsigned char *stage = smem + S::Q + st * S::TILE;
+                    const int w0 = 32 * (warp & 3), ch = lane % LPR, sub = lane / LPR;
+                    const int rows_here = min(s.rows - (row - lane), 32);
+                    const int per_turn = partial ? DP / 2 : DP;         // columns staged at a time
 #pragma unroll 1
-                    for (int w = 0; w < DP / 32; ++w) {
-                        float o[32];
-                        __syncwarp();
-                        tmem_ld32(to + 32 * w, o);
-                        if (join) {
-                            float o1[32];
-                            tmem_ld32(to + DP + 32 * w, o1);
+                    for (int turn = 0; turn < DP; turn += per_turn) {
+#pragma unroll 1
+                        for (int w = turn; w < turn + per_turn; w += 32) {
+                            float o[32];
+                            __syncwarp();
+                            tmem_ld32(to + w, o);
+                            if (join) {
+                                float o1[32];
+                                tmem_ld32(to + DP + w, o1);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = o[e] * f0 + o1[e] * f1;
-                        }
+                                for (int e = 0; e < 32; ++e) o[e] = o[e] * f0 + o1[e] * f1;
+                            }
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = used && l != 0.0f ? o[e] * inv : 0.0f;
-                        if (odd && used) add_odd<E4M3, T, 32>(a, s, rows, ti, 32 * w, o);
-                        if (live) {
+                            for (int e = 0; e < 32; ++e) o[e] = used && l != 0.0f ? o[e] * inv : 0.0f;
+                            if (odd && used) add_odd<E4M3, T, 32>(a, s, rows, ti, w, o);
                             if (partial) {
-                                float4 *dst = reinterpret_cast<float4 *>(a.part_o + prow * DP + 32 * w);
 #pragma unroll
-                                for (int e = 0; e < 32; e += 4) dst[e / 4] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                                for (int e = 0; e < 32; e += 4)
+                                    *reinterpret_cast<float4 *>(stage + chunk_at(r, (w - turn + e) / 4)) =
+                                        make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                             } else {
-                                T *dst = (T *)a.out + orow * D + 32 * w;
 #pragma unroll
                                 for (int e = 0; e < 32; e += 8) {
                                     const float f[8] = {o[e], o[e + 1], o[e + 2], o[e + 3], o[e + 4], o[e + 5], o[e + 6], o[e + 7]};
-                                    if (32 * w + e < D) *reinterpret_cast<uint4 *>(dst + e) = fa_pack(f, T());
+                                    *reinterpret_cast<uint4 *>(stage + chunk_at(r, (w + e) / 8)) = fa_pack(f, T());
                                 }
                             }
                         }
+                        __syncwarp();
+#pragma unroll 4
+                        for (int i = 0; i < LPR; ++i) {
+                            const int of = i * RPI + sub;
+                            const long long at = __shfl_sync(0xffffffffu, partial ? (long long)prow : (long long)orow, of);
+                            const uint4 v = *reinterpret_cast<const uint4 *>(stage + chunk_at(w0 + of, ch));
+                            if (of >= rows_here) continue;
+                            if (partial) *reinterpret_cast<uint4 *>(a.part_o + at * DP + turn + ch * 4) = v;
+                            else if (ch * 8 < D) *reinterpret_cast<uint4 *>((T *)a.out + at * D + ch * 8) = v;
+                        }
+                        __syncwarp();
                     }
                 }
                 if (live) {
@@ -1195,8 +1296,35 @@ size_t workspace_bytes(int head_dim) {
     return (size_t)MAX_CTAS * 2 * 256 * (dp + 1) * sizeof(float) + MAX_CTAS * sizeof(int);
 }
 
+// Tensor maps of a 16-bit cache: rows of head_dim elements, boxes of up to 128 rows of one page by
+// 64 columns, 128-byte swizzled.  False where the cache cannot have them (pages of fewer than the
+// eight rows of a swizzle atom, more rows than a coordinate holds).
+bool make_maps(const fa_kv_cache *c, int box_rows, CUtensorMap (&maps)[2]) {
+    typedef CUresult (*encode_t)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                                 const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const encode_t encode = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return (encode_t)f;
+    }();
+    const int64_t rows = (int64_t)c->n_pages * c->kv_heads * c->page_size;
+    if (!encode || box_rows < 8 || rows < 1 || rows > 2147483647) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)c->head_dim, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)c->head_dim * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, step[2] = {1, 1};
+    for (int i = 0; i < 2; ++i)
+        if (encode(&maps[i], CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, i ? c->v : c->k, dims, strides, box, step,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return false;
+    return true;
+}
+
 template <int DP, bool E4M3, class T, class M>
-fa_status launch(const AttendArgs &a, cudaStream_t s) {
+fa_status launch(const AttendArgs &a, const CUtensorMap (&maps)[2], cudaStream_t s) {
     constexpr size_t smem = smem_bytes<DP, E4M3>();
     static_assert(smem <= 232448, "shared memory of a block");
     int dev = 0, n_sm = 0;
@@ -1206,7 +1334,7 @@ fa_status launch(const AttendArgs &a, cudaStream_t s) {
         e = cudaFuncSetAttribute(k_attend<DP, E4M3, T, M>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return fa_refuse("fa_tree_attention", cudaGetErrorString(e), FA_ERR_CUDA);
     const int ctas = std::min(n_sm, MAX_CTAS);
-    k_attend<DP, E4M3, T, M><<<ctas, NTHR, smem, s>>>(a);
+    k_attend<DP, E4M3, T, M><<<ctas, NTHR, smem, s>>>(a, maps[0], maps[1]);
     fa_status st = fa_launch_check("tree attention");
     if (st != FA_OK) return st;
     const int64_t units = (int64_t)a.B * a.c.kv_heads * a.blocks;
@@ -1274,10 +1402,13 @@ extern "C" fa_status fa_tree_attention(const fa_kv_cache *cache, int32_t dtype, 
     a.status = (int *)(a.part_lse + (size_t)MAX_CTAS * 2 * 256);
     cudaStream_t s = (cudaStream_t)stream;
     const bool f16 = dtype == FA_DTYPE_F16;
+    CUtensorMap maps[2] = {};
+    const int box_rows = std::min(cache->page_size, TS);
+    a.box_rows = cache->format != FA_CACHE_E4M3 && make_maps(cache, box_rows, maps) ? box_rows : 0;
     if (cache->format == FA_CACHE_E4M3) {
-        if (dp == 64) return f16 ? launch<64, true, __half, __half>(a, s) : launch<64, true, __nv_bfloat16, __half>(a, s);
-        return f16 ? launch<128, true, __half, __half>(a, s) : launch<128, true, __nv_bfloat16, __half>(a, s);
+        if (dp == 64) return f16 ? launch<64, true, __half, __half>(a, maps, s) : launch<64, true, __nv_bfloat16, __half>(a, maps, s);
+        return f16 ? launch<128, true, __half, __half>(a, maps, s) : launch<128, true, __nv_bfloat16, __half>(a, maps, s);
     }
-    if (dp == 64) return f16 ? launch<64, false, __half, __half>(a, s) : launch<64, false, __nv_bfloat16, __nv_bfloat16>(a, s);
-    return f16 ? launch<128, false, __half, __half>(a, s) : launch<128, false, __nv_bfloat16, __nv_bfloat16>(a, s);
+    if (dp == 64) return f16 ? launch<64, false, __half, __half>(a, maps, s) : launch<64, false, __nv_bfloat16, __nv_bfloat16>(a, maps, s);
+    return f16 ? launch<128, false, __half, __half>(a, maps, s) : launch<128, false, __nv_bfloat16, __nv_bfloat16>(a, maps, s);
 }
