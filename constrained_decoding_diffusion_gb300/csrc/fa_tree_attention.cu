@@ -251,41 +251,49 @@ struct Segment {
 };
 
 struct Walk {
-    int g, g1, base, b;
+    int left, t0;             // places of the run still to come; the next place of the unit
+    int b, head, block;       // the unit
     __device__ __forceinline__ Walk(const AttendArgs &a, const Work &w, int cta, int ctas) {
         const int units = a.c.kv_heads * a.blocks, total = w.cum[RUNS] * units;
         ctas = min(total, ctas);                    // no run is empty
-        g = g1 = base = b = 0;
+        left = t0 = b = head = block = 0;
         if (cta >= ctas) return;
-        g = run_start(total, cta, ctas);
-        g1 = run_start(total, cta + 1, ctas);
+        const int g = run_start(total, cta, ctas);
+        left = run_start(total, cta + 1, ctas) - g;
         int lo = 0, hi = RUNS;                      // the last run that starts at or before g
         while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
             if (w.cum[mid] * units <= g) lo = mid; else hi = mid;
         }
         b = lo * run_length(a);
-        base = w.cum[lo] * units;
+        int base = w.cum[lo] * units, places;
         while (true) {
-            const int next = base + places_of(a, b) * units;
-            if (g < next) break;
-            base = next;
+            places = places_of(a, b);
+            if (g < base + places * units) break;
+            base += places * units;
             ++b;
         }
+        const int u = (g - base) / places;
+        t0 = g - base - u * places;
+        head = u / a.blocks;
+        block = u - head * a.blocks;
     }
     __device__ __forceinline__ bool next(const AttendArgs &a, Segment &s) {
-        while (g < g1) {
+        while (left > 0) {
             extent(a, b, s.slots, s.use, s.end);
             s.b = b;
+            s.head = head;
+            s.block = block;
             s.nt = max(1, (s.end + TS - 1) / TS);
-            const int places = s.nt + kUnitCost, off = g - base, u = off / places;
-            s.t0 = off - u * places;
-            s.head = u / a.blocks;
-            s.block = u - s.head * a.blocks;
-            s.n = min(s.nt - s.t0, g1 - g);
-            s.rows = min(a.rows - 256 * s.block, 256);
-            g += min(places - s.t0, g1 - g);
-            if (g - base >= places * a.c.kv_heads * a.blocks) { base = g; ++b; }
+            s.t0 = t0;
+            s.n = min(s.nt - t0, left);
+            s.rows = min(a.rows - 256 * block, 256);
+            left -= s.nt + kUnitCost - t0;
+            t0 = 0;
+            if (++block == a.blocks) {
+                block = 0;
+                if (++head == a.c.kv_heads) { head = 0; ++b; }
+            }
             if (s.n > 0) return true;               // the run may begin behind a unit's last tile
         }
         return false;
@@ -449,6 +457,12 @@ __device__ __forceinline__ uint32_t seen_bits(const AttendArgs &a, const Segment
     return v;
 }
 
+template <class T> __device__ __forceinline__ T bits_as(uint16_t u) {
+    T x;
+    memcpy(&x, &u, 2);
+    return x;
+}
+
 // Drafted values that are not finite are left out of the products (a row that does not see them must
 // not meet them); here they join the rows that do: N columns from col on of drafted token t's result.
 template <bool E4M3, class T, int N>
@@ -546,12 +560,12 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a, const __grid_c
                 }
                 umma_commit(&sh.s_full[st]);
             };
-            auto values = [&](int st, int slot, bool first) {
+            auto values = [&](int st, int slot, bool first, bool last) {
                 const uint64_t vd = umma_desc(ring + slot * S::TILE, TS * 128);
                 const uint32_t d = tmem + 256 + st * DP, p = tmem + st * TS;
 #pragma unroll
                 for (int k = 0; k < TS / 16; ++k) umma_ts(d, p + k * 8, vd + k * (2048 / 16), idesc_o, !first || k > 0);
-                umma_commit(&sh.pv_done[st]);
+                if (last) umma_commit(&sh.pv_done[st]);   // else the next scores' barrier says it too
             };
             auto wait_p = [&](int st) {
                 const bool ok = mbar_wait(&sh.p_full[st], (uint32_t)np[st] & 1, fail);
@@ -574,14 +588,14 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a, const __grid_c
                     for (int j = 0; j < s.n && ok; ++j) {
                         const int vs = next_tile();
                         if (vs < 0 || !wait_p(0)) { ok = false; break; }
-                        values(0, vs, j == 0);
+                        values(0, vs, j == 0, j + 1 == s.n);
                         int ks = -1;
                         if (j + 1 < s.n) {
                             if ((ks = next_tile()) < 0) { ok = false; break; }
                             scores(0, ks);
                         }
                         if (!wait_p(1)) { ok = false; break; }
-                        values(1, vs, j == 0);
+                        values(1, vs, j == 0, j + 1 == s.n);
                         umma_commit(&sh.empty[vs]);
                         if (ks >= 0) {
                             scores(1, ks);
@@ -597,7 +611,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a, const __grid_c
                     for (int j = 0; j < s.n && ok; ++j) {
                         const int st = j & 1;
                         if ((slot = next_tile()) < 0 || !wait_p(st)) { ok = false; break; }
-                        values(st, slot, j < 2);
+                        values(st, slot, j < 2, j + 2 >= s.n);
                         umma_commit(&sh.empty[slot]);
                         if (j + 2 < s.n) {
                             if ((slot = next_tile()) < 0) { ok = false; break; }
@@ -862,46 +876,46 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a, const __grid_c
             const bool used = live && ti < s.use;
             float c = a.scale * kLog2e;
             if (warp_live) {
-                // the warp's rows of Q into the stream's tile: DP / 8 lanes to a row of 16-byte chunks
+                // The warp's rows of Q into the stream's tile, DP / 8 lanes to a row of 16-byte chunks.
+                // (This and the result run once a unit, from a cold instruction cache: short loops.)
                 constexpr int LPR = DP / 8, RPI = 32 / LPR;       // lanes per row, rows per step
                 unsigned char *dst = smem + S::Q + st * S::TILE;
                 const int ch = lane % LPR, sub = lane / LPR, w0 = 32 * (warp & 3);
                 const long long mine_at = s.b * a.qb + ti * a.qt + hq * a.qh;
                 const int rows_here = min(s.rows - (row - lane), 32);
-                int mine_e = 0;
 #pragma unroll 1
-                for (int i0 = 0; i0 < LPR && i0 * RPI < rows_here; i0 += 8) {
-                    uint4 v[8];                            // eight steps' loads under way together
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int of = (i0 + i) * RPI + sub;
-                        const long long at = __shfl_sync(0xffffffffu, mine_at, of & 31);
-                        v[i] = make_uint4(0, 0, 0, 0);
-                        if (of < rows_here && ch < D / 8) v[i] = __ldg(reinterpret_cast<const uint4 *>((const T *)a.q + at) + ch);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        if (E4M3) {
-                            float f[8], top = 0.0f;
-                            fa_unpack(v[i], f, T());
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
-#pragma unroll
-                            for (int o = LPR / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                            // the largest element of the row to [2^8, 2^9)
-                            const int e = top > 0.0f && top < INFINITY ? max(min(fa_exponent(top) - 8, 120), -120) : 0;
-                            const float pow = __int_as_float((127 - e) << 23);
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) f[j] *= pow;
-                            v[i] = fa_pack(f, M());
-                            const int from = __shfl_sync(0xffffffffu, e, (lane % RPI) * LPR);
-                            if (lane / RPI == i0 + i) mine_e = from;        // this thread's own row
-                        }
-                        *reinterpret_cast<uint4 *>(dst + chunk_at(w0 + (i0 + i) * RPI + sub, ch)) = v[i];
-                        if ((i0 + i + 1) * RPI >= rows_here) break;
-                    }
+                for (int of = sub; of - sub < rows_here; of += RPI) {
+                    const long long at = __shfl_sync(0xffffffffu, mine_at, of & 31);
+                    const bool there = of < rows_here && ch < D / 8;
+                    cp_async16(smem_u32(dst) + chunk_at(w0 + of, ch), (const T *)a.q + (there ? at + ch * 8 : 0), there);
                 }
-                if (E4M3) c *= __int_as_float((127 + mine_e) << 23);
+                cp_commit();
+                cp_wait<0>();
+                if (E4M3) {
+                    __syncwarp();
+                    uint32_t top = 0;                             // the row's largest magnitude, as bits of T
+#pragma unroll 1
+                    for (int ch2 = 0; ch2 < LPR; ++ch2) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(dst + chunk_at(r, ch2));
+                        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) top = max(top, max(x[j] & 0x7fffu, x[j] >> 16 & 0x7fffu));
+                    }
+                    const float big = fa_to_f32(bits_as<T>((uint16_t)top));
+                    // the largest element of the row to [2^8, 2^9)
+                    const int e = big > 0.0f && big < INFINITY ? max(min(fa_exponent(big) - 8, 120), -120) : 0;
+                    const float pow = __int_as_float((127 - e) << 23);
+#pragma unroll 1
+                    for (int ch2 = 0; ch2 < LPR; ++ch2) {
+                        uint4 *v = reinterpret_cast<uint4 *>(dst + chunk_at(r, ch2));
+                        float f[8];
+                        fa_unpack(*v, f, T());
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) f[j] *= pow;
+                        *v = fa_pack(f, M());
+                    }
+                    c *= __int_as_float((127 + e) << 23);
+                }
                 proxy_fence();
             }
             warp_arrive(&sh.q_full[st]);
@@ -1010,10 +1024,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a, const __grid_c
                             l *= f;
                         }
                         if (q > 0) {
-                            // the previous tile's values have been added
-                            mbar_wait(&sh.pv_done[st], (uint32_t)(npv - 1) & 1, fail);
-                            __syncwarp();
-                            tc_fence_after();
+                            // (the previous tile's values were added before these scores were made)
 #pragma unroll 1
                             for (int w = 0; w < DP / 32; ++w) {
                                 float o[32];
@@ -1061,10 +1072,9 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a, const __grid_c
                 }
                 tc_fence_before();
                 warp_arrive(&sh.p_full[st]);
-                ++npv;
             }
             // ---- the segment's result
-            mbar_wait(&sh.pv_done[st], (uint32_t)(npv - 1) & 1, fail);
+            mbar_wait(&sh.pv_done[st], (uint32_t)npv++ & 1, fail);
             __syncwarp();
             tc_fence_after();
             const bool pair_up = !s.two() && s.n > 1, join = pair_up && copies == 1, partial = s.n < s.nt;
