@@ -15,30 +15,138 @@ __device__ __forceinline__ float2 turn(int32_t t, uint64_t phase, float mscale, 
     return make_float2(mscale * c, mscale * (inverse ? -s : s));
 }
 
-// y = R x per pair.  One thread per element, any strides, any sizes.
+unsigned blocks_for(int64_t items) { return (unsigned)std::max<int64_t>(1, std::min<int64_t>((items + NT - 1) / NT, 152 * 16)); }
+
+struct RopeArgs {
+    int64_t n_tokens, xt, xh, ot, oh;
+    int heads, dim, rot, interleaved, inverse;
+    const void *x;
+    void *out;
+    const int32_t *pos;
+    const uint64_t *phase;
+    float mscale;
+};
+
+// y = R x per pair, element by element: any strides and sizes.
 template <class T>
-__global__ void __launch_bounds__(NT) k_rope(int64_t n_tokens, int heads, int dim, int rot, int interleaved, bool inverse,
-                                             const T *x, int64_t xt, int64_t xh, const int32_t *__restrict__ pos,
-                                             const uint64_t *__restrict__ phase, float mscale, T *out, int64_t ot,
-                                             int64_t oh) {
-    const int half = rot / 2, per_head = half + (dim - rot);
-    const int64_t total = n_tokens * heads * per_head;
+__global__ void __launch_bounds__(NT) k_rope_any(RopeArgs a) {
+    const int half = a.rot / 2, per_head = half + (a.dim - a.rot);
+    const int64_t total = a.n_tokens * a.heads * per_head;
     for (int64_t it = (int64_t)blockIdx.x * NT + threadIdx.x; it < total; it += (int64_t)gridDim.x * NT) {
         const int i = (int)(it % per_head);
-        const int64_t nh = it / per_head, n = nh / heads;
-        const int h = (int)(nh % heads);
-        const T *xr = x + n * xt + h * xh;
-        T *yr = out + n * ot + h * oh;
+        const int64_t nh = it / per_head, n = nh / a.heads;
+        const int h = (int)(nh % a.heads);
+        const T *xr = (const T *)a.x + n * a.xt + h * a.xh;
+        T *yr = (T *)a.out + n * a.ot + h * a.oh;
         if (i >= half) {
-            yr[rot + i - half] = xr[rot + i - half];
+            yr[a.rot + i - half] = xr[a.rot + i - half];
             continue;
         }
-        const int a = interleaved ? 2 * i : i, b = interleaved ? 2 * i + 1 : i + half;
-        const float2 cs = turn(__ldg(pos + n), __ldg(phase + i), mscale, inverse);
-        const float x0 = fa_to_f32(xr[a]), x1 = fa_to_f32(xr[b]);
-        yr[a] = fa_from_f32<T>(x0 * cs.x - x1 * cs.y);
-        yr[b] = fa_from_f32<T>(x0 * cs.y + x1 * cs.x);
+        const int p = a.interleaved ? 2 * i : i, q = a.interleaved ? 2 * i + 1 : i + half;
+        const float2 cs = turn(__ldg(a.pos + n), __ldg(a.phase + i), a.mscale, a.inverse);
+        const float x0 = fa_to_f32(xr[p]), x1 = fa_to_f32(xr[q]);
+        yr[p] = fa_from_f32<T>(x0 * cs.x - x1 * cs.y);
+        yr[q] = fa_from_f32<T>(x0 * cs.y + x1 * cs.x);
     }
+}
+
+// The same in 16-byte vectors of N elements, where every row is aligned and the rotated part is
+// whole vectors (half layout: each half).  The bound is memory: x is read and out written
+// once.  A block takes a few tokens with all their heads: their sines and cosines, one per token
+// and pair, are made once in shared memory while the first vectors are on their way, and four
+// vectors (half layout: vector pairs) a thread are under way at a time.
+constexpr int ROPE_TOKENS = 8;
+template <class T, bool INTERLEAVED>
+__global__ void __launch_bounds__(NT) k_rope(RopeArgs a, int tokens) {
+    extern __shared__ float2 table[];          // [tokens][rot / 2]
+    constexpr int N = fa_vec<T>::N, U = 4;
+    const int half = a.rot / 2, tid = threadIdx.x;
+    // a head's work items: rotated vectors (pairs of vectors), then the vectors that are copied
+    const int turned = INTERLEAVED ? a.rot / N : half / N, items = turned + (a.dim - a.rot) / N, per_token = items * a.heads;
+    const int64_t n0 = (int64_t)blockIdx.x * tokens;
+    const int here = (int)min((int64_t)tokens, a.n_tokens - n0), total = here * per_token;
+    bool made = false;
+    for (int first = tid; first < total || !made; first += U * NT) {
+        uint4 v[U], w[U];
+        int at[U], tok[U];
+        const T *src[U];
+        int64_t off[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int it = first + u * NT;
+            at[u] = -1;
+            if (it >= total) continue;
+            tok[u] = it / per_token;
+            const int rest = it - tok[u] * per_token, h = rest / items, i = rest - h * items;
+            at[u] = i;
+            const int col = i < turned ? i * N : a.rot + (i - turned) * N;
+            src[u] = (const T *)a.x + (n0 + tok[u]) * a.xt + h * a.xh + col;
+            off[u] = (n0 + tok[u]) * a.ot + h * a.oh + col;
+            v[u] = *reinterpret_cast<const uint4 *>(src[u]);   // (not the read-only path: out may be x)
+            if (!INTERLEAVED && i < turned) w[u] = *reinterpret_cast<const uint4 *>(src[u] + half);
+        }
+        if (!made) {
+            for (int i = tid; i < here * half; i += NT) {
+                const int t = i / half;
+                table[i] = turn(__ldg(a.pos + n0 + t), __ldg(a.phase + i - t * half), a.mscale, a.inverse);
+            }
+            __syncthreads();
+            made = true;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (at[u] < 0) continue;
+            uint4 *dst = reinterpret_cast<uint4 *>((T *)a.out + off[u]);
+            if (at[u] >= turned) { *dst = v[u]; continue; }
+            float x[N];
+            fa_unpack(v[u], x, T());
+            if (INTERLEAVED) {
+                const float2 *cs = table + tok[u] * half + at[u] * (N / 2);
+#pragma unroll
+                for (int e = 0; e < N; e += 2) {
+                    const float2 f = cs[e / 2];
+                    const float p = x[e] * f.x - x[e + 1] * f.y;
+                    x[e + 1] = x[e] * f.y + x[e + 1] * f.x;
+                    x[e] = p;
+                }
+                *dst = fa_pack(x, T());
+            } else {
+                const float2 *cs = table + tok[u] * half + at[u] * N;
+                float y[N];
+                fa_unpack(w[u], y, T());
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    const float2 f = cs[e];
+                    const float p = x[e] * f.x - y[e] * f.y;
+                    y[e] = x[e] * f.y + y[e] * f.x;
+                    x[e] = p;
+                }
+                *dst = fa_pack(x, T());
+                *reinterpret_cast<uint4 *>((T *)a.out + off[u] + half) = fa_pack(y, T());
+            }
+        }
+    }
+}
+
+template <class T> fa_status launch_rope(const RopeArgs &a, cudaStream_t s) {
+    constexpr int N = fa_vec<T>::N;
+    const bool aligned = !(((uintptr_t)a.x | (uintptr_t)a.out) & 15) && !((a.xt | a.xh | a.ot | a.oh) % N);
+    const bool whole = a.dim % N == 0 && (a.interleaved ? a.rot % N == 0 : a.rot / 2 % N == 0);
+    const int64_t per_token = (int64_t)a.heads * ((a.interleaved ? a.rot : a.rot / 2) + a.dim - a.rot) / N;
+    if (!aligned || !whole || per_token > (1 << 24)) {
+        const int64_t items = a.n_tokens * a.heads * (a.dim - a.rot / 2);
+        k_rope_any<T><<<blocks_for(items), NT, 0, s>>>(a);
+        return fa_launch_check("rope");
+    }
+    // about two rounds of vectors a block; fewer tokens where that leaves SMs without a block
+    int tokens = (int)std::min<int64_t>(ROPE_TOKENS, std::max<int64_t>(1, 2 * 4 * NT / std::max<int64_t>(per_token, 1)));
+    tokens = (int)std::min<int64_t>(tokens, std::max<int64_t>(1, a.n_tokens / (152 * 4)));
+    const int64_t blocks = (a.n_tokens + tokens - 1) / tokens;
+    if (blocks > 2147483647) return fa_refuse("fa_rope", "too many tokens");
+    const size_t smem = (size_t)tokens * (a.rot / 2) * sizeof(float2);   // at most 8 * 512 * 8 bytes
+    if (a.interleaved) k_rope<T, true><<<(unsigned)blocks, NT, smem, s>>>(a, tokens);
+    else k_rope<T, false><<<(unsigned)blocks, NT, smem, s>>>(a, tokens);
+    return fa_launch_check("rope");
 }
 
 struct WriteArgs {
@@ -52,9 +160,10 @@ struct WriteArgs {
     float mscale;
 };
 
-// One warp per (token, head): the key's row, then the value's.  Lane l holds elements l, l + 32, ...
+// One warp per (token, head), element by element: any strides and alignment.  Lane l holds elements
+// l, l + 32, ...
 template <class T>
-__global__ void __launch_bounds__(NT) k_cache_write(WriteArgs a) {
+__global__ void __launch_bounds__(NT) k_cache_write_any(WriteArgs a) {
     const int lane = threadIdx.x & 31;
     const int64_t w = (int64_t)blockIdx.x * (NT / 32) + (threadIdx.x >> 5);
     const int H = a.c.kv_heads, D = a.c.head_dim;
@@ -107,27 +216,240 @@ __global__ void __launch_bounds__(NT) k_cache_write(WriteArgs a) {
     }
 }
 
-__device__ __forceinline__ float cached(const void *p, const float *scale, int format, int64_t row, int D, int d) {
-    const int64_t at = row * D + d;
-    if (format == FA_CACHE_F16) return __half2float(((const __half *)p)[at]);
-    if (format == FA_CACHE_BF16) return __bfloat162float(((const __nv_bfloat16 *)p)[at]);
-    const uint32_t h = fa_e4m3x2_to_half2(((const uint8_t *)p)[at]);
-    return __half2float(__ushort_as_half((unsigned short)(h & 0xffff))) * scale[row];
+// x / s for |x| <= 448 s, rounded as a division would be: the product with the reciprocal, then one
+// step of Markstein's correction (the remainder of an fma times the reciprocal).  The remainder is
+// exact unless it falls below the normal range, which the caller excludes.
+__device__ __forceinline__ float quotient(float x, float s, float r) {
+    const float q = x * r;
+    return fmaf(fmaf(-q, s, x), r, q);
 }
 
-template <class T>
-__global__ void __launch_bounds__(NT) k_cache_read(fa_cache_view c, int format, int B, int N, const int32_t *length, T *k, T *v) {
-    const int H = c.kv_heads, D = c.head_dim;
-    const int64_t total = (int64_t)B * N * H * D;
-    for (int64_t it = (int64_t)blockIdx.x * NT + threadIdx.x; it < total; it += (int64_t)gridDim.x * NT) {
-        const int d = (int)(it % D);
-        const int64_t r = it / D;
-        const int h = (int)(r % H);
-        const int64_t bt = r / H;
-        const int b = (int)(bt / N), t = (int)(bt % N);
-        const int64_t row = t < length[b] ? c.row(b, t, h) : -1;
-        k[it] = row < 0 ? fa_from_f32<T>(0.0f) : fa_from_f32<T>(cached(c.k, c.k_scale, format, row, D, d));
-        v[it] = row < 0 ? fa_from_f32<T>(0.0f) : fa_from_f32<T>(cached(c.v, c.v_scale, format, row, D, d));
+// The same in vectors of eight elements: a group of G = 8, 16 or 32 lanes holds a row, a lane eight
+// of its elements, and each row is read once (a rotated half layout reads a lane's mates too, from
+// the lines its neighbours load).  The bound is memory: keys and values in, codes and scales out;
+// sines and cosines are made once per token in shared memory, and the division by the scale is a
+// multiplication with a correction.  A block takes a few tokens with all their heads; a thread has
+// the vectors of two rows' keys and values under way.
+template <class T, int G, int FORMAT>
+__global__ void __launch_bounds__(NT) k_cache_write(WriteArgs a, int tokens) {
+    extern __shared__ float2 table[];           // [tokens][rot / 2]
+    constexpr int V = 8 / fa_vec<T>::N, ROWS = NT / G, U = 2;   // 16-byte loads of eight elements; rows in step
+    const int H = a.c.kv_heads, D = a.c.head_dim, half = a.rot / 2;
+    const int g = threadIdx.x % G, r0 = threadIdx.x / G, d = g * 8;
+    const unsigned all = (unsigned)a.B * (unsigned)a.T, n0 = blockIdx.x * (unsigned)tokens;   // below 2^31
+    const int here = (int)min((unsigned)tokens, all - n0), total = here * H;
+    const unsigned mask = G == 32 ? 0xffffffffu : ((1u << G) - 1) << (threadIdx.x % 32 / G * G);
+    bool made = a.rot == 0;
+    for (int first = r0; first - r0 < total; first += U * ROWS) {
+        int64_t row[U];
+        int tok[U];
+        uint4 x[U][2][V], m[U][V];               // keys, values; the keys' mates in the half layout
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int it = first + u * ROWS;
+            row[u] = -1;
+            if (it >= total) continue;
+            tok[u] = it / H;
+            const int h = it - tok[u] * H;
+            const unsigned bt = n0 + tok[u], b = bt / (unsigned)a.T;
+            const int t = (int)(bt - b * (unsigned)a.T);
+            if (a.count && t >= __ldg(a.count + b)) continue;
+            row[u] = a.c.row((int)b, (int64_t)__ldg(a.start + b) + t, h);
+            if (row[u] < 0 || d >= D) continue;
+            const T *k = (const T *)a.k + b * a.kb + t * a.kt + h * a.kh + d;
+            const T *v = (const T *)a.v + b * a.vb + t * a.vt + h * a.vh + d;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                x[u][0][i] = __ldg(reinterpret_cast<const uint4 *>(k) + i);
+                x[u][1][i] = __ldg(reinterpret_cast<const uint4 *>(v) + i);
+                if (!a.interleaved && d < a.rot) m[u][i] = __ldg(reinterpret_cast<const uint4 *>(d < half ? k + half : k - half) + i);
+            }
+        }
+        if (!made) {
+            for (int i = threadIdx.x; i < here * half; i += NT) {
+                const int t = i / half;
+                table[i] = turn(__ldg(a.pos + n0 + t), __ldg(a.phase + i - t * half), a.mscale, false);
+            }
+            __syncthreads();
+            made = true;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (row[u] < 0) continue;            // the same for a row's whole group
+#pragma unroll
+            for (int side = 0; side < 2; ++side) {
+                float f[8], amax = 0.0f;
+                auto get = [&](const uint4 (&w)[V], float (&y)[8]) {
+                    if constexpr (V == 1) {
+                        fa_unpack(w[0], y, T());
+                    } else {
+                        float p[4];
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            fa_unpack(w[i], p, 0.0f);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) y[4 * i + j] = p[j];
+                        }
+                    }
+                };
+                if (d < D) get(x[u][side], f);
+                else
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) f[e] = 0.0f;
+                if (side == 0 && d < a.rot) {
+                    if (a.interleaved) {
+                        const float2 *cs = table + tok[u] * half + d / 2;
+#pragma unroll
+                        for (int e = 0; e < 8; e += 2) {
+                            const float2 t = cs[e / 2];
+                            const float p = f[e] * t.x - f[e + 1] * t.y;
+                            f[e + 1] = f[e] * t.y + f[e + 1] * t.x;
+                            f[e] = p;
+                        }
+                    } else {
+                        const bool second = d >= half;
+                        const float2 *cs = table + tok[u] * half + (second ? d - half : d);
+                        float y[8];
+                        get(m[u], y);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) f[e] = second ? y[e] * cs[e].y + f[e] * cs[e].x : f[e] * cs[e].x - y[e] * cs[e].y;
+                    }
+                }
+                const int64_t at = row[u] * D + d;
+                void *dst = side ? a.c.v : a.c.k;
+                if (FORMAT == FA_CACHE_E4M3) {
+                    bool odd = false;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        amax = fmaxf(amax, fabsf(f[e]));
+                        odd |= !(fabsf(f[e]) < INFINITY);
+                    }
+                    if (odd) amax = INFINITY;
+#pragma unroll
+                    for (int o = G / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(mask, amax, o));
+                    odd = !(amax < INFINITY);
+                    const float scale = odd ? __int_as_float(0x7fffffff) : amax / FA_E4M3_MAX;
+                    if (odd || amax < 1e-30f) {
+                        // a row of zeros or one that is marked; tiny values take the plain division
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) f[e] = odd || scale == 0.0f ? 0.0f : f[e] / scale;
+                    } else {
+                        const float r = 1.0f / scale;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) f[e] = quotient(f[e], scale, r);
+                    }
+                    if (d < D)
+                        *reinterpret_cast<uint2 *>((uint8_t *)dst + at) =
+                            make_uint2(fa_to_e4m3x2(f[0], f[1]) | fa_to_e4m3x2(f[2], f[3]) << 16,
+                                       fa_to_e4m3x2(f[4], f[5]) | fa_to_e4m3x2(f[6], f[7]) << 16);
+                    if (g == 0) (side ? a.c.v_scale : a.c.k_scale)[row[u]] = scale;
+                } else if (d < D) {
+                    if (FORMAT == FA_CACHE_F16) *reinterpret_cast<uint4 *>((__half *)dst + at) = fa_pack(f, __half());
+                    else *reinterpret_cast<uint4 *>((__nv_bfloat16 *)dst + at) = fa_pack(f, __nv_bfloat16());
+                }
+            }
+        }
+    }
+}
+
+template <class T, int G> void launch_write(const WriteArgs &a, unsigned blocks, int tokens, size_t smem, cudaStream_t s) {
+    if (a.format == FA_CACHE_E4M3) k_cache_write<T, G, FA_CACHE_E4M3><<<blocks, NT, smem, s>>>(a, tokens);
+    else if (a.format == FA_CACHE_F16) k_cache_write<T, G, FA_CACHE_F16><<<blocks, NT, smem, s>>>(a, tokens);
+    else k_cache_write<T, G, FA_CACHE_BF16><<<blocks, NT, smem, s>>>(a, tokens);
+}
+
+template <class T> fa_status launch_write(const WriteArgs &a, cudaStream_t s) {
+    const int H = a.c.kv_heads, D = a.c.head_dim;
+    const int64_t all = (int64_t)a.B * a.T;
+    const bool aligned = !(((uintptr_t)a.k | (uintptr_t)a.v) & 15) && !((a.kb | a.kt | a.kh | a.vb | a.vt | a.vh) % fa_vec<T>::N);
+    if (!aligned || a.rot % 8 || (!a.interleaved && a.rot % 16)) {
+        k_cache_write_any<T><<<(unsigned)((all * H + NT / 32 - 1) / (NT / 32)), NT, 0, s>>>(a);
+        return fa_launch_check("cache write");
+    }
+    const int G = D <= 64 ? 8 : D <= 128 ? 16 : 32;
+    // two steps of rows a block; fewer tokens where that leaves SMs without a block
+    int tokens = (int)std::min<int64_t>(16, std::max(1, 2 * 2 * (NT / G) / H));
+    tokens = (int)std::min<int64_t>(tokens, std::max<int64_t>(1, all / (152 * 8)));
+    const unsigned blocks = (unsigned)((all + tokens - 1) / tokens);
+    const size_t smem = (size_t)tokens * (a.rot / 2) * sizeof(float2);   // at most 16 * 128 * 8 bytes
+    if (G == 8) launch_write<T, 8>(a, blocks, tokens, smem, s);
+    else if (G == 16) launch_write<T, 16>(a, blocks, tokens, smem, s);
+    else launch_write<T, 32>(a, blocks, tokens, smem, s);
+    return fa_launch_check("cache write");
+}
+
+// Slots back as dense rows.  The bound is memory: codes in, twice or four times as many bytes out.
+// A thread takes 16 elements of a row, the keys' and the values', with four rows under way; the
+// lanes of a row write consecutive bytes.
+template <class T, int FORMAT>
+__global__ void __launch_bounds__(NT) k_cache_read(fa_cache_view c, int N, const int32_t *__restrict__ length, T *k_out, T *v_out) {
+    constexpr int U = 2, W = FORMAT == FA_CACHE_E4M3 ? 1 : 2;         // rows under way, 16-byte loads of 16 elements
+    const unsigned H = c.kv_heads, C = c.head_dim / 16, total = (unsigned)N * H * C;
+    const int b = blockIdx.y, n = __ldg(length + b);
+    const int64_t base = (int64_t)b * total;
+    for (unsigned first = blockIdx.x * (NT * U) + threadIdx.x; first < total; first += gridDim.x * NT * U) {
+        uint4 x[U][2][W];
+        float scale[U][2];
+        bool there[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const unsigned it = first + u * NT;
+            there[u] = false;
+            if (it >= total) continue;
+            const unsigned r = it / C, ch = it - r * C, t = r / H, h = r - t * H;
+            const int64_t row = (int)t < n ? c.row(b, t, (int)h) : -1;
+            if (row < 0) continue;
+            there[u] = true;
+#pragma unroll
+            for (int side = 0; side < 2; ++side) {
+                const uint4 *p = (const uint4 *)(side ? c.v : c.k) + (row * C + ch) * W;
+#pragma unroll
+                for (int i = 0; i < W; ++i) x[u][side][i] = __ldg(p + i);
+                if (FORMAT == FA_CACHE_E4M3) scale[u][side] = __ldg((side ? c.v_scale : c.k_scale) + row);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const unsigned it = first + u * NT;
+            if (it >= total) continue;
+#pragma unroll
+            for (int side = 0; side < 2; ++side) {
+                float f[16];
+                if (!there[u]) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) f[e] = 0.0f;
+                } else if (FORMAT == FA_CACHE_E4M3) {
+                    const uint32_t w[4] = {x[u][side][0].x, x[u][side][0].y, x[u][side][0].z, x[u][side][0].w};
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t two = fa_e4m3x2_to_half2(w[i / 2] >> (16 * (i & 1)));
+                        __half2 hh;
+                        memcpy(&hh, &two, 4);
+                        const float2 p = __half22float2(hh);
+                        f[2 * i] = p.x * scale[u][side];
+                        f[2 * i + 1] = p.y * scale[u][side];
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float p[8];
+                        if (FORMAT == FA_CACHE_F16) fa_unpack(x[u][side][i], p, __half());
+                        else fa_unpack(x[u][side][i], p, __nv_bfloat16());
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) f[8 * i + e] = p[e];
+                    }
+                }
+                uint4 *dst = reinterpret_cast<uint4 *>((side ? v_out : k_out) + (base + it) * 16);
+                constexpr int PER = fa_vec<T>::N;
+#pragma unroll
+                for (int i = 0; i < 16 / PER; ++i) {
+                    float p[PER];
+#pragma unroll
+                    for (int e = 0; e < PER; ++e) p[e] = f[PER * i + e];
+                    dst[i] = fa_pack(p, T());
+                }
+            }
+        }
     }
 }
 
@@ -182,8 +504,6 @@ __global__ void k_tree_mask(int T, const int32_t *__restrict__ parents, uint64_t
     }
 }
 
-unsigned blocks_for(int64_t items) { return (unsigned)std::max<int64_t>(1, std::min<int64_t>((items + NT - 1) / NT, 152 * 16)); }
-
 fa_status rope_args(const char *fn, int32_t head_dim, int32_t rot_dim, int32_t interleaved) {
     if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 2) return fa_refuse(fn, "rot_dim must be even and in [0, head_dim]");
     if (interleaved != 0 && interleaved != 1) return fa_refuse(fn, "interleaved must be 0 or 1");
@@ -204,17 +524,11 @@ extern "C" fa_status fa_rope(int32_t dtype, int64_t n_tokens, int32_t n_heads, i
     if (n_tokens == 0 || n_heads == 0) return FA_OK;
     if (!x || !out || (rot_dim > 0 && (!positions || !phase))) return fa_refuse(fn, "NULL buffer");
     cudaStream_t s = (cudaStream_t)stream;
-    const int64_t items = n_tokens * n_heads * (head_dim - rot_dim / 2);
-    auto go = [&](auto tag) {
-        using T = decltype(tag);
-        k_rope<T><<<blocks_for(items), NT, 0, s>>>(n_tokens, n_heads, head_dim, rot_dim, interleaved, inverse != 0,
-                                                   (const T *)x, x_token_stride, x_head_stride, positions, phase, mscale,
-                                                   (T *)out, out_token_stride, out_head_stride);
-    };
-    if (dtype == FA_DTYPE_F32) go(0.0f);
-    else if (dtype == FA_DTYPE_F16) go(__half());
-    else go(__nv_bfloat16());
-    return fa_launch_check("rope");
+    const RopeArgs a{n_tokens, x_token_stride, x_head_stride, out_token_stride, out_head_stride, n_heads, head_dim, rot_dim,
+                     interleaved, inverse != 0, x, out, positions, phase, mscale};
+    if (dtype == FA_DTYPE_F32) return launch_rope<float>(a, s);
+    if (dtype == FA_DTYPE_F16) return launch_rope<__half>(a, s);
+    return launch_rope<__nv_bfloat16>(a, s);
 }
 
 extern "C" fa_status fa_cache_write(const fa_kv_cache *cache, int32_t dtype, int32_t B, int32_t T, const void *k,
@@ -239,14 +553,11 @@ extern "C" fa_status fa_cache_write(const fa_kv_cache *cache, int32_t dtype, int
     a.vb = v_batch_stride; a.vt = v_token_stride; a.vh = v_head_stride;
     a.start = start; a.count = count; a.pos = positions; a.phase = phase;
     a.rot = positions ? rot_dim : 0; a.interleaved = interleaved; a.mscale = mscale;
-    const int64_t warps = (int64_t)B * T * cache->kv_heads;
-    if (warps > (int64_t)2147483647) return fa_refuse(fn, "B * T * kv_heads out of range");
-    const unsigned grid = (unsigned)((warps + NT / 32 - 1) / (NT / 32));
+    if ((int64_t)B * T * cache->kv_heads > (int64_t)2147483647) return fa_refuse(fn, "B * T * kv_heads out of range");
     cudaStream_t s = (cudaStream_t)stream;
-    if (dtype == FA_DTYPE_F32) k_cache_write<float><<<grid, NT, 0, s>>>(a);
-    else if (dtype == FA_DTYPE_F16) k_cache_write<__half><<<grid, NT, 0, s>>>(a);
-    else k_cache_write<__nv_bfloat16><<<grid, NT, 0, s>>>(a);
-    return fa_launch_check("cache write");
+    if (dtype == FA_DTYPE_F32) return launch_write<float>(a, s);
+    if (dtype == FA_DTYPE_F16) return launch_write<__half>(a, s);
+    return launch_write<__nv_bfloat16>(a, s);
 }
 
 extern "C" fa_status fa_cache_read(const fa_kv_cache *cache, int32_t dtype, int32_t B, int32_t N,
@@ -261,11 +572,16 @@ extern "C" fa_status fa_cache_read(const fa_kv_cache *cache, int32_t dtype, int3
     if (B == 0 || N == 0) return FA_OK;
     if (!length || !k_out || !v_out) return fa_refuse(fn, "NULL buffer");
     if (((uintptr_t)k_out | (uintptr_t)v_out) & 15) return fa_refuse(fn, "outputs must be 16-byte aligned");
-    const int64_t items = (int64_t)B * N * cache->kv_heads * cache->head_dim;
+    const int64_t items = (int64_t)N * cache->kv_heads * (cache->head_dim / 16);
+    if (B > 65535 || items > 2147483647 - 152 * 64 * 2 * NT) return fa_refuse(fn, "B or N * kv_heads * head_dim out of range");
+    const dim3 grid((unsigned)std::min<int64_t>((items + 2 * NT - 1) / (2 * NT), 152 * 64), (unsigned)B);
     cudaStream_t s = (cudaStream_t)stream;
     auto go = [&](auto tag) {
         using T = decltype(tag);
-        k_cache_read<T><<<blocks_for(items), NT, 0, s>>>(c, cache->format, B, N, length, (T *)k_out, (T *)v_out);
+        T *ko = (T *)k_out, *vo = (T *)v_out;
+        if (cache->format == FA_CACHE_E4M3) k_cache_read<T, FA_CACHE_E4M3><<<grid, NT, 0, s>>>(c, N, length, ko, vo);
+        else if (cache->format == FA_CACHE_F16) k_cache_read<T, FA_CACHE_F16><<<grid, NT, 0, s>>>(c, N, length, ko, vo);
+        else k_cache_read<T, FA_CACHE_BF16><<<grid, NT, 0, s>>>(c, N, length, ko, vo);
     };
     if (dtype == FA_DTYPE_F32) go(0.0f);
     else if (dtype == FA_DTYPE_F16) go(__half());
