@@ -58,8 +58,9 @@ __global__ void __launch_bounds__(NT) k_rope_any(RopeArgs a) {
 constexpr int ROPE_TOKENS = 8;
 template <class T, bool INTERLEAVED>
 __global__ void __launch_bounds__(NT) k_rope(RopeArgs a, int tokens) {
-    extern __shared__ float2 table[];          // [tokens][rot / 2]
-    constexpr int N = fa_vec<T>::N, U = 4;
+    // [tokens][pair of a vector][vector]: neighbouring lanes' pairs lie side by side
+    extern __shared__ float2 table[];
+    constexpr int N = fa_vec<T>::N, U = 4, P = INTERLEAVED ? N / 2 : N;
     const int half = a.rot / 2, tid = threadIdx.x;
     // a head's work items: rotated vectors (pairs of vectors), then the vectors that are copied
     const int turned = INTERLEAVED ? a.rot / N : half / N, items = turned + (a.dim - a.rot) / N, per_token = items * a.heads;
@@ -87,8 +88,8 @@ __global__ void __launch_bounds__(NT) k_rope(RopeArgs a, int tokens) {
         }
         if (!made) {
             for (int i = tid; i < here * half; i += NT) {
-                const int t = i / half;
-                table[i] = turn(__ldg(a.pos + n0 + t), __ldg(a.phase + i - t * half), a.mscale, a.inverse);
+                const int t = i / half, p = i - t * half;
+                table[t * half + p % P * (half / P) + p / P] = turn(__ldg(a.pos + n0 + t), __ldg(a.phase + p), a.mscale, a.inverse);
             }
             __syncthreads();
             made = true;
@@ -101,22 +102,22 @@ __global__ void __launch_bounds__(NT) k_rope(RopeArgs a, int tokens) {
             float x[N];
             fa_unpack(v[u], x, T());
             if (INTERLEAVED) {
-                const float2 *cs = table + tok[u] * half + at[u] * (N / 2);
+                const float2 *cs = table + tok[u] * half + at[u];
 #pragma unroll
                 for (int e = 0; e < N; e += 2) {
-                    const float2 f = cs[e / 2];
+                    const float2 f = cs[e / 2 * (half / P)];
                     const float p = x[e] * f.x - x[e + 1] * f.y;
                     x[e + 1] = x[e] * f.y + x[e + 1] * f.x;
                     x[e] = p;
                 }
                 *dst = fa_pack(x, T());
             } else {
-                const float2 *cs = table + tok[u] * half + at[u] * N;
+                const float2 *cs = table + tok[u] * half + at[u];
                 float y[N];
                 fa_unpack(w[u], y, T());
 #pragma unroll
                 for (int e = 0; e < N; ++e) {
-                    const float2 f = cs[e];
+                    const float2 f = cs[e * (half / P)];
                     const float p = x[e] * f.x - y[e] * f.y;
                     y[e] = x[e] * f.y + y[e] * f.x;
                     x[e] = p;
@@ -232,10 +233,11 @@ __device__ __forceinline__ float quotient(float x, float s, float r) {
 // the vectors of two rows' keys and values under way.
 template <class T, int G, int FORMAT>
 __global__ void __launch_bounds__(NT) k_cache_write(WriteArgs a, int tokens) {
-    extern __shared__ float2 table[];           // [tokens][rot / 2]
+    extern __shared__ float2 table[];           // [tokens][pair of a lane's eight elements][lane]
     constexpr int V = 8 / fa_vec<T>::N, ROWS = NT / G, U = 2;   // 16-byte loads of eight elements; rows in step
     const int H = a.c.kv_heads, D = a.c.head_dim, half = a.rot / 2;
     const int g = threadIdx.x % G, r0 = threadIdx.x / G, d = g * 8;
+    const int P = a.interleaved ? 4 : 8, lanes = half / P;      // pairs of a lane, lanes with pairs
     const unsigned all = (unsigned)a.B * (unsigned)a.T, n0 = blockIdx.x * (unsigned)tokens;   // below 2^31
     const int here = (int)min((unsigned)tokens, all - n0), total = here * H;
     const unsigned mask = G == 32 ? 0xffffffffu : ((1u << G) - 1) << (threadIdx.x % 32 / G * G);
@@ -267,8 +269,8 @@ __global__ void __launch_bounds__(NT) k_cache_write(WriteArgs a, int tokens) {
         }
         if (!made) {
             for (int i = threadIdx.x; i < here * half; i += NT) {
-                const int t = i / half;
-                table[i] = turn(__ldg(a.pos + n0 + t), __ldg(a.phase + i - t * half), a.mscale, false);
+                const int t = i / half, p = i - t * half;
+                table[t * half + p % P * lanes + p / P] = turn(__ldg(a.pos + n0 + t), __ldg(a.phase + p), a.mscale, false);
             }
             __syncthreads();
             made = true;
@@ -298,21 +300,24 @@ __global__ void __launch_bounds__(NT) k_cache_write(WriteArgs a, int tokens) {
                     for (int e = 0; e < 8; ++e) f[e] = 0.0f;
                 if (side == 0 && d < a.rot) {
                     if (a.interleaved) {
-                        const float2 *cs = table + tok[u] * half + d / 2;
+                        const float2 *cs = table + tok[u] * half + g;
 #pragma unroll
                         for (int e = 0; e < 8; e += 2) {
-                            const float2 t = cs[e / 2];
+                            const float2 t = cs[e / 2 * lanes];
                             const float p = f[e] * t.x - f[e + 1] * t.y;
                             f[e + 1] = f[e] * t.y + f[e + 1] * t.x;
                             f[e] = p;
                         }
                     } else {
                         const bool second = d >= half;
-                        const float2 *cs = table + tok[u] * half + (second ? d - half : d);
+                        const float2 *cs = table + tok[u] * half + (second ? g - lanes : g);
                         float y[8];
                         get(m[u], y);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) f[e] = second ? y[e] * cs[e].y + f[e] * cs[e].x : f[e] * cs[e].x - y[e] * cs[e].y;
+                        for (int e = 0; e < 8; ++e) {
+                            const float2 t = cs[e * lanes];
+                            f[e] = second ? y[e] * t.y + f[e] * t.x : f[e] * t.x - y[e] * t.y;
+                        }
                     }
                 }
                 const int64_t at = row[u] * D + d;
