@@ -24,6 +24,9 @@ __device__ __forceinline__ key_t64 cell_key(float v, uint32_t flat) {
     const uint32_t ord = (u >> 31) ? ~u : (u | 0x80000000u);
     return ((key_t64)ord << 32) | (0xffffffffu - flat);
 }
+__device__ __forceinline__ float key_value(key_t64 k);
+// the value below which no cell passes a threshold
+__device__ __forceinline__ float passing(key_t64 threshold) { return threshold ? key_value(threshold) : -INFINITY; }
 __device__ __forceinline__ float key_value(key_t64 k) {
     const uint32_t ord = (uint32_t)(k >> 32);
     return __uint_as_float((ord >> 31) ? (ord & 0x7fffffffu) : ~ord);
@@ -37,10 +40,11 @@ struct BestShared {
     int count;
 };
 
-// Offer every thread's n keys get(0 .. n) (0 = no cell).  Called by all threads of the block;
-// list has room for top + n * top keys, and work for as many.
+// Offer the threads' keys: best is a thread's largest (0 where none can pass) and push(t, put) calls
+// put for each of its keys above t.  Called by all threads of the block; list has room for
+// top keys and those of top threads.
 template <class F>
-__device__ __forceinline__ void offer(BestShared &sh, key_t64 *list, key_t64 *work, int top, int n, key_t64 best, F get) {
+__device__ __forceinline__ void offer(BestShared &sh, key_t64 *list, key_t64 *work, int top, key_t64 best, F push) {
     const int tid = threadIdx.x;
     key_t64 thr = sh.threshold;
     const int above = __syncthreads_count(best > thr);
@@ -54,11 +58,7 @@ __device__ __forceinline__ void offer(BestShared &sh, key_t64 *list, key_t64 *wo
         __syncthreads();
         thr = sh.threshold;
     }
-    if (best > thr)
-        for (int i = 0; i < n; ++i) {
-            const key_t64 k = get(i);
-            if (k > thr) list[atomicAdd(&sh.count, 1)] = k;
-        }
+    if (best > thr) push(thr, [&](key_t64 k) { list[atomicAdd(&sh.count, 1)] = k; });
     __syncthreads();
     const int m = sh.count;
     if (m >= top) {
@@ -88,6 +88,41 @@ struct SelectArgs {
     float *out_score;
     int32_t *out_parent, *out_token, *out_state;
 };
+
+// The larger of two vectors' elements, pairwise in the 16-bit types; a NaN loses.
+__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b, __half) {
+    uint32_t r;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b, __nv_bfloat16) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// the largest element of a vector whose bit in m is set (-inf or NaN: none)
+__device__ __forceinline__ float top_of(uint4 r, uint32_t m, float) {
+    float t = -INFINITY;
+    const float f[4] = {__uint_as_float(r.x), __uint_as_float(r.y), __uint_as_float(r.z), __uint_as_float(r.w)};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) t = (m >> e & 1) ? fmaxf(t, f[e]) : t;
+    return t;
+}
+template <class T> __device__ __forceinline__ float top_of(uint4 r, uint32_t m, T) {
+    constexpr uint32_t low = std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;   // -inf, twice
+    uint32_t w[4] = {r.x, r.y, r.z, r.w};
+    if (m != 0xffu) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t keep = ((m >> (2 * i) & 1) ? 0x0000ffffu : 0u) | ((m >> (2 * i + 1) & 1) ? 0xffff0000u : 0u);
+            w[i] = (w[i] & keep) | (low & ~keep);
+        }
+    }
+    const uint32_t t = max_pair(max_pair(w[0], w[1], T()), max_pair(w[2], w[3], T()), T());
+    float f[8];
+    fa_unpack(make_uint4(t, t, t, t), f, T());
+    return fmaxf(f[0], f[1]);
+}
 
 // the live bits of W consecutive tokens from v0 on (v0 may be negative or near the row's end)
 template <int W>
@@ -159,7 +194,7 @@ __global__ void __launch_bounds__(NT) k_beam_scan(SelectArgs a) {
             const int v0 = first + (i * NT + tid) * VEC - mis;
             constexpr uint32_t all = VEC == 32 ? 0xffffffffu : (1u << VEC) - 1;
             uint32_t m = v0 < a.V && v0 > -VEC ? all : 0u;
-            if (m && lrow) m &= live_bits<VEC>(lrow, a.words, v0);
+            if (m && lrow) m &= mis ? live_bits<VEC>(lrow, a.words, v0) : __ldg((const uint8_t *)lrow + (v0 >> 3)) >> (v0 & 7);
             if (m && v0 < 0) m &= all << -v0;
             if (m && v0 + VEC > a.V) m &= all >> (v0 + VEC - a.V);
             bits[i] = m;
@@ -177,40 +212,40 @@ __global__ void __launch_bounds__(NT) k_beam_scan(SelectArgs a) {
                 raw[i] = fa_pack(f, T());
             }
         }
-        float top_value = -INFINITY;
-        key_t64 best = 0;
+        // the thread's largest value: the addition is monotone, so it is the score plus the largest cell
+        float most = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (bits[i]) most = fmaxf(most, top_of(raw[i], bits[i], T()));
+        const float top_value = score + most;
         auto cell = [&](int i, int e, float x) -> key_t64 {
-            const float v = score + x;
-            if (!(bits[i] >> e & 1) || !(v > -INFINITY)) return 0;
-            return cell_key(v, (uint32_t)(k * a.V + first + (i * NT + tid) * VEC - mis + e));
+            return cell_key(score + x, (uint32_t)(k * a.V + first + (i * NT + tid) * VEC - mis + e));
         };
+        // its key, where it can pass (after the first batches it hardly ever can)
+        key_t64 best = 0;
+        auto each = [&](auto f) {                            // the cells with a live bit, in their order
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            float f[VEC];
-            fa_unpack(raw[i], f, T());
+            for (int i = 0; i < NV; ++i) {
+                float x[VEC];
+                fa_unpack(raw[i], x, T());
 #pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                if ((bits[i] >> e & 1) && score + f[e] > top_value) {   // a thread's cells come in ascending order
-                    top_value = score + f[e];
-                    best = cell(i, e, f[e]);
+                for (int e = 0; e < VEC; ++e)
+                    if (bits[i] >> e & 1) f(i, e, x[e]);
+            }
+        };
+        if (most > -INFINITY && top_value > -INFINITY && !(top_value < passing(sh.threshold)))
+            each([&](int i, int e, float x) {
+                if (score + x == top_value && !best) best = cell(i, e, x);   // the lowest index of equals
+            });
+        offer(sh, list, work, a.top, best, [&](key_t64 thr, auto put) {
+            const float least = passing(thr);
+            each([&](int i, int e, float x) {
+                const float v = score + x;
+                if (v >= least && v > -INFINITY) {
+                    const key_t64 key = cell(i, e, x);
+                    if (key > thr) put(key);
                 }
-        }
-        offer(sh, list, work, a.top, PER, best, [&](int q) -> key_t64 {
-            const int i = q / VEC, e = q % VEC;
-            uint4 r = raw[0];
-            uint32_t m = bits[0];
-#pragma unroll
-            for (int j = 1; j < NV; ++j)
-                if (i == j) { r = raw[j]; m = bits[j]; }
-            float f[VEC];
-            fa_unpack(r, f, T());
-            float x = f[0];
-#pragma unroll
-            for (int j = 1; j < VEC; ++j)
-                if (e == j) x = f[j];
-            const float v = score + x;
-            if (!(m >> e & 1) || !(v > -INFINITY)) return 0;
-            return cell_key(v, (uint32_t)(k * a.V + first + (i * NT + tid) * VEC - mis + e));
+            });
         });
     }
     finish(a, sh, list, work, n, gridDim.x == 1);
@@ -234,7 +269,11 @@ __global__ void __launch_bounds__(NT) k_beam_merge(SelectArgs a) {
             k[i] = at < total ? keys[at] : 0;
             best = max(best, k[i]);
         }
-        offer(sh, list, work, a.top, 4, best, [&](int q) { return q == 0 ? k[0] : q == 1 ? k[1] : q == 2 ? k[2] : k[3]; });
+        offer(sh, list, work, a.top, best, [&](key_t64 thr, auto put) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (k[i] > thr) put(k[i]);
+        });
     }
     finish(a, sh, list, work, n, true);
 }

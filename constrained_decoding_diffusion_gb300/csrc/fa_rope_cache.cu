@@ -52,9 +52,10 @@ __global__ void __launch_bounds__(NT) k_rope_any(RopeArgs a) {
 
 // The same in 16-byte vectors of N elements, where every row is aligned and the rotated part is
 // whole vectors (half layout: each half).  The bound is memory: x is read and out written
-// once.  A block takes a few tokens with all their heads: their sines and cosines, one per token
-// and pair, are made once in shared memory while the first vectors are on their way, and four
-// vectors (half layout: vector pairs) a thread are under way at a time.
+// once.  A block takes up to eight tokens with all their heads.  Their sines and cosines, one per
+// token and pair, are made once in shared memory while the first vectors are on their way; a
+// thread keeps its place (head and vector) and walks the tokens, four of them under way at a time,
+// so the arithmetic of places is done once.
 constexpr int ROPE_TOKENS = 8;
 template <class T, bool INTERLEAVED>
 __global__ void __launch_bounds__(NT) k_rope(RopeArgs a, int tokens) {
@@ -65,65 +66,61 @@ __global__ void __launch_bounds__(NT) k_rope(RopeArgs a, int tokens) {
     // a head's work items: rotated vectors (pairs of vectors), then the vectors that are copied
     const int turned = INTERLEAVED ? a.rot / N : half / N, items = turned + (a.dim - a.rot) / N, per_token = items * a.heads;
     const int64_t n0 = (int64_t)blockIdx.x * tokens;
-    const int here = (int)min((int64_t)tokens, a.n_tokens - n0), total = here * per_token;
+    const int here = (int)min((int64_t)tokens, a.n_tokens - n0), step = half / P;
     bool made = false;
-    for (int first = tid; first < total || !made; first += U * NT) {
-        uint4 v[U], w[U];
-        int at[U], tok[U];
-        const T *src[U];
-        int64_t off[U];
+    for (int it = tid; it < per_token || !made; it += NT) {
+        const int h = it / items, i = it - h * items, col = i < turned ? i * N : a.rot + (i - turned) * N;
+        const bool mine = it < per_token, pairs = !INTERLEAVED && i < turned;
+        const T *src = (const T *)a.x + n0 * a.xt + h * a.xh + col;
+        T *dst = (T *)a.out + n0 * a.ot + h * a.oh + col;
+        for (int t0 = 0; t0 < here; t0 += U) {
+            uint4 v[U], w[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int it = first + u * NT;
-            at[u] = -1;
-            if (it >= total) continue;
-            tok[u] = it / per_token;
-            const int rest = it - tok[u] * per_token, h = rest / items, i = rest - h * items;
-            at[u] = i;
-            const int col = i < turned ? i * N : a.rot + (i - turned) * N;
-            src[u] = (const T *)a.x + (n0 + tok[u]) * a.xt + h * a.xh + col;
-            off[u] = (n0 + tok[u]) * a.ot + h * a.oh + col;
-            v[u] = *reinterpret_cast<const uint4 *>(src[u]);   // (not the read-only path: out may be x)
-            if (!INTERLEAVED && i < turned) w[u] = *reinterpret_cast<const uint4 *>(src[u] + half);
-        }
-        if (!made) {
-            for (int i = tid; i < here * half; i += NT) {
-                const int t = i / half, p = i - t * half;
-                table[t * half + p % P * (half / P) + p / P] = turn(__ldg(a.pos + n0 + t), __ldg(a.phase + p), a.mscale, a.inverse);
+            for (int u = 0; u < U; ++u) {
+                if (!mine || t0 + u >= here) continue;
+                // (not the read-only path: out may be x)
+                v[u] = *reinterpret_cast<const uint4 *>(src + (t0 + u) * a.xt);
+                if (pairs) w[u] = *reinterpret_cast<const uint4 *>(src + (t0 + u) * a.xt + half);
             }
-            __syncthreads();
-            made = true;
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (at[u] < 0) continue;
-            uint4 *dst = reinterpret_cast<uint4 *>((T *)a.out + off[u]);
-            if (at[u] >= turned) { *dst = v[u]; continue; }
-            float x[N];
-            fa_unpack(v[u], x, T());
-            if (INTERLEAVED) {
-                const float2 *cs = table + tok[u] * half + at[u];
-#pragma unroll
-                for (int e = 0; e < N; e += 2) {
-                    const float2 f = cs[e / 2 * (half / P)];
-                    const float p = x[e] * f.x - x[e + 1] * f.y;
-                    x[e + 1] = x[e] * f.y + x[e + 1] * f.x;
-                    x[e] = p;
+            if (!made) {
+                for (int j = tid; j < here * half; j += NT) {
+                    const int t = j / half, p = j - t * half;
+                    table[t * half + p % P * step + p / P] = turn(__ldg(a.pos + n0 + t), __ldg(a.phase + p), a.mscale, a.inverse);
                 }
-                *dst = fa_pack(x, T());
-            } else {
-                const float2 *cs = table + tok[u] * half + at[u];
-                float y[N];
-                fa_unpack(w[u], y, T());
+                __syncthreads();
+                made = true;
+            }
+            if (!mine) continue;
 #pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    const float2 f = cs[e * (half / P)];
-                    const float p = x[e] * f.x - y[e] * f.y;
-                    y[e] = x[e] * f.y + y[e] * f.x;
-                    x[e] = p;
+            for (int u = 0; u < U; ++u) {
+                if (t0 + u >= here) break;
+                uint4 *to = reinterpret_cast<uint4 *>(dst + (t0 + u) * a.ot);
+                if (i >= turned) { *to = v[u]; continue; }
+                const float2 *cs = table + (t0 + u) * half + i;
+                float x[N];
+                fa_unpack(v[u], x, T());
+                if (INTERLEAVED) {
+#pragma unroll
+                    for (int e = 0; e < N; e += 2) {
+                        const float2 f = cs[e / 2 * step];
+                        const float p = x[e] * f.x - x[e + 1] * f.y;
+                        x[e + 1] = x[e] * f.y + x[e + 1] * f.x;
+                        x[e] = p;
+                    }
+                    *to = fa_pack(x, T());
+                } else {
+                    float y[N];
+                    fa_unpack(w[u], y, T());
+#pragma unroll
+                    for (int e = 0; e < N; ++e) {
+                        const float2 f = cs[e * step];
+                        const float p = x[e] * f.x - y[e] * f.y;
+                        y[e] = x[e] * f.y + y[e] * f.x;
+                        x[e] = p;
+                    }
+                    *to = fa_pack(x, T());
+                    *reinterpret_cast<uint4 *>(dst + (t0 + u) * a.ot + half) = fa_pack(y, T());
                 }
-                *dst = fa_pack(x, T());
-                *reinterpret_cast<uint4 *>((T *)a.out + off[u] + half) = fa_pack(y, T());
             }
         }
     }
@@ -139,9 +136,8 @@ template <class T> fa_status launch_rope(const RopeArgs &a, cudaStream_t s) {
         k_rope_any<T><<<blocks_for(items), NT, 0, s>>>(a);
         return fa_launch_check("rope");
     }
-    // about two rounds of vectors a block; fewer tokens where that leaves SMs without a block
-    int tokens = (int)std::min<int64_t>(ROPE_TOKENS, std::max<int64_t>(1, 2 * 4 * NT / std::max<int64_t>(per_token, 1)));
-    tokens = (int)std::min<int64_t>(tokens, std::max<int64_t>(1, a.n_tokens / (152 * 4)));
+    // fewer tokens where that leaves SMs without a block
+    const int tokens = (int)std::min<int64_t>(ROPE_TOKENS, std::max<int64_t>(1, a.n_tokens / (152 * 4)));
     const int64_t blocks = (a.n_tokens + tokens - 1) / tokens;
     if (blocks > 2147483647) return fa_refuse("fa_rope", "too many tokens");
     const size_t smem = (size_t)tokens * (a.rot / 2) * sizeof(float2);   // at most 8 * 512 * 8 bytes
@@ -225,19 +221,46 @@ __device__ __forceinline__ float quotient(float x, float s, float r) {
     return fmaf(fmaf(-q, s, x), r, q);
 }
 
-// The same in vectors of eight elements: a group of G = 8, 16 or 32 lanes holds a row, a lane eight
-// of its elements, and each row is read once (a rotated half layout reads a lane's mates too, from
-// the lines its neighbours load).  The bound is memory: keys and values in, codes and scales out;
-// sines and cosines are made once per token in shared memory, and the division by the scale is a
-// multiplication with a correction.  A block takes a few tokens with all their heads; a thread has
-// the vectors of two rows' keys and values under way.
+// the larger magnitude, or NaN if either is one
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// four elements in memory (8 bytes of 16-bit types, 16 bytes of fp32)
+__device__ __forceinline__ void load4(const float *p, uint4 &r) { r = __ldg(reinterpret_cast<const uint4 *>(p)); }
+template <class T> __device__ __forceinline__ void load4(const T *p, uint2 &r) { r = __ldg(reinterpret_cast<const uint2 *>(p)); }
+__device__ __forceinline__ void floats4(uint4 r, float *f, float) {
+    f[0] = __uint_as_float(r.x); f[1] = __uint_as_float(r.y); f[2] = __uint_as_float(r.z); f[3] = __uint_as_float(r.w);
+}
+__device__ __forceinline__ void floats4(uint2 r, float *f, __nv_bfloat16) {
+    f[0] = __uint_as_float(r.x << 16); f[1] = __uint_as_float(r.x & 0xffff0000u);
+    f[2] = __uint_as_float(r.y << 16); f[3] = __uint_as_float(r.y & 0xffff0000u);
+}
+__device__ __forceinline__ void floats4(uint2 r, float *f, __half) {
+    __half2 h[2];
+    memcpy(h, &r, 8);
+    const float2 a = __half22float2(h[0]), b = __half22float2(h[1]);
+    f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
+}
+
+// The same in vectors: a group of G = 8, 16 or 32 lanes holds a row, a lane eight of its elements as
+// two pieces of four, and each row is read once.  In the half layout the pieces of a rotated lane are
+// four elements of the first half and their mates of the second, so every pair meets in a lane.
+// The bound is memory (keys and values in, codes and scales out) and, close to it, the issue of
+// instructions: sines and cosines are made once per token in shared memory, the division by the scale
+// is a multiplication with a correction, a maximum that keeps NaN finds the rows to mark.  A block
+// takes a few tokens with all their heads; a thread has two rows' keys and values under way.
 template <class T, int G, int FORMAT>
 __global__ void __launch_bounds__(NT) k_cache_write(WriteArgs a, int tokens) {
-    extern __shared__ float2 table[];           // [tokens][pair of a lane's eight elements][lane]
-    constexpr int V = 8 / fa_vec<T>::N, ROWS = NT / G, U = 2;   // 16-byte loads of eight elements; rows in step
-    const int H = a.c.kv_heads, D = a.c.head_dim, half = a.rot / 2;
-    const int g = threadIdx.x % G, r0 = threadIdx.x / G, d = g * 8;
-    const int P = a.interleaved ? 4 : 8, lanes = half / P;      // pairs of a lane, lanes with pairs
+    extern __shared__ float2 table[];           // [tokens][pair of a lane's four][lane]
+    typedef typename std::conditional<sizeof(T) == 4, uint4, uint2>::type Raw;
+    constexpr int ROWS = NT / G, U = 2;         // rows in step, rows of a thread under way
+    const int H = a.c.kv_heads, D = a.c.head_dim, half = a.rot / 2, lanes = half / 4;   // lanes with pairs
+    const int g = threadIdx.x % G, r0 = threadIdx.x / G;
+    const bool in = g * 8 < D, turned = g < lanes, split = turned && !a.interleaved;
+    const int v0 = g * 8, k0 = split ? g * 4 : v0, k1 = split ? half + g * 4 : v0 + 4;   // the pieces
     const unsigned all = (unsigned)a.B * (unsigned)a.T, n0 = blockIdx.x * (unsigned)tokens;   // below 2^31
     const int here = (int)min((unsigned)tokens, all - n0), total = here * H;
     const unsigned mask = G == 32 ? 0xffffffffu : ((1u << G) - 1) << (threadIdx.x % 32 / G * G);
@@ -245,7 +268,7 @@ __global__ void __launch_bounds__(NT) k_cache_write(WriteArgs a, int tokens) {
     for (int first = r0; first - r0 < total; first += U * ROWS) {
         int64_t row[U];
         int tok[U];
-        uint4 x[U][2][V], m[U][V];               // keys, values; the keys' mates in the half layout
+        Raw x[U][4];                            // the key's pieces, the value's
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int it = first + u * ROWS;
@@ -257,20 +280,18 @@ __global__ void __launch_bounds__(NT) k_cache_write(WriteArgs a, int tokens) {
             const int t = (int)(bt - b * (unsigned)a.T);
             if (a.count && t >= __ldg(a.count + b)) continue;
             row[u] = a.c.row((int)b, (int64_t)__ldg(a.start + b) + t, h);
-            if (row[u] < 0 || d >= D) continue;
-            const T *k = (const T *)a.k + b * a.kb + t * a.kt + h * a.kh + d;
-            const T *v = (const T *)a.v + b * a.vb + t * a.vt + h * a.vh + d;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                x[u][0][i] = __ldg(reinterpret_cast<const uint4 *>(k) + i);
-                x[u][1][i] = __ldg(reinterpret_cast<const uint4 *>(v) + i);
-                if (!a.interleaved && d < a.rot) m[u][i] = __ldg(reinterpret_cast<const uint4 *>(d < half ? k + half : k - half) + i);
-            }
+            if (row[u] < 0 || !in) continue;
+            const T *k = (const T *)a.k + (int)b * a.kb + t * a.kt + h * a.kh;
+            const T *v = (const T *)a.v + (int)b * a.vb + t * a.vt + h * a.vh + v0;
+            load4(k + k0, x[u][0]);
+            load4(k + k1, x[u][1]);
+            load4(v, x[u][2]);
+            load4(v + 4, x[u][3]);
         }
         if (!made) {
             for (int i = threadIdx.x; i < here * half; i += NT) {
                 const int t = i / half, p = i - t * half;
-                table[t * half + p % P * lanes + p / P] = turn(__ldg(a.pos + n0 + t), __ldg(a.phase + p), a.mscale, false);
+                table[t * half + p % 4 * lanes + p / 4] = turn(__ldg(a.pos + n0 + t), __ldg(a.phase + p), a.mscale, false);
             }
             __syncthreads();
             made = true;
@@ -280,59 +301,38 @@ __global__ void __launch_bounds__(NT) k_cache_write(WriteArgs a, int tokens) {
             if (row[u] < 0) continue;            // the same for a row's whole group
 #pragma unroll
             for (int side = 0; side < 2; ++side) {
-                float f[8], amax = 0.0f;
-                auto get = [&](const uint4 (&w)[V], float (&y)[8]) {
-                    if constexpr (V == 1) {
-                        fa_unpack(w[0], y, T());
-                    } else {
-                        float p[4];
-#pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            fa_unpack(w[i], p, 0.0f);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) y[4 * i + j] = p[j];
-                        }
-                    }
-                };
-                if (d < D) get(x[u][side], f);
-                else
+                float f[8];
+                if (in) {
+                    floats4(x[u][2 * side], f, T());
+                    floats4(x[u][2 * side + 1], f + 4, T());
+                } else {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) f[e] = 0.0f;
-                if (side == 0 && d < a.rot) {
-                    if (a.interleaved) {
-                        const float2 *cs = table + tok[u] * half + g;
+                }
+                if (side == 0 && turned) {
+                    const float2 *cs = table + tok[u] * half + g;
 #pragma unroll
-                        for (int e = 0; e < 8; e += 2) {
-                            const float2 t = cs[e / 2 * lanes];
-                            const float p = f[e] * t.x - f[e + 1] * t.y;
-                            f[e + 1] = f[e] * t.y + f[e + 1] * t.x;
-                            f[e] = p;
-                        }
-                    } else {
-                        const bool second = d >= half;
-                        const float2 *cs = table + tok[u] * half + (second ? g - lanes : g);
-                        float y[8];
-                        get(m[u], y);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float2 t = cs[e * lanes];
-                            f[e] = second ? y[e] * t.y + f[e] * t.x : f[e] * t.x - y[e] * t.y;
-                        }
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 t = cs[e * lanes];
+                        auto turn_pair = [&](float &p, float &q) {
+                            const float y = p * t.x - q * t.y;
+                            q = p * t.y + q * t.x;
+                            p = y;
+                        };
+                        if (a.interleaved) turn_pair(f[2 * e], f[2 * e + 1]);
+                        else turn_pair(f[e], f[e + 4]);
                     }
                 }
-                const int64_t at = row[u] * D + d;
+                const int64_t at = row[u] * D;
+                const int p0 = side ? v0 : k0, p1 = side ? v0 + 4 : k1;
                 void *dst = side ? a.c.v : a.c.k;
                 if (FORMAT == FA_CACHE_E4M3) {
-                    bool odd = false;
+                    float amax = 0.0f;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        amax = fmaxf(amax, fabsf(f[e]));
-                        odd |= !(fabsf(f[e]) < INFINITY);
-                    }
-                    if (odd) amax = INFINITY;
+                    for (int e = 0; e < 8; ++e) amax = max_nan(amax, fabsf(f[e]));
 #pragma unroll
-                    for (int o = G / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(mask, amax, o));
-                    odd = !(amax < INFINITY);
+                    for (int o = G / 2; o; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(mask, amax, o));
+                    const bool odd = !(amax < INFINITY);
                     const float scale = odd ? __int_as_float(0x7fffffff) : amax / FA_E4M3_MAX;
                     if (odd || amax < 1e-30f) {
                         // a row of zeros or one that is marked; tiny values take the plain division
@@ -343,14 +343,15 @@ __global__ void __launch_bounds__(NT) k_cache_write(WriteArgs a, int tokens) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e) f[e] = quotient(f[e], scale, r);
                     }
-                    if (d < D)
-                        *reinterpret_cast<uint2 *>((uint8_t *)dst + at) =
-                            make_uint2(fa_to_e4m3x2(f[0], f[1]) | fa_to_e4m3x2(f[2], f[3]) << 16,
-                                       fa_to_e4m3x2(f[4], f[5]) | fa_to_e4m3x2(f[6], f[7]) << 16);
+                    if (in) {
+                        *reinterpret_cast<uint32_t *>((uint8_t *)dst + at + p0) = fa_to_e4m3x2(f[0], f[1]) | fa_to_e4m3x2(f[2], f[3]) << 16;
+                        *reinterpret_cast<uint32_t *>((uint8_t *)dst + at + p1) = fa_to_e4m3x2(f[4], f[5]) | fa_to_e4m3x2(f[6], f[7]) << 16;
+                    }
                     if (g == 0) (side ? a.c.v_scale : a.c.k_scale)[row[u]] = scale;
-                } else if (d < D) {
-                    if (FORMAT == FA_CACHE_F16) *reinterpret_cast<uint4 *>((__half *)dst + at) = fa_pack(f, __half());
-                    else *reinterpret_cast<uint4 *>((__nv_bfloat16 *)dst + at) = fa_pack(f, __nv_bfloat16());
+                } else if (in) {
+                    typedef typename std::conditional<FORMAT == FA_CACHE_F16, __half, __nv_bfloat16>::type O;
+                    *reinterpret_cast<uint2 *>((O *)dst + at + p0) = make_uint2(fa_pack2(f[0], f[1], O()), fa_pack2(f[2], f[3], O()));
+                    *reinterpret_cast<uint2 *>((O *)dst + at + p1) = make_uint2(fa_pack2(f[4], f[5], O()), fa_pack2(f[6], f[7], O()));
                 }
             }
         }
@@ -367,7 +368,7 @@ template <class T> fa_status launch_write(const WriteArgs &a, cudaStream_t s) {
     const int H = a.c.kv_heads, D = a.c.head_dim;
     const int64_t all = (int64_t)a.B * a.T;
     const bool aligned = !(((uintptr_t)a.k | (uintptr_t)a.v) & 15) && !((a.kb | a.kt | a.kh | a.vb | a.vt | a.vh) % fa_vec<T>::N);
-    if (!aligned || a.rot % 8 || (!a.interleaved && a.rot % 16)) {
+    if (!aligned || a.rot % 8) {
         k_cache_write_any<T><<<(unsigned)((all * H + NT / 32 - 1) / (NT / 32)), NT, 0, s>>>(a);
         return fa_launch_check("cache write");
     }
@@ -384,16 +385,17 @@ template <class T> fa_status launch_write(const WriteArgs &a, cudaStream_t s) {
 }
 
 // Slots back as dense rows.  The bound is memory: codes in, twice or four times as many bytes out.
-// A thread takes 16 elements of a row, the keys' and the values', with four rows under way; the
-// lanes of a row write consecutive bytes.
+// A thread takes eight elements of a row, the keys' and the values', with two rows under way (four
+// cost more in occupancy than they hide); a warp's loads and stores are contiguous.
 template <class T, int FORMAT>
 __global__ void __launch_bounds__(NT) k_cache_read(fa_cache_view c, int N, const int32_t *__restrict__ length, T *k_out, T *v_out) {
-    constexpr int U = 2, W = FORMAT == FA_CACHE_E4M3 ? 1 : 2;         // rows under way, 16-byte loads of 16 elements
-    const unsigned H = c.kv_heads, C = c.head_dim / 16, total = (unsigned)N * H * C;
+    constexpr int U = 2;
+    typedef typename std::conditional<FORMAT == FA_CACHE_E4M3, uint2, uint4>::type Raw;   // eight elements
+    const unsigned H = c.kv_heads, C = c.head_dim / 8, total = (unsigned)N * H * C;
     const int b = blockIdx.y, n = __ldg(length + b);
     const int64_t base = (int64_t)b * total;
     for (unsigned first = blockIdx.x * (NT * U) + threadIdx.x; first < total; first += gridDim.x * NT * U) {
-        uint4 x[U][2][W];
+        Raw x[U][2];
         float scale[U][2];
         bool there[U];
 #pragma unroll
@@ -407,9 +409,7 @@ __global__ void __launch_bounds__(NT) k_cache_read(fa_cache_view c, int N, const
             there[u] = true;
 #pragma unroll
             for (int side = 0; side < 2; ++side) {
-                const uint4 *p = (const uint4 *)(side ? c.v : c.k) + (row * C + ch) * W;
-#pragma unroll
-                for (int i = 0; i < W; ++i) x[u][side][i] = __ldg(p + i);
+                x[u][side] = __ldg((const Raw *)(side ? c.v : c.k) + row * C + ch);
                 if (FORMAT == FA_CACHE_E4M3) scale[u][side] = __ldg((side ? c.v_scale : c.k_scale) + row);
             }
         }
@@ -419,14 +419,14 @@ __global__ void __launch_bounds__(NT) k_cache_read(fa_cache_view c, int N, const
             if (it >= total) continue;
 #pragma unroll
             for (int side = 0; side < 2; ++side) {
-                float f[16];
+                float f[8];
                 if (!there[u]) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) f[e] = 0.0f;
-                } else if (FORMAT == FA_CACHE_E4M3) {
-                    const uint32_t w[4] = {x[u][side][0].x, x[u][side][0].y, x[u][side][0].z, x[u][side][0].w};
+                    for (int e = 0; e < 8; ++e) f[e] = 0.0f;
+                } else if constexpr (FORMAT == FA_CACHE_E4M3) {
+                    const uint32_t w[2] = {x[u][side].x, x[u][side].y};
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
+                    for (int i = 0; i < 4; ++i) {
                         const uint32_t two = fa_e4m3x2_to_half2(w[i / 2] >> (16 * (i & 1)));
                         __half2 hh;
                         memcpy(&hh, &two, 4);
@@ -434,20 +434,15 @@ __global__ void __launch_bounds__(NT) k_cache_read(fa_cache_view c, int N, const
                         f[2 * i] = p.x * scale[u][side];
                         f[2 * i + 1] = p.y * scale[u][side];
                     }
+                } else if constexpr (FORMAT == FA_CACHE_F16) {
+                    fa_unpack(x[u][side], f, __half());
                 } else {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float p[8];
-                        if (FORMAT == FA_CACHE_F16) fa_unpack(x[u][side][i], p, __half());
-                        else fa_unpack(x[u][side][i], p, __nv_bfloat16());
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) f[8 * i + e] = p[e];
-                    }
+                    fa_unpack(x[u][side], f, __nv_bfloat16());
                 }
-                uint4 *dst = reinterpret_cast<uint4 *>((side ? v_out : k_out) + (base + it) * 16);
+                uint4 *dst = reinterpret_cast<uint4 *>((side ? v_out : k_out) + (base + it) * 8);
                 constexpr int PER = fa_vec<T>::N;
 #pragma unroll
-                for (int i = 0; i < 16 / PER; ++i) {
+                for (int i = 0; i < 8 / PER; ++i) {
                     float p[PER];
 #pragma unroll
                     for (int e = 0; e < PER; ++e) p[e] = f[PER * i + e];
@@ -577,7 +572,7 @@ extern "C" fa_status fa_cache_read(const fa_kv_cache *cache, int32_t dtype, int3
     if (B == 0 || N == 0) return FA_OK;
     if (!length || !k_out || !v_out) return fa_refuse(fn, "NULL buffer");
     if (((uintptr_t)k_out | (uintptr_t)v_out) & 15) return fa_refuse(fn, "outputs must be 16-byte aligned");
-    const int64_t items = (int64_t)N * cache->kv_heads * (cache->head_dim / 16);
+    const int64_t items = (int64_t)N * cache->kv_heads * (cache->head_dim / 8);
     if (B > 65535 || items > 2147483647 - 152 * 64 * 2 * NT) return fa_refuse(fn, "B or N * kv_heads * head_dim out of range");
     const dim3 grid((unsigned)std::min<int64_t>((items + 2 * NT - 1) / (2 * NT), 152 * 64), (unsigned)B);
     cudaStream_t s = (cudaStream_t)stream;
