@@ -252,9 +252,11 @@ __device__ __forceinline__ void floats4(uint2 r, float *f, __half) {
 // instructions: sines and cosines are made once per token in shared memory, the division by the scale
 // is a multiplication with a correction, a maximum that keeps NaN finds the rows to mark.  A block
 // takes a few tokens with all their heads; a thread has two rows' keys and values under way.
+constexpr int WRITE_TOKENS = 16;
 template <class T, int G, int FORMAT>
 __global__ void __launch_bounds__(NT) k_cache_write(WriteArgs a, int tokens) {
     extern __shared__ float2 table[];           // [tokens][pair of a lane's four][lane]
+    __shared__ int64_t row0[WRITE_TOKENS], key0[WRITE_TOKENS], value0[WRITE_TOKENS];   // a token's row of head 0, or -1; its offsets
     typedef typename std::conditional<sizeof(T) == 4, uint4, uint2>::type Raw;
     constexpr int ROWS = NT / G, U = 2;         // rows in step, rows of a thread under way
     const int H = a.c.kv_heads, D = a.c.head_dim, half = a.rot / 2, lanes = half / 4;   // lanes with pairs
@@ -264,7 +266,19 @@ __global__ void __launch_bounds__(NT) k_cache_write(WriteArgs a, int tokens) {
     const unsigned all = (unsigned)a.B * (unsigned)a.T, n0 = blockIdx.x * (unsigned)tokens;   // below 2^31
     const int here = (int)min((unsigned)tokens, all - n0), total = here * H;
     const unsigned mask = G == 32 ? 0xffffffffu : ((1u << G) - 1) << (threadIdx.x % 32 / G * G);
-    bool made = a.rot == 0;
+    if ((int)threadIdx.x < here) {
+        const unsigned bt = n0 + threadIdx.x, b = bt / (unsigned)a.T;
+        const int t = (int)(bt - b * (unsigned)a.T);
+        const bool used = !a.count || t < __ldg(a.count + b);
+        row0[threadIdx.x] = used ? a.c.row((int)b, (int64_t)__ldg(a.start + b) + t, 0) : -1;
+        key0[threadIdx.x] = (int)b * a.kb + t * a.kt;
+        value0[threadIdx.x] = (int)b * a.vb + t * a.vt;
+    }
+    for (int i = threadIdx.x; i < here * half; i += NT) {
+        const int t = i / half, p = i - t * half;
+        table[t * half + p % 4 * lanes + p / 4] = turn(__ldg(a.pos + n0 + t), __ldg(a.phase + p), a.mscale, false);
+    }
+    __syncthreads();
     for (int first = r0; first - r0 < total; first += U * ROWS) {
         int64_t row[U];
         int tok[U];
@@ -276,25 +290,16 @@ __global__ void __launch_bounds__(NT) k_cache_write(WriteArgs a, int tokens) {
             if (it >= total) continue;
             tok[u] = it / H;
             const int h = it - tok[u] * H;
-            const unsigned bt = n0 + tok[u], b = bt / (unsigned)a.T;
-            const int t = (int)(bt - b * (unsigned)a.T);
-            if (a.count && t >= __ldg(a.count + b)) continue;
-            row[u] = a.c.row((int)b, (int64_t)__ldg(a.start + b) + t, h);
-            if (row[u] < 0 || !in) continue;
-            const T *k = (const T *)a.k + (int)b * a.kb + t * a.kt + h * a.kh;
-            const T *v = (const T *)a.v + (int)b * a.vb + t * a.vt + h * a.vh + v0;
+            row[u] = row0[tok[u]];
+            if (row[u] < 0) continue;
+            row[u] += (int64_t)h << a.c.page_shift;
+            if (!in) continue;
+            const T *k = (const T *)a.k + key0[tok[u]] + h * a.kh;
+            const T *v = (const T *)a.v + value0[tok[u]] + h * a.vh + v0;
             load4(k + k0, x[u][0]);
             load4(k + k1, x[u][1]);
             load4(v, x[u][2]);
             load4(v + 4, x[u][3]);
-        }
-        if (!made) {
-            for (int i = threadIdx.x; i < here * half; i += NT) {
-                const int t = i / half, p = i - t * half;
-                table[t * half + p % 4 * lanes + p / 4] = turn(__ldg(a.pos + n0 + t), __ldg(a.phase + p), a.mscale, false);
-            }
-            __syncthreads();
-            made = true;
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -336,8 +341,13 @@ __global__ void __launch_bounds__(NT) k_cache_write(WriteArgs a, int tokens) {
                     const float scale = odd ? __int_as_float(0x7fffffff) : amax / FA_E4M3_MAX;
                     if (odd || amax < 1e-30f) {
                         // a row of zeros or one that is marked; tiny values take the plain division
+#pragma unroll 1
+                        for (int e = 0; e < 8; ++e) {
+                            const float q = odd || scale == 0.0f ? 0.0f : f[0] / scale;   // rotate through f[0]
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) f[e] = odd || scale == 0.0f ? 0.0f : f[e] / scale;
+                            for (int j = 0; j < 7; ++j) f[j] = f[j + 1];
+                            f[7] = q;
+                        }
                     } else {
                         const float r = 1.0f / scale;
 #pragma unroll
@@ -373,9 +383,8 @@ template <class T> fa_status launch_write(const WriteArgs &a, cudaStream_t s) {
         return fa_launch_check("cache write");
     }
     const int G = D <= 64 ? 8 : D <= 128 ? 16 : 32;
-    // two steps of rows a block; fewer tokens where that leaves SMs without a block
-    int tokens = (int)std::min<int64_t>(16, std::max(1, 2 * 2 * (NT / G) / H));
-    tokens = (int)std::min<int64_t>(tokens, std::max<int64_t>(1, all / (152 * 8)));
+    // fewer tokens where that leaves SMs without a block
+    const int tokens = (int)std::min<int64_t>(WRITE_TOKENS, std::max<int64_t>(1, all / (152 * 8)));
     const unsigned blocks = (unsigned)((all + tokens - 1) / tokens);
     const size_t smem = (size_t)tokens * (a.rot / 2) * sizeof(float2);   // at most 16 * 128 * 8 bytes
     if (G == 8) launch_write<T, 8>(a, blocks, tokens, smem, s);
