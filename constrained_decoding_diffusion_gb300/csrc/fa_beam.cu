@@ -4,12 +4,13 @@
 // A cell (beam k, token v) has the value scores[k] + logp[k, v].  Its key is the value's
 // order-preserving bit pattern above the complement of its flat index k V + v: keys are distinct,
 // larger is better and ties go to the lowest index, so the result does not depend on the order in
-// which cells are met.  Selection is one pass over logp.  A block walks batches of 8192 cells of
-// one beam, 32 per thread in registers, and keeps the `top` best keys met so far in shared
-// memory; the smallest of them is the threshold that nearly every later cell fails.  Where more
-// than `top` threads hold a cell above the threshold, the top-th largest of the threads' maxima
-// is a better one (at least `top` cells reach it), which bounds a batch's candidates by 32 top.
-// A second launch merges the blocks' lists of a sequence the same way and looks up the states.
+// which cells are met.  Selection is one pass over logp.  A block walks batches of 8192 cells of one
+// beam, 32 per thread in registers, and keeps the `top` best keys met so far in shared memory; the
+// smallest of them is the threshold that nearly every later cell fails.  A thread compares the
+// largest of its cells (16-bit types: two at a time), and only where that can pass looks at them one
+// by one.  What costs is a list that fills in vain, so every block first takes a threshold from one
+// batch of the best beam.  A second launch merges the blocks' lists of a sequence the same way and
+// looks up the states.
 #include "fa_lm.cuh"
 
 namespace {
@@ -40,24 +41,49 @@ struct BestShared {
     int count;
 };
 
+// threads that may push in one offer
+__host__ __device__ constexpr int pushers(int top) { return 4 * top < NT ? 4 * top : NT; }
+
+// A key that at least `top` of the threads' best keys reach, and at most pushers(top) exceed (given
+// that more than that exceed the present threshold).  A warp's k-th largest key, k = top / 8
+// rounded up: the smallest of the eight warps' will do, and usually few enough are above it; where
+// not, the top-th largest of all by counting.
+__device__ __forceinline__ key_t64 raise(BestShared &sh, int top, key_t64 best) {
+    const int tid = threadIdx.x;
+    key_t64 x = best, kth = 0;
+    for (int i = 0; i < (top + NT / 32 - 1) / (NT / 32); ++i) {
+        kth = x;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) kth = max(kth, __shfl_xor_sync(0xffffffffu, kth, o));
+        if (x == kth) x = 0;                       // keys are distinct
+    }
+    if (tid % 32 == 0) sh.maxima[tid / 32] = kth;
+    __syncthreads();
+    key_t64 t = sh.maxima[0];
+#pragma unroll
+    for (int w = 1; w < NT / 32; ++w) t = min(t, sh.maxima[w]);
+    t = t ? t - 1 : 0;                             // the least of them still passes
+    if (__syncthreads_count(best > t) <= pushers(top)) return t;
+    sh.maxima[tid] = best;
+    __syncthreads();
+    int rank = 0;
+    for (int i = 0; i < NT; ++i) rank += sh.maxima[i] > best;
+    __syncthreads();
+    if (rank == top - 1) sh.maxima[0] = best - 1;
+    __syncthreads();
+    return sh.maxima[0];
+}
+
 // Offer the threads' keys: best is a thread's largest (0 where none can pass) and push(t, put) calls
 // put for each of its keys above t.  Called by all threads of the block; list has room for
-// top keys and those of top threads.
+// top keys and those of pushers(top) threads.
 template <class F>
 __device__ __forceinline__ void offer(BestShared &sh, key_t64 *list, key_t64 *work, int top, key_t64 best, F push) {
     const int tid = threadIdx.x;
     key_t64 thr = sh.threshold;
     const int above = __syncthreads_count(best > thr);
     if (!above) return;
-    if (above > top) {
-        sh.maxima[tid] = best;
-        __syncthreads();
-        int rank = 0;
-        for (int i = 0; i < NT; ++i) rank += sh.maxima[i] > best;
-        if (rank == top - 1 && best > thr) sh.threshold = best - 1;   // the top-th maximum itself still passes
-        __syncthreads();
-        thr = sh.threshold;
-    }
+    if (above > pushers(top)) thr = max(thr, raise(sh, top, best));
     if (best > thr) push(thr, [&](key_t64 k) { list[atomicAdd(&sh.count, 1)] = k; });
     __syncthreads();
     const int m = sh.count;
@@ -71,7 +97,7 @@ __device__ __forceinline__ void offer(BestShared &sh, key_t64 *list, key_t64 *wo
         }
         __syncthreads();
         for (int i = tid; i < top; i += NT) list[i] = work[i];
-        if (tid == 0) { sh.count = top; sh.threshold = work[top - 1]; }
+        if (tid == 0) { sh.count = top; sh.threshold = max(sh.threshold, work[top - 1]); }
         __syncthreads();
     }
 }
@@ -101,23 +127,18 @@ __device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b, __nv_bfloat
     return r;
 }
 // the largest element of a vector whose bit in m is set (-inf or NaN: none)
-__device__ __forceinline__ float top_of(uint4 r, uint32_t m, float) {
+__device__ __forceinline__ float top_of(uint4 r, uint32_t m, const uint2 *, float) {
     float t = -INFINITY;
     const float f[4] = {__uint_as_float(r.x), __uint_as_float(r.y), __uint_as_float(r.z), __uint_as_float(r.w)};
 #pragma unroll
     for (int e = 0; e < 4; ++e) t = (m >> e & 1) ? fmaxf(t, f[e]) : t;
     return t;
 }
-template <class T> __device__ __forceinline__ float top_of(uint4 r, uint32_t m, T) {
+// masks: for each nibble of live bits the two words that keep its four elements
+template <class T> __device__ __forceinline__ float top_of(uint4 r, uint32_t m, const uint2 *masks, T) {
     constexpr uint32_t low = std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;   // -inf, twice
-    uint32_t w[4] = {r.x, r.y, r.z, r.w};
-    if (m != 0xffu) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t keep = ((m >> (2 * i) & 1) ? 0x0000ffffu : 0u) | ((m >> (2 * i + 1) & 1) ? 0xffff0000u : 0u);
-            w[i] = (w[i] & keep) | (low & ~keep);
-        }
-    }
+    const uint2 a = masks[m & 15], b = masks[m >> 4];
+    const uint32_t w[4] = {(r.x & a.x) | (low & ~a.x), (r.y & a.y) | (low & ~a.y), (r.z & b.x) | (low & ~b.x), (r.w & b.y) | (low & ~b.y)};
     const uint32_t t = max_pair(max_pair(w[0], w[1], T()), max_pair(w[2], w[3], T()), T());
     float f[8];
     fa_unpack(make_uint4(t, t, t, t), f, T());
@@ -174,52 +195,93 @@ __global__ void __launch_bounds__(NT) k_beam_scan(SelectArgs a) {
     extern __shared__ key_t64 dyn[];
     __shared__ BestShared sh;
     constexpr int VEC = fa_vec<T>::N, NV = PER / VEC;
-    key_t64 *list = dyn, *work = dyn + (size_t)(PER + 1) * a.top;
+    key_t64 *list = dyn, *work = dyn + (size_t)PER * pushers(a.top) + a.top;
     const int tid = threadIdx.x, n = blockIdx.y;
+    __shared__ uint2 masks[16];
     if (tid == 0) { sh.threshold = 0; sh.count = 0; }
+    if (tid < 16)
+        masks[tid] = make_uint2((tid & 1 ? 0x0000ffffu : 0u) | (tid & 2 ? 0xffff0000u : 0u), (tid & 4 ? 0x0000ffffu : 0u) | (tid & 8 ? 0xffff0000u : 0u));
     __syncthreads();
+    // the beam with the largest score that is alive, the lowest of equals
+    __shared__ key_t64 best_key;
+    if (tid == 0) best_key = 0;
+    __syncthreads();
+    for (int k = tid; k < a.K; k += NT) {
+        const float x = __ldg(a.scores + (int64_t)n * a.K + k);
+        if (x > -INFINITY && (!a.S || (unsigned)__ldg(a.states + (int64_t)n * a.K + k) < (unsigned)a.S))
+            atomicMax(&best_key, cell_key(x, (uint32_t)k));
+    }
+    __syncthreads();
+    const int best_beam = best_key ? (int)(0xffffffffu - (uint32_t)best_key) : 0;
     const int per_beam = (a.V + VEC - 1 + BATCH - 1) / BATCH;   // a misaligned row starts up to VEC - 1 cells early
-    for (int bt = blockIdx.x; bt < a.K * per_beam; bt += gridDim.x) {
-        const int k = bt / per_beam, first = (bt % per_beam) * BATCH;
-        const float score = a.scores[(int64_t)n * a.K + k];
-        const int state = a.S ? a.states[(int64_t)n * a.K + k] : 0;
-        if (!(score > -INFINITY) || (a.S && (unsigned)state >= (unsigned)a.S)) continue;   // a dead beam
-        const T *row = (const T *)a.logp + n * a.ln + k * a.lk;
-        const int mis = (int)(((uintptr_t)row & 15) / sizeof(T));   // vector i holds cells i VEC - mis ...
-        const uint32_t *lrow = a.S ? a.live + (int64_t)state * a.words : nullptr;
-        uint4 raw[NV];
+    const int batches = a.K * per_beam;
+    // which cells of a batch are live; the loads of one batch's bits overlap the values of the one before
+    struct Cells {
         uint32_t bits[NV];
+        const T *row;
+        float score;
+        int k, first, mis;
+    };
+    auto find = [&](int bt) {
+        Cells x;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) x.bits[i] = 0;
+        x.k = bt / per_beam;
+        x.first = (bt - x.k * per_beam) * BATCH;
+        x.score = -INFINITY;
+        x.mis = 0;
+        x.row = nullptr;
+        if (bt >= batches) return x;
+        x.score = __ldg(a.scores + (int64_t)n * a.K + x.k);
+        const int state = a.S ? __ldg(a.states + (int64_t)n * a.K + x.k) : 0;
+        if (!(x.score > -INFINITY) || (a.S && (unsigned)state >= (unsigned)a.S)) return x;   // a dead beam
+        x.row = (const T *)a.logp + n * a.ln + x.k * a.lk;
+        x.mis = (int)(((uintptr_t)x.row & 15) / sizeof(T));     // vector i holds cells i VEC - mis ...
+        const uint32_t *lrow = a.S ? a.live + (int64_t)state * a.words : nullptr;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int v0 = first + (i * NT + tid) * VEC - mis;
-            constexpr uint32_t all = VEC == 32 ? 0xffffffffu : (1u << VEC) - 1;
+            const int v0 = x.first + (i * NT + tid) * VEC - x.mis;
+            constexpr uint32_t all = (1u << VEC) - 1;
             uint32_t m = v0 < a.V && v0 > -VEC ? all : 0u;
-            if (m && lrow) m &= mis ? live_bits<VEC>(lrow, a.words, v0) : __ldg((const uint8_t *)lrow + (v0 >> 3)) >> (v0 & 7);
+            if (m && lrow) m &= x.mis ? live_bits<VEC>(lrow, a.words, v0) : __ldg((const uint8_t *)lrow + (v0 >> 3)) >> (v0 & 7);
             if (m && v0 < 0) m &= all << -v0;
             if (m && v0 + VEC > a.V) m &= all >> (v0 + VEC - a.V);
-            bits[i] = m;
+            x.bits[i] = m;
         }
+        return x;
+    };
+    // Beams differ by whole units of score, so a block that meets a poor one first would fill its list
+    // in vain: every block looks at one batch of the best beam before its own ones, only for a
+    // threshold (-1), unless it starts there anyway.
+    bool look = (int)blockIdx.x / per_beam != best_beam;
+    Cells next = find(look ? best_beam * per_beam + (int)blockIdx.x % per_beam : blockIdx.x);
+    for (int bt = look ? (int)blockIdx.x - (int)gridDim.x : (int)blockIdx.x; bt < batches; bt += gridDim.x, look = false) {
+        const Cells c = next;
+        const uint32_t (&bits)[NV] = c.bits;
+        const float score = c.score;
+        uint4 raw[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int v0 = first + (i * NT + tid) * VEC - mis;
+            const int v0 = c.first + (i * NT + tid) * VEC - c.mis;
             raw[i] = make_uint4(0, 0, 0, 0);
             if (!bits[i]) continue;
             if (v0 >= 0 && v0 + VEC <= a.V) {
-                raw[i] = __ldg(reinterpret_cast<const uint4 *>(row + v0));
+                raw[i] = __ldg(reinterpret_cast<const uint4 *>(c.row + v0));
             } else {
                 float f[VEC];
-                for (int e = 0; e < VEC; ++e) f[e] = (bits[i] >> e & 1) ? fa_to_f32(row[v0 + e]) : 0.0f;
+                for (int e = 0; e < VEC; ++e) f[e] = (bits[i] >> e & 1) ? fa_to_f32(c.row[v0 + e]) : 0.0f;
                 raw[i] = fa_pack(f, T());
             }
         }
+        next = find(bt + gridDim.x);
         // the thread's largest value: the addition is monotone, so it is the score plus the largest cell
         float most = -INFINITY;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (bits[i]) most = fmaxf(most, top_of(raw[i], bits[i], T()));
+            if (bits[i]) most = fmaxf(most, top_of(raw[i], bits[i], masks, T()));
         const float top_value = score + most;
         auto cell = [&](int i, int e, float x) -> key_t64 {
-            return cell_key(score + x, (uint32_t)(k * a.V + first + (i * NT + tid) * VEC - mis + e));
+            return cell_key(score + x, (uint32_t)(c.k * a.V + c.first + (i * NT + tid) * VEC - c.mis + e));
         };
         // its key, where it can pass (after the first batches it hardly ever can)
         key_t64 best = 0;
@@ -237,6 +299,13 @@ __global__ void __launch_bounds__(NT) k_beam_scan(SelectArgs a) {
             each([&](int i, int e, float x) {
                 if (score + x == top_value && !best) best = cell(i, e, x);   // the lowest index of equals
             });
+        if (look) {
+            // at least `top` of the batch's cells reach it, so all of the best ones do
+            const key_t64 t = raise(sh, a.top, best);
+            if (tid == 0) sh.threshold = t;
+            __syncthreads();
+            continue;
+        }
         offer(sh, list, work, a.top, best, [&](key_t64 thr, auto put) {
             const float least = passing(thr);
             each([&](int i, int e, float x) {
@@ -255,7 +324,7 @@ __global__ void __launch_bounds__(NT) k_beam_scan(SelectArgs a) {
 __global__ void __launch_bounds__(NT) k_beam_merge(SelectArgs a) {
     extern __shared__ key_t64 dyn[];
     __shared__ BestShared sh;
-    key_t64 *list = dyn, *work = dyn + 5 * (size_t)a.top;
+    key_t64 *list = dyn, *work = dyn + (size_t)4 * pushers(a.top) + a.top;
     const int tid = threadIdx.x, n = blockIdx.x;
     if (tid == 0) { sh.threshold = 0; sh.count = 0; }
     __syncthreads();
@@ -395,7 +464,7 @@ extern "C" fa_status fa_beam_select(int32_t dtype, int32_t N, int32_t K, int32_t
     a.keys = (key_t64 *)workspace;
     a.out_score = out_score; a.out_parent = out_parent; a.out_token = out_token; a.out_state = out_state;
     cudaStream_t s = (cudaStream_t)stream;
-    const size_t smem = (size_t)(PER + 1) * top * 8 + (size_t)top * 8;
+    const size_t smem = ((size_t)PER * pushers(top) + 2 * top) * 8;
     auto go = [&](auto tag) {
         using T = decltype(tag);
         if (smem > 40 * 1024) {
@@ -408,7 +477,7 @@ extern "C" fa_status fa_beam_select(int32_t dtype, int32_t N, int32_t K, int32_t
     const cudaError_t e = dtype == FA_DTYPE_F32 ? go(0.0f) : dtype == FA_DTYPE_F16 ? go(__half()) : go(__nv_bfloat16());
     if (e != cudaSuccess) return fa_refuse(fn, cudaGetErrorString(e), FA_ERR_CUDA);
     if ((st = fa_launch_check("beam scan")) != FA_OK || a.nb == 1) return st;
-    k_beam_merge<<<(unsigned)N, NT, (size_t)6 * top * 8, s>>>(a);
+    k_beam_merge<<<(unsigned)N, NT, ((size_t)4 * pushers(top) + 2 * top) * 8, s>>>(a);
     return fa_launch_check("beam merge");
 }
 
