@@ -35,8 +35,29 @@ def _lib():
     return native._lib or native.load()
 
 
-def _stream(stream) -> int:
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+_raw_stream = torch._C._cuda_getCurrentRawStream   # the current stream's handle without a Stream object
+
+
+def _stream(stream, t) -> int:
+    return _raw_stream(t.device.index) if stream is None else stream.cuda_stream
+
+
+def _check(rc: int):
+    if rc:
+        native._check(rc)
+
+
+# The checks below run on every call of a decoding loop, so each takes one pass over the few
+# attributes it needs and leaves the wording of a refusal to _refuse.
+
+def _refuse(t, dtype, name, shape):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    raise ValueError("%s must be contiguous" % name)
 
 
 def _dtype(t, name) -> int:
@@ -52,14 +73,8 @@ def _ptr(t, dtype, name, shape):
     """A contiguous tensor's address after checking it; None for None."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError("%s must be a CUDA tensor" % name)
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.shape != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        _refuse(t, dtype, name, shape)
     return t.data_ptr()
 
 
@@ -68,7 +83,7 @@ def _rows(t, name, shape):
     if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     st = t.stride()
-    if st[-1] != 1 and t.shape[-1] > 1:
+    if st[-1] != 1 and shape[-1] > 1:
         raise ValueError("%s: the innermost dimension must be contiguous" % name)
     return st
 
@@ -125,10 +140,10 @@ def fa_rope(x, positions, phase, out=None, interleaved: bool = False, mscale: fl
     elif _dtype(out, "out") != dt:
         raise TypeError("out must have the type of x")
     xs, os = _rows(x, "x", x.shape), _rows(out, "out", x.shape)
-    native._check(_lib().fa_rope(dt, N, H, D, 2 * phase.numel(), int(interleaved), int(inverse), x.data_ptr(), xs[0], xs[1],
+    _check(_lib().fa_rope(dt, N, H, D, 2 * phase.numel(), int(interleaved), int(inverse), x.data_ptr(), xs[0], xs[1],
                                  _ptr(positions, torch.int32, "positions", (N,)),
                                  _ptr(phase, torch.int64, "phase", phase.shape), mscale, out.data_ptr(), os[0], os[1],
-                                 _stream(stream)))
+                                 _stream(stream, x)))
     return out
 
 
@@ -170,17 +185,22 @@ class KVCache(NamedTuple):
         return cls(k, v, *(torch.empty(shape[:3], dtype=torch.float32, device=device) for _ in range(2)))
 
     def describe(self) -> _Cache:
-        k, dtype = self.k, self.k.dtype
-        if dtype not in _FORMAT or k.dim() != 4:
+        k, v, ks, vs = self
+        dtype, shape = k.dtype, k.shape
+        form = _FORMAT.get(dtype)
+        if form is None or len(shape) != 4:
             raise TypeError("cache pages must be float16, bfloat16 or float8_e4m3fn of shape "
                             "[n_pages, kv_heads, page_size, head_dim]")
-        if (self.k_scale is not None) != (dtype == torch.float8_e4m3fn):
-            raise ValueError("an 8-bit cache has scales, a 16-bit one has none")
-        shape = k.shape
         n, h, g, d = shape
-        return _Cache(_ptr(k, dtype, "cache.k", shape), _ptr(self.v, dtype, "cache.v", shape),
-                      _ptr(self.k_scale, torch.float32, "cache.k_scale", shape[:3]),
-                      _ptr(self.v_scale, torch.float32, "cache.v_scale", shape[:3]), _FORMAT[dtype], n, g, h, d)
+        if form != FA_CACHE_E4M3:
+            if ks is not None or vs is not None:
+                raise ValueError("a 16-bit cache has no scales")
+            return _Cache(_ptr(k, dtype, "cache.k", shape), _ptr(v, dtype, "cache.v", shape), None, None, form, n, g, h, d)
+        if ks is None or vs is None:
+            raise ValueError("an 8-bit cache has scales")
+        rows = (n, h, g)
+        return _Cache(_ptr(k, dtype, "cache.k", shape), _ptr(v, dtype, "cache.v", shape),
+                      _ptr(ks, torch.float32, "cache.k_scale", rows), _ptr(vs, torch.float32, "cache.v_scale", rows), form, n, g, h, d)
 
 
 def fa_cache_write(cache: KVCache, k, v, page_table, start, count=None, positions=None, phase=None,
@@ -195,12 +215,12 @@ def fa_cache_write(cache: KVCache, k, v, page_table, start, count=None, position
     shape = (B, T, c.kv_heads, c.head_dim)
     ks, vs = _rows(k, "k", shape), _rows(v, "v", shape)
     P = page_table.shape[1]
-    native._check(_lib().fa_cache_write(
+    _check(_lib().fa_cache_write(
         ctypes.byref(c), dt, B, T, k.data_ptr(), ks[0], ks[1], ks[2], v.data_ptr(), vs[0], vs[1], vs[2],
         _ptr(page_table, torch.int32, "page_table", (B, P)), P, _ptr(start, torch.int32, "start", (B,)),
         _ptr(count, torch.int32, "count", (B,)), _ptr(positions, torch.int32, "positions", (B, T)),
         None if phase is None else _ptr(phase, torch.int64, "phase", phase.shape), 0 if phase is None else 2 * phase.numel(),
-        int(interleaved), mscale, _stream(stream)))
+        int(interleaved), mscale, _stream(stream, k)))
 
 
 def fa_cache_read(cache: KVCache, page_table, length, k_out, v_out, stream=None):
@@ -210,10 +230,10 @@ def fa_cache_read(cache: KVCache, page_table, length, k_out, v_out, stream=None)
     B, N = k_out.shape[:2]
     shape = (B, N, c.kv_heads, c.head_dim)
     P = page_table.shape[1]
-    native._check(_lib().fa_cache_read(
+    _check(_lib().fa_cache_read(
         ctypes.byref(c), dt, B, N, _ptr(page_table, torch.int32, "page_table", (B, P)), P,
         _ptr(length, torch.int32, "length", (B,)), _ptr(k_out, k_out.dtype, "k_out", shape),
-        _ptr(v_out, k_out.dtype, "v_out", shape), _stream(stream)))
+        _ptr(v_out, k_out.dtype, "v_out", shape), _stream(stream, k_out)))
     return k_out, v_out
 
 
@@ -223,9 +243,9 @@ def fa_cache_keep(cache: KVCache, page_table, length, path, stream=None):
     c = cache.describe()
     B, P = page_table.shape
     n = path.shape[1]
-    native._check(_lib().fa_cache_keep(ctypes.byref(c), B, n, _ptr(page_table, torch.int32, "page_table", (B, P)), P,
+    _check(_lib().fa_cache_keep(ctypes.byref(c), B, n, _ptr(page_table, torch.int32, "page_table", (B, P)), P,
                                        _ptr(length, torch.int32, "length", (B,)), _ptr(path, torch.int32, "path", (B, n)),
-                                       _stream(stream)))
+                                       _stream(stream, path)))
 
 
 # ------------------------------------------------------------------ attention of drafted tokens
@@ -237,9 +257,9 @@ def fa_tree_mask(parents, mask=None, depth=None, stream=None):
         mask = torch.empty((B, T, (T + 63) // 64), dtype=torch.int64, device=parents.device)
     if depth is None:
         depth = torch.empty((B, T), dtype=torch.int32, device=parents.device)
-    native._check(_lib().fa_tree_mask(B, T, _ptr(parents, torch.int32, "parents", (B, T)),
+    _check(_lib().fa_tree_mask(B, T, _ptr(parents, torch.int32, "parents", (B, T)),
                                       _ptr(mask, torch.int64, "mask", (B, T, (T + 63) // 64)),
-                                      _ptr(depth, torch.int32, "depth", (B, T)), _stream(stream)))
+                                      _ptr(depth, torch.int32, "depth", (B, T)), _stream(stream, parents)))
     return mask, depth
 
 
@@ -249,8 +269,9 @@ class TreeAttention:
     def __init__(self, B: int, T: int, q_heads: int, kv_heads: int, head_dim: int, dtype=torch.bfloat16, device="cuda"):
         n = ctypes.c_size_t()
         native.load()
-        native._check(_lib().fa_tree_attention_workspace_bytes(B, T, q_heads, kv_heads, head_dim, ctypes.byref(n)))
+        _check(_lib().fa_tree_attention_workspace_bytes(B, T, q_heads, kv_heads, head_dim, ctypes.byref(n)))
         self.shape = (B, T, q_heads, head_dim)
+        self.ws_bytes = n.value
         self.workspace = torch.empty(max(n.value, 256), dtype=torch.uint8, device=device)
         self.out = torch.empty(self.shape, dtype=dtype, device=device)
         self.lse = torch.empty((B, T, q_heads), dtype=torch.float32, device=device)
@@ -270,12 +291,12 @@ class TreeAttention:
             raise ValueError("the cache's head_dim is %d, not %d" % (c.head_dim, D))
         s = _rows(q, "q", self.shape)
         P = page_table.shape[1]
-        native._check(_lib().fa_tree_attention(
+        _check(_lib().fa_tree_attention(
             ctypes.byref(c), dt, B, T, H, q.data_ptr(), s[0], s[1], s[2],
             _ptr(page_table, torch.int32, "page_table", (B, P)), P, _ptr(length, torch.int32, "length", (B,)),
             _ptr(count, torch.int32, "count", (B,)), _ptr(mask, torch.int64, "mask", (B, T, (T + 63) // 64)),
             D ** -0.5 if scale is None else scale, self.out.data_ptr(), self.lse.data_ptr(), self.workspace.data_ptr(),
-            self.workspace.numel(), _stream(stream)))
+            self.ws_bytes, _stream(stream, q)))
         return self.out, self.lse
 
 
@@ -287,7 +308,7 @@ def fa_beam_tables(aut: native.CompiledAutomaton, stream=None):
     S, V = aut.n_states, aut.vocab
     nxt = torch.empty((S, V), dtype=torch.int16, device="cuda")
     live = torch.empty((S, (V + 31) // 32), dtype=torch.int32, device="cuda")
-    native._check(_lib().fa_beam_tables(aut.handle, nxt.data_ptr(), live.data_ptr(), _stream(stream)))
+    _check(_lib().fa_beam_tables(aut.handle, nxt.data_ptr(), live.data_ptr(), _stream(stream, nxt)))
     return nxt, live
 
 
@@ -297,7 +318,7 @@ class BeamSelect:
     def __init__(self, N: int, K: int, V: int, top: int, dtype=torch.float32, device="cuda"):
         n = ctypes.c_size_t()
         native.load()
-        native._check(_lib().fa_beam_select_workspace_bytes(N, K, V, top, ctypes.byref(n)))
+        _check(_lib().fa_beam_select_workspace_bytes(N, K, V, top, ctypes.byref(n)))
         self.N, self.K, self.V, self.top, self.dtype = N, K, V, top, dtype
         self.workspace = torch.empty(max(n.value, 256), dtype=torch.uint8, device=device)
         self.score = torch.empty((N, top), dtype=torch.float32, device=device)
@@ -312,12 +333,12 @@ class BeamSelect:
             raise TypeError("logp must be %s, got %s" % (self.dtype, logp.dtype))
         st = _rows(logp, "logp", (N, K, V))
         S = 0 if next is None else next.shape[0]
-        native._check(_lib().fa_beam_select(
+        _check(_lib().fa_beam_select(
             dt, N, K, V, self.top, logp.data_ptr(), st[0], st[1], _ptr(scores, torch.float32, "scores", (N, K)),
             _ptr(states, torch.int32, "states", (N, K)), S, _ptr(next, torch.int16, "next", (S, V)),
             _ptr(live, torch.int32, "live", (S, (V + 31) // 32)), self.score.data_ptr(), self.parent.data_ptr(),
             self.token.data_ptr(), self.state.data_ptr() if S else None, self.workspace.data_ptr(), self.workspace.numel(),
-            _stream(stream)))
+            _stream(stream, logp)))
         return self.score, self.parent, self.token, self.state if S else None
 
 
@@ -328,8 +349,8 @@ def fa_beam_reorder(src, parent, dst=None, token=None, at: int = 0, stream=None)
     top = parent.shape[1]
     if dst is None:
         dst = torch.empty((N, top, W), dtype=torch.int32, device=src.device)
-    native._check(_lib().fa_beam_reorder(N, K, top, W, _ptr(src, torch.int32, "src", (N, K, W)),
+    _check(_lib().fa_beam_reorder(N, K, top, W, _ptr(src, torch.int32, "src", (N, K, W)),
                                          _ptr(parent, torch.int32, "parent", (N, top)),
                                          _ptr(token, torch.int32, "token", (N, top)), int(at),
-                                         _ptr(dst, torch.int32, "dst", (N, top, W)), _stream(stream)))
+                                         _ptr(dst, torch.int32, "dst", (N, top, W)), _stream(stream, src)))
     return dst
