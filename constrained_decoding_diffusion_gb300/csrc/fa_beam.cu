@@ -5,12 +5,18 @@
 // order-preserving bit pattern above the complement of its flat index k V + v: keys are distinct,
 // larger is better and ties go to the lowest index, so the result does not depend on the order in
 // which cells are met.  Selection is one pass over logp.  A block walks batches of 8192 cells of one
-// beam, 32 per thread in registers, and keeps the `top` best keys met so far in shared memory; the
-// smallest of them is the threshold that nearly every later cell fails.  A thread compares the
+// beam, 32 per thread in registers, and keeps the best keys met so far in shared memory; the `top`-th
+// best of them is the threshold that nearly every later cell fails.  A thread compares the
 // largest of its cells (16-bit types: two at a time), and only where that can pass looks at them one
 // by one.  What costs is a list that fills in vain, so every block first takes a threshold from one
 // batch of the best beam.  A second launch merges the blocks' lists of a sequence the same way and
 // looks up the states.
+//
+// The floor is memory: logp and the live bits once.  Measured, 16 sequences of 16 beams of 151936
+// tokens in bf16, a tenth of them live, top 16: 47 us for the scan (1.7 TB/s), 7 for the merge; without
+// any cell that passes the scan takes 22, so what bounds it is the threshold's rise (about six of a
+// block's eight batches still hold a cell that passes) and the barriers around it, not the loads.
+// One list of 4 beams of 32000 tokens: 22 us with the reordering, three launches' start and end.
 #include "fa_lm.cuh"
 
 namespace {
@@ -33,8 +39,8 @@ __device__ __forceinline__ float key_value(key_t64 k) {
     return __uint_as_float((ord >> 31) ? (ord & 0x7fffffffu) : ~ord);
 }
 
-// The `top` best keys met so far: list[0 .. count), all distinct; threshold = the smallest of
-// them once there are `top`, else 0 (below every cell's key).
+// The best keys met so far, at least `top` of them once there are so many: list[0 .. count), all distinct;
+// threshold = a key that `top` of them reach, 0 (below every cell's key) before.
 struct BestShared {
     key_t64 maxima[NT];
     key_t64 threshold;
@@ -74,32 +80,39 @@ __device__ __forceinline__ key_t64 raise(BestShared &sh, int top, key_t64 best) 
     return sh.maxima[0];
 }
 
-// Offer the threads' keys: best is a thread's largest (0 where none can pass) and push(t, put) calls
-// put for each of its keys above t.  Called by all threads of the block; list has room for
-// top keys and those of pushers(top) threads.
-template <class F>
-__device__ __forceinline__ void offer(BestShared &sh, key_t64 *list, key_t64 *work, int top, key_t64 best, F push) {
-    const int tid = threadIdx.x;
-    key_t64 thr = sh.threshold;
-    const int above = __syncthreads_count(best > thr);
-    if (!above) return;
-    if (above > pushers(top)) thr = max(thr, raise(sh, top, best));
-    if (best > thr) push(thr, [&](key_t64 k) { list[atomicAdd(&sh.count, 1)] = k; });
-    __syncthreads();
-    const int m = sh.count;
-    if (m >= top) {
-        // keep the best `top` in order; the last of them is the threshold
-        for (int i = tid; i < m; i += NT) {
-            const key_t64 k = list[i];
-            int rank = 0;
-            for (int j = 0; j < m; ++j) rank += list[j] > k;
-            if (rank < top) work[rank] = k;
-        }
-        __syncthreads();
-        for (int i = tid; i < top; i += NT) list[i] = work[i];
-        if (tid == 0) { sh.count = top; sh.threshold = max(sh.threshold, work[top - 1]); }
-        __syncthreads();
+// Offer the threads' keys.  pass says whether a thread has one that may be above the threshold,
+// best() gives its largest (0 where none can pass) and is asked for only where more threads pass than the
+// list has room for; push(t, pass, put) calls put for each key above t of the threads that pass.
+// Called by all threads of the block.  The list is put in order, and the threshold raised, when it holds
+// twice `top` keys, or `top` before there is a threshold.
+constexpr int FULL = 2;
+__device__ __forceinline__ void keep_best(BestShared &sh, key_t64 *list, key_t64 *work, int top) {
+    const int tid = threadIdx.x, m = sh.count;
+    if (m <= top && sh.threshold) return;
+    for (int i = tid; i < m; i += NT) {
+        const key_t64 k = list[i];
+        int rank = 0;
+        for (int j = 0; j < m; ++j) rank += list[j] > k;
+        if (rank < top) work[rank] = k;
     }
+    __syncthreads();
+    for (int i = tid; i < min(m, top); i += NT) list[i] = work[i];
+    if (tid == 0 && m >= top) { sh.count = top; sh.threshold = max(sh.threshold, work[top - 1]); }
+    __syncthreads();
+}
+template <class B, class F>
+__device__ __forceinline__ void offer(BestShared &sh, key_t64 *list, key_t64 *work, int top, bool pass, B best, F push) {
+    key_t64 thr = sh.threshold;
+    const int above = __syncthreads_count(pass);
+    if (!above) return;
+    if (above > pushers(top)) {
+        const key_t64 mine = pass ? best() : 0;
+        if (__syncthreads_count(mine > thr) > pushers(top)) thr = max(thr, raise(sh, top, mine));
+        pass = mine > thr;
+    }
+    push(thr, pass, [&](key_t64 k) { list[atomicAdd(&sh.count, 1)] = k; });
+    __syncthreads();
+    if (sh.count >= (sh.threshold ? FULL * top : top)) keep_best(sh, list, work, top);
 }
 
 struct SelectArgs {
@@ -145,14 +158,18 @@ template <class T> __device__ __forceinline__ float top_of(uint4 r, uint32_t m, 
     return fmaxf(f[0], f[1]);
 }
 
-// the live bits of W consecutive tokens from v0 on (v0 may be negative or near the row's end)
-template <int W>
-__device__ __forceinline__ uint32_t live_bits(const uint32_t *row, int words, int v0) {
-    const int w = v0 >> 5, sh = v0 & 31;
-    const uint32_t lo = w >= 0 && w < words ? __ldg(row + w) : 0u;
-    uint32_t bits = lo >> sh;
-    if (sh + W > 32 && w + 1 < words) bits |= __ldg(row + w + 1) << (32 - sh);
-    return bits;
+// the live bits of tokens v0 .. v0 + 31 (v0 may be negative or near the row's end); no row: all of them
+__device__ __forceinline__ uint32_t live_word(const uint32_t *row, int words, int v0, int V) {
+    if (v0 <= -32 || v0 >= V) return 0;
+    uint32_t m = 0xffffffffu;
+    if (row) {
+        const int w = v0 >> 5, sh = v0 & 31;
+        m = w >= 0 ? __ldg(row + w) >> sh : 0u;
+        if (sh && w + 1 < words) m |= __ldg(row + w + 1) << (32 - sh);
+    }
+    if (v0 < 0) m &= 0xffffffffu << -v0;
+    if (V - v0 < 32) m &= (1u << (V - v0)) - 1;
+    return m;
 }
 
 __device__ void store_cell(const SelectArgs &a, int n, int i, key_t64 k) {
@@ -173,6 +190,8 @@ __device__ void store_cell(const SelectArgs &a, int n, int i, key_t64 k) {
 
 // write the block's best keys: to the outputs when it is the sequence's only block
 __device__ void finish(const SelectArgs &a, BestShared &sh, key_t64 *list, key_t64 *work, int n, bool last) {
+    __syncthreads();
+    if (sh.count > a.top) keep_best(sh, list, work, a.top);
     const int tid = threadIdx.x, m = sh.count;
     if (last) {
         for (int i = tid; i < a.top; i += NT) work[i] = 0;
@@ -191,11 +210,11 @@ __device__ void finish(const SelectArgs &a, BestShared &sh, key_t64 *list, key_t
 }
 
 template <class T>
-__global__ void __launch_bounds__(NT) k_beam_scan(SelectArgs a) {
+__global__ void __launch_bounds__(NT, sizeof(T) == 2 ? 4 : 2) k_beam_scan(SelectArgs a) {
     extern __shared__ key_t64 dyn[];
     __shared__ BestShared sh;
     constexpr int VEC = fa_vec<T>::N, NV = PER / VEC;
-    key_t64 *list = dyn, *work = dyn + (size_t)PER * pushers(a.top) + a.top;
+    key_t64 *list = dyn, *work = dyn + (size_t)PER * pushers(a.top) + FULL * a.top;
     const int tid = threadIdx.x, n = blockIdx.y;
     __shared__ uint2 masks[16];
     if (tid == 0) { sh.threshold = 0; sh.count = 0; }
@@ -215,19 +234,22 @@ __global__ void __launch_bounds__(NT) k_beam_scan(SelectArgs a) {
     const int best_beam = best_key ? (int)(0xffffffffu - (uint32_t)best_key) : 0;
     const int per_beam = (a.V + VEC - 1 + BATCH - 1) / BATCH;   // a misaligned row starts up to VEC - 1 cells early
     const int batches = a.K * per_beam;
-    // which cells of a batch are live; the loads of one batch's bits overlap the values of the one before
+    // Which cells of a batch are live: a warp takes 32 x PER consecutive cells, in rows of 32 vectors, and
+    // a lane loads the bits of PER of them, one batch ahead of the values.
+    static_assert(PER == 32, "a lane's bits are one word");
+    constexpr int RPW = 32 / NV;                             // words of bits of a row of vectors
+    const int lane = tid & 31, warp_cell = (tid >> 5) * 32 * PER;
     struct Cells {
-        uint32_t bits[NV];
+        uint32_t word;
         const T *row;
         float score;
         int k, first, mis;
     };
     auto find = [&](int bt) {
         Cells x;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) x.bits[i] = 0;
+        x.word = 0;
         x.k = bt / per_beam;
-        x.first = (bt - x.k * per_beam) * BATCH;
+        x.first = (bt - x.k * per_beam) * BATCH + warp_cell;
         x.score = -INFINITY;
         x.mis = 0;
         x.row = nullptr;
@@ -236,18 +258,8 @@ __global__ void __launch_bounds__(NT) k_beam_scan(SelectArgs a) {
         const int state = a.S ? __ldg(a.states + (int64_t)n * a.K + x.k) : 0;
         if (!(x.score > -INFINITY) || (a.S && (unsigned)state >= (unsigned)a.S)) return x;   // a dead beam
         x.row = (const T *)a.logp + n * a.ln + x.k * a.lk;
-        x.mis = (int)(((uintptr_t)x.row & 15) / sizeof(T));     // vector i holds cells i VEC - mis ...
-        const uint32_t *lrow = a.S ? a.live + (int64_t)state * a.words : nullptr;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int v0 = x.first + (i * NT + tid) * VEC - x.mis;
-            constexpr uint32_t all = (1u << VEC) - 1;
-            uint32_t m = v0 < a.V && v0 > -VEC ? all : 0u;
-            if (m && lrow) m &= x.mis ? live_bits<VEC>(lrow, a.words, v0) : __ldg((const uint8_t *)lrow + (v0 >> 3)) >> (v0 & 7);
-            if (m && v0 < 0) m &= all << -v0;
-            if (m && v0 + VEC > a.V) m &= all >> (v0 + VEC - a.V);
-            x.bits[i] = m;
-        }
+        x.mis = (int)(((uintptr_t)x.row & 15) / sizeof(T));     // the batch's first cell is `first` - mis
+        x.word = live_word(a.S ? a.live + (int64_t)state * a.words : nullptr, a.words, x.first - x.mis + 32 * lane, a.V);
         return x;
     };
     // Beams differ by whole units of score, so a block that meets a poor one first would fill its list
@@ -257,64 +269,72 @@ __global__ void __launch_bounds__(NT) k_beam_scan(SelectArgs a) {
     Cells next = find(look ? best_beam * per_beam + (int)blockIdx.x % per_beam : blockIdx.x);
     for (int bt = look ? (int)blockIdx.x - (int)gridDim.x : (int)blockIdx.x; bt < batches; bt += gridDim.x, look = false) {
         const Cells c = next;
-        const uint32_t (&bits)[NV] = c.bits;
         const float score = c.score;
+        const int cell0 = c.first - c.mis + lane * VEC;      // of vector 0; vector i is 32 i VEC further
+        const T *at = c.row + cell0;
+        uint32_t bits[NV];
         uint4 raw[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int v0 = c.first + (i * NT + tid) * VEC - c.mis;
+            bits[i] = __shfl_sync(0xffffffffu, c.word, i * RPW + lane / NV) >> lane % NV * VEC & ((1u << VEC) - 1);
+            const int v0 = cell0 + 32 * VEC * i;
             raw[i] = make_uint4(0, 0, 0, 0);
             if (!bits[i]) continue;
             if (v0 >= 0 && v0 + VEC <= a.V) {
-                raw[i] = __ldg(reinterpret_cast<const uint4 *>(c.row + v0));
+                raw[i] = __ldg(reinterpret_cast<const uint4 *>(at + 32 * VEC * i));
             } else {
                 float f[VEC];
-                for (int e = 0; e < VEC; ++e) f[e] = (bits[i] >> e & 1) ? fa_to_f32(c.row[v0 + e]) : 0.0f;
+                for (int e = 0; e < VEC; ++e) f[e] = (bits[i] >> e & 1) ? fa_to_f32(at[32 * VEC * i + e]) : 0.0f;
                 raw[i] = fa_pack(f, T());
             }
         }
         next = find(bt + gridDim.x);
         // the thread's largest value: the addition is monotone, so it is the score plus the largest cell
-        float most = -INFINITY;
+        float most = -INFINITY, tops[NV];
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (bits[i]) most = fmaxf(most, top_of(raw[i], bits[i], masks, T()));
+        for (int i = 0; i < NV; ++i) {
+            tops[i] = top_of(raw[i], bits[i], masks, T());
+            most = fmaxf(most, tops[i]);
+        }
         const float top_value = score + most;
-        auto cell = [&](int i, int e, float x) -> key_t64 {
-            return cell_key(score + x, (uint32_t)(c.k * a.V + c.first + (i * NT + tid) * VEC - c.mis + e));
-        };
-        // its key, where it can pass (after the first batches it hardly ever can)
-        key_t64 best = 0;
-        auto each = [&](auto f) {                            // the cells with a live bit, in their order
+        const uint32_t flat0 = (uint32_t)(c.k * a.V + cell0);   // of the thread's first cell
+        auto best = [&]() {                                  // the key of the thread's largest cell, the lowest index of equals
+            key_t64 key = 0;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 float x[VEC];
                 fa_unpack(raw[i], x, T());
 #pragma unroll
                 for (int e = 0; e < VEC; ++e)
-                    if (bits[i] >> e & 1) f(i, e, x[e]);
+                    if ((bits[i] >> e & 1) && score + x[e] == top_value && !key) key = cell_key(score + x[e], flat0 + 32 * VEC * i + e);
             }
+            return key;
         };
-        if (most > -INFINITY && top_value > -INFINITY && !(top_value < passing(sh.threshold)))
-            each([&](int i, int e, float x) {
-                if (score + x == top_value && !best) best = cell(i, e, x);   // the lowest index of equals
-            });
+        const bool pass = top_value > -INFINITY && !(top_value < passing(sh.threshold));
         if (look) {
             // at least `top` of the batch's cells reach it, so all of the best ones do
-            const key_t64 t = raise(sh, a.top, best);
+            const key_t64 t = raise(sh, a.top, pass ? best() : 0);
             if (tid == 0) sh.threshold = t;
             __syncthreads();
             continue;
         }
-        offer(sh, list, work, a.top, best, [&](key_t64 thr, auto put) {
+        offer(sh, list, work, a.top, pass, best, [&](key_t64 thr, bool mine, auto put) {
             const float least = passing(thr);
-            each([&](int i, int e, float x) {
-                const float v = score + x;
-                if (v >= least && v > -INFINITY) {
-                    const key_t64 key = cell(i, e, x);
-                    if (key > thr) put(key);
+            if (mine)
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    if (!(score + tops[i] >= least)) continue;   // nearly all vectors
+                    float x[VEC];
+                    fa_unpack(raw[i], x, T());
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        const float v = score + x[e];
+                        if ((bits[i] >> e & 1) && v >= least && v > -INFINITY) {
+                            const key_t64 key = cell_key(v, flat0 + 32 * VEC * i + e);
+                            if (key > thr) put(key);
+                        }
+                    }
                 }
-            });
         });
     }
     finish(a, sh, list, work, n, gridDim.x == 1);
@@ -324,7 +344,7 @@ __global__ void __launch_bounds__(NT) k_beam_scan(SelectArgs a) {
 __global__ void __launch_bounds__(NT) k_beam_merge(SelectArgs a) {
     extern __shared__ key_t64 dyn[];
     __shared__ BestShared sh;
-    key_t64 *list = dyn, *work = dyn + (size_t)4 * pushers(a.top) + a.top;
+    key_t64 *list = dyn, *work = dyn + (size_t)4 * pushers(a.top) + FULL * a.top;
     const int tid = threadIdx.x, n = blockIdx.x;
     if (tid == 0) { sh.threshold = 0; sh.count = 0; }
     __syncthreads();
@@ -338,10 +358,10 @@ __global__ void __launch_bounds__(NT) k_beam_merge(SelectArgs a) {
             k[i] = at < total ? keys[at] : 0;
             best = max(best, k[i]);
         }
-        offer(sh, list, work, a.top, best, [&](key_t64 thr, auto put) {
+        offer(sh, list, work, a.top, best > sh.threshold, [&]() { return best; }, [&](key_t64 thr, bool mine, auto put) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (k[i] > thr) put(k[i]);
+                if (mine && k[i] > thr) put(k[i]);
         });
     }
     finish(a, sh, list, work, n, true);
@@ -464,7 +484,7 @@ extern "C" fa_status fa_beam_select(int32_t dtype, int32_t N, int32_t K, int32_t
     a.keys = (key_t64 *)workspace;
     a.out_score = out_score; a.out_parent = out_parent; a.out_token = out_token; a.out_state = out_state;
     cudaStream_t s = (cudaStream_t)stream;
-    const size_t smem = ((size_t)PER * pushers(top) + 2 * top) * 8;
+    const size_t smem = ((size_t)PER * pushers(top) + (FULL + 1) * top) * 8;
     auto go = [&](auto tag) {
         using T = decltype(tag);
         if (smem > 40 * 1024) {
@@ -477,7 +497,7 @@ extern "C" fa_status fa_beam_select(int32_t dtype, int32_t N, int32_t K, int32_t
     const cudaError_t e = dtype == FA_DTYPE_F32 ? go(0.0f) : dtype == FA_DTYPE_F16 ? go(__half()) : go(__nv_bfloat16());
     if (e != cudaSuccess) return fa_refuse(fn, cudaGetErrorString(e), FA_ERR_CUDA);
     if ((st = fa_launch_check("beam scan")) != FA_OK || a.nb == 1) return st;
-    k_beam_merge<<<(unsigned)N, NT, ((size_t)4 * pushers(top) + 2 * top) * 8, s>>>(a);
+    k_beam_merge<<<(unsigned)N, NT, ((size_t)4 * pushers(top) + (FULL + 1) * top) * 8, s>>>(a);
     return fa_launch_check("beam merge");
 }
 
