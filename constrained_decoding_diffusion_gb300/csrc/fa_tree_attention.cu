@@ -1273,7 +1273,7 @@ extern "C" fa_status fa_tree_attention(const fa_kv_cache *cache, int32_t dtype, 
     a.rows = T * a.group;
     a.blocks = (a.rows + 255) / 256;
     const int least = a.rows <= FA_FEW_ROWS ? 16 : TS;   // slots of the smallest tile
-    if ((int64_t)B * cache->kv_heads * a.blocks * ((slots + least - 1) / least + 1 + kUnitCost) > 2147483647)
+    if ((int64_t)B * cache->kv_heads * a.blocks * ((slots + least - 1) / least + 5) > 2147483647)
         return fa_refuse(fn, "B * kv_heads * row blocks * tiles out of range");
     a.q = q; a.qb = q_batch_stride; a.qt = q_token_stride; a.qh = q_head_stride;
     a.length = length; a.count = count; a.mask = mask; a.scale = scale; a.out = out; a.lse = lse;
@@ -1290,7 +1290,7 @@ extern "C" fa_status fa_tree_attention(const fa_kv_cache *cache, int32_t dtype, 
         // against 12 / 15.  16-bit: 32 x 8192 165 / 170 against 176 / 181; 1 x 65536 58 / 65 against
         // 57 / 60; 4 x 509 16 / 20 against 12 / 15.
         a.tile_shift = fa_attend_few_tile_shift(cache->head_dim, e4m3);
-        a.unit_cost = 1;
+        a.unit_cost = 4;                         // 32 ragged sequences of up to 8192 slots: 1 / 2 / 4 / 7 give 74 / 64 / 63 / 64 us
         a.part_rows = FA_FEW_ROWS;
         int ctas = 0;
         const cudaError_t e = block_count(&ctas);
