@@ -217,6 +217,7 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 ? 4 : 2) k_beam_scan(Select
     key_t64 *list = dyn, *work = dyn + (size_t)PER * pushers(a.top) + FULL * a.top;
     const int tid = threadIdx.x, n = blockIdx.y;
     __shared__ uint2 masks[16];
+    fa_let_next_start();
     if (tid == 0) { sh.threshold = 0; sh.count = 0; }
     if (tid < 16)
         masks[tid] = make_uint2((tid & 1 ? 0x0000ffffu : 0u) | (tid & 2 ? 0xffff0000u : 0u), (tid & 4 ? 0x0000ffffu : 0u) | (tid & 8 ? 0xffff0000u : 0u));
@@ -348,6 +349,7 @@ __global__ void __launch_bounds__(NT) k_beam_merge(SelectArgs a) {
     const int tid = threadIdx.x, n = blockIdx.x;
     if (tid == 0) { sh.threshold = 0; sh.count = 0; }
     __syncthreads();
+    fa_wait_for_previous();
     const key_t64 *keys = a.keys + (int64_t)n * a.nb * a.top;
     const int total = a.nb * a.top;
     for (int first = 0; first < total; first += 4 * NT) {
@@ -497,8 +499,7 @@ extern "C" fa_status fa_beam_select(int32_t dtype, int32_t N, int32_t K, int32_t
     const cudaError_t e = dtype == FA_DTYPE_F32 ? go(0.0f) : dtype == FA_DTYPE_F16 ? go(__half()) : go(__nv_bfloat16());
     if (e != cudaSuccess) return fa_refuse(fn, cudaGetErrorString(e), FA_ERR_CUDA);
     if ((st = fa_launch_check("beam scan")) != FA_OK || a.nb == 1) return st;
-    k_beam_merge<<<(unsigned)N, NT, ((size_t)4 * pushers(top) + (FULL + 1) * top) * 8, s>>>(a);
-    return fa_launch_check("beam merge");
+    return fa_launch_second("beam merge", k_beam_merge, dim3((unsigned)N), NT, ((size_t)4 * pushers(top) + (FULL + 1) * top) * 8, s, a);
 }
 
 extern "C" fa_status fa_beam_reorder(int32_t N, int32_t K, int32_t top, int64_t words, const int32_t *src,

@@ -93,7 +93,29 @@ struct fa_cache_view {
     }
 };
 
+// A second kernel of an operator is launched while the first one runs: the first allows it when it
+// starts, the second waits for all of the first's results.
+__device__ __forceinline__ void fa_let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void fa_wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ----------------------------------------------------------------------------- host side
+
+// launch a kernel that calls fa_wait_for_previous() before it touches what the stream's last kernel writes
+template <class... P, class... A>
+fa_status fa_launch_second(const char *what, void (*kernel)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t s, A... args) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c = {};
+    c.gridDim = grid;
+    c.blockDim = dim3(block);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    c.attrs = at;
+    c.numAttrs = 1;
+    (void)cudaLaunchKernelEx(&c, kernel, args...);   // its error is the one the check reads
+    return fa_launch_check(what);
+}
 
 inline fa_status fa_refuse(const char *fn, const char *why, fa_status st = FA_ERR_INVALID_ARG) {
     fa_set_error(std::string(fn) + ": " + why);

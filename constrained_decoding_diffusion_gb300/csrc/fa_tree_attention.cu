@@ -314,6 +314,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a, const __grid_c
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
         tc_fence_before();
     }
+    fa_let_next_start();
     plan(a, work);
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
@@ -1066,10 +1067,12 @@ __global__ void __launch_bounds__(256) k_attend_join(AttendArgs a, int runs, int
     const int c0 = (int)((((int64_t)g0 + 1) * runs - 1) / total), c1 = (int)((((int64_t)g1 + 1) * runs - 1) / total);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, head = u / a.blocks, block = u % a.blocks;
     const int rows = min(a.rows - 256 * block, 256), row0 = RB * blockIdx.y, D = a.c.head_dim, parts = c1 - c0 + 1;
+    fa_wait_for_previous();                     // by every block: the next kernel waits for this one only
+    if (row0 >= rows) return;
     bool failed = false;
     if (statuses)
         for (int c = c0; c <= c1; ++c) failed |= a.status[c] != 0;
-    if ((parts == 1 && !failed) || row0 >= rows) return;
+    if (parts == 1 && !failed) return;
     // of a run's two partial results the second holds a unit's first part
     auto part = [&](int i, int row) { return ((int64_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * a.part_rows + row; };
     auto add = [&](float w, int i, int row, float (&o)[NE]) {
@@ -1189,13 +1192,13 @@ template <int DP, class T> fa_status join(const AttendArgs &a, int runs, int sta
     int rb = 1;
     while (rb < 32 && units * ((rows + rb - 1) / rb) > 8 * MAX_CTAS) rb *= 2;
     const dim3 grid((unsigned)units, (unsigned)((rows + rb - 1) / rb));
-    if (rb == 1) k_attend_join<DP, T, 1><<<grid, 256, 0, s>>>(a, runs, statuses);
-    else if (rb == 2) k_attend_join<DP, T, 2><<<grid, 256, 0, s>>>(a, runs, statuses);
-    else if (rb == 4) k_attend_join<DP, T, 4><<<grid, 256, 0, s>>>(a, runs, statuses);
-    else if (rb == 8) k_attend_join<DP, T, 8><<<grid, 256, 0, s>>>(a, runs, statuses);
-    else if (rb == 16) k_attend_join<DP, T, 16><<<grid, 256, 0, s>>>(a, runs, statuses);
-    else k_attend_join<DP, T, 32><<<grid, 256, 0, s>>>(a, runs, statuses);
-    return fa_launch_check("tree attention join");
+    void (*const kernel)(AttendArgs, int, int) = rb == 1   ? k_attend_join<DP, T, 1>
+                                                 : rb == 2 ? k_attend_join<DP, T, 2>
+                                                 : rb == 4 ? k_attend_join<DP, T, 4>
+                                                 : rb == 8 ? k_attend_join<DP, T, 8>
+                                                 : rb == 16 ? k_attend_join<DP, T, 16>
+                                                            : k_attend_join<DP, T, 32>;
+    return fa_launch_second("tree attention join", kernel, grid, 256, 0, s, a, runs, statuses);
 }
 
 // SMs of the current device, up to the blocks the workspace has room for

@@ -67,6 +67,7 @@ __global__ void __launch_bounds__(32 * NW, 1) k_attend_few(AttendArgs a) {
     constexpr float OFF = std::is_same<M, __half>::value ? 4.0f : 0.0f;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ Work work;
+    fa_let_next_start();
     plan(a, work);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3, D = a.c.head_dim;
     const int run = blockIdx.x * NW + warp;
