@@ -15,8 +15,8 @@
 // The floor is memory: logp and the live bits once.  Measured, 16 sequences of 16 beams of 151936
 // tokens in bf16, a tenth of them live, top 16: 47 us for the scan (1.7 TB/s), 7 for the merge; without
 // any cell that passes the scan takes 22, so what bounds it is the threshold's rise (about six of a
-// block's eight batches still hold a cell that passes) and the barriers around it, not the loads.
-// One list of 4 beams of 32000 tokens: 22 us with the reordering, three launches' start and end.
+// block's eight batches still hold a cell that passes) and the barriers around it, not the loads.  55 us in all with the
+// reordering.  One list of 4 beams of 32000 tokens: 22 us with the reordering, three launches' start and end.
 #include "fa_lm.cuh"
 
 namespace {

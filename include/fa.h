@@ -441,7 +441,7 @@ fa_status fa_cache_write(const fa_kv_cache *cache, int32_t dtype, int32_t B, int
 /*
  * fa_cache_read -- slots [0, min(length[b], N)) of every sequence back as dense arrays
  * k_out, v_out [B, N, kv_heads, head_dim] (contiguous, dtype FA_DTYPE_*, 16-byte aligned);
- * code * scale in fp32, rounded once; the rows past length[b] are set to zero.
+ * code * scale in fp32, rounded once; the rows past length[b] are set to zero.  B <= 65535.
  * Errors: FA_ERR_INVALID_ARG, FA_ERR_CUDA.
  */
 fa_status fa_cache_read(const fa_kv_cache *cache, int32_t dtype, int32_t B, int32_t N, const int32_t *page_table,
@@ -486,12 +486,17 @@ fa_status fa_tree_mask(int32_t B, int32_t T, const int32_t *parents, uint64_t *m
  *                drafted token sees all drafted tokens (a block being denoised)
  *   out          [B, T, q_heads, head_dim] contiguous, 16-byte aligned
  *   lse          [B, T, q_heads] fp32 or NULL: ln sum_t exp(scale * q . k)
+ *   scale        positive and finite
  *   workspace    fa_tree_attention_workspace_bytes() bytes, 256-byte aligned; contents are
  *                overwritten; concurrent calls need separate workspaces
  * A row that sees nothing gives out = 0 and lse = -inf.  What a row does not see has no part in its result,
  * whatever it holds (NaN and infinities included).  Scores, softmax statistics and sums are
  * fp32; the softmax weights are rounded to 16 bits for the product with the values.
- * T <= FA_MAX_DRAFT, B <= 65535.
+ * The same call gives the same bits.  Should a wait inside the kernel run out (about a second), the rows it
+ * held up are NaN.
+ * T <= FA_MAX_DRAFT, B <= 65535, T * group <= 2^24, max_pages * page_size < 2^31 - 4096,
+ * n_pages * kv_heads < 2^31, and B * kv_heads * ceil(T * group / 256) units of
+ * max_pages * page_size / 128 tiles each (/ 16 where T * group <= 16) stay below 2^31 tiles.
  * Errors: FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED (types, head_dim), FA_ERR_WORKSPACE_TOO_SMALL,
  * FA_ERR_CUDA.
  */
