@@ -52,14 +52,15 @@ __global__ void __launch_bounds__(NT) k_rope_any(RopeArgs a) {
 
 // The same in 16-byte vectors of N elements, where every row is aligned and the rotated part is
 // whole vectors (half layout: each half).  The bound is memory: x is read and out written
-// once.  A block takes up to eight tokens with all their heads.  Their sines and cosines, one per
+// once.  A block takes a few tokens with all their heads.  Their sines and cosines, one per
 // token and pair, are made once in shared memory while the first vectors are on their way; a
 // thread keeps its place (head and vector) and walks the tokens, four of them under way at a time,
 // so the arithmetic of places is done once.  Measured, 8192 tokens of 32 heads of 128 in bf16, half of a head
-// rotated: 22 us (134 MB, 6.1 TB/s, nine tenths of a copy).
-constexpr int ROPE_TOKENS = 8;
+// rotated: 25 us (134 MB, 5.4 TB/s, four fifths of a copy).
+constexpr int ROPE_TOKENS = 16;
+template <class T> constexpr int rope_blocks() { return sizeof(T) == 4 ? 0 : 4; }   // of an SM at least (0: no bound), without spills
 template <class T, bool INTERLEAVED>
-__global__ void __launch_bounds__(NT) k_rope(RopeArgs a, int tokens) {
+__global__ void __launch_bounds__(NT, rope_blocks<T>()) k_rope(RopeArgs a, int tokens) {
     // [tokens][pair of a vector][vector]: neighbouring lanes' pairs lie side by side
     extern __shared__ float2 table[];
     constexpr int N = fa_vec<T>::N, U = 4, P = INTERLEAVED ? N / 2 : N;
@@ -137,13 +138,23 @@ template <class T> fa_status launch_rope(const RopeArgs &a, cudaStream_t s) {
         k_rope_any<T><<<blocks_for(items), NT, 0, s>>>(a);
         return fa_launch_check("rope");
     }
-    // fewer tokens where that leaves SMs without a block
-    const int tokens = (int)std::min<int64_t>(ROPE_TOKENS, std::max<int64_t>(1, a.n_tokens / (152 * 4)));
+    // Tokens of a block: 16-bit types, as many as make full waves of four blocks an SM (8192 tokens x 32 heads x
+    // 128: 23.4 us, 25.7 half rotated, against 23.7 and 28.6 with eight whatever the count); fp32, twice the bytes
+    // a token, up to eight and fewer where that leaves SMs without a block (43 us against 46.7 with full waves).
+    int64_t tokens;
+    if (sizeof(T) == 4) {
+        tokens = std::min<int64_t>(8, std::max<int64_t>(1, a.n_tokens / (152 * 4)));
+    } else {
+        const int64_t resident = 152 * rope_blocks<T>();
+        const int64_t most = std::min<int64_t>(ROPE_TOKENS, 40960 / std::max<int64_t>(1, a.rot / 2 * (int64_t)sizeof(float2)));
+        const int64_t waves = (a.n_tokens + resident * most - 1) / (resident * most);
+        tokens = (a.n_tokens + resident * waves - 1) / (resident * waves);
+    }
     const int64_t blocks = (a.n_tokens + tokens - 1) / tokens;
     if (blocks > 2147483647) return fa_refuse("fa_rope", "too many tokens");
-    const size_t smem = (size_t)tokens * (a.rot / 2) * sizeof(float2);   // at most 8 * 512 * 8 bytes
-    if (a.interleaved) k_rope<T, true><<<(unsigned)blocks, NT, smem, s>>>(a, tokens);
-    else k_rope<T, false><<<(unsigned)blocks, NT, smem, s>>>(a, tokens);
+    const size_t smem = (size_t)tokens * (a.rot / 2) * sizeof(float2);   // at most 40 KB
+    if (a.interleaved) k_rope<T, true><<<(unsigned)blocks, NT, smem, s>>>(a, (int)tokens);
+    else k_rope<T, false><<<(unsigned)blocks, NT, smem, s>>>(a, (int)tokens);
     return fa_launch_check("rope");
 }
 
