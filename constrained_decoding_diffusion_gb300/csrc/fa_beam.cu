@@ -13,10 +13,11 @@
 // looks up the states.
 //
 // The floor is memory: logp and the live bits once.  Measured, 16 sequences of 16 beams of 151936
-// tokens in bf16, a tenth of them live, top 16: 47 us for the scan (1.7 TB/s), 7 for the merge; without
-// any cell that passes the scan takes 22, so what bounds it is the threshold's rise (about six of a
-// block's eight batches still hold a cell that passes) and the barriers around it, not the loads.  55 us in all with the
-// reordering.  One list of 4 beams of 32000 tokens: 22 us with the reordering, three launches' start and end.
+// tokens in bf16, a tenth of them live, top 16: 47 us for the scan (1.7 TB/s), 55 with merge and
+// reordering; without any cell that passes the scan takes 22, so what bounds it is the threshold's
+// rise (about six of a block's eight batches still hold a cell that passes) and the barriers around it,
+// not the loads.  4 beams of 32000 tokens: 21 us with the reordering, three launches' start and end (22.5
+// if a block with a single batch takes a threshold first, too).
 #include "fa_lm.cuh"
 
 namespace {
@@ -265,8 +266,8 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 ? 4 : 2) k_beam_scan(Select
     };
     // Beams differ by whole units of score, so a block that meets a poor one first would fill its list
     // in vain: every block looks at one batch of the best beam before its own ones, only for a
-    // threshold (-1), unless it starts there anyway.
-    bool look = (int)blockIdx.x / per_beam != best_beam;
+    // threshold, unless it starts there anyway or has a single batch.
+    bool look = batches > (int)gridDim.x && (int)blockIdx.x / per_beam != best_beam;
     Cells next = find(look ? best_beam * per_beam + (int)blockIdx.x % per_beam : blockIdx.x);
     for (int bt = look ? (int)blockIdx.x - (int)gridDim.x : (int)blockIdx.x; bt < batches; bt += gridDim.x, look = false) {
         const Cells c = next;
