@@ -45,7 +45,7 @@ __device__ __forceinline__ float key_value(key_t64 k) {
 struct BestShared {
     key_t64 maxima[NT];
     key_t64 threshold;
-    int count;
+    int count, kept, sums[2][NT / 32];
 };
 
 // threads that may push in one offer
@@ -70,7 +70,8 @@ __device__ __forceinline__ key_t64 raise(BestShared &sh, int top, key_t64 best) 
 #pragma unroll
     for (int w = 1; w < NT / 32; ++w) t = min(t, sh.maxima[w]);
     t = t ? t - 1 : 0;                             // the least of them still passes
-    if (__syncthreads_count(best > t) <= pushers(top)) return t;
+    const int n = __syncthreads_count(best > t);
+    if (n <= pushers(top) && (t || n < top)) return t;
     sh.maxima[tid] = best;
     __syncthreads();
     int rank = 0;
@@ -84,21 +85,50 @@ __device__ __forceinline__ key_t64 raise(BestShared &sh, int top, key_t64 best) 
 // Offer the threads' keys.  pass says whether a thread has one that may be above the threshold,
 // best() gives its largest (0 where none can pass) and is asked for only where more threads pass than the
 // list has room for; push(t, pass, put) calls put for each key above t of the threads that pass.
-// Called by all threads of the block.  The list is put in order, and the threshold raised, when it holds
-// twice `top` keys, or `top` before there is a threshold.
+// Called by all threads of the block.  The list is cut back to its best `top`, and the threshold raised,
+// when it holds twice as many, or `top` before there is a threshold.
 constexpr int FULL = 2;
+// Keys beyond which a list is searched bit by bit (about 40 counts) and not ranked (a comparison per pair
+// of keys).  A list of thousands comes from a first batch with a large `top`: 50257 tokens, top 256, 2030 us
+// with ranks alone, 40 to 63 with the search; lists of tens, the common ones, are ranked in less than a
+// search's barriers.
+constexpr int LONG = 512;
 __device__ __forceinline__ void keep_best(BestShared &sh, key_t64 *list, key_t64 *work, int top) {
     const int tid = threadIdx.x, m = sh.count;
     if (m <= top && sh.threshold) return;
-    for (int i = tid; i < m; i += NT) {
-        const key_t64 k = list[i];
-        int rank = 0;
-        for (int j = 0; j < m; ++j) rank += list[j] > k;
-        if (rank < top) work[rank] = k;
+    key_t64 least = 0;                             // the smallest of the best `top`
+    if (m <= LONG) {
+        for (int i = tid; i < m; i += NT) {
+            const key_t64 k = list[i];
+            int rank = 0;
+            for (int j = 0; j < m; ++j) rank += list[j] > k;
+            if (rank < top) work[rank] = k;
+        }
+        __syncthreads();
+        if (m >= top) least = work[top - 1];
+    } else {
+        // bit by bit the largest number that `top` keys reach, until just so many do
+        for (int bit = 63; bit >= 0; --bit) {
+            const key_t64 t = least | (key_t64)1 << bit;
+            int n = 0;
+            for (int i = tid; i < m; i += NT) n += list[i] >= t;
+            n = __reduce_add_sync(0xffffffffu, n);
+            if (tid % 32 == 0) sh.sums[bit & 1][tid / 32] = n;
+            __syncthreads();
+            n = 0;
+#pragma unroll
+            for (int w = 0; w < NT / 32; ++w) n += sh.sums[bit & 1][w];
+            if (n >= top) least = t;
+            if (n == top) break;
+        }
+        if (tid == 0) sh.kept = 0;
+        __syncthreads();
+        for (int i = tid; i < m; i += NT)
+            if (list[i] >= least) work[atomicAdd(&sh.kept, 1)] = list[i];
+        __syncthreads();
     }
-    __syncthreads();
     for (int i = tid; i < min(m, top); i += NT) list[i] = work[i];
-    if (tid == 0 && m >= top) { sh.count = top; sh.threshold = max(sh.threshold, work[top - 1]); }
+    if (tid == 0 && m >= top) { sh.count = top; sh.threshold = max(sh.threshold, least); }
     __syncthreads();
 }
 template <class B, class F>
@@ -106,9 +136,9 @@ __device__ __forceinline__ void offer(BestShared &sh, key_t64 *list, key_t64 *wo
     key_t64 thr = sh.threshold;
     const int above = __syncthreads_count(pass);
     if (!above) return;
-    if (above > pushers(top)) {
+    if (above > pushers(top) || (!thr && above >= top)) {
         const key_t64 mine = pass ? best() : 0;
-        if (__syncthreads_count(mine > thr) > pushers(top)) thr = max(thr, raise(sh, top, mine));
+        if (__syncthreads_count(mine > thr) > pushers(top) || !thr) thr = max(thr, raise(sh, top, mine));
         pass = mine > thr;
     }
     push(thr, pass, [&](key_t64 k) { list[atomicAdd(&sh.count, 1)] = k; });
