@@ -13,10 +13,10 @@
 // looks up the states.
 //
 // The floor is memory: logp and the live bits once.  Measured, 16 sequences of 16 beams of 151936
-// tokens in bf16, a tenth of them live, top 16: 47 us for the scan (1.7 TB/s), 55 with merge and
-// reordering; without any cell that passes the scan takes 22, so what bounds it is the threshold's
-// rise (about six of a block's eight batches still hold a cell that passes) and the barriers around it,
-// not the loads.  4 beams of 32000 tokens: 21 us with the reordering, three launches' start and end (22.5
+// tokens in bf16, a tenth of them live, top 16: 48 us with merge and reordering, of which the scan about
+// 40 (2 TB/s); without any cell that passes the scan takes 22, so what bounds it is the threshold's
+// rise (most of a block's eight batches still hold a cell that passes) and the barriers around it,
+// not the loads.  4 beams of 32000 tokens: 20 us with the reordering, three launches' start and end (2 more
 // if a block with a single batch takes a threshold first, too).
 #include "fa_lm.cuh"
 
@@ -51,10 +51,10 @@ struct BestShared {
 // threads that may push in one offer
 __host__ __device__ constexpr int pushers(int top) { return 4 * top < NT ? 4 * top : NT; }
 
-// A key that at least `top` of the threads' best keys reach, and at most pushers(top) exceed (given
-// that more than that exceed the present threshold).  A warp's k-th largest key, k = top / 8
-// rounded up: the smallest of the eight warps' will do, and usually few enough are above it; where
-// not, the top-th largest of all by counting.
+// A key that at least `top` of the threads' best keys reach and at most pushers(top) exceed, or 0 where fewer
+// than `top` threads have one.  A warp's k-th largest key, k = top / 8 rounded up: the smallest of the
+// eight warps' will do, and usually few enough are above it; where not, or where a warp has fewer, the
+// top-th largest of all by counting.
 __device__ __forceinline__ key_t64 raise(BestShared &sh, int top, key_t64 best) {
     const int tid = threadIdx.x;
     key_t64 x = best, kth = 0;
