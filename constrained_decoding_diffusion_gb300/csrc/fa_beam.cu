@@ -13,8 +13,8 @@
 // looks up the states.
 //
 // The floor is memory: logp and the live bits once.  Measured, 16 sequences of 16 beams of 151936
-// tokens in bf16, a tenth of them live, top 16: 48 us with merge and reordering, of which the scan about
-// 40 (2 TB/s); without any cell that passes the scan takes 22, so what bounds it is the threshold's
+// tokens in bf16, a tenth of them live, top 16: 48 us with merge and reordering, of which the scan
+// 41 (2 TB/s); without any cell that passes the scan takes 22, so what bounds it is the threshold's
 // rise (most of a block's eight batches still hold a cell that passes) and the barriers around it,
 // not the loads.  4 beams of 32000 tokens: 20 us with the reordering, three launches' start and end (2 more
 // if a block with a single batch takes a threshold first, too).
