@@ -194,7 +194,11 @@ struct Misc {
     uint32_t raw_rows[8][4];          // which rows of a raw tile were copied
     uint32_t tmem;
     int fail;
-    int odd[8];                       // segment & 7: a drafted value is not finite
+    // A drafted value, or a scale, that is not finite is marked by its segment's number, so that nothing
+    // has to be cleared: the loading warps, at most six segments ahead of stream 0, by odd[segment & 7];
+    // each stream by an entry of its own, since stream 1 passes over segments of a single tile and may be
+    // any number of them ahead of stream 0.
+    int odd[8], odd_scale[2];         // 1 + the last segment that was marked
     int hole[16];                     // key tile & 15: a slot of the tile has no page or lies past the end
     float vtop[2][4];                 // per stream: the largest value scale of 32 slots
 };
@@ -306,6 +310,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a, const __grid_c
         mbar_init(&sh.done, 1);
         sh.fail = 0;
         for (int i = 0; i < 8; ++i) sh.odd[i] = 0;
+        sh.odd_scale[0] = sh.odd_scale[1] = 0;
         for (int i = 0; i < 16; ++i) sh.hole[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -589,7 +594,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a, const __grid_c
                     }
 #pragma unroll
                     for (int q = 0; q < x.ITER; ++q) {
-                        if (first + q * STEP >= (uint32_t)f.s.slots && zero_odd<M>(v[q])) sh.odd[f.seg & 7] = 1;
+                        if (first + q * STEP >= (uint32_t)f.s.slots && zero_odd<M>(v[q])) sh.odd[f.seg & 7] = f.seg + 1;
                         *reinterpret_cast<uint4 *>(dst + q * STEP * 128) = v[q];
                     }
                 }
@@ -626,7 +631,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a, const __grid_c
                                           fa_e4m3x2_to_half2(w[q].w), fa_e4m3x2_to_half2(w[q].w >> 16));
                     if (odd_from != 0xffffffffu && r0 + q * STEP >= (int)odd_from) {
                         const bool o1 = zero_odd<M>(lo), o2 = zero_odd<M>(hi);
-                        if (o1 || o2) sh.odd[f.seg & 7] = 1;
+                        if (o1 || o2) sh.odd[f.seg & 7] = f.seg + 1;
                     }
                     *reinterpret_cast<uint4 *>(dst + to0 + q * STEP * 128) = lo;
                     *reinterpret_cast<uint4 *>(dst + to1 + q * STEP * 128) = hi;
@@ -740,7 +745,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a, const __grid_c
                     for (int o = 16; o; o >>= 1) vt = fmaxf(vt, __shfl_xor_sync(0xffffffffu, vt, o));
                     if (q > 0) scales_sync();             // the previous tile's have been read
                     if (lane == 0) sh.vtop[st][warp & 3] = vt;
-                    if (first + r >= s.slots && !(fabsf(vs) < INFINITY)) { vs = 0.0f; sh.odd[sg & 7] = 1; }
+                    if (first + r >= s.slots && !(fabsf(vs) < INFINITY)) { vs = 0.0f; sh.odd_scale[st] = sg + 1; }
                     sc.k[st][r] = ks;
                     sc.v[st][r] = vs;
                     if (q + 1 < mine) {
@@ -868,6 +873,10 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a, const __grid_c
             mbar_wait(&sh.pv_done[st], (uint32_t)npv++ & 1, fail);
             __syncwarp();
             tc_fence_after();
+            // (after the streams' barrier where both had tiles of the segment)
+            auto any_odd = [&]() {
+                return sh.odd[sg & 7] == sg + 1 || sh.odd_scale[0] == sg + 1 || sh.odd_scale[1] == sg + 1;
+            };
             const bool pair_up = !s.two() && s.n > 1, join = pair_up && copies == 1, partial = s.n < s.nt;
             // of the block's partial results, slot 1 is a unit's first part, slot 0 a later one
             const int64_t prow0 = ((int64_t)blockIdx.x * 2 + (s.t0 == 0 ? 1 : 0)) * 256;
@@ -895,7 +904,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a, const __grid_c
                     if (!(li == 0.0f)) sum += li * ex2(stats[at] - top);
                 }
                 const float f = l == 0.0f || !used ? 0.0f : ex2(bias - top) * (pow2(ev) / sum);
-                const bool odd = sh.odd[sg & 7] != 0;
+                const bool odd = any_odd();
                 const int groups = cols / 4, part = st * copies + copy;
 #pragma unroll 1
                 for (int col0 = 0; col0 < DP; col0 += cols) {
@@ -943,7 +952,6 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a, const __grid_c
                 }
                 tc_fence_before();
                 sync();
-                if (tid == 0) sh.odd[sg & 7] = 0;
                 continue;
             }
             float f0 = 0.0f, f1 = 0.0f;
@@ -966,7 +974,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a, const __grid_c
                 f0 = pow2(ev) / l;
             }
             if (st == 0 || s.two()) {
-                const bool odd = sh.odd[sg & 7] != 0;
+                const bool odd = any_odd();
                 const int64_t orow = ((int64_t)s.b * a.T + ti) * a.heads + hq, prow = prow0 + row;
                 if (warp_live) {
                     // Rows leave through shared memory (the stream's queries are done with), so that a
@@ -1027,10 +1035,9 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a, const __grid_c
                 }
             }
             tc_fence_before();
-            // stream 1 may go on: its accumulator has been read, and so has the segment's flag
+            // stream 1 may go on: its accumulator and its mark have been read
             if (join || s.two()) bar_sync(3, 2 * TS);
             else bar_sync(1 + st, TS);
-            if (tid == 0) sh.odd[sg & 7] = 0;
         }
     }
     __syncwarp();
