@@ -203,20 +203,23 @@ __device__ __forceinline__ uint32_t live_word(const uint32_t *row, int words, in
     return m;
 }
 
-__device__ void store_cell(const SelectArgs &a, int n, int i, key_t64 k) {
-    const int64_t at = (int64_t)n * a.top + i;
-    if (!k) {
-        a.out_score[at] = -INFINITY;
-        a.out_parent[at] = a.out_token[at] = -1;
-        if (a.out_state) a.out_state[at] = -1;
-        return;
-    }
+// The sequence's cells from their keys in order, a thread each (0: none).  The beams' scores and states may
+// lie where the results go, so every parent's state is read before the first result is written.
+__device__ void store_cells(const SelectArgs &a, int n, const key_t64 *keys) {
+    static_assert(FA_MAX_BEAM_TOP <= NT, "a thread per result");
+    const int i = threadIdx.x;
+    const key_t64 k = i < a.top ? keys[i] : 0;
     const uint32_t flat = 0xffffffffu - (uint32_t)k;
-    const int parent = (int)(flat / (uint32_t)a.V), token = (int)(flat % (uint32_t)a.V);
-    a.out_score[at] = key_value(k);
+    const int parent = k ? (int)(flat / (uint32_t)a.V) : -1, token = k ? (int)(flat % (uint32_t)a.V) : -1;
+    int state = -1;
+    if (k && a.out_state) state = a.next[(int64_t)a.states[(int64_t)n * a.K + parent] * a.V + token];
+    __syncthreads();
+    if (i >= a.top) return;
+    const int64_t at = (int64_t)n * a.top + i;
+    a.out_score[at] = k ? key_value(k) : -INFINITY;
     a.out_parent[at] = parent;
     a.out_token[at] = token;
-    if (a.out_state) a.out_state[at] = a.next[(int64_t)a.states[(int64_t)n * a.K + parent] * a.V + token];
+    if (a.out_state) a.out_state[at] = state;
 }
 
 // write the block's best keys: to the outputs when it is the sequence's only block
@@ -233,7 +236,7 @@ __device__ void finish(const SelectArgs &a, BestShared &sh, key_t64 *list, key_t
             work[rank] = list[i];
         }
         __syncthreads();
-        for (int i = tid; i < a.top; i += NT) store_cell(a, n, i, work[i]);
+        store_cells(a, n, work);
     } else {
         key_t64 *out = a.keys + ((int64_t)n * a.nb + blockIdx.x) * a.top;
         for (int i = tid; i < a.top; i += NT) out[i] = i < m ? list[i] : 0;
@@ -512,6 +515,16 @@ extern "C" fa_status fa_beam_select(int32_t dtype, int32_t N, int32_t K, int32_t
     if (ws_bytes < need || (need && !workspace))
         return fa_refuse(fn, ("workspace needs " + std::to_string(need) + " bytes").c_str(), FA_ERR_WORKSPACE_TOO_SMALL);
     if ((uintptr_t)workspace & 255) return fa_refuse(fn, "workspace not 256-byte aligned");
+    // a sequence's scores and states are read before its results are written, other sequences' may be read later
+    const size_t in = (size_t)N * K * 4, out = (size_t)N * top * 4;
+    const bool same_rows = K == top || N == 1;
+    auto in_place = [&](const void *x, const void *y) { return same_rows && x == y; };
+    if ((fa_overlap(scores, in, out_score, out) && !in_place(scores, out_score)) || fa_overlap(scores, in, out_parent, out) ||
+        fa_overlap(scores, in, out_token, out) || (aut && fa_overlap(scores, in, out_state, out)))
+        return fa_refuse(fn, "scores overlaps an output");
+    if (aut && ((fa_overlap(states, in, out_state, out) && !in_place(states, out_state)) || fa_overlap(states, in, out_score, out) ||
+                fa_overlap(states, in, out_parent, out) || fa_overlap(states, in, out_token, out)))
+        return fa_refuse(fn, "states overlaps an output");
     a.logp = logp; a.ln = logp_seq_stride; a.lk = logp_beam_stride;
     a.scores = scores; a.states = states; a.next = next; a.live = live;
     a.keys = (key_t64 *)workspace;

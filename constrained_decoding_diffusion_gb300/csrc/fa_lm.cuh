@@ -122,6 +122,10 @@ inline fa_status fa_refuse(const char *fn, const char *why, fa_status st = FA_ER
     return st;
 }
 
+inline bool fa_overlap(const void *x, size_t x_bytes, const void *y, size_t y_bytes) {
+    return (uintptr_t)x < (uintptr_t)y + y_bytes && (uintptr_t)y < (uintptr_t)x + x_bytes;
+}
+
 inline bool fa_dtype_ok(int32_t dtype) { return dtype >= FA_DTYPE_F32 && dtype <= FA_DTYPE_BF16; }
 inline int fa_dtype_bytes(int32_t dtype) { return dtype == FA_DTYPE_F32 ? 4 : 2; }
 

@@ -84,7 +84,6 @@ class Drafting:
             # every beam reads the position's one row
             scores, parent, token, states = select(logp[:, t:t + 1].expand(B, hist.shape[1], -1), scores, states, self.next, self.live)
             hist = lm.fa_beam_reorder(hist, parent, token=token, at=t)
-            scores, states = scores.clone(), states.clone()     # the next selection writes where these lie
         return hist
 
     def verify(self, hist):

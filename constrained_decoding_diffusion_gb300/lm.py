@@ -313,7 +313,9 @@ def fa_beam_tables(aut: native.CompiledAutomaton, stream=None):
 
 
 class BeamSelect:
-    """Owner of the workspace and outputs of fa_beam_select for a fixed (N, K, V, top)."""
+    """Owner of the workspace and outputs of fa_beam_select for a fixed (N, K, V, top).  A call
+    returns the owner's own tensors, which the next one overwrites; with K == top they may be its
+    scores and states."""
 
     def __init__(self, N: int, K: int, V: int, top: int, dtype=torch.float32, device="cuda"):
         n = ctypes.c_size_t()

@@ -530,7 +530,9 @@ fa_status fa_beam_tables(const fa_automaton *aut, int16_t *next, uint32_t *live,
  *              [0, S) is dead.  All three NULL (S = 0): no automaton
  *   top        in [1, FA_MAX_BEAM_TOP]
  *   out_score  [N, top] fp32, out_parent, out_token [N, top] int32, out_state [N, top] int32
- *              (NULL without an automaton): past the last selectable cell -inf and -1
+ *              (NULL without an automaton): past the last selectable cell -inf and -1.
+ *              out_score may be scores and out_state may be states where K == top or N == 1 (a loop
+ *              that selects in place); outputs may not overlap inputs otherwise
  *   workspace  fa_beam_select_workspace_bytes() bytes, 256-byte aligned
  * K * V < 2^31.  Errors: FA_ERR_INVALID_ARG, FA_ERR_WORKSPACE_TOO_SMALL, FA_ERR_CUDA.
  */
