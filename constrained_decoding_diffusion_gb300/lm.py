@@ -148,20 +148,22 @@ def fa_rope(x, positions, phase, out=None, interleaved: bool = False, mscale: fl
 
 
 class Rope(torch.autograd.Function):
-    """fa_rope with its gradient: Rope.apply(x, positions, phase, interleaved, mscale)."""
+    """fa_rope with its gradient: Rope.apply(x, positions, phase, interleaved, mscale, inverse).  The map
+    is linear and its transpose the inverse rotation, so the gradient is the same function and
+    has derivatives of any order."""
 
     @staticmethod
-    def forward(ctx, x, positions, phase, interleaved=False, mscale=1.0):
+    def forward(ctx, x, positions, phase, interleaved=False, mscale=1.0, inverse=False):
         ctx.save_for_backward(positions, phase)
-        ctx.how = (interleaved, mscale)
-        return fa_rope(x, positions, phase, interleaved=interleaved, mscale=mscale)
+        ctx.how = (interleaved, mscale, not inverse)
+        return fa_rope(x, positions, phase, interleaved=interleaved, mscale=mscale, inverse=inverse)
 
     @staticmethod
     def backward(ctx, grad):
         positions, phase = ctx.saved_tensors
         if grad.stride(-1) != 1:   # a broadcast gradient, as of a sum
             grad = grad.contiguous()
-        return fa_rope(grad, positions, phase, interleaved=ctx.how[0], mscale=ctx.how[1], inverse=True), None, None, None, None
+        return Rope.apply(grad, positions, phase, *ctx.how), None, None, None, None, None
 
 
 # ------------------------------------------------------------------ the cache
