@@ -477,6 +477,9 @@ int select_blocks(int N, int K, int V) {
 
 fa_status select_sizes(const char *fn, int32_t N, int32_t K, int32_t V, int32_t top) {
     if (N < 0 || N > 65535 || K < 1 || V < 1 || (int64_t)K * V >= 2147483648LL) return fa_refuse(fn, "N, K or V out of range");
+    // the scan counts a row's cells in 32 bits up to two batches past its end, and beams and batches (where V is
+    // small as many as beams) up to a launch's blocks past theirs
+    if (std::max(K, V) > 2147483647 - 2 * BATCH) return fa_refuse(fn, "K or V out of range");
     if (top < 1 || top > FA_MAX_BEAM_TOP) return fa_refuse(fn, "top must be in [1, FA_MAX_BEAM_TOP]");
     return FA_OK;
 }

@@ -534,7 +534,8 @@ fa_status fa_beam_tables(const fa_automaton *aut, int16_t *next, uint32_t *live,
  *              out_score may be scores and out_state may be states where K == top or N == 1 (a loop
  *              that selects in place); outputs may not overlap inputs otherwise
  *   workspace  fa_beam_select_workspace_bytes() bytes, 256-byte aligned
- * K * V < 2^31.  Errors: FA_ERR_INVALID_ARG, FA_ERR_WORKSPACE_TOO_SMALL, FA_ERR_CUDA.
+ * N <= 65535, K * V < 2^31, K and V < 2^31 - 2^14.
+ * Errors: FA_ERR_INVALID_ARG, FA_ERR_WORKSPACE_TOO_SMALL, FA_ERR_CUDA.
  */
 #define FA_MAX_BEAM_TOP 256
 fa_status fa_beam_select_workspace_bytes(int32_t N, int32_t K, int32_t V, int32_t top, size_t *bytes);
