@@ -13,6 +13,10 @@ constexpr float kGrow = 6.0f;                // how far a score may exceed the r
 // add up in fp32, and smaller values lose bits of their weights.
 constexpr int kLeastScale = -108;
 
+// Beyond this a reference, times the scale, is rounded so coarsely that a row's largest weight could leave the
+// range of fp32 (at 2^30), so scores are taken less the largest one first, which is one more instruction each.
+constexpr float kFar = 4194304.0f;
+
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");

@@ -809,14 +809,15 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a, const __grid_c
                         float f = 1.0f;
                         if (move) {
                             const bool had = m > -INFINITY;
-                            const float bias0 = bias;
-                            const int ev0 = ev;
+                            const float m0 = m, up = E4M3 ? (float)e2 - (float)ev : 0.0f;
                             m = fmaxf(m, mx);
                             ev = e2;
                             const float b2 = m * c + (E4M3 ? (float)ev : 0.0f) - OFF;
-                            f = had ? ex2(bias - b2) : 0.0f;
+                            // (m0 - m) c - up, exactly that of the weights' references
+                            const float by = fmaxf(fabsf(bias), fabsf(b2)) > kFar ? (m0 - m) * c - up : bias - b2;
+                            f = had ? ex2(by) : 0.0f;
                             bias = b2;
-                            l *= E4M3 ? (had ? ex2((float)ev - (float)ev0 + (bias0 - b2)) : 0.0f) : f;
+                            l *= E4M3 ? (had ? ex2(up + by) : 0.0f) : f;
                         }
                         if (q > 0) {
                             // (the previous tile's values were added before these scores were made)
@@ -830,17 +831,22 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a, const __grid_c
                             }
                         }
                     }
+                    const bool far = fabsf(bias) > kFar, any_far = __any_sync(0xffffffffu, far);
+                    const float ref = far ? (E4M3 ? (float)ev : 0.0f) - OFF : bias;
                     float sum[4] = {0, 0, 0, 0};
 #pragma unroll 1
                     for (int w = w_begin; w < w_end; ++w) {
                         uint32_t p[16];
                         if (copies < 4) load_chunk(w, seen(w));   // else the one chunk is still there
+                        if (any_far)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) x[e] = far ? x[e] - m : x[e];
 #pragma unroll
                         for (int e = 0; e < 32; e += 4) {
                             float y[4];
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                y[j] = ex2(fmaf(x[e + j], c, -bias));
+                                y[j] = ex2(fmaf(x[e + j], c, -ref));
                                 sum[j] += y[j];
                             }
                             if (E4M3) {

@@ -311,20 +311,28 @@ __global__ void __launch_bounds__(32 * NW, 1) k_attend_few(AttendArgs a) {
                 f[h] = 1.0f;
                 if (mx > -INFINITY && ((mx - m[h]) * c[h] > kGrow || e2 > ev[h] || m[h] == -INFINITY)) {
                     const bool had = m[h] > -INFINITY;
-                    const float bias0 = bias[h];
-                    const int ev0 = ev[h];
+                    const float m0 = m[h], up = E4M3 ? (float)e2 - (float)ev[h] : 0.0f;
                     m[h] = fmaxf(m[h], mx);
                     ev[h] = e2;
                     const float b2 = m[h] * c[h] + (E4M3 ? (float)ev[h] : 0.0f) - OFF;
-                    f[h] = had ? ex2(bias[h] - b2) : 0.0f;
+                    const float by = fmaxf(fabsf(bias[h]), fabsf(b2)) > kFar ? (m0 - m[h]) * c[h] - up : bias[h] - b2;
+                    f[h] = had ? ex2(by) : 0.0f;
                     bias[h] = b2;
-                    l[h] *= E4M3 ? (had ? ex2((float)ev[h] - (float)ev0 + (bias0 - b2)) : 0.0f) : f[h];
+                    l[h] *= E4M3 ? (had ? ex2(up + by) : 0.0f) : f[h];
                     moved = true;
                 }
+                const bool far = fabsf(bias[h]) > kFar;
+                const float ref = far ? (E4M3 ? (float)ev[h] : 0.0f) - OFF : bias[h];
+                if (__any_sync(0xffffffffu, far))
+#pragma unroll
+                    for (int nb = 0; nb < NBK; ++nb) {
+                        x[nb][2 * h] -= far ? m[h] : 0.0f;
+                        x[nb][2 * h + 1] -= far ? m[h] : 0.0f;
+                    }
                 float sum = 0.0f;
 #pragma unroll
                 for (int nb = 0; nb < NBK; ++nb) {
-                    float y0 = ex2(fmaf(x[nb][2 * h], c[h], -bias[h])), y1 = ex2(fmaf(x[nb][2 * h + 1], c[h], -bias[h]));
+                    float y0 = ex2(fmaf(x[nb][2 * h], c[h], -ref)), y1 = ex2(fmaf(x[nb][2 * h + 1], c[h], -ref));
                     sum += y0 + y1;
                     if (E4M3) { y0 *= vv[nb].x; y1 *= vv[nb].y; }
                     p[nb][h] = fa_pack2(y0, y1, M());
