@@ -8,10 +8,13 @@ namespace fa_attention {
 constexpr int MAX_CTAS = 152;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 6.0f;                // how far a score may exceed the reference (log2)
-// Weights are multiplied by a power of two that brings the largest value scale seen to one, their own
-// sum without it.  The power ends at scales of 2^-108: a tile's weights, up to 2^(kGrow + 4 + 108) each,
-// add up in fp32, and smaller values lose bits of their weights.
-constexpr int kLeastScale = -108;
+// With an 8-bit cache a weight is rounded together with its value's scale.  The reference follows the
+// largest such product a row has met: it lies a whole power of two from the largest score's, and the
+// weights' own sum is kept without that power.  The power ends at 2^-108, where a tile's weights, up to
+// 2^(kGrow + 4 + 108) each, still add up in fp32 (smaller values lose bits of their weights), and at 2^120.
+constexpr float kLeastScale = -108.0f;
+constexpr float kProductGrow = 10.0f;        // how far a product may exceed the reference: 2^(4 + 10) is below fp16's largest
+constexpr uint32_t kAlike = 2u << 23;        // scales whose bits differ by no more are alike: the largest is at most four times the least
 
 // Beyond this a reference, times the scale, is rounded so coarsely that a row's largest weight could leave the
 // range of fp32 (at 2^30), so scores are taken less the largest one first, which is one more instruction each.
@@ -30,7 +33,17 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// the power of the reference for a largest product 2^x times the largest score's weight (NaN: the least)
+__device__ __forceinline__ float scale_power(float x) { return fminf(fmaxf(rintf(x), kLeastScale), 120.0f); }
+
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((127 + e) << 23); }   // -126 <= e <= 127
+// of a whole number: the sum's last bits are e
+__device__ __forceinline__ float pow2(float e) { return __int_as_float((__float_as_int(e + 12582912.0f) << 23) + 0x3f800000); }
 
 struct AttendArgs {
     fa_cache_view c;

@@ -11,8 +11,11 @@
 // An 8-bit cache (codes times one scale per slot and head): the key's scale multiplies the
 // score, the value's the weight, so the codes themselves go to the tensor cores, as fp16 (exact).
 // q is scaled per row by a power of two into the middle of the fp16 range (exact) and the factor
-// goes to the exponent; B also follows the largest value scale a row sees, so that p_t times
-// the value's scale stays in fp16's range with 28 bits below the largest.
+// goes to the exponent; B follows the largest product of a weight and its value's scale that a row
+// meets, so that the products stay in fp16's range with 25 bits or more below the largest.  Where all
+// slots of a tile are seen and their scales are within four times one another, the largest score with
+// the largest scale stands for the tile's largest product; else the products are looked at one by one
+// (2 x 98304 slots x 64 rows: 185 us, 247 if every tile took that path).
 //
 // The layout.  All query heads of one key/value head and all drafted tokens are rows of one
 // problem, so a cached tile is read once for up to 256 rows: two tiles of 128 rows are two
@@ -50,8 +53,9 @@ namespace {
 constexpr int TS = 128;                      // slots of a tile, rows of a stream
 constexpr int NLOAD = 8 * 32, NTHR = 20 * 32;
 // registers a thread of each role, of the 96 the block is launched with: 256 softmax + 256 load +
-// 128 MMA threads use 640 * 96 either way (the smallest that spill nothing)
-template <bool E4M3> struct Regs { static constexpr int SOFTMAX = E4M3 ? 128 : 112, LOAD = E4M3 ? 72 : 80, MMA = E4M3 ? 80 : 96; };
+// 128 MMA threads use 640 * 96 either way.  (8-bit: the code of masked tiles spills a few; 128, 72 and 80 measured 3%
+// slower, 136, 64 and 80 2%.)
+template <bool E4M3> struct Regs { static constexpr int SOFTMAX = E4M3 ? 128 : 112, LOAD = E4M3 ? 64 : 80, MMA = 96; };
 constexpr long long kSpinCycles = 2000000000LL;
 constexpr int kUnitCost = 3;                 // what starting a unit costs, in tiles
 
@@ -200,7 +204,7 @@ struct Misc {
     // any number of them ahead of stream 0.
     int odd[8], odd_scale[2];         // 1 + the last segment that was marked
     int hole[16];                     // key tile & 15: a slot of the tile has no page or lies past the end
-    float vtop[2][4];                 // per stream: the largest value scale of 32 slots
+    float vtop[2][4];                 // per stream: log2 of the largest value scale of 32 slots, inf where they differ widely
 };
 struct Scales { float k[2][TS], v[2][TS]; };   // per stream, of its tile
 
@@ -713,7 +717,8 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a, const __grid_c
             }
             warp_arrive(&sh.q_full[st]);
             float m = -INFINITY, l = 0.0f, bias = 0.0f;
-            int ev = E4M3 ? kLeastScale : 0;
+            bool any_far = false;                          // a reference of the warp's is
+            float ev = E4M3 ? kLeastScale : 0.0f;          // a whole number
             // the scales of slot r of each tile are fetched one tile ahead, its page's number two
             float ks = 0.0f, vs = 0.0f;
             const Rows rows(a, s);
@@ -740,11 +745,10 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a, const __grid_c
                 const int tile = begin + q * step;
                 const int first = (s.t0 + tile) * TS;
                 if (E4M3) {
-                    float vt = vs;
-#pragma unroll
-                    for (int o = 16; o; o >>= 1) vt = fmaxf(vt, __shfl_xor_sync(0xffffffffu, vt, o));
+                    // (as bits: scales are not negative, and infinities and NaN are the largest)
+                    const uint32_t vt = __reduce_max_sync(0xffffffffu, __float_as_uint(vs)), vl = __reduce_min_sync(0xffffffffu, __float_as_uint(vs));
                     if (q > 0) scales_sync();             // the previous tile's have been read
-                    if (lane == 0) sh.vtop[st][warp & 3] = vt;
+                    if (lane == 0) sh.vtop[st][warp & 3] = vt < 0x7f800000u && vt - vl <= kAlike ? lg2(__uint_as_float(vt)) : INFINITY;
                     if (first + r >= s.slots && !(fabsf(vs) < INFINITY)) { vs = 0.0f; sh.odd_scale[st] = sg + 1; }
                     sc.k[st][r] = ks;
                     sc.v[st][r] = vs;
@@ -757,9 +761,14 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a, const __grid_c
                 mbar_wait(&sh.s_full[st], (uint32_t)ns++ & 1, fail);
                 __syncwarp();
                 tc_fence_after();
-                const bool whole = first + TS <= s.slots && !sh.hole[(keys_before + tile) & 15];
-                // The tile's scores to weights.  WHOLE: every row sees every slot; the code of the
-                // other tiles is kept apart so that the common one stays short.
+                float vmx = 0.0f;                          // log2 of the tile's largest value scale
+                if (E4M3) {
+                    vmx = -INFINITY;
+                    for (int w = w_begin; w < w_end; ++w) vmx = fmaxf(vmx, sh.vtop[st][w]);
+                }
+                const bool whole = first + TS <= s.slots && !sh.hole[(keys_before + tile) & 15] && vmx < INFINITY;
+                // The tile's scores to weights.  WHOLE: every row sees every slot, and the value scales are
+                // alike; the code of the other tiles is kept apart so that the common one stays short.
                 auto weigh = [&](auto whole_tag) {
                     constexpr bool WHOLE = decltype(whole_tag)::value;
                     float x[32];
@@ -770,7 +779,8 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a, const __grid_c
                         const uint32_t held = __ballot_sync(0xffffffffu, slot < (uint32_t)s.end && rows.page(slot) < rows.n_pages);
                         return used ? held & seen_bits(a, s, ti, first + 32 * w) : 0u;
                     };
-                    // chunk w of 32 scores, times the keys' scales, hidden ones to -inf
+                    // chunk w of 32 scores, times the keys' scales (rounded, so that the largest less itself is
+                    // zero), hidden ones to -inf
                     auto load_chunk = [&](int w, uint32_t z) {
                         if (!WHOLE) __syncwarp();
                         tmem_ld32(ts + 32 * w, x);
@@ -778,24 +788,20 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a, const __grid_c
 #pragma unroll
                             for (int e = 0; e < 32; e += 4) {
                                 const float4 f = *reinterpret_cast<const float4 *>(&sc.k[st][32 * w + e]);
-                                x[e] *= f.x; x[e + 1] *= f.y; x[e + 2] *= f.z; x[e + 3] *= f.w;
+                                x[e] = __fmul_rn(x[e], f.x);
+                                x[e + 1] = __fmul_rn(x[e + 1], f.y);
+                                x[e + 2] = __fmul_rn(x[e + 2], f.z);
+                                x[e + 3] = __fmul_rn(x[e + 3], f.w);
                             }
                         if (!WHOLE)
 #pragma unroll
                             for (int e = 0; e < 32; ++e) x[e] = (z >> e & 1) ? x[e] : -INFINITY;
                     };
-                    // the largest score (before the scale), and the largest value scale, that the row sees
-                    float mx = -INFINITY, vmx = 0.0f;
+                    // the largest score (before the scale) that the row sees
+                    float mx = -INFINITY;
 #pragma unroll 1
                     for (int w = w_begin; w < w_end; ++w) {
-                        const uint32_t z = seen(w);
-                        if (E4M3) {
-                            if (WHOLE) vmx = fmaxf(vmx, sh.vtop[st][w]);
-                            else
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) vmx = (z >> e & 1) ? fmaxf(vmx, sc.v[st][32 * w + e]) : vmx;
-                        }
-                        load_chunk(w, z);
+                        load_chunk(w, seen(w));
                         float top[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                         for (int e = 0; e < 32; e += 8)
@@ -803,22 +809,39 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a, const __grid_c
                             for (int j = 0; j < 4; ++j) top[j] = fmaxf(fmaxf(top[j], x[e + 2 * j]), x[e + 2 * j + 1]);
                         mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                     }
-                    const int e2 = E4M3 ? max(ev, min(max(fa_exponent(vmx) + 1, kLeastScale), 120)) : ev;
-                    const bool move = live && mx > -INFINITY && ((mx - m) * c > kGrow || e2 > ev || m == -INFINITY);
+                    // The reference moves where the largest score exceeds it by too much, or the largest product does:
+                    // where scales are alike the largest score with the largest scale stands for it, else the
+                    // products themselves.  (No score yet: m is -inf, and where there is still none the differences
+                    // are not numbers.)
+                    const float by_score = (mx - m) * c, m2 = fmaxf(m, mx);
+                    const float now = (m - m2) * c + ev;  // the reference's product, less the largest score
+                    float most = vmx + (mx - m2) * c;     // the tile's
+                    if (E4M3 && !WHOLE) {
+                        most = -INFINITY;
+#pragma unroll 1
+                        for (int w = w_begin; w < w_end; ++w) {
+                            load_chunk(w, seen(w));
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) most = fmaxf(most, fmaf(x[e] - m2, c, lg2(sc.v[st][32 * w + e])));
+                        }
+                    }
+                    const bool move = live && (by_score > kGrow || (E4M3 && most > now + kProductGrow));
                     if (__any_sync(0xffffffffu, move)) {
                         float f = 1.0f;
                         if (move) {
                             const bool had = m > -INFINITY;
-                            const float m0 = m, up = E4M3 ? (float)e2 - (float)ev : 0.0f;
-                            m = fmaxf(m, mx);
-                            ev = e2;
-                            const float b2 = m * c + (E4M3 ? (float)ev : 0.0f) - OFF;
+                            const float m0 = m, ev0 = ev;
+                            m = m2;
+                            if (E4M3) ev = scale_power(had ? fmaxf(now, most) : most);
+                            const float up = ev - ev0;
+                            const float b2 = m * c + ev - OFF;
                             // (m0 - m) c - up, exactly that of the weights' references
                             const float by = fmaxf(fabsf(bias), fabsf(b2)) > kFar ? (m0 - m) * c - up : bias - b2;
                             f = had ? ex2(by) : 0.0f;
                             bias = b2;
                             l *= E4M3 ? (had ? ex2(up + by) : 0.0f) : f;
                         }
+                        any_far = __any_sync(0xffffffffu, fabsf(bias) > kFar);
                         if (q > 0) {
                             // (the previous tile's values were added before these scores were made)
 #pragma unroll 1
@@ -831,8 +854,8 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a, const __grid_c
                             }
                         }
                     }
-                    const bool far = fabsf(bias) > kFar, any_far = __any_sync(0xffffffffu, far);
-                    const float ref = far ? (E4M3 ? (float)ev : 0.0f) - OFF : bias;
+                    const bool far = fabsf(bias) > kFar;
+                    const float ref = far ? ev - OFF : bias;
                     float sum[4] = {0, 0, 0, 0};
 #pragma unroll 1
                     for (int w = w_begin; w < w_end; ++w) {
@@ -875,7 +898,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a, const __grid_c
                 warp_arrive(&sh.p_full[st]);
             }
             // ---- the segment's result: the sum of the weights is l 2^bias, that of values o pow2(ev) 2^bias
-            bias -= E4M3 ? (float)ev : 0.0f;
+            bias -= ev;
             mbar_wait(&sh.pv_done[st], (uint32_t)npv++ & 1, fail);
             __syncwarp();
             tc_fence_after();

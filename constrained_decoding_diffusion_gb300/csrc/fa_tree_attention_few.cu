@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(32 * NW, 1) k_attend_few(AttendArgs a) {
         int ti[RR];
         bool live[RR], used[RR];
         float c[RR], m[RR], l[RR], bias[RR];
-        int ev[RR];
+        float ev[RR];                           // whole numbers
         int64_t orow[RR];
         uint32_t qf[KS][2 * RR];
 #pragma unroll
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(32 * NW, 1) k_attend_few(AttendArgs a) {
             orow[h] = ((int64_t)s.b * a.T + ti[h]) * a.heads + hq;
             m[h] = -INFINITY;
             l[h] = bias[h] = 0.0f;
-            ev[h] = E4M3 ? kLeastScale : 0;
+            ev[h] = E4M3 ? kLeastScale : 0.0f;
             const T *q = (const T *)a.q + s.b * a.qb + ti[h] * a.qt + hq * a.qh;
             float top = 0.0f;
             uint2 raw[KS];
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(32 * NW, 1) k_attend_few(AttendArgs a) {
 #pragma unroll
                 for (int nb = 0; nb < NBK; ++nb) {
                     float &x0 = x[nb][2 * h], &x1 = x[nb][2 * h + 1];
-                    if (E4M3) { x0 *= kk[nb].x; x1 *= kk[nb].y; }
+                    if (E4M3) { x0 = __fmul_rn(x0, kk[nb].x); x1 = __fmul_rn(x1, kk[nb].y); }
                     if (!all) {
                         const uint32_t z = see[h][nb / 4] >> (8 * (nb & 3) + 2 * t);
                         x0 = z & 1 ? x0 : -INFINITY;
@@ -307,14 +307,30 @@ __global__ void __launch_bounds__(32 * NW, 1) k_attend_few(AttendArgs a) {
                 }
                 mx = quad_max(mx);
                 if (E4M3) vmx = quad_max(vmx);
-                const int e2 = E4M3 ? max(ev[h], min(max(fa_exponent(vmx) + 1, kLeastScale), 120)) : ev[h];
+                // (as in the larger kernel: products are looked at only where their bound says so)
+                const float by_score = (mx - m[h]) * c[h];
+                bool move = by_score > (E4M3 ? fminf(kGrow, ev[h] + kProductGrow - lg2(vmx)) : kGrow);
+                float e2 = ev[h];
+                if (E4M3 && __any_sync(0xffffffffu, move)) {
+                    const float m2 = fmaxf(m[h], mx);
+                    float most = -INFINITY;
+#pragma unroll
+                    for (int nb = 0; nb < NBK; ++nb) {
+                        most = fmaxf(most, fmaf(x[nb][2 * h] - m2, c[h], lg2(vv[nb].x)));
+                        most = fmaxf(most, fmaf(x[nb][2 * h + 1] - m2, c[h], lg2(vv[nb].y)));
+                    }
+                    most = quad_max(most);
+                    const float now = m[h] > -INFINITY ? (m[h] - m2) * c[h] + ev[h] : -INFINITY;
+                    move = move && (by_score > kGrow || most > now + kProductGrow);
+                    e2 = scale_power(fmaxf(now, most));
+                }
                 f[h] = 1.0f;
-                if (mx > -INFINITY && ((mx - m[h]) * c[h] > kGrow || e2 > ev[h] || m[h] == -INFINITY)) {
+                if (move) {
                     const bool had = m[h] > -INFINITY;
-                    const float m0 = m[h], up = E4M3 ? (float)e2 - (float)ev[h] : 0.0f;
+                    const float m0 = m[h], up = e2 - ev[h];
                     m[h] = fmaxf(m[h], mx);
                     ev[h] = e2;
-                    const float b2 = m[h] * c[h] + (E4M3 ? (float)ev[h] : 0.0f) - OFF;
+                    const float b2 = m[h] * c[h] + ev[h] - OFF;
                     const float by = fmaxf(fabsf(bias[h]), fabsf(b2)) > kFar ? (m0 - m[h]) * c[h] - up : bias[h] - b2;
                     f[h] = had ? ex2(by) : 0.0f;
                     bias[h] = b2;
@@ -322,7 +338,7 @@ __global__ void __launch_bounds__(32 * NW, 1) k_attend_few(AttendArgs a) {
                     moved = true;
                 }
                 const bool far = fabsf(bias[h]) > kFar;
-                const float ref = far ? (E4M3 ? (float)ev[h] : 0.0f) - OFF : bias[h];
+                const float ref = far ? ev[h] - OFF : bias[h];
                 if (__any_sync(0xffffffffu, far))
 #pragma unroll
                     for (int nb = 0; nb < NBK; ++nb) {
@@ -426,7 +442,7 @@ __global__ void __launch_bounds__(32 * NW, 1) k_attend_few(AttendArgs a) {
                         }
                     }
                 if (t == 0) {
-                    const float lse = some ? bias[h] - (float)ev[h] + log2f(total) : -INFINITY;
+                    const float lse = some ? bias[h] - ev[h] + log2f(total) : -INFINITY;
                     if (partial) a.part_lse[prow0 + g + 8 * h] = lse;
                     else if (a.lse) a.lse[orow[h]] = lse * kLn2;
                 }
