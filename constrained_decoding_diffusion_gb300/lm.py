@@ -4,7 +4,8 @@ under an automaton.
 
 Like `native`, this module only checks and marshals tensors; every operator runs in the
 library's CUDA kernels on torch's current stream (or the one given).  Tensors must live on the
-current device and stay alive and unchanged until the stream has passed the call.
+current device and stay alive and unchanged until the stream has passed the call; results that a call
+makes on a given stream belong to that stream's memory, like tensors made under torch.cuda.stream.
 """
 from __future__ import annotations
 
@@ -40,6 +41,15 @@ _raw_stream = torch._C._cuda_getCurrentRawStream   # the current stream's handle
 
 def _stream(stream, t) -> int:
     return _raw_stream(t.device.index) if stream is None else stream.cuda_stream
+
+
+def _new(shape, dtype, device, stream):
+    """A result of a call on a stream, from that stream's memory: the current one's may hold a freed tensor
+    that its earlier kernels have yet to read or write."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _check(rc: int):
@@ -136,7 +146,7 @@ def fa_rope(x, positions, phase, out=None, interleaved: bool = False, mscale: fl
         raise ValueError("x must have shape [tokens, heads, dim]")
     N, H, D = x.shape
     if out is None:
-        out = torch.empty((N, H, D), dtype=x.dtype, device=x.device)
+        out = _new((N, H, D), x.dtype, x.device, stream)
     elif _dtype(out, "out") != dt:
         raise TypeError("out must have the type of x")
     xs, os = _rows(x, "x", x.shape), _rows(out, "out", x.shape)
@@ -256,9 +266,9 @@ def fa_tree_mask(parents, mask=None, depth=None, stream=None):
     """The mask words [B, T, ceil(T / 64)] int64 and depths [B, T] of the trees parents [B, T]."""
     B, T = parents.shape
     if mask is None:
-        mask = torch.empty((B, T, (T + 63) // 64), dtype=torch.int64, device=parents.device)
+        mask = _new((B, T, (T + 63) // 64), torch.int64, parents.device, stream)
     if depth is None:
-        depth = torch.empty((B, T), dtype=torch.int32, device=parents.device)
+        depth = _new((B, T), torch.int32, parents.device, stream)
     _check(_lib().fa_tree_mask(B, T, _ptr(parents, torch.int32, "parents", (B, T)),
                                       _ptr(mask, torch.int64, "mask", (B, T, (T + 63) // 64)),
                                       _ptr(depth, torch.int32, "depth", (B, T)), _stream(stream, parents)))
@@ -308,8 +318,8 @@ def fa_beam_tables(aut: native.CompiledAutomaton, stream=None):
     """The next-state table [S, V] int16 and the live bits [S, ceil(V / 32)] int32 of a DFA,
     without the moves from which no accepting state can be reached."""
     S, V = aut.n_states, aut.vocab
-    nxt = torch.empty((S, V), dtype=torch.int16, device="cuda")
-    live = torch.empty((S, (V + 31) // 32), dtype=torch.int32, device="cuda")
+    nxt = _new((S, V), torch.int16, "cuda", stream)
+    live = _new((S, (V + 31) // 32), torch.int32, "cuda", stream)
     _check(_lib().fa_beam_tables(aut.handle, nxt.data_ptr(), live.data_ptr(), _stream(stream, nxt)))
     return nxt, live
 
@@ -352,7 +362,7 @@ def fa_beam_reorder(src, parent, dst=None, token=None, at: int = 0, stream=None)
     N, K, W = src.shape
     top = parent.shape[1]
     if dst is None:
-        dst = torch.empty((N, top, W), dtype=torch.int32, device=src.device)
+        dst = _new((N, top, W), torch.int32, src.device, stream)
     _check(_lib().fa_beam_reorder(N, K, top, W, _ptr(src, torch.int32, "src", (N, K, W)),
                                          _ptr(parent, torch.int32, "parent", (N, top)),
                                          _ptr(token, torch.int32, "token", (N, top)), int(at),
