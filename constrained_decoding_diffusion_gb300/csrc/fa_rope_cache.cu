@@ -513,7 +513,8 @@ __global__ void __launch_bounds__(NT) k_cache_read(fa_cache_view c, int N, const
 }
 
 // One block per (sequence, head).  A thread moves the same 16 bytes of every kept row, in order:
-// path[i] >= i, so a row still to be read is never one that was written.
+// path[i] >= i, so a row still to be read is never one that was written.  A slot that no page holds
+// reads as zeros and is not written, like everywhere.
 __global__ void __launch_bounds__(64) k_cache_keep(fa_cache_view c, int es, int P, const int32_t *length, const int32_t *path) {
     const int b = blockIdx.x / c.kv_heads, h = blockIdx.x % c.kv_heads;
     const int chunks = c.head_dim * es / 16, tid = threadIdx.x;
@@ -526,14 +527,14 @@ __global__ void __launch_bounds__(64) k_cache_keep(fa_cache_view c, int es, int 
         last = j;
         if (j == i) continue;
         const int64_t from = c.row(b, n + j, h), to = c.row(b, n + i, h);
-        if (from < 0 || to < 0) return;
+        if (to < 0) continue;
         for (int q = tid; q < 2 * chunks; q += 64) {
             uint4 *p = (uint4 *)(q < chunks ? c.k : c.v);
-            p[to * chunks + q % chunks] = p[from * chunks + q % chunks];
+            p[to * chunks + q % chunks] = from < 0 ? make_uint4(0, 0, 0, 0) : p[from * chunks + q % chunks];
         }
         if (c.k_scale && tid < 2) {
             float *p = tid ? c.v_scale : c.k_scale;
-            p[to] = p[from];
+            p[to] = from < 0 ? 0.0f : p[from];
         }
     }
 }

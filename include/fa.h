@@ -452,6 +452,7 @@ fa_status fa_cache_read(const fa_kv_cache *cache, int32_t dtype, int32_t B, int3
  * slot length[b] + path[b, i] is copied to slot length[b] + i for i = 0, 1, ... until the
  * first path[b, i] < 0 or P.  path[b, .] must ascend (a node's ancestors come before it),
  * so path[b, i] >= i; an entry that does not ascend ends the path.  Codes and scales move as they are.
+ * A slot that no page holds is moved as zeros, and one is not moved to a slot that no page holds; neither ends the path.
  *   path  [B, P] int32.   Errors: FA_ERR_INVALID_ARG, FA_ERR_CUDA.
  */
 fa_status fa_cache_keep(const fa_kv_cache *cache, int32_t B, int32_t P, const int32_t *page_table, int32_t max_pages,
