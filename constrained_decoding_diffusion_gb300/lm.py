@@ -301,10 +301,12 @@ class TreeAttention:
             raise TypeError("q must be %s, got %s" % (self.out.dtype, q.dtype))
         if c.head_dim != D:
             raise ValueError("the cache's head_dim is %d, not %d" % (c.head_dim, D))
-        s = _rows(q, "q", self.shape)
+        sb, st, sh = _rows(q, "q", self.shape)[:3]
+        if B == 1 or T == 1 or H == 1:   # the stride of a single element means nothing, and torch makes any
+            sb, st, sh = sb if B > 1 else 0, st if T > 1 else 0, sh if H > 1 else 0
         P = page_table.shape[1]
         _check(_lib().fa_tree_attention(
-            ctypes.byref(c), dt, B, T, H, q.data_ptr(), s[0], s[1], s[2],
+            ctypes.byref(c), dt, B, T, H, q.data_ptr(), sb, st, sh,
             _ptr(page_table, torch.int32, "page_table", (B, P)), P, _ptr(length, torch.int32, "length", (B,)),
             _ptr(count, torch.int32, "count", (B,)), _ptr(mask, torch.int64, "mask", (B, T, (T + 63) // 64)),
             D ** -0.5 if scale is None else scale, self.out.data_ptr(), self.lse.data_ptr(), self.workspace.data_ptr(),
