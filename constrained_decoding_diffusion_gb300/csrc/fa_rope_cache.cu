@@ -583,6 +583,7 @@ extern "C" fa_status fa_rope(int32_t dtype, int64_t n_tokens, int32_t n_heads, i
     if (st != FA_OK) return st;
     if (n_tokens == 0 || n_heads == 0) return FA_OK;
     if (!x || !out || (rot_dim > 0 && (!positions || !phase))) return fa_refuse(fn, "NULL buffer");
+    if (n_tokens > ((int64_t)1 << 62) / ((int64_t)n_heads * head_dim)) return fa_refuse(fn, "too many elements");
     cudaStream_t s = (cudaStream_t)stream;
     const RopeArgs a{n_tokens, x_token_stride, x_head_stride, out_token_stride, out_head_stride, n_heads, head_dim, rot_dim,
                      interleaved, inverse != 0, x, out, positions, phase, mscale};
@@ -613,7 +614,7 @@ extern "C" fa_status fa_cache_write(const fa_kv_cache *cache, int32_t dtype, int
     a.vb = v_batch_stride; a.vt = v_token_stride; a.vh = v_head_stride;
     a.start = start; a.count = count; a.pos = positions; a.phase = phase;
     a.rot = positions ? rot_dim : 0; a.interleaved = interleaved; a.mscale = mscale;
-    if ((int64_t)B * T * cache->kv_heads > (int64_t)2147483647) return fa_refuse(fn, "B * T * kv_heads out of range");
+    if ((int64_t)B * T > 2147483647 / cache->kv_heads) return fa_refuse(fn, "B * T * kv_heads out of range");
     cudaStream_t s = (cudaStream_t)stream;
     if (dtype == FA_DTYPE_F32) return launch_write<float>(a, s);
     if (dtype == FA_DTYPE_F16) return launch_write<__half>(a, s);
