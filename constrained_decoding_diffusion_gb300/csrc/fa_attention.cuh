@@ -60,6 +60,7 @@ struct AttendArgs {
     int box_rows;                                  // rows of a tensor-map box, 0 = no tensor maps
     int tile_shift, unit_cost;                     // log2 of the slots of a tile; what starting a unit costs, in tiles
     int part_rows;                                 // rows of a partial result
+    int inject;                                    // (failure tests) a wait of the first block's runs out
 };
 
 // ----------------------------------------------------------------------------- the work list

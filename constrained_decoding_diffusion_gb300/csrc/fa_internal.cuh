@@ -80,6 +80,9 @@ struct fa_automaton {
 void fa_set_error(const std::string &msg);
 // counts a kernel launch and turns its error into a status (fa_step.cu)
 fa_status fa_launch_check(const char *what);
+// whether a launch is to make a wait run out (fa_debug_inject_wait_timeouts), and how long that takes
+int fa_take_injected_timeout();
+constexpr long long kInjectCycles = 1LL << 20;   // (~0.5 ms)
 
 // ----------------------------------------------------------------------------- device side
 

@@ -49,7 +49,6 @@ constexpr int NEPI = 16;                    // epilogue warps of the product ker
 constexpr int NTHR_P = 32 * (2 + NEPI);     // producer warp, MMA warp, epilogue warps
 constexpr uint32_t TMEM_COLS = 512;   // two 256-column accumulators
 constexpr long long kSpinCycles = 2000000000LL;
-constexpr long long kInjectCycles = 1LL << 20;   // the injected wait of a failure test (~0.5 ms)
 constexpr int PREP_KT = 256 / TK;           // K steps converted per k_tc_prep block (256 columns)
 
 // Operand format of the products: each operand is split into three bf16 parts,
@@ -536,8 +535,14 @@ __global__ void __launch_bounds__(NTHR_P, 1) k_span_tc(int S, int L, int k, int 
 
 size_t span_tc_smem() { return (size_t)NSTAGE * STAGE_BYTES; }
 
-// Launches of k_span_tc still to take the injected wait (failure tests only).
+// Launches still to take the injected wait (failure tests only).
 static std::atomic<int> g_inject_timeouts{0};
+
+int fa_take_injected_timeout() {
+    for (int n = g_inject_timeouts.load(); n > 0;)
+        if (g_inject_timeouts.compare_exchange_weak(n, n - 1)) return 1;
+    return 0;
+}
 
 extern "C" fa_status fa_debug_inject_wait_timeouts(int32_t n_launches) {
     if (n_launches < 0) { fa_set_error("fa_debug_inject_wait_timeouts: negative count"); return FA_ERR_INVALID_ARG; }
@@ -571,9 +576,7 @@ fa_status fa_span_tc_level(int S, int B, int L, int k, int nk, const float *mant
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess || n_sm <= 0) { fa_set_error(std::string("span product (tensor cores): ") + cudaGetErrorString(e)); return FA_ERR_CUDA; }
     const long grid = std::min<long>(n_tiles, n_sm);   // persistent: one CTA per SM
-    int inject = 0;
-    for (int n = g_inject_timeouts.load(); n > 0 && !inject;)
-        if (g_inject_timeouts.compare_exchange_weak(n, n - 1)) inject = 1;
+    const int inject = fa_take_injected_timeout();
     k_span_tc<<<(unsigned)grid, NTHR_P, smem, stream>>>(S, L, k, nk, mant_c, rho_c, rmax_c, rminc_c, nc, mu,
                                                         (const unsigned char *)img, mant_p, rho_p, rmax_p, rminc_p,
                                                         err, inject, fflag_p, fmap_p, n_prod);

@@ -370,6 +370,11 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a, const __grid_c
                 tc_fence_after();
                 return ok;
             };
+            if (a.inject && blockIdx.x == 0) {   // a failure test: only this thread completes `done`, later
+                const long long t0 = clock64();
+                while (!mbar_try_wait(&sh.done, 0) && clock64() - t0 < kInjectCycles) {}
+                *fail = 1;
+            }
             while (!*fail && walk.next(a, s)) {
                 const int streams = s.two() || s.n > 1 ? 2 : 1;
                 bool ok = true;
@@ -1247,7 +1252,7 @@ cudaError_t block_count(int *ctas) {
 }
 
 template <int DP, bool E4M3, class T, class M>
-fa_status launch(const AttendArgs &a, const CUtensorMap (&maps)[2], cudaStream_t s) {
+fa_status launch(AttendArgs a, const CUtensorMap (&maps)[2], cudaStream_t s) {
     constexpr size_t smem = smem_bytes<DP, E4M3>();
     static_assert(smem <= 232448, "shared memory of a block");
     int ctas = 0;
@@ -1255,6 +1260,7 @@ fa_status launch(const AttendArgs &a, const CUtensorMap (&maps)[2], cudaStream_t
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(k_attend<DP, E4M3, T, M>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return fa_refuse("fa_tree_attention", cudaGetErrorString(e), FA_ERR_CUDA);
+    a.inject = fa_take_injected_timeout();
     k_attend<DP, E4M3, T, M><<<ctas, NTHR, smem, s>>>(a, maps[0], maps[1]);
     fa_status st = fa_launch_check("tree attention");
     if (st != FA_OK) return st;
@@ -1340,6 +1346,7 @@ extern "C" fa_status fa_tree_attention(const fa_kv_cache *cache, int32_t dtype, 
         return f16 ? join<128, __half>(a, runs, 0, s) : join<128, __nv_bfloat16>(a, runs, 0, s);
     }
     a.tile_shift = 7;
+    a.inject = 0;
     a.unit_cost = kUnitCost;
     a.part_rows = 256;
     CUtensorMap maps[2] = {};
