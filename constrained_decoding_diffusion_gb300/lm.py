@@ -118,8 +118,10 @@ def rope_phases(rot_dim: int, base: float = 10000.0, scaling: Optional[str] = No
         raise ValueError("rot_dim must be even")
     if scaling not in (None, "linear", "base", "blend"):
         raise ValueError("scaling must be None, 'linear', 'base' or 'blend'")
-    if factor < 1.0 or base <= 0.0:
-        raise ValueError("factor must be at least 1 and base positive")
+    if not (1.0 <= factor < math.inf and 0.0 < base < math.inf):
+        raise ValueError("factor must be at least 1, base positive, and both finite")
+    if scaling == "blend" and not fast_turns > slow_turns:
+        raise ValueError("fast_turns must be above slow_turns")
     if scaling == "base" and rot_dim > 2:
         base = base * factor ** (rot_dim / (rot_dim - 2))
     got = []
