@@ -15,7 +15,9 @@
 // Measured (head_dim 128, 8 key/value heads): 32 sequences of 8192 slots, 8-bit cache, 4 rows 101 us
 // (545 MB, 5.4 TB/s), 16 rows 121 us (the instructions of two halves of the left operand begin to count);
 // 16-bit cache 176 us (1.07 GB, 6.1 TB/s).  32 ragged sequences of up to 8192 slots, 8-bit:
-// 60 us (285 MB; 55 the kernel, 5 the join).  4 sequences of 509 slots: 12 us, two launches' start and end.  Up to eight rows leave the operand's second half out (R16 = false: 104 us at 8 rows).
+// 61 us (285 MB; 56 the kernel, 5 the join).  4 sequences of 509 slots: 12 us replayed in a graph, 14 called one by
+// one: two launches' start and end.  Up to eight rows leave the operand's second half out (R16 = false: 104 us at 8
+// rows).
 #include "fa_attention.cuh"
 
 using namespace fa_attention;

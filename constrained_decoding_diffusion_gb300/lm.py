@@ -278,7 +278,8 @@ def fa_tree_mask(parents, mask=None, depth=None, stream=None):
 
 
 class TreeAttention:
-    """Owner of the workspace and outputs of fa_tree_attention for a fixed (B, T, heads, dim)."""
+    """Owner of the workspace and outputs of fa_tree_attention for a fixed (B, T, heads, dim).  A call
+    returns the owner's own tensors, which the next one overwrites."""
 
     def __init__(self, B: int, T: int, q_heads: int, kv_heads: int, head_dim: int, dtype=torch.bfloat16, device="cuda"):
         n = ctypes.c_size_t()

@@ -388,9 +388,9 @@ enum { FA_DTYPE_F32 = 0, FA_DTYPE_F16 = 1, FA_DTYPE_BF16 = 2 };
  *   interleaved  1: pair i = elements (2i, 2i + 1); 0: pair i = (i, i + rot_dim / 2)
  *   positions    [n_tokens] int32 (negative positions rotate backwards)
  *   phase        [rot_dim / 2] turns per position as a 64-bit fraction of a turn: the angle is
- *                reduced exactly at any position, and any scaling for long contexts
- *                (interpolated positions, a stretched base, a blend by wavelength) is a
- *                choice of phase and mscale
+ *                reduced exactly at any position (and then rounded to fp32, by up to 2^-26 turn), and
+ *                any scaling for long contexts (interpolated positions, a stretched base, a blend by
+ *                wavelength) is a choice of phase and mscale
  * Sums and products in fp32, rounded once.  Errors: FA_ERR_INVALID_ARG, FA_ERR_CUDA.
  */
 fa_status fa_rope(int32_t dtype, int64_t n_tokens, int32_t n_heads, int32_t head_dim, int32_t rot_dim,
