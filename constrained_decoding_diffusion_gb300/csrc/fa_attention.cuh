@@ -14,7 +14,7 @@ constexpr float kGrow = 6.0f;                // how far a score may exceed the r
 // 2^(kGrow + 4 + 108) each, still add up in fp32 (smaller values lose bits of their weights), and at 2^120.
 constexpr float kLeastScale = -108.0f;
 constexpr float kProductGrow = 10.0f;        // how far a product may exceed the reference: 2^(4 + 10) is below fp16's largest
-constexpr uint32_t kAlike = 2u << 23;        // scales whose bits differ by no more are alike: the largest is at most four times the least
+constexpr uint32_t kAlike = 4u << 23;        // scales whose bits differ by no more are alike: the largest is at most 16 times the least
 
 // Beyond this a reference, times the scale, is rounded so coarsely that a row's largest weight could leave the
 // range of fp32 (at 2^30), so scores are taken less the largest one first, which is one more instruction each.

@@ -13,8 +13,8 @@
 // q is scaled per row by a power of two into the middle of the fp16 range (exact but for elements below 2^-22 of
 // the row's largest, whose last bits fp16 drops) and the factor
 // goes to the exponent; B follows the largest product of a weight and its value's scale that a row
-// meets, so that the products stay in fp16's range with 25 bits or more below the largest.  Where all
-// slots of a tile are seen and their scales are within four times one another, the largest score with
+// meets, so that the products stay in fp16's range with 24 bits or more below the largest.  Where all
+// slots of a tile are seen and their scales are within 16 times one another, the largest score with
 // the largest scale stands for the tile's largest product; else the products are looked at one by one
 // (2 x 98304 slots x 64 rows: 185 us, 247 if every tile took that path).
 //

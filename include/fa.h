@@ -494,7 +494,7 @@ fa_status fa_tree_mask(int32_t B, int32_t T, const int32_t *parents, uint64_t *m
  * whatever it holds (NaN and infinities included).  Scores, softmax statistics and sums are
  * fp32.  For the product with the values a softmax weight is rounded to bf16 on a bf16 cache and to fp16
  * on an fp16 one, after the weights have been summed; on an 8-bit cache weight times value scale is rounded to fp16, relative
- * to the largest such product of the row (those below 2^-15 of it lose bits, those below 2^-25 vanish).
+ * to the largest such product of the row (those below 2^-13 of it lose bits, those below 2^-24 vanish).
  * On an 8-bit cache q is rounded to fp16 after its row's largest element has been brought to 2^8: elements
  * below 2^-22 of it lose bits.
  * The same call gives the same bits.  Should a wait inside the kernel run out (about a second), the rows it

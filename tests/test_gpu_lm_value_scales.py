@@ -5,7 +5,7 @@ weight takes no bits from the others.
 Tolerance: that of the model-side operators with fp16 weights, (2^-10 + 4 ds) w + half a unit of the result, plus
 what fp16's last step leaves of small products: half a step is 2^-25, the largest product is at least
 2^3.5 of the same measure (it is aimed at 2^4 by whole powers of two), so at most 2^-28 max_t(p_t s_t) sum_t |code_t|.
-Where a tile's scales are within four times one another the largest product may be as small as 2^1.5; the tolerance
+Where a tile's scales are within 16 times one another the largest product may be as small as 2^-0.5; the tolerance
 leaves that out."""
 import pytest
 
