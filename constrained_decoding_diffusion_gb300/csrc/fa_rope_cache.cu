@@ -610,8 +610,8 @@ extern "C" fa_status fa_cache_write(const fa_kv_cache *cache, int32_t dtype, int
     if (st != FA_OK) return st;
     if (!fa_dtype_ok(dtype)) return fa_refuse(fn, "unknown dtype");
     if (B < 0 || T < 0) return fa_refuse(fn, "B or T negative");
-    if ((positions == nullptr) != (phase == nullptr)) return fa_refuse(fn, "positions and phase go together");
-    if (positions && (st = rope_args(fn, cache->head_dim, rot_dim, interleaved)) != FA_OK) return st;
+    if (rot_dim != 0 && (positions == nullptr) != (phase == nullptr)) return fa_refuse(fn, "positions and phase go together");
+    if (positions && phase && (st = rope_args(fn, cache->head_dim, rot_dim, interleaved)) != FA_OK) return st;
     if (B == 0 || T == 0) return FA_OK;
     if (!k || !v || !start) return fa_refuse(fn, "NULL buffer");
     a.format = cache->format; a.B = B; a.T = T;
@@ -619,7 +619,7 @@ extern "C" fa_status fa_cache_write(const fa_kv_cache *cache, int32_t dtype, int
     a.kb = k_batch_stride; a.kt = k_token_stride; a.kh = k_head_stride;
     a.vb = v_batch_stride; a.vt = v_token_stride; a.vh = v_head_stride;
     a.start = start; a.count = count; a.pos = positions; a.phase = phase;
-    a.rot = positions ? rot_dim : 0; a.interleaved = interleaved; a.mscale = mscale;
+    a.rot = positions && phase ? rot_dim : 0; a.interleaved = interleaved; a.mscale = mscale;
     if ((int64_t)B * T > 2147483647 / cache->kv_heads) return fa_refuse(fn, "B * T * kv_heads out of range");
     cudaStream_t s = (cudaStream_t)stream;
     if (dtype == FA_DTYPE_F32) return launch_write<float>(a, s);

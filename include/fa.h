@@ -428,7 +428,7 @@ typedef struct {
  *   page_table      [B, max_pages] int32; slots past max_pages * page_size are ignored
  *   start, count    [B] int32; count may be NULL (all T tokens)
  *   positions       [B, T] int32 and phase [rot_dim / 2] as for fa_rope rotate the keys;
- *                   both NULL stores the keys as they are
+ *                   both NULL, or rot_dim = 0, stores the keys as they are
  * Two tokens of one call must not share a slot.  Errors: FA_ERR_INVALID_ARG, FA_ERR_CUDA.
  */
 fa_status fa_cache_write(const fa_kv_cache *cache, int32_t dtype, int32_t B, int32_t T, const void *k,
