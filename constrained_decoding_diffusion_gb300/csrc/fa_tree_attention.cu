@@ -36,7 +36,7 @@
 // of O += P V, with V read from the same layout as K but as the MN-major operand.
 //
 // What bounds it, and what it measured (head_dim 128, 8 key/value heads, replayed in a graph).  16-bit
-// cache: 16 sequences of 8192 slots x 256 rows 154 us, 549 MB read (3.6 TB/s) and 140 GFLOP (0.9
+// cache: 16 sequences of 8192 slots x 256 rows 152 us, 549 MB read (3.6 TB/s) and 140 GFLOP (0.9
 // PFLOP/s): per tile of 128 slots 2.1 us an SM, of which the softmax of 256 rows takes most (copies
 // 1.45, MMA 1.7); about 40 us are fixed (launch, first tiles, results).  8-bit cache: 2 x 98304 slots
 // x 64 rows 185 us (2.2 TB/s): the conversion of a tile takes 1.6 us, its copy 0.7.
@@ -60,9 +60,12 @@ namespace {
 constexpr int TS = 128;                      // slots of a tile, rows of a stream
 constexpr int NLOAD = 8 * 32, NTHR = 20 * 32;
 // registers a thread of each role, of the 96 the block is launched with: 256 softmax + 256 load +
-// 128 MMA threads use 640 * 96 either way.  (8-bit: the code of masked tiles spills a few; 128, 72 and 80 measured 3%
-// slower, 136, 64 and 80 2%.)
-template <bool E4M3> struct Regs { static constexpr int SOFTMAX = E4M3 ? 128 : 112, LOAD = E4M3 ? 64 : 80, MMA = 96; };
+// 128 MMA threads use 640 * 96 either way.  16-bit, 16 x 8192 slots x 256 rows: 112, 80 and 96 157 us, 120, 72 and
+// 96 153 (head_dim up to 64: the loads would spill), 128, 64 and 96 157.  8-bit, where the code of masked tiles
+// spills a few either way: 128, 72 and 80 and 136, 64 and 80 measured 3% and 2% slower than 128, 64 and 96.
+template <int DP, bool E4M3> struct Regs {
+    static constexpr int SOFTMAX = E4M3 ? 128 : DP == 128 ? 120 : 112, LOAD = E4M3 ? 64 : DP == 128 ? 72 : 80, MMA = 96;
+};
 constexpr long long kSpinCycles = 2000000000LL;
 constexpr int kUnitCost = 3;                 // what starting a unit costs, in tiles
 
@@ -338,7 +341,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a, const __grid_c
     Segment s;
 
     if (warp >= 16) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<E4M3>::MMA));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<DP, E4M3>::MMA));
         if (warp == 16 && lane == 0) {
             // ---- the MMAs
             constexpr uint32_t fmt = F16 ? 0u : 1u;
@@ -553,7 +556,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a, const __grid_c
         }
     } else if (warp >= 8) {
         // ---- loading
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<E4M3>::LOAD));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<DP, E4M3>::LOAD));
         const int lt = tid - 256;
         const uint32_t ring = smem_u32(smem + S::RING);
         Ring<S::NS> put;                         // the tile to fill: free at first, then when it has been used
@@ -661,7 +664,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attend(AttendArgs a, const __grid_c
         }
     } else {
         // ---- softmax: stream st, row r of its tile
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<E4M3>::SOFTMAX));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<DP, E4M3>::SOFTMAX));
         const int st = warp >> 2, r = tid & 127;
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t ts = tmem + lane_base + st * TS, to = tmem + lane_base + 256 + st * DP;
