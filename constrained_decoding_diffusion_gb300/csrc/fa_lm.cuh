@@ -72,6 +72,16 @@ __device__ __forceinline__ uint32_t fa_to_e4m3x2(float a, float b) {
     return r;
 }
 
+// mscale * (cos, sin) of position t times phase (a 64-bit fraction of a turn): the product wraps around at
+// whole turns whatever the position, and its upper 32 bits, rounded to fp32, are the angle: off by up to 2^-26
+// turn (a tenth of a millionth of a radian), where fp32's own sines and products are off by as much.
+__device__ __forceinline__ float2 fa_turn(int32_t t, uint64_t phase, float mscale, bool inverse) {
+    const int32_t frac = (int32_t)(uint32_t)(((uint64_t)(int64_t)t * phase) >> 32);
+    float s, c;
+    sincospif((float)frac * (1.0f / 2147483648.0f), &s, &c);
+    return make_float2(mscale * c, mscale * (inverse ? -s : s));
+}
+
 #define FA_E4M3_MAX 448.0f
 
 // A paged cache as kernels see it.  Rows are (page, head, place); row r starts at element

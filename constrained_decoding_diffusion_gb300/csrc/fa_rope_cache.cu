@@ -6,16 +6,6 @@ namespace {
 
 constexpr int NT = 256;
 
-// mscale * (cos, sin) of position t times phase (a 64-bit fraction of a turn): the product wraps around at
-// whole turns whatever the position, and its upper 32 bits, rounded to fp32, are the angle: off by up to 2^-26
-// turn (a tenth of a millionth of a radian), where fp32's own sines and products are off by as much.
-__device__ __forceinline__ float2 turn(int32_t t, uint64_t phase, float mscale, bool inverse) {
-    const int32_t frac = (int32_t)(uint32_t)(((uint64_t)(int64_t)t * phase) >> 32);
-    float s, c;
-    sincospif((float)frac * (1.0f / 2147483648.0f), &s, &c);
-    return make_float2(mscale * c, mscale * (inverse ? -s : s));
-}
-
 unsigned blocks_for(int64_t items) { return (unsigned)std::max<int64_t>(1, std::min<int64_t>((items + NT - 1) / NT, 152 * 16)); }
 
 struct RopeArgs {
@@ -44,7 +34,7 @@ __global__ void __launch_bounds__(NT) k_rope_any(RopeArgs a) {
             continue;
         }
         const int p = a.interleaved ? 2 * i : i, q = a.interleaved ? 2 * i + 1 : i + half;
-        const float2 cs = turn(__ldg(a.pos + n), __ldg(a.phase + i), a.mscale, a.inverse);
+        const float2 cs = fa_turn(__ldg(a.pos + n), __ldg(a.phase + i), a.mscale, a.inverse);
         const float x0 = fa_to_f32(xr[p]), x1 = fa_to_f32(xr[q]);
         yr[p] = fa_from_f32<T>(x0 * cs.x - x1 * cs.y);
         yr[q] = fa_from_f32<T>(x0 * cs.y + x1 * cs.x);
@@ -88,7 +78,7 @@ __global__ void __launch_bounds__(NT, rope_blocks<T>()) k_rope(RopeArgs a, int t
             if (!made) {
                 for (int j = tid; j < here * half; j += NT) {
                     const int t = j / half, p = j - t * half;
-                    table[t * half + p % P * step + p / P] = turn(__ldg(a.pos + n0 + t), __ldg(a.phase + p), a.mscale, a.inverse);
+                    table[t * half + p % P * step + p / P] = fa_turn(__ldg(a.pos + n0 + t), __ldg(a.phase + p), a.mscale, a.inverse);
                 }
                 __syncthreads();
                 made = true;
@@ -198,7 +188,7 @@ __global__ void __launch_bounds__(NT) k_cache_write_any(WriteArgs a) {
                 const int pair = a.interleaved ? d / 2 : d % half;
                 const bool second = a.interleaved ? d & 1 : d >= half;
                 const int mate = a.interleaved ? d ^ 1 : (second ? d - half : d + half);
-                const float2 cs = turn(a.pos[bt], a.phase[pair], a.mscale, false);
+                const float2 cs = fa_turn(a.pos[bt], a.phase[pair], a.mscale, false);
                 const float y = fa_to_f32(x[mate]);
                 f[i] = second ? y * cs.y + f[i] * cs.x : f[i] * cs.x - y * cs.y;
             }
@@ -295,7 +285,7 @@ __global__ void __launch_bounds__(NT, write_blocks<T>()) k_cache_write(WriteArgs
     }
     for (int i = threadIdx.x; i < here * half; i += NT) {
         const int t = i / half, p = i - t * half;
-        table[t * half + p % 4 * lanes + p / 4] = turn(__ldg(a.pos + n0 + t), __ldg(a.phase + p), a.mscale, false);
+        table[t * half + p % 4 * lanes + p / 4] = fa_turn(__ldg(a.pos + n0 + t), __ldg(a.phase + p), a.mscale, false);
     }
     __syncthreads();
     int64_t row[U], next_row[U];

@@ -373,3 +373,184 @@ def fa_beam_reorder(src, parent, dst=None, token=None, at: int = 0, stream=None)
                                          _ptr(token, torch.int32, "token", (N, top)), int(at),
                                          _ptr(dst, torch.int32, "dst", (N, top, W)), _stream(stream, src)))
     return dst
+
+
+# ------------------------------------------------------------------ verification of a draft
+
+class Verify:
+    """Owner of the outputs of fa_verify for a fixed (B, T, V).  A call returns the owner's own tensors,
+    which the next one overwrites; state may be the states of the next call."""
+
+    def __init__(self, B: int, T: int, V: int, dtype=torch.float32, device="cuda"):
+        native.load()
+        self.shape, self.dtype = (B, T, V), dtype
+        self.path = torch.empty((B, T), dtype=torch.int32, device=device)
+        self.kept, self.token, self.state = (torch.empty(B, dtype=torch.int32, device=device) for _ in range(3))
+
+    def __call__(self, target, tokens, parents, u, draft=None, count=None, states=None, next=None, live=None, stream=None):
+        """The accepted path of the drafted tokens [B, T] with parents [B, T], the target's weights and, where they
+        were drawn at random, the draft's [B, T, V], given uniform numbers u [B, T]: (path [B, T], kept [B],
+        token [B], state [B]), state None without an automaton (states [B], next and live as from fa_beam_tables)."""
+        B, T, V = self.shape
+        dt = _dtype(target, "target")
+        if target.dtype != self.dtype:
+            raise TypeError("target must be %s, got %s" % (self.dtype, target.dtype))
+        tb, tr = _rows(target, "target", self.shape)[:2]
+        q, db, dr = None, 0, 0
+        if draft is not None:
+            if _dtype(draft, "draft") != dt:
+                raise TypeError("draft must have the type of target")
+            db, dr = _rows(draft, "draft", self.shape)[:2]
+            q = draft.data_ptr()
+        S = 0 if next is None else next.shape[0]
+        _check(_lib().fa_verify(
+            dt, B, T, V, target.data_ptr(), tb, tr, q, db, dr, _ptr(tokens, torch.int32, "tokens", (B, T)),
+            _ptr(parents, torch.int32, "parents", (B, T)), _ptr(count, torch.int32, "count", (B,)),
+            _ptr(u, torch.float32, "u", (B, T)), _ptr(states, torch.int32, "states", (B,)), S,
+            _ptr(next, torch.int16, "next", (S, V)), _ptr(live, torch.int32, "live", (S, (V + 31) // 32)),
+            self.path.data_ptr(), self.kept.data_ptr(), self.token.data_ptr(), self.state.data_ptr() if S else None,
+            _stream(stream, target)))
+        return self.path, self.kept, self.token, self.state if S else None
+
+
+# ------------------------------------------------------------------ pages and slots
+
+FA_PAGES_OK, FA_PAGES_SHORT, FA_PAGES_TOO_LONG = 0, 1, 2
+
+
+class PageTables(NamedTuple):
+    """The pages of a cache's sequences: table [B, max_pages] and held [B], and the pool's free pages, a stack
+    free [n_pages] of which the first n_free [1] are in use; all int32."""
+    table: torch.Tensor
+    held: torch.Tensor
+    free: torch.Tensor
+    n_free: torch.Tensor
+    page_size: int
+
+    @classmethod
+    def empty(cls, B: int, max_pages: int, n_pages: int, page_size: int, device="cuda"):
+        i32 = dict(dtype=torch.int32, device=device)
+        return cls(torch.full((B, max_pages), -1, **i32), torch.zeros(B, **i32),
+                   torch.arange(n_pages - 1, -1, -1, **i32), torch.full((1,), n_pages, **i32), page_size)
+
+
+def fa_pages_resize(pages: PageTables, want, status=None, stream=None):
+    """Give every sequence the pages of want [B] slots, from the pool and back to it, in place: status [B]."""
+    table, held, free, n_free, size = pages
+    B, P = table.shape
+    if status is None:
+        status = _new((B,), torch.int32, table.device, stream)
+    _check(_lib().fa_pages_resize(
+        B, P, size, free.shape[0], _ptr(want, torch.int32, "want", (B,)), _ptr(table, torch.int32, "table", (B, P)),
+        _ptr(held, torch.int32, "held", (B,)), _ptr(free, torch.int32, "free", (free.shape[0],)),
+        _ptr(n_free, torch.int32, "n_free", (1,)), _ptr(status, torch.int32, "status", (B,)), _stream(stream, table)))
+    return status
+
+
+def fa_slot_map(pages: PageTables, start, count, N: int, out=None, stream=None):
+    """Where the tokens start[b] .. start[b] + count[b] - 1 of every sequence go, packed one sequence after another:
+    (slot [N], seq [N], position [N], offset [B + 1])."""
+    table = pages.table
+    B, P = table.shape
+    if out is None:
+        out = [_new((n,), torch.int32, table.device, stream) for n in (N, N, N, B + 1)]
+    slot, seq, position, offset = out
+    _check(_lib().fa_slot_map(
+        B, N, pages.page_size, pages.free.shape[0], _ptr(table, torch.int32, "table", (B, P)), P,
+        _ptr(start, torch.int32, "start", (B,)), _ptr(count, torch.int32, "count", (B,)),
+        _ptr(slot, torch.int32, "slot", (N,)), _ptr(seq, torch.int32, "seq", (N,)),
+        _ptr(position, torch.int32, "position", (N,)), _ptr(offset, torch.int32, "offset", (B + 1,)), _stream(stream, table)))
+    return slot, seq, position, offset
+
+
+# ------------------------------------------------------------------ the latent cache
+
+class _Latent(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_void_p), ("format", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("latent_dim", ctypes.c_int32), ("rope_dim", ctypes.c_int32)]
+
+
+class LatentCache(NamedTuple):
+    """Paged vectors [n_pages, page_size, latent_dim + rope_dim] in float16 or bfloat16 that all heads share:
+    a latent part, of which keys and values are made, then the part of the keys that carries the positions."""
+    rows: torch.Tensor
+    latent_dim: int
+
+    @classmethod
+    def empty(cls, n_pages: int, page_size: int, latent_dim: int, rope_dim: int, dtype=torch.bfloat16, device="cuda"):
+        if dtype not in (torch.float16, torch.bfloat16):
+            raise TypeError("a latent cache is float16 or bfloat16, not %s" % dtype)
+        return cls(torch.empty((n_pages, page_size, latent_dim + rope_dim), dtype=dtype, device=device), latent_dim)
+
+    def describe(self) -> _Latent:
+        rows, latent = self
+        shape = rows.shape
+        form = _FORMAT.get(rows.dtype)
+        if form is None or form == FA_CACHE_E4M3 or len(shape) != 3:
+            raise TypeError("latent rows must be float16 or bfloat16 of shape [n_pages, page_size, latent_dim + rope_dim]")
+        n, g, d = shape
+        return _Latent(_ptr(rows, rows.dtype, "cache.rows", shape), form, n, g, latent, d - latent)
+
+
+def fa_latent_write(cache: LatentCache, latent, key, slot, positions=None, phase=None, interleaved: bool = False,
+                    mscale: float = 1.0, stream=None):
+    """Store latent [N, latent_dim] and key [N, rope_dim] in the slots [N] of a slot map, the keys rotated at
+    positions [N] first when given with a phase table."""
+    c = cache.describe()
+    dt = _dtype(latent, "latent")
+    if _dtype(key, "key") != dt:
+        raise TypeError("key must have the type of latent")
+    N = latent.shape[0]
+    ls, ks = _rows(latent, "latent", (N, c.latent_dim))[0], _rows(key, "key", (N, c.rope_dim))[0]
+    _check(_lib().fa_latent_write(
+        ctypes.byref(c), dt, N, latent.data_ptr(), ls, key.data_ptr(), ks, _ptr(slot, torch.int32, "slot", (N,)),
+        _ptr(positions, torch.int32, "positions", (N,)), _ptr(phase, torch.int64, "phase", (c.rope_dim // 2,)),
+        int(interleaved), mscale, _stream(stream, latent)))
+
+
+def fa_latent_keep(cache: LatentCache, page_table, length, path, stream=None):
+    """Move the slots length[b] + path[b, i] of an accepted path (ascending, ended by -1) to
+    length[b] + i."""
+    c = cache.describe()
+    B, P = page_table.shape
+    n = path.shape[1]
+    _check(_lib().fa_latent_keep(ctypes.byref(c), B, n, _ptr(page_table, torch.int32, "page_table", (B, P)), P,
+                                 _ptr(length, torch.int32, "length", (B,)), _ptr(path, torch.int32, "path", (B, n)),
+                                 _stream(stream, path)))
+
+
+class LatentAttention:
+    """Owner of the workspace and outputs of fa_latent_attention for a fixed (B, T, heads, dims).  A call
+    returns the owner's own tensors, which the next one overwrites."""
+
+    def __init__(self, B: int, T: int, heads: int, latent_dim: int, rope_dim: int, dtype=torch.bfloat16, device="cuda"):
+        n = ctypes.c_size_t()
+        native.load()
+        _check(_lib().fa_latent_attention_workspace_bytes(B, T, heads, latent_dim, rope_dim, ctypes.byref(n)))
+        self.shape, self.latent_dim = (B, T, heads, latent_dim + rope_dim), latent_dim
+        self.ws_bytes = n.value
+        self.workspace = torch.empty(max(n.value, 256), dtype=torch.uint8, device=device)
+        self.out = torch.empty((B, T, heads, latent_dim), dtype=dtype, device=device)
+        self.lse = torch.empty((B, T, heads), dtype=torch.float32, device=device)
+
+    def __call__(self, q, cache: LatentCache, page_table, length, scale: float, mask=None, count=None, stream=None):
+        """Attention of q [B, T, heads, latent_dim + rope_dim] over the cache: (out [B, T, heads, latent_dim],
+        lse).  length, mask and count as for TreeAttention; scale is that of the expanded keys."""
+        B, T, H, D = self.shape
+        c = cache.describe()
+        dt = _dtype(q, "q")
+        if q.dtype != self.out.dtype:
+            raise TypeError("q must be %s, got %s" % (self.out.dtype, q.dtype))
+        if (c.latent_dim, c.rope_dim) != (self.latent_dim, D - self.latent_dim):
+            raise ValueError("the cache's parts are %d and %d, not %d and %d" %
+                             (c.latent_dim, c.rope_dim, self.latent_dim, D - self.latent_dim))
+        sb, st, sh = _rows(q, "q", self.shape)[:3]
+        if B == 1 or T == 1 or H == 1:   # the stride of a single element means nothing, and torch makes any
+            sb, st, sh = sb if B > 1 else 0, st if T > 1 else 0, sh if H > 1 else 0
+        P = page_table.shape[1]
+        _check(_lib().fa_latent_attention(
+            ctypes.byref(c), dt, B, T, H, q.data_ptr(), sb, st, sh,
+            _ptr(page_table, torch.int32, "page_table", (B, P)), P, _ptr(length, torch.int32, "length", (B,)),
+            _ptr(count, torch.int32, "count", (B,)), _ptr(mask, torch.int64, "mask", (B, T, (T + 63) // 64)), scale,
+            self.out.data_ptr(), self.lse.data_ptr(), self.workspace.data_ptr(), self.ws_bytes, _stream(stream, q)))
+        return self.out, self.lse

@@ -36,7 +36,9 @@ EXPORTS = ("fa_compile", "fa_destroy", "fa_query", "fa_export_csr", "fa_step_wor
            "fa_launch_count", "fa_last_error",
            "fa_rope", "fa_cache_write", "fa_cache_read", "fa_cache_keep", "fa_tree_mask",
            "fa_tree_attention_workspace_bytes", "fa_tree_attention", "fa_beam_tables",
-           "fa_beam_select_workspace_bytes", "fa_beam_select", "fa_beam_reorder")
+           "fa_beam_select_workspace_bytes", "fa_beam_select", "fa_beam_reorder",
+           "fa_verify", "fa_pages_resize", "fa_slot_map", "fa_latent_write", "fa_latent_keep",
+           "fa_latent_attention_workspace_bytes", "fa_latent_attention")
 N_STAGES = 4
 STAGES = ("reweight", "upsweep", "topdown", "leaf_commit")
 
@@ -110,6 +112,13 @@ def load(path: str = LIB_PATH):
     lib.fa_beam_select_workspace_bytes.argtypes = [i32, i32, i32, i32, ctypes.POINTER(sz)]
     lib.fa_beam_select.argtypes = [i32, i32, i32, i32, i32, P, i64, i64, P, P, i32, P, P, P, P, P, P, P, sz, P]
     lib.fa_beam_reorder.argtypes = [i32, i32, i32, i64, P, P, P, i64, P, P]
+    lib.fa_verify.argtypes = [i32, i32, i32, i32, P, i64, i64, P, i64, i64, P, P, P, P, P, i32, P, P, P, P, P, P, P]
+    lib.fa_pages_resize.argtypes = [i32, i32, i32, i32, P, P, P, P, P, P, P]
+    lib.fa_slot_map.argtypes = [i32, i32, i32, i32, P, i32, P, P, P, P, P, P, P]
+    lib.fa_latent_write.argtypes = [P, i32, i32, P, i64, P, i64, P, P, P, i32, f32, P]
+    lib.fa_latent_keep.argtypes = [P, i32, i32, P, i32, P, P, P]
+    lib.fa_latent_attention_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, ctypes.POINTER(sz)]
+    lib.fa_latent_attention.argtypes = [P, i32, i32, i32, i32, P, i64, i64, i64, P, i32, P, P, P, f32, P, P, P, sz, P]
     for name in EXPORTS[EXPORTS.index("fa_rope"):]:
         getattr(lib, name).restype = st
     lib.fa_last_error.argtypes = []

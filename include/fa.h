@@ -561,6 +561,161 @@ fa_status fa_beam_reorder(int32_t N, int32_t K, int32_t top, int64_t words, cons
                           const int32_t *parent, const int32_t *token, int64_t at, int32_t *dst, fa_stream stream);
 
 /*
+ * fa_verify -- verification of drafted tokens against a target's probabilities, with given random
+ * numbers: the accepted tokens and the one that follows them are distributed as if they had been drawn
+ * from the target one at a time, whatever the draft was.
+ *
+ * Node j of a sequence's draft is the token tokens[b, j]; it follows node parents[b, j] < j, and node 0 is
+ * the last token of the text (a node whose parent is not an earlier node is never reached).  Row j of
+ * `target` is the distribution of the token after node j.  From node 0 on, the children of the
+ * current node are tested in the order of their numbers.  With r the distribution of the token after the
+ * current node, at first the target's row, and q the draft's row of the current node, child x is accepted
+ * if u[b, x's node] q(x) < r(x), and its node becomes the current one; otherwise r becomes
+ * max(r - q, 0), brought to the sum 1.  Where no child is left, the next token is the first v with
+ * sum_{w <= v} r(w) > u[b, 0].
+ *
+ *   dtype         FA_DTYPE_* of target and draft
+ *   target        [B, T, V] with batch and row strides: weights that need not add up to one.  What is
+ *                 not a positive finite number counts as zero
+ *   draft         [B, T, V] likewise: row p is the distribution that the children of node p were drawn
+ *                 from, independently; or NULL: they were chosen without regard to u (the best beams, say),
+ *                 and q(x) = 1
+ *   tokens        [B, T] int32; a node with a token outside [0, V) is passed over
+ *   parents       [B, T] int32
+ *   count         [B] int32 or NULL: nodes in use.  0: the sequence has ended, kept is 0
+ *   u             [B, T] fp32 in [0, 1)
+ *   states        [B] int32: the automaton's state after node 0, with next and live as from
+ *                 fa_beam_tables, S states.  Both rows are restricted to the tokens with a live bit in the
+ *                 current node's state; a state outside [0, S) has none.  All NULL (S = 0): no automaton
+ *   path          [B, T] int32 out: node 0, the accepted nodes, then -1 (as fa_cache_keep takes it)
+ *   kept          [B] int32 out: nodes on the path
+ *   token         [B] int32 out: the next token, -1 where the last distribution is empty (no weight, or a
+ *                 sum beyond fp32)
+ *   state         [B] int32 out: the state after it (-1 without one), NULL without an automaton
+ * Sums and differences carry 46 bits or more, so that a draw is that of 64-bit arithmetic but for about one
+ * in 10^8.  A rejection that would leave nothing (rounding alone can do it) leaves r as it is.
+ * T <= FA_MAX_DRAFT, B <= 65535, V < 2^31 - 2^16.  Errors: FA_ERR_INVALID_ARG, FA_ERR_CUDA.
+ */
+fa_status fa_verify(int32_t dtype, int32_t B, int32_t T, int32_t V, const void *target, int64_t target_batch_stride,
+                    int64_t target_row_stride, const void *draft, int64_t draft_batch_stride, int64_t draft_row_stride,
+                    const int32_t *tokens, const int32_t *parents, const int32_t *count, const float *u,
+                    const int32_t *states, int32_t S, const int16_t *next, const uint32_t *live, int32_t *path,
+                    int32_t *kept, int32_t *token, int32_t *state, fa_stream stream);
+
+/*
+ * fa_pages_resize -- pages of a cache given out and taken back on the device.  The pool's free pages are a
+ * stack free_pages[0 .. n_free); sequence b holds page_table[b, 0 .. held[b]).  First every sequence that wants
+ * fewer than it holds gives its last pages back: they go on the stack so that the first sequence's first one is
+ * on top.  Then the sequences that want more take theirs from the top, in order; the first one for which there are
+ * not enough and all after it that want more get none.  A call that undoes another restores the stack.
+ *
+ *   page_size    slots of a page, n_pages: pages of the pool
+ *   want         [B] int32 slots: ceil(want / page_size) pages (negative: none)
+ *   page_table   [B, max_pages] int32, in place: entries past held[b] become -1
+ *   held         [B] int32, in place
+ *   free_pages   [n_pages] int32, in place; places past n_free that were taken become -1
+ *   n_free       [1] int32, in place
+ *   status       [B] int32 out: FA_PAGES_*; a refused sequence keeps what it holds
+ * held outside [0, max_pages] and n_free outside [0, n_pages] are taken as the nearest bound; nothing is
+ * written outside the arrays whatever they hold.  B <= 65535, B * max_pages < 2^31.
+ * Errors: FA_ERR_INVALID_ARG, FA_ERR_CUDA.
+ */
+enum {
+    FA_PAGES_OK = 0,
+    FA_PAGES_SHORT = 1,   /* the pool had not enough */
+    FA_PAGES_TOO_LONG = 2 /* more than max_pages pages wanted */
+};
+fa_status fa_pages_resize(int32_t B, int32_t max_pages, int32_t page_size, int32_t n_pages, const int32_t *want,
+                          int32_t *page_table, int32_t *held, int32_t *free_pages, int32_t *n_free, int32_t *status,
+                          fa_stream stream);
+
+/*
+ * fa_slot_map -- where a ragged batch of tokens goes.  Sequence b has count[b] tokens (negative: none) at the
+ * positions start[b], start[b] + 1, ...; they are numbered one sequence after another, up to N.
+ *
+ *   slot      [N] int32 out: page * page_size + place, -1 where the table has no page in [0, n_pages) for it
+ *   seq       [N] int32 out: the sequence, or NULL
+ *   position  [N] int32 out: the position (as fa_rope takes it), or NULL
+ *   offset    [B + 1] int32 out: the number of each sequence's first token, then that of all, at most N; or NULL
+ * Numbers past the last token get -1 in all three.  start + count < 2^31, B <= 65535,
+ * n_pages * page_size < 2^31.
+ * Errors: FA_ERR_INVALID_ARG, FA_ERR_CUDA.
+ */
+fa_status fa_slot_map(int32_t B, int32_t N, int32_t page_size, int32_t n_pages, const int32_t *page_table,
+                      int32_t max_pages, const int32_t *start, const int32_t *count, int32_t *slot, int32_t *seq,
+                      int32_t *position, int32_t *offset, fa_stream stream);
+
+/* A paged cache of one vector a token that all heads share: a latent part, from which keys and values are
+ * made, and a key part that carries the positions.  Sequence b's slot t lies in page
+ * page_table[b * max_pages + t / page_size], place t % page_size. */
+typedef struct {
+    void *rows;          /* [n_pages, page_size, latent_dim + rope_dim], contiguous, 16-byte aligned */
+    int32_t format;      /* FA_CACHE_F16 or FA_CACHE_BF16 */
+    int32_t n_pages;
+    int32_t page_size;   /* a power of two in [1, 1024]; n_pages * page_size < 2^31 */
+    int32_t latent_dim;  /* a multiple of 128 in [128, 512] */
+    int32_t rope_dim;    /* a multiple of 16 in [16, 64] */
+} fa_latent_cache;
+
+/*
+ * fa_latent_write -- store N tokens' vectors in the slots of a slot map, the key part rotated first.
+ *
+ *   dtype           FA_DTYPE_* of latent and key
+ *   latent, key     [N, latent_dim] and [N, rope_dim] with token strides (parts of one projection are fine)
+ *   slot            [N] int32 as from fa_slot_map; a token whose slot is outside [0, n_pages * page_size) is left out
+ *   positions       [N] int32 and phase [rope_dim / 2] as for fa_rope (all of the key part is rotated), or both NULL
+ * Two tokens of one call must not share a slot.  Each element is rounded once.
+ * Errors: FA_ERR_INVALID_ARG, FA_ERR_CUDA.
+ */
+fa_status fa_latent_write(const fa_latent_cache *cache, int32_t dtype, int32_t N, const void *latent,
+                          int64_t latent_stride, const void *key, int64_t key_stride, const int32_t *slot,
+                          const int32_t *positions, const uint64_t *phase, int32_t interleaved, float mscale,
+                          fa_stream stream);
+
+/*
+ * fa_latent_keep -- fa_cache_keep for a latent cache: slot length[b] + path[b, i] is copied to slot length[b] + i
+ * for i = 0, 1, ... until the first path[b, i] that is negative or does not ascend.  P <= FA_MAX_DRAFT.
+ * Errors: FA_ERR_INVALID_ARG, FA_ERR_CUDA.
+ */
+fa_status fa_latent_keep(const fa_latent_cache *cache, int32_t B, int32_t P, const int32_t *page_table,
+                         int32_t max_pages, const int32_t *length, const int32_t *path, fa_stream stream);
+
+/*
+ * fa_latent_attention -- attention of drafted tokens over a latent cache that already holds them, in its absorbed
+ * form: with c[b, t] a slot's whole vector and c'[b, t] its latent part,
+ *     out[b, i, h] = sum_t softmax_t(scale * q[b, i, h] . c[b, t]) c'[b, t]
+ * over the slots that fa_tree_attention takes.  A head's query is its own latent-side product (its query times
+ * the matrix that would make its keys of the latent part), then the rotated part; its result goes through
+ * the matrix that would make its values.
+ *
+ *   dtype        FA_DTYPE_F16 or FA_DTYPE_BF16 of q and out, that of the cache
+ *   q            [B, T, heads, latent_dim + rope_dim] with batch, token and head strides that are
+ *                multiples of 8, 16-byte aligned
+ *   length, count, mask   as for fa_tree_attention
+ *   out          [B, T, heads, latent_dim] contiguous, 16-byte aligned
+ *   lse          [B, T, heads] fp32 or NULL: ln sum_t exp(scale * q . c)
+ *   scale        positive and finite (of the expanded keys' dimension, so there is no default)
+ *   workspace    fa_latent_attention_workspace_bytes() bytes, 256-byte aligned; contents are
+ *                overwritten; concurrent calls need separate workspaces
+ * A row that sees nothing gives out = 0 and lse = -inf.  What a row does not see has no part in its result,
+ * whatever it holds; a row that sees an element that is not finite has no defined result.  Scores, softmax
+ * statistics and sums are fp32; a softmax weight is rounded to the cache's type for the product with the
+ * latent parts, after the weights have been summed.
+ * The same call gives the same bits.  Should a wait inside the kernel run out (about a second), the rows it
+ * held up are NaN.
+ * T <= FA_MAX_DRAFT, B <= 65535, heads <= 1024, max_pages * page_size < 2^31 - 4096, and B * ceil(T * heads / 64) units
+ * of max_pages * page_size / 64 tiles each stay below 2^31 tiles.
+ * Errors: FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED (types), FA_ERR_WORKSPACE_TOO_SMALL, FA_ERR_CUDA.
+ */
+fa_status fa_latent_attention_workspace_bytes(int32_t B, int32_t T, int32_t heads, int32_t latent_dim,
+                                              int32_t rope_dim, size_t *bytes);
+fa_status fa_latent_attention(const fa_latent_cache *cache, int32_t dtype, int32_t B, int32_t T, int32_t heads,
+                              const void *q, int64_t q_batch_stride, int64_t q_token_stride, int64_t q_head_stride,
+                              const int32_t *page_table, int32_t max_pages, const int32_t *length,
+                              const int32_t *count, const uint64_t *mask, float scale, void *out, float *lse,
+                              void *workspace, size_t ws_bytes, fa_stream stream);
+
+/*
  * fa_debug_inject_wait_timeouts -- failure-injection hook for tests (no counterpart on the
  * pages).  The next n_launches launches of the tensor-core span product (|S| >= 128) make
  * their MMA-issuing thread wait, with a short limit (about half a millisecond), on a
