@@ -1,71 +1,613 @@
-// Attention of drafted tokens over a paged latent cache (the absorbed form).
+// Attention of drafted tokens over a paged latent cache (the absorbed form), on the 5th-generation tensor cores.
 //
-// The mathematics: with x_t = log2(e) scale q . c_t, out = sum_t 2^(x_t - m) c'_t / sum_t 2^(x_t - m) in one pass
-// over the slots, m the largest x_t so far; O and the sum are scaled where m grows.
-#include "fa_attention.cuh"
+// The mathematics: with x_t = scale q . c_t, out = sum_t e^(x_t) c'_t / sum_t e^(x_t) in one pass over the slots, c' the
+// latent part of c.  Every weight is taken relative to a reference m of the row, p_t = e^(x_t - m), with l = sum p_t and
+// O = sum p_t c'_t; where a tile's largest score exceeds the reference's by more than 6 / log2(e) (a factor of 64), m moves
+// and O and l are scaled.  Parts over disjoint slots join by their log-sum.
+//
+// The layout.  All heads of all drafted tokens are rows of one problem, 64 to a block, so a slot is read once for 64
+// rows and serves as key and as value.  The accumulator of 64 rows by 512 columns takes half of tensor
+// memory only if it is transposed, with a full 128 lanes of columns: O^T = C'^T P^T, C' read from the very
+// tile that was the key of S = Q C^T, as the MN-major left operand.  (Untransposed, 128 rows would take all of tensor memory
+// and leave no room for S, and 64 rows would leave half the lanes idle.)  S is not transposed, so that a row's maximum and
+// sum lie in four lanes of a warp.  A tile is 64 slots: two of them, the queries and the weights fill shared memory.
+//
+// The work is the list of all tiles of all (sequence, row block) units; one block per SM takes an equal run of it.
+// A unit that is cut leaves partial results, joined by a second small kernel in a fixed order.
+//
+// Roles (14 warps): warps 0-3 softmax and results, warp 4 issues the MMAs, warp 5 the tensor copies of
+// whole tiles before the draft, warps 6-13 load the queries and the tiles in which the draft lies or a sequence ends.
+// Every wait is bounded (about a second).  A wait that runs out marks the block's status; the joining kernel then sets
+// the rows the block had a part in to NaN.
 #include "fa_latent.cuh"
+#include "fa_tensor.cuh"
 
 using namespace fa_attention;
 
 namespace {
 
-constexpr int ROWS = 8;
+constexpr int TS = 64, RB = 64;              // slots of a tile, rows of a block
+constexpr int NLOAD = 8 * 32, NTHR = 14 * 32;
+constexpr int GROUP = 64 * 128;              // 64 rows of 64 columns, 128-byte swizzled
+constexpr int kUnitCost = 2;                 // what starting a unit costs, in tiles
 
-// a warp a row: lane's elements 2 lane + 64 k
-template <class T> __global__ void __launch_bounds__(ROWS * 32) k_latent_simple(AttendArgs a, int latent) {
-    constexpr int K = 9;
-    const int lane = threadIdx.x & 31, D = a.c.head_dim, b = blockIdx.y, row = blockIdx.x * ROWS + (threadIdx.x >> 5);
-    if (row >= a.rows) return;
-    const int ti = row / a.heads, h = row - ti * a.heads;
-    Segment s;
-    extent(a, b, s.slots, s.use, s.end);
-    s.b = b;
-    s.head = 0;
-    const T *q = (const T *)a.q + b * a.qb + ti * a.qt + h * a.qh;
-    float2 x[K], o[K];
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int i = 2 * lane + 64 * k;
-        o[k] = make_float2(0.0f, 0.0f);
-        x[k] = i < D ? make_float2(fa_to_f32(q[i]), fa_to_f32(q[i + 1])) : make_float2(0.0f, 0.0f);
-    }
-    float m = -INFINITY, l = 0.0f;
-    const Rows rows(a, s);
-    uint32_t sees = 0;
-    for (int t = 0; t < s.end && ti < s.use; ++t) {
-        if (t % 32 == 0) sees = seen_bits(a, s, ti, t);
-        if (!(sees >> (t & 31) & 1)) continue;
-        const int64_t at = rows.row((uint32_t)t);
-        if (at < 0) continue;
-        const T *c = (const T *)a.c.k + at * D;
-        float2 y[K];
-        float dot = 0.0f;
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int i = 2 * lane + 64 * k;
-            y[k] = i < D ? make_float2(fa_to_f32(c[i]), fa_to_f32(c[i + 1])) : make_float2(0.0f, 0.0f);
-            dot = fmaf(x[k].x, y[k].x, fmaf(x[k].y, y[k].y, dot));
-        }
-        dot = fa_warp_sum(dot) * (a.scale * kLog2e);
-        const float top = fmaxf(m, dot), f = m == -INFINITY ? 0.0f : ex2(m - top), p = ex2(dot - top);
-        m = top;
-        l = l * f + p;
-#pragma unroll
-        for (int k = 0; k < K; ++k) o[k] = make_float2(fmaf(p, y[k].x, o[k].x * f), fmaf(p, y[k].y, o[k].y * f));
-    }
-    const int64_t to = ((int64_t)b * a.T + ti) * a.heads + h;
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int i = 2 * lane + 64 * k;
-        if (i >= latent) continue;
-        ((T *)a.out)[to * latent + i] = fa_from_f32<T>(o[k].x * inv);
-        ((T *)a.out)[to * latent + i + 1] = fa_from_f32<T>(o[k].y * inv);
-    }
-    if (a.lse && lane == 0) a.lse[to] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+template <int L> struct Shape {
+    static constexpr int G = L / 64 + 1, TILE = G * GROUP;                        // the key part pads to 64 columns
+    static constexpr int NS = L == 128 ? 6 : L == 256 ? 4 : 2;                    // tiles in the ring
+    static constexpr int Q = 0, RING = TILE, P = RING + NS * TILE, MISC = P + RB * 128;
+};
+
+struct Misc {
+    uint64_t full[6], empty[6], s_full[2], by_hand[8], p_full, pv_done, q_full, q_free, o_free, done;
+    uint32_t there[6][2], odd[6][2];   // per place of the ring: slots that a page holds; (by hand) those with an element that is not finite
+    float factor[2][RB], inverse[2][RB];
+    uint32_t tmem;
+    int fail;
+};
+
+template <int L> constexpr size_t smem_bytes() { return Shape<L>::MISC + sizeof(Misc) + sizeof(Work); }
+
+// where chunk c (16 bytes = 8 elements) of row r lies in a 128-byte-swizzled tile of 64 rows
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+    return (uint32_t)((c >> 3) * GROUP + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+// a tile that the loading warps bring: the draft or a sequence's end lies in it
+__device__ __forceinline__ bool by_hand(const AttendArgs &a, const Segment &s, int tile) {
+    return !a.box_rows || (s.t0 + tile + 1) * TS > s.slots;
+}
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// 16 lanes by 64 columns: r[4 j + e] is row lane / 4 + 8 (e / 2), column 8 j + 2 (lane % 4) + e % 2
+__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, float (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+          "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+          "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+// whether any of the four softmax warps says so; what they wrote to shared memory before is seen after
+__device__ __forceinline__ bool any_warp(bool x) {
+    uint32_t y;
+    __syncwarp();
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
+        : "=r"(y)
+        : "r"((uint32_t)x)
+        : "memory");
+    return y != 0;
 }
 
-size_t workspace_bytes(int latent) { return 256; }
+template <int L, class T>
+__global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_constant__ CUtensorMap map) {
+    using S = Shape<L>;
+    constexpr int G = S::G;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    static_assert(S::MISC % 8 == 0 && sizeof(Misc) % 4 == 0, "alignment of the parts");
+    Misc &sh = *reinterpret_cast<Misc *>(smem + S::MISC);
+    Work &work = *reinterpret_cast<Work *>(smem + S::MISC + sizeof(Misc));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    constexpr bool F16 = std::is_same<T, __half>::value;
+    constexpr float OFF = F16 ? 8.0f : 0.0f;      // fp16 weights reach from 2^14 down to 2^-24, with 2^8 for the reference
+    const int D = a.c.head_dim;
+    volatile int *fail = &sh.fail;
+    if (smem_u32(smem) & 1023) {                  // the swizzled tiles need it
+        if (tid == 0) a.status[blockIdx.x] = 1;
+        return;
+    }
+    if (tid == 0) {
+        for (int i = 0; i < S::NS; ++i) { mbar_init(&sh.full[i], NLOAD / 32); mbar_init(&sh.empty[i], 1); }
+        for (int i = 0; i < 2; ++i) mbar_init(&sh.s_full[i], 1);
+        for (int i = 0; i < 8; ++i) mbar_init(&sh.by_hand[i], 1);
+        mbar_init(&sh.p_full, 4);
+        mbar_init(&sh.pv_done, 1);
+        mbar_init(&sh.q_full, NLOAD / 32);
+        mbar_init(&sh.q_free, 1);
+        mbar_init(&sh.o_free, 4);
+        mbar_init(&sh.done, 1);
+        sh.fail = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 4) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        tc_fence_before();
+    }
+    fa_let_next_start();
+    plan(a, work);
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem, ring = smem_u32(smem + S::RING);
+    Walk walk(a, work, blockIdx.x, gridDim.x);
+    Segment s;
+
+    if (warp == 4) {
+        if (lane == 0) {
+            // ---- the MMAs
+            constexpr uint32_t fmt = F16 ? 0u : 1u, idesc = (1u << 4) | (fmt << 7) | (fmt << 10);
+            constexpr uint32_t idesc_s = idesc | (uint32_t)(RB >> 4) << 24 | (uint32_t)(TS >> 3) << 17;
+            const uint64_t qd = umma_desc(smem_u32(smem + S::Q), 16), pd = umma_desc(smem_u32(smem + S::P), 16);
+            Ring<S::NS> get, use;                 // the next tile's place for scores, and for values
+            uint32_t ns = 0, np = 0, nseg = 0;
+            const int steps = D / 16;
+            if (a.inject && blockIdx.x == 0) {    // a failure test: only this thread completes `done`, later
+                const long long t0 = clock64();
+                while (!mbar_try_wait(&sh.done, 0) && clock64() - t0 < kInjectCycles) {}
+                *fail = 1;
+            }
+            while (!*fail && walk.next(a, s)) {
+                if (!mbar_wait(&sh.q_full, nseg & 1, fail)) break;
+                const int rows = min(a.rows - RB * s.block, RB);
+                const uint32_t idesc_o = idesc | (uint32_t)(128 >> 4) << 24 | (uint32_t)((rows + 15) / 16 * 2) << 17 | 1u << 15;
+                int issued = 0;
+                bool ok = true;
+                for (int j = 0; j < s.n && ok; ++j) {
+                    const long long t0 = clock64();
+                    while (true) {
+                        // the next tile's scores as soon as it has come, these weights' product as soon as they are there
+                        if (issued < s.n && issued <= j + 1 && mbar_test(&sh.full[get.slot], get.phase)) {
+                            tc_fence_after();
+                            const uint64_t kd = umma_desc(ring + get.slot * S::TILE, 16);
+                            const uint32_t d = tmem + 256 + (ns & 1) * TS;
+                            for (int k = 0; k < steps; ++k) {
+                                const uint32_t off = ((k >> 2) * GROUP + (k & 3) * 32) / 16;
+                                umma_ss(d, qd + off, kd + off, idesc_s, k > 0);
+                            }
+                            umma_commit(&sh.s_full[ns & 1]);
+                            ++ns;
+                            ++get;
+                            if (++issued == s.n) umma_commit(&sh.q_free);
+                        }
+                        if (issued > j && mbar_test(&sh.p_full, np & 1)) break;
+                        if (*fail || clock64() - t0 > kSpinCycles) { *fail = 1; ok = false; break; }
+                    }
+                    if (!ok) break;
+                    ++np;
+                    if (j == 0 && nseg > 0 && !mbar_wait(&sh.o_free, (nseg - 1) & 1, fail)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint64_t vd = umma_desc(ring + use.slot * S::TILE, GROUP);
+#pragma unroll 1
+                    for (int c = 0; c < L / 128; ++c)
+#pragma unroll
+                        for (int k = 0; k < TS / 16; ++k)
+                            umma_ss(tmem + c * RB, vd + (2 * c * GROUP + k * 2048) / 16, pd + k * 32 / 16, idesc_o, j > 0 || k > 0);
+                    umma_commit(&sh.pv_done);
+                    umma_commit(&sh.empty[use.slot]);
+                    ++use;
+                }
+                if (!ok) break;
+                ++nseg;
+            }
+            // every MMA issued has completed before tensor memory is released
+            umma_commit(&sh.done);
+            const long long t0 = clock64();
+            while (!mbar_try_wait(&sh.done, 0))
+                if (clock64() - t0 > kSpinCycles) { *fail = 1; break; }
+        }
+    } else if (warp == 5) {
+        // ---- tensor copies: a lane per box of (a page's rows) x 64 columns
+        const int box = a.box_rows ? a.box_rows : TS, boxes = TS / box, mine = lane % boxes;
+        const uint32_t in_page = (1u << a.c.page_shift) - 1;
+        Ring<S::NS> put;
+        bool again = false, ok = true;
+        uint32_t hand = 0, copied = 0, copied_phase = 0;   // bit i: place i's last tile came by copies, and its phase
+        while (ok && walk.next(a, s)) {
+            const int32_t *pages = a.c.page_table + (int64_t)s.b * a.c.max_pages;
+            for (int j = 0; j < s.n; ++j) {
+                const bool hand_tile = by_hand(a, s, j);
+                const uint32_t first = (uint32_t)(s.t0 + j) * TS + mine * box;
+                uint32_t page = 0;
+                if (!hand_tile) page = (uint32_t)__ldg(pages + (first >> a.c.page_shift));
+                if (again && !mbar_wait(&sh.empty[put.slot], put.phase ^ 1, fail)) { ok = false; break; }
+                __syncwarp();
+                if (!hand_tile) {
+                    const bool held = page < (uint32_t)a.c.n_pages;
+                    const uint32_t all = __ballot_sync(0xffffffffu, held);
+                    if (lane == 0) {
+                        uint64_t there = ~0ull;
+                        if (all != 0xffffffffu)
+                            for (int i = 0; i < boxes; ++i)
+                                if (!(all >> i & 1)) there &= ~((box == 64 ? ~0ull : (1ull << box) - 1) << (i * box));
+                        sh.there[put.slot][0] = (uint32_t)there;
+                        sh.there[put.slot][1] = (uint32_t)(there >> 32);
+                        mbar_expect(&sh.full[put.slot], S::TILE);
+                    }
+                    __syncwarp();
+                    if (lane > 0 && lane < NLOAD / 32) mbar_arrive(&sh.full[put.slot]);
+                    const int y = held ? (int)((page << a.c.page_shift) + (first & in_page)) : a.c.n_pages << a.c.page_shift;   // past the end: zeros
+                    for (int k = lane; k < boxes * G; k += 32)
+                        tensor_copy(ring + put.slot * S::TILE + k / boxes * GROUP + mine * box * 128, &map, k / boxes * 64, y,
+                                    &sh.full[put.slot]);
+                    copied |= 1u << put.slot;
+                    copied_phase = (copied_phase & ~(1u << put.slot)) | put.phase << put.slot;
+                } else {
+                    // at most NS tiles are under way, so the loading warps are never 8 behind
+                    if (lane == 0) mbar_arrive(&sh.by_hand[hand & 7]);
+                    ++hand;
+                    copied &= ~(1u << put.slot);           // the place is free: its last copy has landed
+                }
+                ++put;
+                again |= put.slot == 0;
+            }
+        }
+        // no copy may land after the block has gone
+        for (int i = 0; i < S::NS; ++i)
+            if (copied >> i & 1) {
+                const long long t0 = clock64();
+                while (!mbar_try_wait(&sh.full[i], copied_phase >> i & 1) && clock64() - t0 < kSpinCycles) {}
+            }
+    } else if (warp > 5) {
+        // ---- queries, and tiles by hand
+        const int lt = tid - 6 * 32;
+        constexpr int CPR = G * 8, ITER = CPR * 64 / NLOAD;   // chunks of a row; of a thread
+        Ring<S::NS> put;
+        uint32_t nseg = 0, hand = 0;
+        bool ok = true;
+        while (ok && walk.next(a, s)) {
+            if (nseg > 0 && !mbar_wait(&sh.q_free, (nseg - 1) & 1, fail)) break;
+            const int rows = min(a.rows - RB * s.block, RB);
+            const uint32_t q_at = smem_u32(smem + S::Q);
+#pragma unroll 6
+            for (int i = 0; i < ITER; ++i) {
+                const int c = lt + i * NLOAD, r = c / CPR, ch = c - r * CPR;
+                const int rr = RB * s.block + (r < rows ? r : 0), ti = rr / a.heads;
+                const bool there = r < rows && ch * 8 < D;
+                const T *src = (const T *)a.q + s.b * a.qb + ti * a.qt + (rr - ti * a.heads) * a.qh + (there ? ch * 8 : 0);
+                cp_async16(q_at + chunk_at(r, ch), src, there);
+            }
+            cp_commit();
+            cp_wait<0>();
+            proxy_fence();
+            warp_arrive(&sh.q_full);
+            ++nseg;
+            const Rows at(a, s);
+            for (int j = 0; j < s.n; ++j, ++put) {
+                if (!by_hand(a, s, j)) continue;
+                if (!mbar_wait(&sh.by_hand[hand & 7], hand >> 3 & 1, fail)) { ok = false; break; }
+                ++hand;
+                const uint32_t first = (uint32_t)(s.t0 + j) * TS;
+                const bool draft = first + TS > (uint32_t)s.slots;
+                if (lt < 32) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t t = first + 32 * h + lane;
+                        const bool there = t < (uint32_t)s.end && at.page(t) < at.n_pages;
+                        const uint32_t bits = __ballot_sync(0xffffffffu, there);
+                        if (lane == 0) { sh.there[put.slot][h] = bits; sh.odd[put.slot][h] = 0; }
+                    }
+                }
+                const uint32_t dst = ring + put.slot * S::TILE;
+#pragma unroll 6
+                for (int i = 0; i < ITER; ++i) {
+                    const int c = lt + i * NLOAD, r = c / CPR, ch = c - r * CPR;
+                    const uint32_t t = first + r;
+                    const int64_t row = t < (uint32_t)s.end ? at.row(t) : -1;
+                    const bool there = row >= 0 && ch * 8 < D;
+                    cp_async16(dst + chunk_at(r, ch), (const T *)a.c.k + (there ? row * D + ch * 8 : 0), there);
+                }
+                cp_commit();
+                cp_wait<0>();
+                if (draft) {
+                    // drafted elements that are not finite are left out, and their slots marked
+                    bar_sync(2, NLOAD);                    // the marks have been cleared
+#pragma unroll 1
+                    for (int i = 0; i < ITER; ++i) {
+                        const int c = lt + i * NLOAD, r = c / CPR, ch = c - r * CPR;
+                        if (first + r < (uint32_t)s.slots || first + r >= (uint32_t)s.end) continue;
+                        uint4 *v = reinterpret_cast<uint4 *>(smem + S::RING + put.slot * S::TILE + chunk_at(r, ch));
+                        uint4 x = *v;
+                        if (zero_odd<T>(x)) {
+                            *v = x;
+                            atomicOr(&sh.odd[put.slot][r >> 5], 1u << (r & 31));
+                        }
+                    }
+                }
+                proxy_fence();
+                warp_arrive(&sh.full[put.slot]);
+            }
+        }
+    } else {
+        // ---- softmax: a thread has the rows r0 and r0 + 8, columns 8 i + 2 (lane % 4) and the next
+        const int r0 = 16 * warp + (lane >> 2), col = 2 * (lane & 3);
+        const uint32_t lanes = (uint32_t)(32 * warp) << 16, to = tmem + lanes;
+        const float c = a.scale * kLog2e;
+        unsigned char *const p_at = smem + S::P + r0 * 128 + (lane & 3) * 4;
+        Ring<S::NS> get;
+        uint32_t tiles = 0, npv = 0, nseg = 0;
+        while (walk.next(a, s)) {
+            const int rows = min(a.rows - RB * s.block, RB);
+            int ti[2];
+            bool used[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int row = r0 + 8 * q;
+                ti[q] = (RB * s.block + row) / a.heads;
+                used[q] = row < rows && ti[q] < s.use;
+            }
+            float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+            for (int j = 0; j < s.n; ++j) {
+                const int first = (s.t0 + j) * TS;
+                mbar_wait(&sh.full[get.slot], get.phase, fail);            // (its marks)
+                mbar_wait(&sh.s_full[tiles & 1], tiles >> 1 & 1, fail);
+                __syncwarp();
+                tc_fence_after();
+                float x[32];
+                tmem_ld_rows(to + 256 + (tiles & 1) * TS, x);
+                const bool hand = by_hand(a, s, j);
+                const uint32_t there0 = sh.there[get.slot][0], there1 = sh.there[get.slot][1];
+                if (hand || (there0 & there1) != 0xffffffffu) {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t see[2] = {0, 0}, odd[2] = {0, 0};
+                        if (used[q]) {
+                            see[0] = there0 & seen_bits(a, s, ti[q], first);
+                            see[1] = there1 & seen_bits(a, s, ti[q], first + 32);
+                        }
+                        if (hand) {
+                            odd[0] = see[0] & sh.odd[get.slot][0];
+                            odd[1] = see[1] & sh.odd[get.slot][1];
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                float &y = x[4 * i + 2 * q + e];
+                                const int at = 8 * (i & 3) + col + e;
+                                if (!(see[i >> 2] >> at & 1)) y = -INFINITY;
+                                if (odd[i >> 2] >> at & 1) y = NAN;
+                            }
+                    }
+                }
+                float f[2];
+                bool grow = false;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(x[4 * i + 2 * q], x[4 * i + 2 * q + 1]));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    f[q] = 1.0f;
+                    if ((top - m[q]) * c > kGrow) {                         // (not where both are -inf)
+                        f[q] = ex2((m[q] - top) * c);
+                        m[q] = top;
+                        grow = true;
+                    }
+                    const float ref = m[q] == -INFINITY ? 0.0f : m[q];
+                    l[q] *= f[q];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float &y = x[4 * i + 2 * q + e];
+                            y = ex2(fmaf(y - ref, c, OFF));
+                            l[q] += y;
+                        }
+                }
+                bool scale_now = false;
+                if (j > 0) {
+                    if ((lane & 3) == 0) {
+                        sh.factor[tiles & 1][r0] = f[0];
+                        sh.factor[tiles & 1][r0 + 8] = f[1];
+                    }
+                    scale_now = any_warp(grow);
+                    // the accumulator and the weights' place are free
+                    mbar_wait(&sh.pv_done, npv++ & 1, fail);
+                    __syncwarp();
+                    tc_fence_after();
+                }
+                if (scale_now) {
+                    const float *by = sh.factor[tiles & 1];
+#pragma unroll 1
+                    for (int w = 0; w < L / 128 * RB; w += 32) {
+                        if ((w & (RB - 1)) >= rows) continue;
+                        float o[32];
+                        tmem_ld32(to + w, o);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            const float4 y = *reinterpret_cast<const float4 *>(by + (w & (RB - 1)) + i);
+                            o[i] *= y.x; o[i + 1] *= y.y; o[i + 2] *= y.z; o[i + 3] *= y.w;
+                        }
+                        tmem_st32(to + w, o);
+                    }
+                    tmem_st_wait();
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    unsigned char *at = p_at + ((i ^ (lane >> 2)) << 4);
+                    *reinterpret_cast<uint32_t *>(at) = fa_pack2(x[4 * i], x[4 * i + 1], T());
+                    *reinterpret_cast<uint32_t *>(at + 8 * 128) = fa_pack2(x[4 * i + 2], x[4 * i + 3], T());
+                }
+                proxy_fence();
+                tc_fence_before();
+                warp_arrive(&sh.p_full);
+                ++tiles;
+                ++get;
+            }
+            // ---- the result
+            const bool partial = s.n < s.nt;
+            const int64_t prow = ((int64_t)blockIdx.x * 2 + (s.t0 == 0 ? 1 : 0)) * RB, orow = (int64_t)s.b * a.T * a.heads + RB * s.block;
+            float *inverse = sh.inverse[nseg & 1];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int row = r0 + 8 * q;
+                l[q] += __shfl_xor_sync(0xffffffffu, l[q], 1);
+                l[q] += __shfl_xor_sync(0xffffffffu, l[q], 2);
+                if ((lane & 3) == 0) {
+                    const bool some = used[q] && l[q] != 0.0f;
+                    inverse[row] = some ? 1.0f / l[q] : 0.0f;
+                    const float lse = some ? fmaf(m[q], c, log2f(l[q]) - OFF) : -INFINITY;
+                    if (row < rows) {
+                        if (partial) a.part_lse[prow + row] = lse;
+                        else if (a.lse) a.lse[orow + row] = lse * kLn2;
+                    }
+                }
+            }
+            mbar_wait(&sh.pv_done, npv++ & 1, fail);
+            bar_sync(1, 128);
+            tc_fence_after();
+            const int dim = 32 * warp + lane;
+#pragma unroll 1
+            for (int w = 0; w < L / 128 * RB; w += 32) {
+                const int row = w & (RB - 1);
+                if (row >= rows) continue;
+                float o[32];
+                tmem_ld32(to + w, o);
+                const int n = min(rows - row, 32);
+                const int64_t at = (w / RB) * 128 + dim;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    if (i >= n) break;
+                    const float by = inverse[row + i], y = by == 0.0f ? 0.0f : o[i] * by;
+                    if (partial) a.part_o[(prow + row + i) * L + at] = y;
+                    else ((T *)a.out)[(orow + row + i) * L + at] = fa_from_f32<T>(y);
+                }
+            }
+            tc_fence_before();
+            warp_arrive(&sh.o_free);
+            ++nseg;
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (tid == 0) a.status[blockIdx.x] = sh.fail;
+    if (warp == 4) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// Joins the parts of units that were cut, in an order that depends on nothing but the lengths.  Block (unit, N rows):
+// 8 / N warps share a row's parts, their lanes across the columns, and their sums are added up.
+template <int L, class T, int N>
+__global__ void __launch_bounds__(256) k_latent_join(AttendArgs a, int runs) {
+    constexpr int SUBS = 8 / N, V = L / 128;               // vectors of four columns a lane
+    __shared__ Work work;
+    __shared__ int before;
+    __shared__ float4 sums[SUBS > 1 ? 8 : 1][V][32];
+    __shared__ float totals[8];
+    plan(a, work);
+    const int b = (int)(blockIdx.x / a.blocks), block = (int)(blockIdx.x % a.blocks);
+    if (threadIdx.x == 0) {
+        const int per = run_length(a);
+        int g = work.cum[b / per];
+        for (int i = b / per * per; i < b; ++i) g += places_of(a, i);
+        before = g;
+    }
+    __syncthreads();
+    const int nt = tiles_of(a, b), total = work.cum[RUNS] * a.blocks, g0 = before * a.blocks + block * (nt + a.unit_cost), g1 = g0 + nt - 1;
+    runs = min(total, runs);
+    // the runs that hold the unit's first and last tile
+    const int c0 = (int)((((int64_t)g0 + 1) * runs - 1) / total), c1 = (int)((((int64_t)g1 + 1) * runs - 1) / total);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, parts = c1 - c0 + 1;
+    const int rows = min(a.rows - RB * block, RB), row = N * blockIdx.y + warp / SUBS, sub = warp % SUBS;
+    fa_wait_for_previous();                                // by every block: the next kernel waits for this one only
+    if (N * (int)blockIdx.y >= rows) return;
+    bool failed = false;
+    for (int c = c0; c <= c1; ++c) failed |= a.status[c] != 0;
+    if (parts == 1 && !failed) return;
+    // of a run's two partial results the second holds a unit's first part
+    auto part = [&](int i) { return ((int64_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * RB + row; };
+    float top = -INFINITY, l = 0.0f;
+    float4 o[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) o[v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (row < rows && parts > 1) {
+        for (int i = lane; i < parts; i += 32) top = fmaxf(top, a.part_lse[part(i)]);   // a NaN is met below
+#pragma unroll
+        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        for (int first = sub; first < parts; first += 32 * SUBS) {
+            const int mine = first + lane * SUBS, n = min(32, (parts - first + SUBS - 1) / SUBS);
+            const float x = mine < parts ? a.part_lse[part(mine)] : -INFINITY, f = x == -INFINITY ? 0.0f : ex2(x - top);
+#pragma unroll 4
+            for (int i = 0; i < n; ++i) {
+                const float w = __shfl_sync(0xffffffffu, f, i);
+                const float4 *src = reinterpret_cast<const float4 *>(a.part_o + part(first + i * SUBS) * L) + lane;
+                l += w;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const float4 y = src[32 * v];
+                    o[v].x = fmaf(w, y.x, o[v].x); o[v].y = fmaf(w, y.y, o[v].y);
+                    o[v].z = fmaf(w, y.z, o[v].z); o[v].w = fmaf(w, y.w, o[v].w);
+                }
+            }
+        }
+    }
+    if (SUBS > 1) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) sums[warp][v][lane] = o[v];
+        if (lane == 0) totals[warp] = l;
+        __syncthreads();
+        if (sub) return;
+#pragma unroll
+        for (int i = 1; i < SUBS; ++i) {
+            l += totals[warp + i];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float4 y = sums[warp + i][v][lane];
+                o[v].x += y.x; o[v].y += y.y; o[v].z += y.z; o[v].w += y.w;
+            }
+        }
+    }
+    if (row >= rows) return;
+    const float inv = failed ? NAN : l == 0.0f ? 0.0f : 1.0f / l;
+    const int64_t at = (int64_t)b * a.T * a.heads + RB * block + row;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        *reinterpret_cast<uint2 *>((T *)a.out + at * L + 128 * v + 4 * lane) =
+            make_uint2(fa_pack2(o[v].x * inv, o[v].y * inv, T()), fa_pack2(o[v].z * inv, o[v].w * inv, T()));
+    if (a.lse && lane == 0) a.lse[at] = failed ? NAN : l == 0.0f ? -INFINITY : (top + log2f(l)) * kLn2;
+}
+
+// two partial results of 64 rows and a status for each block
+size_t workspace_bytes(int latent) { return (size_t)MAX_CTAS * 2 * RB * (latent + 1) * sizeof(float) + MAX_CTAS * sizeof(int); }
+
+// The cache's tensor map: rows of its elements, boxes of one page's rows by 64 columns, 128-byte swizzled.  False where
+// it cannot have one (pages of fewer than the eight rows of a swizzle atom).
+bool make_map(const fa_latent_cache *c, int box_rows, CUtensorMap *map) {
+    const fa_encode_t encode = fa_tensor_map_encoder();
+    const int64_t rows = (int64_t)c->n_pages * c->page_size;
+    if (!encode || box_rows < 8 || rows < 1) return false;
+    const cuuint64_t dim = (cuuint64_t)(c->latent_dim + c->rope_dim), dims[2] = {dim, (cuuint64_t)rows}, strides[1] = {dim * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, step[2] = {1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, c->rows, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int L, class T> fa_status launch(AttendArgs a, const CUtensorMap &map, cudaStream_t s) {
+    constexpr size_t smem = smem_bytes<L>();
+    static_assert(smem <= 232448, "shared memory of a block");
+    int ctas = 0;
+    cudaError_t e = block_count(&ctas);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k_latent<L, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return fa_refuse("fa_latent_attention", cudaGetErrorString(e), FA_ERR_CUDA);
+    a.inject = fa_take_injected_timeout();
+    k_latent<L, T><<<ctas, NTHR, smem, s>>>(a, map);
+    fa_status st = fa_launch_check("latent attention");
+    if (st != FA_OK) return st;
+    const int64_t units = (int64_t)a.B * a.blocks;
+    const int rows = std::min(a.rows, RB);
+    int n = 1;                                             // as few rows a block as keep all blocks on the GPU at once
+    while (n < 8 && units * ((rows + n - 1) / n) > 8 * MAX_CTAS) n *= 2;
+    void (*const join)(AttendArgs, int) = n == 1 ? k_latent_join<L, T, 1> : n == 2 ? k_latent_join<L, T, 2> : n == 4 ? k_latent_join<L, T, 4> : k_latent_join<L, T, 8>;
+    return fa_launch_second("latent attention join", join, dim3((unsigned)units, (unsigned)((rows + n - 1) / n)), 256, 0, s, a, ctas);
+}
+
+template <class T> fa_status launch(const AttendArgs &a, int latent, const CUtensorMap &map, cudaStream_t s) {
+    if (latent == 128) return launch<128, T>(a, map, s);
+    if (latent == 256) return launch<256, T>(a, map, s);
+    if (latent == 384) return launch<384, T>(a, map, s);
+    return launch<512, T>(a, map, s);
+}
 
 fa_status sizes(const char *fn, int32_t B, int32_t T, int32_t heads) {
     if (B < 0 || B > 65535 || T < 0 || T > FA_MAX_DRAFT || heads < 1 || heads > 1024) return fa_refuse(fn, "B, T or heads out of range");
@@ -103,8 +645,8 @@ extern "C" fa_status fa_latent_attention(const fa_latent_cache *cache, int32_t d
     const int64_t slots = (int64_t)max_pages << a.c.page_shift;
     if (slots > 2147483647LL - 4096) return fa_refuse(fn, "max_pages * page_size out of range");
     a.rows = T * heads;
-    a.blocks = (a.rows + 63) / 64;
-    if ((int64_t)B * a.blocks > 2147483647 || (int64_t)B * a.blocks * ((slots + 63) / 64 + 5) > 2147483647)
+    a.blocks = (a.rows + RB - 1) / RB;
+    if ((int64_t)B * a.blocks > 2147483647 || (int64_t)B * a.blocks * ((slots + TS - 1) / TS + 5) > 2147483647)
         return fa_refuse(fn, "B * row blocks * tiles out of range");
     if (B == 0 || T == 0) return FA_OK;
     if (!q || !out || !length) return fa_refuse(fn, "NULL buffer");
@@ -117,9 +659,15 @@ extern "C" fa_status fa_latent_attention(const fa_latent_cache *cache, int32_t d
     a.B = B; a.T = T; a.heads = a.group = heads; a.words = (T + 63) / 64;
     a.q = q; a.qb = q_batch_stride; a.qt = q_token_stride; a.qh = q_head_stride;
     a.length = length; a.count = count; a.mask = mask; a.scale = scale; a.out = out; a.lse = lse;
-    const dim3 grid((unsigned)((a.rows + ROWS - 1) / ROWS), (unsigned)B);
+    a.part_o = (float *)workspace;
+    a.part_lse = a.part_o + (size_t)MAX_CTAS * 2 * RB * cache->latent_dim;
+    a.status = (int *)(a.part_lse + (size_t)MAX_CTAS * 2 * RB);
+    a.tile_shift = 6;
+    a.unit_cost = kUnitCost;
+    CUtensorMap map = {};
+    const int box_rows = std::min(cache->page_size, TS);
+    a.box_rows = make_map(cache, box_rows, &map) ? box_rows : 0;
     cudaStream_t s = (cudaStream_t)stream;
-    if (dtype == FA_DTYPE_F16) k_latent_simple<__half><<<grid, ROWS * 32, 0, s>>>(a, cache->latent_dim);
-    else k_latent_simple<__nv_bfloat16><<<grid, ROWS * 32, 0, s>>>(a, cache->latent_dim);
-    return fa_launch_check("latent attention");
+    if (dtype == FA_DTYPE_F16) return launch<__half>(a, cache->latent_dim, map, s);
+    return launch<__nv_bfloat16>(a, cache->latent_dim, map, s);
 }
