@@ -132,68 +132,74 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
     Segment s;
 
     if (warp == 4) {
-        if (lane == 0) {
-            // ---- the MMAs
-            constexpr uint32_t fmt = F16 ? 0u : 1u, idesc = (1u << 4) | (fmt << 7) | (fmt << 10);
-            constexpr uint32_t idesc_s = idesc | (uint32_t)(RB >> 4) << 24 | (uint32_t)(TS >> 3) << 17;
-            const uint64_t qd = umma_desc(smem_u32(smem + S::Q), 16), pd = umma_desc(smem_u32(smem + S::P), 16);
-            Ring<S::NS> get, use;                 // the next tile's place for scores, and for values
-            uint32_t ns = 0, np = 0, nseg = 0;
-            const int steps = D / 16;
-            if (a.inject && blockIdx.x == 0) {    // a failure test: only this thread completes `done`, later
-                const long long t0 = clock64();
-                while (!mbar_try_wait(&sh.done, 0) && clock64() - t0 < kInjectCycles) {}
-                *fail = 1;
-            }
-            while (!*fail && walk.next(a, s)) {
-                if (!mbar_wait(&sh.q_full, nseg & 1, fail)) break;
-                const int rows = min(a.rows - RB * s.block, RB);
-                const uint32_t idesc_o = idesc | (uint32_t)(128 >> 4) << 24 | (uint32_t)((rows + 15) / 16 * 2) << 17 | 1u << 15;
-                int issued = 0;
-                bool ok = true;
-                for (int j = 0; j < s.n && ok; ++j) {
-                    const long long t0 = clock64();
-                    while (true) {
-                        // the next tile's scores as soon as it has come, these weights' product as soon as they are there
-                        if (issued < s.n && issued <= j + 1 && mbar_test(&sh.full[get.slot], get.phase)) {
-                            tc_fence_after();
-                            const uint64_t kd = umma_desc(ring + get.slot * S::TILE, 16);
-                            const uint32_t d = tmem + 256 + (ns & 1) * TS;
-                            for (int k = 0; k < steps; ++k) {
-                                const uint32_t off = ((k >> 2) * GROUP + (k & 3) * 32) / 16;
-                                umma_ss(d, qd + off, kd + off, idesc_s, k > 0);
-                            }
-                            umma_commit(&sh.s_full[ns & 1]);
-                            ++ns;
-                            ++get;
-                            if (++issued == s.n) umma_commit(&sh.q_free);
-                        }
-                        if (issued > j && mbar_test(&sh.p_full, np & 1)) break;
-                        if (*fail || clock64() - t0 > kSpinCycles) { *fail = 1; ok = false; break; }
-                    }
-                    if (!ok) break;
-                    ++np;
-                    if (j == 0 && nseg > 0 && !mbar_wait(&sh.o_free, (nseg - 1) & 1, fail)) { ok = false; break; }
-                    tc_fence_after();
-                    const uint64_t vd = umma_desc(ring + use.slot * S::TILE, GROUP);
-#pragma unroll 1
-                    for (int c = 0; c < L / 128; ++c)
+        // ---- the MMAs: the warp runs as one
+        constexpr uint32_t fmt = F16 ? 0u : 1u, idesc = (1u << 4) | (fmt << 7) | (fmt << 10);
+        constexpr uint32_t idesc_s = idesc | (uint32_t)(RB >> 4) << 24 | (uint32_t)(TS >> 3) << 17;
+        const uint64_t qd = umma_desc(smem_u32(smem + S::Q), 16), pd = umma_desc(smem_u32(smem + S::P), 16);
+        Ring<S::NS> get, use;                     // the next tile's place for scores, and for values
+        uint32_t ns = 0, np = 0, nseg = 0;
+        const int last_steps = (D - L) / 16;
+        if (a.inject && blockIdx.x == 0) {        // a failure test: only this warp completes `done`, later
+            const long long t0 = clock64();
+            while (!mbar_try_wait(&sh.done, 0) && clock64() - t0 < kInjectCycles) {}
+            *fail = 1;
+            __syncwarp();
+        }
+        // (all steps in one piece of straight code: with a choice of pieces between which the other product has its turn the
+        // offsets reach the instruction by way of ordinary registers, and the issue takes twice as long as the product)
+        auto scores = [&]() {
+            tc_fence_after();
+            const uint64_t kd = umma_desc(ring + get.slot * S::TILE, 16);
+            const uint32_t d = tmem + 256 + (ns & 1) * TS;
 #pragma unroll
-                        for (int k = 0; k < TS / 16; ++k)
-                            umma_ss(tmem + c * RB, vd + (2 * c * GROUP + k * 2048) / 16, pd + k * 32 / 16, idesc_o, j > 0 || k > 0);
-                    umma_commit(&sh.pv_done);
-                    umma_commit(&sh.empty[use.slot]);
-                    ++use;
+            for (int k = 0; k < 4 * G; ++k) {
+                if (k >= L / 16 && k - L / 16 >= last_steps) break;
+                const uint32_t off = ((k >> 2) * GROUP + (k & 3) * 32) / 16;
+                umma_ss_warp(d, qd + off, kd + off, idesc_s, k > 0);
+            }
+            umma_commit_warp(&sh.s_full[ns & 1]);
+            ++ns;
+            ++get;
+        };
+        bool ok = !__any_sync(0xffffffffu, *fail);
+        while (ok && walk.next(a, s)) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&sh.q_full, nseg & 1, fail))) break;
+            const int rows = min(a.rows - RB * s.block, RB);
+            const uint32_t idesc_o = idesc | (uint32_t)(128 >> 4) << 24 | (uint32_t)((rows + 15) / 16 * 2) << 17 | 1u << 15;
+            int issued = 0;
+            for (int j = 0; j < s.n; ++j) {
+                const long long t0 = clock64();
+                while (true) {
+                    // the next tile's scores as soon as it has come, these weights' product as soon as they are there
+                    if (issued < s.n && issued <= j + 1 && __all_sync(0xffffffffu, mbar_test(&sh.full[get.slot], get.phase))) {
+                        scores();
+                        if (++issued == s.n) umma_commit_warp(&sh.q_free);
+                    }
+                    if (issued > j && __all_sync(0xffffffffu, mbar_test(&sh.p_full, np & 1))) break;
+                    if (__any_sync(0xffffffffu, *fail || clock64() - t0 > kSpinCycles)) { *fail = 1; ok = false; break; }
                 }
                 if (!ok) break;
-                ++nseg;
+                ++np;
+                if (j == 0 && nseg > 0 && !__all_sync(0xffffffffu, mbar_wait(&sh.o_free, (nseg - 1) & 1, fail))) { ok = false; break; }
+                tc_fence_after();
+                const uint64_t vd = umma_desc(ring + use.slot * S::TILE, GROUP);
+#pragma unroll
+                for (int c = 0; c < L / 128; ++c)
+#pragma unroll
+                    for (int k = 0; k < TS / 16; ++k)
+                        umma_ss_warp(tmem + c * RB, vd + (2 * c * GROUP + k * 2048) / 16, pd + k * 32 / 16, idesc_o, j > 0 || k > 0);
+                umma_commit_warp(&sh.pv_done);
+                umma_commit_warp(&sh.empty[use.slot]);
+                ++use;
             }
-            // every MMA issued has completed before tensor memory is released
-            umma_commit(&sh.done);
-            const long long t0 = clock64();
-            while (!mbar_try_wait(&sh.done, 0))
-                if (clock64() - t0 > kSpinCycles) { *fail = 1; break; }
+            ++nseg;
         }
+        // every MMA issued has completed before tensor memory is released
+        umma_commit_warp(&sh.done);
+        const long long t0 = clock64();
+        while (!mbar_try_wait(&sh.done, 0))
+            if (clock64() - t0 > kSpinCycles) { *fail = 1; break; }
+        __syncwarp();
     } else if (warp == 5) {
         // ---- tensor copies: a lane per box of (a page's rows) x 64 columns
         const int box = a.box_rows ? a.box_rows : TS, boxes = TS / box, mine = lane % boxes;
@@ -225,9 +231,13 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
                     __syncwarp();
                     if (lane > 0 && lane < NLOAD / 32) mbar_arrive(&sh.full[put.slot]);
                     const int y = held ? (int)((page << a.c.page_shift) + (first & in_page)) : a.c.n_pages << a.c.page_shift;   // past the end: zeros
-                    for (int k = lane; k < boxes * G; k += 32)
-                        tensor_copy(ring + put.slot * S::TILE + k / boxes * GROUP + mine * box * 128, &map, k / boxes * 64, y,
-                                    &sh.full[put.slot]);
+                    const uint32_t dst = ring + put.slot * S::TILE;
+                    for (int i = 0; i < boxes; ++i) {
+                        const int yi = __shfl_sync(0xffffffffu, y, i);
+#pragma unroll
+                        for (int g = 0; g < G; ++g)
+                            tensor_copy_warp(dst + g * GROUP + i * box * 128, &map, g * 64, yi, &sh.full[put.slot]);
+                    }
                     copied |= 1u << put.slot;
                     copied_phase = (copied_phase & ~(1u << put.slot)) | put.phase << put.slot;
                 } else {
@@ -248,22 +258,25 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
             }
     } else if (warp > 5) {
         // ---- queries, and tiles by hand
-        const int lt = tid - 6 * 32;
-        constexpr int CPR = G * 8, ITER = CPR * 64 / NLOAD;   // chunks of a row; of a thread
+        // A warp has every eighth row, its lanes the row's chunks.
+        const int lw = warp - 6;
+        constexpr int CPR = G * 8, LANES = (CPR + 31) / 32, MINE = RB / 8;   // chunks of a row; a lane's; a warp's rows
         Ring<S::NS> put;
         uint32_t nseg = 0, hand = 0;
         bool ok = true;
         while (ok && walk.next(a, s)) {
             if (nseg > 0 && !mbar_wait(&sh.q_free, (nseg - 1) & 1, fail)) break;
-            const int rows = min(a.rows - RB * s.block, RB);
+            const int rows = min(a.rows - RB * s.block, RB);   // (what the others' places hold is of no account)
             const uint32_t q_at = smem_u32(smem + S::Q);
-#pragma unroll 6
-            for (int i = 0; i < ITER; ++i) {
-                const int c = lt + i * NLOAD, r = c / CPR, ch = c - r * CPR;
-                const int rr = RB * s.block + (r < rows ? r : 0), ti = rr / a.heads;
-                const bool there = r < rows && ch * 8 < D;
-                const T *src = (const T *)a.q + s.b * a.qb + ti * a.qt + (rr - ti * a.heads) * a.qh + (there ? ch * 8 : 0);
-                cp_async16(q_at + chunk_at(r, ch), src, there);
+#pragma unroll 2
+            for (int r = lw; r < rows; r += 8) {
+                const int rr = RB * s.block + r, ti = rr / a.heads;
+                const T *src = (const T *)a.q + s.b * a.qb + ti * a.qt + (rr - ti * a.heads) * a.qh;
+#pragma unroll
+                for (int i = 0; i < LANES; ++i) {
+                    const int ch = lane + 32 * i;
+                    if (ch < CPR) cp_async16(q_at + chunk_at(r, ch), src + (ch * 8 < D ? ch * 8 : 0), ch * 8 < D);
+                }
             }
             cp_commit();
             cp_wait<0>();
@@ -273,11 +286,29 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
             const Rows at(a, s);
             for (int j = 0; j < s.n; ++j, ++put) {
                 if (!by_hand(a, s, j)) continue;
-                if (!mbar_wait(&sh.by_hand[hand & 7], hand >> 3 & 1, fail)) { ok = false; break; }
-                ++hand;
                 const uint32_t first = (uint32_t)(s.t0 + j) * TS;
                 const bool draft = first + TS > (uint32_t)s.slots;
-                if (lt < 32) {
+                int64_t row[MINE];
+#pragma unroll
+                for (int k = 0; k < MINE; ++k) {
+                    const uint32_t t = first + lw + 8 * k;
+                    row[k] = t < (uint32_t)s.end ? at.row(t) : -1;
+                }
+                if (!mbar_wait(&sh.by_hand[hand & 7], hand >> 3 & 1, fail)) { ok = false; break; }
+                ++hand;
+                const uint32_t dst = ring + put.slot * S::TILE;
+#pragma unroll
+                for (int k = 0; k < MINE; ++k) {
+                    const T *src = (const T *)a.c.k + (row[k] >= 0 ? row[k] * D : 0);
+#pragma unroll
+                    for (int i = 0; i < LANES; ++i) {
+                        const int ch = lane + 32 * i;
+                        const bool there = row[k] >= 0 && ch * 8 < D;
+                        if (ch < CPR) cp_async16(dst + chunk_at(lw + 8 * k, ch), src + (there ? ch * 8 : 0), there);
+                    }
+                }
+                cp_commit();
+                if (lw == 0) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t t = first + 32 * h + lane;
@@ -286,30 +317,24 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
                         if (lane == 0) { sh.there[put.slot][h] = bits; sh.odd[put.slot][h] = 0; }
                     }
                 }
-                const uint32_t dst = ring + put.slot * S::TILE;
-#pragma unroll 6
-                for (int i = 0; i < ITER; ++i) {
-                    const int c = lt + i * NLOAD, r = c / CPR, ch = c - r * CPR;
-                    const uint32_t t = first + r;
-                    const int64_t row = t < (uint32_t)s.end ? at.row(t) : -1;
-                    const bool there = row >= 0 && ch * 8 < D;
-                    cp_async16(dst + chunk_at(r, ch), (const T *)a.c.k + (there ? row * D + ch * 8 : 0), there);
-                }
-                cp_commit();
                 cp_wait<0>();
                 if (draft) {
                     // drafted elements that are not finite are left out, and their slots marked
                     bar_sync(2, NLOAD);                    // the marks have been cleared
 #pragma unroll 1
-                    for (int i = 0; i < ITER; ++i) {
-                        const int c = lt + i * NLOAD, r = c / CPR, ch = c - r * CPR;
+                    for (int k = 0; k < MINE; ++k) {
+                        const int r = lw + 8 * k;
                         if (first + r < (uint32_t)s.slots || first + r >= (uint32_t)s.end) continue;
-                        uint4 *v = reinterpret_cast<uint4 *>(smem + S::RING + put.slot * S::TILE + chunk_at(r, ch));
-                        uint4 x = *v;
-                        if (zero_odd<T>(x)) {
-                            *v = x;
-                            atomicOr(&sh.odd[put.slot][r >> 5], 1u << (r & 31));
+                        bool odd = false;
+#pragma unroll
+                        for (int i = 0; i < LANES; ++i) {
+                            const int ch = lane + 32 * i;
+                            if (ch >= CPR) continue;
+                            uint4 *v = reinterpret_cast<uint4 *>(smem + S::RING + put.slot * S::TILE + chunk_at(r, ch));
+                            uint4 x = *v;
+                            if (zero_odd<T>(x)) { *v = x; odd = true; }
                         }
+                        if (__any_sync(0xffffffffu, odd) && lane == 0) atomicOr(&sh.odd[put.slot][r >> 5], 1u << (r & 31));
                     }
                 }
                 proxy_fence();
@@ -456,23 +481,28 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
             mbar_wait(&sh.pv_done, npv++ & 1, fail);
             bar_sync(1, 128);
             tc_fence_after();
-            const int dim = 32 * warp + lane;
+            auto store = [&](auto *out) {
+                typedef typename std::remove_pointer<decltype(out)>::type O;
 #pragma unroll 1
-            for (int w = 0; w < L / 128 * RB; w += 32) {
-                const int row = w & (RB - 1);
-                if (row >= rows) continue;
-                float o[32];
-                tmem_ld32(to + w, o);
-                const int n = min(rows - row, 32);
-                const int64_t at = (w / RB) * 128 + dim;
+                for (int w = 0; w < L / 128 * RB; w += 32) {
+                    const int row = w & (RB - 1);
+                    if (row >= rows) continue;
+                    float o[32];
+                    tmem_ld32(to + w, o);
+                    O *dst = out + row * L + (w / RB) * 128;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    if (i >= n) break;
-                    const float by = inverse[row + i], y = by == 0.0f ? 0.0f : o[i] * by;
-                    if (partial) a.part_o[(prow + row + i) * L + at] = y;
-                    else ((T *)a.out)[(orow + row + i) * L + at] = fa_from_f32<T>(y);
+                    for (int i = 0; i < 32; i += 4) {
+                        if (row + i >= rows) break;
+                        const float4 by = *reinterpret_cast<const float4 *>(inverse + row + i);
+                        const float f[4] = {by.x, by.y, by.z, by.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (row + i + e < rows) dst[(i + e) * L] = fa_from_f32<O>(f[e] == 0.0f ? 0.0f : o[i + e] * f[e]);
+                    }
                 }
-            }
+            };
+            if (partial) store(a.part_o + prow * L + 32 * warp + lane);
+            else store((T *)a.out + orow * L + 32 * warp + lane);
             tc_fence_before();
             warp_arrive(&sh.o_free);
             ++nseg;
@@ -572,7 +602,8 @@ __global__ void __launch_bounds__(256) k_latent_join(AttendArgs a, int runs) {
 size_t workspace_bytes(int latent) { return (size_t)MAX_CTAS * 2 * RB * (latent + 1) * sizeof(float) + MAX_CTAS * sizeof(int); }
 
 // The cache's tensor map: rows of its elements, boxes of one page's rows by 64 columns, 128-byte swizzled.  False where
-// it cannot have one (pages of fewer than the eight rows of a swizzle atom).
+// it cannot have one (pages of fewer than the eight rows of a swizzle atom).  (One box of three dimensions for a whole
+// tile takes 3100 clocks to arrive, nine of two dimensions side by side 600 to 1500.)
 bool make_map(const fa_latent_cache *c, int box_rows, CUtensorMap *map) {
     const fa_encode_t encode = fa_tensor_map_encoder();
     const int64_t rows = (int64_t)c->n_pages * c->page_size;
