@@ -8,8 +8,8 @@
 // one at x: accepted if u S_k < p(x), else S_{k+1} = S_k - p(x), with no pass at all.  The next token is found in
 // the sums of the vocabulary's segments (one a warp) and then in its segment.
 //
-// A draw compares u with a sum over the vocabulary, so sums are kept as unevaluated sums of two floats (Knuth's and
-// Dekker's exact additions, 46 bits or more): fp64 runs at two lanes a clock and SM here.
+// A draw compares u with a sum over the vocabulary, so everything is kept as unevaluated sums of two floats (Knuth's and
+// Dekker's exact additions and products, 46 bits or more): fp64 runs at two lanes a clock and SM here.
 //
 // A cluster of blocks takes a sequence: each block a slice of the vocabulary, from node to node.  The first
 // block decides and tells the others, so that they never part ways whatever the inputs hold.
@@ -23,7 +23,15 @@ namespace {
 
 constexpr int NT = 512, WARPS = NT / 32, MAX_CLUSTER = 8;
 
-struct Sum { float h, l; };   // h + l, |l| at most half a unit of h's last place
+// vectors of a thread under way, and the distance from one to the next (the target's and the draft's) in the ring
+template <bool DRAFT> constexpr int RING = DRAFT ? 5 : 8;
+template <bool DRAFT> constexpr int PER = DRAFT ? 2 * NT : NT;
+
+__device__ __forceinline__ void cp_async16(uint4 *to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+}
+
+struct Sum { float h, l; };   // h + l
 
 __device__ __forceinline__ Sum two_sum(float a, float b) {
     const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
@@ -34,33 +42,62 @@ __device__ __forceinline__ Sum fast_two_sum(float a, float b) {   // |a| >= |b|
     return {s, __fsub_rn(b, __fsub_rn(s, a))};
 }
 __device__ __forceinline__ Sum operator+(Sum a, Sum b) {
-    Sum s = two_sum(a.h, b.h);
+    const Sum s = two_sum(a.h, b.h);
     return fast_two_sum(s.h, __fadd_rn(s.l, __fadd_rn(a.l, b.l)));
 }
-__device__ __forceinline__ Sum operator+(Sum a, float b) {
-    Sum s = two_sum(a.h, b);
-    return fast_two_sum(s.h, __fadd_rn(s.l, a.l));
+// a running sum: what each addition loses is added up apart (a few dozen terms lose less than 2^-46 of the sum)
+__device__ __forceinline__ void add(Sum &a, float b) {
+    const Sum s = two_sum(a.h, b);
+    a.h = s.h;
+    a.l = __fadd_rn(a.l, s.l);
 }
-__device__ __forceinline__ double value(Sum a) { return (double)a.h + (double)a.l; }
-__device__ __forceinline__ Sum split(double x) {
-    const float h = (float)x;
-    return {h, (float)(x - (double)h)};
+__device__ __forceinline__ void add(Sum &a, Sum b) {
+    const Sum s = two_sum(a.h, b.h);
+    a.h = s.h;
+    a.l = __fadd_rn(a.l, __fadd_rn(s.l, b.l));
+}
+__device__ __forceinline__ Sum operator*(Sum a, float b) {
+    const float h = __fmul_rn(a.h, b);
+    return fast_two_sum(h, __fmaf_rn(a.l, b, __fmaf_rn(a.h, b, -h)));
+}
+__device__ __forceinline__ Sum operator-(Sum a) { return {-a.h, -a.l}; }
+__device__ __forceinline__ bool operator<(Sum a, Sum b) { return (a + -b).h < 0.0f; }
+// a / b: two quotients and what they leave over
+__device__ __forceinline__ Sum operator/(Sum a, Sum b) {
+    const float q0 = __fdiv_rn(a.h, b.h);
+    const Sum r = a + -(b * q0);
+    const float q1 = __fdiv_rn(r.h, b.h);
+    const Sum t = r + -(b * q1);
+    return fast_two_sum(q0, __fadd_rn(q1, __fdiv_rn(t.h, b.h)));
+}
+__device__ __forceinline__ Sum shfl_xor(Sum a, int o) {
+    return {__shfl_xor_sync(0xffffffffu, a.h, o), __shfl_xor_sync(0xffffffffu, a.l, o)};
 }
 __device__ __forceinline__ Sum warp_sum(Sum a) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1)
-        a = a + Sum{__shfl_xor_sync(0xffffffffu, a.h, o), __shfl_xor_sync(0xffffffffu, a.l, o)};
+    for (int o = 16; o; o >>= 1) a = a + shfl_xor(a, o);
+    return a;
+}
+// inclusive sums over the lanes
+__device__ __forceinline__ Sum warp_scan(Sum a) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const Sum up = {__shfl_up_sync(0xffffffffu, a.h, o), __shfl_up_sync(0xffffffffu, a.l, o)};
+        if ((threadIdx.x & 31) >= o) a = up + a;
+    }
     return a;
 }
 
-// max(p - l q, 0)
+// max(p - l q, 0) as two floats
 __device__ __forceinline__ Sum left(float p, float q, Sum l) {
     const float h = __fmul_rn(l.h, q), e = __fmaf_rn(l.l, q, __fmaf_rn(l.h, q, -h));
-    const Sum d = two_sum(p, -h), r = fast_two_sum(d.h, __fsub_rn(d.l, e));
+    const Sum d = two_sum(p, -h);
+    const Sum r = fast_two_sum(d.h, __fsub_rn(d.l, e));
     return r.h > 0.0f ? r : Sum{0.0f, 0.0f};
 }
 
-__device__ __forceinline__ float weight(float x) { return x > 0.0f && x < INFINITY ? x : 0.0f; }
+// x where it is a positive finite number, else 0
+__device__ __forceinline__ float weight(float x) { return __float_as_uint(x) - 1u < 0x7f7fffffu ? x : 0.0f; }
 
 struct VerifyArgs {
     int B, T, V, S, words;
@@ -75,19 +112,16 @@ struct VerifyArgs {
 };
 
 struct Plan {          // what the first block tells the others
-    int action;        // draw from the segment sums, go to `node` with `state`, or sweep again with l
-    int node, state, owner;
-    Sum l;
-    double before;     // the sum before the owner's slice, and what the draw looks for
-    double goal;
+    int action;        // draw from segment `segment`, go to `node` with `state`, or sweep again with l
+    int node, state, segment, tried;
+    Sum l, before, goal;   // the sum before the segment, and what the draw looks for
 };
 enum { DRAW = 0, NODE = 1, SWEEP = 2 };
 
 struct Shared {
     Plan plan;
-    Sum seg[WARPS], seg_q[WARPS];                       // this block's segments
-    Sum part[MAX_CLUSTER], part_q[MAX_CLUSTER];         // (first block) every block's slice
-    int picked;
+    Sum seg[MAX_CLUSTER * WARPS], seg_q[MAX_CLUSTER * WARPS];   // (first block) the sums of all segments
+    Sum row[WARPS];                                             // (the draw) of the rows of one segment
 };
 
 // A row of the vocabulary in vectors of 16 bytes, counted from the aligned address at or before its start.
@@ -96,15 +130,12 @@ template <class T> struct Row {
     const T *p;
     int V;
     // elements i .. i + N - 1, zero outside the row
-    __device__ __forceinline__ void load(int i, float (&f)[N]) const {
-        if (i >= 0 && i <= V - N && !((uintptr_t)(p + i) & 15)) {
-            fa_unpack(__ldg(reinterpret_cast<const uint4 *>(p + i)), f, T());
-        } else {
+    __device__ __forceinline__ uint4 load(int i) const {
+        if (i >= 0 && i <= V - N && !((uintptr_t)(p + i) & 15)) return __ldg(reinterpret_cast<const uint4 *>(p + i));
+        float f[N];
 #pragma unroll
-            for (int e = 0; e < N; ++e) f[e] = i + e >= 0 && i + e < V ? fa_to_f32(p[i + e]) : 0.0f;
-        }
-#pragma unroll
-        for (int e = 0; e < N; ++e) f[e] = weight(f[e]);
+        for (int e = 0; e < N; ++e) f[e] = i + e >= 0 && i + e < V ? fa_to_f32(p[i + e]) : 0.0f;
+        return fa_pack(f, T());
     }
 };
 
@@ -112,15 +143,86 @@ template <class T> struct Row {
 __device__ __forceinline__ uint32_t bits_at(const uint32_t *live, int words, int i) {
     if (i < 0) return __ldg(live) << -i;                // -8 < i
     const int w = i >> 5;
-    const uint32_t lo = __ldg(live + w), hi = w + 1 < words ? __ldg(live + w + 1) : 0u;
-    return __funnelshift_r(lo, hi, i & 31);
+    const uint32_t lo = __ldg(live + w);
+    if (!(i & 7)) return lo >> (i & 31);
+    return __funnelshift_r(lo, w + 1 < words ? __ldg(live + w + 1) : 0u, i & 31);
 }
 
+// What a block knows of the current node.
+template <class T, bool DRAFT> struct Node {
+    static constexpr int N = fa_vec<T>::N;
+    Row<T> p, q;
+    const uint32_t *live;
+    int words, lead, chunks, per;                        // of the row: first element's place, vectors, vectors of a segment
+    Sum lam;
+    __device__ __forceinline__ uint32_t bits(int c) const { return live ? bits_at(live, words, c * N - lead) : 0xffffffffu; }
+    __device__ __forceinline__ int segment(int x) const { return (x + lead) / N / per; }
+    // vector c of the rows to the thread's place of the ring: an asynchronous copy where it is aligned
+    __device__ __forceinline__ void fetch(uint4 *to, int c) const {
+        const int i = c * N - lead;
+        const bool inside = i >= 0 && i <= V() - N;
+        if (inside) cp_async16(to, p.p + i);             // (p's vectors are aligned by their count)
+        else *to = p.load(i);
+        if (DRAFT) {
+            if (inside && !((uintptr_t)(q.p + i) & 15)) cp_async16(to + NT, q.p + i);
+            else to[NT] = q.load(i);
+        }
+    }
+    __device__ __forceinline__ int V() const { return p.V; }
+    // The sums of vectors c0 + lane, c0 + lane + 32, ... below c1; FRESH: l = 0, and the draft's sum too.  The vectors
+    // come through a ring in shared memory, which keeps more of them under way than registers would; a thread
+    // reads what it has copied itself.
+    template <bool FRESH> __device__ __forceinline__ void sweep(uint4 *ring, int c0, int c1, Sum &w, Sum &wq) const {
+        ring += threadIdx.x;
+        int put = c0 + (threadIdx.x & 31);
+#pragma unroll
+        for (int k = 0; k < RING<DRAFT>; ++k, put += 32) {
+            if (put < c1) fetch(ring + k * PER<DRAFT>, put);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+        int k = 0;
+        for (int c = c0 + (threadIdx.x & 31); c < c1; c += 32, put += 32) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(RING<DRAFT> - 1) : "memory");
+            uint4 *at = ring + k * PER<DRAFT>;
+            const uint4 x = *at, y = DRAFT ? at[NT] : x;
+            const uint32_t b = live ? bits(c) : 0xffffffffu;
+            float f[N], g[N];
+            fa_unpack(x, f, T());
+            if (DRAFT) fa_unpack(y, g, T());
+            // all of them nonnegative and finite, and allowed: the common case
+            uint32_t most = 0;
+#pragma unroll
+            for (int e = 0; e < N; ++e) most = max(most, max(__float_as_uint(f[e]), DRAFT ? __float_as_uint(g[e]) : 0u));
+            if (most >= 0x7f800000u || (b & ((1u << N) - 1)) != (1u << N) - 1) {
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    const bool in = b >> e & 1;
+                    f[e] = in ? weight(f[e]) : 0.0f;
+                    if (DRAFT) g[e] = in ? weight(g[e]) : 0.0f;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                if (DRAFT && !FRESH) {
+                    add(w, left(f[e], g[e], lam));
+                } else {
+                    add(w, f[e]);
+                    if (DRAFT) add(wq, g[e]);
+                }
+            }
+            if (put < c1) fetch(at, put);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            if (++k == RING<DRAFT>) k = 0;
+        }
+    }
+};
+
 template <class T, bool DRAFT>
-__global__ void __launch_bounds__(NT) k_verify(VerifyArgs a) {
+__global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
     constexpr int N = fa_vec<T>::N;
     __shared__ Shared sh;
-    extern __shared__ int dyn[];
+    extern __shared__ uint4 ring[];
+    int *dyn = reinterpret_cast<int *>(ring + RING<DRAFT> * PER<DRAFT>);
     int *parent = dyn, *tok = dyn + a.T, *path = dyn + 2 * a.T, *after = dyn + 3 * a.T, *tried = dyn + 4 * a.T;
     float *us = (float *)(dyn + 5 * a.T), *px = us + a.T, *qx = px + a.T;
     const cg::cluster_group cluster = cg::this_cluster();
@@ -128,282 +230,275 @@ __global__ void __launch_bounds__(NT) k_verify(VerifyArgs a) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     Shared *first = cluster.map_shared_rank(&sh, 0);
     const int use = a.count ? min(max(a.count[b], 0), a.T) : a.T;
-    for (int j = tid; j < a.T; j += NT) {
-        parent[j] = a.parents[(int64_t)b * a.T + j];
-        tok[j] = a.tokens[(int64_t)b * a.T + j];
-        us[j] = a.u[(int64_t)b * a.T + j];
-    }
-    // kept by the first block's first thread
-    int j = 1, kept = 0, n_tried = 0;
-    double l = 0.0, old_l = 0.0;
+    if (rank == 0)
+        for (int j = tid; j < a.T; j += NT) {
+            parent[j] = a.parents[(int64_t)b * a.T + j];
+            tok[j] = a.tokens[(int64_t)b * a.T + j];
+            us[j] = a.u[(int64_t)b * a.T + j];
+            path[j] = 0;
+        }
+    // kept by the first block's first lane
+    int j = 1, kept = use > 0 ? 1 : 0, n_tried = 0;
+    Sum l = {0.0f, 0.0f}, old_l = l;
     bool again = false;                                  // this sweep only restores the sums of old_l
     bool probing = false;                                // this sweep is a rejection's
-    Sum total = {0.0f, 0.0f}, total_q = {0.0f, 0.0f};
+    Sum total_q = {0.0f, 0.0f};
     int node = 0, state = a.S ? a.states[b] : 0;
-    Sum lam = {0.0f, 0.0f};
     bool fresh = true;
-    const int known = a.S;                               // states
-    if (tid == 0 && use > 0) path[0] = 0;
-    kept = use > 0 ? 1 : 0;
+    Node<T, DRAFT> at;
+    at.words = a.words;
     __syncthreads();
     while (true) {
         // (nothing that a block reads for itself decides how often the cluster meets)
-        const bool any = use > 0 && (!known || (unsigned)state < (unsigned)known);
-        const T *p = (const T *)a.target + b * a.tb + node * a.tr, *q = DRAFT ? (const T *)a.draft + b * a.db + node * a.dr : nullptr;
-        const int lead = (int)(((uintptr_t)p / sizeof(T)) % N);
-        const int chunks = (int)(((int64_t)a.V + lead + N - 1) / N);
-        const int per = (chunks + C * NT - 1) / (C * NT) * 32;               // chunks of a segment
-        const uint32_t *live = known && any ? a.live + (int64_t)state * a.words : nullptr;
-        if (rank == 0 && fresh) {
-            // what the tests of this node's children need
-            for (int i = tid; i < use; i += NT) {
-                if (parent[i] != node || i <= node) continue;
-                const int x = tok[i];
-                px[i] = qx[i] = 0.0f;
-                after[i] = -1;
-                if ((unsigned)x >= (unsigned)a.V || !any) continue;
-                const int to = known ? a.next[(int64_t)state * a.V + x] : 0;
-                after[i] = to;
-                if (to < 0) continue;
-                px[i] = weight(fa_to_f32(p[x]));
-                if (DRAFT) qx[i] = weight(fa_to_f32(q[x]));
+        const bool any = use > 0 && (!a.S || (unsigned)state < (unsigned)a.S);
+        if (fresh) {
+            at.p = {(const T *)a.target + b * a.tb + node * a.tr, a.V};
+            at.q = {DRAFT ? (const T *)a.draft + b * a.db + node * a.dr : nullptr, a.V};
+            at.live = a.S && any ? a.live + (int64_t)state * a.words : nullptr;
+            at.lead = (int)(((uintptr_t)at.p.p / sizeof(T)) % N);
+            at.chunks = (int)(((int64_t)a.V + at.lead + N - 1) / N);
+            at.per = (at.chunks + C * NT - 1) / (C * NT) * 32;
+            at.lam = {0.0f, 0.0f};
+            if (rank == 0) {
+                // what the tests of this node's children need
+                for (int i = node + 1 + tid; i < use; i += NT) {
+                    if (parent[i] != node) continue;
+                    const int x = tok[i];
+                    px[i] = qx[i] = 0.0f;
+                    after[i] = -1;
+                    if ((unsigned)x >= (unsigned)a.V || !any) continue;
+                    const int to = a.S ? a.next[(int64_t)state * a.V + x] : 0;
+                    after[i] = to;
+                    if (to < 0) continue;
+                    px[i] = weight(fa_to_f32(at.p.p[x]));
+                    if (DRAFT) qx[i] = weight(fa_to_f32(at.q.p[x]));
+                }
             }
         }
         // ---- this warp's segment
-        const int s0 = (rank * WARPS + warp) * per, s1 = min(s0 + per, chunks);
-        const Row<T> rp{p, a.V}, rq{q, a.V};
+        const int mine = rank * WARPS + warp, s0 = mine * at.per, s1 = min(s0 + at.per, at.chunks);
         Sum w = {0.0f, 0.0f}, wq = {0.0f, 0.0f};
-        constexpr int U = 4;
-        if (any)
-            for (int c = s0 + lane; c < s1; c += 32 * U) {
-                float f[U][N], g[U][N];
-                uint32_t bits[U];
-#pragma unroll
-                for (int k = 0; k < U; ++k) {
-                    const int i = (c + 32 * k) * N - lead;
-                    bits[k] = 0;
-                    if (c + 32 * k >= s1) continue;
-                    bits[k] = live ? bits_at(live, a.words, i) : 0xffffffffu;
-                    rp.load(i, f[k]);
-                    if (DRAFT) rq.load(i, g[k]);
-                }
-#pragma unroll
-                for (int k = 0; k < U; ++k)
-#pragma unroll
-                    for (int e = 0; e < N; ++e) {
-                        if (!(bits[k] >> e & 1)) continue;
+        if (any) {
+            if (fresh || !DRAFT) at.template sweep<true>(ring, s0, s1, w, wq);
+            else at.template sweep<false>(ring, s0, s1, w, wq);
+        }
+        w = warp_sum(fast_two_sum(w.h, w.l));
+        if (DRAFT && fresh) wq = warp_sum(fast_two_sum(wq.h, wq.l));
+        if (lane == 0) {
+            first->seg[mine] = w;
+            if (DRAFT && fresh) first->seg_q[mine] = wq;
+        }
+        cluster.sync();
+        if (rank == 0 && warp == 0) {
+            const int each = (C * WARPS + 31) / 32;       // segments of a lane
+            Sum total = {0.0f, 0.0f}, t = {0.0f, 0.0f};
+            for (int i = lane * each; i < min((lane + 1) * each, C * WARPS); ++i) {
+                total = total + sh.seg[i];
+                if (DRAFT && fresh) t = t + sh.seg_q[i];
+            }
+            total = warp_sum(total);
+            if (fresh) {
+                n_tried = 0;
+                l = {0.0f, 0.0f};
+                if (DRAFT) total_q = warp_sum(t);
+            }
+            Plan plan = {};
+            const bool some = total.h > 0.0f && total.h < INFINITY;
+            if (lane == 0) {
+                if (probing && !again && !(total.h > 0.0f)) {
+                    // nothing would be left: the distribution stays as it was
+                    l = old_l;
+                    plan.action = SWEEP;
+                    plan.l = l;
+                    again = true;
+                } else {
+                    again = probing = false;
+                    if (!some) j = use;                              // nothing can be accepted
+                    const bool drafts = DRAFT && total_q.h > 0.0f;   // a row without weight: q(x) = 0
+                    Sum ratio = {0.0f, 0.0f};
+                    if (drafts && j < use) ratio = total / total_q;
+                    for (; j < use; ++j) {
+                        if (parent[j] != node || (unsigned)tok[j] >= (unsigned)a.V) continue;
+                        const float u = us[j], x = px[j];
+                        bool take, known = false;
                         if (DRAFT) {
-                            wq = wq + g[k][e];
-                            w = w + left(f[k][e], g[k][e], lam);
+                            take = ratio * qx[j] * u < left(x, qx[j], l);
                         } else {
-                            w = w + f[k][e];
+                            for (int i = 0; i < n_tried; ++i) known |= tried[i] == tok[j];
+                            take = !known && total * u < Sum{x, 0.0f};
                         }
+                        if (take) {
+                            plan.action = NODE;
+                            plan.node = j;
+                            plan.state = after[j];
+                            path[kept++] = j;
+                            ++j;
+                            break;
+                        }
+                        if (DRAFT) {
+                            if (!drafts) continue;
+                            old_l = l;
+                            l = l + ratio;
+                            plan.action = SWEEP;
+                            plan.l = l;
+                            probing = true;
+                            ++j;
+                            break;
+                        }
+                        if (known || x == 0.0f) continue;
+                        const Sum rest = total + Sum{-x, 0.0f};
+                        if (!(rest.h > 0.0f)) continue;
+                        total = rest;
+                        Sum &from = sh.seg[at.segment(tok[j])];
+                        from = from + Sum{-x, 0.0f};
+                        tried[n_tried++] = tok[j];
                     }
+                    plan.goal = total * us[0];
+                }
             }
-        w = warp_sum(w);
-        if (DRAFT) wq = warp_sum(wq);
-        if (lane == 0) { sh.seg[warp] = w; if (DRAFT) sh.seg_q[warp] = wq; }
-        __syncthreads();
-        if (tid == 0) {
-            Sum s = {0.0f, 0.0f}, t = {0.0f, 0.0f};
-            for (int i = 0; i < WARPS; ++i) { s = s + sh.seg[i]; if (DRAFT) t = t + sh.seg_q[i]; }
-            first->part[rank] = s;
-            first->part_q[rank] = t;
+            plan.action = __shfl_sync(0xffffffffu, plan.action, 0);
+            if (plan.action == DRAW) {
+                // the segment that holds the draw
+                const Sum goal = {__shfl_sync(0xffffffffu, plan.goal.h, 0), __shfl_sync(0xffffffffu, plan.goal.l, 0)};
+                const int i0 = lane * each, i1 = min(i0 + each, C * WARPS);
+                Sum here = {0.0f, 0.0f};
+                bool weighs = false;
+                for (int i = i0; i < i1; ++i) {
+                    here = here + sh.seg[i];
+                    weighs |= sh.seg[i].h > 0.0f;
+                }
+                const Sum upto = warp_scan(here);
+                const Sum start = {__shfl_up_sync(0xffffffffu, upto.h, 1), __shfl_up_sync(0xffffffffu, upto.l, 1)};
+                const uint32_t past = __ballot_sync(0xffffffffu, weighs && goal < upto), all = __ballot_sync(0xffffffffu, weighs);
+                const int who = past ? __ffs(past) - 1 : all ? 31 - __clz(all) : 0;
+                plan.segment = -1;
+                if (lane == who && all && some) {
+                    Sum before = lane ? start : Sum{0.0f, 0.0f};
+                    for (int i = i0; i < i1; ++i) {
+                        if (!(sh.seg[i].h > 0.0f)) continue;
+                        const Sum next = before + sh.seg[i];
+                        plan.segment = i;                 // the last one if rounding hides all others
+                        plan.before = before;
+                        if (goal < next) break;
+                        before = next;
+                    }
+                }
+                plan.segment = __shfl_sync(0xffffffffu, plan.segment, who);
+                plan.before = {__shfl_sync(0xffffffffu, plan.before.h, who), __shfl_sync(0xffffffffu, plan.before.l, who)};
+                plan.goal = goal;
+            }
+            plan.node = __shfl_sync(0xffffffffu, plan.node, 0);
+            plan.state = __shfl_sync(0xffffffffu, plan.state, 0);
+            plan.l.h = __shfl_sync(0xffffffffu, plan.l.h, 0);
+            plan.l.l = __shfl_sync(0xffffffffu, plan.l.l, 0);
+            plan.tried = __shfl_sync(0xffffffffu, n_tried, 0);
+            if (lane < C) cluster.map_shared_rank(&sh, lane)->plan = plan;
         }
         cluster.sync();
-        if (rank == 0 && tid == 0) {
-            Sum s = {0.0f, 0.0f}, t = {0.0f, 0.0f};
-            for (int i = 0; i < C; ++i) { s = s + sh.part[i]; t = t + sh.part_q[i]; }
-            if (fresh) { n_tried = 0; l = 0.0; total_q = t; }
-            Plan plan;
-            plan.action = DRAW;
-            bool restore = false;
-            if (probing && !again && !(value(s) > 0.0)) { restore = true; l = old_l; }
-            total = s;
-            if (restore) {
-                plan.action = SWEEP;
-                plan.l = split(l);
-                again = true;
-            } else {
-                again = probing = false;
-                double S = value(total);
-                const double Q = DRAFT ? value(total_q) : 1.0;
-                if (!(S > 0.0 && S < INFINITY)) j = use;         // nothing can be accepted
-                for (; j < use; ++j) {
-                    if (parent[j] != node || (unsigned)tok[j] >= (unsigned)a.V) continue;
-                    const double u = us[j], x = px[j];
-                    bool take, known_token = false;
-                    if (DRAFT) {
-                        const double y = qx[j], r = x - l * y;
-                        take = u * S * y < (r > 0.0 ? r : 0.0) * (Q > 0.0 ? Q : 1.0);   // a row without weight: q(x) = 0
-                    } else {
-                        for (int i = 0; i < n_tried; ++i) known_token |= tried[i] == tok[j];
-                        take = !known_token && u * S < x;
-                    }
-                    if (take) {
-                        plan.action = NODE;
-                        plan.node = j;
-                        plan.state = after[j];
-                        path[kept++] = j;
-                        ++j;
-                        break;
-                    }
-                    if (DRAFT) {
-                        if (!(Q > 0.0)) continue;
-                        old_l = l;
-                        l += S / Q;
-                        plan.action = SWEEP;
-                        plan.l = split(l);
-                        probing = true;
-                        ++j;
-                        break;
-                    }
-                    if (known_token || x == 0.0) continue;
-                    const Sum rest = total + (float)-x;
-                    if (!(value(rest) > 0.0)) continue;
-                    total = rest;
-                    S = value(total);
-                    tried[n_tried++] = tok[j];
-                }
-                if (plan.action == DRAW) {
-                    // the slice that holds the draw: without what was tried
-                    plan.goal = (double)us[0] * S;
-                    plan.owner = -1;
-                    plan.before = 0.0;
-                    int last = -1;
-                    double last_before = 0.0;
-                    if (S > 0.0 && S < INFINITY)
-                        for (int c = 0; c < C; ++c) {
-                            Sum here = sh.part[c];
-                            if (!DRAFT)
-                                for (int i = 0; i < n_tried; ++i)
-                                    if ((tried[i] + lead) / N / per / WARPS == c) here = here + -weight(fa_to_f32(p[tried[i]]));
-                            const double v = value(here);
-                            if (!(v > 0.0)) continue;
-                            last = c;
-                            last_before = plan.before;
-                            if (plan.goal < plan.before + v) { plan.owner = c; break; }
-                            plan.before += v;
-                        }
-                    if (plan.owner < 0) { plan.owner = last; plan.before = last_before; }
-                    plan.node = n_tried;
-                }
-            }
-            for (int c = 0; c < C; ++c) cluster.map_shared_rank(&sh, c)->plan = plan;
-        }
-        cluster.sync();
-        const Plan plan = sh.plan;
-        fresh = plan.action == NODE;
-        if (plan.action == NODE) {
-            node = plan.node;
-            state = plan.state;
-            lam = {0.0f, 0.0f};
+        const int action = sh.plan.action;
+        fresh = action == NODE;
+        if (action == NODE) {
+            node = sh.plan.node;
+            state = sh.plan.state;
             continue;
         }
-        if (plan.action == SWEEP) {
-            lam = plan.l;
+        if (action == SWEEP) {
+            at.lam = sh.plan.l;
             continue;
-        }
-        // ---- the draw
-        if (plan.owner < 0) {
-            if (rank == 0 && tid == 0) {
-                a.token[b] = -1;
-                if (a.state) a.state[b] = -1;
-            }
-        } else {
-            const int *list = tried;
-            if (!DRAFT && plan.owner != 0 && rank == plan.owner) {
-                const int *theirs = cluster.map_shared_rank(tried, 0);
-                for (int i = tid; i < plan.node; i += NT) tried[i] = theirs[i];
-                __syncthreads();
-            }
-            if (rank == plan.owner && warp == 0) {
-                const int n = DRAFT ? 0 : plan.node;
-                int pick = -1, last = -1;
-                double before = plan.before, last_before = 0.0;
-                if (lane == 0) {
-                    for (int k = 0; k < WARPS; ++k) {
-                        Sum here = sh.seg[k];
-                        for (int i = 0; i < n; ++i)
-                            if ((list[i] + lead) / N / per == rank * WARPS + k) here = here + -weight(fa_to_f32(p[list[i]]));
-                        const double v = value(here);
-                        if (!(v > 0.0)) continue;
-                        last = k;
-                        last_before = before;
-                        if (plan.goal < before + v) { pick = k; break; }
-                        before += v;
-                    }
-                    if (pick < 0) { pick = last; before = last_before; }
-                }
-                pick = __shfl_sync(0xffffffffu, pick, 0);
-                before = __shfl_sync(0xffffffffu, before, 0);
-                int found = -1, best = -1;                // best: the last element with a weight
-                if (pick >= 0) {
-                    const int c0 = (rank * WARPS + pick) * per, c1 = min(c0 + per, chunks);
-                    for (int c = c0; c < c1 && found < 0; c += 32) {
-                        const int i = (c + lane) * N - lead;
-                        float f[N], g[N];
-                        Sum x[N], sum = {0.0f, 0.0f};
-                        const uint32_t bits = c + lane < c1 ? live ? bits_at(live, a.words, i) : 0xffffffffu : 0u;
-                        if (c + lane < c1) {
-                            rp.load(i, f);
-                            if (DRAFT) rq.load(i, g);
-                        }
-#pragma unroll
-                        for (int e = 0; e < N; ++e) {
-                            x[e] = {0.0f, 0.0f};
-                            if (!(bits >> e & 1)) continue;
-                            bool out = false;
-                            for (int k = 0; k < n; ++k) out |= list[k] == i + e;
-                            if (out) continue;
-                            if (DRAFT) x[e] = left(f[e], g[e], lam);
-                            else x[e] = {f[e], 0.0f};
-                            if (x[e].h > 0.0f) best = i + e;
-                            sum = sum + x[e];
-                        }
-                        Sum upto = sum;
-#pragma unroll
-                        for (int o = 1; o < 32; o <<= 1) {
-                            const Sum up = {__shfl_up_sync(0xffffffffu, upto.h, o), __shfl_up_sync(0xffffffffu, upto.l, o)};
-                            if (lane >= o) upto = up + upto;
-                        }
-                        const double end = before + value(upto);
-                        const uint32_t past = __ballot_sync(0xffffffffu, end > plan.goal && sum.h > 0.0f);
-                        if (past) {
-                            const int who = __ffs(past) - 1;
-                            // the lanes before
-                            const Sum start = {__shfl_up_sync(0xffffffffu, upto.h, 1), __shfl_up_sync(0xffffffffu, upto.l, 1)};
-                            if (lane == who) {
-                                Sum at = lane ? start : Sum{0.0f, 0.0f};
-                                int mine = -1, some = -1;
-#pragma unroll
-                                for (int e = 0; e < N; ++e) {
-                                    at = at + x[e];
-                                    if (!(x[e].h > 0.0f)) continue;
-                                    some = i + e;
-                                    if (mine < 0 && before + value(at) > plan.goal) mine = i + e;
-                                }
-                                found = mine >= 0 ? mine : some;
-                            }
-                            found = __shfl_sync(0xffffffffu, found, who);
-                        }
-                        before = __shfl_sync(0xffffffffu, end, 31);
-                    }
-                    if (found < 0) found = __reduce_max_sync(0xffffffffu, best);
-                }
-                if (lane == 0) {
-                    a.token[b] = found;
-                    if (a.state) a.state[b] = found >= 0 ? a.next[(int64_t)state * a.V + found] : -1;
-                }
-            }
         }
         break;
     }
-    __syncthreads();
+    // ---- the draw: the block that has the segment takes it row by row of 32 vectors, a warp a row
+    const int segment = sh.plan.segment;
+    if (segment < 0) {
+        if (rank == 0 && tid == 0) {
+            a.token[b] = -1;
+            if (a.state) a.state[b] = -1;
+        }
+    } else if (rank == segment / WARPS) {
+        const int n = DRAFT ? 0 : sh.plan.tried, c0 = segment * at.per, c1 = min(c0 + at.per, at.chunks);
+        const Sum goal = sh.plan.goal;
+        if (!DRAFT && rank != 0) {
+            const int *theirs = cluster.map_shared_rank(tried, 0);
+            for (int i = tid; i < n; i += NT) tried[i] = theirs[i];
+            __syncthreads();
+        }
+        Sum before = sh.plan.before;
+        int last = -1;                                    // the last element with a weight so far
+        for (int r0 = c0; r0 < c1; r0 += NT) {
+            const int c = r0 + tid, i = c * N - at.lead;
+            float f[N], g[N];
+            uint32_t bits = 0;
+            uint4 x = make_uint4(0, 0, 0, 0), y = x;
+            if (c < c1) {
+                x = at.p.load(i);
+                if (DRAFT) y = at.q.load(i);
+                bits = at.bits(c);
+            }
+            fa_unpack(x, f, T());
+            if (DRAFT) fa_unpack(y, g, T());
+            Sum sum = {0.0f, 0.0f};
+            int best = -1;
+            uint32_t in = 0;
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                bool out = !(bits >> e & 1);
+                for (int k = 0; k < n; ++k) out |= tried[k] == i + e;
+                const float pe = out ? 0.0f : weight(f[e]), qe = DRAFT ? weight(g[e]) : 0.0f;
+                const Sum v = DRAFT ? left(pe, qe, at.lam) : Sum{pe, 0.0f};
+                if (v.h > 0.0f) { best = i + e; in |= 1u << e; }
+                add(sum, v);
+            }
+            const Sum upto = warp_scan(fast_two_sum(sum.h, sum.l));
+            if (lane == 31) sh.row[warp] = upto;
+            __syncthreads();
+            // the rows' sums in the lanes; the warp whose row holds the draw
+            const Sum mine = lane < WARPS ? sh.row[lane] : Sum{0.0f, 0.0f}, rows = warp_scan(lane ? mine : before + mine);
+            const uint32_t holds = __ballot_sync(0xffffffffu, mine.h > 0.0f && goal < rows);
+            const int who = holds ? __ffs(holds) - 1 : -1, prior = max(who - 1, 0);
+            Sum start = {__shfl_sync(0xffffffffu, rows.h, prior), __shfl_sync(0xffffffffu, rows.l, prior)};
+            if (who <= 0) start = before;
+            const Sum end = {__shfl_sync(0xffffffffu, rows.h, 31), __shfl_sync(0xffffffffu, rows.l, 31)};
+            if (warp == who) {
+                const Sum lanes = {__shfl_up_sync(0xffffffffu, upto.h, 1), __shfl_up_sync(0xffffffffu, upto.l, 1)};
+                const uint32_t past = __ballot_sync(0xffffffffu, in && goal < start + upto), some = __ballot_sync(0xffffffffu, in != 0);
+                const int pick = past ? __ffs(past) - 1 : 31 - __clz(some);
+                if (lane == pick) {
+                    Sum run = lane ? start + lanes : start;   // of the lanes before, then through the elements
+                    int found = best;
+                    bool done = false;
+#pragma unroll
+                    for (int e = 0; e < N; ++e) {
+                        if (!(in >> e & 1) || done) continue;
+                        const float pe = weight(f[e]), qe = DRAFT ? weight(g[e]) : 0.0f;
+                        const Sum v = DRAFT ? left(pe, qe, at.lam) : Sum{pe, 0.0f};
+                        run = run + fast_two_sum(v.h, v.l);
+                        if (goal < run) { found = i + e; done = true; }
+                    }
+                    a.token[b] = found;
+                    if (a.state) a.state[b] = a.next[(int64_t)state * a.V + found];
+                }
+            }
+            if (who >= 0) { last = -1; break; }
+            best = __reduce_max_sync(0xffffffffu, best);
+            __syncthreads();                              // the rows' sums have been read
+            if (lane == 0) sh.row[warp].h = __int_as_float(best);
+            __syncthreads();
+            for (int k = 0; k < WARPS; ++k) last = max(last, __float_as_int(sh.row[k].h));
+            __syncthreads();
+            before = end;
+        }
+        if (last >= 0 && tid == 0) {                      // rounding hid the draw: the last element with a weight
+            a.token[b] = last;
+            if (a.state) a.state[b] = a.next[(int64_t)state * a.V + last];
+        }
+    }
     if (rank == 0) {
-        if (tid == 0) { sh.picked = kept; a.kept[b] = kept; }
+        __syncthreads();                                  // the rows' sums have been read
+        if (tid == 0) { sh.row[0].h = __int_as_float(kept); a.kept[b] = kept; }
         __syncthreads();
-        for (int i = tid; i < a.T; i += NT) a.path[(int64_t)b * a.T + i] = i < sh.picked ? path[i] : -1;
+        const int n = __float_as_int(sh.row[0].h);
+        for (int i = tid; i < a.T; i += NT) a.path[(int64_t)b * a.T + i] = i < n ? path[i] : -1;
     }
     cluster.sync();                                       // no block leaves while another reads its list
 }
@@ -416,11 +511,12 @@ template <class T, bool DRAFT> void launch(const VerifyArgs &a, int cluster, cud
     cudaLaunchConfig_t c = {};
     c.gridDim = dim3((unsigned)a.B * cluster);
     c.blockDim = dim3(NT);
-    c.dynamicSmemBytes = (size_t)a.T * 8 * sizeof(int);
+    c.dynamicSmemBytes = sizeof(uint4) * RING<DRAFT> * PER<DRAFT> + (size_t)a.T * 8 * sizeof(int);
     c.stream = s;
     c.attrs = at;
     c.numAttrs = 1;
-    (void)cudaLaunchKernelEx(&c, k_verify<T, DRAFT>, a);   // its error is the one the check reads
+    if (cudaFuncSetAttribute(k_verify<T, DRAFT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)c.dynamicSmemBytes) == cudaSuccess)
+        (void)cudaLaunchKernelEx(&c, k_verify<T, DRAFT>, a);   // its error is the one the check reads
 }
 
 }  // namespace
