@@ -21,15 +21,7 @@ namespace cg = cooperative_groups;
 
 namespace {
 
-constexpr int NT = 512, WARPS = NT / 32, MAX_CLUSTER = 8;
-
-// vectors of a thread under way, and the distance from one to the next (the target's and the draft's) in the ring
-template <bool DRAFT> constexpr int RING = DRAFT ? 5 : 8;
-template <bool DRAFT> constexpr int PER = DRAFT ? 2 * NT : NT;
-
-__device__ __forceinline__ void cp_async16(uint4 *to, const void *from) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
-}
+constexpr int NT = 256, WARPS = NT / 32, MAX_CLUSTER = 8, ROWS = 32;   // rows of a segment that the draw takes at a time
 
 struct Sum { float h, l; };   // h + l
 
@@ -45,17 +37,38 @@ __device__ __forceinline__ Sum operator+(Sum a, Sum b) {
     const Sum s = two_sum(a.h, b.h);
     return fast_two_sum(s.h, __fadd_rn(s.l, __fadd_rn(a.l, b.l)));
 }
-// a running sum: what each addition loses is added up apart (a few dozen terms lose less than 2^-46 of the sum)
-__device__ __forceinline__ void add(Sum &a, float b) {
-    const Sum s = two_sum(a.h, b);
-    a.h = s.h;
-    a.l = __fadd_rn(a.l, s.l);
+// Two floats in a register pair: one instruction adds, subtracts or multiplies both.
+typedef unsigned long long Two;
+__device__ __forceinline__ Two two(float a, float b) {
+    Two r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
 }
-__device__ __forceinline__ void add(Sum &a, Sum b) {
-    const Sum s = two_sum(a.h, b.h);
-    a.h = s.h;
-    a.l = __fadd_rn(a.l, __fadd_rn(s.l, b.l));
+__device__ __forceinline__ float2 apart(Two a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+    return r;
 }
+__device__ __forceinline__ Two add2(Two a, Two b) { Two r; asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b)); return r; }
+__device__ __forceinline__ Two sub2(Two a, Two b) { Two r; asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b)); return r; }
+__device__ __forceinline__ Two mul2(Two a, Two b) { Two r; asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b)); return r; }
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) { Two r; asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c)); return r; }
+
+// two running sums: what each addition loses is added up apart (a few dozen terms lose less than 2^-46 of a sum)
+struct Sums {
+    Two h, l;
+    __device__ __forceinline__ void add(Two b) {
+        const Two s = add2(h, b), t = sub2(s, h);
+        l = add2(l, add2(sub2(h, sub2(s, t)), sub2(b, t)));
+        h = s;
+    }
+    __device__ __forceinline__ void add(Two b, Two low) {
+        add(b);
+        l = add2(l, low);
+    }
+    __device__ __forceinline__ Sum first() const { return fast_two_sum(apart(h).x, apart(l).x); }
+    __device__ __forceinline__ Sum second() const { return fast_two_sum(apart(h).y, apart(l).y); }
+};
 __device__ __forceinline__ Sum operator*(Sum a, float b) {
     const float h = __fmul_rn(a.h, b);
     return fast_two_sum(h, __fmaf_rn(a.l, b, __fmaf_rn(a.h, b, -h)));
@@ -73,19 +86,35 @@ __device__ __forceinline__ Sum operator/(Sum a, Sum b) {
 __device__ __forceinline__ Sum shfl_xor(Sum a, int o) {
     return {__shfl_xor_sync(0xffffffffu, a.h, o), __shfl_xor_sync(0xffffffffu, a.l, o)};
 }
+// without bringing the low part below the high one's last place, which a chain of sums needs only once
+__device__ __forceinline__ Sum loosely(Sum a, Sum b) {
+    const Sum s = two_sum(a.h, b.h);
+    return {s.h, __fadd_rn(s.l, __fadd_rn(a.l, b.l))};
+}
 __device__ __forceinline__ Sum warp_sum(Sum a) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) a = a + shfl_xor(a, o);
-    return a;
+    for (int o = 16; o; o >>= 1) a = loosely(a, shfl_xor(a, o));
+    return fast_two_sum(a.h, a.l);
+}
+// two sums over the warp, side by side
+__device__ __forceinline__ void warp_sums(Sum &a, Sum &b) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const Sum x = shfl_xor(a, o), y = shfl_xor(b, o);
+        a = loosely(a, x);
+        b = loosely(b, y);
+    }
+    a = fast_two_sum(a.h, a.l);
+    b = fast_two_sum(b.h, b.l);
 }
 // inclusive sums over the lanes
 __device__ __forceinline__ Sum warp_scan(Sum a) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const Sum up = {__shfl_up_sync(0xffffffffu, a.h, o), __shfl_up_sync(0xffffffffu, a.l, o)};
-        if ((threadIdx.x & 31) >= o) a = up + a;
+        if ((threadIdx.x & 31) >= o) a = loosely(up, a);
     }
-    return a;
+    return fast_two_sum(a.h, a.l);
 }
 
 // max(p - l q, 0) as two floats
@@ -94,6 +123,17 @@ __device__ __forceinline__ Sum left(float p, float q, Sum l) {
     const Sum d = two_sum(p, -h);
     const Sum r = fast_two_sum(d.h, __fsub_rn(d.l, e));
     return r.h > 0.0f ? r : Sum{0.0f, 0.0f};
+}
+
+// the same for two elements
+__device__ __forceinline__ void left2(Two p, Two q, Two lh, Two ll, Two &high, Two &low) {
+    const Two n = mul2(lh, q ^ 0x8000000080000000ull);   // -l q
+    const Two e = fma2(ll, q, fma2(lh, q, n));            // and what that lacks
+    const Two s = add2(p, n), t = sub2(s, p), d = sub2(add2(sub2(p, sub2(s, t)), sub2(n, t)), e);
+    const Two r = add2(s, d);
+    const float2 h = apart(r), l = apart(sub2(d, sub2(r, s)));
+    high = two(h.x > 0.0f ? h.x : 0.0f, h.y > 0.0f ? h.y : 0.0f);
+    low = two(h.x > 0.0f ? l.x : 0.0f, h.y > 0.0f ? l.y : 0.0f);
 }
 
 // x where it is a positive finite number, else 0
@@ -121,7 +161,8 @@ enum { DRAW = 0, NODE = 1, SWEEP = 2 };
 struct Shared {
     Plan plan;
     Sum seg[MAX_CLUSTER * WARPS], seg_q[MAX_CLUSTER * WARPS];   // (first block) the sums of all segments
-    Sum row[WARPS];                                             // (the draw) of the rows of one segment
+    Sum row[ROWS];                                              // (the draw) of the rows of one segment
+    int last;
 };
 
 // A row of the vocabulary in vectors of 16 bytes, counted from the aligned address at or before its start.
@@ -139,13 +180,11 @@ template <class T> struct Row {
     }
 };
 
-// bits i .. i + 7 of a row of live bits
+// bits i .. i + 7 of a row of live bits (any past its end), -8 < i; without a branch, so that loads go on behind it
 __device__ __forceinline__ uint32_t bits_at(const uint32_t *live, int words, int i) {
-    if (i < 0) return __ldg(live) << -i;                // -8 < i
-    const int w = i >> 5;
-    const uint32_t lo = __ldg(live + w);
-    if (!(i & 7)) return lo >> (i & 31);
-    return __funnelshift_r(lo, w + 1 < words ? __ldg(live + w + 1) : 0u, i & 31);
+    const int w = max(i, 0) >> 5;
+    const uint32_t lo = __ldg(live + w), hi = __ldg(live + min(w + 1, words - 1));
+    return i < 0 ? lo << (-i & 31) : __funnelshift_r(lo, hi, i & 31);
 }
 
 // What a block knows of the current node.
@@ -157,63 +196,106 @@ template <class T, bool DRAFT> struct Node {
     Sum lam;
     __device__ __forceinline__ uint32_t bits(int c) const { return live ? bits_at(live, words, c * N - lead) : 0xffffffffu; }
     __device__ __forceinline__ int segment(int x) const { return (x + lead) / N / per; }
-    // vector c of the rows to the thread's place of the ring: an asynchronous copy where it is aligned
-    __device__ __forceinline__ void fetch(uint4 *to, int c) const {
-        const int i = c * N - lead;
-        const bool inside = i >= 0 && i <= V() - N;
-        if (inside) cp_async16(to, p.p + i);             // (p's vectors are aligned by their count)
-        else *to = p.load(i);
-        if (DRAFT) {
-            if (inside && !((uintptr_t)(q.p + i) & 15)) cp_async16(to + NT, q.p + i);
-            else to[NT] = q.load(i);
-        }
-    }
-    __device__ __forceinline__ int V() const { return p.V; }
-    // The sums of vectors c0 + lane, c0 + lane + 32, ... below c1; FRESH: l = 0, and the draft's sum too.  The vectors
-    // come through a ring in shared memory, which keeps more of them under way than registers would; a thread
-    // reads what it has copied itself.
-    template <bool FRESH> __device__ __forceinline__ void sweep(uint4 *ring, int c0, int c1, Sum &w, Sum &wq) const {
-        ring += threadIdx.x;
-        int put = c0 + (threadIdx.x & 31);
+    // two elements' worth of sums for every vector: fresh, the target's and the draft's sum; else those of even and of odd
+    // elements
+    template <bool FRESH, bool LIVE> __device__ __forceinline__ void take(Sums &run, uint4 x, uint4 y, uint32_t b) const {
+        float f[N], g[N];
+        fa_unpack(x, f, T());
+        if (DRAFT) fa_unpack(y, g, T());
+        // all of them nonnegative and finite: the common case
+        uint32_t most = 0;
 #pragma unroll
-        for (int k = 0; k < RING<DRAFT>; ++k, put += 32) {
-            if (put < c1) fetch(ring + k * PER<DRAFT>, put);
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        }
-        int k = 0;
-        for (int c = c0 + (threadIdx.x & 31); c < c1; c += 32, put += 32) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(RING<DRAFT> - 1) : "memory");
-            uint4 *at = ring + k * PER<DRAFT>;
-            const uint4 x = *at, y = DRAFT ? at[NT] : x;
-            const uint32_t b = live ? bits(c) : 0xffffffffu;
-            float f[N], g[N];
-            fa_unpack(x, f, T());
-            if (DRAFT) fa_unpack(y, g, T());
-            // all of them nonnegative and finite, and allowed: the common case
-            uint32_t most = 0;
-#pragma unroll
-            for (int e = 0; e < N; ++e) most = max(most, max(__float_as_uint(f[e]), DRAFT ? __float_as_uint(g[e]) : 0u));
-            if (most >= 0x7f800000u || (b & ((1u << N) - 1)) != (1u << N) - 1) {
-#pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    const bool in = b >> e & 1;
-                    f[e] = in ? weight(f[e]) : 0.0f;
-                    if (DRAFT) g[e] = in ? weight(g[e]) : 0.0f;
-                }
-            }
+        for (int e = 0; e < N; ++e) most = max(most, max(__float_as_uint(f[e]), DRAFT ? __float_as_uint(g[e]) : 0u));
+        if (most >= 0x7f800000u) {
 #pragma unroll
             for (int e = 0; e < N; ++e) {
-                if (DRAFT && !FRESH) {
-                    add(w, left(f[e], g[e], lam));
-                } else {
-                    add(w, f[e]);
-                    if (DRAFT) add(wq, g[e]);
-                }
+                f[e] = weight(f[e]);
+                if (DRAFT) g[e] = weight(g[e]);
             }
-            if (put < c1) fetch(at, put);
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            if (++k == RING<DRAFT>) k = 0;
         }
+        if (LIVE) {
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const int in = (int)(b << (31 - e)) >> 31;
+                f[e] = __int_as_float(__float_as_int(f[e]) & in);
+                if (DRAFT) g[e] = __int_as_float(__float_as_int(g[e]) & in);
+            }
+        }
+        if (DRAFT && FRESH) {
+#pragma unroll
+            for (int e = 0; e < N; ++e) run.add(two(f[e], g[e]));
+        } else {
+            const Two lh = two(lam.h, lam.h), ll = two(lam.l, lam.l);
+#pragma unroll
+            for (int e = 0; e < N; e += 2) {
+                if (!DRAFT) { run.add(two(f[e], f[e + 1])); continue; }
+                Two high, low;
+                left2(two(f[e], f[e + 1]), two(g[e], g[e + 1]), lh, ll, high, low);
+                run.add(high, low);
+            }
+        }
+    }
+    // vectors c, c + step, ... below c1 of both rows (zeros past it): plain loads for those that the row fills, all
+    // issued before the row's ends or a draft row of another alignment are looked after
+    template <int U> __device__ __forceinline__ void fetch(int c, int step, int c1, uint4 (&x)[U], uint4 (&y)[U]) const {
+        const int from = lead ? 1 : 0, to = (p.V + lead) % N ? chunks - 1 : chunks;
+        const uint4 *pv = reinterpret_cast<const uint4 *>(p.p - lead) + c, *qv = reinterpret_cast<const uint4 *>(q.p - lead) + c;
+        const bool together = !((uintptr_t)qv & 15);
+        bool left_over = false;
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int at = c + step * k;
+            const bool whole = at >= from && at < min(to, c1);
+            x[k] = y[k] = make_uint4(0, 0, 0, 0);
+            if (whole) x[k] = __ldg(pv + step * k);
+            if (DRAFT && whole && together) y[k] = __ldg(qv + step * k);
+            left_over |= at < c1 && !(whole && (!DRAFT || together));
+        }
+        if (left_over) {
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const int at = c + step * k;
+                if (at >= c1) continue;
+                x[k] = p.load(at * N - lead);
+                if (DRAFT) y[k] = q.load(at * N - lead);
+            }
+        }
+    }
+    // the sums of vectors c0 + lane, c0 + lane + 32, ... below c1, U of them under way; FRESH: l = 0, and the draft's sum too
+    template <bool FRESH, bool LIVE> __device__ __forceinline__ void sweep(int c0, int c1, Sum &w, Sum &wq) const {
+        constexpr int U = DRAFT ? 5 : 8;
+        Sums run = {0ull, 0ull};
+        for (int c = c0 + (threadIdx.x & 31); c < c1; c += 32 * U) {
+            uint4 x[U], y[U];
+            uint32_t b[U];
+#pragma unroll
+            for (int k = 0; k < U; ++k) b[k] = LIVE && c + 32 * k < c1 ? bits_at(live, words, (c + 32 * k) * N - lead) : 0u;
+            fetch(c, 32, c1, x, y);
+#pragma unroll
+            for (int k = 0; k < U; ++k) take<FRESH, LIVE>(run, x[k], y[k], b[k]);
+        }
+        w = run.first();
+        wq = run.second();
+        if (!(DRAFT && FRESH)) w = w + wq;
+    }
+    // the weights of vector c for the draw, without the n tokens of `tried`, and their sum
+    __device__ __forceinline__ Sum weigh(int c, uint4 x, uint4 y, uint32_t b, Sum (&v)[N], const int *tried, int n) const {
+        const int i = c * N - lead;
+        float f[N], g[N];
+        fa_unpack(x, f, T());
+        if (DRAFT) fa_unpack(y, g, T());
+        for (int k = 0; k < n; ++k) {
+            const uint32_t e = (uint32_t)(tried[k] - i);
+            if (e < N) b &= ~(1u << e);
+        }
+        Sum sum = {0.0f, 0.0f};
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const float pe = b >> e & 1 ? weight(f[e]) : 0.0f;
+            v[e] = DRAFT ? left(pe, weight(g[e]), lam) : Sum{pe, 0.0f};
+            sum = sum + v[e];
+        }
+        return sum;
     }
 };
 
@@ -221,8 +303,7 @@ template <class T, bool DRAFT>
 __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
     constexpr int N = fa_vec<T>::N;
     __shared__ Shared sh;
-    extern __shared__ uint4 ring[];
-    int *dyn = reinterpret_cast<int *>(ring + RING<DRAFT> * PER<DRAFT>);
+    extern __shared__ int dyn[];
     int *parent = dyn, *tok = dyn + a.T, *path = dyn + 2 * a.T, *after = dyn + 3 * a.T, *tried = dyn + 4 * a.T;
     float *us = (float *)(dyn + 5 * a.T), *px = us + a.T, *qx = px + a.T;
     const cg::cluster_group cluster = cg::this_cluster();
@@ -259,49 +340,65 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
             at.chunks = (int)(((int64_t)a.V + at.lead + N - 1) / N);
             at.per = (at.chunks + C * NT - 1) / (C * NT) * 32;
             at.lam = {0.0f, 0.0f};
-            if (rank == 0) {
-                // what the tests of this node's children need
-                for (int i = node + 1 + tid; i < use; i += NT) {
-                    if (parent[i] != node) continue;
-                    const int x = tok[i];
-                    px[i] = qx[i] = 0.0f;
-                    after[i] = -1;
-                    if ((unsigned)x >= (unsigned)a.V || !any) continue;
-                    const int to = a.S ? a.next[(int64_t)state * a.V + x] : 0;
-                    after[i] = to;
-                    if (to < 0) continue;
-                    px[i] = weight(fa_to_f32(at.p.p[x]));
-                    if (DRAFT) qx[i] = weight(fa_to_f32(at.q.p[x]));
-                }
-            }
+        }
+        // what the test of a child needs, one a thread (and the rest of a long draft below): under way during the sweep
+        const int child = node + 1 + tid;
+        const bool tests = rank == 0 && fresh && any && child < use && parent[child] == node && (unsigned)tok[child] < (unsigned)a.V;
+        int to = -1;
+        float child_p = 0.0f, child_q = 0.0f;
+        if (tests) {
+            const int x = tok[child];
+            to = a.S ? a.next[(int64_t)state * a.V + x] : 0;
+            child_p = fa_to_f32(at.p.p[x]);
+            if (DRAFT) child_q = fa_to_f32(at.q.p[x]);
         }
         // ---- this warp's segment
         const int mine = rank * WARPS + warp, s0 = mine * at.per, s1 = min(s0 + at.per, at.chunks);
         Sum w = {0.0f, 0.0f}, wq = {0.0f, 0.0f};
         if (any) {
-            if (fresh || !DRAFT) at.template sweep<true>(ring, s0, s1, w, wq);
-            else at.template sweep<false>(ring, s0, s1, w, wq);
+            if (fresh || !DRAFT) {
+                if (at.live) at.template sweep<true, true>(s0, s1, w, wq);
+                else at.template sweep<true, false>(s0, s1, w, wq);
+            } else {
+                if (at.live) at.template sweep<false, true>(s0, s1, w, wq);
+                else at.template sweep<false, false>(s0, s1, w, wq);
+            }
         }
-        w = warp_sum(fast_two_sum(w.h, w.l));
-        if (DRAFT && fresh) wq = warp_sum(fast_two_sum(wq.h, wq.l));
+        if (DRAFT && fresh) warp_sums(w, wq);
+        else w = warp_sum(w);
         if (lane == 0) {
             first->seg[mine] = w;
             if (DRAFT && fresh) first->seg_q[mine] = wq;
         }
+        if (tests) {
+            after[child] = to;
+            px[child] = to < 0 ? 0.0f : weight(child_p);
+            qx[child] = to < 0 ? 0.0f : weight(child_q);
+        }
+        if (rank == 0 && fresh && any)
+            for (int i = child + NT; i < use; i += NT) {
+                const int x = tok[i];
+                if (parent[i] != node || (unsigned)x >= (unsigned)a.V) continue;
+                const int there = a.S ? a.next[(int64_t)state * a.V + x] : 0;
+                after[i] = there;
+                px[i] = there < 0 ? 0.0f : weight(fa_to_f32(at.p.p[x]));
+                qx[i] = DRAFT && there >= 0 ? weight(fa_to_f32(at.q.p[x])) : 0.0f;
+            }
         cluster.sync();
         if (rank == 0 && warp == 0) {
             const int each = (C * WARPS + 31) / 32;       // segments of a lane
             Sum total = {0.0f, 0.0f}, t = {0.0f, 0.0f};
             for (int i = lane * each; i < min((lane + 1) * each, C * WARPS); ++i) {
                 total = total + sh.seg[i];
-                if (DRAFT && fresh) t = t + sh.seg_q[i];
+                if (DRAFT) t = t + sh.seg_q[i];
             }
-            total = warp_sum(total);
             if (fresh) {
                 n_tried = 0;
                 l = {0.0f, 0.0f};
-                if (DRAFT) total_q = warp_sum(t);
+                if (DRAFT) warp_sums(total, t);
+                total_q = t;
             }
+            if (!DRAFT || !fresh) total = warp_sum(total);
             Plan plan = {};
             const bool some = total.h > 0.0f && total.h < INFINITY;
             if (lane == 0) {
@@ -408,7 +505,7 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
         }
         break;
     }
-    // ---- the draw: the block that has the segment takes it row by row of 32 vectors, a warp a row
+    // ---- the draw: the block that has the segment sums its rows of 32 vectors, and a warp takes the row that holds it
     const int segment = sh.plan.segment;
     if (segment < 0) {
         if (rank == 0 && tid == 0) {
@@ -417,87 +514,74 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
         }
     } else if (rank == segment / WARPS) {
         const int n = DRAFT ? 0 : sh.plan.tried, c0 = segment * at.per, c1 = min(c0 + at.per, at.chunks);
-        const Sum goal = sh.plan.goal;
-        if (!DRAFT && rank != 0) {
+        Sum goal = sh.plan.goal;
+        if (!DRAFT && rank != 0 && n > 0) {
             const int *theirs = cluster.map_shared_rank(tried, 0);
             for (int i = tid; i < n; i += NT) tried[i] = theirs[i];
             __syncthreads();
         }
         Sum before = sh.plan.before;
-        int last = -1;                                    // the last element with a weight so far
-        for (int r0 = c0; r0 < c1; r0 += NT) {
-            const int c = r0 + tid, i = c * N - at.lead;
-            float f[N], g[N];
-            uint32_t bits = 0;
-            uint4 x = make_uint4(0, 0, 0, 0), y = x;
-            if (c < c1) {
-                x = at.p.load(i);
-                if (DRAFT) y = at.q.load(i);
-                bits = at.bits(c);
-            }
-            fa_unpack(x, f, T());
-            if (DRAFT) fa_unpack(y, g, T());
-            Sum sum = {0.0f, 0.0f};
-            int best = -1;
-            uint32_t in = 0;
+        Sum v[N];
+        int held = -1;                                    // the last row with a weight so far
+        bool found_row = false;
+        for (int r0 = c0; r0 < c1; r0 += 32 * ROWS) {
+            constexpr int U = ROWS / WARPS;
+            Sum sums[U];
+            uint4 x[U], y[U];
+            uint32_t bits[U];
+            const int c = r0 + tid;
+            at.fetch(c, NT, c1, x, y);
 #pragma unroll
-            for (int e = 0; e < N; ++e) {
-                bool out = !(bits >> e & 1);
-                for (int k = 0; k < n; ++k) out |= tried[k] == i + e;
-                const float pe = out ? 0.0f : weight(f[e]), qe = DRAFT ? weight(g[e]) : 0.0f;
-                const Sum v = DRAFT ? left(pe, qe, at.lam) : Sum{pe, 0.0f};
-                if (v.h > 0.0f) { best = i + e; in |= 1u << e; }
-                add(sum, v);
-            }
-            const Sum upto = warp_scan(fast_two_sum(sum.h, sum.l));
-            if (lane == 31) sh.row[warp] = upto;
-            __syncthreads();
-            // the rows' sums in the lanes; the warp whose row holds the draw
-            const Sum mine = lane < WARPS ? sh.row[lane] : Sum{0.0f, 0.0f}, rows = warp_scan(lane ? mine : before + mine);
-            const uint32_t holds = __ballot_sync(0xffffffffu, mine.h > 0.0f && goal < rows);
-            const int who = holds ? __ffs(holds) - 1 : -1, prior = max(who - 1, 0);
-            Sum start = {__shfl_sync(0xffffffffu, rows.h, prior), __shfl_sync(0xffffffffu, rows.l, prior)};
-            if (who <= 0) start = before;
-            const Sum end = {__shfl_sync(0xffffffffu, rows.h, 31), __shfl_sync(0xffffffffu, rows.l, 31)};
-            if (warp == who) {
-                const Sum lanes = {__shfl_up_sync(0xffffffffu, upto.h, 1), __shfl_up_sync(0xffffffffu, upto.l, 1)};
-                const uint32_t past = __ballot_sync(0xffffffffu, in && goal < start + upto), some = __ballot_sync(0xffffffffu, in != 0);
-                const int pick = past ? __ffs(past) - 1 : 31 - __clz(some);
-                if (lane == pick) {
-                    Sum run = lane ? start + lanes : start;   // of the lanes before, then through the elements
-                    int found = best;
-                    bool done = false;
+            for (int k = 0; k < U; ++k) bits[k] = c + NT * k < c1 ? at.bits(c + NT * k) : 0u;
 #pragma unroll
-                    for (int e = 0; e < N; ++e) {
-                        if (!(in >> e & 1) || done) continue;
-                        const float pe = weight(f[e]), qe = DRAFT ? weight(g[e]) : 0.0f;
-                        const Sum v = DRAFT ? left(pe, qe, at.lam) : Sum{pe, 0.0f};
-                        run = run + fast_two_sum(v.h, v.l);
-                        if (goal < run) { found = i + e; done = true; }
-                    }
-                    a.token[b] = found;
-                    if (a.state) a.state[b] = a.next[(int64_t)state * a.V + found];
-                }
-            }
-            if (who >= 0) { last = -1; break; }
-            best = __reduce_max_sync(0xffffffffu, best);
-            __syncthreads();                              // the rows' sums have been read
-            if (lane == 0) sh.row[warp].h = __int_as_float(best);
+            for (int k = 0; k < U; ++k) sums[k] = at.weigh(c + NT * k, x[k], y[k], bits[k], v, tried, n);
+#pragma unroll
+            for (int k = 0; k < ROWS / WARPS; k += 2) warp_sums(sums[k], sums[k + 1]);
+            __syncthreads();                              // the last rows' sums have been read
+            if (lane == 0)
+#pragma unroll
+                for (int k = 0; k < ROWS / WARPS; ++k) sh.row[warp + WARPS * k] = sums[k];
             __syncthreads();
-            for (int k = 0; k < WARPS; ++k) last = max(last, __float_as_int(sh.row[k].h));
-            __syncthreads();
-            before = end;
+            // the rows' sums in the lanes
+            const Sum mine = sh.row[lane], upto = warp_scan(lane ? mine : before + mine);
+            const uint32_t holds = __ballot_sync(0xffffffffu, mine.h > 0.0f && goal < upto), some = __ballot_sync(0xffffffffu, mine.h > 0.0f);
+            if (some) held = r0 + 32 * (31 - __clz(some));
+            const int who = holds ? __ffs(holds) - 1 : 31;
+            if (holds) held = r0 + 32 * who;
+            const int prior = holds ? who - 1 : 31;
+            const Sum next = {__shfl_sync(0xffffffffu, upto.h, max(prior, 0)), __shfl_sync(0xffffffffu, upto.l, max(prior, 0))};
+            if (prior >= 0) before = next;
+            if (holds) { found_row = true; break; }
         }
-        if (last >= 0 && tid == 0) {                      // rounding hid the draw: the last element with a weight
-            a.token[b] = last;
-            if (a.state) a.state[b] = a.next[(int64_t)state * a.V + last];
+        if (!found_row) goal = {INFINITY, 0.0f};          // rounding hid the draw: the last element with a weight
+        if (warp == 0 && held >= 0) {
+            const int c = held + lane;
+            uint4 x[1], y[1];
+            at.fetch(c, 32, c1, x, y);
+            const Sum sum = at.weigh(c, x[0], y[0], c < c1 ? at.bits(c) : 0u, v, tried, n), upto = warp_scan(lane ? sum : before + sum);
+            const uint32_t past = __ballot_sync(0xffffffffu, sum.h > 0.0f && goal < upto), some = __ballot_sync(0xffffffffu, sum.h > 0.0f);
+            const int pick = past ? __ffs(past) - 1 : 31 - __clz(some);
+            Sum run = {__shfl_up_sync(0xffffffffu, upto.h, 1), __shfl_up_sync(0xffffffffu, upto.l, 1)};   // of the lanes before, then through the elements
+            if (lane == 0) run = before;
+            if (lane == pick) {
+                int found = -1;
+                bool done = false;
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    if (done || !(v[e].h > 0.0f)) continue;
+                    run = run + v[e];
+                    found = c * N - at.lead + e;
+                    done = goal < run;
+                }
+                a.token[b] = found;
+                if (a.state) a.state[b] = a.next[(int64_t)state * a.V + found];
+            }
         }
     }
     if (rank == 0) {
-        __syncthreads();                                  // the rows' sums have been read
-        if (tid == 0) { sh.row[0].h = __int_as_float(kept); a.kept[b] = kept; }
+        if (tid == 0) { sh.last = kept; a.kept[b] = kept; }
         __syncthreads();
-        const int n = __float_as_int(sh.row[0].h);
+        const int n = sh.last;
         for (int i = tid; i < a.T; i += NT) a.path[(int64_t)b * a.T + i] = i < n ? path[i] : -1;
     }
     cluster.sync();                                       // no block leaves while another reads its list
@@ -511,12 +595,11 @@ template <class T, bool DRAFT> void launch(const VerifyArgs &a, int cluster, cud
     cudaLaunchConfig_t c = {};
     c.gridDim = dim3((unsigned)a.B * cluster);
     c.blockDim = dim3(NT);
-    c.dynamicSmemBytes = sizeof(uint4) * RING<DRAFT> * PER<DRAFT> + (size_t)a.T * 8 * sizeof(int);
+    c.dynamicSmemBytes = (size_t)a.T * 8 * sizeof(int);
     c.stream = s;
     c.attrs = at;
     c.numAttrs = 1;
-    if (cudaFuncSetAttribute(k_verify<T, DRAFT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)c.dynamicSmemBytes) == cudaSuccess)
-        (void)cudaLaunchKernelEx(&c, k_verify<T, DRAFT>, a);   // its error is the one the check reads
+    (void)cudaLaunchKernelEx(&c, k_verify<T, DRAFT>, a);   // its error is the one the check reads
 }
 
 }  // namespace
@@ -539,7 +622,12 @@ extern "C" fa_status fa_verify(int32_t dtype, int32_t B, int32_t T, int32_t V, c
     if (((uintptr_t)target | (uintptr_t)draft) % es) return fa_refuse(fn, "target and draft must be aligned to their type");
     const VerifyArgs a{B, T, V, S, (V + 31) / 32, target, draft, target_batch_stride, target_row_stride, draft_batch_stride,
                        draft_row_stride, tokens, parents, count, u, states, next, live, path, kept, token, S > 0 ? state : nullptr};
-    const int cluster = V > 4096 ? MAX_CLUSTER : 1;
+    // Blocks of a sequence: eight where the vocabulary gives each thread some work (1 / 2 / 4 / 8 blocks, 8 sequences of
+    // 5 x 32000: 46 / 34 / 27 / 23 us, of 5 x 8000 27 / 23 / 23 / 22), fewer where that would take more than two rounds of
+    // blocks for short sweeps (64 sequences of 5 x 32000 48 / 36 / 31 / 48 us, of 5 x 8000 28 / 24 / 25 / 43, but of
+    // 9 x 151936 335 / 185 / 131 / 99).
+    int cluster = MAX_CLUSTER;
+    while (cluster > 1 && (V < 2048 * cluster || (V < 65536 && B * cluster > 2 * 152))) cluster /= 2;
     auto go = [&](auto tag) {
         using T_ = decltype(tag);
         if (draft) launch<T_, true>(a, cluster, (cudaStream_t)stream);
