@@ -12,9 +12,9 @@ namespace {
 
 constexpr int NT = 1024;
 
-// inclusive sums of x over the block, and the block's total; all threads
-__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t *warps, int64_t &total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = blockDim.x >> 5;
+// inclusive sums of x over the block's n warps, and the block's total; all threads
+__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t *warps, int n, int64_t &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int64_t up = __shfl_up_sync(0xffffffffu, x, o);
@@ -23,13 +23,16 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t *warps, int64_t
     __syncthreads();                     // the last call's sums have been read
     if (lane == 31) warps[warp] = x;
     __syncthreads();
-    int64_t before = 0;
-    total = 0;
-    for (int i = 0; i < n; ++i) {
-        before += i < warp ? warps[i] : 0;
-        total += warps[i];
+    // every warp adds up the warps' sums itself
+    int64_t all = lane < n ? warps[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, all, o);
+        if (lane >= o) all += up;
     }
-    return before + x;
+    total = __shfl_sync(0xffffffffu, all, 31);
+    const int64_t before = __shfl_sync(0xffffffffu, all, max(warp - 1, 0));
+    return warp ? before + x : x;
 }
 
 struct PagesArgs {
@@ -38,112 +41,145 @@ struct PagesArgs {
     int32_t *table, *held, *free_pages, *n_free, *status;
 };
 
-// what sequence b holds and wants
-__device__ __forceinline__ void sequence(const PagesArgs &a, int b, int &held, int64_t &need) {
-    held = min(max(a.held[b], 0), a.max_pages);
-    need = ((int64_t)max(a.want[b], 0) + (1 << a.shift) - 1) >> a.shift;
-}
+// The sequences of a tile: what each holds and wants, and the pages given back and wanted before each.
+struct Tile {
+    int64_t warps[NT / 32];
+    int32_t held[NT], need[NT], back[NT + 1], grow[NT + 1];
+};
 
-// the sequence of the tile whose pages' range holds move k: sums[i] is the number of moves before sequence i
-__device__ __forceinline__ int owner(const int64_t *sums, int n, int64_t k) {
-    int lo = 0, hi = n;                  // sums[lo] <= k < sums[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (sums[mid] <= k) lo = mid; else hi = mid;
-    }
+// the sequence of a tile of N (a power of two) whose range holds move k: sums[i] is the number of moves before sequence i
+template <int N, class S> __device__ __forceinline__ int owner(const S *sums, int64_t k) {
+    int lo = 0;                          // sums[lo] <= k < sums[N]
+#pragma unroll
+    for (int step = N / 2; step; step /= 2)
+        if (sums[lo + step] <= k) lo += step;
     return lo;
 }
 
-// One cluster.  Every block makes the sums itself, over the sequences in tiles of NT, and moves its part of the
-// pages; what is read stays unchanged until all blocks have read it.
-__global__ void __launch_bounds__(NT) k_pages_resize(PagesArgs a) {
-    __shared__ int64_t warps[NT / 32], sums[NT + 1];
+// One block, or a cluster of them whose blocks all make the sums and move a part of the pages each.  Sequences come in
+// tiles of a block's threads; up to one tile (the common case) is read and summed up once.
+// What bounds it is the chain of steps: lengths, two sums, the copies down and up the stack with a barrier between.
+template <bool CLUSTER> __global__ void __launch_bounds__(NT) k_pages_resize(PagesArgs a) {
+    constexpr int U = 4;                 // moves of a thread under way
+    __shared__ Tile t;
     const cg::cluster_group cluster = cg::this_cluster();
-    const int tid = threadIdx.x, part = cluster.block_rank() * NT + tid, parts = cluster.num_blocks() * NT;
+    const int tid = threadIdx.x, rank = CLUSTER ? cluster.block_rank() : 0, parts = CLUSTER ? cluster.num_blocks() * NT : NT;
+    const int part = rank * NT + tid;
+    const bool single = a.B <= NT;
+    auto meet = [&]() {                  // the others' writes are seen after
+        if (CLUSTER) { __threadfence(); cluster.sync(); }
+        else __syncthreads();
+    };
+    int held = 0;                        // of the thread's sequence of the tile
+    int64_t need = 0, grow = 0, upto = 0;
+    auto load = [&](int b) {
+        held = 0;
+        need = 0;
+        if (b < a.B) {
+            held = min(max(a.held[b], 0), a.max_pages);
+            need = ((int64_t)max(a.want[b], 0) + (1 << a.shift) - 1) >> a.shift;
+        }
+        grow = need <= a.max_pages ? max(need - held, (int64_t)0) : 0;
+    };
+    // the tile's sums, pages given back in the low half and wanted in the high one (the host has checked that both fit)
+    int64_t tile_back, tile_grow;
+    auto sum = [&](int b0) {
+        load(b0 + tid);
+        int64_t total;
+        const int64_t both = block_scan(max((int64_t)held - need, (int64_t)0) + (grow << 32), t.warps, NT / 32, total);
+        tile_back = total & 0xffffffff;
+        tile_grow = total >> 32;
+        upto = both >> 32;
+        t.held[tid] = held;
+        t.need[tid] = (int)min(need, (int64_t)a.max_pages);
+        t.back[tid + 1] = (int)(both & 0xffffffff);
+        t.grow[tid + 1] = (int)upto;
+        if (tid == 0) t.back[0] = t.grow[0] = 0;
+        __syncthreads();
+    };
     const int64_t n_free = min(max(*a.n_free, 0), a.n_pages);
-    // what is given back in all
-    int64_t mine = 0, returned, total;
-    for (int b = tid; b < a.B; b += NT) {
-        int held;
-        int64_t need;
-        sequence(a, b, held, need);
-        mine += max((int64_t)held - need, (int64_t)0);
+    int64_t returned = 0;
+    if (single) {
+        sum(0);
+        returned = tile_back;
+    } else {
+        int64_t mine = 0;
+        for (int b = tid; b < a.B; b += NT) { load(b); mine += max((int64_t)held - need, (int64_t)0); }
+        block_scan(mine, t.warps, NT / 32, returned);
     }
-    block_scan(mine, warps, returned);
     const int64_t there = n_free + returned;
-    // pages given back
+    // ---- pages given back: move k goes k places below the new top
     int64_t before = 0;
     for (int b0 = 0; b0 < a.B && returned > 0; b0 += NT) {
-        int held = 0;
-        int64_t need = 0;
-        if (b0 + tid < a.B) sequence(a, b0 + tid, held, need);
-        const int64_t sum = block_scan(max((int64_t)held - need, (int64_t)0), warps, total);
-        sums[tid + 1] = sum;
-        if (tid == 0) sums[0] = 0;
-        __syncthreads();
-        for (int64_t k = part; k < total; k += parts) {
-            const int i = owner(sums, NT, k), b = b0 + i;
-            int h;
-            int64_t n;
-            sequence(a, b, h, n);
-            int32_t *entry = a.table + (int64_t)b * a.max_pages + n + (k - sums[i]);
-            const int64_t to = there - 1 - (before + k);
-            if (to < a.n_pages) a.free_pages[to] = *entry;
-            *entry = -1;
+        if (!single) sum(b0);
+        for (int64_t k0 = part; k0 < tile_back; k0 += U * parts) {
+            int32_t *entry[U], page[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t k = k0 + u * parts;
+                if (k >= tile_back) break;
+                const int i = owner<NT>(t.back, k);
+                entry[u] = a.table + (int64_t)(b0 + i) * a.max_pages + t.need[i] + (k - t.back[i]);
+                page[u] = *entry[u];
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t k = k0 + u * parts, to = there - 1 - (before + k);
+                if (k >= tile_back) break;
+                if (to < a.n_pages) a.free_pages[to] = page[u];
+                *entry[u] = -1;
+            }
         }
-        before += total;
+        before += tile_back;
     }
-    __threadfence();
-    cluster.sync();
-    // pages taken; granted while the sum of all that is wanted up to here is there
+    if (returned > 0 || CLUSTER) meet();
+    // ---- pages taken, from the top: granted while the sum of all that is wanted up to here is there
     before = 0;
     int64_t taken = 0;
     for (int b0 = 0; b0 < a.B; b0 += NT) {
-        int held = 0;
-        int64_t need = 0;
-        if (b0 + tid < a.B) sequence(a, b0 + tid, held, need);
-        const int64_t grow = need <= a.max_pages ? max(need - held, (int64_t)0) : 0;
-        const int64_t sum = block_scan(grow, warps, total);
-        // a sequence that is refused takes nothing: the sums end before it
-        sums[tid + 1] = before + sum <= there ? sum : -1;
-        if (tid == 0) sums[0] = 0;
-        __syncthreads();
-        int n = NT;
-        if (sums[NT] < 0) {
-            int lo = 0, hi = NT;         // sums[lo] >= 0, sums[hi] < 0
+        if (!single) sum(b0);
+        int n = NT;                      // the sequences that take theirs
+        if (before + tile_grow > there) {
+            int lo = 0, hi = NT;         // grow[lo] is there, grow[hi] is not
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
-                if (sums[mid] >= 0) lo = mid; else hi = mid;
+                if (before + t.grow[mid] <= there) lo = mid; else hi = mid;
             }
-            n = lo;
+            n = before <= there ? lo : 0;
         }
-        const int64_t here = sums[n];
-        for (int64_t k = part; k < here; k += parts) {
-            const int i = owner(sums, n, k), b = b0 + i;
-            const int64_t from = there - 1 - (before + k);
-            const int h = min(max(a.held[b], 0), a.max_pages);
-            a.table[(int64_t)b * a.max_pages + h + (k - sums[i])] = from < a.n_pages ? a.free_pages[from] : -1;
-            if (from < a.n_pages) a.free_pages[from] = -1;
+        const int64_t here = t.grow[n];
+        for (int64_t k0 = part; k0 < here; k0 += U * parts) {
+            int32_t page[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t k = k0 + u * parts, from = there - 1 - (before + k);
+                page[u] = k < here && from < a.n_pages ? a.free_pages[from] : -1;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t k = k0 + u * parts, from = there - 1 - (before + k);
+                if (k >= here) break;
+                const int i = owner<NT>(t.grow, k);
+                if (from < a.n_pages) a.free_pages[from] = -1;
+                a.table[(int64_t)(b0 + i) * a.max_pages + t.held[i] + (k - t.grow[i])] = page[u];
+            }
         }
         taken += here;
-        before += total;
+        before += tile_grow;
     }
-    cluster.sync();                      // all blocks have read what changes now
-    if (cluster.block_rank() != 0) return;
+    // ---- what changed, once all blocks have read what was (a single tile: before the last meeting)
+    if (!single) meet();
+    if (rank != 0) return;
     before = 0;
     for (int b0 = 0; b0 < a.B; b0 += NT) {
+        if (!single) sum(b0);
         const int b = b0 + tid;
-        int held = 0;
-        int64_t need = 0;
-        if (b < a.B) sequence(a, b, held, need);
-        const int64_t grow = need <= a.max_pages ? max(need - held, (int64_t)0) : 0;
-        const int64_t sum = before + block_scan(grow, warps, total);
         if (b < a.B) {
-            const bool fits = need <= a.max_pages, granted = grow == 0 || sum <= there;
+            const bool fits = need <= a.max_pages, granted = grow == 0 || before + upto <= there;
             a.held[b] = fits && granted ? (int)need : held;
             a.status[b] = !fits ? FA_PAGES_TOO_LONG : granted ? FA_PAGES_OK : FA_PAGES_SHORT;
         }
-        before += total;
+        before += tile_grow;
     }
     if (tid == 0) *a.n_free = (int)min(there - taken, (int64_t)a.n_pages);
 }
@@ -161,9 +197,9 @@ __global__ void __launch_bounds__(MT) k_slot_map(MapArgs a) {
     const int tid = threadIdx.x, b0 = blockIdx.x * MT, b = b0 + tid;
     int64_t mine = 0, before, total;
     for (int i = tid; i < b0; i += MT) mine += max(a.count[i], 0);
-    block_scan(mine, warps, before);
+    block_scan(mine, warps, MT / 32, before);
     const int64_t n = b < a.B ? max(a.count[b], 0) : 0;
-    const int64_t sum = block_scan(n, warps, total);
+    const int64_t sum = block_scan(n, warps, MT / 32, total);
     sums[tid + 1] = sum;
     if (tid == 0) sums[0] = 0;
     __syncthreads();
@@ -173,7 +209,7 @@ __global__ void __launch_bounds__(MT) k_slot_map(MapArgs a) {
     }
     const int64_t end = min(total, a.N - before), step = (int64_t)gridDim.y * MT;
     for (int64_t k = (int64_t)blockIdx.y * MT + tid; k < end; k += step) {
-        const int i = owner(sums, MT, k), s = b0 + i;
+        const int i = owner<MT>(sums, k), s = b0 + i;
         const int64_t pos = a.start[s] + (k - sums[i]), page_at = pos >> a.shift, at = before + k;
         int page = -1;
         if (pos >= 0 && page_at < a.max_pages) page = a.table[(int64_t)s * a.max_pages + page_at];
@@ -211,17 +247,24 @@ extern "C" fa_status fa_pages_resize(int32_t B, int32_t max_pages, int32_t page_
     if (!want || !held || !n_free || !status || (max_pages > 0 && !page_table) || (n_pages > 0 && !free_pages))
         return fa_refuse(fn, "NULL buffer");
     const PagesArgs a{B, max_pages, shift, n_pages, want, page_table, held, free_pages, n_free, status};
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = 8;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t c = {};
-    c.gridDim = dim3(8);
-    c.blockDim = dim3(NT);
-    c.stream = (cudaStream_t)stream;
-    c.attrs = at;
-    c.numAttrs = 1;
-    (void)cudaLaunchKernelEx(&c, k_pages_resize, a);   // its error is the one the check reads
+    cudaStream_t s = (cudaStream_t)stream;
+    // One block where the tables are small: 64 sequences of up to 257 pages ONE / CLUSTER us; 256 of 528 pages, half of
+    // them given back and taken, ONE2 / CLUSTER2 us.
+    if ((int64_t)B * max_pages <= 65536) {
+        k_pages_resize<false><<<1, NT, 0, s>>>(a);
+    } else {
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = 8;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cudaLaunchConfig_t c = {};
+        c.gridDim = dim3(8);
+        c.blockDim = dim3(NT);
+        c.stream = s;
+        c.attrs = at;
+        c.numAttrs = 1;
+        (void)cudaLaunchKernelEx(&c, k_pages_resize<true>, a);   // its error is the one the check reads
+    }
     return fa_launch_check("pages resize");
 }
 
