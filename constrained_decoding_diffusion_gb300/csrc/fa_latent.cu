@@ -15,40 +15,67 @@ struct WriteArgs {
     float mscale;
 };
 
-// A warp per token: the latent part in vectors of 16 bytes of the source (one element at a time where its rows are
-// not aligned), the key part pair by pair.
-template <class T, class O, bool ALIGNED>
+// A warp takes two tokens at a time, so that all that it reads of both is under way before it stores: the latent part in
+// vectors of 16 bytes of the source, R a lane (R = 0: one element at a time, where its rows are not aligned), the key
+// part a pair a lane.  The bound is memory: a vector is read once and written once.
+template <class T, class O, int R>
 __global__ void __launch_bounds__(NT) k_latent_write(WriteArgs a) {
-    const int lane = threadIdx.x & 31;
-    const int n = (int)((blockIdx.x * (unsigned)NT + threadIdx.x) >> 5);
-    if (n >= a.N) return;
-    const int64_t at = a.slot[n];
-    if (at < 0 || at >= a.n_slots) return;
-    O *row = (O *)a.rows + at * (a.latent + a.rope);
-    const T *x = (const T *)a.x + n * a.ls, *k = (const T *)a.key + n * a.ks;
-    if constexpr (ALIGNED) {
-        constexpr int N = fa_vec<T>::N;
-        for (int c = lane; c < a.latent / N; c += 32) {
-            float f[N];
-            fa_unpack(__ldg(reinterpret_cast<const uint4 *>(x) + c), f, T());
-            if constexpr (N == 8) {
-                reinterpret_cast<uint4 *>(row)[c] = fa_pack(f, O());
+    constexpr int N = fa_vec<T>::N, U = 2, RR = R > 0 ? R : 1;
+    const int lane = threadIdx.x & 31, half = a.rope / 2, vectors = a.latent / N;
+    const int n0 = (int)((blockIdx.x * (unsigned)NT + threadIdx.x) >> 5) * U;
+    const int p = a.interleaved ? 2 * lane : lane, q = a.interleaved ? 2 * lane + 1 : lane + half;
+    int64_t at[U];
+    int pos[U];
+    uint4 v[U][RR];
+    T k0[U], k1[U];
+    const uint64_t phase = a.pos && lane < half ? __ldg(a.phase + lane) : 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int n = n0 + u;
+        at[u] = n < a.N ? a.slot[n] : -1;
+        pos[u] = a.pos && n < a.N ? __ldg(a.pos + n) : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int n = min(n0 + u, a.N - 1);
+        const T *x = (const T *)a.x + n * a.ls, *k = (const T *)a.key + n * a.ks;
+        if (R > 0)
+#pragma unroll
+            for (int r = 0; r < RR; ++r)
+                if (lane + 32 * r < vectors) v[u][r] = __ldg(reinterpret_cast<const uint4 *>(x) + lane + 32 * r);
+        if (lane < half) { k0[u] = k[p]; k1[u] = k[q]; }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (at[u] < 0 || at[u] >= a.n_slots) continue;
+        O *row = (O *)a.rows + at[u] * (a.latent + a.rope);
+        if (R > 0) {
+#pragma unroll
+            for (int r = 0; r < RR; ++r) {
+                const int c = lane + 32 * r;
+                if (c >= vectors) break;
+                float f[N];
+                fa_unpack(v[u][r], f, T());
+                if constexpr (N == 8) reinterpret_cast<uint4 *>(row)[c] = fa_pack(f, O());
+                else reinterpret_cast<uint2 *>(row)[c] = make_uint2(fa_pack2(f[0], f[1], O()), fa_pack2(f[2], f[3], O()));
+            }
+        } else {
+            const T *x = (const T *)a.x + (n0 + u) * a.ls;
+            for (int c = lane; c < a.latent; c += 32) row[c] = fa_from_f32<O>(fa_to_f32(x[c]));
+        }
+        if (lane < half) {
+            row += a.latent;
+            const float x0 = fa_to_f32(k0[u]), x1 = fa_to_f32(k1[u]);
+            if (a.pos) {
+                const float2 cs = fa_turn(pos[u], phase, a.mscale, false);
+                row[p] = fa_from_f32<O>(x0 * cs.x - x1 * cs.y);
+                row[q] = fa_from_f32<O>(x0 * cs.y + x1 * cs.x);
             } else {
-                reinterpret_cast<uint2 *>(row)[c] = make_uint2(fa_pack2(f[0], f[1], O()), fa_pack2(f[2], f[3], O()));
+                row[p] = fa_from_f32<O>(x0);
+                row[q] = fa_from_f32<O>(x1);
             }
         }
-    } else {
-        for (int c = lane; c < a.latent; c += 32) row[c] = fa_from_f32<O>(fa_to_f32(x[c]));
     }
-    row += a.latent;
-    const int half = a.rope / 2;
-    if (lane >= half) return;
-    const int p = a.interleaved ? 2 * lane : lane, q = a.interleaved ? 2 * lane + 1 : lane + half;
-    const float x0 = fa_to_f32(k[p]), x1 = fa_to_f32(k[q]);
-    float2 cs = make_float2(1.0f, 0.0f);
-    if (a.pos) cs = fa_turn(__ldg(a.pos + n), __ldg(a.phase + lane), a.mscale, false);
-    row[p] = fa_from_f32<O>(a.pos ? x0 * cs.x - x1 * cs.y : x0);
-    row[q] = fa_from_f32<O>(a.pos ? x0 * cs.y + x1 * cs.x : x1);
 }
 
 // One block per sequence.  The path's slots are looked up all at once; then its rows move, eight under
@@ -89,9 +116,12 @@ __global__ void __launch_bounds__(128) k_latent_keep(fa_cache_view c, int P, con
 
 template <class T, class O> fa_status launch_write(const WriteArgs &a, cudaStream_t s) {
     const bool aligned = !((uintptr_t)a.x & 15) && a.ls % fa_vec<T>::N == 0;
-    const unsigned blocks = (unsigned)(((int64_t)a.N * 32 + NT - 1) / NT);
-    if (aligned) k_latent_write<T, O, true><<<blocks, NT, 0, s>>>(a);
-    else k_latent_write<T, O, false><<<blocks, NT, 0, s>>>(a);
+    const unsigned blocks = (unsigned)((((int64_t)a.N + 1) / 2 * 32 + NT - 1) / NT);
+    const int each = (a.latent / fa_vec<T>::N + 31) / 32;
+    if (!aligned) k_latent_write<T, O, 0><<<blocks, NT, 0, s>>>(a);
+    else if (each == 1) k_latent_write<T, O, 1><<<blocks, NT, 0, s>>>(a);
+    else if (each == 2) k_latent_write<T, O, 2><<<blocks, NT, 0, s>>>(a);
+    else k_latent_write<T, O, 4><<<blocks, NT, 0, s>>>(a);
     return fa_launch_check("latent write");
 }
 
