@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
         return;
     }
     if (tid == 0) {
+        if (a.box_rows) asm volatile("prefetch.tensormap [%0];" ::"l"(&map) : "memory");
         for (int i = 0; i < S::NS; ++i) { mbar_init(&sh.full[i], NLOAD / 32); mbar_init(&sh.empty[i], 1); }
         for (int i = 0; i < 2; ++i) mbar_init(&sh.s_full[i], 1);
         for (int i = 0; i < 8; ++i) mbar_init(&sh.by_hand[i], 1);
@@ -188,8 +189,8 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
 #pragma unroll
                     for (int k = 0; k < TS / 16; ++k)
                         umma_ss_warp(tmem + c * RB, vd + (2 * c * GROUP + k * 2048) / 16, pd + k * 32 / 16, idesc_o, j > 0 || k > 0);
-                umma_commit_warp(&sh.pv_done);
                 umma_commit_warp(&sh.empty[use.slot]);
+                umma_commit_warp(&sh.pv_done);
                 ++use;
             }
             ++nseg;
@@ -627,8 +628,10 @@ template <int L, class T> fa_status launch(AttendArgs a, const CUtensorMap &map,
     if (st != FA_OK) return st;
     const int64_t units = (int64_t)a.B * a.blocks;
     const int rows = std::min(a.rows, RB);
-    int n = 1;                                             // as few rows a block as keep all blocks on the GPU at once
-    while (n < 8 && units * ((rows + n - 1) / n) > 8 * MAX_CTAS) n *= 2;
+    // A block has 8 / n warps for each of its n rows: as few rows as keep all blocks on the GPU at once, but not more
+    // warps than a row of an evenly cut list has parts.
+    int n = 1;
+    while (n < 8 && (units * ((rows + n - 1) / n) > 8 * MAX_CTAS || 8 / n > ctas / units)) n *= 2;
     void (*const join)(AttendArgs, int) = n == 1 ? k_latent_join<L, T, 1> : n == 2 ? k_latent_join<L, T, 2> : n == 4 ? k_latent_join<L, T, 4> : k_latent_join<L, T, 8>;
     return fa_launch_second("latent attention join", join, dim3((unsigned)units, (unsigned)((rows + n - 1) / n)), 256, 0, s, a, ctas);
 }
