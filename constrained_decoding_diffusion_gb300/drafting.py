@@ -3,8 +3,9 @@
 A drafter gives the log-probabilities of the next `depth` positions at once, as a diffusion model's
 block does.  Beams over them that stay inside the automaton become a tree of drafted tokens, one
 attention layer verifies the whole tree in a single pass over its paged cache, and the longest path
-that agrees with the layer's own choices is kept.  The text is that of choosing one token at a time;
-the draft only decides how many come from one pass.
+that agrees with the layer's own choices is kept.  The text is that of choosing one token at a time,
+the best one or a random one; the draft only decides how many come from one pass.  The sequences share a
+pool of pages: each has those that its text takes, and for the length of a pass those of its draft.
 
     python -m constrained_decoding_diffusion_gb300.drafting
 """
@@ -37,34 +38,76 @@ class Layer(NamedTuple):
                    4 * made(heads * dim, vocab, fan=heads * dim))
 
 
+class LatentLayer(NamedTuple):
+    """The same with one latent vector a token for all heads, in absorbed form: embed [V, E], wq [E, H, L + R] and
+    down [E, L + R] in a 16-bit type, and head [H * L, V] in float32.  The last R elements carry the positions."""
+    embed: torch.Tensor
+    wq: torch.Tensor
+    down: torch.Tensor
+    head: torch.Tensor
+
+    @classmethod
+    def random(cls, vocab: int, width: int, heads: int, latent: int, rope: int, seed: int = 0, dtype=torch.bfloat16):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+
+        def made(*shape, fan):
+            return torch.randn(shape, generator=g, device="cuda") * fan ** -0.5
+        return cls(made(vocab, width, fan=1).to(dtype), made(width, heads, latent + rope, fan=width).to(dtype),
+                   made(width, latent + rope, fan=width).to(dtype), 4 * made(heads * latent, vocab, fan=heads * latent))
+
+    @property
+    def latent_dim(self) -> int:
+        return self.head.shape[0] // self.wq.shape[1]
+
+
 class Drafting:
     """The text of B sequences under a DFA.  `pending` [B] is each sequence's next token, chosen but
-    not yet in the cache (-1: the sequence has ended), `state` [B] the automaton's state after it."""
+    not yet in the cache (-1: the sequence has ended), `state` [B] the automaton's state after it.
 
-    def __init__(self, aut: native.CompiledAutomaton, layer: Layer, first, start_state: int, beams: int = 4, depth: int = 4,
-                 max_length: int = 1024, page_size: int = 16, cache_dtype=torch.float8_e4m3fn):
+    With a generator tokens are drawn from the softmax of the layer's logits / temperature under the automaton,
+    else the best one is taken.  n_pages is the size of the pool (enough for all sequences and their drafts by
+    default): a sequence whose draft finds no pages sits the round out.  Texts keep their pages until release(), so
+    the pool must hold all of them and one draft, or a round comes in which nobody moves."""
+
+    def __init__(self, aut: native.CompiledAutomaton, layer, first, start_state: int, beams: int = 4, depth: int = 4,
+                 max_length: int = 1024, page_size: int = 16, cache_dtype=torch.float8_e4m3fn, n_pages=None, generator=None,
+                 temperature: float = 1.0):
         B, K = first.shape[0], beams
-        (V, _), (_, H, D), KV = layer.embed.shape, layer.wq.shape, layer.wk.shape[1]
+        (V, _), (_, H, D) = layer.embed.shape, layer.wq.shape
+        self.latent = isinstance(layer, LatentLayer)
         if depth < 1 or 1 + K * depth > lm.FA_MAX_DRAFT:
             raise ValueError("beams * depth must be in [1, %d)" % lm.FA_MAX_DRAFT)
         self.layer, self.beams, self.depth, self.max_length = layer, K, depth, max_length
         T = 1 + K * depth                                  # the pending token, then the beams, one after another
         per = -(-(max_length + T) // page_size)
         i32 = dict(dtype=torch.int32, device="cuda")
-        self.cache = lm.KVCache.empty(B * per, KV, page_size, D, cache_dtype)
-        self.table = torch.arange(B * per, **i32).view(B, per)
+        self.pages = lm.PageTables.empty(B, per, B * per if n_pages is None else n_pages, page_size)
+        self.table, n_pages = self.pages.table, self.pages.free.shape[0]
         self.length = torch.zeros(B, **i32)
-        self.phase, _ = lm.rope_phases(D)
+        if self.latent:
+            L = layer.latent_dim
+            self.cache = lm.LatentCache.empty(n_pages, page_size, L, D - L, layer.wq.dtype)
+            self.attend = lm.LatentAttention(B, T, H, L, D - L, layer.wq.dtype)
+            self.drafted = torch.full((B,), T, **i32)
+        else:
+            KV = layer.wk.shape[1]
+            self.cache = lm.KVCache.empty(n_pages, KV, page_size, D, cache_dtype)
+            self.attend = lm.TreeAttention(B, T, H, KV, D, layer.wq.dtype)
+        self.phase, _ = lm.rope_phases(D - L if self.latent else D)
         self.next, self.live = lm.fa_beam_tables(aut)
         node = torch.arange(T, **i32)
         parents = torch.where((node - 1) % depth == 0, 0, node - 1)
         parents[0] = -1
-        self.mask, self.below = lm.fa_tree_mask(parents.expand(B, T).contiguous())
-        self.attend = lm.TreeAttention(B, T, H, KV, D, layer.wq.dtype)
+        self.parents = parents.expand(B, T).contiguous()
+        self.mask, self.below = lm.fa_tree_mask(self.parents)
         self.first_beam = lm.BeamSelect(B, 1, V, K)
         self.more_beams = lm.BeamSelect(B, K, V, K)
-        self.choose = lm.BeamSelect(B * T, 1, V, 1)
-        self.nothing = torch.zeros((B * T, 1), device="cuda")
+        self.generator, self.temperature = generator, temperature
+        if generator is not None:
+            self.accept = lm.Verify(B, T, V)
+        else:
+            self.choose = lm.BeamSelect(B * T, 1, V, 1)
+            self.nothing = torch.zeros((B * T, 1), device="cuda")
         self.pending = first.to(**i32)
         self.state = self._move(torch.full((B,), start_state, **i32), self.pending)
         self.text = []                                     # [B, at most 1 + depth] of each round, -1 where there is none
@@ -86,24 +129,38 @@ class Drafting:
             hist = lm.fa_beam_reorder(hist, parent, token=token, at=t)
         return hist
 
-    def verify(self, hist):
-        """One pass over the tree; returns the tokens that join the text [B, 1 + depth]."""
-        B, K, depth = hist.shape
-        tokens = torch.cat((self.pending.view(B, 1), hist.view(B, K * depth)), 1)
-        T = tokens.shape[1]
-        count = torch.where(self.pending >= 0, T, 0).int()
+    def logits(self, tokens, count):
+        """The layer's logits [B, T, V] after the drafted tokens [B, T], of which count [B] are in use; their keys
+        and values join the cache."""
+        B, T = tokens.shape
         positions = self.length.view(B, 1) + self.below
         x = self.layer.embed[tokens.clamp(min=0).long()]
-        q, k, v = (torch.einsum("bte,ehd->bthd", x, w) for w in self.layer[1:4])
-        lm.fa_rope(q.view(B * T, *q.shape[2:]), positions.view(-1), self.phase, out=q.view(B * T, *q.shape[2:]))
-        lm.fa_cache_write(self.cache, k, v, self.table, self.length, count, positions, self.phase)
-        out, _ = self.attend(q, self.cache, self.table, self.length, self.mask, count)
-        logp = torch.log_softmax(out.float().view(B, T, -1) @ self.layer.head, -1)
+        if self.latent:
+            L, scale = self.layer.latent_dim, self.layer.wq.shape[2] ** -0.5
+            q = torch.einsum("bte,ehd->bthd", x, self.layer.wq)
+            turned = q.view(B * T, *q.shape[2:])[..., L:]
+            lm.fa_rope(turned, positions.view(-1), self.phase, out=turned)
+            down = (x @ self.layer.down).view(B * T, -1)
+            slot, _, _, _ = lm.fa_slot_map(self.pages, self.length, self.drafted, B * T)
+            lm.fa_latent_write(self.cache, down[:, :L], down[:, L:], slot, positions.view(-1), self.phase)
+            out, _ = self.attend(q, self.cache, self.table, self.length, scale, self.mask, count)
+        else:
+            q, k, v = (torch.einsum("bte,ehd->bthd", x, w) for w in self.layer[1:4])
+            lm.fa_rope(q.view(B * T, *q.shape[2:]), positions.view(-1), self.phase, out=q.view(B * T, *q.shape[2:]))
+            lm.fa_cache_write(self.cache, k, v, self.table, self.length, count, positions, self.phase)
+            out, _ = self.attend(q, self.cache, self.table, self.length, self.mask, count)
+        return out.float().view(B, T, -1) @ self.layer.head
+
+    def best(self, logits, tokens, hist):
+        """The longest path of drafted tokens that are the best ones, and what follows: (path, token, state)."""
+        B, K, depth = hist.shape
+        T = tokens.shape[1]
         # the automaton's state at every node, and the layer's choice there
         state = torch.empty((B, K, depth), dtype=torch.int32, device="cuda")
         for t in range(depth):
             state[:, :, t] = self._move(state[:, :, t - 1] if t else self.state.view(B, 1).expand(B, K), hist[:, :, t])
         state = torch.cat((self.state.view(B, 1), state.view(B, K * depth)), 1)
+        logp = torch.log_softmax(logits, -1)
         _, _, want, after = self.choose(logp.view(B * T, 1, -1), self.nothing, state.view(B * T, 1).contiguous(), self.next, self.live)
         want, after = want.view(B, T), after.view(B, T)
         # a beam's tokens are kept while each is the choice at the node before
@@ -113,17 +170,42 @@ class Drafting:
         kept, beam = same.int().cumprod(-1).sum(-1).max(1)
         path = torch.where(torch.arange(depth, device="cuda") < kept.view(B, 1), 1 + beam.view(B, 1) * depth + torch.arange(depth, device="cuda"), -1)
         path = torch.cat((torch.zeros((B, 1), dtype=path.dtype, device="cuda"), path), 1)
-        path = torch.where(self.pending.view(B, 1) >= 0, path, -1).int()
-        lm.fa_cache_keep(self.cache, self.table, self.length, path)
-        joined = torch.where(path >= 0, tokens.gather(1, path.clamp(min=0).long()), -1)
-        last = path.max(1, keepdim=True).values.clamp(min=0).long()
+        last = path.max(1, keepdim=True).values
+        return path, want.gather(1, last).view(B), after.gather(1, last).view(B)
+
+    def drawn(self, logits, tokens, count):
+        """The same with tokens drawn at random: the draft is kept as far as the draws agree with it."""
+        u = torch.rand(tokens.shape, generator=self.generator, device="cuda")
+        path, _, token, state = self.accept(torch.softmax(logits / self.temperature, -1), tokens, self.parents, u, count=count,
+                                            states=self.state, next=self.next, live=self.live)
+        return path[:, :1 + self.depth], token, state
+
+    def verify(self, hist):
+        """One pass over the tree; returns the tokens that join the text [B, 1 + depth]."""
+        B, K, depth = hist.shape
+        tokens = torch.cat((self.pending.view(B, 1), hist.view(B, K * depth)), 1)
+        T = tokens.shape[1]
         alive = self.pending >= 0
+        room = lm.fa_pages_resize(self.pages, self.length + T * alive.int())
+        alive &= room == lm.FA_PAGES_OK
+        count = torch.where(alive, T, 0).int()
+        logits = self.logits(tokens, count)
+        path, token, after = self.best(logits, tokens, hist) if self.generator is None else self.drawn(logits, tokens, count)
+        path = torch.where(alive.view(B, 1), path, -1).int()
+        (lm.fa_latent_keep if self.latent else lm.fa_cache_keep)(self.cache, self.table, self.length, path)
+        joined = torch.where(path >= 0, tokens.gather(1, path.clamp(min=0).long()), -1)
         self.length += (path >= 0).sum(1).int()
-        alive &= self.length < self.max_length
-        self.state = torch.where(alive, after.gather(1, last).view(B), -1)
-        self.pending = torch.where(alive, want.gather(1, last).view(B), -1)
+        lm.fa_pages_resize(self.pages, self.length)
+        done = alive & (self.length >= self.max_length)
+        self.state = torch.where(done, -1, torch.where(alive, after, self.state))
+        self.pending = torch.where(done, -1, torch.where(alive, token, self.pending))
         self.text.append(joined)
         return joined
+
+    def release(self):
+        """The pages of sequences that have ended go back to the pool, and their texts leave the cache."""
+        self.length = torch.where(self.pending >= 0, self.length, 0)
+        lm.fa_pages_resize(self.pages, self.length)
 
     def round(self, drafter):
         """drafter(pending [B]) -> log-probabilities [B, depth, V] of the positions after pending."""
