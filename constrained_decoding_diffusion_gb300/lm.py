@@ -437,29 +437,45 @@ class PageTables(NamedTuple):
 def fa_pages_resize(pages: PageTables, want, status=None, stream=None):
     """Give every sequence the pages of want [B] slots, from the pool and back to it, in place: status [B]."""
     table, held, free, n_free, size = pages
+    i32 = torch.int32
     B, P = table.shape
+    n = free.shape[0]
+    row = (B,)
+    at = _ptr(want, i32, "want", row)
     if status is None:
-        status = _new((B,), torch.int32, table.device, stream)
-    _check(_lib().fa_pages_resize(
-        B, P, size, free.shape[0], _ptr(want, torch.int32, "want", (B,)), _ptr(table, torch.int32, "table", (B, P)),
-        _ptr(held, torch.int32, "held", (B,)), _ptr(free, torch.int32, "free", (free.shape[0],)),
-        _ptr(n_free, torch.int32, "n_free", (1,)), _ptr(status, torch.int32, "status", (B,)), _stream(stream, table)))
+        status = torch.empty_like(want) if stream is None else _new(row, i32, table.device, stream)
+        to = status.data_ptr()
+    else:
+        to = _ptr(status, i32, "status", row)
+    rc = _lib().fa_pages_resize(B, P, size, n, at, _ptr(table, i32, "table", (B, P)), _ptr(held, i32, "held", row),
+                                _ptr(free, i32, "free", (n,)), _ptr(n_free, i32, "n_free", (1,)), to, _stream(stream, table))
+    if rc:
+        _check(rc)
     return status
 
 
 def fa_slot_map(pages: PageTables, start, count, N: int, out=None, stream=None):
     """Where the tokens start[b] .. start[b] + count[b] - 1 of every sequence go, packed one sequence after another:
     (slot [N], seq [N], position [N], offset [B + 1])."""
-    table = pages.table
+    table, _, free, _, size = pages
+    i32 = torch.int32
     B, P = table.shape
+    row = (B,)
+    begin, n, where = _ptr(start, i32, "start", row), _ptr(count, i32, "count", row), _ptr(table, i32, "table", (B, P))
     if out is None:
-        out = [_new((n,), torch.int32, table.device, stream) for n in (N, N, N, B + 1)]
-    slot, seq, position, offset = out
-    _check(_lib().fa_slot_map(
-        B, N, pages.page_size, pages.free.shape[0], _ptr(table, torch.int32, "table", (B, P)), P,
-        _ptr(start, torch.int32, "start", (B,)), _ptr(count, torch.int32, "count", (B,)),
-        _ptr(slot, torch.int32, "slot", (N,)), _ptr(seq, torch.int32, "seq", (N,)),
-        _ptr(position, torch.int32, "position", (N,)), _ptr(offset, torch.int32, "offset", (B + 1,)), _stream(stream, table)))
+        slot = _new((N,), i32, table.device, stream)
+        if stream is None:
+            seq, position, offset = torch.empty_like(slot), torch.empty_like(slot), torch.empty((B + 1,), dtype=i32, device=table.device)
+        else:
+            seq, position, offset = (_new((m,), i32, table.device, stream) for m in (N, N, B + 1))
+        to = slot.data_ptr(), seq.data_ptr(), position.data_ptr(), offset.data_ptr()
+    else:
+        slot, seq, position, offset = out
+        to = (_ptr(slot, i32, "slot", (N,)), _ptr(seq, i32, "seq", (N,)), _ptr(position, i32, "position", (N,)),
+              _ptr(offset, i32, "offset", (B + 1,)))
+    rc = _lib().fa_slot_map(B, N, size, free.shape[0], where, P, begin, n, *to, _stream(stream, table))
+    if rc:
+        _check(rc)
     return slot, seq, position, offset
 
 

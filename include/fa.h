@@ -722,7 +722,8 @@ fa_status fa_latent_attention(const fa_latent_cache *cache, int32_t dtype, int32
  * barrier that nothing completes.  The wait runs out, every CTA of the launch abandons its
  * tile after the copies and products it already issued have completed, and the step reports
  * FA_ROW_TIMEOUT for every sequence; the next step is unaffected.  A launch of fa_tree_attention with more
- * than 16 rows takes its turn likewise, in its first block: the rows that block has a part in are NaN.  n_launches = 0 disarms.
+ * than 16 rows, or of fa_latent_attention, takes its turn likewise, in its first block: the rows that block has a part in
+ * are NaN.  n_launches = 0 disarms.
  * Process-wide.  Errors: FA_ERR_INVALID_ARG (n_launches < 0).
  */
 fa_status fa_debug_inject_wait_timeouts(int32_t n_launches);

@@ -141,6 +141,20 @@ def test_rows_without_weight(draft):
     assert token[0] == -1 and kept[0] == 1
 
 
+@pytest.mark.parametrize("draft", [True, False])
+@pytest.mark.parametrize("V", [50, 9001])
+def test_sums_beyond_fp32(draft, V):
+    """A target row whose sum leaves fp32 has no token; a draft row whose sum does accepts nothing that the target's lacks,
+    and its sequence still ends with a token."""
+    d = make(19, 3, chain(3), V, draft=draft)
+    d["target"][0, 0] = 3e38
+    if draft:
+        d["draft"][1] = 3e38
+    path, kept, token, _ = lm.Verify(3, 3, V)(**d)
+    assert token[0] == -1 and kept[0] == 1 and path[0].tolist() == [0, -1, -1]
+    assert ((token[1:] >= 0) & (token[1:] < V)).all() and ((kept[1:] >= 1) & (kept[1:] <= 3)).all()
+
+
 def test_states_outside_and_dead():
     d = make(10, 6, chain(4), 700, states=4)
     d["states"] = torch.tensor([-1, 4, 0, 1, 2, 3], dtype=torch.int32).cuda()
