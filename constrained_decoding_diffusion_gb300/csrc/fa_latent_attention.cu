@@ -97,7 +97,8 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
     static_assert(S::MISC % 8 == 0 && sizeof(Misc) % 4 == 0, "alignment of the parts");
     Misc &sh = *reinterpret_cast<Misc *>(smem + S::MISC);
     Work &work = *reinterpret_cast<Work *>(smem + S::MISC + sizeof(Misc));
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // (the warp's number by way of a shuffle: its roles' code is then known to run in step)
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     constexpr bool F16 = std::is_same<T, __half>::value;
     constexpr float OFF = F16 ? 8.0f : 0.0f;      // fp16 weights reach from 2^14 down to 2^-24, with 2^8 for the reference
     const int D = a.c.head_dim;
