@@ -32,15 +32,20 @@ constexpr int GROUP = 64 * 128;              // 64 rows of 64 columns, 128-byte 
 constexpr int kUnitCost = 2;                 // what starting a unit costs, in tiles
 
 template <int L> struct Shape {
-    static constexpr int G = L / 64 + 1, TILE = G * GROUP;                        // the key part pads to 64 columns
-    static constexpr int NS = L == 128 ? 6 : L == 256 ? 4 : 2;                    // tiles in the ring
-    static constexpr int Q = 0, RING = TILE, P = RING + NS * TILE, MISC = P + RB * 128;
+    // A tile's latent columns lie in one of NS places, its key part (padded to 64 columns), which only the scores need,
+    // in one of NK.  A single place is filled while the next tile's scores over the latent columns are computed, and has
+    // barriers of its own.
+    static constexpr int G = L / 64 + 1, TILE = (G - 1) * GROUP;
+    static constexpr int NS = L == 128 ? 6 : L == 256 ? 4 : L == 384 ? 3 : 2, NK = L < 384 ? NS : 1;
+    static constexpr int Q = 0, RING = G * GROUP, KEYS = RING + NS * TILE, P = KEYS + NK * GROUP, MISC = P + 2 * RB * 128;
 };
 
 struct Misc {
-    uint64_t full[6], empty[6], s_full[2], by_hand[8], p_full, pv_done, q_full, q_free, o_free, done;
-    uint32_t there[6][2], odd[6][2];   // per place of the ring: slots that a page holds; (by hand) those with an element that is not finite
-    float factor[2][RB], inverse[2][RB];
+    uint64_t full[6], empty[6], s_full[2], by_hand[8], p_full[2], pv_done[2], keys_full, keys_used, q_full, q_free, o_free, done;
+    uint32_t there[6][2];              // per place of the ring: slots that a page holds
+    uint8_t odd[6][8];                 // (by hand) bit k of byte w: slot w + 8 k, which loading warp w brought, holds an element that is not finite
+    alignas(16) float factor[2][RB];   // read four at a time
+    alignas(16) float inverse[2][RB];
     uint32_t tmem;
     int fail;
 };
@@ -94,7 +99,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
     using S = Shape<L>;
     constexpr int G = S::G;
     extern __shared__ __align__(1024) unsigned char smem[];
-    static_assert(S::MISC % 8 == 0 && sizeof(Misc) % 4 == 0, "alignment of the parts");
+    static_assert(S::MISC % 16 == 0 && alignof(Misc) == 16 && sizeof(Misc) % alignof(Work) == 0, "alignment of the parts");
     Misc &sh = *reinterpret_cast<Misc *>(smem + S::MISC);
     Work &work = *reinterpret_cast<Work *>(smem + S::MISC + sizeof(Misc));
     // (the warp's number by way of a shuffle: its roles' code is then known to run in step)
@@ -112,8 +117,9 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
         for (int i = 0; i < S::NS; ++i) { mbar_init(&sh.full[i], NLOAD / 32); mbar_init(&sh.empty[i], 1); }
         for (int i = 0; i < 2; ++i) mbar_init(&sh.s_full[i], 1);
         for (int i = 0; i < 8; ++i) mbar_init(&sh.by_hand[i], 1);
-        mbar_init(&sh.p_full, 4);
-        mbar_init(&sh.pv_done, 1);
+        for (int i = 0; i < 2; ++i) { mbar_init(&sh.p_full[i], 4); mbar_init(&sh.pv_done[i], 1); }
+        mbar_init(&sh.keys_full, NLOAD / 32);
+        mbar_init(&sh.keys_used, 1);
         mbar_init(&sh.q_full, NLOAD / 32);
         mbar_init(&sh.q_free, 1);
         mbar_init(&sh.o_free, 4);
@@ -129,7 +135,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
     fa_let_next_start();
     plan(a, work);
     tc_fence_after();
-    const uint32_t tmem = sh.tmem, ring = smem_u32(smem + S::RING);
+    const uint32_t tmem = sh.tmem, ring = smem_u32(smem + S::RING), keys = smem_u32(smem + S::KEYS);
     Walk walk(a, work, blockIdx.x, gridDim.x);
     Segment s;
 
@@ -139,7 +145,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
         constexpr uint32_t idesc_s = idesc | (uint32_t)(RB >> 4) << 24 | (uint32_t)(TS >> 3) << 17;
         const uint64_t qd = umma_desc(smem_u32(smem + S::Q), 16), pd = umma_desc(smem_u32(smem + S::P), 16);
         Ring<S::NS> get, use;                     // the next tile's place for scores, and for values
-        uint32_t ns = 0, np = 0, nseg = 0;
+        uint32_t ns = 0, np = 0, nseg = 0, tiles = 0;
         const int last_steps = (D - L) / 16;
         if (a.inject && blockIdx.x == 0) {        // a failure test: only this warp completes `done`, later
             const long long t0 = clock64();
@@ -151,15 +157,24 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
         // offsets reach the instruction by way of ordinary registers, and the issue takes twice as long as the product)
         auto scores = [&]() {
             tc_fence_after();
-            const uint64_t kd = umma_desc(ring + get.slot * S::TILE, 16);
+            const uint64_t cd = umma_desc(ring + get.slot * S::TILE, 16), kd = umma_desc(keys + (S::NK == 1 ? 0 : get.slot) * GROUP, 16);
             const uint32_t d = tmem + 256 + (ns & 1) * TS;
 #pragma unroll
-            for (int k = 0; k < 4 * G; ++k) {
-                if (k >= L / 16 && k - L / 16 >= last_steps) break;
+            for (int k = 0; k < L / 16; ++k) {
                 const uint32_t off = ((k >> 2) * GROUP + (k & 3) * 32) / 16;
-                umma_ss_warp(d, qd + off, kd + off, idesc_s, k > 0);
+                umma_ss_warp(d, qd + off, cd + off, idesc_s, k > 0);
             }
+            if (S::NK < S::NS) {                           // (should the wait run out, what is there is as good as anything)
+                mbar_wait(&sh.keys_full, tiles & 1, fail);
+                __syncwarp();
+                ++tiles;
+                tc_fence_after();
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (k < last_steps) umma_ss_warp(d, qd + ((G - 1) * GROUP + k * 32) / 16, kd + k * 32 / 16, idesc_s, 1);
             umma_commit_warp(&sh.s_full[ns & 1]);
+            if (S::NK < S::NS) umma_commit_warp(&sh.keys_used);
             ++ns;
             ++get;
         };
@@ -177,11 +192,11 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
                         scores();
                         if (++issued == s.n) umma_commit_warp(&sh.q_free);
                     }
-                    if (issued > j && __all_sync(0xffffffffu, mbar_test(&sh.p_full, np & 1))) break;
+                    if (issued > j && __all_sync(0xffffffffu, mbar_test(&sh.p_full[np & 1], np >> 1 & 1))) break;
                     if (__any_sync(0xffffffffu, *fail || clock64() - t0 > kSpinCycles)) { *fail = 1; ok = false; break; }
                 }
                 if (!ok) break;
-                ++np;
+                const uint64_t pj = pd + (np & 1) * (RB * 128 / 16);
                 if (j == 0 && nseg > 0 && !__all_sync(0xffffffffu, mbar_wait(&sh.o_free, (nseg - 1) & 1, fail))) { ok = false; break; }
                 tc_fence_after();
                 const uint64_t vd = umma_desc(ring + use.slot * S::TILE, GROUP);
@@ -189,9 +204,10 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
                 for (int c = 0; c < L / 128; ++c)
 #pragma unroll
                     for (int k = 0; k < TS / 16; ++k)
-                        umma_ss_warp(tmem + c * RB, vd + (2 * c * GROUP + k * 2048) / 16, pd + k * 32 / 16, idesc_o, j > 0 || k > 0);
+                        umma_ss_warp(tmem + c * RB, vd + (2 * c * GROUP + k * 2048) / 16, pj + k * 32 / 16, idesc_o, j > 0 || k > 0);
                 umma_commit_warp(&sh.empty[use.slot]);
-                umma_commit_warp(&sh.pv_done);
+                umma_commit_warp(&sh.pv_done[np & 1]);
+                ++np;
                 ++use;
             }
             ++nseg;
@@ -208,7 +224,9 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
         const uint32_t in_page = (1u << a.c.page_shift) - 1;
         Ring<S::NS> put;
         bool again = false, ok = true;
-        uint32_t hand = 0, copied = 0, copied_phase = 0;   // bit i: place i's last tile came by copies, and its phase
+        bool keys_copied = false;
+        uint32_t keys_phase = 0;
+        uint32_t hand = 0, tile = 0, copied = 0, copied_phase = 0;   // bit i: place i's last tile came by copies, and its phase
         while (ok && walk.next(a, s)) {
             const int32_t *pages = a.c.page_table + (int64_t)s.b * a.c.max_pages;
             for (int j = 0; j < s.n; ++j) {
@@ -216,8 +234,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
                 const uint32_t first = (uint32_t)(s.t0 + j) * TS + mine * box;
                 uint32_t page = 0;
                 if (!hand_tile) page = (uint32_t)__ldg(pages + (first >> a.c.page_shift));
-                if (again && !mbar_wait(&sh.empty[put.slot], put.phase ^ 1, fail)) { ok = false; break; }
-                __syncwarp();
+                if (again && !__all_sync(0xffffffffu, mbar_wait(&sh.empty[put.slot], put.phase ^ 1, fail))) { ok = false; break; }
                 if (!hand_tile) {
                     const bool held = page < (uint32_t)a.c.n_pages;
                     const uint32_t all = __ballot_sync(0xffffffffu, held);
@@ -228,28 +245,44 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
                                 if (!(all >> i & 1)) there &= ~((box == 64 ? ~0ull : (1ull << box) - 1) << (i * box));
                         sh.there[put.slot][0] = (uint32_t)there;
                         sh.there[put.slot][1] = (uint32_t)(there >> 32);
-                        mbar_expect(&sh.full[put.slot], S::TILE);
+                        mbar_expect(&sh.full[put.slot], S::NK < S::NS ? S::TILE : S::TILE + GROUP);
                     }
                     __syncwarp();
                     if (lane > 0 && lane < NLOAD / 32) mbar_arrive(&sh.full[put.slot]);
                     const int y = held ? (int)((page << a.c.page_shift) + (first & in_page)) : a.c.n_pages << a.c.page_shift;   // past the end: zeros
-                    const uint32_t dst = ring + put.slot * S::TILE;
+                    const uint32_t dst = ring + put.slot * S::TILE, key = keys + (S::NK == 1 ? 0 : put.slot) * GROUP;
                     for (int i = 0; i < boxes; ++i) {
                         const int yi = __shfl_sync(0xffffffffu, y, i);
 #pragma unroll
-                        for (int g = 0; g < G; ++g)
+                        for (int g = 0; g < G - 1; ++g)
                             tensor_copy_warp(dst + g * GROUP + i * box * 128, &map, g * 64, yi, &sh.full[put.slot]);
                     }
+                    // (should the wait run out the tile still comes whole, so that its copies can be waited for)
+                    uint64_t *const bar = S::NK < S::NS ? &sh.keys_full : &sh.full[put.slot];
+                    if (S::NK < S::NS) {
+                        if (tile > 0) ok = __all_sync(0xffffffffu, mbar_wait(&sh.keys_used, (tile - 1) & 1, fail));
+                        if (lane == 0) mbar_expect(bar, GROUP);
+                        else if (lane < NLOAD / 32) mbar_arrive(bar);
+                    }
+                    __syncwarp();
+                    for (int i = 0; i < boxes; ++i)
+                        tensor_copy_warp(key + i * box * 128, &map, L, __shfl_sync(0xffffffffu, y, i), bar);
+                    keys_copied = true;
+                    keys_phase = tile & 1;
                     copied |= 1u << put.slot;
                     copied_phase = (copied_phase & ~(1u << put.slot)) | put.phase << put.slot;
                 } else {
+                    if (S::NK < S::NS && tile > 0 && !__all_sync(0xffffffffu, mbar_wait(&sh.keys_used, (tile - 1) & 1, fail))) { ok = false; break; }
                     // at most NS tiles are under way, so the loading warps are never 8 behind
                     if (lane == 0) mbar_arrive(&sh.by_hand[hand & 7]);
                     ++hand;
                     copied &= ~(1u << put.slot);           // the place is free: its last copy has landed
+                    keys_copied = false;
                 }
                 ++put;
+                ++tile;
                 again |= put.slot == 0;
+                if (!ok) break;
             }
         }
         // no copy may land after the block has gone
@@ -258,6 +291,10 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
                 const long long t0 = clock64();
                 while (!mbar_try_wait(&sh.full[i], copied_phase >> i & 1) && clock64() - t0 < kSpinCycles) {}
             }
+        if (S::NK < S::NS && keys_copied) {
+            const long long t0 = clock64();
+            while (!mbar_try_wait(&sh.keys_full, keys_phase) && clock64() - t0 < kSpinCycles) {}
+        }
     } else if (warp > 5) {
         // ---- queries, and tiles by hand
         // A warp has every eighth row, its lanes the row's chunks.
@@ -298,7 +335,9 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
                 }
                 if (!mbar_wait(&sh.by_hand[hand & 7], hand >> 3 & 1, fail)) { ok = false; break; }
                 ++hand;
-                const uint32_t dst = ring + put.slot * S::TILE;
+                // where a row's chunk goes: the latent columns' place, or the key part's
+                const uint32_t dst = S::RING + put.slot * S::TILE, key = S::KEYS + (S::NK == 1 ? 0 : put.slot) * GROUP;
+                auto place = [&](int r, int ch) { return ch < (G - 1) * 8 ? dst + chunk_at(r, ch) : key + chunk_at(r, ch - (G - 1) * 8); };
 #pragma unroll
                 for (int k = 0; k < MINE; ++k) {
                     const T *src = (const T *)a.c.k + (row[k] >= 0 ? row[k] * D : 0);
@@ -306,7 +345,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
                     for (int i = 0; i < LANES; ++i) {
                         const int ch = lane + 32 * i;
                         const bool there = row[k] >= 0 && ch * 8 < D;
-                        if (ch < CPR) cp_async16(dst + chunk_at(lw + 8 * k, ch), src + (there ? ch * 8 : 0), there);
+                        if (ch < CPR) cp_async16(smem_u32(smem) + place(lw + 8 * k, ch), src + (there ? ch * 8 : 0), there);
                     }
                 }
                 cp_commit();
@@ -316,31 +355,32 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
                         const uint32_t t = first + 32 * h + lane;
                         const bool there = t < (uint32_t)s.end && at.page(t) < at.n_pages;
                         const uint32_t bits = __ballot_sync(0xffffffffu, there);
-                        if (lane == 0) { sh.there[put.slot][h] = bits; sh.odd[put.slot][h] = 0; }
+                        if (lane == 0) sh.there[put.slot][h] = bits;
                     }
                 }
                 cp_wait<0>();
-                if (draft) {
-                    // drafted elements that are not finite are left out, and their slots marked
-                    bar_sync(2, NLOAD);                    // the marks have been cleared
+                // drafted elements that are not finite are left out, and their slots marked
+                uint32_t marks = 0;
+                if (draft)
 #pragma unroll 1
                     for (int k = 0; k < MINE; ++k) {
                         const int r = lw + 8 * k;
-                        if (first + r < (uint32_t)s.slots || first + r >= (uint32_t)s.end) continue;
                         bool odd = false;
+                        if (first + r >= (uint32_t)s.slots && first + r < (uint32_t)s.end)
 #pragma unroll
-                        for (int i = 0; i < LANES; ++i) {
-                            const int ch = lane + 32 * i;
-                            if (ch >= CPR) continue;
-                            uint4 *v = reinterpret_cast<uint4 *>(smem + S::RING + put.slot * S::TILE + chunk_at(r, ch));
-                            uint4 x = *v;
-                            if (zero_odd<T>(x)) { *v = x; odd = true; }
-                        }
-                        if (__any_sync(0xffffffffu, odd) && lane == 0) atomicOr(&sh.odd[put.slot][r >> 5], 1u << (r & 31));
+                            for (int i = 0; i < LANES; ++i) {
+                                const int ch = lane + 32 * i;
+                                if (ch >= CPR) continue;
+                                uint4 *v = reinterpret_cast<uint4 *>(smem + place(r, ch));
+                                uint4 x = *v;
+                                if (zero_odd<T>(x)) { *v = x; odd = true; }
+                            }
+                        marks |= (uint32_t)__any_sync(0xffffffffu, odd) << k;
                     }
-                }
+                if (lane == 0) sh.odd[put.slot][lw] = (uint8_t)marks;
                 proxy_fence();
                 warp_arrive(&sh.full[put.slot]);
+                if (S::NK < S::NS) warp_arrive(&sh.keys_full);
             }
         }
     } else {
@@ -350,7 +390,9 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
         const float c = a.scale * kLog2e;
         unsigned char *const p_at = smem + S::P + r0 * 128 + (lane & 3) * 4;
         Ring<S::NS> get;
-        uint32_t tiles = 0, npv = 0, nseg = 0;
+        uint32_t tiles = 0, nseg = 0;
+        // tile t's product with the values is done (asked for no later than two tiles after)
+        auto done = [&](uint32_t t) { mbar_wait(&sh.pv_done[t & 1], t >> 1 & 1, fail); };
         while (walk.next(a, s)) {
             const int rows = min(a.rows - RB * s.block, RB);
             int ti[2];
@@ -373,17 +415,19 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
                 const bool hand = by_hand(a, s, j);
                 const uint32_t there0 = sh.there[get.slot][0], there1 = sh.there[get.slot][1];
                 if (hand || (there0 & there1) != 0xffffffffu) {
+                    uint32_t marks[2] = {0, 0};
+                    if (hand)
+                        for (int w = 0; w < 8; ++w)
+                            if (const uint32_t bits = sh.odd[get.slot][w])
+                                for (int k = 0; k < 8; ++k) marks[k >> 2] |= (bits >> k & 1) << (w + 8 * (k & 3));
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
-                        uint32_t see[2] = {0, 0}, odd[2] = {0, 0};
+                        uint32_t see[2] = {0, 0};
                         if (used[q]) {
                             see[0] = there0 & seen_bits(a, s, ti[q], first);
                             see[1] = there1 & seen_bits(a, s, ti[q], first + 32);
                         }
-                        if (hand) {
-                            odd[0] = see[0] & sh.odd[get.slot][0];
-                            odd[1] = see[1] & sh.odd[get.slot][1];
-                        }
+                        const uint32_t odd[2] = {see[0] & marks[0], see[1] & marks[1]};
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -428,8 +472,9 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
                         sh.factor[tiles & 1][r0 + 8] = f[1];
                     }
                     scale_now = any_warp(grow);
-                    // the accumulator and the weights' place are free
-                    mbar_wait(&sh.pv_done, npv++ & 1, fail);
+                    // the weights' place is free, and the accumulator, if it is to be scaled
+                    if (scale_now) done(tiles - 1);
+                    else if (j > 1) done(tiles - 2);
                     __syncwarp();
                     tc_fence_after();
                 }
@@ -451,13 +496,13 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    unsigned char *at = p_at + ((i ^ (lane >> 2)) << 4);
+                    unsigned char *at = p_at + (tiles & 1) * (RB * 128) + ((i ^ (lane >> 2)) << 4);
                     *reinterpret_cast<uint32_t *>(at) = fa_pack2(x[4 * i], x[4 * i + 1], T());
                     *reinterpret_cast<uint32_t *>(at + 8 * 128) = fa_pack2(x[4 * i + 2], x[4 * i + 3], T());
                 }
                 proxy_fence();
                 tc_fence_before();
-                warp_arrive(&sh.p_full);
+                warp_arrive(&sh.p_full[tiles & 1]);
                 ++tiles;
                 ++get;
             }
@@ -480,7 +525,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
                     }
                 }
             }
-            mbar_wait(&sh.pv_done, npv++ & 1, fail);
+            done(tiles - 1);
             bar_sync(1, 128);
             tc_fence_after();
             auto store = [&](auto *out) {
