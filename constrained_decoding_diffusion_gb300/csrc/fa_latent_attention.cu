@@ -29,7 +29,10 @@ namespace {
 constexpr int TS = 64, RB = 64;              // slots of a tile, rows of a block
 constexpr int NLOAD = 8 * 32, NTHR = 14 * 32;
 constexpr int GROUP = 64 * 128;              // 64 rows of 64 columns, 128-byte swizzled
-constexpr int kUnitCost = 2;                 // what starting a unit costs, in tiles
+// What a unit costs besides its tiles, in tiles: its queries, its tiles by hand (whose masks are looked up where several
+// tokens are drafted) and its result.  Without it / 2 / 4 / 6 / 8: 32 ragged sequences of up to 8192 slots x 32 rows
+// 52.8 / 48.8 / 48.8 / 50.4 / 50.3 us, 16 ragged ones of up to 4096 x 1024 rows of 32 tokens 273 / 201 / 142 / 133 / 130.
+constexpr int kUnitCost = 4, kDraftCost = 3;
 
 template <int L> struct Shape {
     // A tile's latent columns lie in one of NS places, its key part (padded to 64 columns), which only the scores need,
@@ -362,7 +365,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
                 // drafted elements that are not finite are left out, and their slots marked
                 uint32_t marks = 0;
                 if (draft)
-#pragma unroll 1
+#pragma unroll 4
                     for (int k = 0; k < MINE; ++k) {
                         const int r = lw + 8 * k;
                         bool odd = false;
@@ -726,7 +729,7 @@ extern "C" fa_status fa_latent_attention(const fa_latent_cache *cache, int32_t d
     if (slots > 2147483647LL - 4096) return fa_refuse(fn, "max_pages * page_size out of range");
     a.rows = T * heads;
     a.blocks = (a.rows + RB - 1) / RB;
-    if ((int64_t)B * a.blocks > 2147483647 || (int64_t)B * a.blocks * ((slots + TS - 1) / TS + 5) > 2147483647)
+    if ((int64_t)B * a.blocks > 2147483647 || (int64_t)B * a.blocks * ((slots + TS - 1) / TS + 8) > 2147483647)
         return fa_refuse(fn, "B * row blocks * tiles out of range");
     if (B == 0 || T == 0) return FA_OK;
     if (!q || !out || !length) return fa_refuse(fn, "NULL buffer");
@@ -743,7 +746,7 @@ extern "C" fa_status fa_latent_attention(const fa_latent_cache *cache, int32_t d
     a.part_lse = a.part_o + (size_t)MAX_CTAS * 2 * RB * cache->latent_dim;
     a.status = (int *)(a.part_lse + (size_t)MAX_CTAS * 2 * RB);
     a.tile_shift = 6;
-    a.unit_cost = kUnitCost;
+    a.unit_cost = kUnitCost + (T > 1 ? kDraftCost : 0);
     CUtensorMap map = {};
     const int box_rows = std::min(cache->page_size, TS);
     a.box_rows = make_map(cache, box_rows, &map) ? box_rows : 0;
