@@ -1,6 +1,7 @@
 """The model-side operators of libfa.so (include/fa.h) on torch tensors: rotary positions, a
-paged and quantised key/value cache, attention of drafted tokens over it, and beam selection
-under an automaton.
+paged and quantised key/value cache, attention of drafted tokens over it, beam selection
+under an automaton, verification of drafted tokens, pages handed out on the device, and a paged
+cache of latent vectors with the attention over it.
 
 Like `native`, this module only checks and marshals tensors; every operator runs in the
 library's CUDA kernels on torch's current stream (or the one given).  Tensors must live on the
