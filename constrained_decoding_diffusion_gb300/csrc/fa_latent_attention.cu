@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
         uint32_t nseg = 0, hand = 0;
         bool ok = true;
         while (ok && walk.next(a, s)) {
-            if (nseg > 0 && !mbar_wait(&sh.q_free, (nseg - 1) & 1, fail)) break;
+            if (nseg > 0 && !__all_sync(0xffffffffu, mbar_wait(&sh.q_free, (nseg - 1) & 1, fail))) break;
             const int rows = min(a.rows - RB * s.block, RB);   // (what the others' places hold is of no account)
             const uint32_t q_at = smem_u32(smem + S::Q);
 #pragma unroll 2
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
                     const uint32_t t = first + lw + 8 * k;
                     row[k] = t < (uint32_t)s.end ? at.row(t) : -1;
                 }
-                if (!mbar_wait(&sh.by_hand[hand & 7], hand >> 3 & 1, fail)) { ok = false; break; }
+                if (!__all_sync(0xffffffffu, mbar_wait(&sh.by_hand[hand & 7], hand >> 3 & 1, fail))) { ok = false; break; }
                 ++hand;
                 // where a row's chunk goes: the latent columns' place, or the key part's
                 const uint32_t dst = S::RING + put.slot * S::TILE, key = S::KEYS + (S::NK == 1 ? 0 : put.slot) * GROUP;
@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                     f[q] = 1.0f;
-                    if ((top - m[q]) * c > kGrow) {                         // (not where both are -inf)
+                    if (r0 + 8 * q < rows && (top - m[q]) * c > kGrow) {   // (not where both are -inf)
                         f[q] = ex2((m[q] - top) * c);
                         m[q] = top;
                         grow = true;

@@ -322,6 +322,8 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     Shared *first = cluster.map_shared_rank(&sh, 0);
     const int use = a.count ? min(max(a.count[b], 0), a.T) : a.T;
+    // (waited for before the first store to another block, which has to have started)
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     if (rank == 0)
         for (int j = tid; j < a.T; j += NT) {
             parent[j] = a.parents[(int64_t)b * a.T + j];
@@ -340,6 +342,7 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
     Node<T, DRAFT> at;
     at.words = a.words;
     __syncthreads();
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     while (true) {
         // (nothing that a block reads for itself decides how often the cluster meets)
         const bool any = use > 0 && (!a.S || (unsigned)state < (unsigned)a.S);
