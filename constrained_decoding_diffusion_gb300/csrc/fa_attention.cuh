@@ -112,12 +112,8 @@ __device__ __forceinline__ void plan(const AttendArgs &a, Work &w) {
     __syncthreads();
 }
 
-// the first place of run c, of `total` places over `ctas` runs: total * c / ctas, without a 64-bit division (the rest
-// of total / ctas times c stays below the square of the number of runs)
-__device__ __forceinline__ int run_start(int total, int c, int ctas) {
-    const int q = total / ctas, r = total - q * ctas;
-    return q * c + r * c / ctas;
-}
+// the first place of run c, of `total` places over `ctas` runs
+__device__ __forceinline__ int run_start(int total, int c, int ctas) { return (int)((int64_t)total * c / ctas); }
 
 struct Segment {
     int b, head, block;       // the unit
