@@ -51,13 +51,17 @@ constexpr int GROUP = 64 * 128;              // 64 rows of 64 columns, 128-byte 
 // 52.8 / 48.8 / 48.8 / 50.4 / 50.3 us, 16 ragged ones of up to 4096 x 1024 rows of 32 tokens 273 / 201 / 142 / 133 / 130.
 constexpr int kUnitCost = 4, kDraftCost = 3;
 
-template <int L> struct Shape {
+// QR: rows that the queries' and the weights' places hold, 64 or, for problems of no more, 16 (S reads on past them, into what
+// lies behind, for rows that nobody looks at).  With 16 there is room for a third tile of 512 columns: 32 ragged sequences of
+// up to 8192 slots x 16 rows 47.2 -> 40.5 us.  (Tiles of 32 slots, five of them: 45.6, and 47.1 against 48.3 for 32 rows; an
+// instruction of 32 columns takes as long as one of 64.)
+template <int L, int QR> struct Shape {
     // A tile's latent columns lie in one of NS places, its key part (padded to 64 columns), which only the scores need,
     // in one of NK.  A single place is filled while the next tile's scores over the latent columns are computed, and has
     // barriers of its own.
     static constexpr int G = L / 64 + 1, TILE = (G - 1) * GROUP;
-    static constexpr int NS = L == 128 ? 6 : L == 256 ? 4 : L == 384 ? 3 : 2, NK = L < 384 ? NS : 1;
-    static constexpr int Q = 0, RING = G * GROUP, KEYS = RING + NS * TILE, P = KEYS + NK * GROUP, MISC = P + 2 * RB * 128;
+    static constexpr int NS = L == 128 ? 6 : L == 256 ? 4 : L == 384 || QR == 16 ? 3 : 2, NK = L < 384 ? NS : 1;
+    static constexpr int QG = QR * 128, Q = 0, RING = G * QG, KEYS = RING + NS * TILE, P = KEYS + NK * GROUP, MISC = P + 2 * QG;
 };
 
 struct Misc {
@@ -70,11 +74,11 @@ struct Misc {
     int fail;
 };
 
-template <int L> constexpr size_t smem_bytes() { return Shape<L>::MISC + sizeof(Misc) + sizeof(Work); }
+template <int L, int QR> constexpr size_t smem_bytes() { return Shape<L, QR>::MISC + sizeof(Misc) + sizeof(Work); }
 
-// where chunk c (16 bytes = 8 elements) of row r lies in a 128-byte-swizzled tile of 64 rows
-__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
-    return (uint32_t)((c >> 3) * GROUP + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+// where chunk c (16 bytes = 8 elements) of row r lies in 128-byte-swizzled groups of 64 columns, each `group` bytes long
+__device__ __forceinline__ uint32_t chunk_at(int r, int c, int group = GROUP) {
+    return (uint32_t)((c >> 3) * group + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 // a tile that the loading warps bring: the draft or a sequence's end lies in it
 __device__ __forceinline__ bool by_hand(const AttendArgs &a, const Segment &s, int tile) {
@@ -114,9 +118,9 @@ __device__ __forceinline__ bool any_warp(bool x) {
     return y != 0;
 }
 
-template <int L, class T>
+template <int L, class T, int QR>
 __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_constant__ CUtensorMap map) {
-    using S = Shape<L>;
+    using S = Shape<L, QR>;
     constexpr int G = S::G;
     extern __shared__ __align__(1024) unsigned char smem[];
     static_assert(S::MISC % 16 == 0 && alignof(Misc) == 16 && sizeof(Misc) % alignof(Work) == 0, "alignment of the parts");
@@ -181,8 +185,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
             const uint32_t d = tmem + 256 + (ns & 1) * TS;
 #pragma unroll
             for (int k = 0; k < L / 16; ++k) {
-                const uint32_t off = ((k >> 2) * GROUP + (k & 3) * 32) / 16;
-                umma_ss_warp(d, qd + off, cd + off, idesc_s, k > 0);
+                umma_ss_warp(d, qd + ((k >> 2) * S::QG + (k & 3) * 32) / 16, cd + ((k >> 2) * GROUP + (k & 3) * 32) / 16, idesc_s, k > 0);
             }
             if (S::NK < S::NS) {                           // (should the wait run out, what is there is as good as anything)
                 mbar_wait(&sh.keys_full, tiles & 1, fail);
@@ -192,7 +195,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                if (k < last_steps) umma_ss_warp(d, qd + ((G - 1) * GROUP + k * 32) / 16, kd + k * 32 / 16, idesc_s, 1);
+                if (k < last_steps) umma_ss_warp(d, qd + ((G - 1) * S::QG + k * 32) / 16, kd + k * 32 / 16, idesc_s, 1);
             umma_commit_warp(&sh.s_full[ns & 1]);
             if (S::NK < S::NS) umma_commit_warp(&sh.keys_used);
             ++ns;
@@ -216,7 +219,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
                     if (__any_sync(0xffffffffu, *fail || clock64() - t0 > kSpinCycles)) { *fail = 1; ok = false; break; }
                 }
                 if (!ok) break;
-                const uint64_t pj = pd + (np & 1) * (RB * 128 / 16);
+                const uint64_t pj = pd + (np & 1) * (S::QG / 16);
                 if (j == 0 && nseg > 0 && !__all_sync(0xffffffffu, mbar_wait(&sh.o_free, (nseg - 1) & 1, fail))) { ok = false; break; }
                 tc_fence_after();
                 const uint64_t vd = umma_desc(ring + use.slot * S::TILE, GROUP);
@@ -334,7 +337,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
 #pragma unroll
                 for (int i = 0; i < LANES; ++i) {
                     const int ch = lane + 32 * i;
-                    if (ch < CPR) cp_async16(q_at + chunk_at(r, ch), src + (ch * 8 < D ? ch * 8 : 0), ch * 8 < D);
+                    if (ch < CPR) cp_async16(q_at + chunk_at(r, ch, S::QG), src + (ch * 8 < D ? ch * 8 : 0), ch * 8 < D);
                 }
             }
             cp_commit();
@@ -514,11 +517,13 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
                     }
                     tmem_st_wait();
                 }
+                if (16 * warp < QR) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    unsigned char *at = p_at + (tiles & 1) * (RB * 128) + ((i ^ (lane >> 2)) << 4);
-                    *reinterpret_cast<uint32_t *>(at) = fa_pack2(x[4 * i], x[4 * i + 1], T());
-                    *reinterpret_cast<uint32_t *>(at + 8 * 128) = fa_pack2(x[4 * i + 2], x[4 * i + 3], T());
+                    for (int i = 0; i < 8; ++i) {
+                        unsigned char *at = p_at + (tiles & 1) * S::QG + ((i ^ (lane >> 2)) << 4);
+                        *reinterpret_cast<uint32_t *>(at) = fa_pack2(x[4 * i], x[4 * i + 1], T());
+                        *reinterpret_cast<uint32_t *>(at + 8 * 128) = fa_pack2(x[4 * i + 2], x[4 * i + 3], T());
+                    }
                 }
                 proxy_fence();
                 tc_fence_before();
@@ -681,15 +686,15 @@ bool make_map(const fa_latent_cache *c, int box_rows, CUtensorMap *map) {
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int L, class T> fa_status launch(AttendArgs a, const CUtensorMap &map, cudaStream_t s) {
-    constexpr size_t smem = smem_bytes<L>();
+template <int L, class T, int QR> fa_status launch(AttendArgs a, const CUtensorMap &map, cudaStream_t s) {
+    constexpr size_t smem = smem_bytes<L, QR>();
     static_assert(smem <= 232448, "shared memory of a block");
     int ctas = 0;
     cudaError_t e = block_count(&ctas);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(k_latent<L, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k_latent<L, T, QR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return fa_refuse("fa_latent_attention", cudaGetErrorString(e), FA_ERR_CUDA);
     a.inject = fa_take_injected_timeout();
-    k_latent<L, T><<<ctas, NTHR, smem, s>>>(a, map);
+    k_latent<L, T, QR><<<ctas, NTHR, smem, s>>>(a, map);
     fa_status st = fa_launch_check("latent attention");
     if (st != FA_OK) return st;
     const int64_t units = (int64_t)a.B * a.blocks;
@@ -703,10 +708,10 @@ template <int L, class T> fa_status launch(AttendArgs a, const CUtensorMap &map,
 }
 
 template <class T> fa_status launch(const AttendArgs &a, int latent, const CUtensorMap &map, cudaStream_t s) {
-    if (latent == 128) return launch<128, T>(a, map, s);
-    if (latent == 256) return launch<256, T>(a, map, s);
-    if (latent == 384) return launch<384, T>(a, map, s);
-    return launch<512, T>(a, map, s);
+    if (latent == 128) return launch<128, T, RB>(a, map, s);
+    if (latent == 256) return launch<256, T, RB>(a, map, s);
+    if (latent == 384) return launch<384, T, RB>(a, map, s);
+    return a.rows <= 16 ? launch<512, T, 16>(a, map, s) : launch<512, T, RB>(a, map, s);
 }
 
 fa_status sizes(const char *fn, int32_t B, int32_t T, int32_t heads) {
