@@ -26,7 +26,8 @@
 // 2 x 98304 slots x 256 rows 70 us (55 GFLOP, 0.78 PFLOP/s).
 // Tried and dropped: eight softmax warps of half a tile each (a barrier more; 4 to 13% slower), a tile's columns refilled as
 // the values' product leaves them (the copies' issue takes 1.7 times as long), one three-dimensional copy a tile, scores
-// issued in pieces between which the other product has its turn.
+// issued in pieces between which the other product has its turn, the two to four blocks of rows of a sequence side by side on
+// neighbouring SMs so that a slot is read once (16 x 8192 slots x 128 rows 77.2 -> 76.1 us, for a second order of the list).
 //
 // Roundings.  Both operands of the second product have one 16-bit type, so the weights take the cache's: bf16 (8 bits), or
 // fp16 with 2^8 for the reference's weight, so that all down to 2^-22 of it keep 11 bits.  The sum of the weights is taken before
@@ -53,8 +54,8 @@ constexpr int kUnitCost = 4, kDraftCost = 3;
 
 // QR: rows that the queries' and the weights' places hold, 64 or, for problems of no more, 16 (S reads on past them, into what
 // lies behind, for rows that nobody looks at).  With 16 there is room for a third tile of 512 columns: 32 ragged sequences of
-// up to 8192 slots x 16 rows 47.2 -> 40.5 us.  (Tiles of 32 slots, five of them: 45.6, and 47.1 against 48.3 for 32 rows; an
-// instruction of 32 columns takes as long as one of 64.)
+// up to 8192 slots x 16 rows 47.2 -> 40.5 us.  (Tiles of 32 slots, five of them: 45.6, and 47.1 against 48.3 for 32 rows: an
+// instruction of 32 columns takes 26 clocks, one of 64 takes 33.)
 template <int L, int QR> struct Shape {
     // A tile's latent columns lie in one of NS places, its key part (padded to 64 columns), which only the scores need,
     // in one of NK.  A single place is filled while the next tile's scores over the latent columns are computed, and has
