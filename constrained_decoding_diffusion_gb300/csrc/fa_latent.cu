@@ -23,7 +23,7 @@ template <class T, class O, int R>
 __global__ void __launch_bounds__(NT) k_latent_write(WriteArgs a) {
     constexpr int N = fa_vec<T>::N, U = 2, RR = R > 0 ? R : 1;
     const int lane = threadIdx.x & 31, half = a.rope / 2, vectors = a.latent / N;
-    const int n0 = (int)((blockIdx.x * (unsigned)NT + threadIdx.x) >> 5) * U;
+    const int64_t n0 = ((int64_t)blockIdx.x * (NT / 32) + (threadIdx.x >> 5)) * U;
     const int p = a.interleaved ? 2 * lane : lane, q = a.interleaved ? 2 * lane + 1 : lane + half;
     int64_t at[U];
     int pos[U];
@@ -32,13 +32,13 @@ __global__ void __launch_bounds__(NT) k_latent_write(WriteArgs a) {
     const uint64_t phase = a.pos && lane < half ? __ldg(a.phase + lane) : 0;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int n = n0 + u;
+        const int64_t n = n0 + u;
         at[u] = n < a.N ? a.slot[n] : -1;
         pos[u] = a.pos && n < a.N ? __ldg(a.pos + n) : 0;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int n = min(n0 + u, a.N - 1);
+        const int64_t n = min(n0 + u, (int64_t)a.N - 1);
         const T *x = (const T *)a.x + n * a.ls, *k = (const T *)a.key + n * a.ks;
         if (R > 0)
 #pragma unroll

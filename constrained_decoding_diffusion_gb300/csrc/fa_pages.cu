@@ -285,7 +285,7 @@ extern "C" fa_status fa_slot_map(int32_t B, int32_t N, int32_t page_size, int32_
         return fa_refuse(fn, "NULL buffer");
     const MapArgs a{B, N, shift, n_pages, max_pages, page_table, start, count, slot, seq, position, offset};
     const unsigned tiles = (unsigned)std::max(1, (B + MT - 1) / MT);
-    const unsigned split = (unsigned)std::max<int64_t>(1, std::min<int64_t>((N + 4 * MT - 1) / (4 * MT), 8 * 152 / tiles));
+    const unsigned split = (unsigned)std::max<int64_t>(1, std::min<int64_t>(((int64_t)N + 4 * MT - 1) / (4 * MT), 8 * 152 / tiles));
     k_slot_map<<<dim3(tiles, split), MT, 0, (cudaStream_t)stream>>>(a);
     return fa_launch_check("slot map");
 }

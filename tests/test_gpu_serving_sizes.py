@@ -109,3 +109,16 @@ def test_many_tokens_written_and_a_long_path():
     lm.fa_latent_keep(cache, table, ints([100]), path)
     # (as bits: some slots have never been written and may hold NaN)
     assert torch.equal(flat[100:100 + 1024].view(torch.int16), want.view(torch.int16))
+
+
+def test_write_of_more_tokens_than_32_bits_count_threads():
+    """The tokens share one vector (a stride of zero); the last ones' slots are written, and no other."""
+    N = 2 ** 28 + 41
+    cache = lm.LatentCache(torch.zeros(8, 16, 144, dtype=HF, device="cuda"), 128)
+    x, key = normal(1, 1, 128, dtype=HF), normal(2, 1, 16, dtype=HF)
+    slot = torch.full((N,), -1, dtype=torch.int32, device="cuda")
+    slot[2 ** 28 - 1:] = torch.arange(3, 45, dtype=torch.int32, device="cuda")
+    lm.fa_latent_write(cache, x.expand(N, 128), key.expand(N, 16), slot)
+    want = torch.zeros(128, 144, dtype=HF, device="cuda")
+    want[3:45] = torch.cat([x, key], 1)
+    assert torch.equal(cache.rows.view(128, 144), want)
