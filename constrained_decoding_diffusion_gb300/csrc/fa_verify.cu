@@ -590,6 +590,9 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
                 a.token[b] = found;
                 if (a.state) a.state[b] = a.next[(int64_t)state * a.V + found];
             }
+        } else if (tid == 0 && held < 0) {                // all that weighed was tried, and roundings are left of its sum
+            a.token[b] = -1;
+            if (a.state) a.state[b] = -1;
         }
     }
     if (rank == 0) {

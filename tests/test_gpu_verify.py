@@ -256,3 +256,21 @@ def test_many_sequences_over_a_large_vocabulary():
     d = make(18, 40, chain(3), 70001, BF, states=2)
     first = check(d)
     assert all(torch.equal(x, y) for x, y in zip(first, check(d)))
+
+
+@pytest.mark.parametrize("V", [4, 40000])
+def test_a_sum_of_which_only_roundings_are_left(V):
+    """Four tokens weigh 1, 2^-23, x and 3/4 of x's last place, x = 1.5 2^-47, and all are tried with the largest u.  As two
+    floats the sum is 1 + 2^-23 + (x + 1 last place), so each is rejected, and a quarter of x's last place is left of
+    nothing.  The next token is none rather than what the buffer held."""
+    x, last = 1.5 * 2.0 ** -47, 2.0 ** -70
+    target = torch.zeros(1, 5, V)
+    target[0, 0, :4] = torch.tensor([1.0, x, 2.0 ** -23, 0.75 * last])
+    verify = lm.Verify(1, 5, V)
+    for out in (verify.path, verify.kept, verify.token):
+        out.fill_(77)
+    path, kept, token, _ = verify(target.cuda(), torch.tensor([[0, 0, 2, 1, 3]], dtype=torch.int32).cuda(),
+                                  torch.tensor([[-1, 0, 0, 0, 0]], dtype=torch.int32).cuda(),
+                                  torch.full((1, 5), 1 - 2.0 ** -24).cuda())
+    assert path.tolist() == [[0, -1, -1, -1, -1]] and kept.tolist() == [1]
+    assert token.tolist() == [-1]
