@@ -12,8 +12,9 @@
 // Dekker's exact additions and products, 46 bits or more): fp64 runs at two lanes a clock and SM here.
 //
 // A cluster of blocks takes a sequence: each block a slice of the vocabulary, from node to node, so that only the rows of
-// nodes that are visited are read.  The first block decides and tells the others, so that they never part ways whatever
-// the inputs hold.
+// nodes that are visited are read.  Every block gets every segment's sums and decides for itself, so that the cluster meets
+// once a row; what else a decision rests on is read by the first block and sent to all, so that they never part ways
+// whatever the inputs hold.
 //
 // What bounds it is the chain from node to node.  In eight blocks a row of 151936 takes 6 us with a draft (2900 cycles of
 // additions, 14 a token, and their loads 5800 clocks; the sums of warps, the decision and the cluster's two meetings 5000)
@@ -32,7 +33,7 @@ namespace cg = cooperative_groups;
 
 namespace {
 
-constexpr int NT = 256, WARPS = NT / 32, MAX_CLUSTER = 8, ROWS = 32;   // rows of a segment that the draw takes at a time
+constexpr int NT_LOG = 8, NT = 1 << NT_LOG, WARPS = NT / 32, MAX_CLUSTER = 8, SEGS = MAX_CLUSTER * WARPS, ROWS = 32;   // rows of a segment that the draw takes at a time
 
 struct Sum { float h, l; };   // h + l
 
@@ -162,7 +163,7 @@ struct VerifyArgs {
     int32_t *path, *kept, *token, *state;
 };
 
-struct Plan {          // what the first block tells the others
+struct Plan {          // what a block's first warp tells the others
     int action;        // draw from segment `segment`, go to `node` with `state`, or sweep again with l
     int node, state, segment, tried;
     Sum l, before, goal;   // the sum before the segment, and what the draw looks for
@@ -171,10 +172,14 @@ enum { DRAW = 0, NODE = 1, SWEEP = 2 };
 
 struct Shared {
     Plan plan;
-    Sum seg[MAX_CLUSTER * WARPS], seg_q[MAX_CLUSTER * WARPS];   // (first block) the sums of all segments
-    Sum row[ROWS];                                              // (the draw) of the rows of one segment
-    int last;
+    Sum seg[2][SEGS], seg_q[2][SEGS];   // the sums of all segments, of this sweep and the next (zero where there are fewer)
+    Sum row[ROWS];                      // (the draw) of the rows of one segment
+    int use, last;
 };
+
+// A drafted token.
+struct __align__(16) Child { int parent, token; float u, unused; };
+constexpr size_t kBytesOfToken = sizeof(Child) + sizeof(float2) + 3 * sizeof(int);   // with its weights, place on the path ...
 
 // A row of the vocabulary in vectors of 16 bytes, counted from the aligned address at or before its start.
 template <class T> struct Row {
@@ -314,36 +319,62 @@ template <class T, bool DRAFT>
 __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
     constexpr int N = fa_vec<T>::N;
     __shared__ Shared sh;
-    extern __shared__ int dyn[];
-    int *parent = dyn, *tok = dyn + a.T, *path = dyn + 2 * a.T, *after = dyn + 3 * a.T, *tried = dyn + 4 * a.T;
-    float *us = (float *)(dyn + 5 * a.T), *px = us + a.T, *qx = px + a.T;
+    extern __shared__ Child child[];
+    float2 *pq = reinterpret_cast<float2 *>(child + a.T);   // the target's and the draft's weight
+    int *after = reinterpret_cast<int *>(pq + a.T), *path = after + a.T, *tried = path + a.T;
     const cg::cluster_group cluster = cg::this_cluster();
-    const int C = cluster.num_blocks(), rank = cluster.block_rank(), b = blockIdx.x / C;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    Shared *first = cluster.map_shared_rank(&sh, 0);
+    const int C = cluster.num_blocks(), log_c = 31 - __clz(C), rank = cluster.block_rank(), b = blockIdx.x >> log_c;
+    // (what all threads of a warp have alike goes through a shuffle where shuffles depend on it: the compiler then knows that
+    // the warp runs as one)
+    auto alike = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+    const int tid = threadIdx.x, warp = alike(tid >> 5), lane = tid & 31;
     const int use = a.count ? min(max(a.count[b], 0), a.T) : a.T;
-    // (waited for before the first store to another block, which has to have started)
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-    if (rank == 0)
-        for (int j = tid; j < a.T; j += NT) {
-            parent[j] = a.parents[(int64_t)b * a.T + j];
-            tok[j] = a.tokens[(int64_t)b * a.T + j];
-            us[j] = a.u[(int64_t)b * a.T + j];
-            path[j] = 0;
+    path[0] = 0;
+    for (int i = C * WARPS + tid; i < SEGS; i += NT)
+        for (int k = 0; k < 2; ++k) sh.seg[k][i] = sh.seg_q[k][i] = {0.0f, 0.0f};
+    // the drafted token j, and its weights in its parent's rows
+    auto read = [&](int j) {
+        const int64_t i = (int64_t)b * a.T + j;
+        return Child{a.parents[i], a.tokens[i], a.u[i], 0.0f};
+    };
+    auto weights = [&](int j, Child c) {
+        float2 w = {0.0f, 0.0f};
+        if ((unsigned)c.parent < (unsigned)j && (unsigned)c.token < (unsigned)a.V) {
+            w.x = fa_to_f32(((const T *)a.target + b * a.tb + c.parent * a.tr)[c.token]);
+            if (DRAFT) w.y = fa_to_f32(((const T *)a.draft + b * a.db + c.parent * a.dr)[c.token]);
         }
-    // kept by the first block's first lane
+        return w;
+    };
+    Child own = {-1, -1, 0.0f, 0.0f};
+    if (rank == 0 && tid < a.T) own = read(tid);
+    // all blocks have started before the first store to another
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    // stores x at y in every block
+    auto tell = [&](auto *y, auto x) {
+#pragma unroll
+        for (int c = 0; c < MAX_CLUSTER; ++c)
+            if (c < C) *cluster.map_shared_rank(y, c) = x;
+    };
+    float2 own_pq = {0.0f, 0.0f};
+    if (rank == 0) {
+        for (int j = tid; j < a.T; j += NT) tell(child + j, j == tid ? own : read(j));
+        if (tid == 0) tell(&sh.use, use);
+        if (tid < a.T) own_pq = weights(tid, own);        // under way during the first sweep
+    }
+    // kept by a block's first lane, and the same in all blocks
     int j = 1, kept = use > 0 ? 1 : 0, n_tried = 0;
     Sum l = {0.0f, 0.0f}, old_l = l;
     bool again = false;                                  // this sweep only restores the sums of old_l
     bool probing = false;                                // this sweep is a rejection's
     Sum total_q = {0.0f, 0.0f};
     int node = 0, state = a.S ? a.states[b] : 0;
-    bool fresh = true;
+    bool fresh = true, first = true;
     Node<T, DRAFT> at;
     at.words = a.words;
     __syncthreads();
-    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-    while (true) {
+    for (int turn = 0;; turn ^= 1) {
+        Sum *const seg = sh.seg[turn], *const seg_q = sh.seg_q[turn];
         // (nothing that a block reads for itself decides how often the cluster meets)
         const bool any = use > 0 && (!a.S || (unsigned)state < (unsigned)a.S);
         if (fresh) {
@@ -352,20 +383,15 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
             at.live = a.S && any ? a.live + (int64_t)state * a.words : nullptr;
             at.lead = (int)(((uintptr_t)at.p.p / sizeof(T)) % N);
             at.chunks = (int)(((int64_t)a.V + at.lead + N - 1) / N);
-            at.per = (at.chunks + C * NT - 1) / (C * NT) * 32;
+            at.per = ((at.chunks + (NT << log_c) - 1) >> (NT_LOG + log_c)) * 32;
             at.lam = {0.0f, 0.0f};
         }
-        // what the test of a child needs, one a thread (and the rest of a long draft below): under way during the sweep
-        const int child = node + 1 + tid;
-        const bool tests = rank == 0 && fresh && any && child < use && parent[child] == node && (unsigned)tok[child] < (unsigned)a.V;
-        int to = -1;
-        float child_p = 0.0f, child_q = 0.0f;
-        if (tests) {
-            const int x = tok[child];
-            to = a.S ? a.next[(int64_t)state * a.V + x] : 0;
-            child_p = fa_to_f32(at.p.p[x]);
-            if (DRAFT) child_q = fa_to_f32(at.q.p[x]);
-        }
+        // where the automaton goes by a child, one a thread (and the rest of a long draft below): under way during the sweep
+        const int mine_too = node + 1 + tid;
+        auto is_child = [&](int j) { return child[j].parent == node && (unsigned)child[j].token < (unsigned)a.V; };
+        auto goes = [&](int j) { return any ? a.next[(int64_t)state * a.V + child[j].token] : -1; };
+        const bool moves = a.S && rank == 0 && fresh && mine_too < use && is_child(mine_too);
+        const int to = moves ? goes(mine_too) : -1;
         // ---- this warp's segment
         const int mine = rank * WARPS + warp, s0 = mine * at.per, s1 = min(s0 + at.per, at.chunks);
         Sum w = {0.0f, 0.0f}, wq = {0.0f, 0.0f};
@@ -380,32 +406,31 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
         }
         if (DRAFT && fresh) warp_sums(w, wq);
         else w = warp_sum(w);
-        if (lane == 0) {
-            first->seg[mine] = w;
-            if (DRAFT && fresh) first->seg_q[mine] = wq;
+        // (the first lane's, to the last bit, for all blocks)
+        w = {__shfl_sync(0xffffffffu, w.h, 0), __shfl_sync(0xffffffffu, w.l, 0)};
+        if (DRAFT && fresh) wq = {__shfl_sync(0xffffffffu, wq.h, 0), __shfl_sync(0xffffffffu, wq.l, 0)};
+        if (lane < C) {
+            *cluster.map_shared_rank(seg + mine, lane) = w;
+            if (DRAFT && fresh) *cluster.map_shared_rank(seg_q + mine, lane) = wq;
         }
-        if (tests) {
-            after[child] = to;
-            px[child] = to < 0 ? 0.0f : weight(child_p);
-            qx[child] = to < 0 ? 0.0f : weight(child_q);
-        }
-        if (rank == 0 && fresh && any)
-            for (int i = child + NT; i < use; i += NT) {
-                const int x = tok[i];
-                if (parent[i] != node || (unsigned)x >= (unsigned)a.V) continue;
-                const int there = a.S ? a.next[(int64_t)state * a.V + x] : 0;
-                after[i] = there;
-                px[i] = there < 0 ? 0.0f : weight(fa_to_f32(at.p.p[x]));
-                qx[i] = DRAFT && there >= 0 ? weight(fa_to_f32(at.q.p[x])) : 0.0f;
+        if (moves) tell(after + mine_too, to);
+        if (rank == 0 && first) {
+            for (int j = tid; j < a.T; j += NT) {
+                const float2 x = j == tid ? own_pq : weights(j, child[j]);
+                tell(pq + j, make_float2(weight(x.x), weight(x.y)));
             }
+        }
+        if (a.S && rank == 0 && fresh)
+            for (int j = mine_too + NT; j < use; j += NT)
+                if (is_child(j)) tell(after + j, goes(j));
+        first = false;
         cluster.sync();
-        if (rank == 0 && warp == 0) {
-            const int each = (C * WARPS + 31) / 32;       // segments of a lane
-            Sum total = {0.0f, 0.0f}, t = {0.0f, 0.0f};
-            for (int i = lane * each; i < min((lane + 1) * each, C * WARPS); ++i) {
-                total = total + sh.seg[i];
-                if (DRAFT) t = t + sh.seg_q[i];
-            }
+        if (warp == 0) {
+            const int use = sh.use;
+            constexpr int each = SEGS / 32;               // segments of a lane
+            static_assert(each == 2, "two segments of a lane");
+            Sum total = seg[lane * 2] + seg[lane * 2 + 1], t = {0.0f, 0.0f};
+            if (DRAFT && fresh) t = seg_q[lane * 2] + seg_q[lane * 2 + 1];
             if (fresh) {
                 n_tried = 0;
                 l = {0.0f, 0.0f};
@@ -426,17 +451,25 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
                     again = probing = false;
                     if (!some) j = use;                              // nothing can be accepted
                     const bool drafts = DRAFT && total_q.h > 0.0f;   // a row without weight: q(x) = 0
-                    Sum ratio = {0.0f, 0.0f};
-                    if (drafts && j < use) ratio = total / total_q;
                     for (; j < use; ++j) {
-                        if (parent[j] != node || (unsigned)tok[j] >= (unsigned)a.V) continue;
-                        const float u = us[j], x = px[j];
+                        const Child x = child[j];
+                        if (x.parent != node || (unsigned)x.token >= (unsigned)a.V) continue;
+                        const bool there = !a.S || after[j] >= 0;
+                        const float p = there ? pq[j].x : 0.0f, q = there ? pq[j].y : 0.0f;
                         bool take, known = false;
+                        Sum ratio = {0.0f, 0.0f};
                         if (DRAFT) {
-                            take = ratio * qx[j] * u < left(x, qx[j], l);
+                            // 24 bits mostly tell, without the quotient; where they do not, or leave fp32's range, 48 do
+                            const Sum rest = left(p, q, l);
+                            const float less = total.h * q * x.u, more = rest.h * total_q.h;
+                            take = less > 1e-30f && more < 1e30f && less * 1.0001f < more;
+                            if (!take) {
+                                if (drafts) ratio = total / total_q;
+                                take = ratio * q * x.u < rest;
+                            }
                         } else {
-                            for (int i = 0; i < n_tried; ++i) known |= tried[i] == tok[j];
-                            take = !known && total * u < Sum{x, 0.0f};
+                            for (int i = 0; i < n_tried; ++i) known |= tried[i] == x.token;
+                            take = !known && total * x.u < Sum{p, 0.0f};
                         }
                         if (take) {
                             plan.action = NODE;
@@ -456,27 +489,27 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
                             ++j;
                             break;
                         }
-                        if (known || x == 0.0f) continue;
-                        const Sum rest = total + Sum{-x, 0.0f};
+                        if (known || p == 0.0f) continue;
+                        const Sum rest = total + Sum{-p, 0.0f};
                         if (!(rest.h > 0.0f)) continue;
                         total = rest;
-                        Sum &from = sh.seg[at.segment(tok[j])];
-                        from = from + Sum{-x, 0.0f};
-                        tried[n_tried++] = tok[j];
+                        Sum &from = seg[at.segment(x.token)];
+                        from = from + Sum{-p, 0.0f};
+                        tried[n_tried++] = x.token;
                     }
-                    plan.goal = total * us[0];
+                    plan.goal = total * child[0].u;
                 }
             }
             plan.action = __shfl_sync(0xffffffffu, plan.action, 0);
             if (plan.action == DRAW) {
                 // the segment that holds the draw
                 const Sum goal = {__shfl_sync(0xffffffffu, plan.goal.h, 0), __shfl_sync(0xffffffffu, plan.goal.l, 0)};
-                const int i0 = lane * each, i1 = min(i0 + each, C * WARPS);
+                const int i0 = lane * each, i1 = i0 + each;
                 Sum here = {0.0f, 0.0f};
                 bool weighs = false;
                 for (int i = i0; i < i1; ++i) {
-                    here = here + sh.seg[i];
-                    weighs |= sh.seg[i].h > 0.0f;
+                    here = here + seg[i];
+                    weighs |= seg[i].h > 0.0f;
                 }
                 const Sum upto = warp_scan(here);
                 const Sum start = {__shfl_up_sync(0xffffffffu, upto.h, 1), __shfl_up_sync(0xffffffffu, upto.l, 1)};
@@ -486,8 +519,8 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
                 if (lane == who && all && some) {
                     Sum before = lane ? start : Sum{0.0f, 0.0f};
                     for (int i = i0; i < i1; ++i) {
-                        if (!(sh.seg[i].h > 0.0f)) continue;
-                        const Sum next = before + sh.seg[i];
+                        if (!(seg[i].h > 0.0f)) continue;
+                        const Sum next = before + seg[i];
                         plan.segment = i;                 // the last one if rounding hides all others
                         plan.before = before;
                         if (goal < next) break;
@@ -503,14 +536,14 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
             plan.l.h = __shfl_sync(0xffffffffu, plan.l.h, 0);
             plan.l.l = __shfl_sync(0xffffffffu, plan.l.l, 0);
             plan.tried = __shfl_sync(0xffffffffu, n_tried, 0);
-            if (lane < C) cluster.map_shared_rank(&sh, lane)->plan = plan;
+            if (lane == 0) sh.plan = plan;
         }
-        cluster.sync();
-        const int action = sh.plan.action;
+        __syncthreads();
+        const int action = alike(sh.plan.action);
         fresh = action == NODE;
         if (action == NODE) {
-            node = sh.plan.node;
-            state = sh.plan.state;
+            node = alike(sh.plan.node);
+            state = alike(sh.plan.state);
             continue;
         }
         if (action == SWEEP) {
@@ -520,7 +553,8 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
         break;
     }
     // ---- the draw: the block that has the segment sums its rows of 32 vectors, and a warp takes the row that holds it
-    const int segment = sh.plan.segment;
+    // (nothing is read from or written to another block from here on: each may end)
+    const int segment = alike(sh.plan.segment);
     if (segment < 0) {
         if (rank == 0 && tid == 0) {
             a.token[b] = -1;
@@ -529,11 +563,6 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
     } else if (rank == segment / WARPS) {
         const int n = DRAFT ? 0 : sh.plan.tried, c0 = segment * at.per, c1 = min(c0 + at.per, at.chunks);
         Sum goal = sh.plan.goal;
-        if (!DRAFT && rank != 0 && n > 0) {
-            const int *theirs = cluster.map_shared_rank(tried, 0);
-            for (int i = tid; i < n; i += NT) tried[i] = theirs[i];
-            __syncthreads();
-        }
         Sum before = sh.plan.before;
         Sum v[N];
         int held = -1;                                    // the last row with a weight so far
@@ -601,7 +630,6 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
         const int n = sh.last;
         for (int i = tid; i < a.T; i += NT) a.path[(int64_t)b * a.T + i] = i < n ? path[i] : -1;
     }
-    cluster.sync();                                       // no block leaves while another reads its list
 }
 
 template <class T, bool DRAFT> void launch(const VerifyArgs &a, int cluster, cudaStream_t s) {
@@ -612,7 +640,7 @@ template <class T, bool DRAFT> void launch(const VerifyArgs &a, int cluster, cud
     cudaLaunchConfig_t c = {};
     c.gridDim = dim3((unsigned)a.B * cluster);
     c.blockDim = dim3(NT);
-    c.dynamicSmemBytes = (size_t)a.T * 8 * sizeof(int);
+    c.dynamicSmemBytes = a.T * kBytesOfToken;
     c.stream = s;
     c.attrs = at;
     c.numAttrs = 1;
