@@ -33,7 +33,7 @@ namespace cg = cooperative_groups;
 
 namespace {
 
-constexpr int NT_LOG = 8, NT = 1 << NT_LOG, WARPS = NT / 32, MAX_CLUSTER = 8, SEGS = MAX_CLUSTER * WARPS, ROWS = 32;   // rows of a segment that the draw takes at a time
+constexpr int NT_LOG = 8, NT = 1 << NT_LOG, WARPS = NT / 32, MAX_CLUSTER = 16, SEGS = MAX_CLUSTER * WARPS, ROWS = 32;   // rows of a segment that the draw takes at a time
 
 struct Sum { float h, l; };   // h + l
 
@@ -427,10 +427,15 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
         cluster.sync();
         if (warp == 0) {
             const int use = sh.use;
-            constexpr int each = SEGS / 32;               // segments of a lane
-            static_assert(each == 2, "two segments of a lane");
-            Sum total = seg[lane * 2] + seg[lane * 2 + 1], t = {0.0f, 0.0f};
-            if (DRAFT && fresh) t = seg_q[lane * 2] + seg_q[lane * 2 + 1];
+            static_assert(SEGS == 128, "four segments of a lane at most");
+            const int each = C * WARPS > 64 ? 4 : 2;      // segments of a lane
+            auto of_lane = [&](const Sum *x) {
+                Sum y = x[lane * each] + x[lane * each + 1];
+                if (each == 4) y = y + (x[lane * 4 + 2] + x[lane * 4 + 3]);
+                return y;
+            };
+            Sum total = of_lane(seg), t = {0.0f, 0.0f};
+            if (DRAFT && fresh) t = of_lane(seg_q);
             if (fresh) {
                 n_tried = 0;
                 l = {0.0f, 0.0f};
@@ -644,6 +649,7 @@ template <class T, bool DRAFT> void launch(const VerifyArgs &a, int cluster, cud
     c.stream = s;
     c.attrs = at;
     c.numAttrs = 1;
+    if (cluster > 8) (void)cudaFuncSetAttribute(k_verify<T, DRAFT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     (void)cudaLaunchKernelEx(&c, k_verify<T, DRAFT>, a);   // its error is the one the check reads
 }
 
@@ -668,11 +674,16 @@ extern "C" fa_status fa_verify(int32_t dtype, int32_t B, int32_t T, int32_t V, c
     const VerifyArgs a{B, T, V, S, (V + 31) / 32, target, draft, target_batch_stride, target_row_stride, draft_batch_stride,
                        draft_row_stride, tokens, parents, count, u, states, next, live, path, kept, token, S > 0 ? state : nullptr};
     // Blocks of a sequence: eight where the vocabulary gives each thread some work (1 / 2 / 4 / 8 blocks, 8 sequences of
-    // 5 x 32000: 46 / 34 / 27 / 23 us, of 5 x 8000 27 / 23 / 23 / 22), fewer where that would take more than two rounds of
-    // blocks for short sweeps (64 sequences of 5 x 32000 48 / 36 / 31 / 48 us, of 5 x 8000 28 / 24 / 25 / 43, but of
-    // 9 x 151936 335 / 185 / 131 / 99).
-    int cluster = MAX_CLUSTER;
-    while (cluster > 1 && (V < 2048 * cluster || (V < 65536 && B * cluster > 2 * 152))) cluster /= 2;
+    // 5 x 32000: 46 / 34 / 23 / 19 us, of 5 x 8000 27 / 23 / 23 / 22), fewer where that would take more than two rounds of
+    // blocks for short sweeps (64 sequences of 5 x 32000 48 / 36 / 31 / 46 us, of 5 x 8000 28 / 24 / 25 / 43, but of
+    // 9 x 151936 335 / 185 / 120 / 85).  Sixteen where a few sequences have long sweeps: 8 / 16 blocks, 4 sequences of 5 x
+    // 102400 27.3 / 25.4, 12 26.6 / 28.9, 16 28.9 / 37.3; of 5 x 262144 36.6 / 28.9, 44.1 / 38.0, 47.6 / 45.1, 18 55.6 / 56.5;
+    // trees of 17 x 151936 bf16 under an automaton, 1 / 8 / 16 / 24 of them: 13.9 / 34.0 / 31.0 / 34.8 against 12.5 / 25.8 /
+    // 25.3 / 31.9.
+    int cluster = 8;
+    if (V >= 98304 && B <= std::min(16, V / 8192)) cluster = 16;
+    else
+        while (cluster > 1 && (V < 2048 * cluster || (V < 65536 && B * cluster > 2 * 152))) cluster /= 2;
     auto go = [&](auto tag) {
         using T_ = decltype(tag);
         if (draft) launch<T_, true>(a, cluster, (cudaStream_t)stream);

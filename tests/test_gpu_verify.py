@@ -274,3 +274,24 @@ def test_a_sum_of_which_only_roundings_are_left(V):
                                   torch.full((1, 5), 1 - 2.0 ** -24).cuda())
     assert path.tolist() == [[0, -1, -1, -1, -1]] and kept.tolist() == [1]
     assert token.tolist() == [-1]
+
+
+@pytest.mark.parametrize("dtype,draft,states", [(F32, True, 0), (BF, False, 3), (HF, True, 3)])
+@pytest.mark.parametrize("B,V", [(1, 98303), (1, 98304), (12, 98304), (13, 98311), (15, 122887), (16, 131075), (17, 131072)])
+def test_large_vocabularies_of_few_sequences(B, V, dtype, draft, states):
+    check(make(V + B, B, chain(3), V, dtype, draft, states))
+    check(make(V, B, [-1, 0, 0, 0], V, dtype, draft, states, sampled=False))
+
+
+def test_more_drafted_tokens_than_threads_over_a_large_vocabulary():
+    """600 children of the last token, then a chain; a state's moves are looked up for all of them."""
+    g = torch.Generator().manual_seed(2)
+    d = make(3, 2, [-1] + [0] * 600, 5, draft=False)
+    V = 98400
+    d["target"] = torch.rand(2, 601, V, generator=g).cuda()
+    d["tokens"] = torch.randperm(V, generator=g)[:1202].view(2, 601).int().cuda()
+    d["u"][:, 1:] = 1 - 2.0 ** -20
+    d["u"][1, 500] = 0.0
+    d["next"], d["live"] = automaton(g, 4, V, dead=0.3)
+    d["states"] = torch.tensor([1, 2], dtype=torch.int32).cuda()
+    check(d)
