@@ -16,15 +16,16 @@
 // once a row; what else a decision rests on is read by the first block and sent to all, so that they never part ways
 // whatever the inputs hold.
 //
-// What bounds it is the chain from node to node.  In eight blocks a row of 151936 takes 6 us with a draft (2900 cycles of
-// additions, 14 a token, and their loads 5800 clocks; the sums of warps, the decision and the cluster's two meetings 5000)
-// and 4 without, the draw 3.  Measured in a graph: 64 sequences of 9 x 151936 fp32 with a draft 97 us (210 MB read, 2.2 TB/s;
-// the longest path takes 10 rows, and 36 clusters run at a time), 16 trees of 17 x 151936 bf16 under an automaton 35,
-// a chain of 5 x 32000 19.
+// What bounds it is the chain from node to node.  In eight blocks a row of 151936 takes 5.5 us with a draft (2900 cycles of
+// additions, 14 a token, and their loads 6700 clocks; the sums of warps, the cluster's meeting and the decision 3500)
+// and 4 without, the draw 3.  Measured in a graph: 64 sequences of 9 x 151936 fp32 with a draft 87 us (210 MB read, 2.4 TB/s;
+// the longest path takes 10 rows, and 36 clusters run at a time), 16 trees of 17 x 151936 bf16 under an automaton 25,
+// a chain of 5 x 32000 15.
 // Tried and dropped: a ring of asynchronous copies in shared memory (5% slower, more instructions), two sums at a time in
 // packed registers against one (equal: the packed addition takes twice as long), the next vectors loaded while
-// these are added up (10% slower, registers), arrivals on barriers in the other blocks' memory for the cluster's
-// (equal: either waits for the stores before).
+// these are added up (10% slower, registers), three blocks an SM with fewer vectors under way (8 to 15% slower), arrivals on
+// barriers in the other blocks' memory for the cluster's (equal: either waits for the stores before), one block that decides
+// and tells the others in a second meeting (5 to 9% slower).
 #include <cooperative_groups.h>
 
 #include "fa_lm.cuh"
