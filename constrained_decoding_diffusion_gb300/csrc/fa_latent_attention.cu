@@ -611,7 +611,8 @@ __global__ void __launch_bounds__(256) k_latent_join(AttendArgs a, int runs) {
     runs = min(total, runs);
     // the runs that hold the unit's first and last tile
     const int c0 = (int)((((int64_t)g0 + 1) * runs - 1) / total), c1 = (int)((((int64_t)g1 + 1) * runs - 1) / total);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, parts = c1 - c0 + 1;
+    // (the warp's number by way of a shuffle, as above: 16 x 4096 slots x 1024 rows 215 -> 212 us)
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), parts = c1 - c0 + 1;
     const int rows = min(a.rows - RB * block, RB), row = N * blockIdx.y + warp / SUBS, sub = warp % SUBS;
     fa_wait_for_previous();                                // by every block: the next kernel waits for this one only
     if (N * (int)blockIdx.y >= rows) return;
