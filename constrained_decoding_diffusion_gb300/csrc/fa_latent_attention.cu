@@ -26,8 +26,9 @@
 // 2 x 98304 slots x 256 rows 70 us (55 GFLOP, 0.78 PFLOP/s).
 // Tried and dropped: eight softmax warps of half a tile each (a barrier more; 4 to 13% slower), a tile's columns refilled as
 // the values' product leaves them (the copies' issue takes 1.7 times as long), one three-dimensional copy a tile, scores
-// issued in pieces between which the other product has its turn, the two to four blocks of rows of a sequence side by side on
-// neighbouring SMs so that a slot is read once (16 x 8192 slots x 128 rows 77.2 -> 76.1 us, for a second order of the list).
+// issued in pieces between which the other product has its turn, the blocks of rows of a sequence side by side on neighbouring
+// SMs, so that a slot is read from memory once, where the slots are more than 128 MiB (16 x 8192 slots x 128 rows equal, 256
+// 131 -> 121, 512 232 -> 207, 1024 414 -> 398, but 2 to 4 us more in every other call with more than one block of rows).
 //
 // Roundings.  Both operands of the second product have one 16-bit type, so the weights take the cache's: bf16 (8 bits), or
 // fp16 with 2^8 for the reference's weight, so that all down to 2^-22 of it keep 11 bits.  The sum of the weights is taken before

@@ -359,3 +359,24 @@ def test_refusals_of_the_binding():
         lm.LatentAttention(1, 1, 4, 256, 16, HF)(normal(1, 1, 1, 4, 272, dtype=HF), cache, table, ints([50]), 0.1)
     with pytest.raises(Exception):
         attend(q, cache, table, ints([50]), 0.0)
+
+
+@pytest.mark.parametrize("dtype,latent,rope,size,length,T,H", [
+    (BF, 512, 64, 64, [61000, 47003, 20, 15001], 3, 64),
+    (HF, 512, 64, 16, [119000, 0, 1], 2, 128),
+    (BF, 512, 16, 4, [40001, 90003], 5, 67),
+    (BF, 384, 32, 128, [100000, 71777], 1, 1000),
+    (HF, 256, 32, 64, [250001], 3, 80),
+    (BF, 256, 32, 256, [150000, 99999], 1, 200),
+    (HF, 128, 16, 32, [300000, 199999], 2, 99)])
+def test_more_slots_than_the_cache_keeps(dtype, latent, rope, size, length, T, H):
+    """Caches of 128 MiB and more: many tiles a run, 3 to 16 blocks of rows, whole and ragged, a page that is not held."""
+    cache, table = make(T, length, T, size, latent, rope, dtype)
+    table[0, 3] = -1
+    B = len(length)
+    count = [max(T - b, 0) for b in range(B)]
+    q = normal(H, B, T, H, latent + rope, dtype=dtype)
+    out, lse = check(q, cache, table, length, 0.06, chains(B, T), count)
+    again = lm.LatentAttention(B, T, H, latent, rope, dtype)(q, cache, table, ints(length), 0.06, chains(B, T), ints(count))
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    check(q, cache, table, [min(n, 9000) for n in length], 0.06, chains(B, T))
