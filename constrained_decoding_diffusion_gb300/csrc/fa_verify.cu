@@ -8,6 +8,10 @@
 // one at x: accepted if u S_k < p(x), else S_{k+1} = S_k - p(x), with no pass at all.  The next token is found in
 // the sums of the vocabulary's segments (one a warp) and then in its segment.
 //
+// Under an automaton both rows are those of its tokens alone, and a child with another token is passed over.  Of children
+// drawn from the whole row those that are left are draws from the restricted one, so the result has the target's distribution
+// whether or not the drafter knew the automaton; a rejection of the others would take from the target what they cannot stand for.
+//
 // A draw compares u with a sum over the vocabulary, so everything is kept as unevaluated sums of two floats (Knuth's and
 // Dekker's exact additions and products, 46 bits or more): fp64 runs at two lanes a clock and SM here.
 //
@@ -460,8 +464,8 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
                     for (; j < use; ++j) {
                         const Child x = child[j];
                         if (x.parent != node || (unsigned)x.token >= (unsigned)a.V) continue;
-                        const bool there = !a.S || after[j] >= 0;
-                        const float p = there ? pq[j].x : 0.0f, q = there ? pq[j].y : 0.0f;
+                        if (a.S && after[j] < 0) continue;           // not of the distributions that are compared
+                        const float p = pq[j].x, q = pq[j].y;
                         bool take, known = false;
                         Sum ratio = {0.0f, 0.0f};
                         if (DRAFT) {

@@ -580,7 +580,8 @@ fa_status fa_beam_reorder(int32_t N, int32_t K, int32_t top, int64_t words, cons
  *   draft         [B, T, V] likewise: row p is the distribution that the children of node p were drawn
  *                 from, independently; or NULL: they were chosen without regard to u (the best beams, say),
  *                 and q(x) = 1
- *   tokens        [B, T] int32; a node with a token outside [0, V) is passed over
+ *   tokens        [B, T] int32; a node whose token is outside [0, V), or not allowed by the automaton after its parent,
+ *                 is passed over (children may be drawn from the draft's whole row or from its allowed tokens alone)
  *   parents       [B, T] int32
  *   count         [B] int32 or NULL: nodes in use.  0: the sequence has ended, kept is 0
  *   u             [B, T] fp32 in [0, 1)

@@ -45,7 +45,7 @@ def verify(target, tokens, parents, u, draft=None, count=None, states=None, next
         j = 1
         while j < use:
             x = int(tok[b, j])
-            if par[b, j] != node or not 0 <= x < V or r.sum() == 0:
+            if par[b, j] != node or not 0 <= x < V or r.sum() == 0 or not allowed()[x]:
                 j += 1
                 continue
             if q is None:
