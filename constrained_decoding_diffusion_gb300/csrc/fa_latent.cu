@@ -143,6 +143,7 @@ extern "C" fa_status fa_latent_write(const fa_latent_cache *cache, int32_t dtype
     if (interleaved != 0 && interleaved != 1) return fa_refuse(fn, "interleaved must be 0 or 1");
     if (N == 0) return FA_OK;
     if (!latent || !key || !slot) return fa_refuse(fn, "NULL buffer");
+    if (((uintptr_t)latent | (uintptr_t)key) % fa_dtype_bytes(dtype)) return fa_refuse(fn, "latent and key must be aligned to their type");
     const WriteArgs a{cache->rows, (int64_t)cache->n_pages * cache->page_size, latent_stride, key_stride, N, cache->latent_dim,
                       cache->rope_dim, interleaved, latent, key, slot, positions, phase, mscale};
     cudaStream_t s = (cudaStream_t)stream;

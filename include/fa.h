@@ -662,7 +662,8 @@ typedef struct {
  * fa_latent_write -- store N tokens' vectors in the slots of a slot map, the key part rotated first.
  *
  *   dtype           FA_DTYPE_* of latent and key
- *   latent, key     [N, latent_dim] and [N, rope_dim] with token strides (parts of one projection are fine)
+ *   latent, key     [N, latent_dim] and [N, rope_dim] with token strides (parts of one projection are fine), aligned to
+ *                   their type
  *   slot            [N] int32 as from fa_slot_map; a token whose slot is outside [0, n_pages * page_size) is left out
  *   positions       [N] int32 and phase [rope_dim / 2] as for fa_rope (all of the key part is rotated), or both NULL
  * Two tokens of one call must not share a slot.  Each element is rounded once.
