@@ -13,7 +13,8 @@
 // whether or not the drafter knew the automaton; a rejection of the others would take from the target what they cannot stand for.
 //
 // A draw compares u with a sum over the vocabulary, so everything is kept as unevaluated sums of two floats (Knuth's and
-// Dekker's exact additions and products, 46 bits or more): fp64 runs at two lanes a clock and SM here.
+// Dekker's exact additions and products, 46 bits or more): fp64 runs at two lanes a clock and SM here.  A row whose sum is far
+// from one is taken times a power of two, so that S_k / Q and the low parts stay within fp32's range.
 //
 // A cluster of blocks takes a sequence: each block a slice of the vocabulary, from node to node, so that only the rows of
 // nodes that are visited are read.  Every block gets every segment's sums and decides for itself, so that the cluster meets
@@ -153,6 +154,22 @@ __device__ __forceinline__ void left2(Two p, Two q, Two lh, Two ll, Two &high, T
     low = two(h.x > 0.0f ? l.x : 0.0f, h.y > 0.0f ? l.y : 0.0f);
 }
 
+// x 2^e for |e| < 250, by two powers that are floats themselves; exact but for bits below 2^-149
+__device__ __forceinline__ float scaled(float x, int e) {
+    auto power = [](int i) { return __int_as_float((127 + i) << 23); };
+    return x * power(e / 2) * power(e - e / 2);
+}
+// A sum beyond 2^48, not finite, or below 2^-48.  (Sums between leave quotients and products that fp32 holds with their low parts.
+// fp16's sums are all between: its weights lie within 2^-24 and 2^16, and a row has fewer than 2^31.)
+__device__ __forceinline__ bool far(float h) { return !(h >= 0x1p-48f && h < 0x1p48f); }
+// such a sum is brought near one if it is positive and finite; the power of two that this took
+__device__ __forceinline__ int settle(Sum &s) {
+    if (!far(s.h) || !(s.h > 0.0f && s.h < INFINITY)) return 0;
+    const int e = (__float_as_int(s.h) >> 23) - 127;
+    s = {scaled(s.h, -e), scaled(s.l, -e)};
+    return -e;
+}
+
 // x where it is a positive finite number, else 0
 __device__ __forceinline__ float weight(float x) { return __float_as_uint(x) - 1u < 0x7f7fffffu ? x : 0.0f; }
 
@@ -169,11 +186,12 @@ struct VerifyArgs {
 };
 
 struct Plan {          // what a block's first warp tells the others
-    int action;        // draw from segment `segment`, go to `node` with `state`, or sweep again with l
+    int action;        // draw from segment `segment`, go to `node` with `state`, or sweep again, with l or for other powers
     int node, state, segment, tried;
+    int ep, eq;        // powers of two by which both rows are multiplied
     Sum l, before, goal;   // the sum before the segment, and what the draw looks for
 };
-enum { DRAW = 0, NODE = 1, SWEEP = 2 };
+enum { DRAW = 0, NODE = 1, SWEEP = 2, RESUM = 3 };
 
 struct Shared {
     Plan plan;
@@ -320,9 +338,61 @@ template <class T, bool DRAFT> struct Node {
     }
 };
 
+// What few rows need lies apart from the kernel, which slows down with the code between its loops.
+
+// elements times 2^e
+template <class T> __device__ __noinline__ uint4 scaled_vector(uint4 x, int e) {
+    float f[fa_vec<T>::N];
+    fa_unpack(x, f, T());
+#pragma unroll
+    for (float &y : f) y = scaled(y, e);
+    return fa_pack(f, T());
+}
+// The sums of a segment of rows that are scaled, a vector at a time.
+struct Pair { Sum w, wq; };
+template <class T>
+__device__ __noinline__ Pair sweep_scaled(const T *p, const T *q, int V, const uint32_t *live, int words, Sum lam, int ep, int eq, bool fresh,
+                                          int c0, int c1, int lead, int chunks) {
+    const Node<T, true> at = {{p, V}, {q, V}, live, words, lead, chunks, 0, lam};
+    Sums run = {0ull, 0ull};
+    for (int c = c0 + (threadIdx.x & 31); c < c1; c += 32) {
+        uint4 x[1], y[1];
+        at.fetch(c, 32, c1, x, y);
+        x[0] = scaled_vector<T>(x[0], ep);
+        y[0] = scaled_vector<T>(y[0], eq);
+        if (fresh) at.template take<true, true>(run, x[0], y[0], at.bits(c));
+        else at.template take<false, true>(run, x[0], y[0], at.bits(c));
+    }
+    Pair r = {run.first(), run.second()};
+    if (!fresh) r.w = r.w + r.wq;
+    return r;
+}
+// Brings the sums of fresh rows near one where they are far from it: the row's segments (`each` a lane), and both sums.  A draft's
+// sum beyond fp32 is asked for again, of smaller weights (finite ones add up to no more than 2^159).
+struct Settled {
+    Sum total, total_q;
+    int ep, eq;
+    bool beyond;
+};
+__device__ __noinline__ Settled settle_rows(Sum *seg, int each, Sum total, Sum total_q, int eq, bool draft) {
+    Settled r = {total, total_q, 0, eq, false};
+    if (draft && !(total_q.h < INFINITY)) {
+        r.eq = -40;
+        r.beyond = eq == 0;
+        return r;
+    }
+    r.ep = __shfl_sync(0xffffffffu, settle(r.total), 0);
+    if (draft) r.eq += __shfl_sync(0xffffffffu, settle(r.total_q), 0);
+    const int i0 = (threadIdx.x & 31) * each;
+    for (int i = i0; i < i0 + each; ++i) seg[i] = {scaled(seg[i].h, r.ep), scaled(seg[i].l, r.ep)};
+    __syncwarp();
+    return r;
+}
+
 template <class T, bool DRAFT>
 __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
     constexpr int N = fa_vec<T>::N;
+    constexpr bool SCALES = !std::is_same<T, __half>::value;
     __shared__ Shared sh;
     extern __shared__ Child child[];
     float2 *pq = reinterpret_cast<float2 *>(child + a.T);   // the target's and the draft's weight
@@ -374,7 +444,8 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
     bool probing = false;                                // this sweep is a rejection's
     Sum total_q = {0.0f, 0.0f};
     int node = 0, state = a.S ? a.states[b] : 0;
-    bool fresh = true, first = true;
+    bool entered = true, fresh = true, first = true;     // a new node, sums with l = 0, the first turn
+    int ep = 0, eq = 0;
     Node<T, DRAFT> at;
     at.words = a.words;
     __syncthreads();
@@ -382,7 +453,7 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
         Sum *const seg = sh.seg[turn], *const seg_q = sh.seg_q[turn];
         // (nothing that a block reads for itself decides how often the cluster meets)
         const bool any = use > 0 && (!a.S || (unsigned)state < (unsigned)a.S);
-        if (fresh) {
+        if (entered) {
             at.p = {(const T *)a.target + b * a.tb + node * a.tr, a.V};
             at.q = {DRAFT ? (const T *)a.draft + b * a.db + node * a.dr : nullptr, a.V};
             at.live = a.S && any ? a.live + (int64_t)state * a.words : nullptr;
@@ -395,13 +466,17 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
         const int mine_too = node + 1 + tid;
         auto is_child = [&](int j) { return child[j].parent == node && (unsigned)child[j].token < (unsigned)a.V; };
         auto goes = [&](int j) { return any ? a.next[(int64_t)state * a.V + child[j].token] : -1; };
-        const bool moves = a.S && rank == 0 && fresh && mine_too < use && is_child(mine_too);
+        const bool moves = a.S && rank == 0 && entered && mine_too < use && is_child(mine_too);
         const int to = moves ? goes(mine_too) : -1;
         // ---- this warp's segment
         const int mine = rank * WARPS + warp, s0 = mine * at.per, s1 = min(s0 + at.per, at.chunks);
         Sum w = {0.0f, 0.0f}, wq = {0.0f, 0.0f};
         if (any) {
-            if (fresh || !DRAFT) {
+            if (DRAFT && SCALES && (ep | eq)) {
+                const Pair r = sweep_scaled<T>(at.p.p, at.q.p, a.V, at.live, at.words, at.lam, ep, eq, fresh, s0, s1, at.lead, at.chunks);
+                w = r.w;
+                wq = r.wq;
+            } else if (fresh || !DRAFT) {
                 if (at.live) at.template sweep<true, true>(s0, s1, w, wq);
                 else at.template sweep<true, false>(s0, s1, w, wq);
             } else {
@@ -425,7 +500,7 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
                 tell(pq + j, make_float2(weight(x.x), weight(x.y)));
             }
         }
-        if (a.S && rank == 0 && fresh)
+        if (a.S && rank == 0 && entered)
             for (int j = mine_too + NT; j < use; j += NT)
                 if (is_child(j)) tell(after + j, goes(j));
         first = false;
@@ -450,8 +525,19 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
             if (!DRAFT || !fresh) total = warp_sum(total);
             Plan plan = {};
             const bool some = total.h > 0.0f && total.h < INFINITY;
+            bool beyond = false;
+            if (SCALES && fresh && some && (far(total.h) || (DRAFT && far(total_q.h)))) {
+                const Settled r = settle_rows(seg, each, total, total_q, eq, DRAFT);
+                total = r.total;
+                total_q = r.total_q;
+                ep = r.ep;
+                eq = r.eq;
+                beyond = r.beyond;
+            }
             if (lane == 0) {
-                if (probing && !again && !(total.h > 0.0f)) {
+                if (beyond) {
+                    plan.action = RESUM;
+                } else if (probing && !again && !(total.h > 0.0f)) {
                     // nothing would be left: the distribution stays as it was
                     l = old_l;
                     plan.action = SWEEP;
@@ -465,7 +551,11 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
                         const Child x = child[j];
                         if (x.parent != node || (unsigned)x.token >= (unsigned)a.V) continue;
                         if (a.S && after[j] < 0) continue;           // not of the distributions that are compared
-                        const float p = pq[j].x, q = pq[j].y;
+                        float p = pq[j].x, q = pq[j].y;
+                        if (SCALES && (ep | eq)) {
+                            p = scaled(p, ep);
+                            q = scaled(q, eq);
+                        }
                         bool take, known = false;
                         Sum ratio = {0.0f, 0.0f};
                         if (DRAFT) {
@@ -546,15 +636,24 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
             plan.l.h = __shfl_sync(0xffffffffu, plan.l.h, 0);
             plan.l.l = __shfl_sync(0xffffffffu, plan.l.l, 0);
             plan.tried = __shfl_sync(0xffffffffu, n_tried, 0);
+            plan.ep = ep;
+            plan.eq = eq;
             if (lane == 0) sh.plan = plan;
         }
         __syncthreads();
         const int action = alike(sh.plan.action);
-        fresh = action == NODE;
-        if (action == NODE) {
+        entered = action == NODE;
+        fresh = entered || action == RESUM;
+        if (entered) {
             node = alike(sh.plan.node);
             state = alike(sh.plan.state);
+            ep = eq = 0;
             continue;
+        }
+        if (SCALES && alike(sh.plan.ep | sh.plan.eq)) {
+            ep = alike(sh.plan.ep);
+            eq = alike(sh.plan.eq);
+            if (action == RESUM) continue;
         }
         if (action == SWEEP) {
             at.lam = sh.plan.l;
@@ -575,6 +674,12 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
         Sum goal = sh.plan.goal;
         Sum before = sh.plan.before;
         Sum v[N];
+        auto scale = [&](auto &x, auto &y) {
+            if (SCALES && (ep | eq))
+                for (auto &v : x) v = scaled_vector<T>(v, ep);
+            if (SCALES && DRAFT && (ep | eq))
+                for (auto &v : y) v = scaled_vector<T>(v, eq);
+        };
         int held = -1;                                    // the last row with a weight so far
         bool found_row = false;
         for (int r0 = c0; r0 < c1; r0 += 32 * ROWS) {
@@ -584,6 +689,7 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
             uint32_t bits[U];
             const int c = r0 + tid;
             at.fetch(c, NT, c1, x, y);
+            scale(x, y);
 #pragma unroll
             for (int k = 0; k < U; ++k) bits[k] = c + NT * k < c1 ? at.bits(c + NT * k) : 0u;
 #pragma unroll
@@ -611,6 +717,7 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
             const int c = held + lane;
             uint4 x[1], y[1];
             at.fetch(c, 32, c1, x, y);
+            scale(x, y);
             const Sum sum = at.weigh(c, x[0], y[0], c < c1 ? at.bits(c) : 0u, v, tried, n), upto = warp_scan(lane ? sum : before + sum);
             const uint32_t past = __ballot_sync(0xffffffffu, sum.h > 0.0f && goal < upto), some = __ballot_sync(0xffffffffu, sum.h > 0.0f);
             const int pick = past ? __ffs(past) - 1 : 31 - __clz(some);
