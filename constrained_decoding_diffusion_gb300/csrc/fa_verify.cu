@@ -602,6 +602,7 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
             }
             plan.action = __shfl_sync(0xffffffffu, plan.action, 0);
             if (plan.action == DRAW) {
+                __syncwarp();                             // what the first lane took from segments is seen
                 // the segment that holds the draw
                 const Sum goal = {__shfl_sync(0xffffffffu, plan.goal.h, 0), __shfl_sync(0xffffffffu, plan.goal.l, 0)};
                 const int i0 = lane * each, i1 = i0 + each;
@@ -663,14 +664,13 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
     }
     // ---- the draw: the block that has the segment sums its rows of 32 vectors, and a warp takes the row that holds it
     // (nothing is read from or written to another block from here on: each may end)
-    const int segment = alike(sh.plan.segment);
-    if (segment < 0) {
+    const int segment = alike(sh.plan.segment), n = DRAFT ? 0 : alike(sh.plan.tried);
+    if (segment < 0 && n == 0) {
         if (rank == 0 && tid == 0) {
             a.token[b] = -1;
             if (a.state) a.state[b] = -1;
         }
-    } else if (rank == segment / WARPS) {
-        const int n = DRAFT ? 0 : sh.plan.tried, c0 = segment * at.per, c1 = min(c0 + at.per, at.chunks);
+    } else if (rank == max(segment, 0) / WARPS) {
         Sum goal = sh.plan.goal;
         Sum before = sh.plan.before;
         Sum v[N];
@@ -680,39 +680,53 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
             if (SCALES && DRAFT && (ep | eq))
                 for (auto &v : y) v = scaled_vector<T>(v, eq);
         };
+        // Where tried tokens have left a rounding of a segment and no other weight, the first weight behind it is the next token,
+        // or the last before it.
+        int c0 = max(segment, 0) * at.per, c1 = segment < 0 ? 0 : min(c0 + at.per, at.chunks);
         int held = -1;                                    // the last row with a weight so far
-        bool found_row = false;
-        for (int r0 = c0; r0 < c1; r0 += 32 * ROWS) {
-            constexpr int U = ROWS / WARPS;
-            Sum sums[U];
-            uint4 x[U], y[U];
-            uint32_t bits[U];
-            const int c = r0 + tid;
-            at.fetch(c, NT, c1, x, y);
-            scale(x, y);
+        for (int look = 0; look < (n ? 3 : 1) && held < 0; ++look) {
+            if (look == 1) {
+                c0 = c1;
+                c1 = at.chunks;
+                before = {0.0f, 0.0f};
+                goal = {-1.0f, 0.0f};
+            } else if (look == 2) {
+                c1 = segment * at.per;
+                c0 = 0;
+            }
+            bool found_row = false;
+            for (int r0 = c0; r0 < c1; r0 += 32 * ROWS) {
+                constexpr int U = ROWS / WARPS;
+                Sum sums[U];
+                uint4 x[U], y[U];
+                uint32_t bits[U];
+                const int c = r0 + tid;
+                at.fetch(c, NT, c1, x, y);
+                scale(x, y);
 #pragma unroll
-            for (int k = 0; k < U; ++k) bits[k] = c + NT * k < c1 ? at.bits(c + NT * k) : 0u;
+                for (int k = 0; k < U; ++k) bits[k] = c + NT * k < c1 ? at.bits(c + NT * k) : 0u;
 #pragma unroll
-            for (int k = 0; k < U; ++k) sums[k] = at.weigh(c + NT * k, x[k], y[k], bits[k], v, tried, n);
+                for (int k = 0; k < U; ++k) sums[k] = at.weigh(c + NT * k, x[k], y[k], bits[k], v, tried, n);
 #pragma unroll
-            for (int k = 0; k < ROWS / WARPS; k += 2) warp_sums(sums[k], sums[k + 1]);
-            __syncthreads();                              // the last rows' sums have been read
-            if (lane == 0)
+                for (int k = 0; k < ROWS / WARPS; k += 2) warp_sums(sums[k], sums[k + 1]);
+                __syncthreads();                          // the last rows' sums have been read
+                if (lane == 0)
 #pragma unroll
-                for (int k = 0; k < ROWS / WARPS; ++k) sh.row[warp + WARPS * k] = sums[k];
-            __syncthreads();
-            // the rows' sums in the lanes
-            const Sum mine = sh.row[lane], upto = warp_scan(lane ? mine : before + mine);
-            const uint32_t holds = __ballot_sync(0xffffffffu, mine.h > 0.0f && goal < upto), some = __ballot_sync(0xffffffffu, mine.h > 0.0f);
-            if (some) held = r0 + 32 * (31 - __clz(some));
-            const int who = holds ? __ffs(holds) - 1 : 31;
-            if (holds) held = r0 + 32 * who;
-            const int prior = holds ? who - 1 : 31;
-            const Sum next = {__shfl_sync(0xffffffffu, upto.h, max(prior, 0)), __shfl_sync(0xffffffffu, upto.l, max(prior, 0))};
-            if (prior >= 0) before = next;
-            if (holds) { found_row = true; break; }
+                    for (int k = 0; k < ROWS / WARPS; ++k) sh.row[warp + WARPS * k] = sums[k];
+                __syncthreads();
+                // the rows' sums in the lanes
+                const Sum mine = sh.row[lane], upto = warp_scan(lane ? mine : before + mine);
+                const uint32_t holds = __ballot_sync(0xffffffffu, mine.h > 0.0f && goal < upto), some = __ballot_sync(0xffffffffu, mine.h > 0.0f);
+                if (some) held = r0 + 32 * (31 - __clz(some));
+                const int who = holds ? __ffs(holds) - 1 : 31;
+                if (holds) held = r0 + 32 * who;
+                const int prior = holds ? who - 1 : 31;
+                const Sum next = {__shfl_sync(0xffffffffu, upto.h, max(prior, 0)), __shfl_sync(0xffffffffu, upto.l, max(prior, 0))};
+                if (prior >= 0) before = next;
+                if (holds) { found_row = true; break; }
+            }
+            if (!found_row) goal = {INFINITY, 0.0f};   // rounding hid the draw: the last element with a weight
         }
-        if (!found_row) goal = {INFINITY, 0.0f};          // rounding hid the draw: the last element with a weight
         if (warp == 0 && held >= 0) {
             const int c = held + lane;
             uint4 x[1], y[1];
@@ -736,7 +750,7 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
                 a.token[b] = found;
                 if (a.state) a.state[b] = a.next[(int64_t)state * a.V + found];
             }
-        } else if (tid == 0 && held < 0) {                // all that weighed was tried, and roundings are left of its sum
+        } else if (tid == 0 && held < 0) {                // all that weighed has been tried
             a.token[b] = -1;
             if (a.state) a.state[b] = -1;
         }

@@ -591,7 +591,7 @@ fa_status fa_beam_reorder(int32_t N, int32_t K, int32_t top, int64_t words, cons
  *   path          [B, T] int32 out: node 0, the accepted nodes, then -1 (as fa_cache_keep takes it)
  *   kept          [B] int32 out: nodes on the path
  *   token         [B] int32 out: the next token, -1 where the last distribution is empty (no weight, a
- *                 target's sum beyond fp32, or one of which rejections have left roundings alone)
+ *                 target's sum beyond fp32, or one of which every token with a weight has been tried)
  *   state         [B] int32 out: the state after it (-1 without one), NULL without an automaton
  * Sums and differences carry 46 bits or more, whatever the rows' scales (each is brought near a sum of one), so that a draw is
  * that of 64-bit arithmetic but for about one in 10^8.  A rejection that would leave nothing (rounding alone can do it) leaves r as it is.
