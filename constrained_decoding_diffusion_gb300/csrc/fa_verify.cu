@@ -72,7 +72,10 @@ __device__ __forceinline__ Two sub2(Two a, Two b) { Two r; asm("sub.rn.f32x2 %0,
 __device__ __forceinline__ Two mul2(Two a, Two b) { Two r; asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b)); return r; }
 __device__ __forceinline__ Two fma2(Two a, Two b, Two c) { Two r; asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c)); return r; }
 
-// two running sums: what each addition loses is added up apart (a few dozen terms lose less than 2^-46 of a sum)
+// Two running sums: what each addition loses is added up apart.  Every few dozen terms the low parts are folded into the high
+// ones: they would else grow with the terms and lose bits of their own.  Emulated in fp32, log-normal weights (sigma 4),
+// 2048 lanes: a row's sum is off by 2^-41 at V = 10^7 and 2^-38 at 2.4 10^7 without it, by 2^-47 and 2^-48 with it;
+// 64 x 9 x 151936 91.1 -> 91.4 us.
 struct Sums {
     Two h, l;
     __device__ __forceinline__ void add(Two b) {
@@ -83,6 +86,11 @@ struct Sums {
     __device__ __forceinline__ void add(Two b, Two low) {
         add(b);
         l = add2(l, low);
+    }
+    __device__ __forceinline__ void fold() {
+        const Two s = add2(h, l);
+        l = sub2(l, sub2(s, h));
+        h = s;
     }
     __device__ __forceinline__ Sum first() const { return fast_two_sum(apart(h).x, apart(l).x); }
     __device__ __forceinline__ Sum second() const { return fast_two_sum(apart(h).y, apart(l).y); }
@@ -312,6 +320,7 @@ template <class T, bool DRAFT> struct Node {
             fetch(c, 32, c1, x, y);
 #pragma unroll
             for (int k = 0; k < U; ++k) take<FRESH, LIVE>(run, x[k], y[k], b[k]);
+            run.fold();
         }
         w = run.first();
         wq = run.second();
@@ -362,6 +371,7 @@ __device__ __noinline__ Pair sweep_scaled(const T *p, const T *q, int V, const u
         y[0] = scaled_vector<T>(y[0], eq);
         if (fresh) at.template take<true, true>(run, x[0], y[0], at.bits(c));
         else at.template take<false, true>(run, x[0], y[0], at.bits(c));
+        run.fold();
     }
     Pair r = {run.first(), run.second()};
     if (!fresh) r.w = r.w + r.wq;

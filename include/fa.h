@@ -593,8 +593,8 @@ fa_status fa_beam_reorder(int32_t N, int32_t K, int32_t top, int64_t words, cons
  *   token         [B] int32 out: the next token, -1 where the last distribution is empty (no weight, a
  *                 target's sum beyond fp32, or one of which every token with a weight has been tried)
  *   state         [B] int32 out: the state after it (-1 without one), NULL without an automaton
- * Sums and differences carry 46 bits or more, whatever the rows' scales (each is brought near a sum of one), so that a draw is
- * that of 64-bit arithmetic but for about one in 10^8.  A rejection that would leave nothing (rounding alone can do it) leaves r as it is.
+ * Sums and differences carry 46 bits or more (45 from V = 2^30 on; roundings taken as independent), whatever the rows'
+ * scales (each is brought near a sum of one), so that a draw is that of 64-bit arithmetic but for about one in 10^8.  A rejection that would leave nothing (rounding alone can do it) leaves r as it is.
  * T <= FA_MAX_DRAFT, B <= 65535, V < 2^31 - 2^16.  Errors: FA_ERR_INVALID_ARG, FA_ERR_CUDA.
  */
 fa_status fa_verify(int32_t dtype, int32_t B, int32_t T, int32_t V, const void *target, int64_t target_batch_stride,
