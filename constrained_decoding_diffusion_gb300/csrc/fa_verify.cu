@@ -31,9 +31,12 @@
 // these are added up (10% slower, registers), three blocks an SM with fewer vectors under way (8 to 15% slower), arrivals on
 // barriers in the other blocks' memory for the cluster's (equal: either waits for the stores before), one block that decides
 // and tells the others in a second meeting (5 to 9% slower).
+#include <atomic>
+
 #include <cooperative_groups.h>
 
 #include "fa_lm.cuh"
+#include "fa_verify_blocks.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -773,19 +776,44 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
     }
 }
 
-template <class T, bool DRAFT> void launch(const VerifyArgs &a, int cluster, cudaStream_t s) {
-    cudaLaunchAttribute at[1];
+template <class T, bool DRAFT> cudaLaunchConfig_t config(cudaLaunchAttribute *at, int B, int cluster, int tokens, cudaStream_t s) {
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = cluster;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t c = {};
-    c.gridDim = dim3((unsigned)a.B * cluster);
+    c.gridDim = dim3((unsigned)B * cluster);
     c.blockDim = dim3(NT);
-    c.dynamicSmemBytes = a.T * kBytesOfToken;
+    c.dynamicSmemBytes = tokens * kBytesOfToken;
     c.stream = s;
     c.attrs = at;
     c.numAttrs = 1;
-    if (cluster > 8) (void)cudaFuncSetAttribute(k_verify<T, DRAFT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    return c;
+}
+
+// The clusters of sixteen blocks that the current device runs at a time: 0 where it has none that large, which is beyond the portable
+// size.  Asked once a device, for the longest draft.
+template <class T, bool DRAFT> int wide_clusters() {
+    constexpr int DEVICES = 64;
+    static std::atomic<int> known[DEVICES];               // one more than the answer
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) dev = DEVICES;
+    if (dev < DEVICES && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n - 1;
+    cudaLaunchAttribute at[1];
+    const cudaLaunchConfig_t c = config<T, DRAFT>(at, 1, MAX_CLUSTER, FA_MAX_DRAFT, nullptr);
+    cudaError_t e = cudaFuncSetAttribute(k_verify<T, DRAFT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, k_verify<T, DRAFT>, &c);
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();                         // the launch's own is the one that counts
+        n = 0;
+    }
+    if (dev < DEVICES) known[dev].store(n + 1, std::memory_order_relaxed);
+    return n;
+}
+
+template <class T, bool DRAFT> void launch(const VerifyArgs &a, cudaStream_t s) {
+    const int wide = a.V >= 98304 ? wide_clusters<T, DRAFT>() : 0;
+    cudaLaunchAttribute at[1];
+    const cudaLaunchConfig_t c = config<T, DRAFT>(at, a.B, fa_verify_blocks(a.B, a.V, wide), a.T, s);
     (void)cudaLaunchKernelEx(&c, k_verify<T, DRAFT>, a);   // its error is the one the check reads
 }
 
@@ -809,21 +837,10 @@ extern "C" fa_status fa_verify(int32_t dtype, int32_t B, int32_t T, int32_t V, c
     if (((uintptr_t)target | (uintptr_t)draft) % es) return fa_refuse(fn, "target and draft must be aligned to their type");
     const VerifyArgs a{B, T, V, S, (V + 31) / 32, target, draft, target_batch_stride, target_row_stride, draft_batch_stride,
                        draft_row_stride, tokens, parents, count, u, states, next, live, path, kept, token, S > 0 ? state : nullptr};
-    // Blocks of a sequence: eight where the vocabulary gives each thread some work (1 / 2 / 4 / 8 blocks, 8 sequences of
-    // 5 x 32000: 46 / 34 / 23 / 19 us, of 5 x 8000 27 / 23 / 23 / 22), fewer where that would take more than two rounds of
-    // blocks for short sweeps (64 sequences of 5 x 32000 48 / 36 / 31 / 46 us, of 5 x 8000 28 / 24 / 25 / 43, but of
-    // 9 x 151936 335 / 185 / 120 / 85).  Sixteen where a few sequences have long sweeps: 8 / 16 blocks, 4 sequences of 5 x
-    // 102400 27.3 / 25.4, 12 26.6 / 28.9, 16 28.9 / 37.3; of 5 x 262144 36.6 / 28.9, 44.1 / 38.0, 47.6 / 45.1, 18 55.6 / 56.5;
-    // trees of 17 x 151936 bf16 under an automaton, 1 / 8 / 16 / 24 of them: 13.9 / 34.0 / 31.0 / 34.8 against 12.5 / 25.8 /
-    // 25.3 / 31.9.
-    int cluster = 8;
-    if (V >= 98304 && B <= std::min(16, V / 8192)) cluster = 16;
-    else
-        while (cluster > 1 && (V < 2048 * cluster || (V < 65536 && B * cluster > 2 * 152))) cluster /= 2;
     auto go = [&](auto tag) {
         using T_ = decltype(tag);
-        if (draft) launch<T_, true>(a, cluster, (cudaStream_t)stream);
-        else launch<T_, false>(a, cluster, (cudaStream_t)stream);
+        if (draft) launch<T_, true>(a, (cudaStream_t)stream);
+        else launch<T_, false>(a, (cudaStream_t)stream);
     };
     if (dtype == FA_DTYPE_F32) go(0.0f);
     else if (dtype == FA_DTYPE_F16) go(__half());
