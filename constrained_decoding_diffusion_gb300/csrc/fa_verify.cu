@@ -813,7 +813,7 @@ template <class T, bool DRAFT> int wide_clusters() {
 template <class T, bool DRAFT> void launch(const VerifyArgs &a, cudaStream_t s) {
     const int wide = a.V >= 98304 ? wide_clusters<T, DRAFT>() : 0;
     cudaLaunchAttribute at[1];
-    const cudaLaunchConfig_t c = config<T, DRAFT>(at, a.B, fa_verify_blocks(a.B, a.V, wide), a.T, s);
+    const cudaLaunchConfig_t c = config<T, DRAFT>(at, a.B, fa_verify_blocks(a.B, a.V, sizeof(T), DRAFT, a.S > 0, wide), a.T, s);
     (void)cudaLaunchKernelEx(&c, k_verify<T, DRAFT>, a);   // its error is the one the check reads
 }
 
