@@ -65,16 +65,19 @@ class Drafting:
     not yet in the cache (-1: the sequence has ended), `state` [B] the automaton's state after it.
 
     With a generator tokens are drawn from the softmax of the layer's logits / temperature under the automaton,
-    else the best one is taken.  n_pages is the size of the pool (enough for all sequences and their drafts by
+    else the best one is taken.  cache_dtype is that of the keys and values, float8_e4m3fn by default; a latent cache has its
+    layer's type.  n_pages is the size of the pool (enough for all sequences and their drafts by
     default): a sequence whose draft finds no pages sits the round out.  Texts keep their pages until release(), so
     the pool must hold all of them and one draft, or a round comes in which nobody moves."""
 
     def __init__(self, aut: native.CompiledAutomaton, layer, first, start_state: int, beams: int = 4, depth: int = 4,
-                 max_length: int = 1024, page_size: int = 16, cache_dtype=torch.float8_e4m3fn, n_pages=None, generator=None,
+                 max_length: int = 1024, page_size: int = 16, cache_dtype=None, n_pages=None, generator=None,
                  temperature: float = 1.0):
         B, K = first.shape[0], beams
         (V, _), (_, H, D) = layer.embed.shape, layer.wq.shape
         self.latent = isinstance(layer, LatentLayer)
+        if self.latent and cache_dtype not in (None, layer.wq.dtype):
+            raise TypeError("a latent cache has its layer's type, %s, not %s" % (layer.wq.dtype, cache_dtype))
         if depth < 1 or 1 + K * depth > lm.FA_MAX_DRAFT:
             raise ValueError("beams * depth must be in [1, %d)" % lm.FA_MAX_DRAFT)
         self.layer, self.beams, self.depth, self.max_length = layer, K, depth, max_length
@@ -91,7 +94,7 @@ class Drafting:
             self.drafted = torch.full((B,), T, **i32)
         else:
             KV = layer.wk.shape[1]
-            self.cache = lm.KVCache.empty(n_pages, KV, page_size, D, cache_dtype)
+            self.cache = lm.KVCache.empty(n_pages, KV, page_size, D, torch.float8_e4m3fn if cache_dtype is None else cache_dtype)
             self.attend = lm.TreeAttention(B, T, H, KV, D, layer.wq.dtype)
         self.phase, _ = lm.rope_phases(D - L if self.latent else D)
         self.next, self.live = lm.fa_beam_tables(aut)
