@@ -67,8 +67,9 @@ class Drafting:
     With a generator tokens are drawn from the softmax of the layer's logits / temperature under the automaton,
     else the best one is taken.  cache_dtype is that of the keys and values, float8_e4m3fn by default; a latent cache has its
     layer's type.  n_pages is the size of the pool (enough for all sequences and their drafts by
-    default): a sequence whose draft finds no pages sits the round out.  Texts keep their pages until release(), so
-    the pool must hold all of them and one draft, or a round comes in which nobody moves."""
+    default): a sequence whose draft finds no pages sits the round out (`waits` [B]).  Texts keep their pages until
+    release(), so the pool must hold all of them and one draft, or a round comes in which nobody moves: stuck() says so, and
+    release() may help where some texts have ended."""
 
     def __init__(self, aut: native.CompiledAutomaton, layer, first, start_state: int, beams: int = 4, depth: int = 4,
                  max_length: int = 1024, page_size: int = 16, cache_dtype=None, n_pages=None, generator=None,
@@ -82,6 +83,8 @@ class Drafting:
             raise ValueError("beams * depth must be in [1, %d)" % lm.FA_MAX_DRAFT)
         self.layer, self.beams, self.depth, self.max_length = layer, K, depth, max_length
         T = 1 + K * depth                                  # the pending token, then the beams, one after another
+        if n_pages is not None and n_pages * page_size < T:
+            raise ValueError("a pool of %d pages of %d slots cannot hold a draft of %d tokens" % (n_pages, page_size, T))
         per = -(-(max_length + T) // page_size)
         i32 = dict(dtype=torch.int32, device="cuda")
         self.pages = lm.PageTables.empty(B, per, B * per if n_pages is None else n_pages, page_size)
@@ -113,6 +116,7 @@ class Drafting:
             self.nothing = torch.zeros((B * T, 1), device="cuda")
         self.pending = first.to(**i32)
         self.state = self._move(torch.full((B,), start_state, **i32), self.pending)
+        self.waits = self.moved = torch.zeros(B, dtype=torch.bool, device="cuda")   # of the last round
         self.text = []                                     # [B, at most 1 + depth] of each round, -1 where there is none
 
     def _move(self, state, token):
@@ -189,8 +193,10 @@ class Drafting:
         tokens = torch.cat((self.pending.view(B, 1), hist.view(B, K * depth)), 1)
         T = tokens.shape[1]
         alive = self.pending >= 0
-        room = lm.fa_pages_resize(self.pages, self.length + T * alive.int())
-        alive &= room == lm.FA_PAGES_OK
+        room = lm.fa_pages_resize(self.pages, self.length + T * alive.int()) == lm.FA_PAGES_OK
+        self.waits = alive & ~room
+        alive &= room
+        self.moved = alive.clone()
         count = torch.where(alive, T, 0).int()
         logits = self.logits(tokens, count)
         path, token, after = self.best(logits, tokens, hist) if self.generator is None else self.drawn(logits, tokens, count)
@@ -209,6 +215,11 @@ class Drafting:
         """The pages of sequences that have ended go back to the pool, and their texts leave the cache."""
         self.length = torch.where(self.pending >= 0, self.length, 0)
         lm.fa_pages_resize(self.pages, self.length)
+
+    def stuck(self) -> bool:
+        """Whether the last round moved nobody for want of pages, so that the next one will not either unless pages are
+        released (reads the device)."""
+        return bool(self.waits.any() & ~self.moved.any())
 
     def round(self, drafter):
         """drafter(pending [B]) -> log-probabilities [B, depth, V] of the positions after pending."""
@@ -231,6 +242,8 @@ def main():
     rounds = 0
     while bool((run.pending >= 0).any()) and rounds < 200:
         run.round(drafter)
+        if run.stuck():
+            raise SystemExit("the pool holds none of the drafts that are left")
         rounds += 1
     print("%d rounds, lengths %s" % (rounds, run.length.tolist()))
 

@@ -14,3 +14,8 @@ def latent_layer(dtype=torch.bfloat16):
 def test_a_latent_cache_of_another_type(dtype, cache):
     with pytest.raises(TypeError, match="latent cache"):
         drafting.Drafting(None, latent_layer(dtype), torch.zeros(2, dtype=torch.int32), 0, cache_dtype=cache)
+
+
+def test_a_pool_that_holds_no_draft():
+    with pytest.raises(ValueError, match="draft of 13 tokens"):
+        drafting.Drafting(None, latent_layer(), torch.zeros(2, dtype=torch.int32), 0, beams=4, depth=3, page_size=4, n_pages=3)
