@@ -5,7 +5,8 @@ block does.  Beams over them that stay inside the automaton become a tree of dra
 attention layer verifies the whole tree in a single pass over its paged cache, and the longest path
 that agrees with the layer's own choices is kept.  The text is that of choosing one token at a time,
 the best one or a random one; the draft only decides how many come from one pass.  The sequences share a
-pool of pages: each has those that its text takes, and for the length of a pass those of its draft.
+pool of pages: each has those that its text takes, and for the length of a pass those of its draft (or, of a pool
+with room for all, those of its longest text from the start).
 
     python -m constrained_decoding_diffusion_gb300.drafting
 """
@@ -87,9 +88,12 @@ class Drafting:
             raise ValueError("a pool of %d pages of %d slots cannot hold a draft of %d tokens" % (n_pages, page_size, T))
         per = -(-(max_length + T) // page_size)
         i32 = dict(dtype=torch.int32, device="cuda")
-        self.pages = lm.PageTables.empty(B, per, B * per if n_pages is None else n_pages, page_size)
-        self.table, n_pages = self.pages.table, self.pages.free.shape[0]
+        self._pages = lm.PageTables.empty(B, per, B * per if n_pages is None else n_pages, page_size)
+        self.table, n_pages = self._pages.table, self._pages.free.shape[0]
         self.length = torch.zeros(B, **i32)
+        self.dealt = n_pages >= B * per
+        if self.dealt:                                     # room for every text and its draft: no round need ask for pages
+            lm.fa_pages_resize(self._pages, torch.full((B,), per * page_size, **i32))
         if self.latent:
             L = layer.latent_dim
             self.cache = lm.LatentCache.empty(n_pages, page_size, L, D - L, layer.wq.dtype)
@@ -118,6 +122,15 @@ class Drafting:
         self.state = self._move(torch.full((B,), start_state, **i32), self.pending)
         self.waits = self.moved = torch.zeros(B, dtype=torch.bool, device="cuda")   # of the last round
         self.text = []                                     # [B, at most 1 + depth] of each round, -1 where there is none
+
+    @property
+    def pages(self) -> lm.PageTables:
+        """The pool, and the pages that each text takes.  A pool with room for everything is dealt out at the start; from the
+        first look at it on, pages go round by round, as from a smaller one."""
+        if self.dealt:
+            self.dealt = False
+            lm.fa_pages_resize(self._pages, self.length)
+        return self._pages
 
     def _move(self, state, token):
         """The automaton's next state, -1 from and by -1."""
@@ -148,7 +161,7 @@ class Drafting:
             turned = q.view(B * T, *q.shape[2:])[..., L:]
             lm.fa_rope(turned, positions.view(-1), self.phase, out=turned)
             down = (x @ self.layer.down).view(B * T, -1)
-            slot, _, _, _ = lm.fa_slot_map(self.pages, self.length, self.drafted, B * T)
+            slot, _, _, _ = lm.fa_slot_map(self._pages, self.length, self.drafted, B * T)
             lm.fa_latent_write(self.cache, down[:, :L], down[:, L:], slot, positions.view(-1), self.phase)
             out, _ = self.attend(q, self.cache, self.table, self.length, scale, self.mask, count)
         else:
@@ -193,10 +206,11 @@ class Drafting:
         tokens = torch.cat((self.pending.view(B, 1), hist.view(B, K * depth)), 1)
         T = tokens.shape[1]
         alive = self.pending >= 0
-        room = lm.fa_pages_resize(self.pages, self.length + T * alive.int()) == lm.FA_PAGES_OK
-        self.waits = alive & ~room
-        alive &= room
-        self.moved = alive.clone()
+        if not self.dealt:
+            room = lm.fa_pages_resize(self._pages, self.length + T * alive.int()) == lm.FA_PAGES_OK
+            self.waits = alive & ~room
+            alive &= room
+        self.moved = alive
         count = torch.where(alive, T, 0).int()
         logits = self.logits(tokens, count)
         path, token, after = self.best(logits, tokens, hist) if self.generator is None else self.drawn(logits, tokens, count)
@@ -204,7 +218,8 @@ class Drafting:
         (lm.fa_latent_keep if self.latent else lm.fa_cache_keep)(self.cache, self.table, self.length, path)
         joined = torch.where(path >= 0, tokens.gather(1, path.clamp(min=0).long()), -1)
         self.length += (path >= 0).sum(1).int()
-        lm.fa_pages_resize(self.pages, self.length)
+        if not self.dealt:
+            lm.fa_pages_resize(self._pages, self.length)
         done = alive & (self.length >= self.max_length)
         self.state = torch.where(done, -1, torch.where(alive, after, self.state))
         self.pending = torch.where(done, -1, torch.where(alive, token, self.pending))
@@ -214,7 +229,8 @@ class Drafting:
     def release(self):
         """The pages of sequences that have ended go back to the pool, and their texts leave the cache."""
         self.length = torch.where(self.pending >= 0, self.length, 0)
-        lm.fa_pages_resize(self.pages, self.length)
+        if not self.dealt:
+            lm.fa_pages_resize(self._pages, self.length)
 
     def stuck(self) -> bool:
         """Whether the last round moved nobody for want of pages, so that the next one will not either unless pages are
