@@ -590,33 +590,16 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
     if (warp == 4) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-// Joins the parts of units that were cut, in an order that depends on nothing but the lengths.  Block (unit, N rows):
-// 8 / N warps share a row's parts, their lanes across the columns, and their sums are added up.
+// The rows of a unit whose tiles lie in the runs c0 to c1: 8 / N warps share a row's parts, their lanes across the columns, and their
+// sums are added up.
+template <int L, class T, int N> struct JoinMemory {
+    float4 sums[8 / N > 1 ? 8 : 1][L / 128][32];
+    float totals[8];
+};
 template <int L, class T, int N>
-__global__ void __launch_bounds__(256) k_latent_join(AttendArgs a, int runs) {
+__device__ __forceinline__ void join_unit(const AttendArgs &a, int b, int block, int c0, int c1, int row, int rows, JoinMemory<L, T, N> &sh) {
     constexpr int SUBS = 8 / N, V = L / 128;               // vectors of four columns a lane
-    __shared__ Work work;
-    __shared__ int before;
-    __shared__ float4 sums[SUBS > 1 ? 8 : 1][V][32];
-    __shared__ float totals[8];
-    plan(a, work);
-    const int b = (int)(blockIdx.x / a.blocks), block = (int)(blockIdx.x % a.blocks);
-    if (threadIdx.x == 0) {
-        const int per = run_length(a);
-        int g = work.cum[b / per];
-        for (int i = b / per * per; i < b; ++i) g += places_of(a, i);
-        before = g;
-    }
-    __syncthreads();
-    const int nt = tiles_of(a, b), total = work.cum[RUNS] * a.blocks, g0 = before * a.blocks + block * (nt + a.unit_cost), g1 = g0 + nt - 1;
-    runs = min(total, runs);
-    // the runs that hold the unit's first and last tile
-    const int c0 = (int)((((int64_t)g0 + 1) * runs - 1) / total), c1 = (int)((((int64_t)g1 + 1) * runs - 1) / total);
-    // (the warp's number by way of a shuffle, as above: 16 x 4096 slots x 1024 rows 215 -> 212 us)
-    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), parts = c1 - c0 + 1;
-    const int rows = min(a.rows - RB * block, RB), row = N * blockIdx.y + warp / SUBS, sub = warp % SUBS;
-    fa_wait_for_previous();                                // by every block: the next kernel waits for this one only
-    if (N * (int)blockIdx.y >= rows) return;
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), sub = warp % SUBS, parts = c1 - c0 + 1;
     bool failed = false;
     for (int c = c0; c <= c1; ++c) failed |= a.status[c] != 0;
     if (parts == 1 && !failed) return;
@@ -649,16 +632,16 @@ __global__ void __launch_bounds__(256) k_latent_join(AttendArgs a, int runs) {
     }
     if (SUBS > 1) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) sums[warp][v][lane] = o[v];
-        if (lane == 0) totals[warp] = l;
+        for (int v = 0; v < V; ++v) sh.sums[warp][v][lane] = o[v];
+        if (lane == 0) sh.totals[warp] = l;
         __syncthreads();
         if (sub) return;
 #pragma unroll
         for (int i = 1; i < SUBS; ++i) {
-            l += totals[warp + i];
+            l += sh.totals[warp + i];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float4 y = sums[warp + i][v][lane];
+                const float4 y = sh.sums[warp + i][v][lane];
                 o[v].x += y.x; o[v].y += y.y; o[v].z += y.z; o[v].w += y.w;
             }
         }
@@ -671,6 +654,66 @@ __global__ void __launch_bounds__(256) k_latent_join(AttendArgs a, int runs) {
         *reinterpret_cast<uint2 *>((T *)a.out + at * L + 128 * v + 4 * lane) =
             make_uint2(fa_pack2(o[v].x * inv, o[v].y * inv, T()), fa_pack2(o[v].z * inv, o[v].w * inv, T()));
     if (a.lse && lane == 0) a.lse[at] = failed ? NAN : l == 0.0f ? -INFINITY : (top + log2f(l)) * kLn2;
+}
+
+// Joins the parts of units that were cut, in an order that depends on nothing but the lengths.  Block (unit, N rows).
+template <int L, class T, int N>
+__global__ void __launch_bounds__(256) k_latent_join(AttendArgs a, int runs) {
+    constexpr int SUBS = 8 / N;
+    __shared__ Work work;
+    __shared__ int before;
+    __shared__ JoinMemory<L, T, N> sh;
+    plan(a, work);
+    const int b = (int)(blockIdx.x / a.blocks), block = (int)(blockIdx.x % a.blocks);
+    if (threadIdx.x == 0) {
+        const int per = run_length(a);
+        int g = work.cum[b / per];
+        for (int i = b / per * per; i < b; ++i) g += places_of(a, i);
+        before = g;
+    }
+    __syncthreads();
+    const int nt = tiles_of(a, b), total = work.cum[RUNS] * a.blocks, g0 = before * a.blocks + block * (nt + a.unit_cost), g1 = g0 + nt - 1;
+    runs = min(total, runs);
+    // the runs that hold the unit's first and last tile
+    const int c0 = (int)((((int64_t)g0 + 1) * runs - 1) / total), c1 = (int)((((int64_t)g1 + 1) * runs - 1) / total);
+    // (the warp's number by way of a shuffle, as above: 16 x 4096 slots x 1024 rows 215 -> 212 us)
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+    const int rows = min(a.rows - RB * block, RB), row = N * blockIdx.y + warp / SUBS;
+    fa_wait_for_previous();                                // by every block: the next kernel waits for this one only
+    if (N * (int)blockIdx.y >= rows) return;
+    join_unit<L, T, N>(a, b, block, c0, c1, row, rows, sh);
+}
+
+// The same of many sequences.  Every block makes the plan, so with a block a unit the work grows with the square of the sequences;
+// the units that are cut are fewer than the runs, and here block x looks at run x: it joins the unit that the run begins in, if it is
+// the first to, and looks after the whole units of a run that failed.  A block a unit / a run, B sequences of 64 slots x 16 rows:
+// 256 23.0 / 21.3 us, 1024 43.6 / 38.6, 4096 245 / 130, 16384 2302 / 482, 65535 32746 / 1908, but 16 x 4096 slots x 1024
+// rows (256 units) 213.8 / 216.2.
+constexpr int kManySequences = 512;                        // (more than the runs)
+template <int L, class T>
+__global__ void __launch_bounds__(256) k_latent_join_many(AttendArgs a, int runs) {
+    __shared__ Work work;
+    __shared__ JoinMemory<L, T, 8> sh;
+    plan(a, work);
+    const int lane = threadIdx.x & 31, run = blockIdx.x, row = 8 * blockIdx.y + (threadIdx.x >> 5), total = work.cum[RUNS] * a.blocks;
+    Walk walk(a, work, run, runs);
+    runs = min(total, runs);
+    fa_wait_for_previous();
+    if (run >= runs) return;
+    const int b = walk.b, block = walk.block, nt = tiles_of(a, b), g0 = run_start(total, run, runs) - walk.t0, g1 = g0 + nt - 1;
+    const bool cut = walk.t0 > 0 && walk.t0 < nt;
+    if (a.status[run] != 0) {
+        Segment s;
+        while (walk.next(a, s)) {
+            if (s.n < s.nt || row >= min(a.rows - RB * s.block, RB)) continue;
+            const int64_t at = (int64_t)s.b * a.T * a.heads + RB * s.block + row;
+            for (int c = lane; c < L; c += 32) ((T *)a.out)[at * L + c] = fa_from_f32<T>(NAN);
+            if (a.lse && lane == 0) a.lse[at] = NAN;
+        }
+    }
+    const int c0 = (int)((((int64_t)g0 + 1) * runs - 1) / total), c1 = (int)((((int64_t)g1 + 1) * runs - 1) / total);
+    const int rows = min(a.rows - RB * block, RB);
+    if (cut && c0 == run - 1 && 8 * (int)blockIdx.y < rows) join_unit<L, T, 8>(a, b, block, c0, c1, row, rows, sh);
 }
 
 // two partial results of 64 rows and a status for each block
@@ -706,6 +749,8 @@ template <int L, class T, int QR> fa_status launch(AttendArgs a, const CUtensorM
     // warps than a row of an evenly cut list has parts.
     int n = 1;
     while (n < 8 && (units * ((rows + n - 1) / n) > 8 * MAX_CTAS || 8 / n > ctas / units)) n *= 2;
+    if (a.B >= kManySequences)
+        return fa_launch_second("latent attention join", k_latent_join_many<L, T>, dim3((unsigned)ctas, (unsigned)((rows + 7) / 8)), 256, 0, s, a, ctas);
     void (*const join)(AttendArgs, int) = n == 1 ? k_latent_join<L, T, 1> : n == 2 ? k_latent_join<L, T, 2> : n == 4 ? k_latent_join<L, T, 4> : k_latent_join<L, T, 8>;
     return fa_launch_second("latent attention join", join, dim3((unsigned)units, (unsigned)((rows + n - 1) / n)), 256, 0, s, a, ctas);
 }
