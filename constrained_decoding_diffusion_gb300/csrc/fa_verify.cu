@@ -77,8 +77,8 @@ __device__ __forceinline__ Two fma2(Two a, Two b, Two c) { Two r; asm("fma.rn.f3
 
 // Two running sums: what each addition loses is added up apart.  Every few dozen terms the low parts are folded into the high
 // ones: they would else grow with the terms and lose bits of their own.  Emulated in fp32, log-normal weights (sigma 4),
-// 2048 lanes: a row's sum is off by 2^-41 at V = 10^7 and 2^-38 at 2.4 10^7 without it, by 2^-47 and 2^-48 with it;
-// 64 x 9 x 151936 91.1 -> 91.4 us.
+// 2048 lanes: a row's sum is off by 2^-41 at V = 10^7 and 2^-38 at 2.4 10^7 without it, by 2^-47 and 2^-48 with it
+// (64 x 9 x 151936 90.5 -> 90.7 us; behind the additions rather than before the next loads 91.3).
 struct Sums {
     Two h, l;
     __device__ __forceinline__ void add(Two b) {
@@ -173,12 +173,10 @@ __device__ __forceinline__ float scaled(float x, int e) {
 // A sum beyond 2^48, not finite, or below 2^-48.  (Sums between leave quotients and products that fp32 holds with their low parts.
 // fp16's sums are all between: its weights lie within 2^-24 and 2^16, and a row has fewer than 2^31.)
 __device__ __forceinline__ bool far(float h) { return !(h >= 0x1p-48f && h < 0x1p48f); }
-// such a sum is brought near one if it is positive and finite; the power of two that this took
-__device__ __forceinline__ int settle(Sum &s) {
-    if (!far(s.h) || !(s.h > 0.0f && s.h < INFINITY)) return 0;
-    const int e = (__float_as_int(s.h) >> 23) - 127;
-    s = {scaled(s.h, -e), scaled(s.l, -e)};
-    return -e;
+// the power of two that brings such a sum near one (a draft's beyond fp32 is 2^159 at most, of finite weights); 0: none does, or need be
+__device__ __forceinline__ int power_for(float h) {
+    if (!far(h) || h == 0.0f) return 0;
+    return h < INFINITY ? 127 - (__float_as_int(h) >> 23) : -140;
 }
 
 // x where it is a positive finite number, else 0
@@ -316,6 +314,7 @@ template <class T, bool DRAFT> struct Node {
         constexpr int U = DRAFT ? 5 : 8;
         Sums run = {0ull, 0ull};
         for (int c = c0 + (threadIdx.x & 31); c < c1; c += 32 * U) {
+            run.fold();
             uint4 x[U], y[U];
             uint32_t b[U];
 #pragma unroll
@@ -323,7 +322,6 @@ template <class T, bool DRAFT> struct Node {
             fetch(c, 32, c1, x, y);
 #pragma unroll
             for (int k = 0; k < U; ++k) take<FRESH, LIVE>(run, x[k], y[k], b[k]);
-            run.fold();
         }
         w = run.first();
         wq = run.second();
@@ -350,7 +348,8 @@ template <class T, bool DRAFT> struct Node {
     }
 };
 
-// What few rows need lies apart from the kernel, which slows down with the code between its loops.
+// What few rows need lies apart from the kernel, which slows down with the code between its loops (64 x 9 x 151936 fp32: a choice in
+// the loops 96 us, beside them 93, apart 91, and no scales at all 90).
 
 // elements times 2^e
 template <class T> __device__ __noinline__ uint4 scaled_vector(uint4 x, int e) {
@@ -362,43 +361,22 @@ template <class T> __device__ __noinline__ uint4 scaled_vector(uint4 x, int e) {
 }
 // The sums of a segment of rows that are scaled, a vector at a time.
 struct Pair { Sum w, wq; };
-template <class T>
+template <class T, bool DRAFT>
 __device__ __noinline__ Pair sweep_scaled(const T *p, const T *q, int V, const uint32_t *live, int words, Sum lam, int ep, int eq, bool fresh,
                                           int c0, int c1, int lead, int chunks) {
-    const Node<T, true> at = {{p, V}, {q, V}, live, words, lead, chunks, 0, lam};
+    const Node<T, DRAFT> at = {{p, V}, {q, V}, live, words, lead, chunks, 0, lam};
     Sums run = {0ull, 0ull};
     for (int c = c0 + (threadIdx.x & 31); c < c1; c += 32) {
         uint4 x[1], y[1];
         at.fetch(c, 32, c1, x, y);
         x[0] = scaled_vector<T>(x[0], ep);
-        y[0] = scaled_vector<T>(y[0], eq);
-        if (fresh) at.template take<true, true>(run, x[0], y[0], at.bits(c));
+        if (DRAFT) y[0] = scaled_vector<T>(y[0], eq);
+        if (fresh || !DRAFT) at.template take<true, true>(run, x[0], y[0], at.bits(c));
         else at.template take<false, true>(run, x[0], y[0], at.bits(c));
         run.fold();
     }
     Pair r = {run.first(), run.second()};
-    if (!fresh) r.w = r.w + r.wq;
-    return r;
-}
-// Brings the sums of fresh rows near one where they are far from it: the row's segments (`each` a lane), and both sums.  A draft's
-// sum beyond fp32 is asked for again, of smaller weights (finite ones add up to no more than 2^159).
-struct Settled {
-    Sum total, total_q;
-    int ep, eq;
-    bool beyond;
-};
-__device__ __noinline__ Settled settle_rows(Sum *seg, int each, Sum total, Sum total_q, int eq, bool draft) {
-    Settled r = {total, total_q, 0, eq, false};
-    if (draft && !(total_q.h < INFINITY)) {
-        r.eq = -40;
-        r.beyond = eq == 0;
-        return r;
-    }
-    r.ep = __shfl_sync(0xffffffffu, settle(r.total), 0);
-    if (draft) r.eq += __shfl_sync(0xffffffffu, settle(r.total_q), 0);
-    const int i0 = (threadIdx.x & 31) * each;
-    for (int i = i0; i < i0 + each; ++i) seg[i] = {scaled(seg[i].h, r.ep), scaled(seg[i].l, r.ep)};
-    __syncwarp();
+    if (!(DRAFT && fresh)) r.w = r.w + r.wq;
     return r;
 }
 
@@ -485,8 +463,8 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
         const int mine = rank * WARPS + warp, s0 = mine * at.per, s1 = min(s0 + at.per, at.chunks);
         Sum w = {0.0f, 0.0f}, wq = {0.0f, 0.0f};
         if (any) {
-            if (DRAFT && SCALES && (ep | eq)) {
-                const Pair r = sweep_scaled<T>(at.p.p, at.q.p, a.V, at.live, at.words, at.lam, ep, eq, fresh, s0, s1, at.lead, at.chunks);
+            if (SCALES && (ep | eq)) {
+                const Pair r = sweep_scaled<T, DRAFT>(at.p.p, at.q.p, a.V, at.live, at.words, at.lam, ep, eq, fresh, s0, s1, at.lead, at.chunks);
                 w = r.w;
                 wq = r.wq;
             } else if (fresh || !DRAFT) {
@@ -538,17 +516,15 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
             if (!DRAFT || !fresh) total = warp_sum(total);
             Plan plan = {};
             const bool some = total.h > 0.0f && total.h < INFINITY;
-            bool beyond = false;
-            if (SCALES && fresh && some && (far(total.h) || (DRAFT && far(total_q.h)))) {
-                const Settled r = settle_rows(seg, each, total, total_q, eq, DRAFT);
-                total = r.total;
-                total_q = r.total_q;
-                ep = r.ep;
-                eq = r.eq;
-                beyond = r.beyond;
-            }
             if (lane == 0) {
-                if (beyond) {
+                // Rows whose sums are far from one are summed again, times powers of two that bring them near it, so that quotients,
+                // products and their low parts stay within fp32.
+                const bool again_scaled = SCALES && fresh && some && !(ep | eq) && (far(total.h) || (DRAFT && far(total_q.h)));
+                if (again_scaled) {
+                    ep = power_for(total.h);
+                    eq = DRAFT ? power_for(total_q.h) : 0;
+                }
+                if (again_scaled && (ep | eq)) {
                     plan.action = RESUM;
                 } else if (probing && !again && !(total.h > 0.0f)) {
                     // nothing would be left: the distribution stays as it was
@@ -664,10 +640,10 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
             ep = eq = 0;
             continue;
         }
-        if (SCALES && alike(sh.plan.ep | sh.plan.eq)) {
+        if (SCALES && action == RESUM) {
             ep = alike(sh.plan.ep);
             eq = alike(sh.plan.eq);
-            if (action == RESUM) continue;
+            continue;
         }
         if (action == SWEEP) {
             at.lam = sh.plan.l;
