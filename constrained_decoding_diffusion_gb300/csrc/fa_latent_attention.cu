@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
     static_assert(S::MISC % 16 == 0 && alignof(Misc) == 16 && sizeof(Misc) % alignof(Work) == 0, "alignment of the parts");
     Misc &sh = *reinterpret_cast<Misc *>(smem + S::MISC);
     Work &work = *reinterpret_cast<Work *>(smem + S::MISC + sizeof(Misc));
-    // (the warp's number by way of a shuffle: its roles' code is then known to run in step)
+    // (the warp's number by way of a shuffle: 2 x 98304 slots x 256 rows 83 -> 69 us)
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     constexpr bool F16 = std::is_same<T, __half>::value;
     constexpr float OFF = F16 ? 8.0f : 0.0f;      // fp16 weights reach from 2^14 down to 2^-24, with 2^8 for the reference
@@ -179,8 +179,8 @@ __global__ void __launch_bounds__(NTHR, 1) k_latent(AttendArgs a, const __grid_c
             *fail = 1;
             __syncwarp();
         }
-        // (all steps in one piece of straight code: with a choice of pieces between which the other product has its turn the
-        // offsets reach the instruction by way of ordinary registers, and the issue takes twice as long as the product)
+        // (all steps in one piece of straight code: with a choice of pieces between which the other product has its turn, the
+        // issue takes twice as long as the product)
         auto scores = [&]() {
             tc_fence_after();
             const uint64_t cd = umma_desc(ring + get.slot * S::TILE, 16), kd = umma_desc(keys + (S::NK == 1 ? 0 : get.slot) * GROUP, 16);

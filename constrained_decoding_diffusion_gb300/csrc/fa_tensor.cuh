@@ -115,8 +115,8 @@ __device__ __forceinline__ void umma_commit(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                  : "memory");
 }
-// The same from a whole warp that runs as one, with one of its lanes chosen in the instruction: the operands then go to
-// uniform registers at once.  32 products of 64 x 64 x 16 take 33 clocks each, 128 x 64 x 16 47 (the rates of the
+// The same from a whole warp that runs as one, with one of its lanes chosen in the instruction.
+// 32 products of 64 x 64 x 16 take 33 clocks each, 128 x 64 x 16 47 (the rates of the
 // tensor cores and of shared memory); from a lane's branch of its own 54 to 76, whatever the size.
 __device__ __forceinline__ void umma_ss_warp(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(

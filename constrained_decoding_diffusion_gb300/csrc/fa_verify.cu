@@ -23,9 +23,9 @@
 //
 // What bounds it is the chain from node to node.  In eight blocks a row of 151936 takes 5.5 us with a draft (2900 cycles of
 // additions, 14 a token, and their loads 6700 clocks; the sums of warps, the cluster's meeting and the decision 3500)
-// and 4 without, the draw 3.  Measured in a graph: 64 sequences of 9 x 151936 fp32 with a draft 87 us (210 MB read, 2.4 TB/s;
-// the longest path takes 10 rows, and 36 clusters run at a time), 16 trees of 17 x 151936 bf16 under an automaton 25,
-// a chain of 5 x 32000 15.
+// and 4 without, the draw 3.  Measured in a graph: 64 sequences of 9 x 151936 fp32 with a draft 88 to 100 us (206 MB read, 2.3
+// TB/s; the longest path takes 10 rows or more, and 36 clusters run at a time), 16 trees of 17 x 151936 bf16 under an automaton 25
+// to 28, a chain of 5 x 32000 14 to 16.
 // Tried and dropped: a ring of asynchronous copies in shared memory (5% slower, more instructions), two sums at a time in
 // packed registers against one (equal: the packed addition takes twice as long), the next vectors loaded while
 // these are added up (10% slower, registers), three blocks an SM with fewer vectors under way (8 to 15% slower), arrivals on
@@ -390,8 +390,7 @@ __global__ void __launch_bounds__(NT, 2) k_verify(VerifyArgs a) {
     int *after = reinterpret_cast<int *>(pq + a.T), *path = after + a.T, *tried = path + a.T;
     const cg::cluster_group cluster = cg::this_cluster();
     const int C = cluster.num_blocks(), log_c = 31 - __clz(C), rank = cluster.block_rank(), b = blockIdx.x >> log_c;
-    // (what all threads of a warp have alike goes through a shuffle where shuffles depend on it: the compiler then knows that
-    // the warp runs as one)
+    // (what all threads of a warp have alike goes through a shuffle where later shuffles depend on it)
     auto alike = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
     const int tid = threadIdx.x, warp = alike(tid >> 5), lane = tid & 31;
     const int use = a.count ? min(max(a.count[b], 0), a.T) : a.T;

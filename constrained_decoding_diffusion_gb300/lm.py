@@ -391,7 +391,8 @@ class Verify:
     def __call__(self, target, tokens, parents, u, draft=None, count=None, states=None, next=None, live=None, stream=None):
         """The accepted path of the drafted tokens [B, T] with parents [B, T], the target's weights and, where they
         were drawn at random, the draft's [B, T, V], given uniform numbers u [B, T]: (path [B, T], kept [B],
-        token [B], state [B]), state None without an automaton (states [B], next and live as from fa_beam_tables)."""
+        token [B], state [B]), state None without an automaton (states [B], next and live as from fa_beam_tables).  Tokens
+        that the automaton does not allow are passed over: the draft need not know it."""
         B, T, V = self.shape
         dt = _dtype(target, "target")
         if target.dtype != self.dtype:

@@ -14,8 +14,8 @@ pytestmark = pytest.mark.gpu
 
 def split_row(V, sign, seed):
     """Log-normal weights of which the first half weighs sign 2^-42 of the sum more than the second: the prefix to the
-    middle lies sign 2^-43 of the sum from a half of it.  The first weights of a half make up the difference, three floats of 24
-    bits each; what that leaves is below 2^-60 of the sum.  fsum rounds once."""
+    middle lies sign 2^-43 of the sum from a half of it.  The first weights of a half make up the difference, up to four floats of
+    24 bits each; what that leaves is below 2^-60 of the sum.  fsum rounds once."""
     g = np.random.default_rng(seed)
     w = np.exp(4 * g.standard_normal(V)).astype(np.float32)
     half = V // 2
