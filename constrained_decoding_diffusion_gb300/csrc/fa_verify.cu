@@ -786,9 +786,14 @@ template <class T, bool DRAFT> int wide_clusters() {
 }
 
 template <class T, bool DRAFT> void launch(const VerifyArgs &a, cudaStream_t s) {
-    const int wide = a.V >= 98304 ? wide_clusters<T, DRAFT>() : 0;
+    auto blocks = [&](int wide) { return fa_verify_blocks(a.B, a.V, sizeof(T), DRAFT, a.S > 0, wide); };
+    int cluster = blocks(a.V >= 98304 ? wide_clusters<T, DRAFT>() : 0);
+    if (cluster > 8 && cudaFuncSetAttribute(k_verify<T, DRAFT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+        (void)cudaGetLastError();
+        cluster = blocks(0);
+    }
     cudaLaunchAttribute at[1];
-    const cudaLaunchConfig_t c = config<T, DRAFT>(at, a.B, fa_verify_blocks(a.B, a.V, sizeof(T), DRAFT, a.S > 0, wide), a.T, s);
+    const cudaLaunchConfig_t c = config<T, DRAFT>(at, a.B, cluster, a.T, s);
     (void)cudaLaunchKernelEx(&c, k_verify<T, DRAFT>, a);   // its error is the one the check reads
 }
 

@@ -578,8 +578,8 @@ fa_status fa_beam_reorder(int32_t N, int32_t K, int32_t top, int64_t words, cons
  *   target        [B, T, V] with batch and row strides: weights that need not add up to one.  What is
  *                 not a positive finite number counts as zero
  *   draft         [B, T, V] likewise: row p is the distribution that the children of node p were drawn
- *                 from, independently; or NULL: they were chosen without regard to u (the best beams, say),
- *                 and q(x) = 1
+ *                 from, independently (a row without weight: q = 0); or NULL: they were chosen without regard to u
+ *                 (the best beams, say), and q(x) = 1
  *   tokens        [B, T] int32; a node whose token is outside [0, V), or not allowed by the automaton after its parent,
  *                 is passed over (children may be drawn from the draft's whole row or from its allowed tokens alone)
  *   parents       [B, T] int32
