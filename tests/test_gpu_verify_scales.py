@@ -3,7 +3,6 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-import serving_reference as ref  # noqa: E402
 from constrained_decoding_diffusion_gb300 import lm  # noqa: E402
 from test_gpu_verify import BF, F32, beams, chain, check, make  # noqa: E402
 
@@ -56,6 +55,18 @@ def test_each_row_has_its_own_scale():
     for name in ("target", "draft"):
         half = torch.randint(-50, 51, (30, 6, 1), generator=g).cuda()
         d[name] = d[name] * torch.exp2(half.float()) * torch.exp2(half.float())
+    check(d)
+
+
+@pytest.mark.parametrize("draft,states", [(True, 0), (True, 3), (False, 3)])
+@pytest.mark.parametrize("B,V", [(3, 131075), (40, 98311)])
+def test_scales_of_large_vocabularies(B, V, draft, states):
+    """In sixteen blocks a sequence and in eight, with rows that start anywhere and a draft of another alignment."""
+    d = scaled(make(V, B, [-1, 0, 0, 1], V, F32, draft, states), -100, 90)
+    if draft:
+        wide = torch.zeros(B, 4, V + 3, device="cuda")
+        wide[..., 2:2 + V] = d["draft"]
+        d["draft"] = wide[..., 2:2 + V]
     check(d)
 
 
